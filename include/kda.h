@@ -78,8 +78,13 @@ typedef enum { KDA_F32 = 0, KDA_BF16 = 1 } kda_dtype;
 #define KDA_DEVICE_RANGE 3        /* a value the tensor-core prefill keeps in fp16 operands (v, the
                                      state, the pseudo-values) reached 65504 in magnitude: the
                                      results of that call are not valid                          */
+#define KDA_DEVICE_BAD_PAGE 5     /* a page table entry that a cache length reaches is no page      */
+#define KDA_DEVICE_BAD_LENGTH 6   /* a cache length below 0 or past the page table's room          */
 #define KDA_DEVICE_BAD_SNAPSHOT 4 /* a snapshot offset outside (0, T], out of order, or neither a
                                      multiple of KDA_SNAPSHOT_ALIGN into its document nor its end */
+
+/* The most nodes a sequence's tree of drafted tokens may have. */
+#define KDA_MAX_TREE_NODES 64
 
 /* Prefix snapshots are taken every multiple of this many tokens into a document. */
 #define KDA_SNAPSHOT_ALIGN 64
@@ -329,6 +334,140 @@ KDA_API kda_status kda_decode_verify(const void *q, const void *k, const void *v
  */
 KDA_API kda_status kda_output_gate(const void *o, const void *z, const float *weight, int64_t T,
                                    kda_dims dims, float eps, void *y, void *stream);
+
+/*
+ * ---- Decoding with a tree of drafted tokens -------------------------------
+ *
+ * Speculative decoding ("From GPT-2 to Kimi K3", Chapter 14) where each of N
+ * sequences drafts a tree instead of one chain.  Five calls make a step:
+ * kda_decode_tree in the KDA layers and kda_tree_attention in the softmax
+ * layers give every node's output, kda_verify_drafts decides on the target's
+ * probabilities which nodes are kept, and kda_decode_commit and
+ * kda_cache_append bring states and caches behind the kept path.
+ *
+ * A sequence has M nodes, rows n*M .. n*M + M-1 of every per-node tensor.
+ *   parent [N, M] int32 device: node m hangs below node parent[n, m] < m, or
+ *     with -1 directly below the tokens that came before.  Any other value
+ *     (-2 by custom) says that m is no node: a sequence may have fewer nodes
+ *     than M, in any places.  What hangs below no node is none either.  The
+ *     outputs of such rows are zeros, and what their inputs hold (infinities
+ *     and NaN too) reaches no other row.
+ *   1 <= M <= KDA_MAX_TREE_NODES (KDA_ERR_UNSUPPORTED above it); N = 0 is
+ *     allowed and launches nothing.
+ */
+
+/*
+ * The KDA recurrence over the tree, from a read-only state: node m's output is
+ * o_m = S_m^T q_m with S_m = (I - beta_m k_m k_m^T) Diag(exp(g_m)) S_parent +
+ * beta_m k_m v_m^T, and S_parent = state for parent -1.  A chain
+ * (parent[m] = m - 1) gives kda_decode_verify's outputs.
+ *   q, k [N*M, H, d_k], v, out [N*M, H, d_v] qkv_dtype;  g [N*M, H, d_k] fp32
+ *   (<= 0), beta [N*M, H] fp32;  state [N, H, d_k, d_v] fp32, read once
+ */
+KDA_API kda_status kda_decode_tree(const void *q, const void *k, const void *v, const float *g,
+                                   const float *beta, const float *state, const int32_t *parent,
+                                   int32_t N, int32_t M, kda_dims dims, void *out, void *stream);
+
+/*
+ * The states after the accepted path: for t = 0 .. accept[n]-1 the update of
+ * node path[n, t], from state_in.
+ *   k, v, g, beta as kda_decode_tree (M may be any number of rows per sequence)
+ *   path   [N, P] int32 device: rows within the sequence, in order; an entry
+ *          outside 0..M-1 ends the path
+ *   accept [N] int32 device, clamped to 0..P
+ *   state_out [N, H, d_k, d_v] fp32; may be state_in (the update in place)
+ */
+KDA_API kda_status kda_decode_commit(const void *k, const void *v, const float *g, const float *beta,
+                                     const float *state_in, const int32_t *path, const int32_t *accept,
+                                     int32_t N, int32_t M, int32_t P, kda_dims dims, float *state_out,
+                                     void *stream);
+
+/* Bytes of device workspace kda_tree_attention needs (0 for invalid arguments). */
+KDA_API size_t kda_tree_attention_workspace_size(kda_dims dims, int32_t H_kv, int32_t N, int32_t M,
+                                                 int32_t page_size, int32_t max_pages);
+
+/*
+ * Softmax attention of the drafted tree over a paged cache and itself.  Node
+ * m's query head hq reads the cache head hq / (H / H_kv): the keys 0 ..
+ * cache_lens[n]-1 of its sequence, and the drafted keys of m and the nodes
+ * above it.
+ *     out = sum_j softmax_j(scale q . k_j) v_j,   lse = ln sum_j exp(scale q . k_j)
+ *   q, out [N*M, H, d] and k_new, v_new [N*M, H_kv, d]  qkv_dtype (dims.H = H,
+ *          d_k = d_v = d)
+ *   k_cache, v_cache [num_pages, H_kv, page_size, d] qkv_dtype
+ *   page_table [N, max_pages] int32 device: token t of sequence n is in slot
+ *          t % page_size of page page_table[n, t / page_size]; only the
+ *          entries that cache_lens reaches are read
+ *   cache_lens [N] int32 device, 0 .. max_pages * page_size.  What the cache
+ *          holds past a length is never used.
+ *   lse    [N*M, H] fp32 or NULL (-infinity in the rows of no node)
+ *   workspace  kda_tree_attention_workspace_size() bytes, 256-byte aligned or
+ *          more; its first word is the device status word: KDA_DEVICE_BAD_PAGE
+ *          and KDA_DEVICE_BAD_LENGTH are reported there (out and lse are then
+ *          unspecified; no access leaves the buffers)
+ * Any page_size serves; multiples of 8 take the tensor-core path (bf16, d = 64
+ * or 128).  N * M * H must not exceed 2^29.
+ */
+KDA_API kda_status kda_tree_attention(const void *q, const void *k_new, const void *v_new,
+                                      const void *k_cache, const void *v_cache,
+                                      const int32_t *page_table, const int32_t *cache_lens,
+                                      const int32_t *parent, int32_t N, int32_t M, int32_t H_kv,
+                                      int32_t num_pages, int32_t page_size, int32_t max_pages,
+                                      float scale, kda_dims dims, void *out, float *lse,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Which drafted nodes the target keeps, and the token after them, so that the
+ * tokens are distributed as the target's own.  Node 0 is the last certain
+ * token (it is always kept); the walk starts there.  At the current node c,
+ * its children are tried in index order with the uniform number
+ * uniforms[n, c]; the first kept child becomes the current node, and when none
+ * is kept (or there is none) the next token is drawn with uniforms[n, M].
+ *   target_probs [N, M, V]: row m is the target's distribution after node m
+ *   draft_probs  [N, M, V] or NULL: row m is the distribution that m's child
+ *       was sampled from.  Then child x is kept when u * draft[x] < target[x],
+ *       only the first child of a node is tried, and after a refusal the next
+ *       token is drawn from max(target - draft, 0).  NULL: the children are
+ *       the draft's own choice (its likeliest tokens, say); child x is kept
+ *       when u falls into its share of the target's mass, counted after its
+ *       elder siblings', and after refusals the next token is drawn from the
+ *       target's distribution without the refused tokens.
+ *   tokens [N, M] int32 (a token outside 0..V-1 is never kept), parent [N, M]
+ *   uniforms [N, M + 1] fp32 in [0, 1), used in steps of 2^-24 (against
+ *       draft_probs: as given)
+ *   probs_dtype  kda_dtype of both distributions, which need not sum to one
+ *       exactly: the draw divides by their sum
+ *   accept [N] int32: kept nodes, node 0 among them (0 when node 0 is no node)
+ *   path   [N, M] int32: their indices in order, -1 beyond
+ *   next_token [N] int32: -1 when node 0 is no node or the row has no mass
+ * Probabilities are compared and summed as whole multiples of 2^-38: the
+ * results do not depend on the order of any sum.  Where nothing is left after
+ * refusals the token is drawn from the target's row itself.
+ */
+KDA_API kda_status kda_verify_drafts(const void *target_probs, const void *draft_probs,
+                                     const int32_t *tokens, const int32_t *parent,
+                                     const float *uniforms, int32_t N, int32_t M, int32_t V,
+                                     int32_t probs_dtype, int32_t *accept, int32_t *path,
+                                     int32_t *next_token, void *stream);
+
+/*
+ * New keys and values into the pages: token t < accept[n] of sequence n comes
+ * from row path[n, t] of its M new rows (row t without a path) and goes to
+ * position cache_lens[n] + t.
+ *   k_new, v_new [N*M, H, d] qkv_dtype (dims.H = the cache's heads; M any number)
+ *   path [N, P] int32 device or NULL (then P <= M);  accept [N] int32 device,
+ *       clamped to 0..P, or NULL (all P)
+ *   k_cache, v_cache, page_table, page_size as kda_tree_attention
+ *   lens_out [N] int32 or NULL: cache_lens + accept; must not be cache_lens
+ * A token whose path entry, position or page is out of range is left out.
+ * Sequences must not share the pages that are written.
+ */
+KDA_API kda_status kda_cache_append(const void *k_new, const void *v_new, const int32_t *path,
+                                    const int32_t *accept, const int32_t *page_table,
+                                    const int32_t *cache_lens, int32_t N, int32_t M, int32_t P,
+                                    int32_t num_pages, int32_t page_size, int32_t max_pages,
+                                    kda_dims dims, void *k_cache, void *v_cache, int32_t *lens_out,
+                                    void *stream);
 
 /*
  * Diagnostic of the bounded device-side waits (the method's sources have no

@@ -66,6 +66,26 @@ kda_status maybe(const void *p, const char *name) {
 
 constexpr size_t kStatusBytes = 256;
 
+// a batch of drafted trees: N sequences of M nodes (one bit per node), H heads
+kda_status check_tree(int32_t N, int32_t M, int32_t H) {
+    if (N < 0) return fail(KDA_ERR_INVALID, "N must be >= 0%s");
+    if (M < 1) return fail(KDA_ERR_INVALID, "M must be >= 1%s");
+    if (M > KDA_MAX_TREE_NODES) return fail(KDA_ERR_UNSUPPORTED, "M must be <= 64%s");
+    if ((int64_t)N * M * H > INT32_MAX) return fail(KDA_ERR_INVALID, "N * M * H too large%s");
+    return KDA_OK;
+}
+
+// a paged cache of H_kv heads serving dims.H query heads
+kda_status check_pages(const kda_dims &d, int32_t H_kv, int32_t num_pages, int32_t page_size,
+                       int32_t max_pages) {
+    if (H_kv < 1 || d.H % H_kv != 0) return fail(KDA_ERR_INVALID, "H must be a multiple of H_kv >= 1%s");
+    if (num_pages < 1) return fail(KDA_ERR_INVALID, "num_pages must be >= 1%s");
+    if (page_size < 1) return fail(KDA_ERR_INVALID, "page_size must be >= 1%s");
+    if (max_pages < 1 || (int64_t)max_pages * page_size > INT32_MAX - 4096)
+        return fail(KDA_ERR_INVALID, "max_pages * page_size must be in [1, 2^31 - 4096)%s");
+    return KDA_OK;
+}
+
 // KDA_PREFILL_PATH=recurrent forces the CUDA-core prefill everywhere (used to
 // cross-check the two prefill kernels on the same inputs); read once.
 bool force_recurrent() {
@@ -409,6 +429,158 @@ kda_status kda_output_gate(const void *o, const void *z, const float *weight, in
     return KDA_OK;
 }
 
+kda_status kda_decode_tree(const void *q, const void *k, const void *v, const float *g,
+                           const float *beta, const float *state, const int32_t *parent, int32_t N,
+                           int32_t M, kda_dims dims, void *out, void *stream) {
+    g_last_error[0] = '\0';
+    KDA_TRY(check_dims(dims));
+    KDA_TRY(check_tree(N, M, dims.H));
+    if (N == 0) return KDA_OK;
+    KDA_TRY(need(q, "q"));
+    KDA_TRY(need(k, "k"));
+    KDA_TRY(need(v, "v"));
+    KDA_TRY(need(g, "g"));
+    KDA_TRY(need4(beta, "beta"));
+    KDA_TRY(need(state, "state"));
+    KDA_TRY(need4(parent, "parent"));
+    KDA_TRY(need(out, "out"));
+    cudaError_t err = kda::launch_decode_tree(q, k, v, g, beta, state, parent, N, M, dims.H, dims.d_k,
+                                              (kda_dtype)dims.qkv_dtype, out,
+                                              static_cast<cudaStream_t>(stream));
+    if (err != cudaSuccess) return cuda_fail(err, "tree decode launch");
+    return KDA_OK;
+}
+
+kda_status kda_decode_commit(const void *k, const void *v, const float *g, const float *beta,
+                             const float *state_in, const int32_t *path, const int32_t *accept,
+                             int32_t N, int32_t M, int32_t P, kda_dims dims, float *state_out,
+                             void *stream) {
+    g_last_error[0] = '\0';
+    KDA_TRY(check_dims(dims));
+    if (N < 0 || M < 1 || P < 1) return fail(KDA_ERR_INVALID, "N must be >= 0, M and P >= 1%s");
+    if ((int64_t)N * M > INT32_MAX || (int64_t)N * P > INT32_MAX || (int64_t)N * dims.H > INT32_MAX)
+        return fail(KDA_ERR_INVALID, "N * M, N * P or N * H too large%s");
+    if (N == 0) return KDA_OK;
+    KDA_TRY(need(k, "k"));
+    KDA_TRY(need(v, "v"));
+    KDA_TRY(need(g, "g"));
+    KDA_TRY(need4(beta, "beta"));
+    KDA_TRY(need(state_in, "state_in"));
+    KDA_TRY(need4(path, "path"));
+    KDA_TRY(need4(accept, "accept"));
+    KDA_TRY(need(state_out, "state_out"));
+    cudaError_t err = kda::launch_decode_commit(k, v, g, beta, state_in, path, accept, N, M, P, dims.H,
+                                                dims.d_k, (kda_dtype)dims.qkv_dtype, state_out,
+                                                static_cast<cudaStream_t>(stream));
+    if (err != cudaSuccess) return cuda_fail(err, "commit launch");
+    return KDA_OK;
+}
+
+size_t kda_tree_attention_workspace_size(kda_dims dims, int32_t H_kv, int32_t N, int32_t M,
+                                         int32_t page_size, int32_t max_pages) {
+    if (check_dims(dims) != KDA_OK || check_tree(N, M, dims.H) != KDA_OK ||
+        check_pages(dims, H_kv, 1, page_size, max_pages) != KDA_OK || N == 0)
+        return 0;
+    return kStatusBytes + kda::tree_attention_partial_bytes(N, M, dims.H, H_kv, dims.d_k,
+                                                            (kda_dtype)dims.qkv_dtype, page_size, max_pages);
+}
+
+kda_status kda_tree_attention(const void *q, const void *k_new, const void *v_new, const void *k_cache,
+                              const void *v_cache, const int32_t *page_table, const int32_t *cache_lens,
+                              const int32_t *parent, int32_t N, int32_t M, int32_t H_kv,
+                              int32_t num_pages, int32_t page_size, int32_t max_pages, float scale,
+                              kda_dims dims, void *out, float *lse, void *workspace,
+                              size_t workspace_bytes, void *stream) {
+    g_last_error[0] = '\0';
+    KDA_TRY(check_dims(dims));
+    KDA_TRY(check_tree(N, M, dims.H));
+    KDA_TRY(check_pages(dims, H_kv, num_pages, page_size, max_pages));
+    if ((int64_t)N * M * dims.H > (1 << 29)) return fail(KDA_ERR_INVALID, "N * M * H must be <= 2^29%s");
+    if (!(scale > 0.f) || scale > 3.402823466e38f)
+        return fail(KDA_ERR_INVALID, "scale must be positive and finite%s");
+    if (N == 0) return KDA_OK;
+    KDA_TRY(need(q, "q"));
+    KDA_TRY(need(k_new, "k_new"));
+    KDA_TRY(need(v_new, "v_new"));
+    KDA_TRY(need(k_cache, "k_cache"));
+    KDA_TRY(need(v_cache, "v_cache"));
+    KDA_TRY(need4(page_table, "page_table"));
+    KDA_TRY(need4(cache_lens, "cache_lens"));
+    KDA_TRY(need4(parent, "parent"));
+    KDA_TRY(need(out, "out"));
+    if (lse != nullptr) KDA_TRY(need4(lse, "lse"));
+    KDA_TRY(need(workspace, "workspace"));
+    if (workspace_bytes < kda_tree_attention_workspace_size(dims, H_kv, N, M, page_size, max_pages))
+        return fail(KDA_ERR_INVALID, "workspace too small (see kda_tree_attention_workspace_size)%s");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    kda::TreeAttention a{q, k_new, v_new, k_cache, v_cache, page_table, cache_lens, parent, out, lse,
+                         static_cast<int32_t *>(workspace), N, M, dims.H, H_kv, num_pages, page_size,
+                         max_pages, scale};
+    cudaError_t err = cudaMemsetAsync(workspace, 0, sizeof(int32_t), s);
+    if (err != cudaSuccess) return cuda_fail(err, "clearing the status word");
+    err = kda::launch_tree_attention(a, dims.d_k, (kda_dtype)dims.qkv_dtype,
+                                     static_cast<unsigned char *>(workspace) + kStatusBytes, s);
+    if (err != cudaSuccess) return cuda_fail(err, "tree attention launch");
+    return KDA_OK;
+}
+
+kda_status kda_verify_drafts(const void *target_probs, const void *draft_probs, const int32_t *tokens,
+                             const int32_t *parent, const float *uniforms, int32_t N, int32_t M,
+                             int32_t V, int32_t probs_dtype, int32_t *accept, int32_t *path,
+                             int32_t *next_token, void *stream) {
+    g_last_error[0] = '\0';
+    if (probs_dtype != KDA_F32 && probs_dtype != KDA_BF16)
+        return fail(KDA_ERR_UNSUPPORTED, "probs_dtype must be KDA_F32 or KDA_BF16%s");
+    KDA_TRY(check_tree(N, M, 1));
+    if (V < 1 || V > (1 << 30)) return fail(KDA_ERR_INVALID, "V must be in [1, 2^30]%s");
+    if (N == 0) return KDA_OK;
+    KDA_TRY(need(target_probs, "target_probs"));
+    KDA_TRY(maybe(draft_probs, "draft_probs"));
+    KDA_TRY(need4(tokens, "tokens"));
+    KDA_TRY(need4(parent, "parent"));
+    KDA_TRY(need4(uniforms, "uniforms"));
+    KDA_TRY(need4(accept, "accept"));
+    KDA_TRY(need4(path, "path"));
+    KDA_TRY(need4(next_token, "next_token"));
+    cudaError_t err = kda::launch_verify_drafts(target_probs, draft_probs, tokens, parent, uniforms, N, M, V,
+                                                (kda_dtype)probs_dtype, accept, path, next_token,
+                                                static_cast<cudaStream_t>(stream));
+    if (err != cudaSuccess) return cuda_fail(err, "draft verification launch");
+    return KDA_OK;
+}
+
+kda_status kda_cache_append(const void *k_new, const void *v_new, const int32_t *path,
+                            const int32_t *accept, const int32_t *page_table, const int32_t *cache_lens,
+                            int32_t N, int32_t M, int32_t P, int32_t num_pages, int32_t page_size,
+                            int32_t max_pages, kda_dims dims, void *k_cache, void *v_cache,
+                            int32_t *lens_out, void *stream) {
+    g_last_error[0] = '\0';
+    KDA_TRY(check_dims(dims));
+    if (N < 0 || N > 65535 || M < 1 || P < 1)
+        return fail(KDA_ERR_INVALID, "N must be in [0, 65535], M and P >= 1%s");
+    if (path == nullptr && P > M) return fail(KDA_ERR_INVALID, "P must be <= M without a path%s");
+    if ((int64_t)N * M > INT32_MAX || (int64_t)N * P > INT32_MAX)
+        return fail(KDA_ERR_INVALID, "N * M or N * P too large%s");
+    KDA_TRY(check_pages(dims, dims.H, num_pages, page_size, max_pages));
+    if (N == 0) return KDA_OK;
+    KDA_TRY(need(k_new, "k_new"));
+    KDA_TRY(need(v_new, "v_new"));
+    if (path != nullptr) KDA_TRY(need4(path, "path"));
+    if (accept != nullptr) KDA_TRY(need4(accept, "accept"));
+    KDA_TRY(need4(page_table, "page_table"));
+    KDA_TRY(need4(cache_lens, "cache_lens"));
+    KDA_TRY(need(k_cache, "k_cache"));
+    KDA_TRY(need(v_cache, "v_cache"));
+    if (lens_out != nullptr) KDA_TRY(need4(lens_out, "lens_out"));
+    if (lens_out == cache_lens) return fail(KDA_ERR_INVALID, "lens_out must not alias cache_lens%s");
+    cudaError_t err = kda::launch_cache_append(k_new, v_new, path, accept, page_table, cache_lens, N, M, P,
+                                               dims.H, dims.d_k, num_pages, page_size, max_pages,
+                                               (kda_dtype)dims.qkv_dtype, k_cache, v_cache, lens_out,
+                                               static_cast<cudaStream_t>(stream));
+    if (err != cudaSuccess) return cuda_fail(err, "cache append launch");
+    return KDA_OK;
+}
+
 kda_status kda_selftest_wait(int64_t limit_ns, void *workspace, size_t workspace_bytes,
                              void *stream) {
     g_last_error[0] = '\0';
@@ -442,6 +614,10 @@ kda_status kda_get_device_status(const void *workspace, int32_t *status_out,
         return fail(KDA_ERR_DEVICE, "a value held in fp16 operands reached 65504 in magnitude%s");
     if (word == KDA_DEVICE_BAD_SNAPSHOT)
         return fail(KDA_ERR_DEVICE, "a snapshot offset is out of range, out of order or misaligned%s");
+    if (word == KDA_DEVICE_BAD_PAGE)
+        return fail(KDA_ERR_DEVICE, "a page table entry is outside the cache%s");
+    if (word == KDA_DEVICE_BAD_LENGTH)
+        return fail(KDA_ERR_DEVICE, "a cache length is negative or past the page table's room%s");
     return fail(KDA_ERR_DEVICE, "the device rejected cu_seqlens (not 0..T, non-decreasing)%s");
 }
 

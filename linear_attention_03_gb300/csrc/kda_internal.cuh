@@ -182,6 +182,44 @@ cudaError_t launch_verify(const void *q, const void *k, const void *v, const flo
 cudaError_t launch_output_gate(const void *o, const void *z, const float *weight, int64_t rows,
                                int32_t D, kda_dtype dt, float eps, void *y, cudaStream_t stream);
 
+// the KDA recurrence over a tree of drafted tokens: every node's output
+cudaError_t launch_decode_tree(const void *q, const void *k, const void *v, const float *g,
+                               const float *beta, const float *state, const int32_t *parent, int32_t N,
+                               int32_t M, int32_t H, int32_t D, kda_dtype dt, void *out,
+                               cudaStream_t stream);
+// the state after a path through the tree
+cudaError_t launch_decode_commit(const void *k, const void *v, const float *g, const float *beta,
+                                 const float *state_in, const int32_t *path, const int32_t *accept,
+                                 int32_t N, int32_t M, int32_t P, int32_t H, int32_t D, kda_dtype dt,
+                                 float *state_out, cudaStream_t stream);
+
+// Softmax attention of a drafted tree over a paged cache: the arguments of
+// kda_tree_attention.
+struct TreeAttention {
+    const void *q, *k_new, *v_new, *k_cache, *v_cache;
+    const int32_t *page_table, *cache_lens, *parent;
+    void *out;
+    float *lse;
+    int32_t *status;
+    int32_t N, M, H, H_kv, num_pages, page_size, max_pages;
+    float scale;
+};
+size_t tree_attention_partial_bytes(int32_t N, int32_t M, int32_t H, int32_t H_kv, int32_t D, kda_dtype dt,
+                                    int32_t page_size, int32_t max_pages);
+cudaError_t launch_tree_attention(const TreeAttention &a, int32_t D, kda_dtype dt, void *workspace,
+                                  cudaStream_t stream);
+
+cudaError_t launch_verify_drafts(const void *target, const void *draft, const int32_t *tokens,
+                                 const int32_t *parent, const float *uniforms, int32_t N, int32_t M,
+                                 int32_t V, kda_dtype dt, int32_t *accept, int32_t *path,
+                                 int32_t *next_token, cudaStream_t stream);
+cudaError_t launch_cache_append(const void *k_new, const void *v_new, const int32_t *path,
+                                const int32_t *accept, const int32_t *page_table,
+                                const int32_t *cache_lens, int32_t N, int32_t M, int32_t P, int32_t H,
+                                int32_t D, int32_t num_pages, int32_t page_size, int32_t max_pages,
+                                kda_dtype dt, void *k_cache, void *v_cache, int32_t *lens_out,
+                                cudaStream_t stream);
+
 cudaError_t launch_selftest_wait(uint64_t limit_ns, int32_t *status, cudaStream_t stream);
 
 // Tensor-core chunked prefill (d = 128, bf16 q/k/v).  With out_f32 set, the

@@ -25,7 +25,8 @@ KDA_OK, KDA_ERR_INVALID, KDA_ERR_UNSUPPORTED, KDA_ERR_CUDA, KDA_ERR_TIMEOUT, \
     KDA_ERR_DEVICE = range(6)
 KDA_F32, KDA_BF16 = 0, 1
 KDA_DEVICE_OK, KDA_DEVICE_BAD_OFFSETS, KDA_DEVICE_TIMEOUT, KDA_DEVICE_RANGE, \
-    KDA_DEVICE_BAD_SNAPSHOT = range(5)
+    KDA_DEVICE_BAD_SNAPSHOT, KDA_DEVICE_BAD_PAGE, KDA_DEVICE_BAD_LENGTH = range(7)
+KDA_MAX_TREE_NODES = 64
 KDA_SNAPSHOT_ALIGN = 64
 SYMBOLS = ("kda_prefill_workspace_size", "kda_prefill", "kda_decode_step",
            "kda_prologue", "kda_get_device_status", "kda_last_error",
@@ -33,7 +34,9 @@ SYMBOLS = ("kda_prefill_workspace_size", "kda_prefill", "kda_decode_step",
            "kda_output_gate", "kda_prefill_noalloc", "kda_selftest_wait",
            "kda_prefill_segmented_workspace_size", "kda_prefill_segmented",
            "kda_prologue_prefill_workspace_size", "kda_prologue_prefill",
-           "kda_prefill_snapshots")
+           "kda_prefill_snapshots", "kda_decode_tree", "kda_decode_commit",
+           "kda_tree_attention_workspace_size", "kda_tree_attention",
+           "kda_verify_drafts", "kda_cache_append")
 
 
 class kda_dims(ctypes.Structure):
@@ -63,6 +66,15 @@ lib.kda_get_device_status.argtypes = [_P, ctypes.POINTER(ctypes.c_int32), _P]
 lib.kda_decode_step_conv.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _P, _i32, kda_dims, _P]
 lib.kda_decode_verify.argtypes = [_P, _P, _P, _P, _P, _P, _P, _i32, _i32, kda_dims, _P, _P, _P]
 lib.kda_output_gate.argtypes = [_P, _P, _P, _i64, kda_dims, ctypes.c_float, _P, _P]
+lib.kda_decode_tree.argtypes = [_P, _P, _P, _P, _P, _P, _P, _i32, _i32, kda_dims, _P, _P]
+lib.kda_decode_commit.argtypes = [_P, _P, _P, _P, _P, _P, _P, _i32, _i32, _i32, kda_dims, _P, _P]
+lib.kda_tree_attention_workspace_size.argtypes = [kda_dims, _i32, _i32, _i32, _i32, _i32]
+lib.kda_tree_attention_workspace_size.restype = _sz
+lib.kda_tree_attention.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _i32, _i32,
+                                   ctypes.c_float, kda_dims, _P, _P, _P, _sz, _P]
+lib.kda_verify_drafts.argtypes = [_P, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _P, _P, _P, _P]
+lib.kda_cache_append.argtypes = [_P, _P, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _i32, _i32, kda_dims,
+                                 _P, _P, _P, _P]
 lib.kda_selftest_wait.argtypes = [_i64, _P, _sz, _P]
 lib.kda_selftest_wait.restype = ctypes.c_int
 lib.kda_last_error.argtypes = []
@@ -73,7 +85,9 @@ for _fn in (lib.kda_prefill, lib.kda_prefill_snapshots, lib.kda_prefill_segmente
             lib.kda_prologue_prefill,
             lib.kda_decode_step, lib.kda_prologue,
             lib.kda_get_device_status,
-            lib.kda_decode_step_conv, lib.kda_decode_verify, lib.kda_output_gate):
+            lib.kda_decode_step_conv, lib.kda_decode_verify, lib.kda_output_gate,
+            lib.kda_decode_tree, lib.kda_decode_commit, lib.kda_tree_attention,
+            lib.kda_verify_drafts, lib.kda_cache_append):
     _fn.restype = ctypes.c_int
 
 
@@ -422,6 +436,186 @@ def kda_output_gate(o, z, weight=None, eps=1e-6, out=None):
     if st != KDA_OK:
         raise KDAError(st, "kda_output_gate")
     return out
+
+
+def _tree(parent, rows):
+    """(N, M) of a [N, M] int32 parent tensor that covers `rows` node rows."""
+    _dev(parent, "parent", torch.int32)
+    if parent.dim() != 2 or parent.shape[0] * parent.shape[1] != rows:
+        raise ValueError(f"parent must be [N, M] with N * M = {rows}, got {tuple(parent.shape)}")
+    return parent.shape
+
+
+def kda_decode_tree(q, k, v, g, beta, state, parent, out=None):
+    """The KDA recurrence over a tree of drafted tokens per sequence, from the
+    read-only `state`; returns every node's output.
+
+    q, k, v, g [N*M, H, d], beta [N*M, H], state [N, H, d, d]; parent [N, M]
+    int32: node m's parent (< m), -1 below the prefix, other values no node."""
+    rows, H, d = q.shape
+    N, M = _tree(parent, rows)
+    _dev(q, "q")
+    _dev(k, "k", q.dtype, q.shape)
+    _dev(v, "v", q.dtype, q.shape)
+    _dev(g, "g", torch.float32, q.shape)
+    _dev(beta, "beta", torch.float32, (rows, H))
+    _dev(state, "state", torch.float32, (N, H, d, d))
+    if out is None:
+        out = torch.empty_like(q)
+    _dev(out, "out", q.dtype, q.shape)
+    st = lib.kda_decode_tree(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), _ptr(parent),
+                             N, M, dims_of(q), _ptr(out), _stream())
+    if st != KDA_OK:
+        raise KDAError(st, "kda_decode_tree")
+    return out
+
+
+def kda_decode_commit(k, v, g, beta, state, path, accept, state_out=None):
+    """The states after the first accept[n] nodes of path[n] ([N, P] int32 row
+    indices within the sequence), in place unless `state_out` is given;
+    returns the updated states."""
+    rows, H, d = k.shape
+    N = state.shape[0]
+    _dev(k, "k")
+    _dev(v, "v", k.dtype, k.shape)
+    _dev(g, "g", torch.float32, k.shape)
+    _dev(beta, "beta", torch.float32, (rows, H))
+    _dev(state, "state", torch.float32, (N, H, d, d))
+    _dev(path, "path", torch.int32)
+    _dev(accept, "accept", torch.int32, (N,))
+    if path.dim() != 2 or path.shape[0] != N or path.shape[1] < 1:
+        raise ValueError(f"path must be [{N}, P], got {tuple(path.shape)}")
+    if N and rows % N:
+        raise ValueError("k must hold N*M rows")
+    if state_out is None:
+        state_out = state
+    _dev(state_out, "state_out", torch.float32, (N, H, d, d))
+    st = lib.kda_decode_commit(_ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), _ptr(path), _ptr(accept),
+                               N, rows // N if N else 1, path.shape[1], dims_of(k), _ptr(state_out), _stream())
+    if st != KDA_OK:
+        raise KDAError(st, "kda_decode_commit")
+    return state_out
+
+
+def kda_tree_attention_workspace_size(H: int, H_kv: int, d: int, dtype: torch.dtype, N: int, M: int,
+                                      page_size: int, max_pages: int) -> int:
+    code = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
+    return int(lib.kda_tree_attention_workspace_size(kda_dims(H, d, d, code), H_kv, N, M, page_size, max_pages))
+
+
+def kda_tree_attention(q, k_new, v_new, k_cache, v_cache, page_table, cache_lens, parent, scale=None,
+                       out=None, lse=None, want_lse=False, workspace=None):
+    """Softmax attention of a drafted tree over a paged cache and itself;
+    returns (out, lse), lse None unless given or asked for.
+
+    q [N*M, H, d]; k_new, v_new [N*M, H_kv, d]; k_cache, v_cache [num_pages,
+    H_kv, page_size, d]; page_table [N, max_pages], cache_lens [N], parent
+    [N, M] int32.  scale defaults to d ** -0.5.  The workspace's first word is
+    the device status word (kda_get_device_status)."""
+    rows, H, d = q.shape
+    N, M = _tree(parent, rows)
+    _dev(q, "q")
+    _dev(k_cache, "k_cache", q.dtype)
+    if k_cache.dim() != 4 or k_cache.shape[3] != d:
+        raise ValueError(f"k_cache must be [num_pages, H_kv, page_size, {d}], got {tuple(k_cache.shape)}")
+    num_pages, H_kv, page_size, _ = k_cache.shape
+    _dev(v_cache, "v_cache", q.dtype, k_cache.shape)
+    _dev(k_new, "k_new", q.dtype, (rows, H_kv, d))
+    _dev(v_new, "v_new", q.dtype, (rows, H_kv, d))
+    _dev(page_table, "page_table", torch.int32)
+    if page_table.dim() != 2 or page_table.shape[0] != N:
+        raise ValueError(f"page_table must be [{N}, max_pages], got {tuple(page_table.shape)}")
+    _dev(cache_lens, "cache_lens", torch.int32, (N,))
+    if out is None:
+        out = torch.empty_like(q)
+    _dev(out, "out", q.dtype, q.shape)
+    if lse is None and want_lse:
+        lse = torch.empty((rows, H), dtype=torch.float32, device=q.device)
+    _dev(lse, "lse", torch.float32, (rows, H))
+    dims, max_pages = dims_of(q), page_table.shape[1]
+    if workspace is None:
+        ws_bytes = int(lib.kda_tree_attention_workspace_size(dims, H_kv, N, M, page_size, max_pages))
+        workspace = torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device=q.device)
+    _dev(workspace, "workspace", torch.uint8)
+    st = lib.kda_tree_attention(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
+                                _ptr(page_table), _ptr(cache_lens), _ptr(parent), N, M, H_kv, num_pages,
+                                page_size, max_pages, d ** -0.5 if scale is None else float(scale), dims,
+                                _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _stream())
+    if st != KDA_OK:
+        raise KDAError(st, "kda_tree_attention")
+    return out, lse
+
+
+def kda_verify_drafts(target_probs, tokens, parent, uniforms, draft_probs=None, accept=None, path=None,
+                      next_token=None):
+    """Which drafted nodes the target keeps; returns (accept [N], path [N, M],
+    next_token [N]), int32.
+
+    target_probs [N, M, V] bf16 or fp32: the target's distribution after each
+    node; tokens, parent [N, M] int32; uniforms [N, M + 1] fp32; draft_probs
+    [N, M, V] when the drafts were sampled from them, None when they are the
+    draft's own choice."""
+    if target_probs.dim() != 3:
+        raise ValueError(f"target_probs must be [N, M, V], got {tuple(target_probs.shape)}")
+    N, M, V = target_probs.shape
+    code, dev = _dtype_code(target_probs), target_probs.device
+    _dev(target_probs, "target_probs")
+    _dev(draft_probs, "draft_probs", target_probs.dtype, target_probs.shape)
+    _dev(tokens, "tokens", torch.int32, (N, M))
+    _dev(parent, "parent", torch.int32, (N, M))
+    _dev(uniforms, "uniforms", torch.float32, (N, M + 1))
+    if accept is None:
+        accept = torch.empty(N, dtype=torch.int32, device=dev)
+    if path is None:
+        path = torch.empty((N, M), dtype=torch.int32, device=dev)
+    if next_token is None:
+        next_token = torch.empty(N, dtype=torch.int32, device=dev)
+    _dev(accept, "accept", torch.int32, (N,))
+    _dev(path, "path", torch.int32, (N, M))
+    _dev(next_token, "next_token", torch.int32, (N,))
+    st = lib.kda_verify_drafts(_ptr(target_probs), _ptr(draft_probs), _ptr(tokens), _ptr(parent),
+                               _ptr(uniforms), N, M, V, code, _ptr(accept), _ptr(path), _ptr(next_token),
+                               _stream())
+    if st != KDA_OK:
+        raise KDAError(st, "kda_verify_drafts")
+    return accept, path, next_token
+
+
+def kda_cache_append(k_new, v_new, k_cache, v_cache, page_table, cache_lens, path=None, accept=None,
+                     lens_out=None):
+    """The first accept[n] new tokens (all without `accept`; rows path[n, t],
+    or t without `path`) of each sequence behind its cache_lens[n] cached ones;
+    returns the new lengths."""
+    rows, H, d = k_new.shape
+    N = cache_lens.shape[0]
+    _dev(k_new, "k_new")
+    _dev(v_new, "v_new", k_new.dtype, k_new.shape)
+    _dev(k_cache, "k_cache", k_new.dtype)
+    if k_cache.dim() != 4 or k_cache.shape[1] != H or k_cache.shape[3] != d:
+        raise ValueError(f"k_cache must be [num_pages, {H}, page_size, {d}], got {tuple(k_cache.shape)}")
+    _dev(v_cache, "v_cache", k_new.dtype, k_cache.shape)
+    _dev(cache_lens, "cache_lens", torch.int32, (N,))
+    _dev(page_table, "page_table", torch.int32)
+    if page_table.dim() != 2 or page_table.shape[0] != N:
+        raise ValueError(f"page_table must be [{N}, max_pages], got {tuple(page_table.shape)}")
+    if N and rows % N:
+        raise ValueError("k_new must hold N*M rows")
+    M = rows // N if N else 1
+    _dev(path, "path", torch.int32)
+    if path is not None and (path.dim() != 2 or path.shape[0] != N):
+        raise ValueError(f"path must be [{N}, P], got {tuple(path.shape)}")
+    P = M if path is None else path.shape[1]
+    _dev(accept, "accept", torch.int32, (N,))
+    if lens_out is None:
+        lens_out = torch.empty_like(cache_lens)
+    _dev(lens_out, "lens_out", torch.int32, (N,))
+    st = lib.kda_cache_append(_ptr(k_new), _ptr(v_new), _ptr(path), _ptr(accept), _ptr(page_table),
+                              _ptr(cache_lens), N, M, P, k_cache.shape[0], k_cache.shape[2],
+                              page_table.shape[1], dims_of(k_new), _ptr(k_cache), _ptr(v_cache),
+                              _ptr(lens_out), _stream())
+    if st != KDA_OK:
+        raise KDAError(st, "kda_cache_append")
+    return lens_out
 
 
 def kda_get_device_status(workspace) -> int:
