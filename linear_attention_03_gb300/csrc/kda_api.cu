@@ -458,7 +458,7 @@ kda_status kda_decode_commit(const void *k, const void *v, const float *g, const
     g_last_error[0] = '\0';
     KDA_TRY(check_dims(dims));
     if (N < 0 || M < 1 || P < 1) return fail(KDA_ERR_INVALID, "N must be >= 0, M and P >= 1%s");
-    if ((int64_t)N * M > INT32_MAX || (int64_t)N * P > INT32_MAX || (int64_t)N * dims.H > INT32_MAX)
+    if ((int64_t)N * M > INT32_MAX || (int64_t)N * P > INT32_MAX || (int64_t)N * dims.H * 2 > INT32_MAX)
         return fail(KDA_ERR_INVALID, "N * M, N * P or N * H too large%s");
     if (N == 0) return KDA_OK;
     KDA_TRY(need(k, "k"));

@@ -14,6 +14,7 @@
 // Every product of decays is taken by walking up the line (factors <= 1), so
 // deep trees underflow to zero and never overflow.
 #include "kda_internal.cuh"
+#include "kda_tc.cuh"
 #include "kda_tree.cuh"
 
 namespace kda {
@@ -150,73 +151,486 @@ decode_tree_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const T
     }
 }
 
-// The state after the first accept[n] nodes of path[n]: a thread keeps one
-// state column in registers, and the column's read S^T k, the decay and the
-// write stay in that thread, so the state moves once in each direction and a
-// token costs no exchange between threads.
+// The state after the first accept[n] nodes of path[n].  A warp keeps 16 state
+// columns in registers: lane = (row group r of 8, column quad c of 4), rows
+// 8i + r, so that a column's read S^T k closes with three shuffles and the
+// warps never wait for one another.  The state moves once in each direction.
+// A CTA has up to four such warps, so d = 128 takes two CTAs per state.
+template <int D> struct CommitCfg {
+    static constexpr int WARPS = D < 64 ? D / 16 : 4, SPLIT = D / 16 / WARPS;
+};
 template <typename Tin, int D>
-__global__ void __launch_bounds__(D < 32 ? 32 : D)
+__global__ void __launch_bounds__(32 * CommitCfg<D>::WARPS, D == 128 ? 4 : 1)
 decode_commit_kernel(const Tin *__restrict__ k, const Tin *__restrict__ v, const float *__restrict__ g,
                      const float *__restrict__ beta, const float *state_in,
                      const int32_t *__restrict__ path, const int32_t *__restrict__ accept, int32_t M,
                      int32_t P, int32_t H, float *state_out) {
+    constexpr int SPLIT = CommitCfg<D>::SPLIT, THREADS = 32 * CommitCfg<D>::WARPS;
     constexpr int BATCH = 4;                         // path nodes staged at a time
-    __shared__ __align__(16) float2 ak[BATCH][D];   // (decay, k) per channel
+    constexpr int ROWS = D / 8;                      // state rows per lane
+    __shared__ __align__(16) float2 ak[BATCH][D];    // (decay, k) per channel
     __shared__ int32_t node[BATCH];
-    const int tid = threadIdx.x;
-    const int64_t n = blockIdx.x / H;
-    const int h = blockIdx.x % H;
-    const int c = tid < D ? tid : 0;
-    const size_t base = (size_t)blockIdx.x * D * D + c;
-    float s[D];
+    const int tid = threadIdx.x, lane = tid & 31, r = lane >> 2;
+    const int col = (blockIdx.x % SPLIT) * (16 * CommitCfg<D>::WARPS) + (tid >> 5) * 16 + (lane & 3) * 4;
+    const int unit = blockIdx.x / SPLIT;
+    const int64_t n = unit / H;
+    const int h = unit % H;
+    const size_t base = (size_t)unit * D * D + (size_t)r * D + col;
+    float4 s[ROWS];
 #pragma unroll
-    for (int i = 0; i < D; ++i) s[i] = __ldcs(state_in + base + (size_t)i * D);
+    for (int i = 0; i < ROWS; ++i)
+        s[i] = __ldcs(reinterpret_cast<const float4 *>(state_in + base + (size_t)i * 8 * D));
     int acc = accept[n];
     acc = acc < 0 ? 0 : (acc > P ? P : acc);
-    bool open = true;                                // no entry outside the tree so far
-    for (int t0 = 0; t0 < acc && open; t0 += BATCH) {
-        const int cnt = acc - t0 < BATCH ? acc - t0 : BATCH;
+    for (int t0 = 0; t0 < acc; t0 += BATCH) {
+        // the batch ends at its first entry outside the tree, and the path with it
+        int cnt = 0;
         __syncthreads();
-        if (tid < cnt) node[tid] = path[n * P + t0 + tid];
-        __syncthreads();
-        for (int t = 0; t < cnt; ++t) {
-            const int m = node[t];
-            if (m < 0 || m >= M) break;
-            if (tid < D) {
-                const int64_t at = ((n * M + m) * H + h) * D + tid;
-                ak[t][tid] = make_float2(__expf(g[at]), Elem<Tin>::load(k + at));
-            }
-        }
-        __syncthreads();
-        for (int t = 0; t < cnt; ++t) {
-            const int m = node[t];
+        for (; cnt < BATCH && t0 + cnt < acc; ++cnt) {
+            const int m = path[n * P + t0 + cnt];
             if (m < 0 || m >= M) {
-                open = false;
+                acc = 0;
                 break;
             }
-            const int64_t row = (n * M + m) * H + h;
-            const float vt = Elem<Tin>::load(v + row * D + c), bt = beta[row];
-            float x[4] = {0.f, 0.f, 0.f, 0.f};
+            if (tid == 0) node[cnt] = m;
+            const int64_t at = ((n * M + m) * H + h) * D;
+            for (int i = tid; i < D; i += THREADS)
+                ak[cnt][i] = make_float2(__expf(g[at + i]), Elem<Tin>::load(k + at + i));
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int t = 0; t < cnt; ++t) {
+            const int64_t row = (n * M + node[t]) * H + h;
+            const float bt = beta[row];
+            float vt[4];
 #pragma unroll
-            for (int i = 0; i < D; i += 2) {
-                const float4 f = *reinterpret_cast<const float4 *>(&ak[t][i]);
-                s[i] *= f.x;
-                s[i + 1] *= f.z;
-                x[i & 3] += f.y * s[i];
-                x[(i + 1) & 3] += f.w * s[i + 1];
+            for (int e = 0; e < 4; ++e) vt[e] = Elem<Tin>::load(v + row * D + col + e);
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                const float2 f = ak[t][i * 8 + r];
+                s[i].x *= f.x; s[i].y *= f.x; s[i].z *= f.x; s[i].w *= f.x;
+                x.x += f.y * s[i].x; x.y += f.y * s[i].y; x.z += f.y * s[i].z; x.w += f.y * s[i].w;
             }
-            const float u = bt * (vt - ((x[0] + x[1]) + (x[2] + x[3])));
 #pragma unroll
-            for (int i = 0; i < D; i += 2) {
-                const float4 f = *reinterpret_cast<const float4 *>(&ak[t][i]);
-                s[i] += f.y * u;
-                s[i + 1] += f.w * u;
+            for (int o = 4; o < 32; o <<= 1) {
+                x.x += __shfl_xor_sync(0xffffffffu, x.x, o);
+                x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
+                x.z += __shfl_xor_sync(0xffffffffu, x.z, o);
+                x.w += __shfl_xor_sync(0xffffffffu, x.w, o);
+            }
+            const float4 u = make_float4(bt * (vt[0] - x.x), bt * (vt[1] - x.y), bt * (vt[2] - x.z),
+                                         bt * (vt[3] - x.w));
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                const float ki = ak[t][i * 8 + r].y;
+                s[i].x += ki * u.x; s[i].y += ki * u.y; s[i].z += ki * u.z; s[i].w += ki * u.w;
             }
         }
     }
-    if (tid < D) {
 #pragma unroll
-        for (int i = 0; i < D; ++i) __stcs(state_out + base + (size_t)i * D, s[i]);
+    for (int i = 0; i < ROWS; ++i)
+        __stcs(reinterpret_cast<float4 *>(state_out + base + (size_t)i * 8 * D), s[i]);
+}
+
+// ---- bf16 inputs, d = 128: the products with S_0 on the tensor cores ----
+//
+// One CTA of four warps per (sequence, head).  Nodes 8i .. 8i+7 make row tile
+// i: rows 0-7 are E_m k_m, rows 8-15 E_m q_m, so a tile is full whether the
+// tree has 8 nodes or 64.  Warp w multiplies all tiles with state columns
+// 32w .. 32w+31 (mma.sync m16n8k16): a lane loads 16 bytes of four state rows
+// and takes its four columns as column g of four 8-wide tiles, so the fp32
+// state goes from HBM to the fragments without passing shared memory, in whole
+// 128-byte lines.
+//
+// The solve does not touch the 128 columns: with y = v - (the k sums) the
+// outputs are (the q sums) + W y, where row m of W lives on m's line.  Let s
+// count the steps up that line, j_s the node reached, A and B the line
+// products.  Then W_m,j_s = z_s beta_{j_s} with, from the bottom up,
+//     z_s = B_m,j_s - sum_{s' < s} z_s' beta_{j_s'} A_{j_s',j_s},
+// which eight lanes solve for each node in as many steps as its line is long,
+// all nodes at once.  W y is one more small product whose accumulators are the
+// q sums where they already are; y turns into its operand by 8x8 transposes in
+// registers.
+//
+// All operands are split into a bf16 part and a bf16 rest (16 significant bits
+// together), and three of the four partial products are summed in fp32: the
+// fourth is below 2^-16 of the product.
+constexpr int kTcThreads = 128;
+constexpr int kALd = 136;                             // bf16 per operand row: 17 x 16 bytes, no bank conflicts
+
+template <int TILES> struct TcCfg {
+    static constexpr int PAIRS = (TILES + 1) / 2;     // 16-node blocks of W
+    static constexpr int WLD = PAIRS * 16 + 8;        // bf16 per row of W: an odd number of 16-byte pieces
+    static constexpr size_t A_BYTES = (size_t)TILES * 16 * kALd * 2 * 2;
+    static constexpr size_t W_BYTES = (size_t)PAIRS * 16 * WLD * 2 * 2;
+    static size_t smem(int M) {
+        return A_BYTES + W_BYTES + (size_t)M * (128 * (4 + 4) + 16) + (size_t)M * M * (8 + 1);
+    }
+};
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&x);
+}
+__device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+// two floats as bf16 pairs: the rounded values and the rounded rests
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+    hi = pack2(a, b);
+    lo = pack2(a - lo_f(hi), b - hi_f(hi));
+}
+__device__ __forceinline__ void mma16816(float &d0, float &d1, float &d2, float &d3, const uint32_t (&a)[4],
+                                         uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};"
+                 : "+f"(d0), "+f"(d1), "+f"(d2), "+f"(d3)
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// an 8x8 tile of 16-bit values held as (row lane/4, columns 2(lane%4), +1), transposed
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+// a b + c on two pairs of fp32
+__device__ __forceinline__ float2 f2fma(float2 a, float2 b, float2 c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(tc::f2u(a)), "l"(tc::f2u(b)), "l"(tc::f2u(c)));
+    return tc::u2f(d);
+}
+__device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+
+template <int TILES>
+__global__ void __launch_bounds__(kTcThreads, TILES <= 2 ? 4 : TILES == 4 ? 3 : 1)
+decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ k,
+                      const __nv_bfloat16 *__restrict__ v, const float *__restrict__ g,
+                      const float *__restrict__ beta, const float *__restrict__ state,
+                      const int32_t *__restrict__ parent, int32_t M, int32_t H,
+                      __nv_bfloat16 *__restrict__ out) {
+    using C = TcCfg<TILES>;
+    constexpr int D = 128, KS = D / 16, WARPS = kTcThreads / 32;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    __nv_bfloat16 *ahi = reinterpret_cast<__nv_bfloat16 *>(smem_raw), *alo = ahi + TILES * 16 * kALd;
+    __nv_bfloat16 *whi = reinterpret_cast<__nv_bfloat16 *>(smem_raw + C::A_BYTES),
+                  *wlo = whi + C::PAIRS * 16 * C::WLD;
+    float *al = reinterpret_cast<float *>(smem_raw + C::A_BYTES + C::W_BYTES);
+    float *kk = al + M * D;
+    uint64_t *line = reinterpret_cast<uint64_t *>(kk + M * D);
+    // by steps up m's line: the products with the node reached, and its index
+    float2 *AB = reinterpret_cast<float2 *>(line + M);
+    int32_t *par = reinterpret_cast<int32_t *>(AB + M * M);
+    float *bet = reinterpret_cast<float *>(par + M);
+    uint8_t *up = reinterpret_cast<uint8_t *>(bet + M);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t n = blockIdx.x / H;
+    const int h = blockIdx.x % H;
+    const int64_t row0 = n * M * H + h;                // row of node m: row0 + m H
+    const float *S = state + (size_t)blockIdx.x * D * D;
+
+    // the state comes to the L2 while the line products run
+    if (tid == 0)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(S), "r"(D * D * 4) : "memory");
+    for (int m = tid; m < M; m += kTcThreads) {
+        par[m] = parent[n * M + m];
+        bet[m] = beta[row0 + (int64_t)m * H];
+    }
+    for (int i = tid; i < M * (D / 8); i += kTcThreads) {
+        const int m = i / (D / 8), c = i % (D / 8) * 8;
+        const int64_t at = (row0 + (int64_t)m * H) * D + c;
+        float x[8], y[8];
+        Elem<float>::load8(g + at, x);
+        Elem<__nv_bfloat16>::load8(k + at, y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __expf(x[e]);
+        Elem<float>::store8(al + m * D + c, x);
+        Elem<float>::store8(kk + m * D + c, y);
+    }
+    for (int i = tid; i < (int)(C::W_BYTES / 16); i += kTcThreads)
+        reinterpret_cast<uint4 *>(whi)[i] = make_uint4(0u, 0u, 0u, 0u);
+    // line products: eight lanes per node, channels 32 p + 4 (lane % 8) .. + 3
+    const int l8 = lane & 7;
+    const unsigned group = 0xffu << (lane & 24);
+    int m = warp * 4 + (lane >> 3);
+    uint2 qm[4];
+    auto load_q = [&]() {
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+            qm[p] = m < M ? __ldg(reinterpret_cast<const uint2 *>(q + (row0 + (int64_t)m * H) * D + 32 * p + 4 * l8))
+                          : make_uint2(0u, 0u);
+    };
+    load_q();
+    __syncthreads();
+    for (; m < TILES * 8; m += 4 * WARPS) {
+        float2 kd[8], qd[8];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const float4 f = m < M ? *reinterpret_cast<const float4 *>(kk + m * D + 32 * p + 4 * l8)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+            kd[2 * p] = make_float2(f.x, f.y);
+            kd[2 * p + 1] = make_float2(f.z, f.w);
+            qd[2 * p] = make_float2(lo_f(qm[p].x), hi_f(qm[p].x));
+            qd[2 * p + 1] = make_float2(lo_f(qm[p].y), hi_f(qm[p].y));
+        }
+        uint64_t on = 0;
+        int at = m < M ? m : -1, steps = 0;
+        bool whole = false;                           // the walk ended below the prefix
+        float a = 0.f, b = 0.f;
+        // lanes 0-3 of the group sum the k products of a step, lanes 4-7 the q products
+        auto close = [&](int step) {
+            float x = (l8 < 4 ? a : b) + __shfl_xor_sync(group, l8 < 4 ? b : a, 4);
+            x += __shfl_xor_sync(group, x, 2);
+            x += __shfl_xor_sync(group, x, 1);
+            if ((l8 & 3) == 0) reinterpret_cast<float *>(AB + m * M + step)[l8 >> 2] = x;
+        };
+        while (at >= 0) {
+            const int next = par[at];
+            float4 kj[4], aj[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                kj[p] = *reinterpret_cast<const float4 *>(kk + at * D + 32 * p + 4 * l8);
+                aj[p] = *reinterpret_cast<const float4 *>(al + at * D + 32 * p + 4 * l8);
+            }
+            if (steps > 0) close(steps - 1);          // the step before, while these load
+            if (l8 == 1) up[m * M + steps] = (uint8_t)at;
+            on |= uint64_t{1} << at;
+            float2 a2[2], b2[2];
+            a2[0] = a2[1] = b2[0] = b2[1] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const float2 k0 = make_float2(kj[p].x, kj[p].y), k1 = make_float2(kj[p].z, kj[p].w);
+                const float2 a0 = make_float2(aj[p].x, aj[p].y), a1 = make_float2(aj[p].z, aj[p].w);
+                a2[0] = f2fma(kd[2 * p], k0, a2[0]);
+                a2[1] = f2fma(kd[2 * p + 1], k1, a2[1]);
+                b2[0] = f2fma(qd[2 * p], k0, b2[0]);
+                b2[1] = f2fma(qd[2 * p + 1], k1, b2[1]);
+                kd[2 * p] = tc::f2mul(kd[2 * p], a0);
+                kd[2 * p + 1] = tc::f2mul(kd[2 * p + 1], a1);
+                qd[2 * p] = tc::f2mul(qd[2 * p], a0);
+                qd[2 * p + 1] = tc::f2mul(qd[2 * p + 1], a1);
+            }
+            a = (a2[0].x + a2[0].y) + (a2[1].x + a2[1].y);
+            b = (b2[0].x + b2[0].y) + (b2[1].x + b2[1].y);
+            ++steps;
+            whole = next == -1;
+            at = next < at ? next : -2;
+        }
+        if (steps > 0) close(steps - 1);
+        if (!whole) {
+            on = 0;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) kd[x] = qd[x] = make_float2(0.f, 0.f);
+        }
+        if (l8 == 0 && m < M) line[m] = on;
+        // row of the k operand, and eight rows on the q operand (zeros where there is no node)
+        const int row = (m >> 3) * 16 + (m & 7);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const int c = 32 * p + 4 * l8;
+            uint32_t hi[2], lo[2];
+            split2(kd[2 * p].x, kd[2 * p].y, hi[0], lo[0]);
+            split2(kd[2 * p + 1].x, kd[2 * p + 1].y, hi[1], lo[1]);
+            *reinterpret_cast<uint2 *>(ahi + row * kALd + c) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2 *>(alo + row * kALd + c) = make_uint2(lo[0], lo[1]);
+            split2(qd[2 * p].x, qd[2 * p].y, hi[0], lo[0]);
+            split2(qd[2 * p + 1].x, qd[2 * p + 1].y, hi[1], lo[1]);
+            *reinterpret_cast<uint2 *>(ahi + (row + 8) * kALd + c) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2 *>(alo + (row + 8) * kALd + c) = make_uint2(lo[0], lo[1]);
+        }
+        m += 4 * WARPS;
+        load_q();
+        m -= 4 * WARPS;
+    }
+    // the first state rows and the values set out before the operands are ready
+    const int gq = lane & 3, gg = lane >> 2;
+    const float *Sw = S + (size_t)(2 * gq) * D + warp * 32 + gg * 4;
+    auto fetch = [&](int ks, float4 (&f)[4]) {
+        const float *p = Sw + (size_t)ks * 16 * D;
+        f[0] = __ldcs(reinterpret_cast<const float4 *>(p));
+        f[1] = __ldcs(reinterpret_cast<const float4 *>(p + D));
+        f[2] = __ldcs(reinterpret_cast<const float4 *>(p + 8 * D));
+        f[3] = __ldcs(reinterpret_cast<const float4 *>(p + 9 * D));
+    };
+    constexpr int AHEAD = TILES <= 4 ? 2 : 1;         // steps of 16 state rows on their way
+    float4 buf[AHEAD + 1][4];
+    const int64_t vcol = warp * 32 + 8 * gq;          // values of node 8i + gg, state columns vcol .. + 7
+    uint4 vv[TILES];
+#pragma unroll
+    for (int ks = 0; ks < AHEAD; ++ks) fetch(ks, buf[ks]);
+#pragma unroll
+    for (int i = 0; i < TILES; ++i) {
+        const int mm = 8 * i + gg;
+        vv[i] = mm < M ? __ldg(reinterpret_cast<const uint4 *>(v + (row0 + (int64_t)mm * H) * D + vcol))
+                       : make_uint4(0u, 0u, 0u, 0u);
+    }
+    __syncthreads();
+
+    // the rows of W: eight lanes per node, lane l8 the steps l8, l8 + 8, ...
+    for (m = warp * 4 + (lane >> 3); m < M; m += 4 * WARPS) {
+        const int steps = __popcll((long long)line[m]);
+        float z[TILES];
+#pragma unroll
+        for (int r = 0; r < TILES; ++r) z[r] = 8 * r + l8 < steps ? AB[m * M + 8 * r + l8].y : 0.f;
+#pragma unroll
+        for (int r = 0; r < TILES; ++r) {
+            for (int s8 = 0; s8 < 8 && 8 * r + s8 < steps; ++s8) {
+                const int s = 8 * r + s8, j = up[m * M + s];
+                const float w = __shfl_sync(group, z[r], s8, 8) * bet[j];
+                const float2 *ab = AB + j * M - s;
+#pragma unroll
+                for (int i = r; i < TILES; ++i) {
+                    const int t = 8 * i + l8;
+                    if (t > s && t < steps) z[i] -= w * ab[t].x;
+                }
+                if (l8 == 0) {
+                    const __nv_bfloat16 hi = __float2bfloat16_rn(w);
+                    whi[m * C::WLD + j] = hi;
+                    wlo[m * C::WLD + j] = __float2bfloat16_rn(w - __bfloat162float(hi));
+                }
+            }
+        }
+    }
+
+    float acc[TILES][4][4];
+#pragma unroll
+    for (int i = 0; i < TILES; ++i)
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][t][e] = 0.f;
+    const uint32_t frag = (uint32_t)(lane & 15), piece = (uint32_t)(lane >> 4) * 16;
+    const uint32_t abase = static_cast<uint32_t>(__cvta_generic_to_shared(ahi)) + frag * (kALd * 2) + piece;
+    constexpr uint32_t kALo = TILES * 16 * kALd * 2;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+        if (ks + AHEAD < KS) fetch(ks + AHEAD, buf[(ks + AHEAD) % (AHEAD + 1)]);
+        const float4 *f = buf[ks % (AHEAD + 1)];
+        uint32_t bh[4][2], bl[4][2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            split2(f[2 * half].x, f[2 * half + 1].x, bh[0][half], bl[0][half]);
+            split2(f[2 * half].y, f[2 * half + 1].y, bh[1][half], bl[1][half]);
+            split2(f[2 * half].z, f[2 * half + 1].z, bh[2][half], bl[2][half]);
+            split2(f[2 * half].w, f[2 * half + 1].w, bh[3][half], bl[3][half]);
+        }
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) {
+            uint32_t xh[4], xl[4];
+            ldsm4(abase + (i * 16 * kALd + ks * 16) * 2, xh);
+            ldsm4(abase + (i * 16 * kALd + ks * 16) * 2 + kALo, xl);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                float(&d)[4] = acc[i][t];
+                mma16816(d[0], d[1], d[2], d[3], xh, bh[t][0], bh[t][1]);
+                mma16816(d[0], d[1], d[2], d[3], xh, bl[t][0], bl[t][1]);
+                mma16816(d[0], d[1], d[2], d[3], xl, bh[t][0], bh[t][1]);
+            }
+        }
+    }
+    // lane (gg, gq): node 8i + gg's k sums (entries 0, 1; they become y) and q sums
+    // (2, 3) of the tile columns 2 gq and 2 gq + 1, i.e. columns vcol + t and vcol + 4 + t
+    float clean = 0.f;                                // NaN once any y is not finite
+#pragma unroll
+    for (int i = 0; i < TILES; ++i) {
+        const uint32_t u[4] = {vv[i].x, vv[i].y, vv[i].z, vv[i].w};
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            acc[i][t][0] = ((t & 1) ? hi_f(u[t >> 1]) : lo_f(u[t >> 1])) - acc[i][t][0];
+            acc[i][t][1] = ((t & 1) ? hi_f(u[2 + (t >> 1)]) : lo_f(u[2 + (t >> 1)])) - acc[i][t][1];
+            clean += 0.f * acc[i][t][0];
+            clean += 0.f * acc[i][t][1];
+        }
+    }
+    const bool dirty = __any_sync(0xffffffffu, clean != 0.f);
+    __syncthreads();                                  // W is there
+    // A y that is not finite belongs to its own line only: the dense product
+    // takes a zero in its place, and it is added where it is seen
+    float seen[TILES][4][2];
+    if (dirty) {
+#pragma unroll
+        for (int i = 0; i < TILES; ++i)
+#pragma unroll
+            for (int x = 0; x < 8; ++x) seen[i][x >> 1][x & 1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) {
+#pragma unroll 1
+            for (int r = 0; r < 8 && 8 * i + r < M; ++r) {
+                float y[4][2];
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    y[x >> 1][x & 1] = __shfl_sync(0xffffffffu, acc[i][x >> 1][x & 1], r * 4 + gq);
+#pragma unroll
+                for (int o = 0; o < TILES; ++o) {
+                    const int m = 8 * o + gg;
+                    if (m >= M || (line[m] >> (8 * i + r) & 1) == 0) continue;
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        if (!is_finite(y[x >> 1][x & 1])) seen[o][x >> 1][x & 1] += y[x >> 1][x & 1];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < TILES; ++i)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                if (!is_finite(acc[i][t][0])) acc[i][t][0] = 0.f;
+                if (!is_finite(acc[i][t][1])) acc[i][t][1] = 0.f;
+            }
+    }
+    uint32_t yh[2 * C::PAIRS][4], yl[2 * C::PAIRS][4];
+#pragma unroll
+    for (int i = 0; i < 2 * C::PAIRS; ++i)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            yh[i][t] = yl[i][t] = 0u;
+            if (i < TILES) {
+                uint32_t hi, lo;
+                split2(acc[i % TILES][t][0], acc[i % TILES][t][1], hi, lo);
+                yh[i][t] = transpose8x8(hi);
+                yl[i][t] = transpose8x8(lo);
+            }
+        }
+    const uint32_t wbase = static_cast<uint32_t>(__cvta_generic_to_shared(whi)) + frag * (C::WLD * 2) + piece;
+    constexpr uint32_t kWLo = C::PAIRS * 16 * C::WLD * 2;
+#pragma unroll
+    for (int i = 0; i < C::PAIRS; ++i) {
+        float none[4][2];                             // the upper half of a lone tile
+#pragma unroll
+        for (int t = 0; t < 4; ++t) none[t][0] = none[t][1] = 0.f;
+#pragma unroll
+        for (int b = 0; b <= i; ++b) {                // nodes above have lower indices
+            uint32_t xh[4], xl[4];
+            ldsm4(wbase + (i * 16 * C::WLD + b * 16) * 2, xh);
+            ldsm4(wbase + (i * 16 * C::WLD + b * 16) * 2 + kWLo, xl);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                float &d0 = acc[2 * i][t][2], &d1 = acc[2 * i][t][3];
+                float &d2 = 2 * i + 1 < TILES ? acc[(2 * i + 1) % TILES][t][2] : none[t][0];
+                float &d3 = 2 * i + 1 < TILES ? acc[(2 * i + 1) % TILES][t][3] : none[t][1];
+                mma16816(d0, d1, d2, d3, xh, yh[2 * b][t], yh[2 * b + 1][t]);
+                mma16816(d0, d1, d2, d3, xh, yl[2 * b][t], yl[2 * b + 1][t]);
+                mma16816(d0, d1, d2, d3, xl, yh[2 * b][t], yh[2 * b + 1][t]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < TILES; ++i) {
+        const int m = 8 * i + gg;
+        if (m >= M) continue;
+        if (dirty) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                acc[i][t][2] += seen[i][t][0];
+                acc[i][t][3] += seen[i][t][1];
+            }
+        }
+        *reinterpret_cast<uint4 *>(out + (row0 + (int64_t)m * H) * D + vcol) =
+            make_uint4(pack2(acc[i][0][2], acc[i][1][2]), pack2(acc[i][2][2], acc[i][3][2]),
+                       pack2(acc[i][0][3], acc[i][1][3]), pack2(acc[i][2][3], acc[i][3][3]));
     }
 }
 
@@ -234,11 +648,27 @@ cudaError_t run_tree(const void *q, const void *k, const void *v, const float *g
     return cudaGetLastError();
 }
 
+template <int TILES>
+cudaError_t run_tree_tc(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                        const float *state, const int32_t *parent, int32_t N, int32_t M, int32_t H,
+                        void *out, cudaStream_t stream) {
+    static std::atomic<uint64_t> smem_set{0};
+    cudaError_t e = allow_dynamic_smem(decode_tree_tc_kernel<TILES>, TcCfg<TILES>::smem(8 * TILES), smem_set);
+    if (e != cudaSuccess) return e;
+    decode_tree_tc_kernel<TILES><<<(unsigned)N * (unsigned)H, kTcThreads, TcCfg<TILES>::smem(M), stream>>>(
+        static_cast<const __nv_bfloat16 *>(q), static_cast<const __nv_bfloat16 *>(k),
+        static_cast<const __nv_bfloat16 *>(v), g, beta, state, parent, M, H,
+        static_cast<__nv_bfloat16 *>(out));
+    count_launches(1);
+    return cudaGetLastError();
+}
+
 template <typename Tin, int D>
 cudaError_t run_commit(const void *k, const void *v, const float *g, const float *beta,
                        const float *state_in, const int32_t *path, const int32_t *accept, int32_t N,
                        int32_t M, int32_t P, int32_t H, float *state_out, cudaStream_t stream) {
-    decode_commit_kernel<Tin, D><<<(unsigned)N * (unsigned)H, D < 32 ? 32 : D, 0, stream>>>(
+    decode_commit_kernel<Tin, D><<<(unsigned)N * (unsigned)H * CommitCfg<D>::SPLIT, 32 * CommitCfg<D>::WARPS, 0,
+                                    stream>>>(
         static_cast<const Tin *>(k), static_cast<const Tin *>(v), g, beta, state_in, path, accept, M, P,
         H, state_out);
     count_launches(1);
@@ -260,6 +690,13 @@ cudaError_t launch_decode_tree(const void *q, const void *k, const void *v, cons
                                const float *beta, const float *state, const int32_t *parent, int32_t N,
                                int32_t M, int32_t H, int32_t D, kda_dtype dt, void *out,
                                cudaStream_t stream) {
+    if (dt == KDA_BF16 && D == 128) {
+        // row tiles of eight nodes, as few as hold M
+        if (M <= 8) return run_tree_tc<1>(q, k, v, g, beta, state, parent, N, M, H, out, stream);
+        if (M <= 16) return run_tree_tc<2>(q, k, v, g, beta, state, parent, N, M, H, out, stream);
+        if (M <= 32) return run_tree_tc<4>(q, k, v, g, beta, state, parent, N, M, H, out, stream);
+        return run_tree_tc<8>(q, k, v, g, beta, state, parent, N, M, H, out, stream);
+    }
     if (dt == KDA_BF16)
         KDA_DISPATCH_D(D, (run_tree<__nv_bfloat16, DD>(q, k, v, g, beta, state, parent, N, M, H, out, stream)))
     KDA_DISPATCH_D(D, (run_tree<float, DD>(q, k, v, g, beta, state, parent, N, M, H, out, stream)))
