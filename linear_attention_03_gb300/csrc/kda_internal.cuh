@@ -208,6 +208,10 @@ size_t tree_attention_partial_bytes(int32_t N, int32_t M, int32_t H, int32_t H_k
                                     int32_t page_size, int32_t max_pages);
 cudaError_t launch_tree_attention(const TreeAttention &a, int32_t D, kda_dtype dt, void *workspace,
                                   cudaStream_t stream);
+// the same on the tensor cores: bf16, d = 64 or 128, pages of whole groups of eight tokens
+bool tree_attention_tc_supported(int32_t H_kv, int32_t D, kda_dtype dt, int64_t num_pages, int32_t page_size);
+size_t tree_attention_tc_partial_bytes(int32_t M, int32_t H, int32_t H_kv, int32_t D);
+cudaError_t launch_tree_attention_tc(const TreeAttention &a, int32_t D, void *workspace, cudaStream_t stream);
 
 cudaError_t launch_verify_drafts(const void *target, const void *draft, const int32_t *tokens,
                                  const int32_t *parent, const float *uniforms, int32_t N, int32_t M,

@@ -297,12 +297,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-// a b + c on two pairs of fp32
-__device__ __forceinline__ float2 f2fma(float2 a, float2 b, float2 c) {
-    unsigned long long d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(tc::f2u(a)), "l"(tc::f2u(b)), "l"(tc::f2u(c)));
-    return tc::u2f(d);
-}
 __device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
 template <int TILES>
@@ -404,10 +398,10 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
             for (int p = 0; p < 4; ++p) {
                 const float2 k0 = make_float2(kj[p].x, kj[p].y), k1 = make_float2(kj[p].z, kj[p].w);
                 const float2 a0 = make_float2(aj[p].x, aj[p].y), a1 = make_float2(aj[p].z, aj[p].w);
-                a2[0] = f2fma(kd[2 * p], k0, a2[0]);
-                a2[1] = f2fma(kd[2 * p + 1], k1, a2[1]);
-                b2[0] = f2fma(qd[2 * p], k0, b2[0]);
-                b2[1] = f2fma(qd[2 * p + 1], k1, b2[1]);
+                a2[0] = tc::f2fma(kd[2 * p], k0, a2[0]);
+                a2[1] = tc::f2fma(kd[2 * p + 1], k1, a2[1]);
+                b2[0] = tc::f2fma(qd[2 * p], k0, b2[0]);
+                b2[1] = tc::f2fma(qd[2 * p + 1], k1, b2[1]);
                 kd[2 * p] = tc::f2mul(kd[2 * p], a0);
                 kd[2 * p + 1] = tc::f2mul(kd[2 * p + 1], a1);
                 qd[2 * p] = tc::f2mul(qd[2 * p], a0);

@@ -1,0 +1,723 @@
+// kda_tree_attention_tc.cu -- tree attention over a paged cache on the tensor
+// cores (tcgen05): bf16, head sizes 64 and 128, page sizes that are multiples
+// of 8.  The mathematics is that of kda_tree_attention.cu.
+//
+// All M x G rows of a cache head read the same keys, so they make the row
+// dimension of one product: tiles of 128 rows against tiles of 128 keys,
+// S = Q K^T into TMEM, the weights back into TMEM as the operand of O += P V.
+// One tile (QT = 1) or two (QT = 2, more than 128 rows) share each key tile in
+// shared memory.  The work is bound by the bytes of the cache as long as one
+// key tile's two products per row tile (2 x 512 clocks at d = 128) and its
+// softmax stay below the tile's 64 KB at the SM's share of HBM (~2,800 clocks).
+//
+// Split: every (sequence, cache head, row group) is a unit of ceil(len / 128)
+// + 1 key tiles, the last of them the tree.  The units' tiles in one line are
+// cut into equal pieces, one per CTA, one CTA per SM: ragged lengths cost no
+// imbalance, and a long cache needs no separate split.  Only the two ends of a
+// piece can be parts of a unit; those go to the workspace as sums, and a second
+// kernel joins them.  The cut depends on the lengths alone, so results repeat
+// bit for bit.
+//
+// Roles: warp 0 loads (TMA, one box per page or part of one), warp 1 issues the
+// products, a warpgroup per row tile does the softmax with a thread per row
+// (the running maximum needs no exchange).  The sums are rescaled only when the
+// maximum grows by more than 2^8: weights up to 2^8 lose nothing in bf16 or in
+// the fp32 sums.  The weights are rounded to bf16 for the product (2^-9
+// relative, the size of the output's own rounding); maximum, sum and output
+// sums are fp32.
+#include "kda_internal.cuh"
+#include "kda_tc.cuh"
+#include "kda_tree.cuh"
+
+#include <cuda.h>
+#include <math.h>
+
+namespace kda {
+namespace {
+
+using namespace tc;
+
+constexpr int kTile = 128;                 // rows per row tile, keys per key tile
+constexpr int kMinTiles = 2;               // key tiles per CTA at least
+constexpr float kGrow = 8.f;               // log2 growth of the maximum that rescales the sums
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+template <int D, int QT> struct Cfg {
+    static constexpr int HALVES = D / 64;
+    static constexpr int THREADS = 128 + 128 * QT;
+    static constexpr int SLOT = kTile * D * 2;                    // bytes of a key or value tile
+    static constexpr int SLOTS = D == 64 ? 8 : (QT == 1 ? 6 : 5);
+    static constexpr int Q_BYTES = QT * SLOT;
+    static constexpr int O_RING = Q_BYTES;
+    static constexpr int O_MISC = O_RING + SLOTS * SLOT;
+    static constexpr int NBARS = 2 * SLOTS + 9;
+    static constexpr int O_LINES = O_MISC + 8 * NBARS, O_WORDS = O_LINES + 8 * kMaxTreeNodes;
+    static constexpr int SMEM = O_MISC + 1024;
+    static_assert(O_WORDS + 64 <= SMEM, "misc");
+    // TMEM columns: scores (and the weights in their place), then the sums
+    static constexpr int TM_O = 256;
+};
+static_assert(Cfg<128, 1>::SMEM <= 232448 && Cfg<128, 2>::SMEM <= 232448, "227 KB of shared memory");
+
+// misc: the mbarriers, the tree's lines, then these 32-bit words
+enum { W_TMEM = 0, W_ABORT, W_BAD0, W_BAD1, W_WORDS };
+
+struct Maps {
+    CUtensorMap k, v, kn, vn;
+};
+
+struct Shape {
+    int32_t box;            // rows per load: the power of two that divides the page size, at most 128
+    int32_t groups;         // row groups (q tiles of QT x 128 rows) per cache head
+    int32_t ctas;
+    float *part;            // two slots per CTA: D/4 x rows float4, then rows maxima, rows sums
+};
+
+__device__ __forceinline__ int clamped_len(const TreeAttention &a, int64_t n) {
+    const int len = a.cache_lens[n];
+    const int64_t room = (int64_t)a.max_pages * a.page_size;
+    return len < 0 ? 0 : (len > room ? (int)room : len);
+}
+__device__ __forceinline__ int unit_tiles(int len) { return (len + kTile - 1) / kTile + 1; }
+
+// where CTA b's piece of `total` tiles starts
+__device__ __forceinline__ int64_t piece_start(int64_t total, int ctas, int b) {
+    if (total < (int64_t)ctas * kMinTiles) {
+        const int64_t s = (int64_t)b * kMinTiles;
+        return s < total ? s : total;
+    }
+    return total * b / ctas;
+}
+
+// The line of all tiles: total, and the sequence and unit that hold tile `at`.
+struct Place {
+    int64_t total, unit0;   // unit0: where the unit starts on the line
+    int32_t n, r, len;      // sequence, unit within it, its clamped length
+};
+// The whole block calls it; `buf` holds 34 int64 of shared memory.
+__device__ void find_place(const TreeAttention &a, int groups, int ctas, int b, int64_t *buf, Place &out) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    const int per_seq = a.H_kv * groups;
+    int64_t sum = 0;
+    for (int n = tid; n < a.N; n += blockDim.x) {
+        const int len = a.cache_lens[n];
+        if (len < 0 || len > (int64_t)a.max_pages * a.page_size) flag_status(a.status, KDA_DEVICE_BAD_LENGTH);
+        sum += (int64_t)unit_tiles(clamped_len(a, n)) * per_seq;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) buf[warp] = sum;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < warps; ++w) total += buf[w];
+    __syncthreads();
+    out.total = total;
+    const int64_t at = piece_start(total, ctas, b);
+    if (warp == 0) {
+        // one warp walks the sequences, 32 at a time
+        int64_t base = 0;
+        for (int n0 = 0; n0 < a.N; n0 += 32) {
+            const int n = n0 + lane;
+            const int len = n < a.N ? clamped_len(a, n) : 0;
+            const int64_t mine = n < a.N ? (int64_t)unit_tiles(len) * per_seq : 0;
+            int64_t run = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, run, o);
+                if (lane >= o) run += x;
+            }
+            const int64_t begin = base + run - mine;
+            if (mine > 0 && at >= begin && at < begin + mine) {
+                const int64_t r = (at - begin) / unit_tiles(len);
+                buf[0] = n;
+                buf[1] = r;
+                buf[2] = begin + r * unit_tiles(len);
+                buf[3] = len;
+            }
+            base += __shfl_sync(0xffffffffu, run, 31);
+            if (at < base) break;
+        }
+    }
+    __syncthreads();
+    out.n = (int32_t)buf[0];
+    out.r = (int32_t)buf[1];
+    out.unit0 = buf[2];
+    out.len = (int32_t)buf[3];
+}
+
+// A CTA's run through its piece: segments are the parts of units in it.
+struct Run {
+    int64_t left;           // tiles still to do
+    int32_t n, r, len, t0;  // the current unit and its first tile here
+    int32_t tiles;          // tiles of the unit
+    __device__ __forceinline__ int count() const { return left < tiles - t0 ? (int)left : tiles - t0; }
+    __device__ __forceinline__ void advance(const TreeAttention &a, int groups) {
+        left -= count();
+        t0 = 0;
+        if (++r == a.H_kv * groups) {
+            r = 0;
+            if (++n < a.N && left > 0) {
+                len = clamped_len(a, n);
+                tiles = unit_tiles(len);
+            }
+        }
+    }
+};
+
+template <int D, int QT>
+__global__ void __launch_bounds__(Cfg<D, QT>::THREADS, 1)
+tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention a, const Shape sh) {
+    using C = Cfg<D, QT>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const uint32_t base = smem_u32(smem);
+    volatile uint32_t *words = reinterpret_cast<uint32_t *>(smem + C::O_WORDS);
+    uint64_t *line = reinterpret_cast<uint64_t *>(smem + C::O_LINES);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int G = a.H / a.H_kv, rows = a.M * G;
+
+    const uint32_t bars = base + C::O_MISC;
+    auto full = [&](int s) { return bars + 8u * s; };
+    auto empty = [&](int s) { return bars + 8u * (C::SLOTS + s); };
+    auto s_full = [&](int b) { return bars + 8u * (2 * C::SLOTS + b); };
+    auto p_full = [&](int b) { return bars + 8u * (2 * C::SLOTS + 2 + b); };
+    auto o_full = [&](int t) { return bars + 8u * (2 * C::SLOTS + 4 + t); };
+    auto q_full = [&](int t) { return bars + 8u * (2 * C::SLOTS + 6 + t); };
+    const uint32_t meet_bar = bars + 8u * (2 * C::SLOTS + 8);
+
+    Place place;
+    find_place(a, sh.groups, sh.ctas, blockIdx.x, reinterpret_cast<int64_t *>(smem), place);
+    const int64_t start = piece_start(place.total, sh.ctas, blockIdx.x);
+    const int64_t stop = piece_start(place.total, sh.ctas, blockIdx.x + 1);
+    if (start >= stop) return;                               // the whole block
+    Run run;
+    run.left = stop - start;
+    run.n = place.n;
+    run.r = place.r;
+    run.len = place.len;
+    run.tiles = unit_tiles(place.len);
+    run.t0 = (int32_t)(start - place.unit0);
+
+    if (warp == 0) tmem_alloc(base + C::O_WORDS + 4 * W_TMEM, 512);
+    if (tid == 32) {
+        for (int s = 0; s < C::SLOTS; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(s_full(b), 1);
+            mbar_init(p_full(b), 128);
+            mbar_init(o_full(b), 1);
+            mbar_init(q_full(b), 128);
+        }
+        mbar_init(meet_bar, 128 * QT);
+        fence_mbar_init();
+        words[W_ABORT] = 0;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = words[W_TMEM];
+    bool ok = true;
+    // a bounded wait of a whole warp; once one gives up, the warp stops
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (ok) {
+            ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
+            if (!ok) {
+                words[W_ABORT] = 1;
+                flag_status(a.status, KDA_DEVICE_TIMEOUT);
+            }
+        }
+        return ok;
+    };
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- loads
+        const uint32_t box_bytes = (uint32_t)sh.box * D * 2;
+        const int32_t none = (int32_t)((int64_t)a.num_pages * a.H_kv * a.page_size / 8);   // past the end: zeros
+        uint32_t use = 0;                                    // ring uses so far: K of tile j is 2j, V 2j + 1
+        for (; run.left > 0 && ok; run.advance(a, sh.groups)) {
+            const int h = run.r / sh.groups, cnt = run.count();
+            const int32_t *table = a.page_table + (int64_t)run.n * a.max_pages;
+            for (int t = run.t0; t < run.t0 + cnt && ok; ++t) {
+                const bool tree = t == run.tiles - 1;
+                const int valid = tree ? a.M : min(kTile, run.len - t * kTile);
+                const int loads = tree ? (a.M + 7) / 8 : (valid + sh.box - 1) / sh.box;
+                int32_t group = 0;
+                if (!tree && lane < loads) {
+                    const int pos = t * kTile + lane * sh.box;
+                    const int page = table[pos / a.page_size];
+                    if (page < 0 || page >= a.num_pages) {
+                        flag_status(a.status, KDA_DEVICE_BAD_PAGE);
+                        group = none;
+                    } else {
+                        group = (int32_t)((((int64_t)page * a.H_kv + h) * a.page_size + pos % a.page_size) / 8);
+                    }
+                }
+                const uint32_t bytes = tree ? (uint32_t)loads * 8 * D * 2 : (uint32_t)loads * box_bytes;
+#pragma unroll 1
+                for (int kv = 0; kv < 2; ++kv, ++use) {
+                    const int s = use % C::SLOTS;
+                    if (use >= C::SLOTS && !wait(empty(s), (use / C::SLOTS - 1) & 1)) break;
+                    if (lane == 0) mbar_expect_tx(full(s), bytes);
+                    __syncwarp();
+                    const uint32_t dst = base + C::O_RING + s * C::SLOT;
+                    if (lane < loads) {
+                        if (tree)
+                            tma_load_4d(dst + lane * 8 * D * 2, kv ? &maps.vn : &maps.kn, 0, run.n * a.M + lane * 8, 0,
+                                        h, full(s));
+                        else
+                            tma_load_4d(dst + lane * box_bytes, kv ? &maps.v : &maps.k, 0, 0, 0, group, full(s));
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        if (words[W_ABORT] != 0 || !ok) {
+            // loads in flight land before the block leaves
+            for (int s = 0; s < C::SLOTS; ++s)
+                if (use > (uint32_t)s) {
+                    const uint32_t last = (use - 1 - s) / C::SLOTS;
+                    mbar_wait(full(s), last & 1, 100000000ull);
+                }
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- products
+        constexpr uint32_t ID_QK = idesc_bf16(kTile, kTile, 0, 0), ID_QK64 = idesc_bf16(kTile, 64, 0, 0);
+        constexpr uint32_t ID_PV = idesc_bf16(kTile, D, 0, 1);
+        constexpr uint64_t HI_Q = sw128_hi(0, 1024), HI_K = sw128_hi(0, C::HALVES * 1024);
+        constexpr uint64_t HI_V = sw128_hi(1024, C::HALVES * 1024);
+        uint32_t j = 0, seg = 0;
+        auto slot = [&](uint32_t use) { return base + C::O_RING + (use % C::SLOTS) * C::SLOT; };
+        auto slot_wait = [&](uint32_t use) { return wait(full(use % C::SLOTS), (use / C::SLOTS) & 1); };
+        // scores of row tile t against the keys of tile jj
+        auto scores = [&](int t, uint32_t jj, uint32_t s_col, int cols) {
+            const uint32_t kb = slot(2 * jj), qb = base + t * C::SLOT;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+                mma_bf16_w(tmem + s_col, HI_Q | sw128_lo(qb + (ks >> 2) * 16384 + (ks & 3) * 32),
+                           HI_K | sw128_lo(kb + (ks >> 2) * 1024 + (ks & 3) * 32), cols == 64 ? ID_QK64 : ID_QK, ks > 0);
+        };
+        auto values = [&](int t, uint32_t jj, uint32_t s_col, int steps, bool first) {
+            const uint32_t vb = slot(2 * jj + 1);
+            for (int ks = 0; ks < steps; ++ks)
+                mma_tmem_a_w(tmem + C::TM_O + t * 128, tmem + s_col + ks * 8,
+                             HI_V | sw128_lo(vb + ks * 2 * C::HALVES * 1024), ID_PV, !(first && ks == 0));
+        };
+        auto valid_of = [&](int t) { return t == run.tiles - 1 ? a.M : min(kTile, run.len - t * kTile); };
+        for (; run.left > 0 && ok; run.advance(a, sh.groups), ++seg) {
+            const int cnt = run.count();
+            for (int t = 0; t < QT; ++t) wait(q_full(t), seg & 1);
+            tc_fence_after();
+            if constexpr (QT == 1) {
+                for (int i = 0; i <= cnt && ok; ++i) {
+                    if (i < cnt) {
+                        const uint32_t jj = j + i;
+                        if (!slot_wait(2 * jj)) break;
+                        scores(0, jj, (jj & 1) * 128, valid_of(run.t0 + i) <= 64 ? 64 : 128);
+                        mma_commit_w(s_full(jj & 1));
+                        mma_commit_w(empty((2 * jj) % C::SLOTS));
+                    }
+                    if (i > 0) {
+                        const uint32_t jj = j + i - 1;
+                        if (!wait(p_full(jj & 1), (jj >> 1) & 1) || !slot_wait(2 * jj + 1)) break;
+                        tc_fence_after();
+                        values(0, jj, (jj & 1) * 128, (valid_of(run.t0 + i - 1) + 15) / 16, i == 1);
+                        mma_commit_w(o_full(0));
+                        mma_commit_w(empty((2 * jj + 1) % C::SLOTS));
+                    }
+                }
+            } else {
+                for (int i = -1; i < cnt && ok; ++i) {
+                    const uint32_t jj = j + i;               // values of tile i, then scores of tile i + 1
+                    const bool more = i + 1 < cnt;
+                    if (i >= 0 && !slot_wait(2 * jj + 1)) break;
+                    if (more && !slot_wait(2 * jj + 2)) break;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (i >= 0) {
+                            if (!wait(p_full(t), jj & 1)) break;
+                            tc_fence_after();
+                            values(t, jj, t * 128, (valid_of(run.t0 + i) + 15) / 16, i == 0);
+                            mma_commit_w(o_full(t));
+                        }
+                        if (more) {
+                            scores(t, jj + 1, t * 128, valid_of(run.t0 + i + 1) <= 64 ? 64 : 128);
+                            mma_commit_w(s_full(t));
+                        }
+                    }
+                    if (i >= 0) mma_commit_w(empty((2 * jj + 1) % C::SLOTS));
+                    if (more) mma_commit_w(empty((2 * jj + 2) % C::SLOTS));
+                }
+            }
+            j += cnt;
+        }
+    } else if (warp >= 4) {
+        // ---------------------------------------------------------------- softmax
+        const int t = (warp - 4) >> 2, wg = tid - 128 - 128 * t;             // row tile, row in it
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;                   // TMEM lane 32 (warp % 4)
+        const uint32_t o_col = tmem + lanes + C::TM_O + t * 128;
+        const float c = a.scale * kLog2e;
+        unsigned char *qs = smem + t * C::SLOT;
+        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q);
+        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out);
+        uint32_t j = 0, met = 0;
+        bool first_seg = true;
+        // all softmax threads meet
+        auto meet = [&]() {
+            mbar_arrive(meet_bar);
+            return wait(meet_bar, met++ & 1);
+        };
+        for (; run.left > 0 && ok; run.advance(a, sh.groups)) {
+            const int h = run.r / sh.groups, row0 = (run.r % sh.groups) * (QT * kTile) + t * kTile;
+            const int cnt = run.count(), row = row0 + wg;
+            const int64_t n = run.n;
+            // the row tile's queries, swizzled as the product reads them
+            for (int i = wg; i < kTile * (D / 8); i += 128) {
+                const int r = i / (D / 8), x = i % (D / 8), rr = row0 + r;
+                uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                if (rr < rows)
+                    u = __ldg(reinterpret_cast<const uint4 *>(
+                            q + ((n * a.M + rr / G) * a.H + h * G + rr % G) * (int64_t)D) + x);
+                *reinterpret_cast<uint4 *>(qs + (x >> 3) * 16384 + sw128_off(r, x & 7)) = u;
+            }
+            fence_proxy_async();
+            mbar_arrive(q_full(t));
+            float top = -INFINITY, sum = 0.f;
+            uint64_t mine = 0, bad = 0;              // known from the tree tile on
+            for (int i = 0; i < cnt; ++i) {
+                const uint32_t jj = j + i;
+                const int tl = run.t0 + i;
+                const bool tree = tl == run.tiles - 1;
+                const int valid = tree ? a.M : min(kTile, run.len - tl * kTile);
+                const bool wide = valid > 64;
+                const int b = QT == 1 ? (int)(jj & 1) : t;
+                const uint32_t s_col = tmem + lanes + b * 128;
+                if (tree || valid < kTile) {
+                    // the value tile's rows past the last key: zeros (a weight of zero would
+                    // not cancel a NaN).  In the tree tile also the rows of no node, and every
+                    // value that is not finite: those are added at the end to the rows that see them.
+                    const uint32_t use = 2 * jj + 1;
+                    if (!wait(full(use % C::SLOTS), (use / C::SLOTS) & 1)) break;
+                    if (tree) {
+                        if (!meet()) break;          // the unit before is done with the lines
+                        if (tid == 128) words[W_BAD0] = words[W_BAD1] = 0;
+                        if (t == 0 && wg < a.M) line[wg] = tree_line(a.parent + n * a.M, wg);
+                        if (!meet()) break;
+                        mine = row < rows ? line[row / G] : 0;
+                    }
+                    if (t == 0) {
+                        unsigned char *vs = smem + C::O_RING + (use % C::SLOTS) * C::SLOT;
+                        const int until = (valid + 15) & ~15;
+                        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+                        auto piece = [&](int r, int x) {
+                            return reinterpret_cast<uint4 *>(vs + (r >> 3) * (C::HALVES * 1024) + (x >> 3) * 1024 +
+                                                             sw128_off(r & 7, x & 7));
+                        };
+                        for (int e = wg; e < (until - valid) * (D / 8); e += 128)
+                            *piece(valid + e / (D / 8), e % (D / 8)) = zero;
+                        if (tree) {
+                            for (int e = wg; e < valid * (D / 8); e += 128) {
+                                const int r = e / (D / 8);
+                                uint4 *p = piece(r, e % (D / 8)), u = *p;
+                                const bool node = line[r] != 0;
+                                uint32_t *w = reinterpret_cast<uint32_t *>(&u);
+                                bool odd = false;
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) {
+                                    const uint32_t f = w[x] & 0x7f807f80u;
+                                    if ((f & 0xffffu) == 0x7f80u) { w[x] &= 0xffff0000u; odd = true; }
+                                    if ((f >> 16) == 0x7f80u) { w[x] &= 0x0000ffffu; odd = true; }
+                                }
+                                if (!node) *p = zero;
+                                else if (odd) {
+                                    *p = u;
+                                    atomicOr(const_cast<uint32_t *>(&words[r < 32 ? W_BAD0 : W_BAD1]), 1u << (r & 31));
+                                }
+                            }
+                        }
+                        fence_proxy_async();
+                    }
+                    if (tree) {
+                        if (!meet()) break;
+                        bad = words[W_BAD0] | (uint64_t)words[W_BAD1] << 32;
+                    }
+                }
+                if (!wait(s_full(b), (QT == 1 ? jj >> 1 : jj) & 1)) break;
+                tc_fence_after();
+                float v[64];
+                auto mask = [&](int off) {
+                    if (tree) {
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) v[e] = (mine >> e & 1) != 0 ? v[e] : -INFINITY;
+                    } else if (valid < kTile) {
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) v[e] = off + e < valid ? v[e] : -INFINITY;
+                    }
+                };
+                float mx = -INFINITY;
+                if (wide) {
+                    tmem_ld64(s_col + 64, v);
+                    mask(64);
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) mx = fmaxf(mx, v[e]);
+                }
+                tmem_ld64(s_col, v);
+                mask(0);
+#pragma unroll
+                for (int e = 0; e < 64; ++e) mx = fmaxf(mx, v[e]);
+                mx *= c;
+                const bool grow = mx > top + kGrow;
+                const bool rescale = __any_sync(0xffffffffu, grow) && i > 0;
+                const float was = top;
+                if (grow) top = mx;
+                const float shrink = grow ? ex2(was - top) : 1.f;
+                sum *= shrink;
+                if (i > 0) {
+                    // the sums of the tile before are in (also before the weights of
+                    // this one are handed over, so that the phases stay in step)
+                    if (rescale) {
+                        if (!wait(o_full(t), (jj - 1) & 1)) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int x = 0; x < D; x += 32) {
+                            float o[32];
+                            tmem_ld32(o_col + x, o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] *= shrink;
+                            tmem_st32(o_col + x, o);
+                        }
+                    }
+                }
+                const float from = top == -INFINITY ? 0.f : top;
+                const float2 c2 = make_float2(c, c), f2 = make_float2(-from, -from);
+                float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                float w[32];
+                auto weigh = [&]() {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        float2 x = f2fma(make_float2(v[2 * e], v[2 * e + 1]), c2, f2);
+                        x.x = ex2(x.x);
+                        x.y = ex2(x.y);
+                        add[e & 1] = f2add(add[e & 1], x);
+                        w[e] = __uint_as_float(pack_bf16x2(x.x, x.y));
+                    }
+                };
+                weigh();
+                tmem_st32_nowait(s_col, w);
+                if (wide) {
+                    tmem_ld64(s_col + 64, v);
+                    mask(64);
+                    weigh();
+                    tmem_st32_nowait(s_col + 32, w);
+                }
+                sum += (add[0].x + add[0].y) + (add[1].x + add[1].y);
+                tmem_wait_st();
+                if (i > 0 && !rescale && !wait(o_full(t), (jj - 1) & 1)) break;
+                tc_fence_before();
+                mbar_arrive(p_full(b));
+            }
+            j += cnt;
+            if (!ok) break;
+            if (!wait(o_full(t), (j - 1) & 1)) break;
+            tc_fence_after();
+            const bool whole = run.t0 == 0 && cnt == run.tiles;
+            const int64_t o_row = (n * a.M + row / G) * (int64_t)a.H + h * G + row % G;
+            const uint64_t add_bad = bad & mine;
+            constexpr int R = QT * kTile;
+            const int slot = 2 * blockIdx.x + (first_seg && run.t0 > 0 ? 0 : 1);
+            float *part = sh.part + (size_t)slot * R * (D + 2);
+            const float inv = mine == 0 ? 0.f : 1.f / sum;
+#pragma unroll 1
+            for (int x = 0; x < D; x += 32) {
+                float o[32];
+                tmem_ld32(o_col + x, o);
+                if (add_bad != 0) {
+                    for (uint64_t left = add_bad; left != 0; left &= left - 1) {
+                        const int jn = __ffsll((long long)left) - 1;
+                        const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(a.v_new) +
+                                                  ((n * a.M + jn) * a.H_kv + h) * (int64_t)D + x;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float y = __bfloat162float(vn[e]);
+                            if (!(fabsf(y) <= 3.402823466e38f)) o[e] += y;
+                        }
+                    }
+                }
+                if (row >= rows) continue;
+                if (whole) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(out + o_row * D + x);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t u[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            u[y] = mine == 0 ? 0u : pack_bf16x2(o[8 * e + 2 * y] * inv, o[8 * e + 2 * y + 1] * inv);
+                        dst[e] = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
+                } else {
+                    float4 *dst = reinterpret_cast<float4 *>(part) + (size_t)(x / 4) * R + t * kTile + wg;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        dst[(size_t)e * R] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                }
+            }
+            if (row < rows) {
+                if (whole) {
+                    if (a.lse != nullptr) a.lse[o_row] = mine == 0 ? -INFINITY : (top + log2f(sum)) * kLn2;
+                } else {
+                    float *ml = part + (size_t)R * D + t * kTile + wg;
+                    ml[0] = top;
+                    ml[R] = sum;
+                }
+            }
+            tc_fence_before();
+            first_seg = false;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the units that were cut.  Block (b, y): the cut between CTAs b and
+// b + 1, rows 16 y .. 16 y + 15 of its unit; it works when that is the unit's
+// first cut.
+template <int D, int QT>
+__global__ void __launch_bounds__(256)
+tree_attention_tc_join_kernel(const TreeAttention a, const Shape sh) {
+    constexpr int R = QT * kTile, ROWS = 16;
+    __shared__ int64_t buf[34];
+    const int b = blockIdx.x + 1;
+    const int G = a.H / a.H_kv, rows = a.M * G;
+    Place p;
+    find_place(a, sh.groups, sh.ctas, b, buf, p);
+    const int64_t at = piece_start(p.total, sh.ctas, b);
+    if (at >= p.total || p.unit0 == at || piece_start(p.total, sh.ctas, b - 1) > p.unit0) return;
+    const int64_t end = p.unit0 + unit_tiles(p.len);
+    int parts = 1;
+    for (int c = b; c < sh.ctas && piece_start(p.total, sh.ctas, c) < end; ++c) ++parts;
+    const int h = p.r / sh.groups, row0 = (p.r % sh.groups) * R;
+    // part i is CTA b - 1 + i's: its last segment for the first, its first one after that
+    auto part_of = [&](int i) { return sh.part + (size_t)(2 * (b - 1 + i) + (i == 0 ? 1 : 0)) * R * (D + 2); };
+    for (int e = threadIdx.x; e < ROWS * (D / 4); e += 256) {
+        const int lr = blockIdx.y * ROWS + e % ROWS, c4 = e / ROWS, row = row0 + lr;
+        if (lr >= R || row >= rows) continue;
+        float top = -INFINITY;
+        for (int i = 0; i < parts; ++i) top = fmaxf(top, part_of(i)[(size_t)R * D + lr]);
+        const float from = top == -INFINITY ? 0.f : top;
+        float sum = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = 0; i < parts; ++i) {
+            const float *q = part_of(i);
+            const float w = ex2(q[(size_t)R * D + lr] - from);
+            const float4 x = reinterpret_cast<const float4 *>(q)[(size_t)c4 * R + lr];
+            sum += w * q[(size_t)R * D + R + lr];
+            o.x += w * x.x; o.y += w * x.y; o.z += w * x.z; o.w += w * x.w;
+        }
+        const bool none = tree_line(a.parent + (int64_t)p.n * a.M, row / G) == 0;
+        const float inv = 1.f / sum;
+        const int64_t o_row = ((int64_t)p.n * a.M + row / G) * a.H + h * G + row % G;
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + o_row * D + 4 * c4) =
+            none ? make_uint2(0u, 0u)
+                 : make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (c4 == 0 && a.lse != nullptr) a.lse[o_row] = none ? -INFINITY : (top + log2f(sum)) * kLn2;
+    }
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static const EncodeTiledFn fn = [] {
+        cudaDriverEntryPointQueryResult q;
+        void *p = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess || q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiledFn>(p);
+    }();
+    return fn;
+}
+
+bool make_map(CUtensorMap *map, const void *base, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3],
+              const cuuint32_t (&box)[4]) {
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, ones,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The cache as groups of eight rows: [groups][D/64 halves][8 rows][64], so that
+// a box lands as whole 128-byte-swizzle blocks, the halves of a row next to
+// each other.
+bool cache_map(CUtensorMap *map, const void *base, const TreeAttention &a, int D, int box) {
+    const cuuint64_t groups = (cuuint64_t)a.num_pages * a.H_kv * a.page_size / 8;
+    return make_map(map, base, {64, 8, (cuuint64_t)(D / 64), groups}, {(cuuint64_t)D * 2, 128, (cuuint64_t)D * 16},
+                    {64, 8, (cuuint32_t)(D / 64), (cuuint32_t)(box / 8)});
+}
+// The drafted rows [N * M][H_kv][D], eight rows of one head per box.
+bool new_map(CUtensorMap *map, const void *base, const TreeAttention &a, int D) {
+    return make_map(map, base, {64, (cuuint64_t)a.N * a.M, (cuuint64_t)(D / 64), (cuuint64_t)a.H_kv},
+                    {(cuuint64_t)a.H_kv * D * 2, 128, (cuuint64_t)D * 2}, {64, 8, (cuuint32_t)(D / 64), 1});
+}
+
+int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+        sms = 152;
+    return sms;
+}
+
+template <int D, int QT> cudaError_t run_tc(const TreeAttention &a, void *workspace, cudaStream_t stream) {
+    using C = Cfg<D, QT>;
+    Maps maps;
+    Shape sh;
+    sh.box = kTile;
+    while (a.page_size % sh.box != 0) sh.box /= 2;
+    if (encode_fn() == nullptr || !cache_map(&maps.k, a.k_cache, a, D, sh.box) ||
+        !cache_map(&maps.v, a.v_cache, a, D, sh.box) || !new_map(&maps.kn, a.k_new, a, D) ||
+        !new_map(&maps.vn, a.v_new, a, D))
+        return cudaErrorInvalidValue;
+    const int rows = a.M * (a.H / a.H_kv);
+    sh.groups = (rows + QT * kTile - 1) / (QT * kTile);
+    sh.ctas = sm_count();
+    sh.part = static_cast<float *>(workspace);
+    static std::atomic<uint64_t> smem_set{0};
+    cudaError_t e = allow_dynamic_smem(tree_attention_tc_kernel<D, QT>, C::SMEM, smem_set);
+    if (e != cudaSuccess) return e;
+    tree_attention_tc_kernel<D, QT><<<sh.ctas, C::THREADS, C::SMEM, stream>>>(maps, a, sh);
+    count_launches(1);
+    if (sh.ctas > 1) {
+        const int blocks = ((rows < QT * kTile ? rows : QT * kTile) + 15) / 16;
+        tree_attention_tc_join_kernel<D, QT><<<dim3(sh.ctas - 1, blocks), 256, 0, stream>>>(a, sh);
+        count_launches(1);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool tree_attention_tc_supported(int32_t H_kv, int32_t D, kda_dtype dt, int64_t num_pages, int32_t page_size) {
+    return dt == KDA_BF16 && (D == 64 || D == 128) && page_size % 8 == 0 &&
+           num_pages * H_kv * page_size / 8 < INT32_MAX;
+}
+
+size_t tree_attention_tc_partial_bytes(int32_t M, int32_t H, int32_t H_kv, int32_t D) {
+    const int tiles = M * (H / H_kv) <= kTile ? 1 : 2;
+    return (size_t)sm_count() * 2 * tiles * kTile * (D + 2) * 4;
+}
+
+cudaError_t launch_tree_attention_tc(const TreeAttention &a, int32_t D, void *workspace, cudaStream_t stream) {
+    const bool one = a.M * (a.H / a.H_kv) <= kTile;
+    if (D == 64) return one ? run_tc<64, 1>(a, workspace, stream) : run_tc<64, 2>(a, workspace, stream);
+    return one ? run_tc<128, 1>(a, workspace, stream) : run_tc<128, 2>(a, workspace, stream);
+}
+
+}  // namespace kda
