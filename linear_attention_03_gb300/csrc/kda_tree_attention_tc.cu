@@ -20,7 +20,8 @@
 //
 // Roles: warp 0 loads (TMA, one box per page or part of one), warp 1 issues the
 // products, a warpgroup per row tile does the softmax with a thread per row
-// (the running maximum needs no exchange).  The sums are rescaled only when the
+// (the running maximum needs no exchange).  The weights of a tile's first 64
+// keys are handed over while the others are computed.  The sums are rescaled only when the
 // maximum grows by more than 2^8: weights up to 2^8 lose nothing in bf16 or in
 // the fp32 sums.  The weights are rounded to bf16 for the product (2^-9
 // relative, the size of the output's own rounding); maximum, sum and output
@@ -50,7 +51,7 @@ template <int D, int QT> struct Cfg {
     static constexpr int Q_BYTES = QT * SLOT;
     static constexpr int O_RING = Q_BYTES;
     static constexpr int O_MISC = O_RING + SLOTS * SLOT;
-    static constexpr int NBARS = 2 * SLOTS + 9;
+    static constexpr int NBARS = 2 * SLOTS + 11;
     static constexpr int O_LINES = O_MISC + 8 * NBARS, O_WORDS = O_LINES + 8 * kMaxTreeNodes;
     static constexpr int SMEM = O_MISC + 1024;
     static_assert(O_WORDS + 64 <= SMEM, "misc");
@@ -164,6 +165,11 @@ struct Run {
     }
 };
 
+// keys of the unit's tile t
+__device__ __forceinline__ int valid_keys(const TreeAttention &a, const Run &run, int t) {
+    return t == run.tiles - 1 ? a.M : min(kTile, run.len - t * kTile);
+}
+
 template <int D, int QT>
 __global__ void __launch_bounds__(Cfg<D, QT>::THREADS, 1)
 tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention a, const Shape sh) {
@@ -179,10 +185,10 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
     auto full = [&](int s) { return bars + 8u * s; };
     auto empty = [&](int s) { return bars + 8u * (C::SLOTS + s); };
     auto s_full = [&](int b) { return bars + 8u * (2 * C::SLOTS + b); };
-    auto p_full = [&](int b) { return bars + 8u * (2 * C::SLOTS + 2 + b); };
-    auto o_full = [&](int t) { return bars + 8u * (2 * C::SLOTS + 4 + t); };
-    auto q_full = [&](int t) { return bars + 8u * (2 * C::SLOTS + 6 + t); };
-    const uint32_t meet_bar = bars + 8u * (2 * C::SLOTS + 8);
+    auto p_full = [&](int b, int half) { return bars + 8u * (2 * C::SLOTS + 2 + 2 * b + half); };
+    auto o_full = [&](int t) { return bars + 8u * (2 * C::SLOTS + 6 + t); };
+    auto q_full = [&](int t) { return bars + 8u * (2 * C::SLOTS + 8 + t); };
+    const uint32_t meet_bar = bars + 8u * (2 * C::SLOTS + 10);
 
     Place place;
     find_place(a, sh.groups, sh.ctas, blockIdx.x, reinterpret_cast<int64_t *>(smem), place);
@@ -205,7 +211,8 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(s_full(b), 1);
-            mbar_init(p_full(b), 128);
+            mbar_init(p_full(b, 0), 128);
+            mbar_init(p_full(b, 1), 128);
             mbar_init(o_full(b), 1);
             mbar_init(q_full(b), 128);
         }
@@ -240,7 +247,7 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
             const int32_t *table = a.page_table + (int64_t)run.n * a.max_pages;
             for (int t = run.t0; t < run.t0 + cnt && ok; ++t) {
                 const bool tree = t == run.tiles - 1;
-                const int valid = tree ? a.M : min(kTile, run.len - t * kTile);
+                const int valid = valid_keys(a, run, t);
                 const int loads = tree ? (a.M + 7) / 8 : (valid + sh.box - 1) / sh.box;
                 int32_t group = 0;
                 if (!tree && lane < loads) {
@@ -297,57 +304,54 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                 mma_bf16_w(tmem + s_col, HI_Q | sw128_lo(qb + (ks >> 2) * 16384 + (ks & 3) * 32),
                            HI_K | sw128_lo(kb + (ks >> 2) * 1024 + (ks & 3) * 32), cols == 64 ? ID_QK64 : ID_QK, ks > 0);
         };
-        auto values = [&](int t, uint32_t jj, uint32_t s_col, int steps, bool first) {
-            const uint32_t vb = slot(2 * jj + 1);
-            for (int ks = 0; ks < steps; ++ks)
-                mma_tmem_a_w(tmem + C::TM_O + t * 128, tmem + s_col + ks * 8,
-                             HI_V | sw128_lo(vb + ks * 2 * C::HALVES * 1024), ID_PV, !(first && ks == 0));
+        // sums of row tile t: the weights of buffer b, of tile jj, 64 keys after 64
+        auto values = [&](int t, int b, uint32_t jj, uint32_t parity, int valid, bool first) {
+            const uint32_t vb = slot(2 * jj + 1), p = tmem + b * 128;
+            if (!slot_wait(2 * jj + 1)) return false;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int steps = min(4, (valid - 64 * half + 15) / 16);
+                if (steps <= 0) break;
+                if (!wait(p_full(b, half), parity)) return false;
+                tc_fence_after();
+                for (int ks = 4 * half; ks < 4 * half + steps; ++ks)
+                    mma_tmem_a_w(tmem + C::TM_O + t * 128, p + ks * 8,
+                                 HI_V | sw128_lo(vb + ks * 2 * C::HALVES * 1024), ID_PV, !(first && ks == 0));
+            }
+            mma_commit_w(o_full(t));
+            return true;
         };
-        auto valid_of = [&](int t) { return t == run.tiles - 1 ? a.M : min(kTile, run.len - t * kTile); };
         for (; run.left > 0 && ok; run.advance(a, sh.groups), ++seg) {
             const int cnt = run.count();
             for (int t = 0; t < QT; ++t) wait(q_full(t), seg & 1);
             tc_fence_after();
-            if constexpr (QT == 1) {
-                for (int i = 0; i <= cnt && ok; ++i) {
+            int valid = 0;                                   // keys of the tile before
+            for (int i = 0; i <= cnt && ok; ++i) {
+                const uint32_t jj = j + i;                   // scores of tile i, values of tile i - 1
+                const int now = i < cnt ? valid_keys(a, run, run.t0 + i) : 0;
+                if (i < cnt && !slot_wait(2 * jj)) break;
+                if constexpr (QT == 1) {
+                    // two score buffers: the scores of a tile run during the softmax of the one before
                     if (i < cnt) {
-                        const uint32_t jj = j + i;
-                        if (!slot_wait(2 * jj)) break;
-                        scores(0, jj, (jj & 1) * 128, valid_of(run.t0 + i) <= 64 ? 64 : 128);
+                        scores(0, jj, (jj & 1) * 128, now <= 64 ? 64 : 128);
                         mma_commit_w(s_full(jj & 1));
                         mma_commit_w(empty((2 * jj) % C::SLOTS));
                     }
-                    if (i > 0) {
-                        const uint32_t jj = j + i - 1;
-                        if (!wait(p_full(jj & 1), (jj >> 1) & 1) || !slot_wait(2 * jj + 1)) break;
-                        tc_fence_after();
-                        values(0, jj, (jj & 1) * 128, (valid_of(run.t0 + i - 1) + 15) / 16, i == 1);
-                        mma_commit_w(o_full(0));
-                        mma_commit_w(empty((2 * jj + 1) % C::SLOTS));
-                    }
-                }
-            } else {
-                for (int i = -1; i < cnt && ok; ++i) {
-                    const uint32_t jj = j + i;               // values of tile i, then scores of tile i + 1
-                    const bool more = i + 1 < cnt;
-                    if (i >= 0 && !slot_wait(2 * jj + 1)) break;
-                    if (more && !slot_wait(2 * jj + 2)) break;
+                    if (i > 0 && !values(0, (jj - 1) & 1, jj - 1, ((jj - 1) >> 1) & 1, valid, i == 1)) break;
+                } else {
+                    // one score buffer per row tile: each row tile's products run during the other's softmax
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (i >= 0) {
-                            if (!wait(p_full(t), jj & 1)) break;
-                            tc_fence_after();
-                            values(t, jj, t * 128, (valid_of(run.t0 + i) + 15) / 16, i == 0);
-                            mma_commit_w(o_full(t));
-                        }
-                        if (more) {
-                            scores(t, jj + 1, t * 128, valid_of(run.t0 + i + 1) <= 64 ? 64 : 128);
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        if (i > 0 && !values(t, t, jj - 1, (jj - 1) & 1, valid, i == 1)) break;
+                        if (i < cnt) {
+                            scores(t, jj, t * 128, now <= 64 ? 64 : 128);
                             mma_commit_w(s_full(t));
                         }
                     }
-                    if (i >= 0) mma_commit_w(empty((2 * jj + 1) % C::SLOTS));
-                    if (more) mma_commit_w(empty((2 * jj + 2) % C::SLOTS));
+                    if (i < cnt) mma_commit_w(empty((2 * jj) % C::SLOTS));
                 }
+                if (i > 0) mma_commit_w(empty((2 * jj - 1) % C::SLOTS));
+                valid = now;
             }
             j += cnt;
         }
@@ -371,14 +375,24 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
             const int h = run.r / sh.groups, row0 = (run.r % sh.groups) * (QT * kTile) + t * kTile;
             const int cnt = run.count(), row = row0 + wg;
             const int64_t n = run.n;
-            // the row tile's queries, swizzled as the product reads them
-            for (int i = wg; i < kTile * (D / 8); i += 128) {
-                const int r = i / (D / 8), x = i % (D / 8), rr = row0 + r;
-                uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                if (rr < rows)
-                    u = __ldg(reinterpret_cast<const uint4 *>(
-                            q + ((n * a.M + rr / G) * a.H + h * G + rr % G) * (int64_t)D) + x);
-                *reinterpret_cast<uint4 *>(qs + (x >> 3) * 16384 + sw128_off(r, x & 7)) = u;
+            // the row tile's queries, swizzled as the product reads them, eight loads on their way
+            constexpr int PIECES = D / 8, ROWS_PER = 128 / PIECES;           // rows per pass of the warpgroup
+#pragma unroll 1
+            for (int r0 = 0; r0 < kTile; r0 += 8 * ROWS_PER) {
+                uint4 u[8];
+                const int x = wg % PIECES;
+#pragma unroll
+                for (int y = 0; y < 8; ++y) {
+                    const int rr = row0 + r0 + y * ROWS_PER + wg / PIECES;
+                    u[y] = make_uint4(0u, 0u, 0u, 0u);
+                    if (rr < rows)
+                        u[y] = __ldg(reinterpret_cast<const uint4 *>(
+                                   q + ((n * a.M + rr / G) * a.H + h * G + rr % G) * (int64_t)D) + x);
+                }
+#pragma unroll
+                for (int y = 0; y < 8; ++y)
+                    *reinterpret_cast<uint4 *>(
+                        qs + (x >> 3) * 16384 + sw128_off(r0 + y * ROWS_PER + wg / PIECES, x & 7)) = u[y];
             }
             fence_proxy_async();
             mbar_arrive(q_full(t));
@@ -388,7 +402,7 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                 const uint32_t jj = j + i;
                 const int tl = run.t0 + i;
                 const bool tree = tl == run.tiles - 1;
-                const int valid = tree ? a.M : min(kTile, run.len - tl * kTile);
+                const int valid = valid_keys(a, run, tl);
                 const bool wide = valid > 64;
                 const int b = QT == 1 ? (int)(jj & 1) : t;
                 const uint32_t s_col = tmem + lanes + b * 128;
@@ -454,45 +468,44 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                         for (int e = 0; e < 64; ++e) v[e] = off + e < valid ? v[e] : -INFINITY;
                     }
                 };
-                float mx = -INFINITY;
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                auto widen = [&]() {
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) m4[e & 3] = fmaxf(m4[e & 3], v[e]);
+                };
                 if (wide) {
                     tmem_ld64(s_col + 64, v);
                     mask(64);
-#pragma unroll
-                    for (int e = 0; e < 64; ++e) mx = fmaxf(mx, v[e]);
+                    widen();
                 }
                 tmem_ld64(s_col, v);
                 mask(0);
-#pragma unroll
-                for (int e = 0; e < 64; ++e) mx = fmaxf(mx, v[e]);
-                mx *= c;
+                widen();
+                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
                 const bool grow = mx > top + kGrow;
                 const bool rescale = __any_sync(0xffffffffu, grow) && i > 0;
                 const float was = top;
                 if (grow) top = mx;
                 const float shrink = grow ? ex2(was - top) : 1.f;
                 sum *= shrink;
-                if (i > 0) {
-                    // the sums of the tile before are in (also before the weights of
-                    // this one are handed over, so that the phases stay in step)
-                    if (rescale) {
-                        if (!wait(o_full(t), (jj - 1) & 1)) break;
-                        tc_fence_after();
+                if (rescale) {
+                    // the sums of the tile before are in
+                    if (!wait(o_full(t), (jj - 1) & 1)) break;
+                    tc_fence_after();
 #pragma unroll 1
-                        for (int x = 0; x < D; x += 32) {
-                            float o[32];
-                            tmem_ld32(o_col + x, o);
+                    for (int x = 0; x < D; x += 32) {
+                        float o[32];
+                        tmem_ld32(o_col + x, o);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] *= shrink;
-                            tmem_st32(o_col + x, o);
-                        }
+                        for (int e = 0; e < 32; ++e) o[e] *= shrink;
+                        tmem_st32(o_col + x, o);
                     }
                 }
                 const float from = top == -INFINITY ? 0.f : top;
                 const float2 c2 = make_float2(c, c), f2 = make_float2(-from, -from);
                 float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                float w[32];
-                auto weigh = [&]() {
+                auto weigh = [&](uint32_t col) {
+                    float w[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         float2 x = f2fma(make_float2(v[2 * e], v[2 * e + 1]), c2, f2);
@@ -501,20 +514,23 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                         add[e & 1] = f2add(add[e & 1], x);
                         w[e] = __uint_as_float(pack_bf16x2(x.x, x.y));
                     }
+                    tmem_st32_nowait(col, w);
                 };
-                weigh();
-                tmem_st32_nowait(s_col, w);
+                weigh(s_col);
+                tmem_wait_st();
+                // (waiting for the sums of the tile before each time keeps the phases in step)
+                if (i > 0 && !rescale && !wait(o_full(t), (jj - 1) & 1)) break;
+                tc_fence_before();
+                mbar_arrive(p_full(b, 0));
                 if (wide) {
                     tmem_ld64(s_col + 64, v);
                     mask(64);
-                    weigh();
-                    tmem_st32_nowait(s_col + 32, w);
+                    weigh(s_col + 32);
+                    tmem_wait_st();
+                    tc_fence_before();
                 }
+                mbar_arrive(p_full(b, 1));
                 sum += (add[0].x + add[0].y) + (add[1].x + add[1].y);
-                tmem_wait_st();
-                if (i > 0 && !rescale && !wait(o_full(t), (jj - 1) & 1)) break;
-                tc_fence_before();
-                mbar_arrive(p_full(b));
             }
             j += cnt;
             if (!ok) break;
