@@ -18,12 +18,18 @@
 // kernel joins them.  The cut depends on the lengths alone, so results repeat
 // bit for bit.
 //
-// Roles: warp 0 loads (TMA, one box per page or part of one), warp 1 issues the
-// products, a warpgroup per row tile does the softmax with a thread per row
-// (the running maximum needs no exchange).  The weights of a tile's first 64
-// keys are handed over while the others are computed.  The sums are rescaled only when the
-// maximum grows by more than 2^8: weights up to 2^8 lose nothing in bf16 or in
-// the fp32 sums.  The weights are rounded to bf16 for the product (2^-9
+// Roles: warp 0 loads (TMA, one box per page or part of one), a warp per row
+// tile issues its products, a warpgroup per row tile does the softmax with a
+// thread per row (the running maximum needs no exchange).  Keys go in steps of
+// 64, half a tile: a row tile's scores have four (QT = 1) or two (QT = 2)
+// buffers of 64 columns, so the products of the next steps run while a step's
+// softmax does, and a row's 64 scores fit its thread's registers (read once).
+// Warp 3 looks at every value tile before its product: rows past the last key
+// become zeros, since a weight of zero would not cancel a NaN; in the tree tile
+// also the rows of no node and every value that is not finite, which the rows
+// that see it get added at the end.  The sums are rescaled only when the maximum
+// grows by more than 2^8: weights up to 2^8 lose nothing in bf16 or in the fp32
+// sums.  The weights are rounded to bf16 for the product (2^-9
 // relative, the size of the output's own rounding); maximum, sum and output
 // sums are fp32.
 #include "kda_internal.cuh"
@@ -51,17 +57,23 @@ template <int D, int QT> struct Cfg {
     static constexpr int Q_BYTES = QT * SLOT;
     static constexpr int O_RING = Q_BYTES;
     static constexpr int O_MISC = O_RING + SLOTS * SLOT;
-    static constexpr int NBARS = 2 * SLOTS + 11;
-    static constexpr int O_LINES = O_MISC + 8 * NBARS, O_WORDS = O_LINES + 8 * kMaxTreeNodes;
-    static constexpr int SMEM = O_MISC + 1024;
-    static_assert(O_WORDS + 64 <= SMEM, "misc");
+    // Segments (and value tiles) that can be under way at once: a unit's end may still be read
+    // while warp 3 prepares the tiles that the ring holds after it.
+    static constexpr int RING = D == 64 ? 8 : 4;
+    static_assert(RING > SLOTS / 2, "ring of lines");
+    static constexpr int NBARS = 2 * SLOTS + 14 + RING;
+    static constexpr int O_LINES = O_MISC + 8 * NBARS, O_WORDS = O_LINES + RING * 8 * kMaxTreeNodes;
+    static constexpr int SMEM = O_MISC + (D == 64 ? 8192 : 3072);
+    static_assert(O_WORDS + 8 + 8 * RING <= SMEM, "misc");
+    static constexpr int BUFS = 4 / QT;        // score buffers per row tile
+    static constexpr int AHEAD = BUFS / 2;     // steps by which the scores lead the sums
     // TMEM columns: scores (and the weights in their place), then the sums
     static constexpr int TM_O = 256;
 };
 static_assert(Cfg<128, 1>::SMEM <= 232448 && Cfg<128, 2>::SMEM <= 232448, "227 KB of shared memory");
 
-// misc: the mbarriers, the tree's lines, then these 32-bit words
-enum { W_TMEM = 0, W_ABORT, W_BAD0, W_BAD1, W_WORDS };
+// misc: the mbarriers, the trees' lines, then these 32-bit words (two of W_BAD per segment of the ring)
+enum { W_TMEM = 0, W_ABORT, W_BAD };
 
 struct Maps {
     CUtensorMap k, v, kn, vn;
@@ -175,20 +187,25 @@ __global__ void __launch_bounds__(Cfg<D, QT>::THREADS, 1)
 tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention a, const Shape sh) {
     using C = Cfg<D, QT>;
     extern __shared__ __align__(1024) unsigned char smem[];
-    const uint32_t base = smem_u32(smem);
+    // warp-uniform by construction (a shuffle from lane 0), so that the compiler keeps
+    // them, the role branches and what is derived from them in uniform registers
+    const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
     volatile uint32_t *words = reinterpret_cast<uint32_t *>(smem + C::O_WORDS);
     uint64_t *line = reinterpret_cast<uint64_t *>(smem + C::O_LINES);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int G = a.H / a.H_kv, rows = a.M * G;
 
     const uint32_t bars = base + C::O_MISC;
     auto full = [&](int s) { return bars + 8u * s; };
     auto empty = [&](int s) { return bars + 8u * (C::SLOTS + s); };
-    auto s_full = [&](int b) { return bars + 8u * (2 * C::SLOTS + b); };
-    auto p_full = [&](int b, int half) { return bars + 8u * (2 * C::SLOTS + 2 + 2 * b + half); };
-    auto o_full = [&](int t) { return bars + 8u * (2 * C::SLOTS + 6 + t); };
-    auto q_full = [&](int t) { return bars + 8u * (2 * C::SLOTS + 8 + t); };
-    const uint32_t meet_bar = bars + 8u * (2 * C::SLOTS + 10);
+    auto s_full = [&](int t, uint32_t b) { return bars + 8u * (2 * C::SLOTS + C::BUFS * t + b); };
+    auto p_full = [&](int t, uint32_t b) { return bars + 8u * (2 * C::SLOTS + 4 + C::BUFS * t + b); };
+    auto o_full = [&](int t, int b) { return bars + 8u * (2 * C::SLOTS + 8 + 2 * t + b); };
+    auto q_full = [&](int t) { return bars + 8u * (2 * C::SLOTS + 12 + t); };
+    auto v_ready = [&](uint32_t i) { return bars + 8u * (2 * C::SLOTS + 14 + i % C::RING); };
+    // scores of row tile t, buffer b (the weights go in their place)
+    auto s_col = [](int t, uint32_t b) { return t * 128 + b * 64; };
 
     Place place;
     find_place(a, sh.groups, sh.ctas, blockIdx.x, reinterpret_cast<int64_t *>(smem), place);
@@ -207,23 +224,25 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
     if (tid == 32) {
         for (int s = 0; s < C::SLOTS; ++s) {
             mbar_init(full(s), 1);
-            mbar_init(empty(s), 1);
+            mbar_init(empty(s), QT);
         }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(s_full(b), 1);
-            mbar_init(p_full(b, 0), 128);
-            mbar_init(p_full(b, 1), 128);
-            mbar_init(o_full(b), 1);
-            mbar_init(q_full(b), 128);
+        for (int t = 0; t < QT; ++t) {
+            for (int b = 0; b < C::BUFS; ++b) {
+                mbar_init(s_full(t, b), 1);
+                mbar_init(p_full(t, b), 128);
+            }
+            mbar_init(o_full(t, 0), 1);
+            mbar_init(o_full(t, 1), 1);
+            mbar_init(q_full(t), 128);
         }
-        mbar_init(meet_bar, 128 * QT);
+        for (int i = 0; i < C::RING; ++i) mbar_init(v_ready(i), 1);
         fence_mbar_init();
         words[W_ABORT] = 0;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = words[W_TMEM];
+    const uint32_t tmem = __shfl_sync(0xffffffffu, words[W_TMEM], 0);
     bool ok = true;
     // a bounded wait of a whole warp; once one gives up, the warp stops
     auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -287,73 +306,164 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                     mbar_wait(full(s), last & 1, 100000000ull);
                 }
         }
-    } else if (warp == 1) {
+    } else if (warp <= QT) {
         // ---------------------------------------------------------------- products
-        constexpr uint32_t ID_QK = idesc_bf16(kTile, kTile, 0, 0), ID_QK64 = idesc_bf16(kTile, 64, 0, 0);
-        constexpr uint32_t ID_PV = idesc_bf16(kTile, D, 0, 1);
+        // A warp per row tile, one elected thread of which issues.  A ready wait costs
+        // the warp some 100 clocks, and the tensor pipe holds little work ahead: with
+        // one warp for both row tiles it stood idle for half of the time.
+        const int t = warp - 1;
+        constexpr uint32_t ID_QK = idesc_bf16(kTile, 64, 0, 0), ID_PV = idesc_bf16(kTile, D, 0, 1);
         constexpr uint64_t HI_Q = sw128_hi(0, 1024), HI_K = sw128_hi(0, C::HALVES * 1024);
         constexpr uint64_t HI_V = sw128_hi(1024, C::HALVES * 1024);
-        uint32_t j = 0, seg = 0;
-        auto slot = [&](uint32_t use) { return base + C::O_RING + (use % C::SLOTS) * C::SLOT; };
-        auto slot_wait = [&](uint32_t use) { return wait(full(use % C::SLOTS), (use / C::SLOTS) & 1); };
-        // scores of row tile t against the keys of tile jj
-        auto scores = [&](int t, uint32_t jj, uint32_t s_col, int cols) {
-            const uint32_t kb = slot(2 * jj), qb = base + t * C::SLOT;
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-                mma_bf16_w(tmem + s_col, HI_Q | sw128_lo(qb + (ks >> 2) * 16384 + (ks & 3) * 32),
-                           HI_K | sw128_lo(kb + (ks >> 2) * 1024 + (ks & 3) * 32), cols == 64 ? ID_QK64 : ID_QK, ks > 0);
+        constexpr uint32_t kHalf = 8 * C::HALVES * 1024;     // bytes of 64 keys
+        auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+        // a run over the segment's steps: the key tile's place in the ring, the step in the tile
+        struct Steps {
+            uint32_t slot, par, tile, j;
+            int i, x, halves, valid;
         };
-        // sums of row tile t: the weights of buffer b, of tile jj, 64 keys after 64
-        auto values = [&](int t, int b, uint32_t jj, uint32_t parity, int valid, bool first) {
-            const uint32_t vb = slot(2 * jj + 1), p = tmem + b * 128;
-            if (!slot_wait(2 * jj + 1)) return false;
+        Steps sc{0, 0, 0, 0, 0, 0, 0, 0}, su{1, 0, 0, 0, 0, 0, 0, 0};
+        uint32_t seg = 0;
+        for (; run.left > 0 && ok; run.advance(a, sh.groups), ++seg) {
+            const int cnt = (int)uniform((uint32_t)run.count());
+            auto enter = [&](Steps &w) {
+                w.x = 0;
+                if (w.i < cnt) {
+                    w.valid = (int)uniform((uint32_t)valid_keys(a, run, run.t0 + w.i));
+                    w.halves = (w.valid + 63) / 64;
+                }
+            };
+            auto next = [&](Steps &w) {
+                ++w.j;
+                if (++w.x < w.halves) return;
+                mma_commit_w(empty(w.slot));                 // the tile is read
+                w.slot += 2;
+                if (w.slot >= (uint32_t)C::SLOTS) {
+                    w.slot -= C::SLOTS;
+                    w.par ^= 1;
+                }
+                ++w.tile;
+                ++w.i;
+                enter(w);
+            };
+            sc.i = su.i = 0;
+            enter(sc);
+            enter(su);
+            wait(q_full(t), seg & 1);
+            tc_fence_after();
+            for (int lead = 0; su.i < cnt && ok;) {
+                if (sc.i < cnt) {
+                    if (sc.x == 0 && !wait(full(sc.slot), sc.par)) break;
+                    const uint32_t kb = uniform(base + C::O_RING + sc.slot * C::SLOT + sc.x * kHalf);
+                    const uint32_t b = uniform(sc.j % C::BUFS), to = tmem + s_col(t, b), qb = base + t * C::SLOT;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int steps = min(4, (valid - 64 * half + 15) / 16);
-                if (steps <= 0) break;
-                if (!wait(p_full(b, half), parity)) return false;
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        mma_bf16_w(to, HI_Q | sw128_lo(qb + (ks >> 2) * 16384 + (ks & 3) * 32),
+                                   HI_K | sw128_lo(kb + (ks >> 2) * 1024 + (ks & 3) * 32), ID_QK, ks > 0);
+                    mma_commit_w(s_full(t, b));
+                    next(sc);
+                    if (++lead <= C::AHEAD) continue;
+                }
+                const uint32_t b = uniform(su.j % C::BUFS);
+                if (su.x == 0 && !wait(v_ready(su.tile), (su.tile / C::RING) & 1)) break;
+                if (!wait(p_full(t, b), (su.j / C::BUFS) & 1)) break;
                 tc_fence_after();
-                for (int ks = 4 * half; ks < 4 * half + steps; ++ks)
-                    mma_tmem_a_w(tmem + C::TM_O + t * 128, p + ks * 8,
-                                 HI_V | sw128_lo(vb + ks * 2 * C::HALVES * 1024), ID_PV, !(first && ks == 0));
+                const uint32_t vb = uniform(base + C::O_RING + su.slot * C::SLOT + su.x * kHalf);
+                const uint32_t p = tmem + s_col(t, b), o = tmem + C::TM_O + t * 128;
+                const int left = su.valid - 64 * su.x;
+                const uint32_t more = su.i > 0 || su.x > 0;  // not the segment's first step
+                if (left > 48) {
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_tmem_a_w(o, p + ks * 8, HI_V | sw128_lo(vb + ks * 2 * C::HALVES * 1024), ID_PV,
+                                     ks > 0 ? 1u : more);
+                } else {
+#pragma unroll
+                    for (int ks = 0; ks < 3; ++ks)
+                        if (16 * ks < left)
+                            mma_tmem_a_w(o, p + ks * 8, HI_V | sw128_lo(vb + ks * 2 * C::HALVES * 1024), ID_PV,
+                                         ks > 0 ? 1u : more);
+                }
+                mma_commit_w(o_full(t, su.j & 1));
+                next(su);
             }
-            mma_commit_w(o_full(t));
-            return true;
-        };
+        }
+    } else if (warp == 3) {
+        // ---------------------------------------------------------------- values
+        uint32_t tile = 0, seg = 0;
         for (; run.left > 0 && ok; run.advance(a, sh.groups), ++seg) {
             const int cnt = run.count();
-            for (int t = 0; t < QT; ++t) wait(q_full(t), seg & 1);
-            tc_fence_after();
-            int valid = 0;                                   // keys of the tile before
-            for (int i = 0; i <= cnt && ok; ++i) {
-                const uint32_t jj = j + i;                   // scores of tile i, values of tile i - 1
-                const int now = i < cnt ? valid_keys(a, run, run.t0 + i) : 0;
-                if (i < cnt && !slot_wait(2 * jj)) break;
-                if constexpr (QT == 1) {
-                    // two score buffers: the scores of a tile run during the softmax of the one before
-                    if (i < cnt) {
-                        scores(0, jj, (jj & 1) * 128, now <= 64 ? 64 : 128);
-                        mma_commit_w(s_full(jj & 1));
-                        mma_commit_w(empty((2 * jj) % C::SLOTS));
-                    }
-                    if (i > 0 && !values(0, (jj - 1) & 1, jj - 1, ((jj - 1) >> 1) & 1, valid, i == 1)) break;
-                } else {
-                    // one score buffer per row tile: each row tile's products run during the other's softmax
+            const bool has_tree = run.t0 + cnt == run.tiles;
+            const int32_t *parent = a.parent + (int64_t)run.n * a.M;
+            int32_t up[2] = {-2, -2};                        // parents of nodes lane and lane + 32
+            if (has_tree) {
+                if (lane < a.M) up[0] = parent[lane];
+                if (lane + 32 < a.M) up[1] = parent[lane + 32];
+            }
+            for (int i = 0; i < cnt && ok; ++i, ++tile) {
+                const bool tree = run.t0 + i == run.tiles - 1;
+                const int valid = valid_keys(a, run, run.t0 + i);
+                // every use of the ring in turn, so that no phase is passed over
+                const uint32_t k_use = 2 * tile, v_use = k_use + 1;
+                if (!wait(full(k_use % C::SLOTS), (k_use / C::SLOTS) & 1)) break;
+                if (!wait(full(v_use % C::SLOTS), (v_use / C::SLOTS) & 1)) break;
+                if (tree || valid < kTile) {
+                    unsigned char *vs = smem + C::O_RING + (v_use % C::SLOTS) * C::SLOT;
+                    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+                    auto piece = [&](int r, int x) {
+                        return reinterpret_cast<uint4 *>(vs + (r >> 3) * (C::HALVES * 1024) + (x >> 3) * 1024 +
+                                                         sw128_off(r & 7, x & 7));
+                    };
+                    const int until = (valid + 15) & ~15;
+                    for (int e = lane; e < (until - valid) * (D / 8); e += 32)
+                        *piece(valid + e / (D / 8), e % (D / 8)) = zero;
+                    if (tree) {
+                        uint64_t *ln = line + (seg % C::RING) * kMaxTreeNodes;
+                        volatile uint32_t *bad = words + W_BAD + 2 * (seg % C::RING);
+                        // both nodes' walks at once; the parents come from the lanes that hold them
+                        int at[2] = {lane < a.M ? lane : -2, lane + 32 < a.M ? lane + 32 : -2};
+                        uint64_t on[2] = {0, 0};
+                        while (__any_sync(0xffffffffu, at[0] >= 0 || at[1] >= 0)) {
 #pragma unroll
-                    for (int t = 0; t < 2 && ok; ++t) {
-                        if (i > 0 && !values(t, t, jj - 1, (jj - 1) & 1, valid, i == 1)) break;
-                        if (i < cnt) {
-                            scores(t, jj, t * 128, now <= 64 ? 64 : 128);
-                            mma_commit_w(s_full(t));
+                            for (int y = 0; y < 2; ++y) {
+                                const int p0 = __shfl_sync(0xffffffffu, up[0], at[y] & 31);
+                                const int p1 = __shfl_sync(0xffffffffu, up[1], at[y] & 31);
+                                if (at[y] >= 0) {
+                                    const int p = at[y] < 32 ? p0 : p1;
+                                    on[y] |= uint64_t{1} << at[y];
+                                    if (p != -1 && (p < 0 || p >= at[y])) on[y] = 0;
+                                    at[y] = p >= 0 && p < at[y] ? p : -1;
+                                }
+                            }
+                        }
+                        ln[lane] = on[0];
+                        ln[lane + 32] = on[1];
+                        if (lane < 2) bad[lane] = 0;
+                        __syncwarp();
+#pragma unroll 4
+                        for (int e = lane; e < valid * (D / 8); e += 32) {
+                            const int r = e / (D / 8);
+                            uint4 *p = piece(r, e % (D / 8)), u = *p;
+                            uint32_t *w = reinterpret_cast<uint32_t *>(&u);
+                            bool odd = false;
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const uint32_t f = w[x] & 0x7f807f80u;
+                                if ((f & 0xffffu) == 0x7f80u) { w[x] &= 0xffff0000u; odd = true; }
+                                if ((f >> 16) == 0x7f80u) { w[x] &= 0x0000ffffu; odd = true; }
+                            }
+                            if (ln[r] == 0) *p = zero;
+                            else if (odd) {
+                                *p = u;
+                                atomicOr(const_cast<uint32_t *>(&bad[r >> 5]), 1u << (r & 31));
+                            }
                         }
                     }
-                    if (i < cnt) mma_commit_w(empty((2 * jj) % C::SLOTS));
+                    fence_proxy_async();
+                    __syncwarp();
                 }
-                if (i > 0) mma_commit_w(empty((2 * jj - 1) % C::SLOTS));
-                valid = now;
+                if (lane == 0) mbar_arrive(v_ready(tile));
             }
-            j += cnt;
         }
     } else if (warp >= 4) {
         // ---------------------------------------------------------------- softmax
@@ -364,183 +474,120 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
         unsigned char *qs = smem + t * C::SLOT;
         const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q);
         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out);
-        uint32_t j = 0, met = 0;
-        bool first_seg = true;
-        // all softmax threads meet
-        auto meet = [&]() {
-            mbar_arrive(meet_bar);
-            return wait(meet_bar, met++ & 1);
+        // a unit's queries of this row tile, swizzled as the product reads them, all loads on their way
+        auto load_q = [&](const Run &u) {
+            constexpr int PIECES = D / 8, ROWS_PER = 128 / PIECES;           // rows per pass of the warpgroup
+            const int x = wg % PIECES, first = (u.r % sh.groups) * (QT * kTile) + t * kTile + wg / PIECES;
+            const __nv_bfloat16 *from = q + ((int64_t)u.n * a.M * a.H + (u.r / sh.groups) * G) * D;
+            uint4 f[PIECES];
+#pragma unroll
+            for (int y = 0; y < PIECES; ++y) {
+                const int rr = first + y * ROWS_PER;
+                f[y] = make_uint4(0u, 0u, 0u, 0u);
+                if (rr < rows)
+                    f[y] = __ldg(reinterpret_cast<const uint4 *>(from + ((int64_t)(rr / G) * a.H + rr % G) * D) + x);
+            }
+#pragma unroll
+            for (int y = 0; y < PIECES; ++y)
+                *reinterpret_cast<uint4 *>(qs + (x >> 3) * 16384 + sw128_off(y * ROWS_PER + wg / PIECES, x & 7)) = f[y];
+            fence_proxy_async();
+            mbar_arrive(q_full(t));
         };
-        for (; run.left > 0 && ok; run.advance(a, sh.groups)) {
+        uint32_t tile = 0, j = 0, seg = 0;                   // tiles, steps and segments before
+        auto sums_in = [&](uint32_t i) { return o_full(t, i & 1); };
+        auto phase = [](uint32_t i) { return (i >> 1) & 1; };
+        load_q(run);
+        for (; run.left > 0 && ok; run.advance(a, sh.groups), ++seg) {
             const int h = run.r / sh.groups, row0 = (run.r % sh.groups) * (QT * kTile) + t * kTile;
             const int cnt = run.count(), row = row0 + wg;
             const int64_t n = run.n;
-            // the row tile's queries, swizzled as the product reads them, eight loads on their way
-            constexpr int PIECES = D / 8, ROWS_PER = 128 / PIECES;           // rows per pass of the warpgroup
-#pragma unroll 1
-            for (int r0 = 0; r0 < kTile; r0 += 8 * ROWS_PER) {
-                uint4 u[8];
-                const int x = wg % PIECES;
-#pragma unroll
-                for (int y = 0; y < 8; ++y) {
-                    const int rr = row0 + r0 + y * ROWS_PER + wg / PIECES;
-                    u[y] = make_uint4(0u, 0u, 0u, 0u);
-                    if (rr < rows)
-                        u[y] = __ldg(reinterpret_cast<const uint4 *>(
-                                   q + ((n * a.M + rr / G) * a.H + h * G + rr % G) * (int64_t)D) + x);
-                }
-#pragma unroll
-                for (int y = 0; y < 8; ++y)
-                    *reinterpret_cast<uint4 *>(
-                        qs + (x >> 3) * 16384 + sw128_off(r0 + y * ROWS_PER + wg / PIECES, x & 7)) = u[y];
-            }
-            fence_proxy_async();
-            mbar_arrive(q_full(t));
             float top = -INFINITY, sum = 0.f;
-            uint64_t mine = 0, bad = 0;              // known from the tree tile on
-            for (int i = 0; i < cnt; ++i) {
-                const uint32_t jj = j + i;
+            uint64_t mine = 0;                       // known from the tree tile on
+            int done = 0;                            // steps of this segment
+            for (int i = 0; i < cnt && ok; ++i) {
                 const int tl = run.t0 + i;
                 const bool tree = tl == run.tiles - 1;
                 const int valid = valid_keys(a, run, tl);
-                const bool wide = valid > 64;
-                const int b = QT == 1 ? (int)(jj & 1) : t;
-                const uint32_t s_col = tmem + lanes + b * 128;
-                if (tree || valid < kTile) {
-                    // the value tile's rows past the last key: zeros (a weight of zero would
-                    // not cancel a NaN).  In the tree tile also the rows of no node, and every
-                    // value that is not finite: those are added at the end to the rows that see them.
-                    const uint32_t use = 2 * jj + 1;
-                    if (!wait(full(use % C::SLOTS), (use / C::SLOTS) & 1)) break;
-                    if (tree) {
-                        if (!meet()) break;          // the unit before is done with the lines
-                        if (tid == 128) words[W_BAD0] = words[W_BAD1] = 0;
-                        if (t == 0 && wg < a.M) line[wg] = tree_line(a.parent + n * a.M, wg);
-                        if (!meet()) break;
-                        mine = row < rows ? line[row / G] : 0;
-                    }
-                    if (t == 0) {
-                        unsigned char *vs = smem + C::O_RING + (use % C::SLOTS) * C::SLOT;
-                        const int until = (valid + 15) & ~15;
-                        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-                        auto piece = [&](int r, int x) {
-                            return reinterpret_cast<uint4 *>(vs + (r >> 3) * (C::HALVES * 1024) + (x >> 3) * 1024 +
-                                                             sw128_off(r & 7, x & 7));
-                        };
-                        for (int e = wg; e < (until - valid) * (D / 8); e += 128)
-                            *piece(valid + e / (D / 8), e % (D / 8)) = zero;
-                        if (tree) {
-                            for (int e = wg; e < valid * (D / 8); e += 128) {
-                                const int r = e / (D / 8);
-                                uint4 *p = piece(r, e % (D / 8)), u = *p;
-                                const bool node = line[r] != 0;
-                                uint32_t *w = reinterpret_cast<uint32_t *>(&u);
-                                bool odd = false;
-#pragma unroll
-                                for (int x = 0; x < 4; ++x) {
-                                    const uint32_t f = w[x] & 0x7f807f80u;
-                                    if ((f & 0xffffu) == 0x7f80u) { w[x] &= 0xffff0000u; odd = true; }
-                                    if ((f >> 16) == 0x7f80u) { w[x] &= 0x0000ffffu; odd = true; }
-                                }
-                                if (!node) *p = zero;
-                                else if (odd) {
-                                    *p = u;
-                                    atomicOr(const_cast<uint32_t *>(&words[r < 32 ? W_BAD0 : W_BAD1]), 1u << (r & 31));
-                                }
-                            }
-                        }
-                        fence_proxy_async();
-                    }
-                    if (tree) {
-                        if (!meet()) break;
-                        bad = words[W_BAD0] | (uint64_t)words[W_BAD1] << 32;
-                    }
+                if (tree) {
+                    if (!wait(v_ready(tile + i), ((tile + i) / C::RING) & 1)) break;
+                    mine = row < rows ? line[(seg % C::RING) * kMaxTreeNodes + row / G] : 0;
                 }
-                if (!wait(s_full(b), (QT == 1 ? jj >> 1 : jj) & 1)) break;
-                tc_fence_after();
-                float v[64];
-                auto mask = [&](int off) {
+                const int halves = (valid + 63) / 64;
+                for (int x = 0; x < halves; ++x, ++done, ++j) {
+                    const uint32_t b = j % C::BUFS, sc = tmem + lanes + s_col(t, b);
+                    if (!wait(s_full(t, b), (j / C::BUFS) & 1)) break;
+                    // step i's sums complete phase i / 2 of barrier i % 2; waiting here for those
+                    // two steps back (in already: the scores were issued after them) keeps a
+                    // phase from being passed over twice
+                    if (done >= 2 && !wait(sums_in(j - 2), phase(j - 2))) break;
+                    tc_fence_after();
+                    float v[64];
+                    tmem_ld64(sc, v);
                     if (tree) {
 #pragma unroll
                         for (int e = 0; e < 64; ++e) v[e] = (mine >> e & 1) != 0 ? v[e] : -INFINITY;
-                    } else if (valid < kTile) {
+                    } else if (valid < 64 * x + 64) {
 #pragma unroll
-                        for (int e = 0; e < 64; ++e) v[e] = off + e < valid ? v[e] : -INFINITY;
+                        for (int e = 0; e < 64; ++e) v[e] = 64 * x + e < valid ? v[e] : -INFINITY;
                     }
-                };
-                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                auto widen = [&]() {
+                    float m4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-                    for (int e = 0; e < 64; ++e) m4[e & 3] = fmaxf(m4[e & 3], v[e]);
-                };
-                if (wide) {
-                    tmem_ld64(s_col + 64, v);
-                    mask(64);
-                    widen();
-                }
-                tmem_ld64(s_col, v);
-                mask(0);
-                widen();
-                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
-                const bool grow = mx > top + kGrow;
-                const bool rescale = __any_sync(0xffffffffu, grow) && i > 0;
-                const float was = top;
-                if (grow) top = mx;
-                const float shrink = grow ? ex2(was - top) : 1.f;
-                sum *= shrink;
-                if (rescale) {
-                    // the sums of the tile before are in
-                    if (!wait(o_full(t), (jj - 1) & 1)) break;
-                    tc_fence_after();
+                    for (int e = 4; e < 64; e += 4) {
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) m4[y] = fmaxf(m4[y], v[e + y]);
+                    }
+                    const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
+                    const bool grow = mx > top + kGrow;
+                    const float was = top;
+                    if (grow) top = mx;
+                    const float shrink = grow ? ex2(was - top) : 1.f;
+                    sum *= shrink;
+                    if (done > 0 && __any_sync(0xffffffffu, grow)) {
+                        if (!wait(sums_in(j - 1), phase(j - 1))) break;
+                        tc_fence_after();
 #pragma unroll 1
-                    for (int x = 0; x < D; x += 32) {
-                        float o[32];
-                        tmem_ld32(o_col + x, o);
+                        for (int y = 0; y < D; y += 32) {
+                            float o[32];
+                            tmem_ld32(o_col + y, o);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] *= shrink;
-                        tmem_st32(o_col + x, o);
+                            for (int e = 0; e < 32; ++e) o[e] *= shrink;
+                            tmem_st32(o_col + y, o);
+                        }
                     }
-                }
-                const float from = top == -INFINITY ? 0.f : top;
-                const float2 c2 = make_float2(c, c), f2 = make_float2(-from, -from);
-                float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                auto weigh = [&](uint32_t col) {
+                    const float from = top == -INFINITY ? 0.f : top;
+                    const float2 c2 = make_float2(c, c), f2 = make_float2(-from, -from);
+                    float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                     float w[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        float2 x = f2fma(make_float2(v[2 * e], v[2 * e + 1]), c2, f2);
-                        x.x = ex2(x.x);
-                        x.y = ex2(x.y);
-                        add[e & 1] = f2add(add[e & 1], x);
-                        w[e] = __uint_as_float(pack_bf16x2(x.x, x.y));
+                        float2 y = f2fma(make_float2(v[2 * e], v[2 * e + 1]), c2, f2);
+                        y.x = ex2(y.x);
+                        y.y = ex2(y.y);
+                        add[e & 1] = f2add(add[e & 1], y);
+                        w[e] = __uint_as_float(pack_bf16x2(y.x, y.y));
                     }
-                    tmem_st32_nowait(col, w);
-                };
-                weigh(s_col);
-                tmem_wait_st();
-                // (waiting for the sums of the tile before each time keeps the phases in step)
-                if (i > 0 && !rescale && !wait(o_full(t), (jj - 1) & 1)) break;
-                tc_fence_before();
-                mbar_arrive(p_full(b, 0));
-                if (wide) {
-                    tmem_ld64(s_col + 64, v);
-                    mask(64);
-                    weigh(s_col + 32);
+                    tmem_st32_nowait(sc, w);
+                    sum += (add[0].x + add[0].y) + (add[1].x + add[1].y);
                     tmem_wait_st();
                     tc_fence_before();
+                    mbar_arrive(p_full(t, b));
                 }
-                mbar_arrive(p_full(b, 1));
-                sum += (add[0].x + add[0].y) + (add[1].x + add[1].y);
             }
-            j += cnt;
+            tile += cnt;
             if (!ok) break;
-            if (!wait(o_full(t), (j - 1) & 1)) break;
+            // the next unit's first scores run during this one's end
+            Run then = run;
+            then.advance(a, sh.groups);
+            if (then.left > 0) load_q(then);
+            if (done >= 2 && !wait(sums_in(j - 2), phase(j - 2))) break;
+            if (!wait(sums_in(j - 1), phase(j - 1))) break;
             tc_fence_after();
             const bool whole = run.t0 == 0 && cnt == run.tiles;
             const int64_t o_row = (n * a.M + row / G) * (int64_t)a.H + h * G + row % G;
-            const uint64_t add_bad = bad & mine;
+            volatile uint32_t *bad = words + W_BAD + 2 * (seg % C::RING);
+            const uint64_t add_bad = mine == 0 ? 0 : mine & (bad[0] | (uint64_t)bad[1] << 32);
             constexpr int R = QT * kTile;
-            const int slot = 2 * blockIdx.x + (first_seg && run.t0 > 0 ? 0 : 1);
+            const int slot = 2 * blockIdx.x + (seg == 0 && run.t0 > 0 ? 0 : 1);
             float *part = sh.part + (size_t)slot * R * (D + 2);
             const float inv = mine == 0 ? 0.f : 1.f / sum;
 #pragma unroll 1
@@ -587,7 +634,6 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                 }
             }
             tc_fence_before();
-            first_seg = false;
         }
     }
     tc_fence_before();
