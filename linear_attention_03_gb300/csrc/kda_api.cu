@@ -516,9 +516,7 @@ kda_status kda_tree_attention(const void *q, const void *k_new, const void *v_ne
     kda::TreeAttention a{q, k_new, v_new, k_cache, v_cache, page_table, cache_lens, parent, out, lse,
                          static_cast<int32_t *>(workspace), N, M, dims.H, H_kv, num_pages, page_size,
                          max_pages, scale};
-    cudaError_t err = cudaMemsetAsync(workspace, 0, sizeof(int32_t), s);
-    if (err != cudaSuccess) return cuda_fail(err, "clearing the status word");
-    err = kda::launch_tree_attention(a, dims.d_k, (kda_dtype)dims.qkv_dtype,
+    cudaError_t err = kda::launch_tree_attention(a, dims.d_k, (kda_dtype)dims.qkv_dtype,
                                      static_cast<unsigned char *>(workspace) + kStatusBytes, s);
     if (err != cudaSuccess) return cuda_fail(err, "tree attention launch");
     return KDA_OK;

@@ -206,6 +206,7 @@ struct TreeAttention {
 };
 size_t tree_attention_partial_bytes(int32_t N, int32_t M, int32_t H, int32_t H_kv, int32_t D, kda_dtype dt,
                                     int32_t page_size, int32_t max_pages);
+// (both forms set the status word: to zero, or to what the device found)
 cudaError_t launch_tree_attention(const TreeAttention &a, int32_t D, kda_dtype dt, void *workspace,
                                   cudaStream_t stream);
 // the same on the tensor cores: bf16, d = 64 or 128, pages of whole groups of eight tokens

@@ -61,6 +61,13 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// ------------------------------------------------------------------ launches
+
+// Lets the next kernel of the stream start, when it was launched to overlap this one.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Waits until the kernels before are complete and their writes are visible.
+__device__ __forceinline__ void wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ------------------------------------------------------------------ TMA
 
 // Prefetch a 2-D tile of a tensor map into L2 (no shared-memory destination).

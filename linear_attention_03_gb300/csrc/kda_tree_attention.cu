@@ -304,6 +304,8 @@ cudaError_t launch_tree_attention(const TreeAttention &a, int32_t D, kda_dtype d
                                   cudaStream_t stream) {
     if (tree_attention_tc_supported(a.H_kv, D, dt, a.num_pages, a.page_size))
         return launch_tree_attention_tc(a, D, workspace, stream);
+    const cudaError_t e = cudaMemsetAsync(a.status, 0, sizeof(int32_t), stream);
+    if (e != cudaSuccess) return e;
     if (dt == KDA_BF16) KDA_DISPATCH_D(D, (run<__nv_bfloat16, DD>(a, workspace, stream)))
     KDA_DISPATCH_D(D, (run<float, DD>(a, workspace, stream)))
 }

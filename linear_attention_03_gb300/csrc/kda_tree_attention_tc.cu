@@ -61,10 +61,10 @@ template <int D, int QT> struct Cfg {
     // while warp 3 prepares the tiles that the ring holds after it.
     static constexpr int RING = D == 64 ? 8 : 4;
     static_assert(RING > SLOTS / 2, "ring of lines");
-    static constexpr int NBARS = 2 * SLOTS + 14 + RING;
+    static constexpr int NBARS = 2 * SLOTS + 18 + RING;
     static constexpr int O_LINES = O_MISC + 8 * NBARS, O_WORDS = O_LINES + RING * 8 * kMaxTreeNodes;
     static constexpr int SMEM = O_MISC + (D == 64 ? 8192 : 3072);
-    static_assert(O_WORDS + 8 + 8 * RING <= SMEM, "misc");
+    static_assert(O_WORDS + 16 + 8 * RING <= SMEM, "misc");
     static constexpr int BUFS = 4 / QT;        // score buffers per row tile
     static constexpr int AHEAD = BUFS / 2;     // steps by which the scores lead the sums
     // TMEM columns: scores (and the weights in their place), then the sums
@@ -73,18 +73,12 @@ template <int D, int QT> struct Cfg {
 static_assert(Cfg<128, 1>::SMEM <= 232448 && Cfg<128, 2>::SMEM <= 232448, "227 KB of shared memory");
 
 // misc: the mbarriers, the trees' lines, then these 32-bit words (two of W_BAD per segment of the ring)
-enum { W_TMEM = 0, W_ABORT, W_BAD };
+enum { W_TMEM = 0, W_ABORT, W_STATUS, W_BAD };
 
 struct Maps {
     CUtensorMap k, v, kn, vn;
 };
 
-struct Shape {
-    int32_t box;            // rows per load: the power of two that divides the page size, at most 128
-    int32_t groups;         // row groups (q tiles of QT x 128 rows) per cache head
-    int32_t ctas;
-    float *part;            // two slots per CTA: D/4 x rows float4, then rows maxima, rows sums
-};
 
 __device__ __forceinline__ int clamped_len(const TreeAttention &a, int64_t n) {
     const int len = a.cache_lens[n];
@@ -102,25 +96,37 @@ __device__ __forceinline__ int64_t piece_start(int64_t total, int ctas, int b) {
     return total * b / ctas;
 }
 
-// The line of all tiles: total, and the sequence and unit that hold tile `at`.
+// Where a CTA's piece starts: total tiles of the line, and the sequence and unit
+// that hold its first tile.  Each CTA leaves its own in the workspace, with the
+// status it found, for the kernel that joins the pieces.
 struct Place {
     int64_t total, unit0;   // unit0: where the unit starts on the line
     int32_t n, r, len;      // sequence, unit within it, its clamped length
+    int32_t status;
 };
+struct Shape {
+    int32_t box;            // rows per load: the power of two that divides the page size, at most 128
+    int32_t groups;         // row groups (q tiles of QT x 128 rows) per cache head
+    int32_t ctas;
+    Place *places;          // one per CTA
+    float *part;            // two slots per CTA: D/4 x rows float4, then rows maxima, rows sums
+};
+
 // The whole block calls it; `buf` holds 34 int64 of shared memory.
 __device__ void find_place(const TreeAttention &a, int groups, int ctas, int b, int64_t *buf, Place &out) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     const int per_seq = a.H_kv * groups;
     int64_t sum = 0;
+    bool bad = false;
     for (int n = tid; n < a.N; n += blockDim.x) {
         const int len = a.cache_lens[n];
-        if (len < 0 || len > (int64_t)a.max_pages * a.page_size) flag_status(a.status, KDA_DEVICE_BAD_LENGTH);
+        bad = bad || len < 0 || len > (int64_t)a.max_pages * a.page_size;
         sum += (int64_t)unit_tiles(clamped_len(a, n)) * per_seq;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) buf[warp] = sum;
-    __syncthreads();
+    out.status = __syncthreads_or(bad) != 0 ? KDA_DEVICE_BAD_LENGTH : KDA_DEVICE_OK;
     int64_t total = 0;
     for (int w = 0; w < warps; ++w) total += buf[w];
     __syncthreads();
@@ -201,9 +207,9 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
     auto empty = [&](int s) { return bars + 8u * (C::SLOTS + s); };
     auto s_full = [&](int t, uint32_t b) { return bars + 8u * (2 * C::SLOTS + C::BUFS * t + b); };
     auto p_full = [&](int t, uint32_t b) { return bars + 8u * (2 * C::SLOTS + 4 + C::BUFS * t + b); };
-    auto o_full = [&](int t, int b) { return bars + 8u * (2 * C::SLOTS + 8 + 2 * t + b); };
-    auto q_full = [&](int t) { return bars + 8u * (2 * C::SLOTS + 12 + t); };
-    auto v_ready = [&](uint32_t i) { return bars + 8u * (2 * C::SLOTS + 14 + i % C::RING); };
+    auto o_full = [&](int t, uint32_t i) { return bars + 8u * (2 * C::SLOTS + 8 + 4 * t + (i & 3)); };
+    auto q_full = [&](int t) { return bars + 8u * (2 * C::SLOTS + 16 + t); };
+    auto v_ready = [&](uint32_t i) { return bars + 8u * (2 * C::SLOTS + 18 + i % C::RING); };
     // scores of row tile t, buffer b (the weights go in their place)
     auto s_col = [](int t, uint32_t b) { return t * 128 + b * 64; };
 
@@ -211,6 +217,9 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
     find_place(a, sh.groups, sh.ctas, blockIdx.x, reinterpret_cast<int64_t *>(smem), place);
     const int64_t start = piece_start(place.total, sh.ctas, blockIdx.x);
     const int64_t stop = piece_start(place.total, sh.ctas, blockIdx.x + 1);
+    Place *left = sh.places + blockIdx.x;
+    if (tid == 0) *left = place;
+    launch_dependents();
     if (start >= stop) return;                               // the whole block
     Run run;
     run.left = stop - start;
@@ -231,26 +240,27 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                 mbar_init(s_full(t, b), 1);
                 mbar_init(p_full(t, b), 128);
             }
-            mbar_init(o_full(t, 0), 1);
-            mbar_init(o_full(t, 1), 1);
+            for (int b = 0; b < 4; ++b) mbar_init(o_full(t, b), 1);
             mbar_init(q_full(t), 128);
         }
         for (int i = 0; i < C::RING; ++i) mbar_init(v_ready(i), 1);
         fence_mbar_init();
         words[W_ABORT] = 0;
+        words[W_STATUS] = place.status;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, words[W_TMEM], 0);
     bool ok = true;
+    auto flag = [&](uint32_t code) { atomicCAS(const_cast<uint32_t *>(&words[W_STATUS]), 0u, code); };
     // a bounded wait of a whole warp; once one gives up, the warp stops
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (ok) {
             ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
             if (!ok) {
                 words[W_ABORT] = 1;
-                flag_status(a.status, KDA_DEVICE_TIMEOUT);
+                flag(KDA_DEVICE_TIMEOUT);
             }
         }
         return ok;
@@ -273,7 +283,7 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                     const int pos = t * kTile + lane * sh.box;
                     const int page = table[pos / a.page_size];
                     if (page < 0 || page >= a.num_pages) {
-                        flag_status(a.status, KDA_DEVICE_BAD_PAGE);
+                        flag(KDA_DEVICE_BAD_PAGE);
                         group = none;
                     } else {
                         group = (int32_t)((((int64_t)page * a.H_kv + h) * a.page_size + pos % a.page_size) / 8);
@@ -384,7 +394,7 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                             mma_tmem_a_w(o, p + ks * 8, HI_V | sw128_lo(vb + ks * 2 * C::HALVES * 1024), ID_PV,
                                          ks > 0 ? 1u : more);
                 }
-                mma_commit_w(o_full(t, su.j & 1));
+                mma_commit_w(o_full(t, su.j));
                 next(su);
             }
         }
@@ -494,8 +504,10 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
             mbar_arrive(q_full(t));
         };
         uint32_t tile = 0, j = 0, seg = 0;                   // tiles, steps and segments before
-        auto sums_in = [&](uint32_t i) { return o_full(t, i & 1); };
-        auto phase = [](uint32_t i) { return (i >> 1) & 1; };
+        // Step i's sums complete phase i / 4 of barrier i % 4.  Who asks for step j - 1 has
+        // seen the scores of step j, and those were issued after the sums of step j - 3 at
+        // least: step j - 5's phase is long over, and step j + 3's cannot be.
+        auto wait_sums = [&](uint32_t i) { return wait(o_full(t, i), (i >> 2) & 1); };
         load_q(run);
         for (; run.left > 0 && ok; run.advance(a, sh.groups), ++seg) {
             const int h = run.r / sh.groups, row0 = (run.r % sh.groups) * (QT * kTile) + t * kTile;
@@ -516,10 +528,6 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                 for (int x = 0; x < halves; ++x, ++done, ++j) {
                     const uint32_t b = j % C::BUFS, sc = tmem + lanes + s_col(t, b);
                     if (!wait(s_full(t, b), (j / C::BUFS) & 1)) break;
-                    // step i's sums complete phase i / 2 of barrier i % 2; waiting here for those
-                    // two steps back (in already: the scores were issued after them) keeps a
-                    // phase from being passed over twice
-                    if (done >= 2 && !wait(sums_in(j - 2), phase(j - 2))) break;
                     tc_fence_after();
                     float v[64];
                     tmem_ld64(sc, v);
@@ -543,7 +551,7 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                     const float shrink = grow ? ex2(was - top) : 1.f;
                     sum *= shrink;
                     if (done > 0 && __any_sync(0xffffffffu, grow)) {
-                        if (!wait(sums_in(j - 1), phase(j - 1))) break;
+                        if (!wait_sums(j - 1)) break;
                         tc_fence_after();
 #pragma unroll 1
                         for (int y = 0; y < D; y += 32) {
@@ -579,8 +587,7 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
             Run then = run;
             then.advance(a, sh.groups);
             if (then.left > 0) load_q(then);
-            if (done >= 2 && !wait(sums_in(j - 2), phase(j - 2))) break;
-            if (!wait(sums_in(j - 1), phase(j - 1))) break;
+            if (!wait_sums(j - 1)) break;
             tc_fence_after();
             const bool whole = run.t0 == 0 && cnt == run.tiles;
             const int64_t o_row = (n * a.M + row / G) * (int64_t)a.H + h * G + row % G;
@@ -642,20 +649,33 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    if (tid == 0) left->status = (int32_t)words[W_STATUS];
 }
 
-// Joins the units that were cut.  Block (b, y): the cut between CTAs b and
-// b + 1, rows 16 y .. 16 y + 15 of its unit; it works when that is the unit's
-// first cut.
+// Joins the units that were cut.  Block (b, y), b > 0: the cut between CTAs
+// b - 1 and b, rows 16 y .. 16 y + 15 of its unit; it works when that is the
+// unit's first cut.  Block (0, 0) gathers the status.  Its launch overlaps the
+// kernel before it, whose results it waits for.
 template <int D, int QT>
 __global__ void __launch_bounds__(256)
 tree_attention_tc_join_kernel(const TreeAttention a, const Shape sh) {
     constexpr int R = QT * kTile, ROWS = 16;
-    __shared__ int64_t buf[34];
-    const int b = blockIdx.x + 1;
+    const int b = blockIdx.x;
     const int G = a.H / a.H_kv, rows = a.M * G;
-    Place p;
-    find_place(a, sh.groups, sh.ctas, b, buf, p);
+    wait_prerequisites();
+    if (b == 0) {
+        if (blockIdx.y != 0) return;
+        int32_t code = 0;
+        for (int i = threadIdx.x; i < sh.ctas; i += 256) code = max(code, sh.places[i].status);
+        const bool timeout = __syncthreads_or(code == KDA_DEVICE_TIMEOUT) != 0;
+        const bool page = __syncthreads_or(code == KDA_DEVICE_BAD_PAGE) != 0;
+        const bool length = __syncthreads_or(code == KDA_DEVICE_BAD_LENGTH) != 0;
+        if (threadIdx.x == 0)
+            *a.status = timeout ? KDA_DEVICE_TIMEOUT : page ? KDA_DEVICE_BAD_PAGE
+                        : length ? KDA_DEVICE_BAD_LENGTH : KDA_DEVICE_OK;
+        return;
+    }
+    const Place p = sh.places[b];
     const int64_t at = piece_start(p.total, sh.ctas, b);
     if (at >= p.total || p.unit0 == at || piece_start(p.total, sh.ctas, b - 1) > p.unit0) return;
     const int64_t end = p.unit0 + unit_tiles(p.len);
@@ -737,6 +757,8 @@ int sm_count() {
     return sms;
 }
 
+size_t place_bytes(int ctas) { return ((size_t)ctas * sizeof(Place) + 255) / 256 * 256; }
+
 template <int D, int QT> cudaError_t run_tc(const TreeAttention &a, void *workspace, cudaStream_t stream) {
     using C = Cfg<D, QT>;
     Maps maps;
@@ -750,17 +772,27 @@ template <int D, int QT> cudaError_t run_tc(const TreeAttention &a, void *worksp
     const int rows = a.M * (a.H / a.H_kv);
     sh.groups = (rows + QT * kTile - 1) / (QT * kTile);
     sh.ctas = sm_count();
-    sh.part = static_cast<float *>(workspace);
+    sh.places = static_cast<Place *>(workspace);
+    sh.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + place_bytes(sh.ctas));
     static std::atomic<uint64_t> smem_set{0};
     cudaError_t e = allow_dynamic_smem(tree_attention_tc_kernel<D, QT>, C::SMEM, smem_set);
     if (e != cudaSuccess) return e;
     tree_attention_tc_kernel<D, QT><<<sh.ctas, C::THREADS, C::SMEM, stream>>>(maps, a, sh);
     count_launches(1);
-    if (sh.ctas > 1) {
-        const int blocks = ((rows < QT * kTile ? rows : QT * kTile) + 15) / 16;
-        tree_attention_tc_join_kernel<D, QT><<<dim3(sh.ctas - 1, blocks), 256, 0, stream>>>(a, sh);
-        count_launches(1);
-    }
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const int blocks = ((rows < QT * kTile ? rows : QT * kTile) + 15) / 16;
+    cudaLaunchAttribute overlap;
+    overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    overlap.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sh.ctas, blocks);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = &overlap;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, tree_attention_tc_join_kernel<D, QT>, a, sh);
+    if (e != cudaSuccess) return e;
+    count_launches(1);
     return cudaGetLastError();
 }
 
@@ -773,7 +805,8 @@ bool tree_attention_tc_supported(int32_t H_kv, int32_t D, kda_dtype dt, int64_t 
 
 size_t tree_attention_tc_partial_bytes(int32_t M, int32_t H, int32_t H_kv, int32_t D) {
     const int tiles = M * (H / H_kv) <= kTile ? 1 : 2;
-    return (size_t)sm_count() * 2 * tiles * kTile * (D + 2) * 4;
+    const int ctas = sm_count();
+    return place_bytes(ctas) + (size_t)ctas * 2 * tiles * kTile * (D + 2) * 4;
 }
 
 cudaError_t launch_tree_attention_tc(const TreeAttention &a, int32_t D, void *workspace, cudaStream_t stream) {

@@ -107,8 +107,9 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 
 def _dev(t, name, dtype=None, shape=None):
-    if t is None:
-        return None
+    if t is None or (isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous()
+                     and (dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape)):
+        return t
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
@@ -121,11 +122,18 @@ def _dev(t, name, dtype=None, shape=None):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    # a plain address: every function's argument types are declared above
+    return None if t is None else t.data_ptr()
+
+
+# the current stream's handle without building a torch.cuda.Stream (3 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _offsets(cu_seqlens, T, device):
@@ -301,7 +309,7 @@ def kda_prologue_prefill(q_raw, k_raw, v_raw, conv_w, z_g, z_beta, init_state=No
     st = lib.kda_prologue_prefill(_ptr(q_raw), _ptr(k_raw), _ptr(v_raw), _ptr(conv_w), _ptr(z_g),
                                   _ptr(z_beta), _ptr(init_state), T, dims, segment_tokens, _ptr(out),
                                   _ptr(final_state), _ptr(workspace), workspace.numel(), _stream(),
-                                  ctypes.c_void_p(side.cuda_stream))
+                                  side.cuda_stream)
     if st != KDA_OK:
         raise KDAError(st, "kda_prologue_prefill")
     return out, final_state
