@@ -12,12 +12,29 @@
 #include "kda_internal.cuh"
 #include "kda_tree.cuh"
 
+#include <cooperative_groups.h>
+
 namespace kda {
 namespace {
 
+// A probability as a whole number of 2^-38, rounded toward zero, in two digits
+// of 19 bits.  Adding 2^23 with rounding toward zero leaves the whole part in
+// the significand's low bits, and what remains is exact: three fused
+// multiply-adds and an add at full rate, where a conversion to 64 bits runs at
+// a small part of it (131,072 tokens x 256 chains with draft probabilities: 125
+// us converting, 57 us with the digits).  The digits carry 2^23's bits with them.
+constexpr uint32_t kBias = 0x4b000000u;
+__device__ __forceinline__ void digits38(float p, uint32_t &hi, uint32_t &lo) {
+    p = fminf(fmaxf(p, 0.f), 1.f);                     // fmaxf drops a NaN
+    const float h = __fmaf_rz(p, 524288.f, 8388608.f);
+    const float rest = fmaf(p, 524288.f, -(h - 8388608.f));
+    hi = __float_as_uint(h);
+    lo = __float_as_uint(__fmaf_rz(rest, 524288.f, 8388608.f));
+}
 __device__ __forceinline__ uint64_t fixed38(float p) {
-    // fmaxf drops a NaN; the scaling is exact, the conversion rounds toward zero
-    return __float2ull_rz(fminf(fmaxf(p, 0.f), 1.f) * 274877906944.f);
+    uint32_t hi, lo;
+    digits38(p, hi, lo);
+    return ((uint64_t)(hi - kBias) << 19) + (lo - kBias);
 }
 // a uniform number in [0, 1) in steps of 2^-24 (out-of-range and NaN clamped)
 __device__ __forceinline__ uint32_t tick24(float u) {
@@ -41,209 +58,298 @@ template <> struct Row<__nv_bfloat16> {
     }
 };
 
-struct Walk {
-    int32_t cur;        // the last accepted node (-1: the sequence is not in use)
-    int32_t refused;    // how many of its children were refused
-};
+constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32;
+constexpr int kMaxCluster = 8;      // CTAs of a sequence
 
-constexpr int kVerifyThreads = 1024;
-
-// One CTA per sequence.  The drafted tokens' probabilities are gathered first,
-// then one thread walks the tree (a child's index exceeds its parent's and the
-// refused siblings' order is the index order, so one ascending pass visits
-// every step), then all warps sum the last node's row and one warp finds the
-// token.
+// One cluster per sequence.  Every CTA gathers the drafted tokens'
+// probabilities and its first warp walks the tree (each step tests one child,
+// in index order); the walk is short, so all CTAs make it.  Then each sums its
+// share of the last node's row, the totals cross the cluster, and the warp
+// whose sums hold the drawn mass finds the token.  The rows' bytes bound it: a
+// row is read once, and the one warp's share a second time, from the L2.
+// Measured: 256 chains over 131,072 tokens, fp32 with draft probabilities (235
+// MB), 52 us, 4.5 TB/s; bf16 40 us.  What is left above the bytes are the
+// prologue's three dependent loads, the cluster's meeting and the second pass.
 template <typename Tin>
-__global__ void __launch_bounds__(kVerifyThreads)
+__global__ void __launch_bounds__(kVerifyThreads, 4)
 verify_kernel(const Tin *__restrict__ target, const Tin *__restrict__ draft,
               const int32_t *__restrict__ tokens, const int32_t *__restrict__ parent,
               const float *__restrict__ uniforms, int32_t M, int32_t V, int32_t *__restrict__ accept,
               int32_t *__restrict__ path, int32_t *__restrict__ next_token) {
-    constexpr int VEC = Row<Tin>::VEC, WARPS = kVerifyThreads / 32;
-    __shared__ float px[kMaxTreeNodes], qx[kMaxTreeNodes];
-    __shared__ int32_t tok[kMaxTreeNodes], par[kMaxTreeNodes], gone[kMaxTreeNodes], step[kMaxTreeNodes];
-    __shared__ Walk walk;
-    __shared__ int32_t count;
-    __shared__ unsigned long long part[WARPS];
-    __shared__ unsigned long long whole;
+    constexpr int VEC = Row<Tin>::VEC, BATCH = 16 / VEC;   // BATCH loads of 16 bytes on their way per lane and row
+    typedef unsigned long long u64;
+    __shared__ int32_t gone[kMaxTreeNodes];            // the last node's refused children's tokens, each once
+    __shared__ int32_t walk_cur, walk_gone, walk_any;
+    __shared__ uint32_t walk_draw;
+    __shared__ u64 part[kVerifyWarps];
+    __shared__ u64 totals[2][kMaxCluster];             // of both attempts
+    cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+    const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t n = blockIdx.x;
+    const int64_t n = blockIdx.x / ranks;
 
-    if (tid < M) {
-        const int p = parent[n * M + tid], t = tokens[n * M + tid];
-        par[tid] = p;
-        tok[tid] = t;
-        float a = 0.f, b = 0.f;
-        if (p >= 0 && p < tid && t >= 0 && t < V) {
-            a = Elem<Tin>::load(target + (n * M + p) * V + t);
-            if (draft != nullptr) b = Elem<Tin>::load(draft + (n * M + p) * V + t);
+    if (warp == 0) {
+        // lane holds nodes lane and lane + 32
+        int par[2], tok[2];
+        float px[2], qx[2], un[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const int m = lane + 32 * y;
+            par[y] = m < M ? parent[n * M + m] : -2;
+            tok[y] = m < M ? tokens[n * M + m] : -1;
+            un[y] = m < M ? uniforms[n * (M + 1) + m] : 0.f;
         }
-        px[tid] = a;
-        qx[tid] = b;
-    }
-    __syncthreads();
-    if (tid == 0) {
-        int cur = par[0] == -1 ? 0 : -1, refused = 0, cnt = cur == 0 ? 1 : 0;
-        if (cur == 0) step[0] = 0;
-        unsigned long long spent = 0;
-        for (int m = 1; m < M && cur >= 0; ++m) {
-            if (par[m] != cur) continue;
-            const int t = tok[m];
-            const bool good = t >= 0 && t < V;
-            bool take;
-            unsigned long long mass = 0;
-            if (draft != nullptr) {
-                // the first child alone was sampled from the whole draft distribution
-                take = good && refused == 0 && uniforms[n * (M + 1) + cur] * qx[m] < px[m];
-            } else {
+        const float u_draw = uniforms[n * (M + 1) + M];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const bool good = par[y] >= 0 && par[y] < lane + 32 * y && tok[y] >= 0 && tok[y] < V;
+            const int64_t at = (n * M + par[y]) * V + tok[y];
+            px[y] = good ? Elem<Tin>::load(target + at) : 0.f;
+            qx[y] = good && draft != nullptr ? Elem<Tin>::load(draft + at) : 0.f;
+            if (par[y] >= lane + 32 * y) par[y] = -2;
+        }
+        auto of = [&](const float (&x)[2], int m) {
+            const float a = __shfl_sync(0xffffffffu, x[0], m & 31), b = __shfl_sync(0xffffffffu, x[1], m & 31);
+            return m < 32 ? a : b;
+        };
+        int cur = __shfl_sync(0xffffffffu, par[0], 0) == -1 ? 0 : -1, cnt = 0, ng = 0, any = 0;
+        while (cur >= 0) {
+            if (rank == 0 && lane == 0) path[n * M + cnt] = cur;
+            ++cnt;
+            const float u = of(un, cur);
+            const u64 tick = (u64)tick24(u) << 14;
+            u64 kids = __ballot_sync(0xffffffffu, par[0] == cur) | (u64)__ballot_sync(0xffffffffu, par[1] == cur) << 32;
+            u64 spent = 0;
+            int into = -1;
+            ng = any = 0;
+            while (kids != 0) {
+                const int m = __ffsll((long long)kids) - 1;
+                kids &= kids - 1;
+                const int t0 = __shfl_sync(0xffffffffu, tok[0], m & 31), t1 = __shfl_sync(0xffffffffu, tok[1], m & 31);
+                const int t = m < 32 ? t0 : t1;
+                const bool good = t >= 0 && t < V;
+                const float p = of(px, m);
+                // was this token refused before, as an elder sibling's?
                 bool twice = false;
-                for (int i = 0; i < refused; ++i) twice |= gone[i] == t;
-                mass = good && !twice ? fixed38(px[m]) : 0;
-                take = ((unsigned long long)tick24(uniforms[n * (M + 1) + cur]) << 14) < spent + mass;
-            }
-            if (take) {
-                cur = m;
-                step[cnt++] = m;
-                refused = 0;
-                spent = 0;
-            } else {
-                gone[refused++] = t;
+                for (int i = lane; i < ng; i += 32) twice |= gone[i] == t;
+                twice = __any_sync(0xffffffffu, twice);
+                bool take;
+                u64 mass = 0;
+                if (draft != nullptr) {
+                    // the first child alone was sampled from the whole draft distribution
+                    take = good && any == 0 && u * of(qx, m) < p;
+                } else {
+                    mass = good && !twice ? fixed38(p) : 0;
+                    take = tick < spent + mass;
+                }
+                if (take) {
+                    into = m;
+                    break;
+                }
                 spent += mass;
+                any = 1;
+                if (good && !twice) {
+                    if (lane == 0) gone[ng] = t;
+                    ++ng;
+                    __syncwarp();
+                }
             }
+            if (into < 0) break;
+            cur = into;
         }
-        walk.cur = cur;
-        walk.refused = refused;
-        count = cnt;
-        accept[n] = cnt;
+        if (rank == 0) {
+            for (int m = cnt + lane; m < M; m += 32) path[n * M + m] = -1;
+            if (lane == 0) accept[n] = cnt;
+        }
+        if (lane == 0) {
+            walk_cur = cur;
+            walk_gone = ng;
+            walk_any = any;
+            walk_draw = tick24(u_draw);
+        }
     }
     __syncthreads();
-    if (tid < M) path[n * M + tid] = tid < count ? step[tid] : -1;
-    const int cur = walk.cur, refused = walk.refused;
-    if (cur < 0) {
-        if (tid == 0) next_token[n] = -1;
+    const int cur = walk_cur, refused = walk_gone;
+    if (cur < 0) {                                     // the whole cluster
+        if (rank == 0 && tid == 0) next_token[n] = -1;
         return;
     }
     const Tin *row = target + (n * M + cur) * V;
-    const Tin *qrow = draft != nullptr && refused > 0 ? draft + (n * M + cur) * V : nullptr;
+    const Tin *qrow = draft != nullptr && walk_any ? draft + (n * M + cur) * V : nullptr;
     bool skip = draft == nullptr && refused > 0;       // leave the refused tokens out
     // vectors from the 16-byte boundary at or below the row's start: element
     // i of the row is element i + lead of that grid
     const int lead = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(Tin));
     const int vecs = (V + lead + VEC - 1) / VEC;
-    const int per_warp = (vecs + WARPS - 1) / WARPS;
-    // weights of vector i of the grid (zero outside the row)
-    auto weights = [&](int i, unsigned long long (&w)[VEC]) {
+    const int per_warp = (vecs + ranks * kVerifyWarps - 1) / (ranks * kVerifyWarps);
+    const int first = min(vecs, (rank * kVerifyWarps + warp) * per_warp), end = min(vecs, first + per_warp);
+    // the raw values of vector i of the grid (zero outside the row)
+    auto fetch = [&](const Tin *r, int i, float (&x)[VEC]) {
         const int e0 = i * VEC - lead;
-        float x[VEC];
         if (e0 >= 0 && e0 + VEC <= V) {
-            Row<Tin>::load(row + e0, x);
-            if (qrow != nullptr) {
-                float y[VEC];
-                Row<Tin>::load(qrow + e0, y);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) x[e] = x[e] - y[e];
-            }
+            Row<Tin>::load(r + e0, x);
         } else {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const int at = e0 + e;
-                x[e] = at >= 0 && at < V ? Elem<Tin>::load(row + at) : 0.f;
-                if (qrow != nullptr && at >= 0 && at < V) x[e] = x[e] - Elem<Tin>::load(qrow + at);
+            for (int e = 0; e < VEC; ++e) x[e] = e0 + e >= 0 && e0 + e < V ? Elem<Tin>::load(r + e0 + e) : 0.f;
+        }
+    };
+    // What is drawn from, at BATCH vectors of a lane, 32 apart.  Only the batches at the
+    // row's and the share's ends look at each vector: a branch per vector kept the
+    // loads from being on their way together.
+    auto weights = [&](int i0, float (&x)[BATCH][VEC]) {
+        if (i0 * VEC >= lead && i0 + 32 * BATCH <= end && (i0 + 32 * BATCH) * VEC - lead <= V) {
+            const int e0 = (i0 + lane) * VEC - lead;
+#pragma unroll
+            for (int y = 0; y < BATCH; ++y) Row<Tin>::load(row + e0 + 32 * VEC * y, x[y]);
+            if (qrow != nullptr) {
+                float z[BATCH][VEC];
+#pragma unroll
+                for (int y = 0; y < BATCH; ++y) Row<Tin>::load(qrow + e0 + 32 * VEC * y, z[y]);
+#pragma unroll
+                for (int y = 0; y < BATCH; ++y)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) x[y][e] = x[y][e] - z[y][e];
             }
+            return;
         }
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) w[e] = fixed38(x[e]);
-    };
-    for (int attempt = 0;; ++attempt) {
-        unsigned long long sum = 0;
-        const int end = min(vecs, (warp + 1) * per_warp);
-        for (int i = warp * per_warp + lane; i < end; i += 32) {
-            unsigned long long w[VEC];
-            weights(i, w);
+        for (int y = 0; y < BATCH; ++y) {
+            const int i = i0 + 32 * y + lane;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) sum += w[e];
+            for (int e = 0; e < VEC; ++e) x[y][e] = 0.f;
+            if (i < end) {
+                fetch(row, i, x[y]);
+                if (qrow != nullptr) {
+                    float z[VEC];
+                    fetch(qrow, i, z);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) x[y][e] = x[y][e] - z[e];
+                }
+            }
+        }
+    };
+    u64 all = 0, before = 0;                           // the row's mass, and that of the CTAs before this one
+    for (int attempt = 0;; ++attempt) {
+        u64 sum = 0;
+        for (int i0 = first; i0 < end; i0 += 32 * BATCH) {
+            float x[BATCH][VEC];
+            uint32_t hi = 0, lo = 0;
+            weights(i0, x);
+#pragma unroll
+            for (int y = 0; y < BATCH; ++y)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    uint32_t h, l;
+                    digits38(x[y][e], h, l);
+                    hi += h - kBias;
+                    lo += l - kBias;
+                }
+            sum += ((u64)hi << 19) + lo;               // 16 digits of 19 bits fit 32 bits
+        }
+        if (skip) {
+            // the refused tokens come out of the sums that hold them
+            for (int i = lane; i < refused; i += 32) {
+                const int at = (gone[i] + lead) / VEC;
+                if (at >= first && at < end) sum -= fixed38(Elem<Tin>::load(row + gone[i]));
+            }
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0) part[warp] = sum;
         __syncthreads();
-        if (tid == 0) {
-            // the refused tokens (each once) come out of the sums that hold them
-            if (skip)
-                for (int i = 0; i < refused; ++i) {
-                    bool again = gone[i] < 0 || gone[i] >= V;
-                    for (int j = 0; j < i; ++j) again |= gone[j] == gone[i];
-                    if (!again)
-                        part[(gone[i] + lead) / VEC / per_warp] -= fixed38(Elem<Tin>::load(row + gone[i]));
-                }
-            unsigned long long all = 0;
-            for (int w = 0; w < WARPS; ++w) all += part[w];
-            whole = all;
+        if (warp == 0) {
+            u64 mine = lane < kVerifyWarps ? part[lane] : 0;
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+            if (lane < ranks) *cluster.map_shared_rank(&totals[attempt][rank], lane) = mine;
         }
-        __syncthreads();
-        if (whole != 0 || attempt > 0 || (qrow == nullptr && !skip)) break;
+        cluster.sync();
+        all = before = 0;
+        for (int r = 0; r < ranks; ++r) {
+            const u64 x = totals[attempt][r];
+            before += r < rank ? x : 0;
+            all += x;
+        }
+        if (all != 0 || attempt > 0 || (qrow == nullptr && !skip)) break;
         // nothing is left beside what was refused: draw from the row itself
         qrow = nullptr;
         skip = false;
-        __syncthreads();
     }
-    const unsigned long long all = whole;
     if (all == 0) {
-        if (tid == 0) next_token[n] = -1;
+        if (rank == 0 && tid == 0) next_token[n] = -1;
         return;
     }
     // the first token whose running sum exceeds floor(u all / 2^24): the sum
     // of all exceeds it, since u < 2^24
-    const unsigned long long need =
-        __umul64hi((unsigned long long)tick24(uniforms[n * (M + 1) + M]) << 40, all);
-    unsigned long long before = 0;
-    int mine = 0;
-    for (; mine < WARPS - 1; ++mine) {
-        if (before + part[mine] > need) break;
-        before += part[mine];
-    }
-    if (warp != mine) return;
-    const int end = min(vecs, (warp + 1) * per_warp);
-    for (int i0 = warp * per_warp; i0 < end; i0 += 32) {
-        unsigned long long w[VEC], sum = 0;
-        const int i = i0 + lane;
-        if (i < end) {
-            weights(i, w);
+    const u64 need = __umul64hi((u64)walk_draw << 40, all);
+    for (int w = 0; w < warp; ++w) before += part[w];
+    if (before > need || before + part[warp] <= need) return;
+    for (int i0 = first; i0 < end; i0 += 32 * BATCH) {
+        float x[BATCH][VEC];
+        weights(i0, x);
+#pragma unroll
+        for (int y = 0; y < BATCH; ++y) {
+            const int e0 = (i0 + 32 * y + lane) * VEC - lead;
+            u64 w[VEC], sum = 0;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) w[e] = fixed38(x[y][e]);
             if (skip) {
-                const int e0 = i * VEC - lead;
                 for (int r = 0; r < refused; ++r)
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e)
-                        if (gone[r] == e0 + e) w[e] = 0;
+                    for (int e = 0; e < VEC; ++e) w[e] = gone[r] == e0 + e ? 0 : w[e];
             }
-        } else {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) w[e] = 0;
-        }
+            for (int e = 0; e < VEC; ++e) sum += w[e];
+            u64 run = sum;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) sum += w[e];
-        unsigned long long run = sum;
+            for (int o = 1; o < 32; o <<= 1) {
+                const u64 z = __shfl_up_sync(0xffffffffu, run, o);
+                if (lane >= o) run += z;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, before + run > need);
+            if (hit != 0) {
+                if (lane == __ffs(hit) - 1) {
+                    u64 at = before + run - sum;
+                    int e = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned long long x = __shfl_up_sync(0xffffffffu, run, o);
-            if (lane >= o) run += x;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, before + run > need);
-        if (hit != 0) {
-            if (lane == __ffs(hit) - 1) {
-                unsigned long long at = before + run - sum;
-                int e = 0;
-#pragma unroll
-                for (int x = 0; x < VEC; ++x) {
-                    at += w[x];
-                    if (at <= need) e = x + 1;
+                    for (int z = 0; z < VEC; ++z) {
+                        at += w[z];
+                        if (at <= need) e = z + 1;
+                    }
+                    next_token[n] = e0 + e;
                 }
-                next_token[n] = i * VEC - lead + e;
+                return;
             }
-            return;
+            before += __shfl_sync(0xffffffffu, run, 31);
         }
-        before += __shfl_sync(0xffffffffu, run, 31);
     }
+}
+
+template <typename Tin>
+cudaError_t run_verify(const void *target, const void *draft, const int32_t *tokens, const int32_t *parent,
+                       const float *uniforms, int32_t N, int32_t M, int32_t V, int32_t *accept, int32_t *path,
+                       int32_t *next_token, cudaStream_t stream) {
+    // CTAs per sequence: up to eight, while all sequences' CTAs make no more than two
+    // rounds of the GPU (256 chains: 62 us with two, 52 with four, 53 with eight) and
+    // each still has 4 KB.
+    int ranks = kMaxCluster;
+    while (ranks > 1 && ((int64_t)ranks * N > 1100 || (int64_t)V * (int64_t)sizeof(Tin) < (int64_t)ranks * 4096)) ranks /= 2;
+    cudaLaunchAttribute cluster;
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = ranks;
+    cluster.val.clusterDim.y = 1;
+    cluster.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)N * ranks);
+    cfg.blockDim = dim3(kVerifyThreads);
+    cfg.stream = stream;
+    cfg.attrs = &cluster;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_kernel<Tin>, static_cast<const Tin *>(target),
+                                             static_cast<const Tin *>(draft), tokens, parent, uniforms, M, V, accept,
+                                             path, next_token);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
 }
 
 // A thread moves 16 bytes: token t of the accepted ones, head h, piece x.
@@ -286,15 +392,9 @@ cudaError_t launch_verify_drafts(const void *target, const void *draft, const in
                                  int32_t V, kda_dtype dt, int32_t *accept, int32_t *path,
                                  int32_t *next_token, cudaStream_t stream) {
     if (dt == KDA_BF16)
-        verify_kernel<__nv_bfloat16><<<N, kVerifyThreads, 0, stream>>>(
-            static_cast<const __nv_bfloat16 *>(target), static_cast<const __nv_bfloat16 *>(draft), tokens,
-            parent, uniforms, M, V, accept, path, next_token);
-    else
-        verify_kernel<float><<<N, kVerifyThreads, 0, stream>>>(
-            static_cast<const float *>(target), static_cast<const float *>(draft), tokens, parent,
-            uniforms, M, V, accept, path, next_token);
-    count_launches(1);
-    return cudaGetLastError();
+        return run_verify<__nv_bfloat16>(target, draft, tokens, parent, uniforms, N, M, V, accept, path, next_token,
+                                         stream);
+    return run_verify<float>(target, draft, tokens, parent, uniforms, N, M, V, accept, path, next_token, stream);
 }
 
 cudaError_t launch_cache_append(const void *k_new, const void *v_new, const int32_t *path,

@@ -156,6 +156,10 @@ decode_tree_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const T
 // 8i + r, so that a column's read S^T k closes with three shuffles and the
 // warps never wait for one another.  The state moves once in each direction.
 // A CTA has up to four such warps, so d = 128 takes two CTAs per state.
+// Measured: 256 x 96 states of 128 x 128, bf16 inputs: 459 us for one token (7.1
+// TB/s), 579 us for 3.5 on average (5.7 TB/s); above one token it is bound by
+// what four CTAs' registers (127 a thread) leave of latency to hide: five spill
+// (700 us).  Pairs of fp32 in one instruction took 17 us off.
 template <int D> struct CommitCfg {
     static constexpr int WARPS = D < 64 ? D / 16 : 4, SPLIT = D / 16 / WARPS;
 };
@@ -165,83 +169,109 @@ decode_commit_kernel(const Tin *__restrict__ k, const Tin *__restrict__ v, const
                      const float *__restrict__ beta, const float *state_in,
                      const int32_t *__restrict__ path, const int32_t *__restrict__ accept, int32_t M,
                      int32_t P, int32_t H, float *state_out) {
-    constexpr int SPLIT = CommitCfg<D>::SPLIT, THREADS = 32 * CommitCfg<D>::WARPS;
+    constexpr int SPLIT = CommitCfg<D>::SPLIT;
+    static_assert(32 * CommitCfg<D>::WARPS >= D, "a thread per channel");
     constexpr int BATCH = 4;                         // path nodes staged at a time
     constexpr int ROWS = D / 8;                      // state rows per lane
+    constexpr int COLS = 16 * CommitCfg<D>::WARPS;   // state columns of the CTA
     __shared__ __align__(16) float2 ak[BATCH][D];    // (decay, k) per channel
-    __shared__ int32_t node[BATCH];
+    __shared__ __align__(16) float vs[BATCH][COLS];
+    __shared__ float bs[BATCH];
     const int tid = threadIdx.x, lane = tid & 31, r = lane >> 2;
-    const int col = (blockIdx.x % SPLIT) * (16 * CommitCfg<D>::WARPS) + (tid >> 5) * 16 + (lane & 3) * 4;
+    const int col0 = (blockIdx.x % SPLIT) * COLS, lcol = (tid >> 5) * 16 + (lane & 3) * 4;
     const int unit = blockIdx.x / SPLIT;
     const int64_t n = unit / H;
     const int h = unit % H;
-    const size_t base = (size_t)unit * D * D + (size_t)r * D + col;
-    float4 s[ROWS];
+    const size_t base = (size_t)unit * D * D + (size_t)r * D + col0 + lcol;
+    float2 s[ROWS][2];
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i)
-        s[i] = __ldcs(reinterpret_cast<const float4 *>(state_in + base + (size_t)i * 8 * D));
+    for (int i = 0; i < ROWS; ++i) {
+        const float4 x = __ldcs(reinterpret_cast<const float4 *>(state_in + base + (size_t)i * 8 * D));
+        s[i][0] = make_float2(x.x, x.y);
+        s[i][1] = make_float2(x.z, x.w);
+    }
     int acc = accept[n];
     acc = acc < 0 ? 0 : (acc > P ? P : acc);
     for (int t0 = 0; t0 < acc; t0 += BATCH) {
         // the batch ends at its first entry outside the tree, and the path with it
-        int cnt = 0;
-        __syncthreads();
-        for (; cnt < BATCH && t0 + cnt < acc; ++cnt) {
-            const int m = path[n * P + t0 + cnt];
-            if (m < 0 || m >= M) {
+        int node[BATCH], cnt = acc - t0 < BATCH ? acc - t0 : BATCH;
+#pragma unroll
+        for (int t = 0; t < BATCH; ++t) node[t] = t0 + t < P ? path[n * P + t0 + t] : -1;
+#pragma unroll
+        for (int t = BATCH - 1; t >= 0; --t)
+            if (t < cnt && (node[t] < 0 || node[t] >= M)) {
+                cnt = t;
                 acc = 0;
-                break;
             }
-            if (tid == 0) node[cnt] = m;
-            const int64_t at = ((n * M + m) * H + h) * D;
-            for (int i = tid; i < D; i += THREADS)
-                ak[cnt][i] = make_float2(__expf(g[at + i]), Elem<Tin>::load(k + at + i));
+        // All of the batch's loads go before the first is used: no branch between them
+        // (the rows past cnt are the first one again), since a branch per token waited
+        // for its loads, 1 us per token.
+        const int some = cnt > 0 ? node[0] : 0;
+        float gt[BATCH], bt8[BATCH];
+        Tin kt[BATCH], vt8[BATCH];
+#pragma unroll
+        for (int t = 0; t < BATCH; ++t) {
+            const int64_t row = (n * M + (t < cnt ? node[t] : some)) * H + h, at = row * D;
+            gt[t] = __ldg(g + at + tid % D);
+            kt[t] = k[at + tid % D];
+            vt8[t] = v[at + col0 + tid % COLS];
+            bt8[t] = __ldg(beta + row);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < BATCH; ++t) {
+            if (tid < D) ak[t][tid] = make_float2(__expf(gt[t]), Elem<Tin>::load(&kt[t]));
+            if (tid < COLS) vs[t][tid] = Elem<Tin>::load(&vt8[t]);
+            if (tid == 0) bs[t] = bt8[t];
         }
         __syncthreads();
 #pragma unroll 1
         for (int t = 0; t < cnt; ++t) {
-            const int64_t row = (n * M + node[t]) * H + h;
-            const float bt = beta[row];
-            float vt[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) vt[e] = Elem<Tin>::load(v + row * D + col + e);
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float bt = bs[t];
+            const float4 vt = *reinterpret_cast<const float4 *>(&vs[t][lcol]);
+            float2 x[2];
+            x[0] = x[1] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < ROWS; ++i) {
                 const float2 f = ak[t][i * 8 + r];
-                s[i].x *= f.x; s[i].y *= f.x; s[i].z *= f.x; s[i].w *= f.x;
-                x.x += f.y * s[i].x; x.y += f.y * s[i].y; x.z += f.y * s[i].z; x.w += f.y * s[i].w;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    s[i][y] = tc::f2mul(s[i][y], make_float2(f.x, f.x));
+                    x[y] = tc::f2fma(s[i][y], make_float2(f.y, f.y), x[y]);
+                }
             }
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
-                x.x += __shfl_xor_sync(0xffffffffu, x.x, o);
-                x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
-                x.z += __shfl_xor_sync(0xffffffffu, x.z, o);
-                x.w += __shfl_xor_sync(0xffffffffu, x.w, o);
+                x[0].x += __shfl_xor_sync(0xffffffffu, x[0].x, o);
+                x[0].y += __shfl_xor_sync(0xffffffffu, x[0].y, o);
+                x[1].x += __shfl_xor_sync(0xffffffffu, x[1].x, o);
+                x[1].y += __shfl_xor_sync(0xffffffffu, x[1].y, o);
             }
-            const float4 u = make_float4(bt * (vt[0] - x.x), bt * (vt[1] - x.y), bt * (vt[2] - x.z),
-                                         bt * (vt[3] - x.w));
+            const float2 u[2] = {make_float2(bt * (vt.x - x[0].x), bt * (vt.y - x[0].y)),
+                                 make_float2(bt * (vt.z - x[1].x), bt * (vt.w - x[1].y))};
 #pragma unroll
             for (int i = 0; i < ROWS; ++i) {
                 const float ki = ak[t][i * 8 + r].y;
-                s[i].x += ki * u.x; s[i].y += ki * u.y; s[i].z += ki * u.z; s[i].w += ki * u.w;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) s[i][y] = tc::f2fma(u[y], make_float2(ki, ki), s[i][y]);
             }
         }
     }
 #pragma unroll
     for (int i = 0; i < ROWS; ++i)
-        __stcs(reinterpret_cast<float4 *>(state_out + base + (size_t)i * 8 * D), s[i]);
+        __stcs(reinterpret_cast<float4 *>(state_out + base + (size_t)i * 8 * D),
+               make_float4(s[i][0].x, s[i][0].y, s[i][1].x, s[i][1].y));
 }
 
 // ---- bf16 inputs, d = 128: the products with S_0 on the tensor cores ----
 //
-// One CTA of four warps per (sequence, head).  Nodes 8i .. 8i+7 make row tile
+// One CTA of four (or eight) warps per (sequence, head).  Nodes 8i .. 8i+7 make row tile
 // i: rows 0-7 are E_m k_m, rows 8-15 E_m q_m, so a tile is full whether the
 // tree has 8 nodes or 64.  Warp w multiplies all tiles with state columns
 // 32w .. 32w+31 (mma.sync m16n8k16): a lane loads 16 bytes of four state rows
-// and takes its four columns as column g of four 8-wide tiles, so the fp32
-// state goes from HBM to the fragments without passing shared memory, in whole
-// 128-byte lines.
+// and takes its four columns as column g of four 8-wide tiles (half of all that
+// with eight warps), so the fp32 state goes from HBM to the fragments without
+// passing shared memory, in whole 128-byte lines.
 //
 // The solve does not touch the 128 columns: with y = v - (the k sums) the
 // outputs are (the q sums) + W y, where row m of W lives on m's line.  Let s
@@ -256,10 +286,15 @@ decode_commit_kernel(const Tin *__restrict__ k, const Tin *__restrict__ v, const
 // All operands are split into a bf16 part and a bf16 rest (16 significant bits
 // together), and three of the four partial products are summed in fp32: the
 // fourth is below 2^-16 of the product.
-constexpr int kTcThreads = 128;
 constexpr int kALd = 136;                             // bf16 per operand row: 17 x 16 bytes, no bank conflicts
 
 template <int TILES> struct TcCfg {
+    // four warps of 32 state columns; eight of 16 above 16 nodes and 16 of eight above 32,
+    // where shared memory leaves room for two CTAs and one (with four warps throughout,
+    // 128 x 32 nodes took 535 us instead of 457, 64 x 64 nodes 986 instead of the figure below)
+    static constexpr int WARPS = TILES <= 2 ? 4 : 2 * TILES, THREADS = 32 * WARPS;
+    static constexpr int NT = 16 / WARPS;             // 8-wide column tiles per warp = columns per lane
+    static constexpr int CTAS = TILES <= 2 ? 4 : TILES == 4 ? 2 : 1;
     static constexpr int PAIRS = (TILES + 1) / 2;     // 16-node blocks of W
     static constexpr int WLD = PAIRS * 16 + 8;        // bf16 per row of W: an odd number of 16-byte pieces
     static constexpr size_t A_BYTES = (size_t)TILES * 16 * kALd * 2 * 2;
@@ -300,14 +335,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 __device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
 template <int TILES>
-__global__ void __launch_bounds__(kTcThreads, TILES <= 2 ? 4 : TILES == 4 ? 3 : 1)
+__global__ void __launch_bounds__(TcCfg<TILES>::THREADS, TcCfg<TILES>::CTAS)
 decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ k,
                       const __nv_bfloat16 *__restrict__ v, const float *__restrict__ g,
                       const float *__restrict__ beta, const float *__restrict__ state,
                       const int32_t *__restrict__ parent, int32_t M, int32_t H,
                       __nv_bfloat16 *__restrict__ out) {
     using C = TcCfg<TILES>;
-    constexpr int D = 128, KS = D / 16, WARPS = kTcThreads / 32;
+    constexpr int D = 128, KS = D / 16, WARPS = C::WARPS, THREADS = C::THREADS, NT = C::NT;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     __nv_bfloat16 *ahi = reinterpret_cast<__nv_bfloat16 *>(smem_raw), *alo = ahi + TILES * 16 * kALd;
     __nv_bfloat16 *whi = reinterpret_cast<__nv_bfloat16 *>(smem_raw + C::A_BYTES),
@@ -329,23 +364,10 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
     // the state comes to the L2 while the line products run
     if (tid == 0)
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(S), "r"(D * D * 4) : "memory");
-    for (int m = tid; m < M; m += kTcThreads) {
-        par[m] = parent[n * M + m];
-        bet[m] = beta[row0 + (int64_t)m * H];
-    }
-    for (int i = tid; i < M * (D / 8); i += kTcThreads) {
-        const int m = i / (D / 8), c = i % (D / 8) * 8;
-        const int64_t at = (row0 + (int64_t)m * H) * D + c;
-        float x[8], y[8];
-        Elem<float>::load8(g + at, x);
-        Elem<__nv_bfloat16>::load8(k + at, y);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = __expf(x[e]);
-        Elem<float>::store8(al + m * D + c, x);
-        Elem<float>::store8(kk + m * D + c, y);
-    }
-    for (int i = tid; i < (int)(C::W_BYTES / 16); i += kTcThreads)
-        reinterpret_cast<uint4 *>(whi)[i] = make_uint4(0u, 0u, 0u, 0u);
+    // every load of the inputs is on its way before the first is used
+    static_assert(THREADS >= kMaxTreeNodes, "a thread per node");
+    const int32_t par_in = tid < M ? parent[n * M + tid] : 0;
+    const float bet_in = tid < M ? __ldg(beta + row0 + (int64_t)tid * H) : 0.f;
     // line products: eight lanes per node, channels 32 p + 4 (lane % 8) .. + 3
     const int l8 = lane & 7;
     const unsigned group = 0xffu << (lane & 24);
@@ -358,6 +380,34 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
                           : make_uint2(0u, 0u);
     };
     load_q();
+    constexpr int PIECES = 2;                         // of eight channels, per thread and pass
+    for (int i0 = tid; i0 < M * (D / 8); i0 += PIECES * THREADS) {
+        float x[PIECES][8];
+        uint4 y[PIECES];
+#pragma unroll
+        for (int z = 0; z < PIECES; ++z) {
+            const int i = min(i0 + z * THREADS, M * (D / 8) - 1);
+            const int64_t at = (row0 + (int64_t)(i / (D / 8)) * H) * D + i % (D / 8) * 8;
+            Elem<float>::load8(g + at, x[z]);
+            y[z] = __ldg(reinterpret_cast<const uint4 *>(k + at));
+        }
+#pragma unroll
+        for (int z = 0; z < PIECES; ++z) {
+            const int i = min(i0 + z * THREADS, M * (D / 8) - 1);   // (the last piece may be written twice)
+            const float kf[8] = {lo_f(y[z].x), hi_f(y[z].x), lo_f(y[z].y), hi_f(y[z].y),
+                                 lo_f(y[z].z), hi_f(y[z].z), lo_f(y[z].w), hi_f(y[z].w)};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[z][e] = __expf(x[z][e]);
+            Elem<float>::store8(al + 8 * i, x[z]);
+            Elem<float>::store8(kk + 8 * i, kf);
+        }
+    }
+    if (tid < M) {
+        par[tid] = par_in;
+        bet[tid] = bet_in;
+    }
+    for (int i = tid; i < (int)(C::W_BYTES / 16); i += THREADS)
+        reinterpret_cast<uint4 *>(whi)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
     for (; m < TILES * 8; m += 4 * WARPS) {
         float2 kd[8], qd[8];
@@ -441,25 +491,46 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
     }
     // the first state rows and the values set out before the operands are ready
     const int gq = lane & 3, gg = lane >> 2;
-    const float *Sw = S + (size_t)(2 * gq) * D + warp * 32 + gg * 4;
-    auto fetch = [&](int ks, float4 (&f)[4]) {
+    const float *Sw = S + (size_t)(2 * gq) * D + warp * 8 * NT + gg * NT;
+    auto fetch = [&](int ks, float (&f)[4][NT]) {
         const float *p = Sw + (size_t)ks * 16 * D;
-        f[0] = __ldcs(reinterpret_cast<const float4 *>(p));
-        f[1] = __ldcs(reinterpret_cast<const float4 *>(p + D));
-        f[2] = __ldcs(reinterpret_cast<const float4 *>(p + 8 * D));
-        f[3] = __ldcs(reinterpret_cast<const float4 *>(p + 9 * D));
+        const int rows[4] = {0, 1, 8, 9};
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            if constexpr (NT == 4) {
+                const float4 x = __ldcs(reinterpret_cast<const float4 *>(p + rows[y] * D));
+                f[y][0] = x.x; f[y][1] = x.y; f[y][2] = x.z; f[y][3] = x.w;
+            } else if constexpr (NT == 2) {
+                const float2 x = __ldcs(reinterpret_cast<const float2 *>(p + rows[y] * D));
+                f[y][0] = x.x; f[y][1] = x.y;
+            } else {
+                f[y][0] = __ldcs(p + rows[y] * D);
+            }
+        }
     };
-    constexpr int AHEAD = TILES <= 4 ? 2 : 1;         // steps of 16 state rows on their way
-    float4 buf[AHEAD + 1][4];
-    const int64_t vcol = warp * 32 + 8 * gq;          // values of node 8i + gg, state columns vcol .. + 7
-    uint4 vv[TILES];
+    constexpr int AHEAD = 3;                          // steps of 16 state rows on their way
+    float buf[AHEAD + 1][4][NT];
+    const int64_t vcol = warp * 8 * NT + 2 * NT * gq; // values of node 8i + gg, 2 NT state columns from vcol
+    uint32_t vv[TILES][NT];
 #pragma unroll
     for (int ks = 0; ks < AHEAD; ++ks) fetch(ks, buf[ks]);
 #pragma unroll
     for (int i = 0; i < TILES; ++i) {
         const int mm = 8 * i + gg;
-        vv[i] = mm < M ? __ldg(reinterpret_cast<const uint4 *>(v + (row0 + (int64_t)mm * H) * D + vcol))
-                       : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int x = 0; x < NT; ++x) vv[i][x] = 0u;
+        if (mm < M) {
+            const __nv_bfloat16 *from = v + (row0 + (int64_t)mm * H) * D + vcol;
+            if constexpr (NT == 4) {
+                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(from));
+                vv[i][0] = x.x; vv[i][1] = x.y; vv[i][2] = x.z; vv[i][3] = x.w;
+            } else if constexpr (NT == 2) {
+                const uint2 x = __ldg(reinterpret_cast<const uint2 *>(from));
+                vv[i][0] = x.x; vv[i][1] = x.y;
+            } else {
+                vv[i][0] = __ldg(reinterpret_cast<const uint32_t *>(from));
+            }
+        }
     }
     __syncthreads();
 
@@ -489,11 +560,11 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
         }
     }
 
-    float acc[TILES][4][4];
+    float acc[TILES][NT][4];
 #pragma unroll
     for (int i = 0; i < TILES; ++i)
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[i][t][e] = 0.f;
     const uint32_t frag = (uint32_t)(lane & 15), piece = (uint32_t)(lane >> 4) * 16;
@@ -502,22 +573,20 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
         if (ks + AHEAD < KS) fetch(ks + AHEAD, buf[(ks + AHEAD) % (AHEAD + 1)]);
-        const float4 *f = buf[ks % (AHEAD + 1)];
-        uint32_t bh[4][2], bl[4][2];
+        const float(&f)[4][NT] = buf[ks % (AHEAD + 1)];
+        uint32_t bh[NT][2], bl[NT][2];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            split2(f[2 * half].x, f[2 * half + 1].x, bh[0][half], bl[0][half]);
-            split2(f[2 * half].y, f[2 * half + 1].y, bh[1][half], bl[1][half]);
-            split2(f[2 * half].z, f[2 * half + 1].z, bh[2][half], bl[2][half]);
-            split2(f[2 * half].w, f[2 * half + 1].w, bh[3][half], bl[3][half]);
-        }
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                split2(f[2 * half][t], f[2 * half + 1][t], bh[t][half], bl[t][half]);
 #pragma unroll
         for (int i = 0; i < TILES; ++i) {
             uint32_t xh[4], xl[4];
             ldsm4(abase + (i * 16 * kALd + ks * 16) * 2, xh);
             ldsm4(abase + (i * 16 * kALd + ks * 16) * 2 + kALo, xl);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
+            for (int t = 0; t < NT; ++t) {
                 float(&d)[4] = acc[i][t];
                 mma16816(d[0], d[1], d[2], d[3], xh, bh[t][0], bh[t][1]);
                 mma16816(d[0], d[1], d[2], d[3], xh, bl[t][0], bl[t][1]);
@@ -526,15 +595,15 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
         }
     }
     // lane (gg, gq): node 8i + gg's k sums (entries 0, 1; they become y) and q sums
-    // (2, 3) of the tile columns 2 gq and 2 gq + 1, i.e. columns vcol + t and vcol + 4 + t
+    // (2, 3) of the tile columns 2 gq and 2 gq + 1, i.e. columns vcol + t and vcol + NT + t
     float clean = 0.f;                                // NaN once any y is not finite
 #pragma unroll
     for (int i = 0; i < TILES; ++i) {
-        const uint32_t u[4] = {vv[i].x, vv[i].y, vv[i].z, vv[i].w};
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            acc[i][t][0] = ((t & 1) ? hi_f(u[t >> 1]) : lo_f(u[t >> 1])) - acc[i][t][0];
-            acc[i][t][1] = ((t & 1) ? hi_f(u[2 + (t >> 1)]) : lo_f(u[2 + (t >> 1)])) - acc[i][t][1];
+        for (int t = 0; t < NT; ++t) {
+            const uint32_t u0 = vv[i][t >> 1], u1 = vv[i][(NT + t) >> 1];
+            acc[i][t][0] = ((t & 1) ? hi_f(u0) : lo_f(u0)) - acc[i][t][0];
+            acc[i][t][1] = (((NT + t) & 1) ? hi_f(u1) : lo_f(u1)) - acc[i][t][1];
             clean += 0.f * acc[i][t][0];
             clean += 0.f * acc[i][t][1];
         }
@@ -543,26 +612,26 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
     __syncthreads();                                  // W is there
     // A y that is not finite belongs to its own line only: the dense product
     // takes a zero in its place, and it is added where it is seen
-    float seen[TILES][4][2];
+    float seen[TILES][NT][2];
     if (dirty) {
 #pragma unroll
         for (int i = 0; i < TILES; ++i)
 #pragma unroll
-            for (int x = 0; x < 8; ++x) seen[i][x >> 1][x & 1] = 0.f;
+            for (int x = 0; x < 2 * NT; ++x) seen[i][x >> 1][x & 1] = 0.f;
 #pragma unroll
         for (int i = 0; i < TILES; ++i) {
 #pragma unroll 1
             for (int r = 0; r < 8 && 8 * i + r < M; ++r) {
-                float y[4][2];
+                float y[NT][2];
 #pragma unroll
-                for (int x = 0; x < 8; ++x)
+                for (int x = 0; x < 2 * NT; ++x)
                     y[x >> 1][x & 1] = __shfl_sync(0xffffffffu, acc[i][x >> 1][x & 1], r * 4 + gq);
 #pragma unroll
                 for (int o = 0; o < TILES; ++o) {
                     const int m = 8 * o + gg;
                     if (m >= M || (line[m] >> (8 * i + r) & 1) == 0) continue;
 #pragma unroll
-                    for (int x = 0; x < 8; ++x)
+                    for (int x = 0; x < 2 * NT; ++x)
                         if (!is_finite(y[x >> 1][x & 1])) seen[o][x >> 1][x & 1] += y[x >> 1][x & 1];
                 }
             }
@@ -570,16 +639,16 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
 #pragma unroll
         for (int i = 0; i < TILES; ++i)
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
+            for (int t = 0; t < NT; ++t) {
                 if (!is_finite(acc[i][t][0])) acc[i][t][0] = 0.f;
                 if (!is_finite(acc[i][t][1])) acc[i][t][1] = 0.f;
             }
     }
-    uint32_t yh[2 * C::PAIRS][4], yl[2 * C::PAIRS][4];
+    uint32_t yh[2 * C::PAIRS][NT], yl[2 * C::PAIRS][NT];
 #pragma unroll
     for (int i = 0; i < 2 * C::PAIRS; ++i)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < NT; ++t) {
             yh[i][t] = yl[i][t] = 0u;
             if (i < TILES) {
                 uint32_t hi, lo;
@@ -592,16 +661,16 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
     constexpr uint32_t kWLo = C::PAIRS * 16 * C::WLD * 2;
 #pragma unroll
     for (int i = 0; i < C::PAIRS; ++i) {
-        float none[4][2];                             // the upper half of a lone tile
+        float none[NT][2];                             // the upper half of a lone tile
 #pragma unroll
-        for (int t = 0; t < 4; ++t) none[t][0] = none[t][1] = 0.f;
+        for (int t = 0; t < NT; ++t) none[t][0] = none[t][1] = 0.f;
 #pragma unroll
         for (int b = 0; b <= i; ++b) {                // nodes above have lower indices
             uint32_t xh[4], xl[4];
             ldsm4(wbase + (i * 16 * C::WLD + b * 16) * 2, xh);
             ldsm4(wbase + (i * 16 * C::WLD + b * 16) * 2 + kWLo, xl);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
+            for (int t = 0; t < NT; ++t) {
                 float &d0 = acc[2 * i][t][2], &d1 = acc[2 * i][t][3];
                 float &d2 = 2 * i + 1 < TILES ? acc[(2 * i + 1) % TILES][t][2] : none[t][0];
                 float &d3 = 2 * i + 1 < TILES ? acc[(2 * i + 1) % TILES][t][3] : none[t][1];
@@ -617,14 +686,19 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
         if (m >= M) continue;
         if (dirty) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
+            for (int t = 0; t < NT; ++t) {
                 acc[i][t][2] += seen[i][t][0];
                 acc[i][t][3] += seen[i][t][1];
             }
         }
-        *reinterpret_cast<uint4 *>(out + (row0 + (int64_t)m * H) * D + vcol) =
-            make_uint4(pack2(acc[i][0][2], acc[i][1][2]), pack2(acc[i][2][2], acc[i][3][2]),
-                       pack2(acc[i][0][3], acc[i][1][3]), pack2(acc[i][2][3], acc[i][3][3]));
+        __nv_bfloat16 *to = out + (row0 + (int64_t)m * H) * D + vcol;
+        if constexpr (NT == 4)
+            *reinterpret_cast<uint4 *>(to) = make_uint4(pack2(acc[i][0][2], acc[i][1][2]), pack2(acc[i][2][2], acc[i][3][2]),
+                                                        pack2(acc[i][0][3], acc[i][1][3]), pack2(acc[i][2][3], acc[i][3][3]));
+        else if constexpr (NT == 1)
+            *reinterpret_cast<uint32_t *>(to) = pack2(acc[i][0][2], acc[i][0][3]);
+        else
+            *reinterpret_cast<uint2 *>(to) = make_uint2(pack2(acc[i][0][2], acc[i][1][2]), pack2(acc[i][0][3], acc[i][1][3]));
     }
 }
 
@@ -649,7 +723,7 @@ cudaError_t run_tree_tc(const void *q, const void *k, const void *v, const float
     static std::atomic<uint64_t> smem_set{0};
     cudaError_t e = allow_dynamic_smem(decode_tree_tc_kernel<TILES>, TcCfg<TILES>::smem(8 * TILES), smem_set);
     if (e != cudaSuccess) return e;
-    decode_tree_tc_kernel<TILES><<<(unsigned)N * (unsigned)H, kTcThreads, TcCfg<TILES>::smem(M), stream>>>(
+    decode_tree_tc_kernel<TILES><<<(unsigned)N * (unsigned)H, TcCfg<TILES>::THREADS, TcCfg<TILES>::smem(M), stream>>>(
         static_cast<const __nv_bfloat16 *>(q), static_cast<const __nv_bfloat16 *>(k),
         static_cast<const __nv_bfloat16 *>(v), g, beta, state, parent, M, H,
         static_cast<__nv_bfloat16 *>(out));
