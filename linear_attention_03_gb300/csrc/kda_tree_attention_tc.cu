@@ -18,12 +18,13 @@
 // kernel joins them.  The cut depends on the lengths alone, so results repeat
 // bit for bit.
 //
-// Roles: warp 0 loads (TMA, one box per page or part of one), a warp per row
-// tile issues its products, a warpgroup per row tile does the softmax with a
-// thread per row (the running maximum needs no exchange).  Keys go in steps of
-// 64, half a tile: a row tile's scores have four (QT = 1) or two (QT = 2)
-// buffers of 64 columns, so the products of the next steps run while a step's
-// softmax does, and a row's 64 scores fit its thread's registers (read once).
+// Roles: warp 0 loads (TMA, one box per page or part of one); per row tile one
+// warp issues the scores' products and one the sums', and a warpgroup does the
+// softmax with a thread per row (the running maximum needs no exchange).  Keys
+// go in steps of 64, half a tile, so that a row's scores fit its thread's
+// registers: they are read once, and their columns are free for the next
+// step's product while the softmax runs.  The weights have two buffers of their
+// own, so neither product waits for the other.
 // Warp 3 looks at every value tile before its product: rows past the last key
 // become zeros, since a weight of zero would not cancel a NaN; in the tree tile
 // also the rows of no node and every value that is not finite, which the rows
@@ -51,23 +52,22 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int D, int QT> struct Cfg {
     static constexpr int HALVES = D / 64;
-    static constexpr int THREADS = 128 + 128 * QT;
+    static constexpr int THREADS = QT == 1 ? 256 : 448;           // QT = 2: two more warps at the end
     static constexpr int SLOT = kTile * D * 2;                    // bytes of a key or value tile
     static constexpr int SLOTS = D == 64 ? 8 : (QT == 1 ? 6 : 5);
     static constexpr int Q_BYTES = QT * SLOT;
     static constexpr int O_RING = Q_BYTES;
     static constexpr int O_MISC = O_RING + SLOTS * SLOT;
+    // TMEM columns per row tile: score buffers of 64, two weight buffers of 32; then the sums
+    static constexpr int BUFS = QT == 1 ? 3 : 1, TM_P = 64 * BUFS;
     // Segments (and value tiles) that can be under way at once: a unit's end may still be read
     // while warp 3 prepares the tiles that the ring holds after it.
     static constexpr int RING = D == 64 ? 8 : 4;
     static_assert(RING > SLOTS / 2, "ring of lines");
-    static constexpr int NBARS = 2 * SLOTS + 18 + RING;
+    static constexpr int NBARS = 2 * SLOTS + (2 * BUFS + 7) * QT + RING;
     static constexpr int O_LINES = O_MISC + 8 * NBARS, O_WORDS = O_LINES + RING * 8 * kMaxTreeNodes;
     static constexpr int SMEM = O_MISC + (D == 64 ? 8192 : 3072);
     static_assert(O_WORDS + 16 + 8 * RING <= SMEM, "misc");
-    static constexpr int BUFS = 4 / QT;        // score buffers per row tile
-    static constexpr int AHEAD = BUFS / 2;     // steps by which the scores lead the sums
-    // TMEM columns: scores (and the weights in their place), then the sums
     static constexpr int TM_O = 256;
 };
 static_assert(Cfg<128, 1>::SMEM <= 232448 && Cfg<128, 2>::SMEM <= 232448, "227 KB of shared memory");
@@ -205,13 +205,17 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
     const uint32_t bars = base + C::O_MISC;
     auto full = [&](int s) { return bars + 8u * s; };
     auto empty = [&](int s) { return bars + 8u * (C::SLOTS + s); };
-    auto s_full = [&](int t, uint32_t b) { return bars + 8u * (2 * C::SLOTS + C::BUFS * t + b); };
-    auto p_full = [&](int t, uint32_t b) { return bars + 8u * (2 * C::SLOTS + 4 + C::BUFS * t + b); };
-    auto o_full = [&](int t, uint32_t i) { return bars + 8u * (2 * C::SLOTS + 8 + 4 * t + (i & 3)); };
-    auto q_full = [&](int t) { return bars + 8u * (2 * C::SLOTS + 16 + t); };
-    auto v_ready = [&](uint32_t i) { return bars + 8u * (2 * C::SLOTS + 18 + i % C::RING); };
-    // scores of row tile t, buffer b (the weights go in their place)
+    constexpr int PER_TILE = 2 * C::BUFS + 7;
+    auto tile_bar = [&](int t, uint32_t i) { return bars + 8u * (2 * C::SLOTS + PER_TILE * t + i); };
+    auto s_full = [&](int t, uint32_t b) { return tile_bar(t, b); };
+    auto s_free = [&](int t, uint32_t b) { return tile_bar(t, C::BUFS + b); };
+    auto p_full = [&](int t, uint32_t i) { return tile_bar(t, 2 * C::BUFS + (i & 1)); };
+    auto o_full = [&](int t, uint32_t i) { return tile_bar(t, 2 * C::BUFS + 2 + (i & 3)); };
+    auto q_full = [&](int t) { return tile_bar(t, 2 * C::BUFS + 6); };
+    auto v_ready = [&](uint32_t i) { return bars + 8u * (2 * C::SLOTS + PER_TILE * QT + i % C::RING); };
+    // columns of row tile t: score buffer b, the weights of step i
     auto s_col = [](int t, uint32_t b) { return t * 128 + b * 64; };
+    auto p_col = [](int t, uint32_t i) { return t * 128 + C::TM_P + (i & 1) * 32; };
 
     Place place;
     find_place(a, sh.groups, sh.ctas, blockIdx.x, reinterpret_cast<int64_t *>(smem), place);
@@ -238,8 +242,9 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
         for (int t = 0; t < QT; ++t) {
             for (int b = 0; b < C::BUFS; ++b) {
                 mbar_init(s_full(t, b), 1);
-                mbar_init(p_full(t, b), 128);
+                mbar_init(s_free(t, b), 128);
             }
+            for (int b = 0; b < 2; ++b) mbar_init(p_full(t, b), 128);
             for (int b = 0; b < 4; ++b) mbar_init(o_full(t, b), 1);
             mbar_init(q_full(t), 128);
         }
@@ -316,86 +321,63 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                     mbar_wait(full(s), last & 1, 100000000ull);
                 }
         }
-    } else if (warp <= QT) {
+    } else if (warp <= 2 || warp >= 12) {
         // ---------------------------------------------------------------- products
-        // A warp per row tile, one elected thread of which issues.  A ready wait costs
-        // the warp some 100 clocks, and the tensor pipe holds little work ahead: with
-        // one warp for both row tiles it stood idle for half of the time.
-        const int t = warp - 1;
+        // One elected thread of the warp issues.  A ready wait costs the warp some 100
+        // clocks and the tensor pipe holds little work ahead: with one warp for all
+        // products it stood idle for half of the time.
+        const bool sums = QT == 1 ? warp == 2 : warp >= 12;
+        const int t = QT == 1 ? 0 : (sums ? warp - 12 : warp - 1);
         constexpr uint32_t ID_QK = idesc_bf16(kTile, 64, 0, 0), ID_PV = idesc_bf16(kTile, D, 0, 1);
         constexpr uint64_t HI_Q = sw128_hi(0, 1024), HI_K = sw128_hi(0, C::HALVES * 1024);
         constexpr uint64_t HI_V = sw128_hi(1024, C::HALVES * 1024);
         constexpr uint32_t kHalf = 8 * C::HALVES * 1024;     // bytes of 64 keys
         auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
-        // a run over the segment's steps: the key tile's place in the ring, the step in the tile
-        struct Steps {
-            uint32_t slot, par, tile, j;
-            int i, x, halves, valid;
-        };
-        Steps sc{0, 0, 0, 0, 0, 0, 0, 0}, su{1, 0, 0, 0, 0, 0, 0, 0};
-        uint32_t seg = 0;
+        uint32_t slot = sums ? 1 : 0, par = 0, tile = 0, j = 0, seg = 0;     // the tile's place in the ring; steps before
         for (; run.left > 0 && ok; run.advance(a, sh.groups), ++seg) {
             const int cnt = (int)uniform((uint32_t)run.count());
-            auto enter = [&](Steps &w) {
-                w.x = 0;
-                if (w.i < cnt) {
-                    w.valid = (int)uniform((uint32_t)valid_keys(a, run, run.t0 + w.i));
-                    w.halves = (w.valid + 63) / 64;
-                }
-            };
-            auto next = [&](Steps &w) {
-                ++w.j;
-                if (++w.x < w.halves) return;
-                mma_commit_w(empty(w.slot));                 // the tile is read
-                w.slot += 2;
-                if (w.slot >= (uint32_t)C::SLOTS) {
-                    w.slot -= C::SLOTS;
-                    w.par ^= 1;
-                }
-                ++w.tile;
-                ++w.i;
-                enter(w);
-            };
-            sc.i = su.i = 0;
-            enter(sc);
-            enter(su);
-            wait(q_full(t), seg & 1);
-            tc_fence_after();
-            for (int lead = 0; su.i < cnt && ok;) {
-                if (sc.i < cnt) {
-                    if (sc.x == 0 && !wait(full(sc.slot), sc.par)) break;
-                    const uint32_t kb = uniform(base + C::O_RING + sc.slot * C::SLOT + sc.x * kHalf);
-                    const uint32_t b = uniform(sc.j % C::BUFS), to = tmem + s_col(t, b), qb = base + t * C::SLOT;
+            if (!sums) wait(q_full(t), seg & 1);
+            for (int i = 0; i < cnt && ok; ++i, ++tile) {
+                const int valid = (int)uniform((uint32_t)valid_keys(a, run, run.t0 + i));
+                if (!(sums ? wait(v_ready(tile), (tile / C::RING) & 1) : wait(full(slot), par))) break;
+                for (int x = 0; 64 * x < valid; ++x, ++j) {
+                    const uint32_t at = uniform(base + C::O_RING + slot * C::SLOT + x * kHalf);
+                    if (!sums) {
+                        const uint32_t b = uniform(j % C::BUFS), to = tmem + s_col(t, b), qb = base + t * C::SLOT;
+                        if (j >= (uint32_t)C::BUFS && !wait(s_free(t, b), (j / C::BUFS - 1) & 1)) break;
+                        tc_fence_after();
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-                        mma_bf16_w(to, HI_Q | sw128_lo(qb + (ks >> 2) * 16384 + (ks & 3) * 32),
-                                   HI_K | sw128_lo(kb + (ks >> 2) * 1024 + (ks & 3) * 32), ID_QK, ks > 0);
-                    mma_commit_w(s_full(t, b));
-                    next(sc);
-                    if (++lead <= C::AHEAD) continue;
-                }
-                const uint32_t b = uniform(su.j % C::BUFS);
-                if (su.x == 0 && !wait(v_ready(su.tile), (su.tile / C::RING) & 1)) break;
-                if (!wait(p_full(t, b), (su.j / C::BUFS) & 1)) break;
-                tc_fence_after();
-                const uint32_t vb = uniform(base + C::O_RING + su.slot * C::SLOT + su.x * kHalf);
-                const uint32_t p = tmem + s_col(t, b), o = tmem + C::TM_O + t * 128;
-                const int left = su.valid - 64 * su.x;
-                const uint32_t more = su.i > 0 || su.x > 0;  // not the segment's first step
-                if (left > 48) {
+                        for (int ks = 0; ks < D / 16; ++ks)
+                            mma_bf16_w(to, HI_Q | sw128_lo(qb + (ks >> 2) * 16384 + (ks & 3) * 32),
+                                       HI_K | sw128_lo(at + (ks >> 2) * 1024 + (ks & 3) * 32), ID_QK, ks > 0);
+                        mma_commit_w(s_full(t, b));
+                    } else {
+                        const uint32_t p = uniform(tmem + p_col(t, j)), o = tmem + C::TM_O + t * 128;
+                        const uint32_t more = i > 0 || x > 0;        // not the segment's first step
+                        const int left = valid - 64 * x;
+                        if (!wait(p_full(t, j), (j >> 1) & 1)) break;
+                        tc_fence_after();
+                        if (left > 48) {
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_tmem_a_w(o, p + ks * 8, HI_V | sw128_lo(vb + ks * 2 * C::HALVES * 1024), ID_PV,
-                                     ks > 0 ? 1u : more);
-                } else {
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_tmem_a_w(o, p + ks * 8, HI_V | sw128_lo(at + ks * 2 * C::HALVES * 1024), ID_PV,
+                                             ks > 0 ? 1u : more);
+                        } else {
 #pragma unroll
-                    for (int ks = 0; ks < 3; ++ks)
-                        if (16 * ks < left)
-                            mma_tmem_a_w(o, p + ks * 8, HI_V | sw128_lo(vb + ks * 2 * C::HALVES * 1024), ID_PV,
-                                         ks > 0 ? 1u : more);
+                            for (int ks = 0; ks < 3; ++ks)
+                                if (16 * ks < left)
+                                    mma_tmem_a_w(o, p + ks * 8, HI_V | sw128_lo(at + ks * 2 * C::HALVES * 1024), ID_PV,
+                                                 ks > 0 ? 1u : more);
+                        }
+                        mma_commit_w(o_full(t, j));
+                    }
                 }
-                mma_commit_w(o_full(t, su.j));
-                next(su);
+                mma_commit_w(empty(slot));                   // the tile is read
+                slot += 2;
+                if (slot >= (uint32_t)C::SLOTS) {
+                    slot -= C::SLOTS;
+                    par ^= 1;
+                }
             }
         }
     } else if (warp == 3) {
@@ -504,9 +486,7 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
             mbar_arrive(q_full(t));
         };
         uint32_t tile = 0, j = 0, seg = 0;                   // tiles, steps and segments before
-        // Step i's sums complete phase i / 4 of barrier i % 4.  Who asks for step j - 1 has
-        // seen the scores of step j, and those were issued after the sums of step j - 3 at
-        // least: step j - 5's phase is long over, and step j + 3's cannot be.
+        // step i's sums complete phase i / 4 of barrier i % 4
         auto wait_sums = [&](uint32_t i) { return wait(o_full(t, i), (i >> 2) & 1); };
         load_q(run);
         for (; run.left > 0 && ok; run.advance(a, sh.groups), ++seg) {
@@ -531,6 +511,8 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                     tc_fence_after();
                     float v[64];
                     tmem_ld64(sc, v);
+                    tc_fence_before();
+                    mbar_arrive(s_free(t, b));
                     if (tree) {
 #pragma unroll
                         for (int e = 0; e < 64; ++e) v[e] = (mine >> e & 1) != 0 ? v[e] : -INFINITY;
@@ -574,11 +556,13 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                         add[e & 1] = f2add(add[e & 1], y);
                         w[e] = __uint_as_float(pack_bf16x2(y.x, y.y));
                     }
-                    tmem_st32_nowait(sc, w);
+                    // the sums two steps back have read this buffer
+                    if (done >= 2 && !wait_sums(j - 2)) break;
+                    tmem_st32_nowait(tmem + lanes + p_col(t, j), w);
                     sum += (add[0].x + add[0].y) + (add[1].x + add[1].y);
                     tmem_wait_st();
                     tc_fence_before();
-                    mbar_arrive(p_full(t, b));
+                    mbar_arrive(p_full(t, j));
                 }
             }
             tile += cnt;
