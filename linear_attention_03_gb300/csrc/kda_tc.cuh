@@ -30,6 +30,17 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
                  : "memory");
 }
 
+// Whether the phase with the given parity is complete (one try, which may
+// suspend the thread for a short time).
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+    return done != 0;
+}
+
 // Wait for the phase with the given parity to complete.  Gives up after
 // roughly `limit_ns` nanoseconds and returns false.  Each try lets the
 // hardware suspend the thread until the phase completes (up to 20 us), so a

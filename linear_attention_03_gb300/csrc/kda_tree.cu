@@ -23,7 +23,7 @@ namespace {
 constexpr int kNodeBlock = 8;   // nodes whose products share one pass over S_0
 
 template <int D> struct TreeCfg {
-    static constexpr int THREADS = D < 32 ? 32 : D;   // a thread per state column
+    static constexpr int THREADS = 256;               // for the line products; a thread per state column solves
     static size_t smem(int M) {
         const size_t rows = (size_t)((M + kNodeBlock - 1) / kNodeBlock) * kNodeBlock;
         return rows * D * 4 * 5 + (size_t)M * M * 8 + (size_t)M * 16;

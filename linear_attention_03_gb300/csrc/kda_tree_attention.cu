@@ -24,7 +24,7 @@ namespace {
 constexpr int kThreads = 128, kRowsPerWarp = 4, kRows = 16, kKeys = 32;
 
 template <int D> constexpr size_t smem_bytes() {
-    return sizeof(float) * (kKeys * (D + 4) + kKeys * D + kRows * D);
+    return sizeof(float) * (kKeys * (D + 4) + kKeys * D + kRows * D + kRows * kKeys);
 }
 
 // Partial results of split s of a row: [unit][s][kRows] x (D sums, maximum, sum).
@@ -51,7 +51,7 @@ tree_attention_kernel(const TreeAttention a, int row_tiles, int splits, Partials
     constexpr int LD = D + 4;                     // padded key rows: no bank conflicts down a column
     constexpr int CPL = D < 32 ? 1 : D / 32;      // output columns per lane
     extern __shared__ __align__(16) float smem[];
-    float *sk = smem, *sv = sk + kKeys * LD, *sq = sv + kKeys * D;
+    float *sk = smem, *sv = sk + kKeys * LD, *sq = sv + kKeys * D, *sp = sq + kRows * D;
     __shared__ int32_t par[kMaxTreeNodes];
     __shared__ uint64_t line[kMaxTreeNodes];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -71,9 +71,14 @@ tree_attention_kernel(const TreeAttention a, int row_tiles, int splits, Partials
     }
     const int32_t *table = a.page_table + n * a.max_pages;
     for (int m = tid; m < M; m += kThreads) par[m] = a.parent[n * M + m];
-    for (int i = tid; i < kRows * D; i += kThreads) {
-        const int r = row0 + i / D;
-        sq[i] = r < rows ? Elem<Tin>::load(q + ((n * M + r / G) * a.H + h * G + r % G) * D + i % D) : 0.f;
+#pragma unroll
+    for (int y = 0; y < (kRows * D / 8 + kThreads - 1) / kThreads; ++y) {
+        const int i = tid + y * kThreads, r = row0 + i / (D / 8), c = i % (D / 8) * 8;
+        float x[8] = {0.f};
+        if (i < kRows * (D / 8)) {
+            if (r < rows) Elem<Tin>::load8(q + ((n * M + r / G) * a.H + h * G + r % G) * D + c, x);
+            Elem<float>::store8(sq + i * 8, x);
+        }
     }
     __syncthreads();
     for (int m = tid; m < M; m += kThreads) line[m] = tree_line(par, m);
@@ -92,15 +97,21 @@ tree_attention_kernel(const TreeAttention a, int row_tiles, int splits, Partials
 #pragma unroll
         for (int e = 0; e < CPL; ++e) acc[r][e] = 0.f;
     }
-    for (int t = t0; t < t1; ++t) {
+    // A tile's keys and values pass through registers, so that the next tile is on its
+    // way while this one is worked on: PIECES runs of eight channels per thread.
+    constexpr int PIECES = kKeys * (D / 8) / kThreads > 0 ? kKeys * (D / 8) / kThreads : 1;
+    float nk[PIECES][8], nv[PIECES][8];
+    auto base_of = [&](int t) { return t >= cache_tiles ? (t - cache_tiles) * kKeys : t * kKeys; };
+    auto count_of = [&](int t) { return min(kKeys, (t >= cache_tiles ? M : len) - base_of(t)); };
+    auto fetch = [&](int t) {
         const bool tree = t >= cache_tiles;
-        const int base = tree ? (t - cache_tiles) * kKeys : t * kKeys;
-        const int count = min(kKeys, (tree ? M : len) - base);
-        __syncthreads();
-        for (int i = tid; i < kKeys * (D / 8); i += kThreads) {
-            const int j = i / (D / 8), c = i % (D / 8) * 8;
-            float x[8] = {0.f}, y[8] = {0.f};
-            if (j < count) {
+        const int base = base_of(t), count = count_of(t);
+#pragma unroll
+        for (int y = 0; y < PIECES; ++y) {
+            const int i = tid + y * kThreads, j = i / (D / 8), c = i % (D / 8) * 8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) nk[y][e] = nv[y][e] = 0.f;
+            if (j < count && j < kKeys) {
                 const Tin *pk, *pv;
                 if (tree) {
                     const int64_t at = ((n * M + base + j) * a.H_kv + h) * D;
@@ -111,17 +122,31 @@ tree_attention_kernel(const TreeAttention a, int row_tiles, int splits, Partials
                     pv = pk == nullptr ? nullptr : v_cache + (pk - k_cache);
                 }
                 if (pk != nullptr) {
-                    Elem<Tin>::load8(pk + c, x);
-                    Elem<Tin>::load8(pv + c, y);
+                    Elem<Tin>::load8(pk + c, nk[y]);
+                    Elem<Tin>::load8(pv + c, nv[y]);
                 }
             }
+        }
+    };
+    if (t0 < t1) fetch(t0);
+    for (int t = t0; t < t1; ++t) {
+        const bool tree = t >= cache_tiles;
+        const int base = base_of(t), count = count_of(t);
+        __syncthreads();
+#pragma unroll
+        for (int y = 0; y < PIECES; ++y) {
+            const int i = tid + y * kThreads, j = i / (D / 8), c = i % (D / 8) * 8;
+            if (j >= kKeys) continue;
 #pragma unroll
             for (int e = 0; e < 8; e += 4) {
-                *reinterpret_cast<float4 *>(sk + j * LD + c + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-                *reinterpret_cast<float4 *>(sv + j * D + c + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                *reinterpret_cast<float4 *>(sk + j * LD + c + e) =
+                    make_float4(nk[y][e], nk[y][e + 1], nk[y][e + 2], nk[y][e + 3]);
+                *reinterpret_cast<float4 *>(sv + j * D + c + e) =
+                    make_float4(nv[y][e], nv[y][e + 1], nv[y][e + 2], nv[y][e + 3]);
             }
         }
         __syncthreads();
+        if (t + 1 < t1) fetch(t + 1);
         // lane j holds key j's scores
         float s[kRowsPerWarp];
 #pragma unroll
@@ -157,17 +182,42 @@ tree_attention_kernel(const TreeAttention a, int row_tiles, int splits, Partials
 #pragma unroll
             for (int e = 0; e < CPL; ++e) acc[r][e] *= shrink;
         }
-        for (int j = 0; j < count; ++j) {
-            float y[CPL];
+        if (!tree) {
+            // (keys past the count have weight 0 and values 0)
+            float *wp = sp + warp * kRowsPerWarp * kKeys;
 #pragma unroll
-            for (int e = 0; e < CPL; ++e) y[e] = CPL * lane + e < D ? sv[j * D + CPL * lane + e] : 0.f;
+            for (int r = 0; r < kRowsPerWarp; ++r) wp[r * kKeys + lane] = s[r];
+            __syncwarp();
+#pragma unroll 2
+            for (int j = 0; j < kKeys; j += 4) {
+                float y[4][CPL];
 #pragma unroll
-            for (int r = 0; r < kRowsPerWarp; ++r) {
-                const float w = __shfl_sync(0xffffffffu, s[r], j);
-                // a key the row does not see adds nothing, whatever it holds
-                if (seen[r] >> j & 1) {
+                for (int z = 0; z < 4; ++z)
 #pragma unroll
-                    for (int e = 0; e < CPL; ++e) acc[r][e] += w * y[e];
+                    for (int e = 0; e < CPL; ++e)
+                        y[z][e] = CPL * lane + e < D ? sv[(j + z) * D + CPL * lane + e] : 0.f;
+#pragma unroll
+                for (int r = 0; r < kRowsPerWarp; ++r) {
+                    const float4 w = *reinterpret_cast<const float4 *>(wp + r * kKeys + j);
+#pragma unroll
+                    for (int e = 0; e < CPL; ++e)
+                        acc[r][e] += w.x * y[0][e] + w.y * y[1][e] + w.z * y[2][e] + w.w * y[3][e];
+                }
+            }
+            __syncwarp();
+        } else {
+            for (int j = 0; j < count; ++j) {
+                float y[CPL];
+#pragma unroll
+                for (int e = 0; e < CPL; ++e) y[e] = CPL * lane + e < D ? sv[j * D + CPL * lane + e] : 0.f;
+#pragma unroll
+                for (int r = 0; r < kRowsPerWarp; ++r) {
+                    const float w = __shfl_sync(0xffffffffu, s[r], j);
+                    // a key the row does not see adds nothing, whatever it holds
+                    if (seen[r] >> j & 1) {
+#pragma unroll
+                        for (int e = 0; e < CPL; ++e) acc[r][e] += w * y[e];
+                    }
                 }
             }
         }
@@ -246,8 +296,10 @@ int sm_count() {
     return sms;
 }
 
-// Splits of the longest cache the table can hold: about four CTAs per SM in
-// all, at least eight key tiles in each.
+// Splits of the longest cache the table can hold: about four CTAs per SM in all
+// (more even out ragged lengths, 1,262 us instead of 1,390 for sixteen of up to
+// 8,192 tokens, but cost 450 us instead of 324 for two long caches), at least
+// eight key tiles in each.
 int splits_of(int64_t units, int64_t room) {
     const int64_t tiles = room / kKeys + 2;
     int64_t s = (4 * (int64_t)sm_count() + units - 1) / units;

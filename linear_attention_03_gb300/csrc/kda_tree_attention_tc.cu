@@ -261,7 +261,7 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
     auto flag = [&](uint32_t code) { atomicCAS(const_cast<uint32_t *>(&words[W_STATUS]), 0u, code); };
     // a bounded wait of a whole warp; once one gives up, the warp stops
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (ok) {
+        if (ok && !__all_sync(0xffffffffu, mbar_try(bar, parity))) {
             ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
             if (!ok) {
                 words[W_ABORT] = 1;
