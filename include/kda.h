@@ -401,12 +401,14 @@ KDA_API size_t kda_tree_attention_workspace_size(kda_dims dims, int32_t H_kv, in
  *   cache_lens [N] int32 device, 0 .. max_pages * page_size.  What the cache
  *          holds past a length is never used.
  *   lse    [N*M, H] fp32 or NULL (-infinity in the rows of no node)
- *   workspace  kda_tree_attention_workspace_size() bytes, 256-byte aligned or
- *          more; its first word is the device status word: KDA_DEVICE_BAD_PAGE
- *          and KDA_DEVICE_BAD_LENGTH are reported there (out and lse are then
- *          unspecified; no access leaves the buffers)
- * Any page_size serves; multiples of 8 take the tensor-core path (bf16, d = 64
- * or 128).  N * M * H must not exceed 2^29.
+ *   workspace  kda_tree_attention_workspace_size() bytes; its first word is the
+ *          device status word, set by this call: KDA_DEVICE_BAD_PAGE,
+ *          KDA_DEVICE_BAD_LENGTH and KDA_DEVICE_TIMEOUT (a bounded wait) are
+ *          reported there (out and lse are then unspecified; no access leaves
+ *          the buffers)
+ * Any page_size serves; bf16 with d = 64 or 128 and pages of whole groups of
+ * eight tokens takes the tensor-core path, everything else the CUDA cores.
+ * N * M * H must not exceed 2^29.  The same call gives the same bits.
  */
 KDA_API kda_status kda_tree_attention(const void *q, const void *k_new, const void *v_new,
                                       const void *k_cache, const void *v_cache,
