@@ -210,7 +210,8 @@ size_t tree_attention_partial_bytes(int32_t N, int32_t M, int32_t H, int32_t H_k
 cudaError_t launch_tree_attention(const TreeAttention &a, int32_t D, kda_dtype dt, void *workspace,
                                   cudaStream_t stream);
 // the same on the tensor cores: bf16, d = 64 or 128, pages of whole groups of eight tokens
-bool tree_attention_tc_supported(int32_t H_kv, int32_t D, kda_dtype dt, int64_t num_pages, int32_t page_size);
+bool tree_attention_tc_supported(int32_t H, int32_t H_kv, int32_t D, kda_dtype dt, int64_t num_pages,
+                                 int32_t page_size);
 size_t tree_attention_tc_partial_bytes(int32_t M, int32_t H, int32_t H_kv, int32_t D);
 cudaError_t launch_tree_attention_tc(const TreeAttention &a, int32_t D, void *workspace, cudaStream_t stream);
 

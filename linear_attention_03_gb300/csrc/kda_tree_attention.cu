@@ -344,7 +344,7 @@ template <typename Tin, int D> cudaError_t run(const TreeAttention &a, void *wor
 size_t tree_attention_partial_bytes(int32_t N, int32_t M, int32_t H, int32_t H_kv, int32_t D, kda_dtype dt,
                                     int32_t page_size, int32_t max_pages) {
     // the number of pages is not known here: room for whichever form the call takes
-    const size_t tc = tree_attention_tc_supported(H_kv, D, dt, 1, page_size)
+    const size_t tc = tree_attention_tc_supported(H, H_kv, D, dt, 1, page_size)
                           ? tree_attention_tc_partial_bytes(M, H, H_kv, D) : 0;
     const int64_t units = (int64_t)N * H_kv * row_tiles_of(M, H, H_kv);
     const int splits = splits_of(units, (int64_t)max_pages * page_size);
@@ -354,7 +354,7 @@ size_t tree_attention_partial_bytes(int32_t N, int32_t M, int32_t H, int32_t H_k
 
 cudaError_t launch_tree_attention(const TreeAttention &a, int32_t D, kda_dtype dt, void *workspace,
                                   cudaStream_t stream) {
-    if (tree_attention_tc_supported(a.H_kv, D, dt, a.num_pages, a.page_size))
+    if (tree_attention_tc_supported(a.H, a.H_kv, D, dt, a.num_pages, a.page_size))
         return launch_tree_attention_tc(a, D, workspace, stream);
     const cudaError_t e = cudaMemsetAsync(a.status, 0, sizeof(int32_t), stream);
     if (e != cudaSuccess) return e;

@@ -3,23 +3,25 @@
 // of 8.  The mathematics is that of kda_tree_attention.cu.
 //
 // All M x G rows of a cache head read the same keys, so they make the row
-// dimension of one product: tiles of 128 rows against tiles of 128 keys,
+// dimension of one product: tiles of 128 rows (as many whole nodes' query heads
+// as fit) against tiles of 128 keys,
 // S = Q K^T into TMEM, the weights back into TMEM as the operand of O += P V.
 // One tile (QT = 1) or two (QT = 2, more than 128 rows) share each key tile in
 // shared memory.  The work is bound by the bytes of the cache as long as one
 // key tile's two products per row tile (2 x 512 clocks at d = 128) and its
 // softmax stay below the tile's 64 KB at the SM's share of HBM (~2,800 clocks).
 //
-// Split: every (sequence, cache head, row group) is a unit of ceil(len / 128)
-// + 1 key tiles, the last of them the tree.  The units' tiles in one line are
+// Split: every (sequence, cache head, row group) is a unit of key tiles, the last
+// of which holds the tree, behind the cache's last keys where they leave room.
+// The units' tiles in one line are
 // cut into equal pieces, one per CTA, one CTA per SM: ragged lengths cost no
 // imbalance, and a long cache needs no separate split.  Only the two ends of a
 // piece can be parts of a unit; those go to the workspace as sums, and a second
 // kernel joins them.  The cut depends on the lengths alone, so results repeat
 // bit for bit.
 //
-// Roles: warp 0 loads (TMA, one box per page or part of one); per row tile one
-// warp issues the scores' products and one the sums', and a warpgroup does the
+// Roles: warp 0 loads (TMA, one box per page or part of one), warp 1 issues the
+// scores' products, warp 2 the sums', and a warpgroup per row tile does the
 // softmax with a thread per row (the running maximum needs no exchange).  Keys
 // go in steps of 64, half a tile, so that a row's scores fit its thread's
 // registers: they are read once, and their columns are free for the next
@@ -48,6 +50,8 @@
 #include <cuda.h>
 #include <math.h>
 
+#include <algorithm>
+
 namespace kda {
 namespace {
 
@@ -60,7 +64,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int D, int QT> struct Cfg {
     static constexpr int HALVES = D / 64;
-    static constexpr int THREADS = QT == 1 ? 256 : 448;           // QT = 2: two more warps at the end
+    static constexpr int THREADS = 128 + 128 * QT;                // twelve warps leave 168 registers a thread
     static constexpr int SLOT = kTile * D * 2;                    // bytes of a key or value tile
     static constexpr int SLOTS = D == 64 ? 8 : (QT == 1 ? 6 : 5);
     static constexpr int Q_BYTES = QT * SLOT;
@@ -72,7 +76,7 @@ template <int D, int QT> struct Cfg {
     // while warp 3 prepares the tiles that the ring holds after it.
     static constexpr int RING = D == 64 ? 8 : 4;
     static_assert(RING > SLOTS / 2, "ring of lines");
-    static constexpr int NBARS = 2 * SLOTS + (2 * BUFS + 7) * QT + RING;
+    static constexpr int NBARS = 2 * SLOTS + (2 * BUFS + 6) * QT + 2 + 2 * RING;
     static constexpr int O_LINES = O_MISC + 8 * NBARS, O_WORDS = O_LINES + RING * 8 * kMaxTreeNodes;
     static constexpr int SMEM = O_MISC + (D == 64 ? 8192 : 3072);
     static_assert(O_WORDS + 16 + 8 * RING <= SMEM, "misc");
@@ -84,7 +88,7 @@ static_assert(Cfg<128, 1>::SMEM <= 232448 && Cfg<128, 2>::SMEM <= 232448, "227 K
 enum { W_TMEM = 0, W_ABORT, W_STATUS, W_BAD };
 
 struct Maps {
-    CUtensorMap k, v, kn, vn;
+    CUtensorMap q, k, v, k8, v8, kn, vn;   // k8, v8: the cache in boxes of eight rows
 };
 
 
@@ -93,7 +97,17 @@ __device__ __forceinline__ int clamped_len(const TreeAttention &a, int64_t n) {
     const int64_t room = (int64_t)a.max_pages * a.page_size;
     return len < 0 ? 0 : (len > room ? (int)room : len);
 }
-__device__ __forceinline__ int unit_tiles(int len) { return (len + kTile - 1) / kTile + 1; }
+// The last tile of a unit: the cache's last `keys` keys, and the tree from row `tree` on.
+struct Last {
+    int keys, tree;
+};
+__device__ __forceinline__ Last last_tile(int len, int M) {
+    const int keys = len % kTile, tree = (keys + 7) & ~7;
+    return keys > 0 && tree + M <= kTile ? Last{keys, tree} : Last{0, 0};
+}
+__device__ __forceinline__ int unit_tiles(int len, int M) {
+    return (len + kTile - 1) / kTile + (last_tile(len, M).keys > 0 ? 0 : 1);
+}
 
 // where CTA b's piece of `total` tiles starts
 __device__ __forceinline__ int64_t piece_start(int64_t total, int ctas, int b) {
@@ -114,7 +128,8 @@ struct Place {
 };
 struct Shape {
     int32_t box;            // rows per load: the power of two that divides the page size, at most 128
-    int32_t groups;         // row groups (q tiles of QT x 128 rows) per cache head
+    int32_t nodes;          // nodes per row tile
+    int32_t groups;         // row groups (of QT row tiles) per cache head
     int32_t ctas;
     Place *places;          // one per CTA
     float *part;            // two slots per CTA: D/4 x rows float4, then rows maxima, rows sums
@@ -129,7 +144,7 @@ __device__ void find_place(const TreeAttention &a, int groups, int ctas, int b, 
     for (int n = tid; n < a.N; n += blockDim.x) {
         const int len = a.cache_lens[n];
         bad = bad || len < 0 || len > (int64_t)a.max_pages * a.page_size;
-        sum += (int64_t)unit_tiles(clamped_len(a, n)) * per_seq;
+        sum += (int64_t)unit_tiles(clamped_len(a, n), a.M) * per_seq;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -146,7 +161,7 @@ __device__ void find_place(const TreeAttention &a, int groups, int ctas, int b, 
         for (int n0 = 0; n0 < a.N; n0 += 32) {
             const int n = n0 + lane;
             const int len = n < a.N ? clamped_len(a, n) : 0;
-            const int64_t mine = n < a.N ? (int64_t)unit_tiles(len) * per_seq : 0;
+            const int64_t mine = n < a.N ? (int64_t)unit_tiles(len, a.M) * per_seq : 0;
             int64_t run = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -155,10 +170,10 @@ __device__ void find_place(const TreeAttention &a, int groups, int ctas, int b, 
             }
             const int64_t begin = base + run - mine;
             if (mine > 0 && at >= begin && at < begin + mine) {
-                const int64_t r = (at - begin) / unit_tiles(len);
+                const int64_t r = (at - begin) / unit_tiles(len, a.M);
                 buf[0] = n;
                 buf[1] = r;
-                buf[2] = begin + r * unit_tiles(len);
+                buf[2] = begin + r * unit_tiles(len, a.M);
                 buf[3] = len;
             }
             base += __shfl_sync(0xffffffffu, run, 31);
@@ -185,15 +200,32 @@ struct Run {
             r = 0;
             if (++n < a.N && left > 0) {
                 len = clamped_len(a, n);
-                tiles = unit_tiles(len);
+                tiles = unit_tiles(len, a.M);
             }
         }
     }
 };
 
+// 64 bytes of a row, in whole 32-byte sectors where the address allows it
+__device__ __forceinline__ void store64(void *to, const uint32_t (&u)[16], bool aligned32) {
+    if (aligned32) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                             static_cast<unsigned char *>(to) + 32 * e),
+                         "r"(u[8 * e]), "r"(u[8 * e + 1]), "r"(u[8 * e + 2]), "r"(u[8 * e + 3]), "r"(u[8 * e + 4]),
+                         "r"(u[8 * e + 5]), "r"(u[8 * e + 6]), "r"(u[8 * e + 7])
+                         : "memory");
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            reinterpret_cast<uint4 *>(to)[e] = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
+    }
+}
+
 // keys of the unit's tile t
 __device__ __forceinline__ int valid_keys(const TreeAttention &a, const Run &run, int t) {
-    return t == run.tiles - 1 ? a.M : min(kTile, run.len - t * kTile);
+    return t == run.tiles - 1 ? last_tile(run.len, a.M).tree + a.M : min(kTile, run.len - t * kTile);
 }
 
 template <int D, int QT>
@@ -208,25 +240,26 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
     uint64_t *line = reinterpret_cast<uint64_t *>(smem + C::O_LINES);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    const int G = a.H / a.H_kv, rows = a.M * G;
+    const int G = a.H / a.H_kv;
 
     const uint32_t bars = base + C::O_MISC;
     auto full = [&](int s) { return bars + 8u * s; };
     auto empty = [&](int s) { return bars + 8u * (C::SLOTS + s); };
-    constexpr int PER_TILE = 2 * C::BUFS + 7;
+    constexpr int PER_TILE = 2 * C::BUFS + 6;
     auto tile_bar = [&](int t, uint32_t i) { return bars + 8u * (2 * C::SLOTS + PER_TILE * t + i); };
     auto s_full = [&](int t, uint32_t b) { return tile_bar(t, b); };
     auto s_free = [&](int t, uint32_t b) { return tile_bar(t, C::BUFS + b); };
     auto p_full = [&](int t, uint32_t i) { return tile_bar(t, 2 * C::BUFS + (i & 1)); };
     auto o_full = [&](int t, uint32_t i) { return tile_bar(t, 2 * C::BUFS + 2 + (i & 3)); };
-    auto q_full = [&](int t) { return tile_bar(t, 2 * C::BUFS + 6); };
-    auto v_ready = [&](uint32_t i) { return bars + 8u * (2 * C::SLOTS + PER_TILE * QT + i % C::RING); };
+    const uint32_t q_full = tile_bar(QT, 0), q_free = tile_bar(QT, 1);
+    auto v_ready = [&](uint32_t i) { return tile_bar(QT, 2 + i % C::RING); };            // by tile
+    auto l_ready = [&](uint32_t i) { return tile_bar(QT, 2 + C::RING + i % C::RING); };  // by segment
     // columns of row tile t: score buffer b, the weights of step i
     auto s_col = [](int t, uint32_t b) { return t * 128 + b * 64; };
     auto p_col = [](int t, uint32_t i) { return t * 128 + C::TM_P + (i & 1) * 32; };
 
     Place place;
-    find_place(a, sh.groups, sh.ctas, blockIdx.x, reinterpret_cast<int64_t *>(smem), place);
+    find_place(a, sh.groups, sh.ctas, blockIdx.x, reinterpret_cast<int64_t *>(line), place);
     const int64_t start = piece_start(place.total, sh.ctas, blockIdx.x);
     const int64_t stop = piece_start(place.total, sh.ctas, blockIdx.x + 1);
     Place *left = sh.places + blockIdx.x;
@@ -238,14 +271,14 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
     run.n = place.n;
     run.r = place.r;
     run.len = place.len;
-    run.tiles = unit_tiles(place.len);
+    run.tiles = unit_tiles(place.len, a.M);
     run.t0 = (int32_t)(start - place.unit0);
 
     if (warp == 0) tmem_alloc(base + C::O_WORDS + 4 * W_TMEM, 512);
     if (tid == 32) {
         for (int s = 0; s < C::SLOTS; ++s) {
             mbar_init(full(s), 1);
-            mbar_init(empty(s), QT);
+            mbar_init(empty(s), 1);
         }
         for (int t = 0; t < QT; ++t) {
             for (int b = 0; b < C::BUFS; ++b) {
@@ -254,9 +287,13 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
             }
             for (int b = 0; b < 2; ++b) mbar_init(p_full(t, b), 128);
             for (int b = 0; b < 4; ++b) mbar_init(o_full(t, b), 1);
-            mbar_init(q_full(t), 128);
         }
-        for (int i = 0; i < C::RING; ++i) mbar_init(v_ready(i), 1);
+        mbar_init(q_full, 1);
+        mbar_init(q_free, 1);
+        for (int i = 0; i < C::RING; ++i) {
+            mbar_init(v_ready(i), 1);
+            mbar_init(l_ready(i), 1);
+        }
         fence_mbar_init();
         words[W_ABORT] = 0;
         words[W_STATUS] = place.status;
@@ -281,19 +318,21 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
 
     if (warp == 0) {
         // ---------------------------------------------------------------- loads
-        const uint32_t box_bytes = (uint32_t)sh.box * D * 2;
         const int32_t none = (int32_t)((int64_t)a.num_pages * a.H_kv * a.page_size / 8);   // past the end: zeros
         uint32_t use = 0;                                    // ring uses so far: K of tile j is 2j, V 2j + 1
         for (; run.left > 0 && ok; run.advance(a, sh.groups)) {
             const int h = run.r / sh.groups, cnt = run.count();
             const int32_t *table = a.page_table + (int64_t)run.n * a.max_pages;
             for (int t = run.t0; t < run.t0 + cnt && ok; ++t) {
+                // a lane per load: boxes of the cache (of eight rows where the tree follows),
+                // then the tree's, eight rows each
                 const bool tree = t == run.tiles - 1;
-                const int valid = valid_keys(a, run, t);
-                const int loads = tree ? (a.M + 7) / 8 : (valid + sh.box - 1) / sh.box;
+                const Last last = last_tile(run.len, a.M);
+                const int keys = tree ? last.keys : valid_keys(a, run, t), box = tree ? 8 : sh.box;
+                const int old = (keys + box - 1) / box, loads = old + (tree ? (a.M + 7) / 8 : 0);
                 int32_t group = 0;
-                if (!tree && lane < loads) {
-                    const int pos = t * kTile + lane * sh.box;
+                if (lane < old) {
+                    const int pos = t * kTile + lane * box;
                     const int page = table[pos / a.page_size];
                     if (page < 0 || page >= a.num_pages) {
                         flag(KDA_DEVICE_BAD_PAGE);
@@ -302,7 +341,7 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                         group = (int32_t)((((int64_t)page * a.H_kv + h) * a.page_size + pos % a.page_size) / 8);
                     }
                 }
-                const uint32_t bytes = tree ? (uint32_t)loads * 8 * D * 2 : (uint32_t)loads * box_bytes;
+                const uint32_t bytes = (uint32_t)loads * box * D * 2;
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv, ++use) {
                     const int s = use % C::SLOTS;
@@ -311,11 +350,13 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                     __syncwarp();
                     const uint32_t dst = base + C::O_RING + s * C::SLOT;
                     if (lane < loads) {
-                        if (tree)
-                            tma_load_4d(dst + lane * 8 * D * 2, kv ? &maps.vn : &maps.kn, 0, run.n * a.M + lane * 8, 0,
-                                        h, full(s));
+                        const uint32_t at = dst + lane * box * D * 2;   // (the tree's rows start at a multiple of 8)
+                        if (lane >= old)
+                            tma_load_4d(at, kv ? &maps.vn : &maps.kn, 0, run.n * a.M + (lane - old) * 8, 0, h, full(s));
+                        else if (tree)
+                            tma_load_4d(at, kv ? &maps.v8 : &maps.k8, 0, 0, 0, group, full(s));
                         else
-                            tma_load_4d(dst + lane * box_bytes, kv ? &maps.v : &maps.k, 0, 0, 0, group, full(s));
+                            tma_load_4d(at, kv ? &maps.v : &maps.k, 0, 0, 0, group, full(s));
                     }
                     __syncwarp();
                 }
@@ -329,13 +370,12 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                     mbar_wait(full(s), last & 1, 100000000ull);
                 }
         }
-    } else if (warp <= 2 || warp >= 12) {
+    } else if (warp <= 2) {
         // ---------------------------------------------------------------- products
         // One elected thread of the warp issues.  A ready wait costs the warp some 100
         // clocks and the tensor pipe holds little work ahead: with one warp for all
         // products it stood idle for half of the time.
-        const bool sums = QT == 1 ? warp == 2 : warp >= 12;
-        const int t = QT == 1 ? 0 : (sums ? warp - 12 : warp - 1);
+        const bool sums = warp == 2;
         constexpr uint32_t ID_QK = idesc_bf16(kTile, 64, 0, 0), ID_PV = idesc_bf16(kTile, D, 0, 1);
         constexpr uint64_t HI_Q = sw128_hi(0, 1024), HI_K = sw128_hi(0, C::HALVES * 1024);
         constexpr uint64_t HI_V = sw128_hi(1024, C::HALVES * 1024);
@@ -344,40 +384,68 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
         uint32_t slot = sums ? 1 : 0, par = 0, tile = 0, j = 0, seg = 0;     // the tile's place in the ring; steps before
         for (; run.left > 0 && ok; run.advance(a, sh.groups), ++seg) {
             const int cnt = (int)uniform((uint32_t)run.count());
-            if (!sums) wait(q_full(t), seg & 1);
+            if (!sums) {
+                // the queries, once the products before are through with the last ones
+                if (seg > 0 && !wait(q_free, (seg - 1) & 1)) break;
+                if (lane == 0) {
+                    mbar_expect_tx(q_full, (uint32_t)(QT * C::HALVES * sh.nodes * G * 128));
+                    for (int t = 0; t < QT; ++t)
+                        for (int x = 0; x < C::HALVES; ++x)
+                            tma_load_4d(base + t * C::SLOT + x * 16384, &maps.q, 0, run.r / sh.groups * G, x,
+                                        run.n * a.M + (run.r % sh.groups * QT + t) * sh.nodes, q_full);
+                }
+                __syncwarp();
+                // the next unit's come to the L2 meanwhile
+                Run then = run;
+                then.advance(a, sh.groups);
+                if (then.left > 0 && lane < QT * C::HALVES)
+                    tma_prefetch_4d(&maps.q, 0, then.r / sh.groups * G, lane % C::HALVES,
+                                    then.n * a.M + (then.r % sh.groups * QT + lane / C::HALVES) * sh.nodes);
+                if (!wait(q_full, seg & 1)) {
+                    mbar_wait(q_full, seg & 1, 100000000ull);
+                    break;
+                }
+            }
             for (int i = 0; i < cnt && ok; ++i, ++tile) {
                 const int valid = (int)uniform((uint32_t)valid_keys(a, run, run.t0 + i));
                 if (!(sums ? wait(v_ready(tile), (tile / C::RING) & 1) : wait(full(slot), par))) break;
-                for (int x = 0; 64 * x < valid; ++x, ++j) {
+                for (int x = 0; 64 * x < valid && ok; ++x, ++j) {
                     const uint32_t at = uniform(base + C::O_RING + slot * C::SLOT + x * kHalf);
                     if (!sums) {
-                        const uint32_t b = uniform(j % C::BUFS), to = tmem + s_col(t, b), qb = base + t * C::SLOT;
-                        if (j >= (uint32_t)C::BUFS && !wait(s_free(t, b), (j / C::BUFS - 1) & 1)) break;
-                        tc_fence_after();
+                        const uint32_t b = uniform(j % C::BUFS);
 #pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks)
-                            mma_bf16_w(to, HI_Q | sw128_lo(qb + (ks >> 2) * 16384 + (ks & 3) * 32),
-                                       HI_K | sw128_lo(at + (ks >> 2) * 1024 + (ks & 3) * 32), ID_QK, ks > 0);
-                        mma_commit_w(s_full(t, b));
+                        for (int t = 0; t < QT; ++t) {
+                            const uint32_t to = tmem + s_col(t, b), qb = base + t * C::SLOT;
+                            if (j >= (uint32_t)C::BUFS && !wait(s_free(t, b), (j / C::BUFS - 1) & 1)) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int ks = 0; ks < D / 16; ++ks)
+                                mma_bf16_w(to, HI_Q | sw128_lo(qb + (ks >> 2) * 16384 + (ks & 3) * 32),
+                                           HI_K | sw128_lo(at + (ks >> 2) * 1024 + (ks & 3) * 32), ID_QK, ks > 0);
+                            mma_commit_w(s_full(t, b));
+                        }
                     } else {
-                        const uint32_t p = uniform(tmem + p_col(t, j)), o = tmem + C::TM_O + t * 128;
                         const uint32_t more = i > 0 || x > 0;        // not the segment's first step
                         const int left = valid - 64 * x;
-                        if (!wait(p_full(t, j), (j >> 1) & 1)) break;
-                        tc_fence_after();
-                        if (left > 48) {
 #pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                mma_tmem_a_w(o, p + ks * 8, HI_V | sw128_lo(at + ks * 2 * C::HALVES * 1024), ID_PV,
-                                             ks > 0 ? 1u : more);
-                        } else {
+                        for (int t = 0; t < QT; ++t) {
+                            const uint32_t p = uniform(tmem + p_col(t, j)), o = tmem + C::TM_O + t * 128;
+                            if (!wait(p_full(t, j), (j >> 1) & 1)) break;
+                            tc_fence_after();
+                            if (left > 48) {
 #pragma unroll
-                            for (int ks = 0; ks < 3; ++ks)
-                                if (16 * ks < left)
+                                for (int ks = 0; ks < 4; ++ks)
                                     mma_tmem_a_w(o, p + ks * 8, HI_V | sw128_lo(at + ks * 2 * C::HALVES * 1024), ID_PV,
                                                  ks > 0 ? 1u : more);
+                            } else {
+#pragma unroll
+                                for (int ks = 0; ks < 3; ++ks)
+                                    if (16 * ks < left)
+                                        mma_tmem_a_w(o, p + ks * 8, HI_V | sw128_lo(at + ks * 2 * C::HALVES * 1024),
+                                                     ID_PV, ks > 0 ? 1u : more);
+                            }
+                            mma_commit_w(o_full(t, j));
                         }
-                        mma_commit_w(o_full(t, j));
                     }
                 }
                 mma_commit_w(empty(slot));                   // the tile is read
@@ -387,6 +455,7 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                     par ^= 1;
                 }
             }
+            if (!sums) mma_commit_w(q_free);
         }
     } else if (warp == 3) {
         // ---------------------------------------------------------------- values
@@ -407,19 +476,10 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                 const uint32_t k_use = 2 * tile, v_use = k_use + 1;
                 if (!wait(full(k_use % C::SLOTS), (k_use / C::SLOTS) & 1)) break;
                 if (!wait(full(v_use % C::SLOTS), (v_use / C::SLOTS) & 1)) break;
-                if (tree || valid < kTile) {
-                    unsigned char *vs = smem + C::O_RING + (v_use % C::SLOTS) * C::SLOT;
-                    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-                    auto piece = [&](int r, int x) {
-                        return reinterpret_cast<uint4 *>(vs + (r >> 3) * (C::HALVES * 1024) + (x >> 3) * 1024 +
-                                                         sw128_off(r & 7, x & 7));
-                    };
-                    const int until = (valid + 15) & ~15;
-                    for (int e = lane; e < (until - valid) * (D / 8); e += 32)
-                        *piece(valid + e / (D / 8), e % (D / 8)) = zero;
-                    if (tree) {
-                        uint64_t *ln = line + (seg % C::RING) * kMaxTreeNodes;
-                        volatile uint32_t *bad = words + W_BAD + 2 * (seg % C::RING);
+                uint64_t *ln = line + (seg % C::RING) * kMaxTreeNodes;
+                volatile uint32_t *bad = words + W_BAD + 2 * (seg % C::RING);
+                if (i == 0) {
+                    if (has_tree) {
                         // both nodes' walks at once; the parents come from the lanes that hold them
                         int at[2] = {lane < a.M ? lane : -2, lane + 32 < a.M ? lane + 32 : -2};
                         uint64_t on[2] = {0, 0};
@@ -440,10 +500,27 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                         ln[lane + 32] = on[1];
                         if (lane < 2) bad[lane] = 0;
                         __syncwarp();
+                    }
+                    if (lane == 0) mbar_arrive(l_ready(seg));
+                }
+                if (tree || valid < kTile) {
+                    unsigned char *vs = smem + C::O_RING + (v_use % C::SLOTS) * C::SLOT;
+                    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+                    auto piece = [&](int r, int x) {
+                        return reinterpret_cast<uint4 *>(vs + (r >> 3) * (C::HALVES * 1024) + (x >> 3) * 1024 +
+                                                         sw128_off(r & 7, x & 7));
+                    };
+                    const Last last = last_tile(run.len, a.M);
+                    const int until = (valid + 15) & ~15;
+                    for (int e = lane; e < (until - valid) * (D / 8); e += 32)
+                        *piece(valid + e / (D / 8), e % (D / 8)) = zero;
+                    if (tree) {
+                        for (int e = lane; e < (last.tree - last.keys) * (D / 8); e += 32)
+                            *piece(last.keys + e / (D / 8), e % (D / 8)) = zero;
 #pragma unroll 4
-                        for (int e = lane; e < valid * (D / 8); e += 32) {
+                        for (int e = lane; e < a.M * (D / 8); e += 32) {
                             const int r = e / (D / 8);
-                            uint4 *p = piece(r, e % (D / 8)), u = *p;
+                            uint4 *p = piece(last.tree + r, e % (D / 8)), u = *p;
                             uint32_t *w = reinterpret_cast<uint32_t *>(&u);
                             bool odd = false;
 #pragma unroll
@@ -471,35 +548,16 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;                   // TMEM lane 32 (warp % 4)
         const uint32_t o_col = tmem + lanes + C::TM_O + t * 128;
         const float c = a.scale * kLog2e;
-        unsigned char *qs = smem + t * C::SLOT;
-        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q);
         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out);
-        // a unit's queries of this row tile, swizzled as the product reads them, all loads on their way
-        auto load_q = [&](const Run &u) {
-            constexpr int PIECES = D / 8, ROWS_PER = 128 / PIECES;           // rows per pass of the warpgroup
-            const int x = wg % PIECES, first = (u.r % sh.groups) * (QT * kTile) + t * kTile + wg / PIECES;
-            const __nv_bfloat16 *from = q + ((int64_t)u.n * a.M * a.H + (u.r / sh.groups) * G) * D;
-            uint4 f[PIECES];
-#pragma unroll
-            for (int y = 0; y < PIECES; ++y) {
-                const int rr = first + y * ROWS_PER;
-                f[y] = make_uint4(0u, 0u, 0u, 0u);
-                if (rr < rows)
-                    f[y] = __ldg(reinterpret_cast<const uint4 *>(from + ((int64_t)(rr / G) * a.H + rr % G) * D) + x);
-            }
-#pragma unroll
-            for (int y = 0; y < PIECES; ++y)
-                *reinterpret_cast<uint4 *>(qs + (x >> 3) * 16384 + sw128_off(y * ROWS_PER + wg / PIECES, x & 7)) = f[y];
-            fence_proxy_async();
-            mbar_arrive(q_full(t));
-        };
+        const bool out32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
         uint32_t tile = 0, j = 0, seg = 0;                   // tiles, steps and segments before
         // step i's sums complete phase i / 4 of barrier i % 4
         auto wait_sums = [&](uint32_t i) { return wait(o_full(t, i), (i >> 2) & 1); };
-        load_q(run);
         for (; run.left > 0 && ok; run.advance(a, sh.groups), ++seg) {
-            const int h = run.r / sh.groups, row0 = (run.r % sh.groups) * (QT * kTile) + t * kTile;
-            const int cnt = run.count(), row = row0 + wg;
+            const int h = run.r / sh.groups, cnt = run.count();
+            // the thread's node and query head; none past the tile's whole nodes
+            const int node = (run.r % sh.groups * QT + t) * sh.nodes + wg / G;
+            const bool real = wg < sh.nodes * G && node < a.M;
             const int64_t n = run.n;
             float top = -INFINITY, sum = 0.f;
             uint64_t mine = 0;                       // known from the tree tile on
@@ -509,8 +567,20 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                 const bool tree = tl == run.tiles - 1;
                 const int valid = valid_keys(a, run, tl);
                 if (tree) {
-                    if (!wait(v_ready(tile + i), ((tile + i) / C::RING) & 1)) break;
-                    mine = row < rows ? line[(seg % C::RING) * kMaxTreeNodes + row / G] : 0;
+                    if (!wait(l_ready(seg), (seg / C::RING) & 1)) break;
+                    mine = real ? line[(seg % C::RING) * kMaxTreeNodes + node] : 0;
+                }
+                // which of the tile's 128 keys the row sees, where that is not all of them
+                const Last last = last_tile(run.len, a.M);
+                auto below = [](int x) { return x >= 64 ? ~uint64_t{0} : x <= 0 ? 0 : (uint64_t{1} << x) - 1; };
+                uint64_t sees[2];
+                if (tree) {
+                    sees[0] = below(last.keys) | (last.tree < 64 ? mine << last.tree : 0);
+                    sees[1] = below(last.keys - 64) | (last.tree >= 64 ? mine << (last.tree - 64)
+                                                       : last.tree > 0 ? mine >> (64 - last.tree) : 0);
+                } else {
+                    sees[0] = below(valid);
+                    sees[1] = below(valid - 64);
                 }
                 const int halves = (valid + 63) / 64;
                 for (int x = 0; x < halves; ++x, ++done, ++j) {
@@ -521,12 +591,10 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                     tmem_ld64(sc, v);
                     tc_fence_before();
                     mbar_arrive(s_free(t, b));
-                    if (tree) {
+                    if (tree || valid < kTile) {
+                        const uint64_t seen = x == 0 ? sees[0] : sees[1];
 #pragma unroll
-                        for (int e = 0; e < 64; ++e) v[e] = (mine >> e & 1) != 0 ? v[e] : -INFINITY;
-                    } else if (valid < 64 * x + 64) {
-#pragma unroll
-                        for (int e = 0; e < 64; ++e) v[e] = 64 * x + e < valid ? v[e] : -INFINITY;
+                        for (int e = 0; e < 64; ++e) v[e] = (seen >> e & 1) != 0 ? v[e] : -INFINITY;
                     }
                     float m4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
@@ -575,14 +643,10 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
             }
             tile += cnt;
             if (!ok) break;
-            // the next unit's first scores run during this one's end
-            Run then = run;
-            then.advance(a, sh.groups);
-            if (then.left > 0) load_q(then);
             if (!wait_sums(j - 1)) break;
             tc_fence_after();
             const bool whole = run.t0 == 0 && cnt == run.tiles;
-            const int64_t o_row = (n * a.M + row / G) * (int64_t)a.H + h * G + row % G;
+            const int64_t o_row = (n * a.M + node) * (int64_t)a.H + h * G + wg % G;
             volatile uint32_t *bad = words + W_BAD + 2 * (seg % C::RING);
             const uint64_t add_bad = mine == 0 ? 0 : mine & (bad[0] | (uint64_t)bad[1] << 32);
             constexpr int R = QT * kTile;
@@ -605,17 +669,13 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                         }
                     }
                 }
-                if (row >= rows) continue;
+                if (!real) continue;
                 if (whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(out + o_row * D + x);
+                    uint32_t u[16];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t u[4];
-#pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            u[y] = mine == 0 ? 0u : pack_bf16x2(o[8 * e + 2 * y] * inv, o[8 * e + 2 * y + 1] * inv);
-                        dst[e] = make_uint4(u[0], u[1], u[2], u[3]);
-                    }
+                    for (int y = 0; y < 16; ++y)
+                        u[y] = mine == 0 ? 0u : pack_bf16x2(o[2 * y] * inv, o[2 * y + 1] * inv);
+                    store64(out + o_row * D + x, u, out32);
                 } else {
                     float4 *dst = reinterpret_cast<float4 *>(part) + (size_t)(x / 4) * R + t * kTile + wg;
 #pragma unroll
@@ -623,7 +683,7 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                         dst[(size_t)e * R] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 }
             }
-            if (row < rows) {
+            if (real) {
                 if (whole) {
                     if (a.lse != nullptr) a.lse[o_row] = mine == 0 ? -INFINITY : (top + log2f(sum)) * kLn2;
                 } else {
@@ -653,7 +713,7 @@ __global__ void __launch_bounds__(256)
 tree_attention_tc_join_kernel(const TreeAttention a, const Shape sh) {
     constexpr int R = QT * kTile, ROWS = 16;
     const int b = blockIdx.x;
-    const int G = a.H / a.H_kv, rows = a.M * G;
+    const int G = a.H / a.H_kv;
     wait_prerequisites();
     if (b == 0) {
         if (blockIdx.y != 0) return;
@@ -670,15 +730,16 @@ tree_attention_tc_join_kernel(const TreeAttention a, const Shape sh) {
     const Place p = sh.places[b];
     const int64_t at = piece_start(p.total, sh.ctas, b);
     if (at >= p.total || p.unit0 == at || piece_start(p.total, sh.ctas, b - 1) > p.unit0) return;
-    const int64_t end = p.unit0 + unit_tiles(p.len);
+    const int64_t end = p.unit0 + unit_tiles(p.len, a.M);
     int parts = 1;
     for (int c = b; c < sh.ctas && piece_start(p.total, sh.ctas, c) < end; ++c) ++parts;
-    const int h = p.r / sh.groups, row0 = (p.r % sh.groups) * R;
+    const int h = p.r / sh.groups, node0 = p.r % sh.groups * QT * sh.nodes;
     // part i is CTA b - 1 + i's: its last segment for the first, its first one after that
     auto part_of = [&](int i) { return sh.part + (size_t)(2 * (b - 1 + i) + (i == 0 ? 1 : 0)) * R * (D + 2); };
     for (int e = threadIdx.x; e < ROWS * (D / 4); e += 256) {
-        const int lr = blockIdx.y * ROWS + e % ROWS, c4 = e / ROWS, row = row0 + lr;
-        if (lr >= R || row >= rows) continue;
+        const int lr = blockIdx.y * ROWS + e % ROWS, c4 = e / ROWS;
+        const int node = node0 + lr / kTile * sh.nodes + lr % kTile / G;
+        if (lr >= R || lr % kTile >= sh.nodes * G || node >= a.M) continue;
         float top = -INFINITY;
         for (int i = 0; i < parts; ++i) top = fmaxf(top, part_of(i)[(size_t)R * D + lr]);
         const float from = top == -INFINITY ? 0.f : top;
@@ -692,9 +753,9 @@ tree_attention_tc_join_kernel(const TreeAttention a, const Shape sh) {
             sum += w * q[(size_t)R * D + R + lr];
             o.x += w * x.x; o.y += w * x.y; o.z += w * x.z; o.w += w * x.w;
         }
-        const bool none = tree_line(a.parent + (int64_t)p.n * a.M, row / G) == 0;
+        const bool none = tree_line(a.parent + (int64_t)p.n * a.M, node) == 0;
         const float inv = 1.f / sum;
-        const int64_t o_row = ((int64_t)p.n * a.M + row / G) * a.H + h * G + row % G;
+        const int64_t o_row = ((int64_t)p.n * a.M + node) * a.H + h * G + lr % kTile % G;
         *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + o_row * D + 4 * c4) =
             none ? make_uint2(0u, 0u)
                  : make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
@@ -735,6 +796,12 @@ bool cache_map(CUtensorMap *map, const void *base, const TreeAttention &a, int D
     return make_map(map, base, {64, 8, (cuuint64_t)(D / 64), groups}, {(cuuint64_t)D * 2, 128, (cuuint64_t)D * 16},
                     {64, 8, (cuuint32_t)(D / 64), (cuuint32_t)(box / 8)});
 }
+// The queries [N * M][H][D]: a row tile's nodes, the query heads of one cache head, half a row.
+bool query_map(CUtensorMap *map, const TreeAttention &a, int D, int nodes) {
+    return make_map(map, a.q, {64, (cuuint64_t)a.H, (cuuint64_t)(D / 64), (cuuint64_t)a.N * a.M},
+                    {(cuuint64_t)D * 2, 128, (cuuint64_t)a.H * D * 2},
+                    {64, (cuuint32_t)(a.H / a.H_kv), 1, (cuuint32_t)nodes});
+}
 // The drafted rows [N * M][H_kv][D], eight rows of one head per box.
 bool new_map(CUtensorMap *map, const void *base, const TreeAttention &a, int D) {
     return make_map(map, base, {64, (cuuint64_t)a.N * a.M, (cuuint64_t)(D / 64), (cuuint64_t)a.H_kv},
@@ -751,18 +818,22 @@ int sm_count() {
 
 size_t place_bytes(int ctas) { return ((size_t)ctas * sizeof(Place) + 255) / 256 * 256; }
 
+// as many whole nodes as 128 rows hold (their query heads are G rows each)
+int nodes_per_tile(int M, int H, int H_kv) { return std::min(M, kTile / (H / H_kv)); }
+
 template <int D, int QT> cudaError_t run_tc(const TreeAttention &a, void *workspace, cudaStream_t stream) {
     using C = Cfg<D, QT>;
     Maps maps;
     Shape sh;
     sh.box = kTile;
     while (a.page_size % sh.box != 0) sh.box /= 2;
-    if (encode_fn() == nullptr || !cache_map(&maps.k, a.k_cache, a, D, sh.box) ||
-        !cache_map(&maps.v, a.v_cache, a, D, sh.box) || !new_map(&maps.kn, a.k_new, a, D) ||
+    sh.nodes = nodes_per_tile(a.M, a.H, a.H_kv);
+    if (encode_fn() == nullptr || !query_map(&maps.q, a, D, sh.nodes) || !cache_map(&maps.k, a.k_cache, a, D, sh.box) ||
+        !cache_map(&maps.v, a.v_cache, a, D, sh.box) || !cache_map(&maps.k8, a.k_cache, a, D, 8) ||
+        !cache_map(&maps.v8, a.v_cache, a, D, 8) || !new_map(&maps.kn, a.k_new, a, D) ||
         !new_map(&maps.vn, a.v_new, a, D))
         return cudaErrorInvalidValue;
-    const int rows = a.M * (a.H / a.H_kv);
-    sh.groups = (rows + QT * kTile - 1) / (QT * kTile);
+    sh.groups = (a.M + QT * sh.nodes - 1) / (QT * sh.nodes);
     sh.ctas = sm_count();
     sh.places = static_cast<Place *>(workspace);
     sh.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + place_bytes(sh.ctas));
@@ -772,7 +843,7 @@ template <int D, int QT> cudaError_t run_tc(const TreeAttention &a, void *worksp
     tree_attention_tc_kernel<D, QT><<<sh.ctas, C::THREADS, C::SMEM, stream>>>(maps, a, sh);
     count_launches(1);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const int blocks = ((rows < QT * kTile ? rows : QT * kTile) + 15) / 16;
+    const int blocks = QT == 1 ? (sh.nodes * (a.H / a.H_kv) + 15) / 16 : QT * kTile / 16;
     cudaLaunchAttribute overlap;
     overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     overlap.val.programmaticStreamSerializationAllowed = 1;
@@ -793,19 +864,20 @@ template <int D, int QT> cudaError_t run_tc(const TreeAttention &a, void *worksp
 
 }  // namespace
 
-bool tree_attention_tc_supported(int32_t H_kv, int32_t D, kda_dtype dt, int64_t num_pages, int32_t page_size) {
-    return dt == KDA_BF16 && (D == 64 || D == 128) && page_size % 8 == 0 &&
+bool tree_attention_tc_supported(int32_t H, int32_t H_kv, int32_t D, kda_dtype dt, int64_t num_pages,
+                                 int32_t page_size) {
+    return dt == KDA_BF16 && H / H_kv <= kTile && (D == 64 || D == 128) && page_size % 8 == 0 &&
            num_pages * H_kv * page_size / 8 < INT32_MAX;
 }
 
 size_t tree_attention_tc_partial_bytes(int32_t M, int32_t H, int32_t H_kv, int32_t D) {
-    const int tiles = M * (H / H_kv) <= kTile ? 1 : 2;
+    const int tiles = M <= nodes_per_tile(M, H, H_kv) ? 1 : 2;
     const int ctas = sm_count();
     return place_bytes(ctas) + (size_t)ctas * 2 * tiles * kTile * (D + 2) * 4;
 }
 
 cudaError_t launch_tree_attention_tc(const TreeAttention &a, int32_t D, void *workspace, cudaStream_t stream) {
-    const bool one = a.M * (a.H / a.H_kv) <= kTile;
+    const bool one = a.M <= nodes_per_tile(a.M, a.H, a.H_kv);
     if (D == 64) return one ? run_tc<64, 1>(a, workspace, stream) : run_tc<64, 2>(a, workspace, stream);
     return one ? run_tc<128, 1>(a, workspace, stream) : run_tc<128, 2>(a, workspace, stream);
 }
