@@ -35,14 +35,17 @@
 // size of the output's own rounding); maximum, sum and output sums are fp32.
 //
 // Measured: four caches of about 256,000 tokens, 4 heads of 128, 7 nodes x 8
-// query heads (one row tile): 316 us, 6.6 TB/s, the rate of a copy.  64 caches
-// of 512 .. 8,192 tokens, 8 heads, 16 nodes x 12 query heads (two row tiles):
-// 262 us, 4.6 TB/s and 0.84 PFLOP/s; there a step's four products (8 x 48 + 4 x
-// 64 clocks each row tile: 64 key columns use three quarters of the tensor
-// pipe) and the two softmaxes share about 1,900 clocks, and a unit's end costs
-// some 4 us.  On the way: one product warp for both row tiles 430 -> 330 us,
-// 128 keys per step 330, value tiles prepared by a warp of their own 286.
-// Moving a part of the exponentials to the FMA pipe made it slower (274).
+// query heads (one row tile): 318 us, 6.6 TB/s, the rate of a copy.  64 caches
+// of 512 .. 8,192 tokens, 8 heads, 16 nodes: x 8 query heads (one row tile) 205
+// us, 5.8 TB/s; x 12 (two row tiles) 266 us, 4.5 TB/s; x 16 265 us, 1.1 PFLOP/s.
+// With two row tiles a step's four products (8 x 48 + 4 x 64 clocks each row
+// tile: 64 key columns use three quarters of the tensor pipe) and the two
+// softmaxes share about 1,700 clocks, against the 1,500 that the bytes take; a
+// unit's end costs some 3 us.  On the way (x 12): one warp for all products 430
+// -> 330 us, value tiles prepared by a warp of their own 286, the joining
+// launch overlapped 262 .. 275.  Tried and slower: a part of the exponentials on
+// the FMA pipe (274 against 264), weights under the old maximum while the new
+// one is taken (290 against 266), 128 keys per step (330).
 #include "kda_internal.cuh"
 #include "kda_tc.cuh"
 #include "kda_tree.cuh"
