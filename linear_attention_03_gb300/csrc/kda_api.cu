@@ -481,8 +481,8 @@ size_t kda_tree_attention_workspace_size(kda_dims dims, int32_t H_kv, int32_t N,
     if (check_dims(dims) != KDA_OK || check_tree(N, M, dims.H) != KDA_OK ||
         check_pages(dims, H_kv, 1, page_size, max_pages) != KDA_OK || N == 0)
         return 0;
-    return kStatusBytes + kda::tree_attention_partial_bytes(N, M, dims.H, H_kv, dims.d_k,
-                                                            (kda_dtype)dims.qkv_dtype, page_size, max_pages);
+    return kStatusBytes + kda::tree_attention_partial_bytes(M, dims.H, H_kv, dims.d_k,
+                                                            (kda_dtype)dims.qkv_dtype, page_size);
 }
 
 kda_status kda_tree_attention(const void *q, const void *k_new, const void *v_new, const void *k_cache,

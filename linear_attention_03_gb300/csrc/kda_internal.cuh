@@ -204,8 +204,7 @@ struct TreeAttention {
     int32_t N, M, H, H_kv, num_pages, page_size, max_pages;
     float scale;
 };
-size_t tree_attention_partial_bytes(int32_t N, int32_t M, int32_t H, int32_t H_kv, int32_t D, kda_dtype dt,
-                                    int32_t page_size, int32_t max_pages);
+size_t tree_attention_partial_bytes(int32_t M, int32_t H, int32_t H_kv, int32_t D, kda_dtype dt, int32_t page_size);
 // (both forms set the status word: to zero, or to what the device found)
 cudaError_t launch_tree_attention(const TreeAttention &a, int32_t D, kda_dtype dt, void *workspace,
                                   cudaStream_t stream);

@@ -13,12 +13,8 @@
 //
 // Split: every (sequence, cache head, row group) is a unit of key tiles, the last
 // of which holds the tree, behind the cache's last keys where they leave room.
-// The units' tiles in one line are
-// cut into equal pieces, one per CTA, one CTA per SM: ragged lengths cost no
-// imbalance, and a long cache needs no separate split.  Only the two ends of a
-// piece can be parts of a unit; those go to the workspace as sums, and a second
-// kernel joins them.  The cut depends on the lengths alone, so results repeat
-// bit for bit.
+// The units' tiles in one line are cut into equal pieces, one per CTA, one CTA per
+// SM: ragged lengths cost no imbalance, and a long cache needs no separate split.
 //
 // Roles: warp 0 loads (TMA, one box per page or part of one), warp 1 issues the
 // scores' products, warp 2 the sums', and a warpgroup per row tile does the
@@ -26,13 +22,14 @@
 // go in steps of 64, half a tile, so that a row's scores fit its thread's
 // registers: they are read once, and their columns are free for the next
 // step's product while the softmax runs.  The weights have two buffers of their
-// own, so neither product waits for the other.  Warp 3 looks at every value tile before its product: rows past the last key
-// become zeros, since a weight of zero would not cancel a NaN; in the tree tile
-// also the rows of no node and every value that is not finite, which the rows
-// that see it get added at the end.  The sums are rescaled only when the maximum
-// grows by more than 2^8: weights up to 2^8 lose nothing in bf16 or in the fp32
-// sums.  The weights are rounded to bf16 for the product (2^-9 relative, the
-// size of the output's own rounding); maximum, sum and output sums are fp32.
+// own, so neither product waits for the other.  Warp 3 looks at every value tile
+// before its product: rows past the last key become zeros, since a weight of zero
+// would not cancel a NaN; in the tree tile also the rows of no node and every
+// value that is not finite, which the rows that see it get added at the end.
+// The sums are rescaled only when the maximum grows by more than 2^8: weights up
+// to 2^8 lose nothing in bf16 or in the fp32 sums.  The weights are rounded to
+// bf16 for the product (2^-9 relative, the size of the output's own rounding);
+// maximum, sum and output sums are fp32.
 //
 // Measured: four caches of about 256,000 tokens, 4 heads of 128, 7 nodes x 8
 // query heads (one row tile): 318 us, 6.6 TB/s, the rate of a copy.  64 caches
@@ -49,6 +46,7 @@
 #include "kda_internal.cuh"
 #include "kda_tc.cuh"
 #include "kda_tree.cuh"
+#include "kda_tree_cut.cuh"
 
 #include <cuda.h>
 #include <math.h>
@@ -61,7 +59,6 @@ namespace {
 using namespace tc;
 
 constexpr int kTile = 128;                 // rows per row tile, keys per key tile
-constexpr int kMinTiles = 2;               // key tiles per CTA at least
 constexpr float kGrow = 8.f;               // log2 growth of the maximum that rescales the sums
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -95,11 +92,6 @@ struct Maps {
 };
 
 
-__device__ __forceinline__ int clamped_len(const TreeAttention &a, int64_t n) {
-    const int len = a.cache_lens[n];
-    const int64_t room = (int64_t)a.max_pages * a.page_size;
-    return len < 0 ? 0 : (len > room ? (int)room : len);
-}
 // The last tile of a unit: the cache's last `keys` keys, and the tree from row `tree` on.
 struct Last {
     int keys, tree;
@@ -112,101 +104,18 @@ __device__ __forceinline__ int unit_tiles(int len, int M) {
     return (len + kTile - 1) / kTile + (last_tile(len, M).keys > 0 ? 0 : 1);
 }
 
-// where CTA b's piece of `total` tiles starts
-__device__ __forceinline__ int64_t piece_start(int64_t total, int ctas, int b) {
-    if (total < (int64_t)ctas * kMinTiles) {
-        const int64_t s = (int64_t)b * kMinTiles;
-        return s < total ? s : total;
-    }
-    return total * b / ctas;
-}
-
-// Where a CTA's piece starts: total tiles of the line, and the sequence and unit
-// that hold its first tile.  Each CTA leaves its own in the workspace, with the
-// status it found, for the kernel that joins the pieces.
-struct Place {
-    int64_t total, unit0;   // unit0: where the unit starts on the line
-    int32_t n, r, len;      // sequence, unit within it, its clamped length
-    int32_t status;
+struct Units {
+    static __device__ __forceinline__ int tiles(int len, int M) { return unit_tiles(len, M); }
 };
+using Run = CutRun<Units>;
 struct Shape {
     int32_t box;            // rows per load: the power of two that divides the page size, at most 128
     int32_t nodes;          // nodes per row tile
     int32_t groups;         // row groups (of QT row tiles) per cache head
     int32_t ctas;
     Place *places;          // one per CTA
-    float *part;            // two slots per CTA: D/4 x rows float4, then rows maxima, rows sums
-};
-
-// The whole block calls it; `buf` holds 34 int64 of shared memory.
-__device__ void find_place(const TreeAttention &a, int groups, int ctas, int b, int64_t *buf, Place &out) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-    const int per_seq = a.H_kv * groups;
-    int64_t sum = 0;
-    bool bad = false;
-    for (int n = tid; n < a.N; n += blockDim.x) {
-        const int len = a.cache_lens[n];
-        bad = bad || len < 0 || len > (int64_t)a.max_pages * a.page_size;
-        sum += (int64_t)unit_tiles(clamped_len(a, n), a.M) * per_seq;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) buf[warp] = sum;
-    out.status = __syncthreads_or(bad) != 0 ? KDA_DEVICE_BAD_LENGTH : KDA_DEVICE_OK;
-    int64_t total = 0;
-    for (int w = 0; w < warps; ++w) total += buf[w];
-    __syncthreads();
-    out.total = total;
-    const int64_t at = piece_start(total, ctas, b);
-    if (warp == 0) {
-        // one warp walks the sequences, 32 at a time
-        int64_t base = 0;
-        for (int n0 = 0; n0 < a.N; n0 += 32) {
-            const int n = n0 + lane;
-            const int len = n < a.N ? clamped_len(a, n) : 0;
-            const int64_t mine = n < a.N ? (int64_t)unit_tiles(len, a.M) * per_seq : 0;
-            int64_t run = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t x = __shfl_up_sync(0xffffffffu, run, o);
-                if (lane >= o) run += x;
-            }
-            const int64_t begin = base + run - mine;
-            if (mine > 0 && at >= begin && at < begin + mine) {
-                const int64_t r = (at - begin) / unit_tiles(len, a.M);
-                buf[0] = n;
-                buf[1] = r;
-                buf[2] = begin + r * unit_tiles(len, a.M);
-                buf[3] = len;
-            }
-            base += __shfl_sync(0xffffffffu, run, 31);
-            if (at < base) break;
-        }
-    }
-    __syncthreads();
-    out.n = (int32_t)buf[0];
-    out.r = (int32_t)buf[1];
-    out.unit0 = buf[2];
-    out.len = (int32_t)buf[3];
-}
-
-// A CTA's run through its piece: segments are the parts of units in it.
-struct Run {
-    int64_t left;           // tiles still to do
-    int32_t n, r, len, t0;  // the current unit and its first tile here
-    int32_t tiles;          // tiles of the unit
-    __device__ __forceinline__ int count() const { return left < tiles - t0 ? (int)left : tiles - t0; }
-    __device__ __forceinline__ void advance(const TreeAttention &a, int groups) {
-        left -= count();
-        t0 = 0;
-        if (++r == a.H_kv * groups) {
-            r = 0;
-            if (++n < a.N && left > 0) {
-                len = clamped_len(a, n);
-                tiles = unit_tiles(len, a.M);
-            }
-        }
-    }
+    float *part;            // two slots per CTA: D/4 x rows float4, then rows maxima, rows sums (-1: no node,
+                            // in the part with the unit's last tile)
 };
 
 // 64 bytes of a row, in whole 32-byte sectors where the address allows it
@@ -262,8 +171,8 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
     auto p_col = [](int t, uint32_t i) { return t * 128 + C::TM_P + (i & 1) * 32; };
 
     Place place;
-    find_place(a, sh.groups, sh.ctas, blockIdx.x, reinterpret_cast<int64_t *>(line), place);
-    const int64_t start = piece_start(place.total, sh.ctas, blockIdx.x);
+    find_place<Units>(a, sh.groups, sh.ctas, blockIdx.x, reinterpret_cast<int64_t *>(line), place);
+    const int64_t start = place.start;
     const int64_t stop = piece_start(place.total, sh.ctas, blockIdx.x + 1);
     Place *left = sh.places + blockIdx.x;
     if (tid == 0) *left = place;
@@ -692,7 +601,7 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                 } else {
                     float *ml = part + (size_t)R * D + t * kTile + wg;
                     ml[0] = top;
-                    ml[R] = sum;
+                    ml[R] = run.t0 + cnt == run.tiles && mine == 0 ? -1.f : sum;
                 }
             }
             tc_fence_before();
@@ -720,22 +629,14 @@ tree_attention_tc_join_kernel(const TreeAttention a, const Shape sh) {
     wait_prerequisites();
     if (b == 0) {
         if (blockIdx.y != 0) return;
-        int32_t code = 0;
-        for (int i = threadIdx.x; i < sh.ctas; i += 256) code = max(code, sh.places[i].status);
-        const bool timeout = __syncthreads_or(code == KDA_DEVICE_TIMEOUT) != 0;
-        const bool page = __syncthreads_or(code == KDA_DEVICE_BAD_PAGE) != 0;
-        const bool length = __syncthreads_or(code == KDA_DEVICE_BAD_LENGTH) != 0;
-        if (threadIdx.x == 0)
-            *a.status = timeout ? KDA_DEVICE_TIMEOUT : page ? KDA_DEVICE_BAD_PAGE
-                        : length ? KDA_DEVICE_BAD_LENGTH : KDA_DEVICE_OK;
+        gather_status(sh.places, sh.ctas, a.status);
         return;
     }
     const Place p = sh.places[b];
-    const int64_t at = piece_start(p.total, sh.ctas, b);
-    if (at >= p.total || p.unit0 == at || piece_start(p.total, sh.ctas, b - 1) > p.unit0) return;
+    const int64_t before = sh.places[b - 1].start;
+    if (p.start >= p.total || p.unit0 == p.start || before > p.unit0) return;
     const int64_t end = p.unit0 + unit_tiles(p.len, a.M);
-    int parts = 1;
-    for (int c = b; c < sh.ctas && piece_start(p.total, sh.ctas, c) < end; ++c) ++parts;
+    const int parts = first_past(p.total, sh.ctas, end) - (b - 1);
     const int h = p.r / sh.groups, node0 = p.r % sh.groups * QT * sh.nodes;
     // part i is CTA b - 1 + i's: its last segment for the first, its first one after that
     auto part_of = [&](int i) { return sh.part + (size_t)(2 * (b - 1 + i) + (i == 0 ? 1 : 0)) * R * (D + 2); };
@@ -743,20 +644,35 @@ tree_attention_tc_join_kernel(const TreeAttention a, const Shape sh) {
         const int lr = blockIdx.y * ROWS + e % ROWS, c4 = e / ROWS;
         const int node = node0 + lr / kTile * sh.nodes + lr % kTile / G;
         if (lr >= R || lr % kTile >= sh.nodes * G || node >= a.M) continue;
-        float top = -INFINITY;
-        for (int i = 0; i < parts; ++i) top = fmaxf(top, part_of(i)[(size_t)R * D + lr]);
-        const float from = top == -INFINITY ? 0.f : top;
-        float sum = 0.f;
+        float top = -INFINITY, sum = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int i = 0; i < parts; ++i) {
-            const float *q = part_of(i);
-            const float w = ex2(q[(size_t)R * D + lr] - from);
-            const float4 x = reinterpret_cast<const float4 *>(q)[(size_t)c4 * R + lr];
-            sum += w * q[(size_t)R * D + R + lr];
-            o.x += w * x.x; o.y += w * x.y; o.z += w * x.z; o.w += w * x.w;
+        const bool none = part_of(parts - 1)[(size_t)R * D + R + lr] < 0.f;
+        for (int i0 = 0; i0 < parts; i0 += 8) {
+            // eight parts at a time, so that their reads are under way together
+            float x[8], z[8];
+            float4 y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float *q = part_of(min(i0 + i, parts - 1));
+                x[i] = i0 + i < parts ? q[(size_t)R * D + lr] : -INFINITY;
+                z[i] = q[(size_t)R * D + R + lr];
+                y[i] = reinterpret_cast<const float4 *>(q)[(size_t)c4 * R + lr];
+            }
+            float was = top;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, x[i]);
+            const float from = top == -INFINITY ? 0.f : top, shrink = ex2(was - from);
+            sum *= shrink;
+            o.x *= shrink; o.y *= shrink; o.z *= shrink; o.w *= shrink;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float w = ex2(x[i] - from);
+                if (w != 0.f) {                              // (no key seen: whatever the sums are)
+                    sum += w * z[i];
+                    o.x += w * y[i].x; o.y += w * y[i].y; o.z += w * y[i].z; o.w += w * y[i].w;
+                }
+            }
         }
-        const bool none = tree_line(a.parent + (int64_t)p.n * a.M, node) == 0;
         const float inv = 1.f / sum;
         const int64_t o_row = ((int64_t)p.n * a.M + node) * a.H + h * G + lr % kTile % G;
         *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + o_row * D + 4 * c4) =
@@ -810,16 +726,6 @@ bool new_map(CUtensorMap *map, const void *base, const TreeAttention &a, int D) 
     return make_map(map, base, {64, (cuuint64_t)a.N * a.M, (cuuint64_t)(D / 64), (cuuint64_t)a.H_kv},
                     {(cuuint64_t)a.H_kv * D * 2, 128, (cuuint64_t)D * 2}, {64, 8, (cuuint32_t)(D / 64), 1});
 }
-
-int sm_count() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
-        sms = 152;
-    return sms;
-}
-
-size_t place_bytes(int ctas) { return ((size_t)ctas * sizeof(Place) + 255) / 256 * 256; }
 
 // as many whole nodes as 128 rows hold (their query heads are G rows each)
 int nodes_per_tile(int M, int H, int H_kv) { return std::min(M, kTile / (H / H_kv)); }

@@ -230,6 +230,30 @@ def test_tree_attention_large_scores(kda, dtype):
     assert (np.abs(f64(got[1]) - w_lse) <= 2e-3).all()
 
 
+@pytest.mark.parametrize("N,dtype,page", [(32, F32, 16), (33, F32, 16), (70, F32, 12), (33, BF, 16), (70, BF, 64),
+                                          (70, BF, 12)])
+def test_tree_attention_many_sequences(kda, N, dtype, page):
+    """More sequences than a warp looks at in one step, ragged, some of them empty."""
+    rng = np.random.default_rng(N + page)
+    lens = rng.integers(0, 300, N)
+    lens[::7] = 0
+    x, par = ref.cache_inputs(N, 5, 6, 2, 64, page, lens, dtype, rng), ref.parents(N, 5, "holes", rng)
+    check_attention(run_attention(kda, cu(x), par), ref_attention(x, par, 0.125), dtype, f"{N} sequences")
+
+
+@pytest.mark.parametrize("H", [1, 4, 9])
+def test_tree_attention_fp32_sums_of_one_sign(kda, H):
+    """Values and weights all positive over a long cache: roundings that all point
+    the same way would add up.  Scores err by 3 2^-22 of sum |q k| scale (about 11
+    with these queries) and a few 2^-24 per product of their own size, the sums by
+    some 2^-21: together below 2^-16 = 1.5e-5 of the sum of weighted values."""
+    rng = np.random.default_rng(16 + H)
+    x, par = ref.cache_inputs(1, 5, H, 1, 128, 16, [6000], F32, rng), ref.parents(1, 5, "tree", rng)
+    for name in ("v_cache", "v_new"):
+        x[name] = x[name].abs() + 1
+    check_attention(run_attention(kda, cu(x), par), ref_attention(x, par, 128 ** -0.5), F32, "one sign")
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_tree_attention_scale(kda, dtype):
     rng = np.random.default_rng(13)
