@@ -408,7 +408,7 @@ KDA_API size_t kda_tree_attention_workspace_size(kda_dims dims, int32_t H_kv, in
  *          the buffers)
  * Any page_size serves; bf16 with d = 64 or 128 and pages of whole groups of
  * eight tokens takes the tcgen05 path, everything else products of tf32 parts
- * (fp32 factors in two parts each: 2^-21, and an infinity among the keys or
+ * (fp32 factors in two parts each: 2^-23, and an infinity among the keys or
  * values that an fp32 row sees makes its results NaN).
  * N * M * H must not exceed 2^29.  The same call gives the same bits.
  */

@@ -16,24 +16,26 @@
 // a tile are dealt to two warps for each sixteen rows, to four where there are two
 // times sixteen rows or fewer.  The units' tiles are cut evenly over the CTAs.
 //
-// Products: mma.sync m16n8k8 on tf32 operands.  An fp32 factor is a part of eleven
-// bits and a rest of eleven, x = x1 + x2 + 2^-21 x; x1 y1 + x1 y2 + x2 y1 is taken,
-// x2 y2 (2^-22) is left out.  The tensor cores cut the sums that they add to, so
-// the scores' small terms have a sum of their own, and the output sums run over
-// one tile there and over the tiles in fp32 registers.  bf16 factors are exact in
-// tf32: one product for the scores, two (the weights' parts) for the sums.  An
-// infinity among the keys or values that a row sees gives NaN (inf - inf in the
-// split).
+// Products: mma.sync m16n8k8 on tf32 operands.  An fp32 factor is the nearest tf32
+// number and a rest of eleven bits, x = x1 + x2 to 2^-23; x1 y1 + x1 y2 + x2 y1 is
+// taken, x2 y2 (2^-24) is left out.  The tensor cores cut the sums that they add
+// to: so sixteen channels' large terms at a time are added up in fp32 registers,
+// as are the tiles' output sums, and the scores' small terms have a sum of their
+// own.  Against 64 bits the outputs err by 1.2e-7 to 3.6e-7 of their RMS (an fp32
+// product and softmax by 5.7e-7; with cut parts and scores summed in the tensor
+// cores it was 1.1e-6, 7% faster).  bf16 factors are exact in tf32: one product for
+// the scores, two (the weights' parts) for the sums.  An infinity among the keys
+// or values that an fp32 row sees gives NaN (inf - inf in the rest).
 //
 // Measured, fp32, from a graph: five caches of up to 3,001 tokens, 4 heads of 64,
-// 11 nodes x 3 query heads 24 us; sixteen of 512 .. 8,192 tokens 92 us; the same
-// with 8 heads of 128 and 16 x 4 rows 379 us, where the products alone take 186
+// 11 nodes x 3 query heads 25 us; sixteen of 512 .. 8,192 tokens 93 us; the same
+// with 8 heads of 128 and 16 x 4 rows 407 us, where the products alone take 186
 // (8 clocks each) and the bytes 85; two of about 62,000 tokens, 4 heads of 128,
-// 7 x 8 rows 359 us (products 168, bytes 77).  The rest is what eight to sixteen
+// 7 x 8 rows 380 us (products 168, bytes 77).  The rest is what eight to sixteen
 // warps per SM do not hide.  On CUDA cores the four took 47, 309, 1,247 and 1,160
 // us with a row and a key per lane, 35, 151, 820 and 572 with two rows x four keys
-// per lane, all of it waiting for shared memory.  With as many splits for every
-// sequence instead of the even cut 33, 125, 472 and 397.
+// per lane, all of it waiting for shared memory.  As many splits for every sequence
+// instead of the even cut took 1.4 times as long with ragged lengths.
 #include "kda_internal.cuh"
 #include "kda_tc.cuh"
 #include "kda_tree.cuh"
@@ -116,7 +118,13 @@ template <int W> __device__ __forceinline__ void read_run(const __nv_bfloat16 *p
     }
 }
 
-__device__ __forceinline__ float tf32_of(float x) { return __uint_as_float(__float_as_uint(x) & 0xffffe000u); }
+// x = part + rest: the nearest tf32 number, and what is left, cut to eleven bits
+__device__ __forceinline__ float part_of(float x) {
+    return __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u);
+}
+__device__ __forceinline__ float rest_of(float x, float part) {
+    return __uint_as_float(__float_as_uint(x - part) & 0xffffe000u);
+}
 
 // Four results: o by, or zeros.
 __device__ __forceinline__ void store4(float *p, bool none, float4 o, float by) {
@@ -158,8 +166,9 @@ tree_attention_kernel(const TreeAttention a, const Shape sh) {
     constexpr bool RESTS = kRests<Tin, WK>;
     constexpr int LK = kLdk<D>, LV = kLdv<Tin, D>, LO = D + 4;
     constexpr int NT = kKeys / 8 / WK;                      // groups of eight keys per warp and tile
-    // columns of a value per read; four for d = 128 keep too many registers (457 us for 379)
+    // columns of a value per read; four for d = 128 keep too many registers (20% slower)
     constexpr int W = D == 16 || D == 128 ? 2 : 4, E = D / 8 / W;
+    constexpr int kAtOnce = D == 128 ? 1 : 2;               // (likewise, 8%)
     extern __shared__ __align__(16) unsigned char smem[];
     Tin *sk = reinterpret_cast<Tin *>(smem), *sv = sk + 2 * kKeys * LK;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
@@ -239,8 +248,8 @@ tree_attention_kernel(const TreeAttention a, const Shape sh) {
             float x1[8], x2[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                x1[e] = RESTS ? tf32_of(x[e]) : x[e];
-                x2[e] = tf32_of(x[e] - x1[e]);
+                x1[e] = RESTS ? part_of(x[e]) : x[e];
+                x2[e] = rest_of(x[e], x1[e]);
             }
             Elem<float>::store8(sq + i / (D / 8) * LK + c, x1);
             if (RESTS) Elem<float>::store8(sq_rest + i / (D / 8) * LK + c, x2);
@@ -281,7 +290,7 @@ tree_attention_kernel(const TreeAttention a, const Shape sh) {
             for (int i = 0; i < NT; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s1[i][e] = s2[i][e] = 0.f;
-#pragma unroll 2
+#pragma unroll kAtOnce
             for (int c = 0; c < D; c += 16) {
                 float qa[4], qb[4], ra[4], rb[4];
                 read_run<4>(sq + my_q + c, qa);
@@ -293,29 +302,32 @@ tree_attention_kernel(const TreeAttention a, const Shape sh) {
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
                         const float xa = qa[y], xb = qb[y];
-                        qa[y] = tf32_of(xa);
-                        qb[y] = tf32_of(xb);
-                        ra[y] = tf32_of(xa - qa[y]);
-                        rb[y] = tf32_of(xb - qb[y]);
+                        qa[y] = part_of(xa);
+                        qb[y] = part_of(xb);
+                        ra[y] = rest_of(xa, qa[y]);
+                        rb[y] = rest_of(xb, qb[y]);
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
-                    float x[4];
+                    float x[4], sum16[4];                   // the large terms of these channels
                     read_run<4>(tk + 8 * i * LK + c, x);
 #pragma unroll
                     for (int y = 0; y < 4; y += 2) {
                         const float f[4] = {qa[y], qb[y], qa[y + 1], qb[y + 1]};
+                        const float x0 = SPLIT ? part_of(x[y]) : x[y], x1 = SPLIT ? part_of(x[y + 1]) : x[y + 1];
+                        if (y == 0)
+                            mma_tf32_first(sum16, f, x0, x1);
+                        else
+                            mma_tf32(sum16, f, x0, x1);
                         if (SPLIT) {
                             const float f2[4] = {ra[y], rb[y], ra[y + 1], rb[y + 1]};
-                            const float x0 = tf32_of(x[y]), x1 = tf32_of(x[y + 1]);
-                            mma_tf32(s1[i], f, x0, x1);
-                            mma_tf32(s2[i], f, tf32_of(x[y] - x0), tf32_of(x[y + 1] - x1));
+                            mma_tf32(s2[i], f, rest_of(x[y], x0), rest_of(x[y + 1], x1));
                             mma_tf32(s2[i], f2, x0, x1);
-                        } else {
-                            mma_tf32(s1[i], f, x[y], x[y + 1]);
                         }
                     }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s1[i][e] += sum16[e];
                 }
             }
             uint32_t seen[2];                                   // which of the tile's keys the row sees
@@ -359,8 +371,8 @@ tree_attention_kernel(const TreeAttention a, const Shape sh) {
                 const float w[4] = {s1[i][0], s1[i][2], s1[i][1], s1[i][3]};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    p1[i][e] = tf32_of(w[e]);
-                    p2[i][e] = tf32_of(w[e] - p1[i][e]);
+                    p1[i][e] = part_of(w[e]);
+                    p2[i][e] = rest_of(w[e], p1[i][e]);
                 }
             }
             bool odd = false;                                   // a value that is no number
@@ -382,12 +394,12 @@ tree_attention_kernel(const TreeAttention a, const Shape sh) {
                                 x[j] = fx ? x[j] : 0.f;
                                 z[j] = fz ? z[j] : 0.f;
                             }
-                            const float x1 = SPLIT ? tf32_of(x[j]) : x[j], z1 = SPLIT ? tf32_of(z[j]) : z[j];
+                            const float x1 = SPLIT ? part_of(x[j]) : x[j], z1 = SPLIT ? part_of(z[j]) : z[j];
                             if (i == 0)
                                 mma_tf32_first(o[j], p2[i], x1, z1);
                             else
                                 mma_tf32(o[j], p2[i], x1, z1);
-                            if (SPLIT) mma_tf32(o[j], p1[i], tf32_of(x[j] - x1), tf32_of(z[j] - z1));
+                            if (SPLIT) mma_tf32(o[j], p1[i], rest_of(x[j], x1), rest_of(z[j], z1));
                             mma_tf32(o[j], p1[i], x1, z1);
                         }
                     }
@@ -498,20 +510,20 @@ tree_attention_join_kernel(const TreeAttention a, const Shape sh) {
     const int parts = first_past(p.total, sh.ctas, end) - (b - 1);
     const int h = p.r / sh.groups;
     // part i is CTA b - 1 + i's: its last unit for the first, its first one after that
-    auto part_of = [&](int i) { return sh.part + (size_t)(2 * (b - 1 + i) + (i == 0 ? 1 : 0)) * crows * (D + 2); };
+    auto piece = [&](int i) { return sh.part + (size_t)(2 * (b - 1 + i) + (i == 0 ? 1 : 0)) * crows * (D + 2); };
     for (int e = threadIdx.x; e < kRowsPerWarp * (D / 4); e += 256) {
         const int lr = blockIdx.y * kRowsPerWarp + e / (D / 4), c = e % (D / 4) * 4, row = p.r % sh.groups * crows + lr;
         if (row >= a.M * G) continue;
         float top = -INFINITY, sum = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        const bool none = part_of(parts - 1)[crows * D + crows + lr] < 0.f;
+        const bool none = piece(parts - 1)[crows * D + crows + lr] < 0.f;
         for (int i0 = 0; i0 < parts; i0 += 8) {
             // eight parts at a time, so that their reads are under way together
             float x[8], z[8];
             float4 y[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float *q = part_of(min(i0 + i, parts - 1));
+                const float *q = piece(min(i0 + i, parts - 1));
                 x[i] = i0 + i < parts ? q[crows * D + lr] : -INFINITY;
                 z[i] = q[crows * D + crows + lr];
                 y[i] = *reinterpret_cast<const float4 *>(q + lr * D + c);
