@@ -20,133 +20,237 @@
 namespace kda {
 namespace {
 
-constexpr int kNodeBlock = 8;   // nodes whose products share one pass over S_0
+constexpr int kNodeBlock = 4;   // nodes of a thread's sums
 
-template <int D> struct TreeCfg {
-    static constexpr int THREADS = 256;               // for the line products; a thread per state column solves
-    static size_t smem(int M) {
-        const size_t rows = (size_t)((M + kNodeBlock - 1) / kNodeBlock) * kNodeBlock;
-        return rows * D * 4 * 5 + (size_t)M * M * 8 + (size_t)M * 16;
-    }
+// The fp32 form: any type and head size.  A unit is a (sequence, head); its threads
+// have four state columns each, for four of up to 32 nodes at a time.  Small units
+// share a CTA.
+struct TreeCut {
+    int nodes, threads, units;  // nodes at a time; threads per unit; units per CTA
 };
+// A unit's shared memory: decays, keys (later v - X_k), and the products' operands E k and
+// E q; the line products and W's rows by steps up the line, the nodes reached; lines,
+// parents, beta.
+__host__ __device__ constexpr size_t tree_unit_bytes(int M, int D) {
+    const size_t rows = (M + kNodeBlock - 1) / kNodeBlock * kNodeBlock;
+    return (rows * D * 16 + (size_t)M * M * 13 + (size_t)M * 16 + 15) / 16 * 16;
+}
 
-// One CTA per (sequence, head): fp32 arithmetic throughout.  The line products
-// first (a warp per node, lanes over channels), then per block of eight nodes
-// one pass over S_0 (thread c reads column c) and the solve, whose columns are
-// independent.
+inline TreeCut tree_cut(int M, int D) {
+    int groups = 1;
+    while (groups * kNodeBlock < M && groups < 8) groups *= 2;
+    const int threads = D / 4 * groups < 8 ? 8 : D / 4 * groups;
+    int units = threads >= 128 ? 1 : 128 / threads;
+    while (units > 1 && units * tree_unit_bytes(M, D) > 100 * 1024) units /= 2;
+    return {groups * kNodeBlock, threads, units};
+}
+
+__device__ __forceinline__ float2 load2(const float *p) { return __ldg(reinterpret_cast<const float2 *>(p)); }
+__device__ __forceinline__ float2 load2(const __nv_bfloat16 *p) {
+    const uint32_t u = __ldg(reinterpret_cast<const uint32_t *>(p));
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ void store4(float *p, float2 lo, float2 hi) {
+    *reinterpret_cast<float4 *>(p) = make_float4(lo.x, lo.y, hi.x, hi.y);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, float2 lo, float2 hi) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(tc::pack_bf16x2(lo.x, lo.y), tc::pack_bf16x2(hi.x, hi.y));
+}
+
+// Line products and W's rows by eight lanes per node, the sums by threads of four
+// nodes x four columns: per four state rows four 16-byte reads of the state and
+// eight of the operands feed 64 paired multiply-adds.  Then o = X_q + W (v - X_k)
+// along the lines.
+// Measured, 16 nodes: 64 x 48 fp32 states of 128 x 128 127 us; 128 x 64 of 64 x 64,
+// bf16, 123 us; 128 x 96 of 32 x 32 104 us, of 16 x 16 77 us (218, 300, 330, 243
+// with a warp per node and a thread per column and eight nodes).
 template <typename Tin, int D>
-__global__ void __launch_bounds__(TreeCfg<D>::THREADS)
+__global__ void __launch_bounds__(256, 2)
 decode_tree_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin *__restrict__ v,
                    const float *__restrict__ g, const float *__restrict__ beta,
-                   const float *__restrict__ state, const int32_t *__restrict__ parent, int32_t M,
-                   int32_t H, Tin *__restrict__ out) {
-    constexpr int THREADS = TreeCfg<D>::THREADS;
-    constexpr int EPL = D < 32 ? 1 : D / 32;          // channels per lane of a warp
+                   const float *__restrict__ state, const int32_t *__restrict__ parent, int64_t all, int32_t M,
+                   int32_t H, int32_t threads, int32_t at_once, Tin *__restrict__ out) {
+    constexpr int CQ = D / 4;
+    constexpr int PW = D / 8 < 4 ? D / 8 : 4, NP = D / 8 / PW;   // a walking lane's channels: NP runs of PW
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    const int rows = (M + kNodeBlock - 1) / kNodeBlock * kNodeBlock;
-    float *kE = reinterpret_cast<float *>(smem_raw);  // E_m k_m
-    float *qE = kE + rows * D;                        // E_m q_m
-    float *kk = qE + rows * D;
-    float *al = kk + rows * D;
-    float *U = al + rows * D;
-    float2 *AB = reinterpret_cast<float2 *>(U + rows * D);   // ((D_mj k_m).k_j, (D_mj q_m).k_j)
-    uint64_t *line = reinterpret_cast<uint64_t *>(AB + M * M);
-    int32_t *par = reinterpret_cast<int32_t *>(line + M);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t n = blockIdx.x / H;
-    const int h = blockIdx.x % H;
+    const int tid = threadIdx.x % threads, lane = threadIdx.x & 31, l8 = lane & 7;
+    const unsigned group = 0xffu << (lane & 24);
+    const int64_t unit = (int64_t)blockIdx.x * (blockDim.x / threads) + threadIdx.x / threads;
+    const bool live = unit < all;
+    const int rows = (M + kNodeBlock - 1) / kNodeBlock * kNodeBlock, walkers = threads / 8, w8 = tid >> 3;
+    float *kE = reinterpret_cast<float *>(smem_raw + tree_unit_bytes(M, D) * (threadIdx.x / threads));
+    float *qE = kE + rows * D, *al = qE + rows * D, *kk = al + rows * D, *y = kk;
+    uint64_t *line = reinterpret_cast<uint64_t *>(kk + rows * D);
+    float2 *AB = reinterpret_cast<float2 *>(line + M);
+    float *W = reinterpret_cast<float *>(AB + M * M);
+    int32_t *par = reinterpret_cast<int32_t *>(W + M * M);
+    float *bet = reinterpret_cast<float *>(par + M);
+    uint8_t *up = reinterpret_cast<uint8_t *>(bet + M);
+    const int64_t n = live ? unit / H : 0, h = live ? unit % H : 0;
+    const int64_t row0 = n * M * H + h;                // row of node m: row0 + m H
+    const int m_end = live ? M : 0;
 
-    for (int m = tid; m < M; m += THREADS) par[m] = parent[n * M + m];
-    for (int i = tid; i < rows * D; i += THREADS) {
-        const int m = i / D, c = i % D;
-        const int64_t at = ((n * M + m) * H + h) * D + c;
-        kk[i] = m < M ? Elem<Tin>::load(k + at) : 0.f;
-        al[i] = m < M ? __expf(g[at]) : 0.f;
-        kE[i] = qE[i] = 0.f;
+    for (int m = tid; m < m_end; m += threads) {
+        par[m] = parent[n * M + m];
+        bet[m] = __ldg(beta + row0 + (int64_t)m * H);
     }
-    __syncthreads();
-    for (int m = tid; m < M; m += THREADS) line[m] = tree_line(par, m);
-    __syncthreads();
-    for (int m = warp; m < M; m += THREADS / 32) {
-        if (line[m] == 0) continue;
-        float kd[EPL], qd[EPL];
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) {
-            const int c = lane + 32 * e;
-            kd[e] = c < D ? kk[m * D + c] : 0.f;
-            qd[e] = c < D ? Elem<Tin>::load(q + ((n * M + m) * H + h) * D + c) : 0.f;
-        }
-        for (int j = m; j >= 0; j = par[j]) {
-            float a = 0.f, b = 0.f;
-#pragma unroll
-            for (int e = 0; e < EPL; ++e) {
-                const int c = lane + 32 * e;
-                const float kj = c < D ? kk[j * D + c] : 0.f, aj = c < D ? al[j * D + c] : 0.f;
-                a += kd[e] * kj;
-                b += qd[e] * kj;
-                kd[e] *= aj;
-                qd[e] *= aj;
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                a += __shfl_xor_sync(0xffffffffu, a, o);
-                b += __shfl_xor_sync(0xffffffffu, b, o);
-            }
-            if (lane == 0) AB[m * M + j] = make_float2(a, b);
-        }
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) {
-            const int c = lane + 32 * e;
-            if (c < D) {
-                kE[m * D + c] = kd[e];
-                qE[m * D + c] = qd[e];
-            }
-        }
-    }
-    __syncthreads();
-    if (tid >= D) return;
-    const int c = tid;
-    const float *S = state + (size_t)blockIdx.x * D * D + c;
-    for (int m0 = 0; m0 < M; m0 += kNodeBlock) {
-        float xk[kNodeBlock], xq[kNodeBlock];
-#pragma unroll
-        for (int b = 0; b < kNodeBlock; ++b) xk[b] = xq[b] = 0.f;
 #pragma unroll 2
-        for (int i = 0; i < D; i += 4) {
-            float s[4];
+    for (int i = tid; i < m_end * (D / 8); i += threads) {
+        const int64_t at = (row0 + (int64_t)(i / (D / 8)) * H) * D + i % (D / 8) * 8;
+        float x[8], f[8];
+        Elem<float>::load8(g + at, x);
+        Elem<Tin>::load8(k + at, f);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] = __ldg(S + (size_t)(i + e) * D);
+        for (int e = 0; e < 8; ++e) x[e] = __expf(x[e]);
+        Elem<float>::store8(al + 8 * i, x);
+        Elem<float>::store8(kk + 8 * i, f);
+    }
+    __syncthreads();
+    for (int m = w8; m < (live ? rows : 0); m += walkers) {
+        float2 kd[NP][PW / 2], qd[NP][PW / 2];
+        auto get = [&](const float *from, float2 (&x)[NP][PW / 2]) {
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                if constexpr (PW == 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(from + 32 * p + 4 * l8);
+                    x[p][0] = make_float2(f.x, f.y);
+                    x[p][1] = make_float2(f.z, f.w);
+                } else {
+                    x[p][0] = *reinterpret_cast<const float2 *>(from + 2 * l8);
+                }
+            }
+        };
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+#pragma unroll
+            for (int e = 0; e < PW / 2; ++e) {
+                kd[p][e] = qd[p][e] = make_float2(0.f, 0.f);
+                if (m < M) qd[p][e] = load2(q + (row0 + (int64_t)m * H) * D + 8 * PW * p + PW * l8 + 2 * e);
+            }
+        if (m < M) get(kk + m * D, kd);
+        uint64_t on = 0;
+        int at = m < M ? m : -1, steps = 0;
+        bool whole = false;                            // the walk ended below the prefix
+        while (at >= 0) {
+            float2 kj[NP][PW / 2], aj[NP][PW / 2], a2 = make_float2(0.f, 0.f), b2 = a2;
+            const int next = par[at];
+            get(kk + at * D, kj);
+            get(al + at * D, aj);
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+#pragma unroll
+                for (int e = 0; e < PW / 2; ++e) {
+                    a2 = tc::f2fma(kd[p][e], kj[p][e], a2);
+                    b2 = tc::f2fma(qd[p][e], kj[p][e], b2);
+                    kd[p][e] = tc::f2mul(kd[p][e], aj[p][e]);
+                    qd[p][e] = tc::f2mul(qd[p][e], aj[p][e]);
+                }
+            const float a = a2.x + a2.y, b = b2.x + b2.y;
+            // lanes 0-3 of the group sum the k products, lanes 4-7 the q products
+            float x = (l8 < 4 ? a : b) + __shfl_xor_sync(group, l8 < 4 ? b : a, 4);
+            x += __shfl_xor_sync(group, x, 2);
+            x += __shfl_xor_sync(group, x, 1);
+            if ((l8 & 3) == 0) reinterpret_cast<float *>(AB + m * M + steps)[l8 >> 2] = x;
+            if (l8 == 1) up[m * M + steps] = (uint8_t)at;
+            on |= uint64_t{1} << at;
+            ++steps;
+            whole = next == -1;
+            at = next < at ? next : -2;
+        }
+        if (m < M && l8 == 0) line[m] = whole ? on : 0;
+        auto put = [&](float *to, const float2 (&x)[NP][PW / 2]) {
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                if constexpr (PW == 4)
+                    *reinterpret_cast<float4 *>(to + 32 * p + 4 * l8) = make_float4(x[p][0].x, x[p][0].y, x[p][1].x, x[p][1].y);
+                else
+                    *reinterpret_cast<float2 *>(to + 2 * l8) = x[p][0];
+            }
+        };
+        put(kE + m * D, kd);                           // (of no node: never read into a result)
+        put(qE + m * D, qd);
+    }
+    __syncthreads();
+
+    // The rows of W by steps up the line: z starts as the q products; a step's w leaves
+    // z's later entries less its k products.  Eight lanes per node, lane l8 the steps
+    // l8, l8 + 8, ...
+    for (int m = w8; m < m_end; m += walkers) {
+        const int steps = __popcll((long long)line[m]);
+        float z[kMaxTreeNodes / 8];
+#pragma unroll
+        for (int r = 0; r < kMaxTreeNodes / 8; ++r) z[r] = 8 * r + l8 < steps ? AB[m * M + 8 * r + l8].y : 0.f;
+#pragma unroll
+        for (int r = 0; r < kMaxTreeNodes / 8; ++r) {
+            for (int s8 = 0; s8 < 8 && 8 * r + s8 < steps; ++s8) {
+                const int s = 8 * r + s8, j = up[m * M + s];
+                const float w = __shfl_sync(group, z[r], s8, 8) * bet[j];
+                const float2 *ab = AB + j * M - s;
+#pragma unroll
+                for (int i = r; i < kMaxTreeNodes / 8; ++i) {
+                    const int t = 8 * i + l8;
+                    if (t > s && t < steps) z[i] -= w * ab[t].x;
+                }
+                if (l8 == 0) W[m * M + s] = w;
+            }
+        }
+    }
+
+    const int c = tid % CQ * 4, mine = tid / CQ * kNodeBlock;
+    const float *S = state + unit * D * D + c;
+    for (int m0 = 0; m0 < M; m0 += at_once) {
+        const int m1 = m0 + mine;                      // this thread's nodes: m1 .. m1 + 3
+        float2 xk[kNodeBlock][2], xq[kNodeBlock][2];
+#pragma unroll
+        for (int b = 0; b < kNodeBlock; ++b) xk[b][0] = xk[b][1] = xq[b][0] = xq[b][1] = make_float2(0.f, 0.f);
+        if (m1 < m_end && mine < at_once) {
+            const float *ke = kE + m1 * D, *qe = qE + m1 * D;
+#pragma unroll 2
+            for (int i = 0; i < D; i += 4) {
+                float4 s4[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s4[e] = __ldg(reinterpret_cast<const float4 *>(S + (i + e) * D));
+#pragma unroll
+                for (int b = 0; b < kNodeBlock; ++b) {
+                    const float4 x = *reinterpret_cast<const float4 *>(ke + b * D + i),
+                                 z = *reinterpret_cast<const float4 *>(qe + b * D + i);
+                    const float xs[4] = {x.x, x.y, x.z, x.w}, zs[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 lo = make_float2(s4[e].x, s4[e].y), hi = make_float2(s4[e].z, s4[e].w);
+                        xk[b][0] = tc::f2fma(make_float2(xs[e], xs[e]), lo, xk[b][0]);
+                        xk[b][1] = tc::f2fma(make_float2(xs[e], xs[e]), hi, xk[b][1]);
+                        xq[b][0] = tc::f2fma(make_float2(zs[e], zs[e]), lo, xq[b][0]);
+                        xq[b][1] = tc::f2fma(make_float2(zs[e], zs[e]), hi, xq[b][1]);
+                    }
+                }
+            }
 #pragma unroll
             for (int b = 0; b < kNodeBlock; ++b) {
-                const float4 ke = *reinterpret_cast<const float4 *>(kE + (m0 + b) * D + i);
-                const float4 qe = *reinterpret_cast<const float4 *>(qE + (m0 + b) * D + i);
-                xk[b] += ke.x * s[0] + ke.y * s[1] + ke.z * s[2] + ke.w * s[3];
-                xq[b] += qe.x * s[0] + qe.y * s[1] + qe.z * s[2] + qe.w * s[3];
+                if (m1 + b >= M) break;
+                const Tin *from = v + (row0 + (int64_t)(m1 + b) * H) * D + c;
+                const float2 lo = load2(from), hi = load2(from + 2);
+                *reinterpret_cast<float4 *>(y + (m1 + b) * D + c) =
+                    make_float4(lo.x - xk[b][0].x, lo.y - xk[b][0].y, hi.x - xk[b][1].x, hi.y - xk[b][1].y);
             }
         }
+        __syncthreads();                               // nodes above are in this pass or an earlier one
+        if (m1 < m_end && mine < at_once) {
 #pragma unroll
-        for (int b = 0; b < kNodeBlock; ++b) {
-            const int m = m0 + b;
-            if (m >= M) break;
-            const int64_t row = (n * M + m) * H + h;
-            uint64_t up = line[m];
-            if (up == 0) {
-                Elem<Tin>::store(out + row * D + c, 0.f);
-                continue;
+            for (int b = 0; b < kNodeBlock; ++b) {
+                const int m = m1 + b;
+                if (m >= M) break;
+                const int steps = __popcll((long long)line[m]);
+                float2 lo = xq[b][0], hi = xq[b][1];
+                for (int s = 0; s < steps; ++s) {
+                    const float w = W[m * M + s];
+                    const float4 yj = *reinterpret_cast<const float4 *>(y + up[m * M + s] * D + c);
+                    lo = tc::f2fma(make_float2(w, w), make_float2(yj.x, yj.y), lo);
+                    hi = tc::f2fma(make_float2(w, w), make_float2(yj.z, yj.w), hi);
+                }
+                if (steps == 0) lo = hi = make_float2(0.f, 0.f);
+                store4(out + (row0 + (int64_t)m * H) * D + c, lo, hi);
             }
-            float x = xk[b], o = xq[b];
-            up &= ~(uint64_t{1} << m);
-            while (up != 0) {
-                const int j = __ffsll((long long)up) - 1;
-                up &= up - 1;
-                const float2 ab = AB[m * M + j];
-                const float uj = U[j * D + c];
-                x += ab.x * uj;
-                o += ab.y * uj;
-            }
-            const float u = beta[row] * (Elem<Tin>::load(v + row * D + c) - x);
-            U[m * D + c] = u;
-            Elem<Tin>::store(out + row * D + c, o + AB[m * M + m].y * u);
         }
     }
 }
@@ -715,11 +819,14 @@ cudaError_t run_tree(const void *q, const void *k, const void *v, const float *g
                      const float *state, const int32_t *parent, int32_t N, int32_t M, int32_t H,
                      void *out, cudaStream_t stream) {
     static std::atomic<uint64_t> smem_set{0};
-    cudaError_t e = allow_dynamic_smem(decode_tree_kernel<Tin, D>, TreeCfg<D>::smem(kMaxTreeNodes), smem_set);
+    const TreeCut c = tree_cut(M, D);
+    const int64_t units = (int64_t)N * H;
+    cudaError_t e = allow_dynamic_smem(decode_tree_kernel<Tin, D>, 227 * 1024, smem_set);
     if (e != cudaSuccess) return e;
-    decode_tree_kernel<Tin, D><<<(unsigned)N * (unsigned)H, TreeCfg<D>::THREADS, TreeCfg<D>::smem(M), stream>>>(
+    decode_tree_kernel<Tin, D><<<(unsigned)((units + c.units - 1) / c.units), c.threads * c.units,
+                                 tree_unit_bytes(M, D) * c.units, stream>>>(
         static_cast<const Tin *>(q), static_cast<const Tin *>(k), static_cast<const Tin *>(v), g, beta,
-        state, parent, M, H, static_cast<Tin *>(out));
+        state, parent, units, M, H, c.threads, c.nodes, static_cast<Tin *>(out));
     count_launches(1);
     return cudaGetLastError();
 }
