@@ -61,9 +61,10 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float2 lo, float2 hi) {
 // nodes x four columns: per four state rows four 16-byte reads of the state and
 // eight of the operands feed 64 paired multiply-adds.  Then o = X_q + W (v - X_k)
 // along the lines.
-// Measured, 16 nodes: 64 x 48 fp32 states of 128 x 128 127 us; 128 x 64 of 64 x 64,
-// bf16, 123 us; 128 x 96 of 32 x 32 104 us, of 16 x 16 77 us (218, 300, 330, 243
-// with a warp per node and a thread per column and eight nodes).
+// Measured, 16 nodes: 64 x 48 fp32 states of 128 x 128 109 us (4 nodes 52); 128 x 64
+// of 64 x 64 112; bf16, 128 x 96 of 16 x 16 77 us.  Issue slots are 40% busy at the
+// 16 warps per SM that the registers allow (three CTAs of 256: 154 us for 112).  With
+// a warp per node, a thread per column and eight nodes it took 218, 288 and 243.
 template <typename Tin, int D>
 __global__ void __launch_bounds__(256, 2)
 decode_tree_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin *__restrict__ v,
@@ -90,10 +91,24 @@ decode_tree_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const T
     const int64_t row0 = n * M * H + h;                // row of node m: row0 + m H
     const int m_end = live ? M : 0;
 
-    for (int m = tid; m < m_end; m += threads) {
-        par[m] = parent[n * M + m];
-        bet[m] = __ldg(beta + row0 + (int64_t)m * H);
-    }
+    // a state that several threads read comes to the L2 meanwhile (read once, it is only
+    // slower: 61 us for 52 with 64 x 48 states, four nodes), and a thread's first node is
+    // asked for before anything is waited for
+    if (tid == 0 && live && at_once > kNodeBlock)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(state + unit * D * D), "r"(D * D * 4)
+                     : "memory");
+    const int32_t par_in = tid < m_end ? parent[n * M + tid] : 0;
+    const float bet_in = tid < m_end ? __ldg(beta + row0 + (int64_t)tid * H) : 0.f;
+    float2 qd[NP][PW / 2];
+    auto load_q = [&](int m) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+#pragma unroll
+            for (int e = 0; e < PW / 2; ++e)
+                qd[p][e] = m < m_end ? load2(q + (row0 + (int64_t)m * H) * D + 8 * PW * p + PW * l8 + 2 * e)
+                                     : make_float2(0.f, 0.f);
+    };
+    load_q(w8);
 #pragma unroll 2
     for (int i = tid; i < m_end * (D / 8); i += threads) {
         const int64_t at = (row0 + (int64_t)(i / (D / 8)) * H) * D + i % (D / 8) * 8;
@@ -105,9 +120,13 @@ decode_tree_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const T
         Elem<float>::store8(al + 8 * i, x);
         Elem<float>::store8(kk + 8 * i, f);
     }
+    for (int m = tid; m < m_end; m += threads) {
+        par[m] = m == tid ? par_in : parent[n * M + m];
+        bet[m] = m == tid ? bet_in : __ldg(beta + row0 + (int64_t)m * H);
+    }
     __syncthreads();
     for (int m = w8; m < (live ? rows : 0); m += walkers) {
-        float2 kd[NP][PW / 2], qd[NP][PW / 2];
+        float2 kd[NP][PW / 2];
         auto get = [&](const float *from, float2 (&x)[NP][PW / 2]) {
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
@@ -123,10 +142,7 @@ decode_tree_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const T
 #pragma unroll
         for (int p = 0; p < NP; ++p)
 #pragma unroll
-            for (int e = 0; e < PW / 2; ++e) {
-                kd[p][e] = qd[p][e] = make_float2(0.f, 0.f);
-                if (m < M) qd[p][e] = load2(q + (row0 + (int64_t)m * H) * D + 8 * PW * p + PW * l8 + 2 * e);
-            }
+            for (int e = 0; e < PW / 2; ++e) kd[p][e] = make_float2(0.f, 0.f);
         if (m < M) get(kk + m * D, kd);
         uint64_t on = 0;
         int at = m < M ? m : -1, steps = 0;
@@ -162,14 +178,24 @@ decode_tree_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const T
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
                 if constexpr (PW == 4)
-                    *reinterpret_cast<float4 *>(to + 32 * p + 4 * l8) = make_float4(x[p][0].x, x[p][0].y, x[p][1].x, x[p][1].y);
+                    store4(to + 32 * p + 4 * l8, x[p][0], x[p][1]);
                 else
                     *reinterpret_cast<float2 *>(to + 2 * l8) = x[p][0];
             }
         };
         put(kE + m * D, kd);                           // (of no node: never read into a result)
         put(qE + m * D, qd);
+        load_q(m + walkers);
     }
+    const int c = tid % CQ * 4, mine = tid / CQ * kNodeBlock;
+    const bool sums = live && mine < at_once && mine < M;
+    const float *S = state + unit * D * D + c;
+    float4 ahead[4];                                   // the next four state rows
+    auto fetch = [&](int i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ahead[e] = __ldg(reinterpret_cast<const float4 *>(S + (i + e) * D));
+    };
+    if (sums) fetch(0);
     __syncthreads();
 
     // The rows of W by steps up the line: z starts as the q products; a step's w leaves
@@ -196,20 +222,17 @@ decode_tree_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const T
         }
     }
 
-    const int c = tid % CQ * 4, mine = tid / CQ * kNodeBlock;
-    const float *S = state + unit * D * D + c;
     for (int m0 = 0; m0 < M; m0 += at_once) {
         const int m1 = m0 + mine;                      // this thread's nodes: m1 .. m1 + 3
         float2 xk[kNodeBlock][2], xq[kNodeBlock][2];
 #pragma unroll
         for (int b = 0; b < kNodeBlock; ++b) xk[b][0] = xk[b][1] = xq[b][0] = xq[b][1] = make_float2(0.f, 0.f);
-        if (m1 < m_end && mine < at_once) {
+        if (sums && m1 < M) {
             const float *ke = kE + m1 * D, *qe = qE + m1 * D;
 #pragma unroll 2
             for (int i = 0; i < D; i += 4) {
-                float4 s4[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s4[e] = __ldg(reinterpret_cast<const float4 *>(S + (i + e) * D));
+                const float4 s4[4] = {ahead[0], ahead[1], ahead[2], ahead[3]};
+                fetch(i + 4 < D ? i + 4 : 0);          // (the first rows again for the next nodes)
 #pragma unroll
                 for (int b = 0; b < kNodeBlock; ++b) {
                     const float4 x = *reinterpret_cast<const float4 *>(ke + b * D + i),
@@ -235,7 +258,7 @@ decode_tree_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const T
             }
         }
         __syncthreads();                               // nodes above are in this pass or an earlier one
-        if (m1 < m_end && mine < at_once) {
+        if (sums && m1 < M) {
 #pragma unroll
             for (int b = 0; b < kNodeBlock; ++b) {
                 const int m = m1 + b;
@@ -367,14 +390,14 @@ decode_commit_kernel(const Tin *__restrict__ k, const Tin *__restrict__ v, const
                make_float4(s[i][0].x, s[i][0].y, s[i][1].x, s[i][1].y));
 }
 
-// ---- bf16 inputs, d = 128: the products with S_0 on the tensor cores ----
+// ---- bf16 inputs, d = 32, 64 or 128: the products with S_0 on the tensor cores ----
 //
-// One CTA of four (or eight) warps per (sequence, head).  Nodes 8i .. 8i+7 make row tile
+// One CTA per (sequence, head), of four warps at d = 128 and up to 16 nodes.  Nodes 8i .. 8i+7 make row tile
 // i: rows 0-7 are E_m k_m, rows 8-15 E_m q_m, so a tile is full whether the
 // tree has 8 nodes or 64.  Warp w multiplies all tiles with state columns
 // 32w .. 32w+31 (mma.sync m16n8k16): a lane loads 16 bytes of four state rows
 // and takes its four columns as column g of four 8-wide tiles (half of all that
-// with eight warps), so the fp32 state goes from HBM to the fragments without
+// with twice the warps), so the fp32 state goes from HBM to the fragments without
 // passing shared memory, in whole 128-byte lines.
 //
 // The solve does not touch the 128 columns: with y = v - (the k sums) the
@@ -398,21 +421,30 @@ decode_commit_kernel(const Tin *__restrict__ k, const Tin *__restrict__ v, const
 // fragments' loads from the L2.  On the way: fp32 products 1,673 us; the solve
 // by a thread per state column 849; its rows on a fifth warp 778; walks of
 // eight lanes per node, all nodes at once, 620; W's rows by eight lanes 453.
-constexpr int kALd = 136;                             // bf16 per operand row: 17 x 16 bytes, no bank conflicts
-
-template <int TILES> struct TcCfg {
-    // four warps of 32 state columns; eight of 16 above 16 nodes and 16 of eight above 32,
-    // where shared memory leaves room for two CTAs and one (with four warps throughout,
-    // 128 x 32 nodes took 535 us instead of 457, 64 x 64 nodes 986 instead of 617)
-    static constexpr int WARPS = TILES <= 2 ? 4 : 2 * TILES, THREADS = 32 * WARPS;
-    static constexpr int NT = 16 / WARPS;             // 8-wide column tiles per warp = columns per lane
-    static constexpr int CTAS = TILES <= 2 ? 4 : TILES == 4 ? 2 : 1;
+// 16 nodes, 128 x 64 states of 64 x 64 74 us (floor 35, the fp32 form 116), 128 x
+// 96 of 32 x 32 58 us (floor 19, the fp32 form 100).
+template <int D, int TILES> struct TcCfg {
+    static constexpr int ALD = D + 8;                 // bf16 per operand row: an odd number of 16-byte pieces
+    // Warps share the state's columns.  d = 128: four of 32; eight of 16 above 16 nodes and
+    // 16 of eight above 32, where shared memory leaves room for two CTAs and one (with four
+    // throughout, 128 x 32 nodes took 535 us instead of 457, 64 x 64 nodes 986 instead of
+    // 617).  Smaller heads: one column tile more per warp saves operand reads while there
+    // are few nodes (d = 64, 6 nodes: 40 us with two warps, 42 with four; d = 32: 26 and
+    // 34), and costs registers when there are many (d = 32, 48 nodes: 204 and 113).
+    static constexpr int WARPS = D == 128  ? (TILES <= 2 ? 4 : 2 * TILES)
+                                 : D == 64 ? (TILES == 1 ? 2 : TILES <= 4 ? 4 : 8)
+                                           : (TILES <= 2 ? 2 : 4);
+    static constexpr int THREADS = 32 * WARPS;
+    static constexpr int NT = D / 8 / WARPS;          // 8-wide column tiles per warp = columns per lane
+    static constexpr int CTAS = D == 128  ? (TILES <= 2 ? 4 : TILES == 4 ? 2 : 1)
+                                : D == 64 ? (TILES == 1 ? 8 : TILES == 2 ? 6 : TILES == 4 ? 4 : 1)
+                                          : (TILES <= 2 ? 12 : 4);
     static constexpr int PAIRS = (TILES + 1) / 2;     // 16-node blocks of W
     static constexpr int WLD = PAIRS * 16 + 8;        // bf16 per row of W: an odd number of 16-byte pieces
-    static constexpr size_t A_BYTES = (size_t)TILES * 16 * kALd * 2 * 2;
+    static constexpr size_t A_BYTES = (size_t)TILES * 16 * ALD * 2 * 2;
     static constexpr size_t W_BYTES = (size_t)PAIRS * 16 * WLD * 2 * 2;
     static size_t smem(int M) {
-        return A_BYTES + W_BYTES + (size_t)M * (128 * (4 + 4) + 16) + (size_t)M * M * (8 + 1);
+        return A_BYTES + W_BYTES + (size_t)M * (D * (4 + 4) + 16) + (size_t)M * M * (8 + 1);
     }
 };
 
@@ -446,15 +478,16 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 __device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
-template <int TILES>
-__global__ void __launch_bounds__(TcCfg<TILES>::THREADS, TcCfg<TILES>::CTAS)
+template <int D, int TILES>
+__global__ void __launch_bounds__(TcCfg<D, TILES>::THREADS, TcCfg<D, TILES>::CTAS)
 decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ k,
                       const __nv_bfloat16 *__restrict__ v, const float *__restrict__ g,
                       const float *__restrict__ beta, const float *__restrict__ state,
                       const int32_t *__restrict__ parent, int32_t M, int32_t H,
                       __nv_bfloat16 *__restrict__ out) {
-    using C = TcCfg<TILES>;
-    constexpr int D = 128, KS = D / 16, WARPS = C::WARPS, THREADS = C::THREADS, NT = C::NT;
+    using C = TcCfg<D, TILES>;
+    constexpr int kALd = C::ALD, RUNS = D / 32;       // a walking lane's runs of four channels
+    constexpr int KS = D / 16, WARPS = C::WARPS, THREADS = C::THREADS, NT = C::NT;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     __nv_bfloat16 *ahi = reinterpret_cast<__nv_bfloat16 *>(smem_raw), *alo = ahi + TILES * 16 * kALd;
     __nv_bfloat16 *whi = reinterpret_cast<__nv_bfloat16 *>(smem_raw + C::A_BYTES),
@@ -477,17 +510,17 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
     if (tid == 0)
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(S), "r"(D * D * 4) : "memory");
     // every load of the inputs is on its way before the first is used
-    static_assert(THREADS >= kMaxTreeNodes, "a thread per node");
+    static_assert(THREADS >= 8 * TILES, "a thread per node");
     const int32_t par_in = tid < M ? parent[n * M + tid] : 0;
     const float bet_in = tid < M ? __ldg(beta + row0 + (int64_t)tid * H) : 0.f;
     // line products: eight lanes per node, channels 32 p + 4 (lane % 8) .. + 3
     const int l8 = lane & 7;
     const unsigned group = 0xffu << (lane & 24);
     int m = warp * 4 + (lane >> 3);
-    uint2 qm[4];
+    uint2 qm[RUNS];
     auto load_q = [&]() {
 #pragma unroll
-        for (int p = 0; p < 4; ++p)
+        for (int p = 0; p < RUNS; ++p)
             qm[p] = m < M ? __ldg(reinterpret_cast<const uint2 *>(q + (row0 + (int64_t)m * H) * D + 32 * p + 4 * l8))
                           : make_uint2(0u, 0u);
     };
@@ -522,9 +555,9 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
         reinterpret_cast<uint4 *>(whi)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
     for (; m < TILES * 8; m += 4 * WARPS) {
-        float2 kd[8], qd[8];
+        float2 kd[2 * RUNS], qd[2 * RUNS];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
+        for (int p = 0; p < RUNS; ++p) {
             const float4 f = m < M ? *reinterpret_cast<const float4 *>(kk + m * D + 32 * p + 4 * l8)
                                    : make_float4(0.f, 0.f, 0.f, 0.f);
             kd[2 * p] = make_float2(f.x, f.y);
@@ -545,9 +578,9 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
         };
         while (at >= 0) {
             const int next = par[at];
-            float4 kj[4], aj[4];
+            float4 kj[RUNS], aj[RUNS];
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
+            for (int p = 0; p < RUNS; ++p) {
                 kj[p] = *reinterpret_cast<const float4 *>(kk + at * D + 32 * p + 4 * l8);
                 aj[p] = *reinterpret_cast<const float4 *>(al + at * D + 32 * p + 4 * l8);
             }
@@ -557,7 +590,7 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
             float2 a2[2], b2[2];
             a2[0] = a2[1] = b2[0] = b2[1] = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
+            for (int p = 0; p < RUNS; ++p) {
                 const float2 k0 = make_float2(kj[p].x, kj[p].y), k1 = make_float2(kj[p].z, kj[p].w);
                 const float2 a0 = make_float2(aj[p].x, aj[p].y), a1 = make_float2(aj[p].z, aj[p].w);
                 a2[0] = tc::f2fma(kd[2 * p], k0, a2[0]);
@@ -579,13 +612,13 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
         if (!whole) {
             on = 0;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) kd[x] = qd[x] = make_float2(0.f, 0.f);
+            for (int x = 0; x < 2 * RUNS; ++x) kd[x] = qd[x] = make_float2(0.f, 0.f);
         }
         if (l8 == 0 && m < M) line[m] = on;
         // row of the k operand, and eight rows on the q operand (zeros where there is no node)
         const int row = (m >> 3) * 16 + (m & 7);
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
+        for (int p = 0; p < RUNS; ++p) {
             const int c = 32 * p + 4 * l8;
             uint32_t hi[2], lo[2];
             split2(kd[2 * p].x, kd[2 * p].y, hi[0], lo[0]);
@@ -620,7 +653,7 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
             }
         }
     };
-    constexpr int AHEAD = 3;                          // steps of 16 state rows on their way
+    constexpr int AHEAD = KS > 3 ? 3 : KS - 1;                          // steps of 16 state rows on their way
     float buf[AHEAD + 1][4][NT];
     const int64_t vcol = warp * 8 * NT + 2 * NT * gq; // values of node 8i + gg, 2 NT state columns from vcol
     uint32_t vv[TILES][NT];
@@ -831,19 +864,31 @@ cudaError_t run_tree(const void *q, const void *k, const void *v, const float *g
     return cudaGetLastError();
 }
 
-template <int TILES>
+template <int D, int TILES>
 cudaError_t run_tree_tc(const void *q, const void *k, const void *v, const float *g, const float *beta,
                         const float *state, const int32_t *parent, int32_t N, int32_t M, int32_t H,
                         void *out, cudaStream_t stream) {
+    using C = TcCfg<D, TILES>;
     static std::atomic<uint64_t> smem_set{0};
-    cudaError_t e = allow_dynamic_smem(decode_tree_tc_kernel<TILES>, TcCfg<TILES>::smem(8 * TILES), smem_set);
+    cudaError_t e = allow_dynamic_smem(decode_tree_tc_kernel<D, TILES>, C::smem(8 * TILES), smem_set);
     if (e != cudaSuccess) return e;
-    decode_tree_tc_kernel<TILES><<<(unsigned)N * (unsigned)H, TcCfg<TILES>::THREADS, TcCfg<TILES>::smem(M), stream>>>(
+    decode_tree_tc_kernel<D, TILES><<<(unsigned)N * (unsigned)H, C::THREADS, C::smem(M), stream>>>(
         static_cast<const __nv_bfloat16 *>(q), static_cast<const __nv_bfloat16 *>(k),
         static_cast<const __nv_bfloat16 *>(v), g, beta, state, parent, M, H,
         static_cast<__nv_bfloat16 *>(out));
     count_launches(1);
     return cudaGetLastError();
+}
+
+// row tiles of eight nodes, as few as hold M
+template <int D>
+cudaError_t run_tree_tiles(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                           const float *state, const int32_t *parent, int32_t N, int32_t M, int32_t H,
+                           void *out, cudaStream_t stream) {
+    if (M <= 8) return run_tree_tc<D, 1>(q, k, v, g, beta, state, parent, N, M, H, out, stream);
+    if (M <= 16) return run_tree_tc<D, 2>(q, k, v, g, beta, state, parent, N, M, H, out, stream);
+    if (M <= 32) return run_tree_tc<D, 4>(q, k, v, g, beta, state, parent, N, M, H, out, stream);
+    return run_tree_tc<D, 8>(q, k, v, g, beta, state, parent, N, M, H, out, stream);
 }
 
 template <typename Tin, int D>
@@ -873,13 +918,9 @@ cudaError_t launch_decode_tree(const void *q, const void *k, const void *v, cons
                                const float *beta, const float *state, const int32_t *parent, int32_t N,
                                int32_t M, int32_t H, int32_t D, kda_dtype dt, void *out,
                                cudaStream_t stream) {
-    if (dt == KDA_BF16 && D == 128) {
-        // row tiles of eight nodes, as few as hold M
-        if (M <= 8) return run_tree_tc<1>(q, k, v, g, beta, state, parent, N, M, H, out, stream);
-        if (M <= 16) return run_tree_tc<2>(q, k, v, g, beta, state, parent, N, M, H, out, stream);
-        if (M <= 32) return run_tree_tc<4>(q, k, v, g, beta, state, parent, N, M, H, out, stream);
-        return run_tree_tc<8>(q, k, v, g, beta, state, parent, N, M, H, out, stream);
-    }
+    if (dt == KDA_BF16 && D == 128) return run_tree_tiles<128>(q, k, v, g, beta, state, parent, N, M, H, out, stream);
+    if (dt == KDA_BF16 && D == 64) return run_tree_tiles<64>(q, k, v, g, beta, state, parent, N, M, H, out, stream);
+    if (dt == KDA_BF16 && D == 32) return run_tree_tiles<32>(q, k, v, g, beta, state, parent, N, M, H, out, stream);
     if (dt == KDA_BF16)
         KDA_DISPATCH_D(D, (run_tree<__nv_bfloat16, DD>(q, k, v, g, beta, state, parent, N, M, H, out, stream)))
     KDA_DISPATCH_D(D, (run_tree<float, DD>(q, k, v, g, beta, state, parent, N, M, H, out, stream)))

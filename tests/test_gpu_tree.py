@@ -62,6 +62,20 @@ def test_decode_tree(kda, N, M, H, d, dtype, kind):
     assert (out[torch.from_numpy(empty).cuda()] == 0).all()
 
 
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (BF, 32), (BF, 16), (F32, 128), (F32, 64), (F32, 32),
+                                     (F32, 16)])
+@pytest.mark.parametrize("M", [1, 4, 5, 8, 9, 16, 24, 32, 33, 64])
+def test_decode_tree_at_each_size(kda, M, d, dtype):
+    """Node counts at and around the row tiles, and units that share a CTA with none left over and some."""
+    for N, H, kind in ((3, 7, "holes"), (1, 1, "tree")):
+        rng = np.random.default_rng(M * 10 + d + N)
+        x, par = ref.kda_inputs(N, M, H, d, dtype, rng), ref.parents(N, M, kind, rng)
+        c = cu(x)
+        out = kda.kda_decode_tree(c["q"], c["k"], c["v"], c["g"], c["beta"], c["state"], i32(par))
+        want = ref.decode_tree(*(f64(x[n]) for n in ("q", "k", "v", "g", "beta", "state")), par)
+        check_kda(out, want, dtype, f"tree {N}x{M} {kind}")
+
+
 def test_decode_tree_chain_is_decode_verify(kda):
     """A chain gives kda_decode_verify's outputs: fp32 inputs, 1e-4."""
     rng = np.random.default_rng(5)
@@ -101,6 +115,11 @@ def test_decode_tree_ignores_what_no_node_holds(kda, dtype, d):
     keep = torch.ones(N * M, dtype=torch.bool)
     keep[[n * M + leaf[n] for n in range(N)]] = False
     assert torch.equal(got[keep.cuda()], want[keep.cuda()])
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 32), (BF, 16), (F32, 128), (F32, 32), (F32, 16)])
+def test_decode_tree_ignores_what_no_node_holds_small_heads(kda, dtype, d):
+    test_decode_tree_ignores_what_no_node_holds(kda, dtype, d)
 
 
 def test_decode_tree_deep_decay(kda):
