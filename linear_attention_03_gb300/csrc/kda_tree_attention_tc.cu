@@ -67,6 +67,10 @@ template <int D, int QT> struct Cfg {
     static constexpr int THREADS = 128 + 128 * QT;                // twelve warps leave 168 registers a thread
     static constexpr int SLOT = kTile * D * 2;                    // bytes of a key or value tile
     static constexpr int SLOTS = D == 64 ? 8 : (QT == 1 ? 6 : 5);
+    // Barriers of landed tiles, an even number, so that each serves keys alone or values alone
+    // (in an odd ring a slot holds them in turn): whoever waits on one waits for all its phases in
+    // order and frees the slot itself, so that no phase is passed over.
+    static constexpr int FULLS = SLOTS % 2 == 0 ? SLOTS : 2 * SLOTS;
     static constexpr int Q_BYTES = QT * SLOT;
     static constexpr int O_RING = Q_BYTES;
     static constexpr int O_MISC = O_RING + SLOTS * SLOT;
@@ -75,8 +79,8 @@ template <int D, int QT> struct Cfg {
     // Segments (and value tiles) that can be under way at once: a unit's end may still be read
     // while warp 3 prepares the tiles that the ring holds after it.
     static constexpr int RING = D == 64 ? 8 : 4;
-    static_assert(RING > SLOTS / 2, "ring of lines");
-    static constexpr int NBARS = 2 * SLOTS + (2 * BUFS + 6) * QT + 2 + 2 * RING;
+    static_assert(RING > (SLOTS + 1) / 2, "ring of lines");
+    static constexpr int NBARS = FULLS + SLOTS + (2 * BUFS + 6) * QT + 2 + 2 * RING;
     static constexpr int O_LINES = O_MISC + 8 * NBARS, O_WORDS = O_LINES + RING * 8 * kMaxTreeNodes;
     static constexpr int SMEM = O_MISC + (D == 64 ? 8192 : 3072);
     static_assert(O_WORDS + 16 + 8 * RING <= SMEM, "misc");
@@ -155,10 +159,10 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
     const int G = a.H / a.H_kv;
 
     const uint32_t bars = base + C::O_MISC;
-    auto full = [&](int s) { return bars + 8u * s; };
-    auto empty = [&](int s) { return bars + 8u * (C::SLOTS + s); };
+    auto full = [&](uint32_t f) { return bars + 8u * f; };   // use % FULLS
+    auto empty = [&](int s) { return bars + 8u * (C::FULLS + s); };
     constexpr int PER_TILE = 2 * C::BUFS + 6;
-    auto tile_bar = [&](int t, uint32_t i) { return bars + 8u * (2 * C::SLOTS + PER_TILE * t + i); };
+    auto tile_bar = [&](int t, uint32_t i) { return bars + 8u * (C::FULLS + C::SLOTS + PER_TILE * t + i); };
     auto s_full = [&](int t, uint32_t b) { return tile_bar(t, b); };
     auto s_free = [&](int t, uint32_t b) { return tile_bar(t, C::BUFS + b); };
     auto p_full = [&](int t, uint32_t i) { return tile_bar(t, 2 * C::BUFS + (i & 1)); };
@@ -188,10 +192,8 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
 
     if (warp == 0) tmem_alloc(base + C::O_WORDS + 4 * W_TMEM, 512);
     if (tid == 32) {
-        for (int s = 0; s < C::SLOTS; ++s) {
-            mbar_init(full(s), 1);
-            mbar_init(empty(s), 1);
-        }
+        for (int f = 0; f < C::FULLS; ++f) mbar_init(full(f), 1);
+        for (int s = 0; s < C::SLOTS; ++s) mbar_init(empty(s), 1);
         for (int t = 0; t < QT; ++t) {
             for (int b = 0; b < C::BUFS; ++b) {
                 mbar_init(s_full(t, b), 1);
@@ -258,17 +260,18 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                 for (int kv = 0; kv < 2; ++kv, ++use) {
                     const int s = use % C::SLOTS;
                     if (use >= C::SLOTS && !wait(empty(s), (use / C::SLOTS - 1) & 1)) break;
-                    if (lane == 0) mbar_expect_tx(full(s), bytes);
+                    const uint32_t landed = full(use % C::FULLS);
+                    if (lane == 0) mbar_expect_tx(landed, bytes);
                     __syncwarp();
                     const uint32_t dst = base + C::O_RING + s * C::SLOT;
                     if (lane < loads) {
                         const uint32_t at = dst + lane * box * D * 2;   // (the tree's rows start at a multiple of 8)
                         if (lane >= old)
-                            tma_load_4d(at, kv ? &maps.vn : &maps.kn, 0, run.n * a.M + (lane - old) * 8, 0, h, full(s));
+                            tma_load_4d(at, kv ? &maps.vn : &maps.kn, 0, run.n * a.M + (lane - old) * 8, 0, h, landed);
                         else if (tree)
-                            tma_load_4d(at, kv ? &maps.v8 : &maps.k8, 0, 0, 0, group, full(s));
+                            tma_load_4d(at, kv ? &maps.v8 : &maps.k8, 0, 0, 0, group, landed);
                         else
-                            tma_load_4d(at, kv ? &maps.v : &maps.k, 0, 0, 0, group, full(s));
+                            tma_load_4d(at, kv ? &maps.v : &maps.k, 0, 0, 0, group, landed);
                     }
                     __syncwarp();
                 }
@@ -276,10 +279,10 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
         }
         if (words[W_ABORT] != 0 || !ok) {
             // loads in flight land before the block leaves
-            for (int s = 0; s < C::SLOTS; ++s)
-                if (use > (uint32_t)s) {
-                    const uint32_t last = (use - 1 - s) / C::SLOTS;
-                    mbar_wait(full(s), last & 1, 100000000ull);
+            for (uint32_t f = 0; f < C::FULLS; ++f)
+                if (use > f) {
+                    const uint32_t last = (use - 1 - f) / C::FULLS;
+                    mbar_wait(full(f), last & 1, 100000000ull);
                 }
         }
     } else if (warp <= 2) {
@@ -293,7 +296,8 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
         constexpr uint64_t HI_V = sw128_hi(1024, C::HALVES * 1024);
         constexpr uint32_t kHalf = 8 * C::HALVES * 1024;     // bytes of 64 keys
         auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
-        uint32_t slot = sums ? 1 : 0, par = 0, tile = 0, j = 0, seg = 0;     // the tile's place in the ring; steps before
+        uint32_t slot = sums ? 1 : 0, fb = 0, par = 0;       // the tile's place in the ring, its keys' barrier
+        uint32_t tile = 0, j = 0, seg = 0;                   // before
         for (; run.left > 0 && ok; run.advance(a, sh.groups), ++seg) {
             const int cnt = (int)uniform((uint32_t)run.count());
             if (!sums) {
@@ -320,7 +324,7 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
             }
             for (int i = 0; i < cnt && ok; ++i, ++tile) {
                 const int valid = (int)uniform((uint32_t)valid_keys(a, run, run.t0 + i));
-                if (!(sums ? wait(v_ready(tile), (tile / C::RING) & 1) : wait(full(slot), par))) break;
+                if (!(sums ? wait(v_ready(tile), (tile / C::RING) & 1) : wait(full(fb), par))) break;
                 for (int x = 0; 64 * x < valid && ok; ++x, ++j) {
                     const uint32_t at = uniform(base + C::O_RING + slot * C::SLOT + x * kHalf);
                     if (!sums) {
@@ -362,8 +366,10 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                 }
                 mma_commit_w(empty(slot));                   // the tile is read
                 slot += 2;
-                if (slot >= (uint32_t)C::SLOTS) {
-                    slot -= C::SLOTS;
+                if (slot >= (uint32_t)C::SLOTS) slot -= C::SLOTS;
+                fb += 2;
+                if (fb >= (uint32_t)C::FULLS) {
+                    fb = 0;
                     par ^= 1;
                 }
             }
@@ -384,10 +390,9 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
             for (int i = 0; i < cnt && ok; ++i, ++tile) {
                 const bool tree = run.t0 + i == run.tiles - 1;
                 const int valid = valid_keys(a, run, run.t0 + i);
-                // every use of the ring in turn, so that no phase is passed over
-                const uint32_t k_use = 2 * tile, v_use = k_use + 1;
-                if (!wait(full(k_use % C::SLOTS), (k_use / C::SLOTS) & 1)) break;
-                if (!wait(full(v_use % C::SLOTS), (v_use / C::SLOTS) & 1)) break;
+                // (not for the keys: their slot can be free and full again before this warp looks)
+                const uint32_t v_use = 2 * tile + 1;
+                if (!wait(full(v_use % C::FULLS), (v_use / C::FULLS) & 1)) break;
                 uint64_t *ln = line + (seg % C::RING) * kMaxTreeNodes;
                 volatile uint32_t *bad = words + W_BAD + 2 * (seg % C::RING);
                 if (i == 0) {
