@@ -83,7 +83,9 @@ verify_kernel(const Tin *__restrict__ target, const Tin *__restrict__ draft,
     __shared__ uint32_t walk_draw;
     __shared__ u64 part[kVerifyWarps];
     __shared__ u64 totals[2][kMaxCluster];             // of both attempts
+    // a CTA's shared memory may be written once it runs: the walk hides the wait for that
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+    cluster.barrier_arrive();
     const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t n = blockIdx.x / ranks;
@@ -171,6 +173,7 @@ verify_kernel(const Tin *__restrict__ target, const Tin *__restrict__ draft,
     __syncthreads();
     const int cur = walk_cur, refused = walk_gone;
     if (cur < 0) {                                     // the whole cluster
+        cluster.barrier_wait();
         if (rank == 0 && tid == 0) next_token[n] = -1;
         return;
     }
@@ -256,6 +259,7 @@ verify_kernel(const Tin *__restrict__ target, const Tin *__restrict__ draft,
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0) part[warp] = sum;
+        if (attempt == 0) cluster.barrier_wait();      // every CTA has started
         __syncthreads();
         if (warp == 0) {
             u64 mine = lane < kVerifyWarps ? part[lane] : 0;

@@ -7,7 +7,8 @@ import pytest
 import torch
 
 from tests import tree_ref as ref
-from tests.test_gpu_tree import BF, F32, check_attention, cu, i32, ref_attention, run_attention
+from tests.test_gpu_tree import (BF, F32, check_attention, check_verify, cu, draft_inputs, ref_attention, run_attention,
+                                 run_verify)
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
 
@@ -28,3 +29,18 @@ def test_tree_attention_short_units_in_a_row(kda, M, H, Hkv, d):
     for _ in range(20):
         again = run_attention(kda, c, par, workspace=ws)
         assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
+
+
+@pytest.mark.parametrize("V", [5000, 20000, 131075])
+@pytest.mark.parametrize("with_draft", [False, True])
+def test_verify_drafts_with_walks_of_all_lengths(kda, V, with_draft):
+    """Two, four and eight CTAs to a sequence, chains that are kept whole beside sequences without a
+    node: the CTAs of a cluster meet whatever each had to do first.  Every run gives the same."""
+    rng = np.random.default_rng(V)
+    p, q, tokens, par, u = draft_inputs(11, 12, V, "chain", with_draft, F32, rng)
+    par[1::3] = -2                                 # no node at all
+    u[::3] = 0.0                                   # kept as far as the target has mass there
+    check_verify(kda, p, q, tokens, par, u)
+    first = run_verify(kda, p, q, tokens, par, u)
+    for _ in range(20):
+        assert all(torch.equal(a, b) for a, b in zip(first, run_verify(kda, p, q, tokens, par, u)))
