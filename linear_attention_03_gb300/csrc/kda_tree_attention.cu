@@ -536,8 +536,10 @@ tree_attention_join_kernel(const TreeAttention a, const Shape sh) {
             o.x *= shrink; o.y *= shrink; o.z *= shrink; o.w *= shrink;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float w = __expf(x[i] - from);
-                if (w != 0.f) {                              // (no key seen: whatever the sums are)
+                // (a part with nothing seen adds zeros; one whose scores are no numbers has a maximum of
+                // -infinity too and makes the row one: a weight of zero skips nothing)
+                if (i0 + i < parts) {
+                    const float w = __expf(x[i] - from);
                     sum += w * z[i];
                     o.x += w * y[i].x; o.y += w * y[i].y; o.z += w * y[i].z; o.w += w * y[i].w;
                 }

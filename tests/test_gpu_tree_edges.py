@@ -44,3 +44,53 @@ def test_verify_drafts_with_walks_of_all_lengths(kda, V, with_draft):
     first = run_verify(kda, p, q, tokens, par, u)
     for _ in range(20):
         assert all(torch.equal(a, b) for a, b in zip(first, run_verify(kda, p, q, tokens, par, u)))
+
+
+@pytest.mark.parametrize("dtype,page", [(BF, 16), (F32, 16), (BF, 20)])
+@pytest.mark.parametrize("M", [1, 3])
+def test_tree_attention_keeps_what_is_no_number(kda, dtype, page, M):
+    """A key, a query or a value that is not finite shows in every row that sees it, wherever the
+    keys are cut (with few tiles each is a piece of its own), and in no other."""
+    rng = np.random.default_rng(page + M)
+    H, Hkv, d = 4, 2, 128
+    x, par = ref.cache_inputs(2, M, H, Hkv, d, page, [640, 700], dtype, rng), ref.parents(2, M, "chain", rng)
+    want = run_attention(kda, cu(x), par)
+    clone = lambda: {n: t.clone() for n, t in x.items()}
+    nan, inf = float("nan"), float("inf")
+
+    def check(c, seen, lse=True):
+        """seen: of sequence 1's rows, [M, H]"""
+        out, l = run_attention(kda, cu(c), par)
+        assert torch.equal(out[:M], want[0][:M]) and torch.equal(l[:M], want[1][:M])
+        seen = seen.cuda()
+        if lse:
+            assert torch.isnan(out[M:][seen]).all() and torch.isnan(l[M:][seen]).all()
+            assert torch.equal(l[M:][~seen], want[1][M:][~seen])
+        else:
+            assert not torch.isfinite(out[M:][seen]).any()
+        assert torch.equal(out[M:][~seen], want[0][M:][~seen])
+
+    for lens in ([640, 700], [640, 640]):
+        x["cache_lens"] = torch.tensor(lens, dtype=torch.int32)
+        want = run_attention(kda, cu(x), par)
+        heads = torch.zeros(M, H, dtype=torch.bool)
+        heads[:, :2] = True                        # those that read cache head 0
+        c = clone()
+        c["k_new"][M, 0] = nan                     # the root's key, in the last tile
+        check(c, heads)
+        c = clone()
+        c["q"][M:, 1] = nan
+        one = torch.zeros(M, H, dtype=torch.bool)
+        one[:, 1] = True
+        check(c, one)
+        c = clone()
+        for pos in range(256, 384):                # whole tiles of the cache
+            c["k_cache"][c["page_table"][1, pos // page], 0, pos % page] = nan
+        check(c, heads)
+        c = clone()                                # an infinite value under a weight that underflows
+        c["q"][M:, :2] = 4.0
+        c["k_cache"][c["page_table"][1, 130 // page], 0, 130 % page] = -8.0
+        c["v_cache"][c["page_table"][1, 130 // page], 0, 130 % page] = inf
+        x2 = dict(c, v_cache=x["v_cache"])
+        want = run_attention(kda, cu(x2), par)
+        check(c, heads, lse=False)
