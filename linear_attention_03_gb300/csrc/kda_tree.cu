@@ -830,10 +830,13 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
         const int m = 8 * i + gg;
         if (m >= M) continue;
         if (dirty) {
+            // (dirty too where the state is not finite: such a column's k sums are not, whatever the
+            // operands, and a row of no node has taken them against zeros)
+            const bool none = line[m] == 0;
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                acc[i][t][2] += seen[i][t][0];
-                acc[i][t][3] += seen[i][t][1];
+                acc[i][t][2] = none ? 0.f : acc[i][t][2] + seen[i][t][0];
+                acc[i][t][3] = none ? 0.f : acc[i][t][3] + seen[i][t][1];
             }
         }
         __nv_bfloat16 *to = out + (row0 + (int64_t)m * H) * D + vcol;

@@ -7,8 +7,8 @@ import pytest
 import torch
 
 from tests import tree_ref as ref
-from tests.test_gpu_tree import (BF, F32, check_attention, check_verify, cu, draft_inputs, ref_attention, run_attention,
-                                 run_verify)
+from tests.test_gpu_tree import (BF, F32, check_attention, check_verify, cu, draft_inputs, i32, ref_attention,
+                                 run_attention, run_verify)
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
 
@@ -94,3 +94,27 @@ def test_tree_attention_keeps_what_is_no_number(kda, dtype, page, M):
         x2 = dict(c, v_cache=x["v_cache"])
         want = run_attention(kda, cu(x2), par)
         check(c, heads, lse=False)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (BF, 32), (BF, 16), (F32, 128), (F32, 16)])
+@pytest.mark.parametrize("M", [6, 20, 64])
+def test_decode_tree_rows_of_no_node_are_zeros_for_any_state(kda, dtype, d, M):
+    """Whatever the state holds: the rows of no node are zeros, the rows of other sequences and heads as
+    they were, and the nodes' rows are not finite in the columns that are not."""
+    rng = np.random.default_rng(d + M)
+    N, H = 3, 2
+    x, par = ref.kda_inputs(N, M, H, d, dtype, rng), ref.parents(N, M, "holes", rng)
+    par[1, 0], par[1, M // 2] = -1, -2
+    args = lambda c: (c["q"], c["k"], c["v"], c["g"], c["beta"], c["state"], i32(par))
+    want = kda.kda_decode_tree(*args(cu(x)))
+    node = torch.tensor([[bool(l) for l in ref.lines(p)] for p in par], device="cuda")
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        c = dict(x, state=x["state"].clone())
+        c["state"][1, 0, :, 3] = bad
+        got = kda.kda_decode_tree(*args(cu(c))).view(N, M, H, d)
+        assert (got[~node] == 0).all()
+        rest = torch.ones(N, H, d, dtype=torch.bool, device="cuda")
+        rest[1, 0, 3] = False
+        rest = rest[:, None].expand(N, M, H, d)
+        assert torch.equal(got[rest], want.view(N, M, H, d)[rest])
+        assert not torch.isfinite(got[1, node[1], 0, 3]).any()
