@@ -411,7 +411,8 @@ KDA_API size_t kda_tree_attention_workspace_size(kda_dims dims, int32_t H_kv, in
  * Any page_size serves; bf16 with d = 64 or 128 and pages of whole groups of
  * eight tokens takes the tcgen05 path, everything else products of tf32 parts
  * (fp32 factors in two parts each: 2^-23, and an infinity among the keys or
- * values that an fp32 row sees makes its results NaN).
+ * values that an fp32 row sees, or a magnitude from 2^128 - 2^116 on among the
+ * keys or the cached values, makes its results NaN).
  * N * M * H must not exceed 2^29.  The same call gives the same bits.
  */
 KDA_API kda_status kda_tree_attention(const void *q, const void *k_new, const void *v_new,

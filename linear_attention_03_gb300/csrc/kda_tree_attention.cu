@@ -25,7 +25,8 @@
 // product and softmax by 5.7e-7; with cut parts and scores summed in the tensor
 // cores it was 1.1e-6, 7% faster).  bf16 factors are exact in tf32: one product for
 // the scores, two (the weights' parts) for the sums.  An infinity among the keys
-// or values that an fp32 row sees gives NaN (inf - inf in the rest).
+// or values that an fp32 row sees gives NaN (inf - inf in the rest), and so does a key or a cached
+// value whose nearest tf32 number is infinity.  Neither reaches a row that does not see it.
 //
 // Measured, fp32, from a graph: five caches of up to 3,001 tokens, 4 heads of 64,
 // 11 nodes x 3 query heads 25 us; sixteen of 512 .. 8,192 tokens 93 us; the same
@@ -118,9 +119,17 @@ template <int W> __device__ __forceinline__ void read_run(const __nv_bfloat16 *p
     }
 }
 
-// x = part + rest: the nearest tf32 number, and what is left, cut to eleven bits
+// x = part + rest: the nearest tf32 number, and what is left, cut to eleven bits.  From
+// 2^128 - 2^116 on the nearest one is infinity.  In the tree's tile, where rows that do not see a
+// value take it into their products, its part ends at the largest tf32 number, and what the rest
+// is cut by has a product of its own, since that rest is longer.  (The limit everywhere took 14%
+// more time, the conversion instruction with saturation 21%; in the tree's tile -3 to +2%.)
 __device__ __forceinline__ float part_of(float x) {
     return __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u);
+}
+__device__ __forceinline__ float part_below_infinity(float x) {
+    const float most = __uint_as_float(0x7f7fe000u);
+    return fminf(fmaxf(part_of(x), -most), most);
 }
 __device__ __forceinline__ float rest_of(float x, float part) {
     return __uint_as_float(__float_as_uint(x - part) & 0xffffe000u);
@@ -394,12 +403,20 @@ tree_attention_kernel(const TreeAttention a, const Shape sh) {
                                 x[j] = fx ? x[j] : 0.f;
                                 z[j] = fz ? z[j] : 0.f;
                             }
-                            const float x1 = SPLIT ? part_of(x[j]) : x[j], z1 = SPLIT ? part_of(z[j]) : z[j];
+                            auto part = [](float f) {
+                                return !SPLIT ? f : decltype(in_tree)::value ? part_below_infinity(f) : part_of(f);
+                            };
+                            const float x1 = part(x[j]), z1 = part(z[j]);
                             if (i == 0)
                                 mma_tf32_first(o[j], p2[i], x1, z1);
                             else
                                 mma_tf32(o[j], p2[i], x1, z1);
-                            if (SPLIT) mma_tf32(o[j], p1[i], rest_of(x[j], x1), rest_of(z[j], z1));
+                            if (SPLIT) {
+                                const float x2 = rest_of(x[j], x1), z2 = rest_of(z[j], z1);
+                                if (decltype(in_tree)::value)
+                                    mma_tf32(o[j], p1[i], x[j] - x1 - x2, z[j] - z1 - z2);
+                                mma_tf32(o[j], p1[i], x2, z2);
+                            }
                             mma_tf32(o[j], p1[i], x1, z1);
                         }
                     }
@@ -424,7 +441,7 @@ tree_attention_kernel(const TreeAttention a, const Shape sh) {
 #pragma unroll
                             for (int r = 0; r < 2; ++r)
                                 if (!(fabsf(x) < INFINITY) && (seen[r] >> k & 1) != 0)
-                                acc[e][y % W][2 * r + y / W] += x;
+                                    acc[e][y % W][2 * r + y / W] += x;
                         }
             }
         }

@@ -118,3 +118,30 @@ def test_decode_tree_rows_of_no_node_are_zeros_for_any_state(kda, dtype, d, M):
         rest = rest[:, None].expand(N, M, H, d)
         assert torch.equal(got[rest], want.view(N, M, H, d)[rest])
         assert not torch.isfinite(got[1, node[1], 0, 3]).any()
+
+
+@pytest.mark.parametrize("dtype,page,d", [(F32, 16, 128), (F32, 16, 32), (BF, 16, 128), (BF, 20, 128), (BF, 16, 16)])
+def test_tree_attention_ignores_the_largest_numbers_in_masked_rows(kda, dtype, page, d):
+    """The type's largest and lowest values in the rows of no node and of a leaf reach no other row; a
+    row that sees nothing but such a value returns it."""
+    rng = np.random.default_rng(page + d)
+    N, M, H, Hkv = 2, 9, 4, 2
+    x, par = ref.cache_inputs(N, M, H, Hkv, d, page, [200, 5], dtype, rng), ref.parents(N, M, "star", rng)
+    par[:, 4] = -2
+    want = run_attention(kda, cu(x), par)
+    big = torch.finfo(dtype).max
+    for value in (big, -big):
+        c = {n: t.clone() for n, t in x.items()}
+        for n in range(N):
+            for row in (n * M + 4, n * M + 8):
+                for name in ("q", "k_new", "v_new"):
+                    c[name][row] = value
+        keep = torch.ones(N * M, dtype=torch.bool)
+        keep[[8, M + 8]] = False
+        got = run_attention(kda, cu(c), par)
+        assert torch.equal(got[0][keep.cuda()], want[0][keep.cuda()])
+        assert torch.equal(got[1][keep.cuda()], want[1][keep.cuda()])
+        one = ref.cache_inputs(1, 1, H, Hkv, d, page, [0], dtype, rng)
+        one["v_new"][:] = value
+        out, _ = run_attention(kda, cu(one), np.array([[-1]]))
+        assert (out == value).all()
