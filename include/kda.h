@@ -466,7 +466,10 @@ KDA_API kda_status kda_verify_drafts(const void *target_probs, const void *draft
  *       clamped to 0..P, or NULL (all P)
  *   k_cache, v_cache, page_table, page_size as kda_tree_attention
  *   lens_out [N] int32 or NULL: cache_lens + accept; must not be cache_lens
- * A token whose path entry, position or page is out of range is left out.
+ * A token whose path entry, position or page is out of range is left out.  Of
+ * a sequence whose length is negative all are, and its lens_out is cache_lens +
+ * accept, but at most -1.  This call has no status word: the next
+ * kda_tree_attention reports such a length, and one past the table's room.
  * Sequences must not share the pages that are written.
  */
 KDA_API kda_status kda_cache_append(const void *k_new, const void *v_new, const int32_t *path,

@@ -373,8 +373,12 @@ append_kernel(const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new,
     const int64_t n = blockIdx.y;
     int acc = accept != nullptr ? accept[n] : P;
     acc = acc < 0 ? 0 : (acc > P ? P : acc);
-    const int len = max(cache_lens[n], 0);
-    if (blockIdx.x == 0 && threadIdx.x == 0 && lens_out != nullptr) lens_out[n] = len + acc;
+    const int len = cache_lens[n];
+    if (blockIdx.x == 0 && threadIdx.x == 0 && lens_out != nullptr) {
+        // (a length below zero stays one, so that the next attention reports it)
+        lens_out[n] = len < 0 ? min(len + acc, -1) : len + acc;
+    }
+    if (len < 0) return;
     // kAppendTokens tokens per block and pass, so that the index arithmetic stays in 32 bits
     const uint32_t per_token = (uint32_t)H << piece_bits;
     for (int64_t t0 = (int64_t)blockIdx.x * kAppendTokens; t0 < acc; t0 += (int64_t)gridDim.x * kAppendTokens) {

@@ -145,3 +145,30 @@ def test_tree_attention_ignores_the_largest_numbers_in_masked_rows(kda, dtype, p
         one["v_new"][:] = value
         out, _ = run_attention(kda, cu(one), np.array([[-1]]))
         assert (out == value).all()
+
+
+@pytest.mark.parametrize("with_path", [False, True])
+def test_cache_append_leaves_a_negative_length_alone(kda, with_path):
+    """Nothing is written for a sequence whose length is below zero, and its length stays below zero, so
+    that the next attention reports it."""
+    rng = np.random.default_rng(41)
+    N, M, H, d, page = 5, 6, 2, 64, 4
+    x = ref.cache_inputs(N, M, H, H, d, page, [9] * N, BF, rng, spare=0)
+    x["k_cache"].nan_to_num_()
+    x["v_cache"].nan_to_num_()
+    lens, accept = np.array([3, -1, -2 ** 31, -4, 0], np.int32), np.array([4, 6, 6, 2, 6], np.int32)
+    path = np.tile(np.arange(M), (N, 1)) if with_path else None
+    c = cu(x)
+    got = kda.kda_cache_append(c["k_new"], c["v_new"], c["k_cache"], c["v_cache"], c["page_table"], i32(lens),
+                               path=None if path is None else i32(path), accept=i32(accept))
+    keep = [0, 4]
+    k, v, _ = ref.append(torch.cat([x["k_new"][n * M:n * M + M] for n in keep]),
+                         torch.cat([x["v_new"][n * M:n * M + M] for n in keep]), x["k_cache"], x["v_cache"],
+                         x["page_table"].numpy()[keep], lens[keep], None if path is None else path[keep], accept[keep])
+    assert torch.equal(c["k_cache"].cpu(), k) and torch.equal(c["v_cache"].cpu(), v)
+    assert got[0].item() == 7 and got[4].item() == 6 and (got[1:4] < 0).all()
+    assert got[3].item() == -2                     # the length and the accepted tokens, while that is negative
+    ws = torch.empty(kda.kda_tree_attention_workspace_size(H, H, d, BF, N, M, page, c["page_table"].shape[1]),
+                     dtype=torch.uint8, device="cuda")
+    run_attention(kda, dict(c, cache_lens=got), ref.parents(N, M, "chain", rng), workspace=ws)
+    assert kda.kda_get_device_status(ws) == kda.KDA_DEVICE_BAD_LENGTH
