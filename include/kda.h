@@ -363,8 +363,9 @@ KDA_API kda_status kda_output_gate(const void *o, const void *z, const float *we
  * (parent[m] = m - 1) gives kda_decode_verify's outputs.
  *   q, k [N*M, H, d_k], v, out [N*M, H, d_v] qkv_dtype;  g [N*M, H, d_k] fp32
  *   (<= 0), beta [N*M, H] fp32;  state [N, H, d_k, d_v] fp32, read once
- * A state column that holds an infinity gives results that are not finite (NaN
- * where the products are of split operands) in the nodes' rows of that column.
+ * A state column that holds an infinity gives results that are not finite in
+ * the nodes' rows of that column (bf16 with d >= 32 takes the products of split
+ * bf16 operands: NaN, and for a magnitude from 2^128 - 2^119 on as well).
  */
 KDA_API kda_status kda_decode_tree(const void *q, const void *k, const void *v, const float *g,
                                    const float *beta, const float *state, const int32_t *parent,

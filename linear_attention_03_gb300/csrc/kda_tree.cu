@@ -17,6 +17,8 @@
 #include "kda_tc.cuh"
 #include "kda_tree.cuh"
 
+#include <math.h>
+
 namespace kda {
 namespace {
 
@@ -476,7 +478,9 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-__device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+// Whether the nearest bf16 number is finite: |x| < 2^128 - 2^119.
+constexpr uint32_t kBf16End = 0x7f7f8000u;
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
 template <int D, int TILES>
 __global__ void __launch_bounds__(TcCfg<D, TILES>::THREADS, TcCfg<D, TILES>::CTAS)
@@ -741,7 +745,7 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
     }
     // lane (gg, gq): node 8i + gg's k sums (entries 0, 1; they become y) and q sums
     // (2, 3) of the tile columns 2 gq and 2 gq + 1, i.e. columns vcol + t and vcol + NT + t
-    float clean = 0.f;                                // NaN once any y is not finite
+    uint32_t most = 0;                                // the largest y (no number is above all)
 #pragma unroll
     for (int i = 0; i < TILES; ++i) {
 #pragma unroll
@@ -749,14 +753,13 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
             const uint32_t u0 = vv[i][t >> 1], u1 = vv[i][(NT + t) >> 1];
             acc[i][t][0] = ((t & 1) ? hi_f(u0) : lo_f(u0)) - acc[i][t][0];
             acc[i][t][1] = (((NT + t) & 1) ? hi_f(u1) : lo_f(u1)) - acc[i][t][1];
-            clean += 0.f * acc[i][t][0];
-            clean += 0.f * acc[i][t][1];
+            most = max(most, max(magnitude(acc[i][t][0]), magnitude(acc[i][t][1])));
         }
     }
-    const bool dirty = __any_sync(0xffffffffu, clean != 0.f);
+    const bool dirty = __any_sync(0xffffffffu, most >= kBf16End);
     __syncthreads();                                  // W is there
-    // A y that is not finite belongs to its own line only: the dense product
-    // takes a zero in its place, and it is added where it is seen
+    // A y that is not finite in bf16 belongs to its own line only: the dense product
+    // takes a zero in its place, and it is added where it is seen (a number weighted)
     float seen[TILES][NT][2];
     if (dirty) {
 #pragma unroll
@@ -775,9 +778,13 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
                 for (int o = 0; o < TILES; ++o) {
                     const int m = 8 * o + gg;
                     if (m >= M || (line[m] >> (8 * i + r) & 1) == 0) continue;
+                    const int at = m * C::WLD + 8 * i + r;
+                    const float w = __bfloat162float(whi[at]) + __bfloat162float(wlo[at]);
 #pragma unroll
-                    for (int x = 0; x < 2 * NT; ++x)
-                        if (!is_finite(y[x >> 1][x & 1])) seen[o][x >> 1][x & 1] += y[x >> 1][x & 1];
+                    for (int x = 0; x < 2 * NT; ++x) {
+                        const float f = y[x >> 1][x & 1];
+                        if (magnitude(f) >= kBf16End) seen[o][x >> 1][x & 1] += fabsf(f) < INFINITY ? w * f : f;
+                    }
                 }
             }
         }
@@ -785,8 +792,8 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
         for (int i = 0; i < TILES; ++i)
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                if (!is_finite(acc[i][t][0])) acc[i][t][0] = 0.f;
-                if (!is_finite(acc[i][t][1])) acc[i][t][1] = 0.f;
+                if (magnitude(acc[i][t][0]) >= kBf16End) acc[i][t][0] = 0.f;
+                if (magnitude(acc[i][t][1]) >= kBf16End) acc[i][t][1] = 0.f;
             }
     }
     uint32_t yh[2 * C::PAIRS][NT], yl[2 * C::PAIRS][NT];

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 from tests import tree_ref as ref
+from tests.kda_testlib import f64
 from tests.test_gpu_tree import (BF, F32, check_attention, check_verify, cu, draft_inputs, i32, ref_attention,
                                  run_attention, run_verify)
 
@@ -172,3 +173,30 @@ def test_cache_append_leaves_a_negative_length_alone(kda, with_path):
                      dtype=torch.uint8, device="cuda")
     run_attention(kda, dict(c, cache_lens=got), ref.parents(N, M, "chain", rng), workspace=ws)
     assert kda.kda_get_device_status(ws) == kda.KDA_DEVICE_BAD_LENGTH
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (BF, 32), (BF, 16), (F32, 64)])
+def test_decode_tree_pseudo_values_past_the_types_range(kda, dtype, d):
+    """v - S^T k of a leaf lies past bf16's largest number (and below fp32's): the leaf's row is right and
+    no other row changes.  The leaf's row: a product of its own weight, checked to 2^-7 of its size."""
+    rng = np.random.default_rng(d)
+    N, M, H = 2, 12, 2
+    x, par = ref.kda_inputs(N, M, H, d, dtype, rng), ref.parents(N, M, "star", rng)
+    leaf = [5, M + 9]
+    for n, row in enumerate(leaf):
+        x["g"][n * M], x["g"][row] = 0.0, 0.0
+        k = x["k"][row, :, :].float()
+        x["state"][n, :, :, 3] = -8e35 * k / (k * k).sum(-1, keepdim=True)
+        x["k"][n * M] = 0.0                        # the root leaves the state alone
+        x["v"][row, :, 3] = torch.finfo(BF).max
+    args = lambda c: (c["q"], c["k"], c["v"], c["g"], c["beta"], c["state"], i32(par))
+    got = kda.kda_decode_tree(*args(cu(x)))
+    other = dict(x, v=x["v"].clone())
+    for row in leaf:
+        other["v"][row, :, 3] = 0.0
+    want = kda.kda_decode_tree(*args(cu(other)))
+    keep = torch.ones(N * M, dtype=torch.bool)
+    keep[leaf] = False
+    assert torch.equal(got[keep.cuda()], want[keep.cuda()])
+    full = ref.decode_tree(*(f64(x[n]) for n in ("q", "k", "v", "g", "beta", "state")), par)[leaf][:, :, 3]
+    assert (np.abs(f64(got)[leaf][:, :, 3] - full) <= 2.0 ** -7 * np.abs(full) + 2.0 ** -7 * 8e35).all()
