@@ -47,6 +47,21 @@ class Hybrid:
         self.k_cache = torch.zeros(n * per, HKV, PAGE, DA, device=device, dtype=torch.bfloat16)
         self.v_cache = torch.zeros_like(self.k_cache)
         self.lens = torch.zeros(n, dtype=torch.int32, device=device)
+        self.workspaces = {}                # by nodes per sequence
+
+    def workspace(self, M):
+        """The attention's workspace, kept: its status word tells of pages and lengths out of range."""
+        if M not in self.workspaces:
+            size = kda.kda_tree_attention_workspace_size(HQ, HKV, DA, torch.bfloat16, self.n, M, PAGE,
+                                                         self.table.shape[1])
+            self.workspaces[M] = torch.zeros(size, dtype=torch.uint8, device=self.device)
+        return self.workspaces[M]
+
+    def check(self):
+        """Raises what the last attention call with each workspace found (waits for the GPU)."""
+        for ws in self.workspaces.values():
+            if kda.kda_get_device_status(ws) != kda.KDA_DEVICE_OK:
+                raise kda.KDAError(kda.KDA_ERR_DEVICE, "kda_tree_attention")
 
     @staticmethod
     def _norm(x):
@@ -71,7 +86,8 @@ class Hybrid:
         y = self._norm(x).bfloat16()
         q = (y @ self.att["q"]).view(n * M, HQ, DA)
         k, v = ((y @ self.att[c]).view(n * M, HKV, DA) for c in "kv")
-        out, _ = kda.kda_tree_attention(q, k, v, self.k_cache, self.v_cache, self.table, self.lens, parent)
+        out, _ = kda.kda_tree_attention(q, k, v, self.k_cache, self.v_cache, self.table, self.lens, parent,
+                                        workspace=self.workspace(M))
         x = x + (out.view(n * M, HQ * DA) @ self.att["o"]).float()
         kept.append((k, v))
         logits = (self._norm(x).bfloat16() @ self.head).float()
@@ -133,6 +149,7 @@ def generate(model, prompt, steps, seed=0):
         for i, (a, row) in enumerate(zip(accept.tolist(), path.tolist())):
             out[i] += [int(tokens[i, m]) for m in row[:a]]
             kept_nodes += a
+    model.check()
     return [o + [int(t)] for o, t in zip(out, last.tolist())], kept_nodes / (n * steps)
 
 

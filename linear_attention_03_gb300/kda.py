@@ -519,7 +519,10 @@ def kda_tree_attention(q, k_new, v_new, k_cache, v_cache, page_table, cache_lens
     q [N*M, H, d]; k_new, v_new [N*M, H_kv, d]; k_cache, v_cache [num_pages,
     H_kv, page_size, d]; page_table [N, max_pages], cache_lens [N], parent
     [N, M] int32.  scale defaults to d ** -0.5.  The workspace's first word is
-    the device status word (kda_get_device_status)."""
+    the device status word (kda_get_device_status): a page or a length out of
+    range is reported there alone, so a caller that makes its own lengths and
+    tables keeps a workspace (kda_tree_attention_workspace_size) and reads it;
+    the one that the call makes by default is gone with the call."""
     rows, H, d = q.shape
     N, M = _tree(parent, rows)
     _dev(q, "q")
@@ -593,7 +596,9 @@ def kda_cache_append(k_new, v_new, k_cache, v_cache, page_table, cache_lens, pat
                      lens_out=None):
     """The first accept[n] new tokens (all without `accept`; rows path[n, t],
     or t without `path`) of each sequence behind its cache_lens[n] cached ones;
-    returns the new lengths."""
+    returns the new lengths.  Tokens whose path entry, position or page is out
+    of range are left out without a report, and counted; a negative length
+    stays negative."""
     rows, H, d = k_new.shape
     N = cache_lens.shape[0]
     _dev(k_new, "k_new")

@@ -2,6 +2,9 @@
 far apart, values that are not finite or close to the largest number, lengths
 out of range.  Plain fp64 implementations: tests/tree_ref.py; tolerances:
 tests/test_gpu_tree.py."""
+import importlib.util
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -11,6 +14,7 @@ from tests.kda_testlib import f64
 from tests.test_gpu_tree import (BF, F32, check_attention, check_verify, cu, draft_inputs, i32, ref_attention,
                                  run_attention, run_verify)
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
 
 
@@ -200,3 +204,18 @@ def test_decode_tree_pseudo_values_past_the_types_range(kda, dtype, d):
     assert torch.equal(got[keep.cuda()], want[keep.cuda()])
     full = ref.decode_tree(*(f64(x[n]) for n in ("q", "k", "v", "g", "beta", "state")), par)[leaf][:, :, 3]
     assert (np.abs(f64(got)[leaf][:, :, 3] - full) <= 2.0 ** -7 * np.abs(full) + 2.0 ** -7 * 8e35).all()
+
+
+def test_example_reports_a_sequence_past_its_pages(kda):
+    spec = importlib.util.spec_from_file_location("tree_speculation", os.path.join(ROOT, "examples",
+                                                                                   "tree_speculation.py"))
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    model = example.Hybrid(2, max_tokens=32, seed=1)
+    prompt = torch.randint(0, example.VOCAB, (2, 20), generator=torch.Generator().manual_seed(1)).int().cuda()
+    model.feed(prompt)
+    model.feed(prompt)                             # 40 tokens, room for 32
+    model.check()
+    model.feed(prompt)
+    with pytest.raises(kda.KDAError, match="length"):
+        model.check()
