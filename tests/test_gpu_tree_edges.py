@@ -219,3 +219,15 @@ def test_example_reports_a_sequence_past_its_pages(kda):
     model.feed(prompt)
     with pytest.raises(kda.KDAError, match="length"):
         model.check()
+
+
+@pytest.mark.parametrize("M,G,Hkv,d,page,dtype", [(7, 24, 2, 128, 16, BF), (5, 17, 3, 64, 64, BF), (3, 64, 1, 128, 32, BF),
+                                                  (9, 96, 2, 128, 16, BF), (4, 128, 1, 64, 128, BF),
+                                                  (64, 128, 1, 128, 16, BF), (3, 129, 1, 128, 16, BF),
+                                                  (2, 200, 2, 64, 24, BF), (4, 40, 2, 128, 16, F32),
+                                                  (3, 130, 1, 32, 16, F32)])
+def test_tree_attention_many_query_heads_to_a_cache_head(kda, M, G, Hkv, d, page, dtype):
+    """More than 16: few nodes to a row tile, down to one, then the other form."""
+    rng = np.random.default_rng(M * G)
+    x, par = ref.cache_inputs(2, M, G * Hkv, Hkv, d, page, [131, 40], dtype, rng), ref.parents(2, M, "holes", rng)
+    check_attention(run_attention(kda, cu(x), par), ref_attention(x, par, d ** -0.5), dtype, f"{M} x {G}")
