@@ -11,6 +11,7 @@
 // shift the distribution by at most 2^-20.
 #include "kda_internal.cuh"
 #include "kda_tree.cuh"
+#include "kda_tree_cut.cuh"
 
 #include <cooperative_groups.h>
 
@@ -60,6 +61,7 @@ template <> struct Row<__nv_bfloat16> {
 
 constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxCluster = 8;      // CTAs of a sequence
+constexpr int kVerifyCtas = 4;      // resident on an SM
 
 // One cluster per sequence.  Every CTA gathers the drafted tokens'
 // probabilities and its first warp walks the tree (each step tests one child,
@@ -71,7 +73,7 @@ constexpr int kMaxCluster = 8;      // CTAs of a sequence
 // MB), 52 us, 4.5 TB/s; bf16 40 us.  What is left above the bytes are the
 // prologue's three dependent loads, the cluster's meeting and the second pass.
 template <typename Tin>
-__global__ void __launch_bounds__(kVerifyThreads, 4)
+__global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas)
 verify_kernel(const Tin *__restrict__ target, const Tin *__restrict__ draft,
               const int32_t *__restrict__ tokens, const int32_t *__restrict__ parent,
               const float *__restrict__ uniforms, int32_t M, int32_t V, int32_t *__restrict__ accept,
@@ -334,10 +336,12 @@ cudaError_t run_verify(const void *target, const void *draft, const int32_t *tok
                        const float *uniforms, int32_t N, int32_t M, int32_t V, int32_t *accept, int32_t *path,
                        int32_t *next_token, cudaStream_t stream) {
     // CTAs per sequence: up to eight, while all sequences' CTAs make no more than two
-    // rounds of the GPU (256 chains: 62 us with two, 52 with four, 53 with eight) and
-    // each still has 4 KB.
+    // rounds of the GPU (256 chains: 62 us with two, 52 with four, 53 with eight; 600
+    // of 65,536 tokens with draft probabilities: 79 with one, 71 with two) and each
+    // still has 4 KB.
+    const int64_t two_rounds = 2 * kVerifyCtas * (int64_t)sm_count();
     int ranks = kMaxCluster;
-    while (ranks > 1 && ((int64_t)ranks * N > 1100 || (int64_t)V * (int64_t)sizeof(Tin) < (int64_t)ranks * 4096)) ranks /= 2;
+    while (ranks > 1 && (ranks * (int64_t)N > two_rounds || (int64_t)V * (int64_t)sizeof(Tin) < (int64_t)ranks * 4096)) ranks /= 2;
     cudaLaunchAttribute cluster;
     cluster.id = cudaLaunchAttributeClusterDimension;
     cluster.val.clusterDim.x = ranks;
