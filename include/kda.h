@@ -343,7 +343,10 @@ KDA_API kda_status kda_output_gate(const void *o, const void *z, const float *we
  * kda_decode_tree in the KDA layers and kda_tree_attention in the softmax
  * layers give every node's output, kda_verify_drafts decides on the target's
  * probabilities which nodes are kept, and kda_decode_commit and
- * kda_cache_append bring states and caches behind the kept path.
+ * kda_cache_append bring states and caches behind the kept path.  The softmax
+ * layers are those with keys and values of one head size, with any number of
+ * query heads to a cache head; a cache of latents is not served, nor is a
+ * convolution along the tree's lines: a layer with one hands in its q, k and v.
  *
  * A sequence has M nodes, rows n*M .. n*M + M-1 of every per-node tensor.
  *   parent [N, M] int32 device: node m hangs below node parent[n, m] < m, or
@@ -409,11 +412,15 @@ KDA_API size_t kda_tree_attention_workspace_size(kda_dims dims, int32_t H_kv, in
  *          KDA_DEVICE_BAD_LENGTH and KDA_DEVICE_TIMEOUT (a bounded wait) are
  *          reported there (out and lse are then unspecified; no access leaves
  *          the buffers)
- * Any page_size serves; bf16 with d = 64 or 128 and pages of whole groups of
- * eight tokens takes the tcgen05 path, everything else products of tf32 parts
- * (fp32 factors in two parts each: 2^-23, and an infinity among the keys or
- * values that an fp32 row sees, or a magnitude from 2^128 - 2^116 on among the
- * keys or the cached values, makes its results NaN).
+ * Any page_size serves; bf16 with d = 64 or 128, pages of whole groups of eight
+ * tokens and up to 128 query heads to a cache head takes the tcgen05 path.  It
+ * rounds the weights to bf16 for their product with the values (2^-9 of each, the
+ * size of the output's own rounding: outputs err by 2.3e-3 of their RMS, of which
+ * that rounding alone is 1.7e-3); maximum, sums and lse are fp32.  Everything
+ * else takes products of tf32 parts: the weights in two, bf16 factors as they
+ * are, fp32 factors in two (2^-21 of a product at most; an infinity among the
+ * keys or values that an fp32 row sees, or a magnitude from 2^128 - 2^116 on among
+ * the keys or the cached values, makes its results NaN).
  * N * M * H must not exceed 2^29.  The same call gives the same bits.
  */
 KDA_API kda_status kda_tree_attention(const void *q, const void *k_new, const void *v_new,

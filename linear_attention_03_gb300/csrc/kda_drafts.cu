@@ -7,7 +7,7 @@
 // Probabilities are compared and summed in fixed point (whole multiples of
 // 2^-38, held in 64 bits), so that the drawn token does not depend on the
 // order of the sums: any split of the vocabulary gives the same one.  A
-// probability of 2^-38 and below counts as zero; 2^18 tokens of rounding
+// probability below 2^-38 counts as zero; 2^18 tokens of rounding
 // shift the distribution by at most 2^-20.
 #include "kda_internal.cuh"
 #include "kda_tree.cuh"

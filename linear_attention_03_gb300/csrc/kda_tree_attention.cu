@@ -1,7 +1,7 @@
 // kda_tree_attention.cu -- softmax attention of a tree of drafted tokens over
 // a paged cache and the tree itself ("From GPT-2 to Kimi K3, from first
 // principles", Chapter 1 for softmax attention and its cache, Chapter 14 for
-// the drafts; the hybrid's softmax layers sit between its KDA layers).
+// the drafts; softmax layers with a cache of whole heads between KDA layers).
 //
 // Row (m, hq) attends to keys 0 .. len-1 of its sequence's cache and to the
 // keys of the nodes on m's line.  One pass over the keys per row with a
@@ -18,7 +18,7 @@
 //
 // Products: mma.sync m16n8k8 on tf32 operands.  An fp32 factor is the nearest tf32
 // number and a rest of eleven bits, x = x1 + x2 to 2^-23; x1 y1 + x1 y2 + x2 y1 is
-// taken, x2 y2 (2^-24) is left out.  The tensor cores cut the sums that they add
+// taken, x2 y2 (up to 2^-22 of x y) is left out.  The tensor cores cut the sums that they add
 // to: so sixteen channels' large terms at a time are added up in fp32 registers,
 // as are the tiles' output sums, and the scores' small terms have a sum of their
 // own.  Against 64 bits the outputs err by 1.2e-7 to 3.6e-7 of their RMS (an fp32
