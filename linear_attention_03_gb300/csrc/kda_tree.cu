@@ -63,10 +63,12 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float2 lo, float2 hi) {
 // nodes x four columns: per four state rows four 16-byte reads of the state and
 // eight of the operands feed 64 paired multiply-adds.  Then o = X_q + W (v - X_k)
 // along the lines.
-// Measured, 16 nodes: 64 x 48 fp32 states of 128 x 128 109 us (4 nodes 52); 128 x 64
-// of 64 x 64 112; bf16, 128 x 96 of 16 x 16 77 us.  Issue slots are 40% busy at the
-// 16 warps per SM that the registers allow (three CTAs of 256: 154 us for 112).  With
-// a warp per node, a thread per column and eight nodes it took 218, 288 and 243.
+// Measured, 16 nodes: 64 x 48 fp32 states of 128 x 128 111 us (bytes 49; 4 nodes 54);
+// 128 x 64 of 64 x 64 114 (45); bf16, 128 x 96 of 16 x 16 90 us, where the bytes are
+// 7.7: the walks and the solve of so small states outweigh them.  Issue slots are 40%
+// busy at the 16 warps per SM that the registers allow (three CTAs of 256: 154 us for
+// 112).  With a warp per node, a thread per column and eight nodes it took 218, 288
+// and 243.
 template <typename Tin, int D>
 __global__ void __launch_bounds__(256, 2)
 decode_tree_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin *__restrict__ v,
@@ -423,8 +425,8 @@ decode_commit_kernel(const Tin *__restrict__ k, const Tin *__restrict__ v, const
 // fragments' loads from the L2.  On the way: fp32 products 1,673 us; the solve
 // by a thread per state column 849; its rows on a fifth warp 778; walks of
 // eight lanes per node, all nodes at once, 620; W's rows by eight lanes 453.
-// 16 nodes, 128 x 64 states of 64 x 64 74 us (floor 35, the fp32 form 116), 128 x
-// 96 of 32 x 32 58 us (floor 19, the fp32 form 100).
+// 16 nodes, 128 x 64 states of 64 x 64 75 us (floor 35, the fp32 form 116), 128 x
+// 96 of 32 x 32 62 us (floor 19, the fp32 form 100).
 template <int D, int TILES> struct TcCfg {
     static constexpr int ALD = D + 8;                 // bf16 per operand row: an odd number of 16-byte pieces
     // Warps share the state's columns.  d = 128: four of 32; eight of 16 above 16 nodes and

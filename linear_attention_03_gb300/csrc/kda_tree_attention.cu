@@ -28,12 +28,14 @@
 // or values that an fp32 row sees gives NaN (inf - inf in the rest), and so does a key or a cached
 // value whose nearest tf32 number is infinity.  Neither reaches a row that does not see it.
 //
-// Measured, fp32, from a graph: five caches of up to 3,001 tokens, 4 heads of 64,
-// 11 nodes x 3 query heads 25 us; sixteen of 512 .. 8,192 tokens 93 us; the same
-// with 8 heads of 128 and 16 x 4 rows 407 us, where the products alone take 186
-// (8 clocks each) and the bytes 85; two of about 62,000 tokens, 4 heads of 128,
-// 7 x 8 rows 380 us (products 168, bytes 77).  The rest is what eight to sixteen
-// warps per SM do not hide.  On CUDA cores the four took 47, 309, 1,247 and 1,160
+// Measured, fp32, graphs of one call on two inputs in turn: five caches of up to
+// 3,001 tokens, 4 heads of 64, 11 nodes x 3 query heads 29 us; sixteen of 512 ..
+// 8,192 tokens 103 us; the same with 8 heads of 128 and 16 x 4 rows 428 us, where the
+// products alone take 186 (8 clocks each) and the bytes 87; two of about 62,000
+// tokens, 4 heads of 128, 7 x 8 rows 369 us (products 168, bytes 76).  The rest is
+// what eight to sixteen warps per SM do not hide.  bf16, the sixteen caches with 8
+// heads of 128 on pages of 20 tokens: 258 us (bytes 44; 73 us on pages of 64, which
+// take the tcgen05 form); with 8 heads of 32: 106 us (bytes 11).  On CUDA cores the four took 47, 309, 1,247 and 1,160
 // us with a row and a key per lane, 35, 151, 820 and 572 with two rows x four keys
 // per lane, all of it waiting for shared memory.  As many splits for every sequence
 // instead of the even cut took 1.4 times as long with ragged lengths.

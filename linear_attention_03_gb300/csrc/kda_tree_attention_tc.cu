@@ -34,11 +34,12 @@
 // Measured: four caches of about 256,000 tokens, 4 heads of 128, 7 nodes x 8
 // query heads (one row tile): 318 us, 6.6 TB/s, the rate of a copy.  64 caches
 // of 512 .. 8,192 tokens, 8 heads, 16 nodes: x 8 query heads (one row tile) 205
-// us, 5.8 TB/s; x 12 (two row tiles) 266 us, 4.5 TB/s; x 16 265 us, 1.1 PFLOP/s.
+// .. 215 us, 5.6 TB/s; x 12 (two row tiles) 263 .. 279, 4.4 TB/s; x 16 265 .. 275.
 // With two row tiles a step's four products (8 x 48 + 4 x 64 clocks each row
 // tile: 64 key columns use three quarters of the tensor pipe) and the two
 // softmaxes share about 1,700 clocks, against the 1,500 that the bytes take; a
-// unit's end costs some 3 us.  On the way (x 12): one warp for all products 430
+// unit's end costs some 3 us.  Together that is some 210 us of the 266 (229 steps and
+// 4 to 5 ends per SM); the rest has no account yet.  On the way (x 12): one warp for all products 430
 // -> 330 us, value tiles prepared by a warp of their own 286, the joining
 // launch overlapped 262 .. 275.  Tried and slower: a part of the exponentials on
 // the FMA pipe (274 against 264), weights under the old maximum while the new
