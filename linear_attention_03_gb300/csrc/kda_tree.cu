@@ -711,6 +711,7 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
         }
     }
 
+    __syncwarp();                                     // groups of lanes were on lines of their own
     float acc[TILES][NT][4];
 #pragma unroll
     for (int i = 0; i < TILES; ++i)
@@ -797,6 +798,7 @@ decode_tree_tc_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *
                 if (magnitude(acc[i][t][0]) >= kBf16End) acc[i][t][0] = 0.f;
                 if (magnitude(acc[i][t][1]) >= kBf16End) acc[i][t][1] = 0.f;
             }
+        __syncwarp();
     }
     uint32_t yh[2 * C::PAIRS][NT], yl[2 * C::PAIRS][NT];
 #pragma unroll

@@ -574,6 +574,7 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
 #pragma unroll 1
             for (int x = 0; x < D; x += 32) {
                 float o[32];
+                __syncwarp();                        // (lanes part below)
                 tmem_ld32(o_col + x, o);
                 if (add_bad != 0) {
                     for (uint64_t left = add_bad; left != 0; left &= left - 1) {

@@ -46,3 +46,22 @@ def test_a_cluster_has_started_before_its_shared_memory_is_touched(path):
         for way in [m.start() for m in re.finditer("return;", body) if m.start() < remote] + [remote]:
             assert any(at < w < way for w in waits)
             at = way
+
+
+@pytest.mark.parametrize("name,branch,aligned", [
+    # lanes without a row skip the stores, and lanes add different numbers of values
+    ("kda_tree_attention_tc.cu", "if (!real) continue;", "tmem_ld32(o_col + x, o);"),
+    # the solve's loops are as long as a group's lines
+    ("kda_tree.cu", "wlo[m * C::WLD + j] =", "ldsm4(abase"),
+    # values that are not finite are added where a lane's node sees them
+    ("kda_tree.cu", "seen[o][x >> 1][x & 1] +=", "yh[i][t] = transpose8x8(hi);")])
+def test_a_warp_is_together_for_its_aligned_instructions(name, branch, aligned):
+    """Instructions that a whole warp issues as one stand behind a __syncwarp where lanes took different
+    ways before them: in a loop, at the iteration's start."""
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, name)).read())
+    at, branched = text.index(aligned), text.index(branch)
+    if branched < at:
+        assert "__syncwarp();" in text[branched:at]
+    else:
+        loop = max(m.start() for m in re.finditer(r"\n +for \(", text[:at]))
+        assert "__syncwarp();" in text[loop:at]
