@@ -488,6 +488,40 @@ KDA_API kda_status kda_cache_append(const void *k_new, const void *v_new, const 
                                     void *stream);
 
 /*
+ * ---- Around the softmax layers of a serving step ---------------------------
+ *
+ * The queries and keys of a softmax layer from its projections (kda_head_norm_rope),
+ * attention for batches whose sequences begin alike (kda_prefix_attention), and the
+ * distributions and tokens from the last layer's logits (kda_sample).  The method's
+ * sources give the layers' place (one softmax layer to three KDA layers) and none of
+ * these; their forms here are the usual ones.
+ */
+
+/*
+ * RMS norm of every query and key head and the rotation by its position, one pass:
+ *   y = x / sqrt(mean over the head's d channels of x^2 + eps) * w
+ *   (y_a, y_b) = (y_a cos t - y_b sin t, y_b cos t + y_a sin t),  t = position * inv_freq[i]
+ * for the pairs i = 0 .. n_freq-1 of the first 2 n_freq channels; the others are
+ * normalised alone.
+ *   q [T, H, d], k [T, H_kv, d]  qkv_dtype (dims.H = H): a token's heads are dense, from
+ *       one token to the next it is q_stride / k_stride elements (at least H d / H_kv d,
+ *       whole 16 bytes), so that both may lie in one projection
+ *   positions [T] int32;  inv_freq [n_freq] fp32, finite, radians per position
+ *   q_weight, k_weight [d] fp32 or NULL (ones), shared by the heads
+ *   interleaved  0: pair i is channels (i, i + n_freq); 1: (2 i, 2 i + 1)
+ *   q_out, k_out  as q and k, with strides of their own; q_out may be q, k_out may be k
+ *       (then with the same stride)
+ * k and k_out are NULL when H_kv = 0.  0 <= n_freq <= d / 2.  T = 0 launches nothing.
+ * Angles are formed modulo one turn in integers: they are as good at position 2^31
+ * as at 1.  The squares' sum is fp32: rows whose squares overflow it become zeros.
+ */
+KDA_API kda_status kda_head_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                      const int32_t *positions, const float *inv_freq, int32_t n_freq,
+                                      const float *q_weight, const float *k_weight, int64_t T, int32_t H_kv,
+                                      kda_dims dims, int32_t interleaved, float eps, void *q_out,
+                                      int64_t q_out_stride, void *k_out, int64_t k_out_stride, void *stream);
+
+/*
  * Diagnostic of the bounded device-side waits (the method's sources have no
  * counterpart).
  * Every wait of the tensor-core prefill gives up after a time limit,

@@ -579,6 +579,47 @@ kda_status kda_cache_append(const void *k_new, const void *v_new, const int32_t 
     return KDA_OK;
 }
 
+kda_status kda_head_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                              const int32_t *positions, const float *inv_freq, int32_t n_freq,
+                              const float *q_weight, const float *k_weight, int64_t T, int32_t H_kv,
+                              kda_dims dims, int32_t interleaved, float eps, void *q_out,
+                              int64_t q_out_stride, void *k_out, int64_t k_out_stride, void *stream) {
+    g_last_error[0] = '\0';
+    KDA_TRY(check_dims(dims));
+    if (H_kv < 0 || (int64_t)dims.H + H_kv > INT32_MAX) return fail(KDA_ERR_INVALID, "H_kv must be >= 0, H + H_kv < 2^31%s");
+    if (T < 0 || T > INT32_MAX) return fail(KDA_ERR_INVALID, "T must be in [0, 2^31)%s");
+    if (n_freq < 0 || n_freq > dims.d_k / 2) return fail(KDA_ERR_INVALID, "n_freq must be in [0, d / 2]%s");
+    if (!(eps >= 0.f)) return fail(KDA_ERR_INVALID, "eps must be >= 0%s");
+    if (T == 0) return KDA_OK;
+    const int64_t whole = dims.qkv_dtype == KDA_BF16 ? 8 : 4;       // elements of 16 bytes
+    auto strides = [&](int64_t in, int64_t out, int32_t heads, bool same, const char *name) {
+        if (in % whole != 0 || out % whole != 0)
+            return fail(KDA_ERR_INVALID, "the strides of %s must be whole 16 bytes", name);
+        if (T > 1 && (in < (int64_t)heads * dims.d_k || out < (int64_t)heads * dims.d_k))
+            return fail(KDA_ERR_INVALID, "the strides of %s must cover a token's heads", name);
+        if (same && in != out) return fail(KDA_ERR_INVALID, "%s in place must keep its stride", name);
+        return KDA_OK;
+    };
+    KDA_TRY(need(q, "q"));
+    KDA_TRY(need(q_out, "q_out"));
+    KDA_TRY(strides(q_stride, q_out_stride, dims.H, q == q_out, "q"));
+    if (H_kv > 0) {
+        KDA_TRY(need(k, "k"));
+        KDA_TRY(need(k_out, "k_out"));
+        KDA_TRY(strides(k_stride, k_out_stride, H_kv, k == k_out, "k"));
+    }
+    KDA_TRY(need4(positions, "positions"));
+    if (n_freq > 0) KDA_TRY(need4(inv_freq, "inv_freq"));
+    KDA_TRY(maybe(q_weight, "q_weight"));
+    KDA_TRY(maybe(k_weight, "k_weight"));
+    cudaError_t err = kda::launch_head_norm_rope(q, q_stride, k, k_stride, positions, inv_freq, n_freq, q_weight,
+                                                 k_weight, T, dims.H, H_kv, dims.d_k, (kda_dtype)dims.qkv_dtype,
+                                                 interleaved != 0, eps, q_out, q_out_stride, k_out, k_out_stride,
+                                                 static_cast<cudaStream_t>(stream));
+    if (err != cudaSuccess) return cuda_fail(err, "head norm and rotation launch");
+    return KDA_OK;
+}
+
 kda_status kda_selftest_wait(int64_t limit_ns, void *workspace, size_t workspace_bytes,
                              void *stream) {
     g_last_error[0] = '\0';

@@ -225,6 +225,13 @@ cudaError_t launch_cache_append(const void *k_new, const void *v_new, const int3
                                 kda_dtype dt, void *k_cache, void *v_cache, int32_t *lens_out,
                                 cudaStream_t stream);
 
+// RMS norm and rotation of query and key heads (strides in elements)
+cudaError_t launch_head_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                  const int32_t *positions, const float *inv_freq, int32_t n_freq,
+                                  const float *q_weight, const float *k_weight, int64_t T, int32_t H,
+                                  int32_t H_kv, int32_t D, kda_dtype dt, bool interleaved, float eps, void *q_out,
+                                  int64_t q_out_stride, void *k_out, int64_t k_out_stride, cudaStream_t stream);
+
 cudaError_t launch_selftest_wait(uint64_t limit_ns, int32_t *status, cudaStream_t stream);
 
 // Tensor-core chunked prefill (d = 128, bf16 q/k/v).  With out_f32 set, the

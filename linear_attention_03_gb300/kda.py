@@ -36,7 +36,7 @@ SYMBOLS = ("kda_prefill_workspace_size", "kda_prefill", "kda_decode_step",
            "kda_prologue_prefill_workspace_size", "kda_prologue_prefill",
            "kda_prefill_snapshots", "kda_decode_tree", "kda_decode_commit",
            "kda_tree_attention_workspace_size", "kda_tree_attention",
-           "kda_verify_drafts", "kda_cache_append")
+           "kda_verify_drafts", "kda_cache_append", "kda_head_norm_rope")
 
 
 class kda_dims(ctypes.Structure):
@@ -75,6 +75,8 @@ lib.kda_tree_attention.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _i32, _i32, _
 lib.kda_verify_drafts.argtypes = [_P, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _P, _P, _P, _P]
 lib.kda_cache_append.argtypes = [_P, _P, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _i32, _i32, kda_dims,
                                  _P, _P, _P, _P]
+lib.kda_head_norm_rope.argtypes = [_P, _i64, _P, _i64, _P, _P, _i32, _P, _P, _i64, _i32, kda_dims, _i32,
+                                   ctypes.c_float, _P, _i64, _P, _i64, _P]
 lib.kda_selftest_wait.argtypes = [_i64, _P, _sz, _P]
 lib.kda_selftest_wait.restype = ctypes.c_int
 lib.kda_last_error.argtypes = []
@@ -87,7 +89,7 @@ for _fn in (lib.kda_prefill, lib.kda_prefill_snapshots, lib.kda_prefill_segmente
             lib.kda_get_device_status,
             lib.kda_decode_step_conv, lib.kda_decode_verify, lib.kda_output_gate,
             lib.kda_decode_tree, lib.kda_decode_commit, lib.kda_tree_attention,
-            lib.kda_verify_drafts, lib.kda_cache_append):
+            lib.kda_verify_drafts, lib.kda_cache_append, lib.kda_head_norm_rope):
     _fn.restype = ctypes.c_int
 
 
@@ -629,6 +631,64 @@ def kda_cache_append(k_new, v_new, k_cache, v_cache, page_table, cache_lens, pat
     if st != KDA_OK:
         raise KDAError(st, "kda_cache_append")
     return lens_out
+
+
+def _heads(t, name, dtype, shape):
+    """A [T, heads, d] tensor whose tokens are dense (a slice of a projection may be given);
+    returns its stride from a token to the next."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    T, heads, d = t.shape
+    stride = t.stride()
+    if stride[2] != 1 or (heads > 1 and stride[1] != d):
+        raise ValueError(f"{name} must hold each token's heads side by side")
+    # (the stride of a single token means nothing)
+    return stride[0] if T > 1 else heads * d
+
+
+def kda_head_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                       q_out=None, k_out=None):
+    """RMS norm of every query and key head and the rotation by its position;
+    returns (q_out, k_out).
+
+    q [T, H, d], k [T, H_kv, d] or None, bf16 or fp32: dense, or slices of a
+    projection that holds them side by side (whole 16 bytes from a token to the
+    next); positions [T] int32; inv_freq [n <= d / 2] fp32, radians per position
+    of the pairs of the first 2 n channels: (i, i + n), or (2 i, 2 i + 1)
+    interleaved; weights [d] fp32.  q_out may be q and k_out may be k."""
+    T, H, d = q.shape
+    q_stride = _heads(q, "q", q.dtype, q.shape)
+    _dev(positions, "positions", torch.int32, (T,))
+    _dev(inv_freq, "inv_freq", torch.float32)
+    _dev(q_weight, "q_weight", torch.float32, (d,))
+    _dev(k_weight, "k_weight", torch.float32, (d,))
+    if q_out is None:
+        q_out = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
+        q_out_stride = H * d
+    else:
+        q_out_stride = _heads(q_out, "q_out", q.dtype, q.shape)
+    H_kv = k_stride = k_out_stride = 0
+    if k is not None:
+        H_kv = k.shape[1]
+        k_stride = _heads(k, "k", q.dtype, (T, H_kv, d))
+        if k_out is None:
+            k_out = torch.empty((T, H_kv, d), dtype=q.dtype, device=q.device)
+            k_out_stride = H_kv * d
+        else:
+            k_out_stride = _heads(k_out, "k_out", q.dtype, k.shape)
+    elif k_out is not None:
+        raise ValueError("k_out is given without k")
+    st = lib.kda_head_norm_rope(_ptr(q), q_stride, _ptr(k), k_stride, _ptr(positions), _ptr(inv_freq),
+                                inv_freq.numel(), _ptr(q_weight), _ptr(k_weight), T, H_kv, dims_of(q),
+                                1 if interleaved else 0, float(eps), _ptr(q_out), q_out_stride, _ptr(k_out),
+                                k_out_stride, _stream())
+    if st != KDA_OK:
+        raise KDAError(st, "kda_head_norm_rope")
+    return q_out, k_out
 
 
 def kda_get_device_status(workspace) -> int:

@@ -1,0 +1,41 @@
+"""Argument checks of the calls around the softmax layers, before anything
+reaches the GPU (no GPU)."""
+import ctypes
+
+import pytest
+
+FAKE = 0x10000     # 16-byte aligned, never dereferenced: the checks fail first
+
+
+def dims(kda, H=96, d=128, dt=1):
+    return kda.kda_dims(H, d, d, dt)
+
+
+@pytest.fixture
+def ptrs():
+    return ctypes.c_void_p(FAKE), ctypes.c_void_p(FAKE + 4)
+
+
+def test_head_norm_rope_argument_checks(kda, ptrs):
+    p, mis = ptrs
+    o = ctypes.c_void_p(FAKE + 4096)
+    call = lambda **a: kda.lib.kda_head_norm_rope(
+        a.get("q", p), a.get("qs", 96 * 128), a.get("k", p), a.get("ks", 1024), a.get("pos", p), a.get("f", p),
+        a.get("n", 64), a.get("w", None), None, a.get("T", 3), a.get("Hkv", 8), a.get("d", dims(kda)), 0,
+        a.get("eps", 1e-6), a.get("qo", o), a.get("qos", 96 * 128), a.get("ko", o), a.get("kos", 1024), None)
+    assert call(T=0) == kda.KDA_OK
+    assert call(T=-1) == kda.KDA_ERR_INVALID and call(T=2 ** 31) == kda.KDA_ERR_INVALID
+    assert call(Hkv=-1) == kda.KDA_ERR_INVALID
+    assert call(n=-1) == kda.KDA_ERR_INVALID and call(n=65) == kda.KDA_ERR_INVALID
+    for eps in (-1.0, float("nan")):
+        assert call(eps=eps) == kda.KDA_ERR_INVALID
+    assert call(q=None) == kda.KDA_ERR_INVALID and call(k=None) == kda.KDA_ERR_INVALID
+    assert call(qo=None) == kda.KDA_ERR_INVALID and call(ko=mis) == kda.KDA_ERR_INVALID
+    assert call(q=mis) == kda.KDA_ERR_INVALID and call(w=mis) == kda.KDA_ERR_INVALID
+    assert call(pos=None) == kda.KDA_ERR_INVALID and call(f=None) == kda.KDA_ERR_INVALID
+    assert call(pos=ctypes.c_void_p(FAKE + 2)) == kda.KDA_ERR_INVALID
+    assert call(qs=96 * 128 + 4) == kda.KDA_ERR_INVALID and "16 bytes" in kda.kda_last_error()
+    assert call(qs=95 * 128) == kda.KDA_ERR_INVALID and call(kos=512) == kda.KDA_ERR_INVALID
+    assert call(qo=p, qs=97 * 128) == kda.KDA_ERR_INVALID and "in place" in kda.kda_last_error()
+    assert call(d=dims(kda, d=256)) == kda.KDA_ERR_UNSUPPORTED
+    assert call(d=dims(kda, dt=2)) == kda.KDA_ERR_UNSUPPORTED
