@@ -636,6 +636,8 @@ def kda_cache_append(k_new, v_new, k_cache, v_cache, page_table, cache_lens, pat
 def _heads(t, name, dtype, shape):
     """A [T, heads, d] tensor whose tokens are dense (a slice of a projection may be given);
     returns its stride from a token to the next."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return shape[1] * shape[2]
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
