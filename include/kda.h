@@ -521,6 +521,42 @@ KDA_API kda_status kda_head_norm_rope(const void *q, int64_t q_stride, const voi
                                       kda_dims dims, int32_t interleaved, float eps, void *q_out,
                                       int64_t q_out_stride, void *k_out, int64_t k_out_stride, void *stream);
 
+/* Bytes of device workspace kda_prefix_attention needs (0 for invalid arguments). */
+KDA_API size_t kda_prefix_attention_workspace_size(kda_dims dims, int32_t H_kv, int32_t N, int32_t M, int32_t P,
+                                                   int32_t page_size, int32_t max_prefix_pages, int32_t max_pages);
+
+/*
+ * kda_tree_attention for sequences that share prefixes: what many sequences begin with
+ * lies in the cache once and is read once for all of them.  Node m of sequence n sees
+ * the keys of its sequence's prefix, its sequence's own cached keys, and the drafted
+ * keys of m and the nodes above it; out and lse are the softmax over all of them.  M = 1
+ * (parent -1) is a plain decoding step.
+ *   prefix_seqs [P + 1] int32 device: prefix p is that of the sequences prefix_seqs[p] ..
+ *          prefix_seqs[p+1]-1 (0 <= prefix_seqs[0] <= ... <= prefix_seqs[P] <= N); the
+ *          sequences before the first and behind the last have none
+ *   prefix_lens [P] int32 device, 0 .. max_prefix_pages * page_size
+ *   prefix_table [P, max_prefix_pages] int32 device: token t of prefix p is in slot
+ *          t % page_size of page prefix_table[p, t / page_size]; only the entries that
+ *          prefix_lens reaches are read
+ *   page_table [N, max_pages], cache_lens [N]: the sequences' own tokens, behind the
+ *          prefix's; they start a page of their own wherever the prefix ends
+ *   the other arguments, the status word, the types, forms and roundings as
+ *          kda_tree_attention; offsets out of order set KDA_DEVICE_BAD_OFFSETS
+ *   workspace  kda_prefix_attention_workspace_size() bytes; calls that overlap on the GPU
+ *          need one each
+ * Positions are the caller's: a key's rotation was applied when it was made.  P = 0 is
+ * kda_tree_attention.  N * M * H must not exceed 2^29.  The same call gives the same bits.
+ */
+KDA_API kda_status kda_prefix_attention(const void *q, const void *k_new, const void *v_new,
+                                        const void *k_cache, const void *v_cache,
+                                        const int32_t *prefix_table, const int32_t *prefix_lens,
+                                        const int32_t *prefix_seqs, const int32_t *page_table,
+                                        const int32_t *cache_lens, const int32_t *parent, int32_t N, int32_t M,
+                                        int32_t P, int32_t H_kv, int32_t num_pages, int32_t page_size,
+                                        int32_t max_prefix_pages, int32_t max_pages, float scale, kda_dims dims,
+                                        void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                        void *stream);
+
 /*
  * Diagnostic of the bounded device-side waits (the method's sources have no
  * counterpart).

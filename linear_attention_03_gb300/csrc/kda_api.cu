@@ -620,6 +620,95 @@ kda_status kda_head_norm_rope(const void *q, int64_t q_stride, const void *k, in
     return KDA_OK;
 }
 
+namespace {
+
+// Parts of kda_prefix_attention's workspace behind the status word, whole 256 bytes each.
+struct PrefixSpace {
+    size_t tree, rows, prefix;
+    size_t all() const { return kStatusBytes + tree + rows + prefix; }
+};
+PrefixSpace prefix_space(const kda_dims &d, int32_t H_kv, int32_t N, int32_t M, int32_t P, int32_t page_size) {
+    auto whole = [](size_t x) { return (x + 255) / 256 * 256; };
+    const kda_dtype dt = (kda_dtype)d.qkv_dtype;
+    PrefixSpace s{whole(kda::tree_attention_partial_bytes(M, d.H, H_kv, d.d_k, dt, page_size)), 0, 0};
+    if (P > 0) {
+        s.rows = whole((size_t)N * M * d.H * (d.d_k + 2) * sizeof(float));
+        s.prefix = whole(kda::prefix_attention_bytes(N, M, P, d.H, H_kv, d.d_k, dt, page_size));
+    }
+    return s;
+}
+
+kda_status check_prefix(const kda_dims &d, int32_t H_kv, int32_t N, int32_t M, int32_t P, int32_t num_pages,
+                        int32_t page_size, int32_t max_prefix_pages, int32_t max_pages) {
+    KDA_TRY(check_dims(d));
+    KDA_TRY(check_tree(N, M, d.H));
+    KDA_TRY(check_pages(d, H_kv, num_pages, page_size, max_pages));
+    if (P < 0 || P > 65535) return fail(KDA_ERR_INVALID, "P must be in [0, 65535]%s");
+    if (P > 0 && (max_prefix_pages < 1 || (int64_t)max_prefix_pages * page_size > INT32_MAX - 4096))
+        return fail(KDA_ERR_INVALID, "max_prefix_pages * page_size must be in [1, 2^31 - 4096)%s");
+    if ((int64_t)N * M * d.H > (1 << 29)) return fail(KDA_ERR_INVALID, "N * M * H must be <= 2^29%s");
+    return KDA_OK;
+}
+
+}  // namespace
+
+size_t kda_prefix_attention_workspace_size(kda_dims dims, int32_t H_kv, int32_t N, int32_t M, int32_t P,
+                                           int32_t page_size, int32_t max_prefix_pages, int32_t max_pages) {
+    if (check_prefix(dims, H_kv, N, M, P, 1, page_size, max_prefix_pages, max_pages) != KDA_OK || N == 0) return 0;
+    return prefix_space(dims, H_kv, N, M, P, page_size).all();
+}
+
+kda_status kda_prefix_attention(const void *q, const void *k_new, const void *v_new, const void *k_cache,
+                                const void *v_cache, const int32_t *prefix_table, const int32_t *prefix_lens,
+                                const int32_t *prefix_seqs, const int32_t *page_table,
+                                const int32_t *cache_lens, const int32_t *parent, int32_t N, int32_t M,
+                                int32_t P, int32_t H_kv, int32_t num_pages, int32_t page_size,
+                                int32_t max_prefix_pages, int32_t max_pages, float scale, kda_dims dims,
+                                void *out, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+    g_last_error[0] = '\0';
+    KDA_TRY(check_prefix(dims, H_kv, N, M, P, num_pages, page_size, max_prefix_pages, max_pages));
+    if (!(scale > 0.f) || scale > 3.402823466e38f)
+        return fail(KDA_ERR_INVALID, "scale must be positive and finite%s");
+    if (N == 0) return KDA_OK;
+    KDA_TRY(need(q, "q"));
+    KDA_TRY(need(k_new, "k_new"));
+    KDA_TRY(need(v_new, "v_new"));
+    KDA_TRY(need(k_cache, "k_cache"));
+    KDA_TRY(need(v_cache, "v_cache"));
+    if (P > 0) {
+        KDA_TRY(need4(prefix_table, "prefix_table"));
+        KDA_TRY(need4(prefix_lens, "prefix_lens"));
+        KDA_TRY(need4(prefix_seqs, "prefix_seqs"));
+    }
+    KDA_TRY(need4(page_table, "page_table"));
+    KDA_TRY(need4(cache_lens, "cache_lens"));
+    KDA_TRY(need4(parent, "parent"));
+    KDA_TRY(need(out, "out"));
+    if (lse != nullptr) KDA_TRY(need4(lse, "lse"));
+    KDA_TRY(need(workspace, "workspace"));
+    const PrefixSpace space = prefix_space(dims, H_kv, N, M, P, page_size);
+    if (workspace_bytes < space.all())
+        return fail(KDA_ERR_INVALID, "workspace too small (see kda_prefix_attention_workspace_size)%s");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const kda_dtype dt = (kda_dtype)dims.qkv_dtype;
+    unsigned char *at = static_cast<unsigned char *>(workspace) + kStatusBytes;
+    kda::PrefixAttention a{{q, k_new, v_new, k_cache, v_cache, page_table, cache_lens, parent, out, lse,
+                            static_cast<int32_t *>(workspace), N, M, dims.H, H_kv, num_pages, page_size,
+                            max_pages, scale},
+                           prefix_table, prefix_lens, prefix_seqs, P, max_prefix_pages};
+    if (P > 0) {
+        const size_t rows = (size_t)N * M * dims.H;
+        a.t.rows.o = reinterpret_cast<float *>(at + space.tree);
+        a.t.rows.top = a.t.rows.o + rows * dims.d_k;
+        a.t.rows.sum = a.t.rows.top + rows;
+    }
+    cudaError_t err = kda::launch_tree_attention(a.t, dims.d_k, dt, at, s);
+    if (err == cudaSuccess && P > 0)
+        err = kda::launch_prefix_attention(a, dims.d_k, dt, at + space.tree + space.rows, s);
+    if (err != cudaSuccess) return cuda_fail(err, "prefix attention launch");
+    return KDA_OK;
+}
+
 kda_status kda_selftest_wait(int64_t limit_ns, void *workspace, size_t workspace_bytes,
                              void *stream) {
     g_last_error[0] = '\0';

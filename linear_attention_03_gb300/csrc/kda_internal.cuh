@@ -193,8 +193,13 @@ cudaError_t launch_decode_commit(const void *k, const void *v, const float *g, c
                                  int32_t N, int32_t M, int32_t P, int32_t H, int32_t D, kda_dtype dt,
                                  float *state_out, cudaStream_t stream);
 
+// Rows of attention sums before their division: o [rows, D], the running maximum (times
+// log2 e in the tcgen05 forms) and the sum of weights (-1: the row of no node).
+struct RowSums {
+    float *o = nullptr, *top = nullptr, *sum = nullptr;
+};
 // Softmax attention of a drafted tree over a paged cache: the arguments of
-// kda_tree_attention.
+// kda_tree_attention.  With `rows` the results go there instead of to out and lse.
 struct TreeAttention {
     const void *q, *k_new, *v_new, *k_cache, *v_cache;
     const int32_t *page_table, *cache_lens, *parent;
@@ -203,6 +208,7 @@ struct TreeAttention {
     int32_t *status;
     int32_t N, M, H, H_kv, num_pages, page_size, max_pages;
     float scale;
+    RowSums rows = {};
 };
 size_t tree_attention_partial_bytes(int32_t M, int32_t H, int32_t H_kv, int32_t D, kda_dtype dt, int32_t page_size);
 // (both forms set the status word: to zero, or to what the device found)
@@ -213,6 +219,20 @@ bool tree_attention_tc_supported(int32_t H, int32_t H_kv, int32_t D, kda_dtype d
                                  int32_t page_size);
 size_t tree_attention_tc_partial_bytes(int32_t M, int32_t H, int32_t H_kv, int32_t D);
 cudaError_t launch_tree_attention_tc(const TreeAttention &a, int32_t D, void *workspace, cudaStream_t stream);
+
+// Attention behind shared prefixes: kda_prefix_attention's arguments.  t.rows holds the sums of
+// the sequences' own keys and nodes, t.out and t.lse take the results.
+struct PrefixAttention {
+    TreeAttention t;
+    const int32_t *table, *lens, *seqs;     // [P, max_pages], [P], [P + 1]
+    int32_t P, max_pages;
+};
+size_t prefix_attention_bytes(int32_t N, int32_t M, int32_t P, int32_t H, int32_t H_kv, int32_t D, kda_dtype dt,
+                              int32_t page_size);
+cudaError_t launch_prefix_attention(const PrefixAttention &a, int32_t D, kda_dtype dt, void *workspace,
+                                    cudaStream_t stream);
+size_t prefix_attention_tc_bytes(int32_t N, int32_t M, int32_t P, int32_t H, int32_t H_kv, int32_t D);
+cudaError_t launch_prefix_attention_tc(const PrefixAttention &a, int32_t D, void *workspace, cudaStream_t stream);
 
 cudaError_t launch_verify_drafts(const void *target, const void *draft, const int32_t *tokens,
                                  const int32_t *parent, const float *uniforms, int32_t N, int32_t M,

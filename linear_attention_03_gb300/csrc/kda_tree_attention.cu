@@ -43,6 +43,7 @@
 #include "kda_tc.cuh"
 #include "kda_tree.cuh"
 #include "kda_tree_cut.cuh"
+#include "kda_prefix_cut.cuh"
 
 #include <math.h>
 
@@ -147,6 +148,15 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, bool none, float4 o, fl
     *reinterpret_cast<uint2 *>(p) = none ? make_uint2(0u, 0u) : x;
 }
 
+// Four of a row's sums, for the kernel that joins them with a prefix's.
+__device__ __forceinline__ void put_sums(const RowSums &rows, int64_t row, int D, int c, float4 o, float top, float sum) {
+    *reinterpret_cast<float4 *>(rows.o + row * D + c) = o;
+    if (c == 0) {
+        rows.top[row] = top;
+        rows.sum[row] = sum;
+    }
+}
+
 // c += a b; a 16 x 8 (lane 4 g + t: rows g, g + 8 of column t, then of column t + 4),
 // b 8 x 8 (rows t, t + 4 of column g), c 16 x 8 (row g, columns 2 t, 2 t + 1; row g + 8)
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const float (&a)[4], float b0, float b1) {
@@ -170,9 +180,17 @@ __device__ __forceinline__ void copy16(void *to, const void *from, bool read) {
                  "l"(from), "r"(read ? 16 : 0) : "memory");
 }
 
-template <typename Tin, int D, int WK>
+__device__ __forceinline__ const TreeAttention &tree_of(const TreeAttention &a) { return a; }
+__device__ __forceinline__ const TreeAttention &tree_of(const PrefixAttention &a) { return a.t; }
+
+// Args: TreeAttention (a sequence's rows, its cache and its tree), or PrefixAttention (the rows of
+// all a prefix's sequences and the prefix's keys; no tree).
+template <typename Tin, int D, int WK, typename Args>
 __global__ void __launch_bounds__(32 * kMaxWarps, 2)
-tree_attention_kernel(const TreeAttention a, const Shape sh) {
+tree_attention_kernel(const Args args, const typename std::conditional<std::is_same<Args, PrefixAttention>::value,
+                                                                       PrefixShape, Shape>::type sh) {
+    constexpr bool PREFIX = std::is_same<Args, PrefixAttention>::value;
+    const TreeAttention &a = tree_of(args);
     constexpr bool SPLIT = sizeof(Tin) == 4;                // operands have a rest
     constexpr bool RESTS = kRests<Tin, WK>;
     constexpr int LK = kLdk<D>, LV = kLdv<Tin, D>, LO = D + 4;
@@ -191,22 +209,58 @@ tree_attention_kernel(const TreeAttention a, const Shape sh) {
     const Tin *q = static_cast<const Tin *>(a.q), *k_new = static_cast<const Tin *>(a.k_new),
               *v_new = static_cast<const Tin *>(a.v_new), *k_cache = static_cast<const Tin *>(a.k_cache),
               *v_cache = static_cast<const Tin *>(a.v_cache);
-    const int G = a.H / a.H_kv, M = a.M, rows = M * G;
+    const int G = a.H / a.H_kv, M = a.M;
 
-    __shared__ int64_t buf[34];
-    Place first;
-    find_place<Units>(a, sh.groups, sh.ctas, blockIdx.x, buf, first);
-    const int64_t stop = piece_start(first.total, sh.ctas, blockIdx.x + 1);
-    if (tid == 0) sh.places[blockIdx.x] = first;
-    if (first.start >= stop) return;                        // the whole block
-    CutRun<Units> run{stop - first.start, first.n, first.r, first.len, (int32_t)(first.start - first.unit0),
-                      Units::tiles(first.len, M)};
+    int32_t status;
+    auto first_run = [&](int64_t &left) {
+        if constexpr (PREFIX) {
+            const PrefixPlace first = find_prefix_place<kKeys>(args, sh.units, sh.ctas, blockIdx.x);
+            const int64_t stop = piece_start(first.total, sh.ctas, blockIdx.x + 1);
+            if (tid == 0) sh.places[blockIdx.x] = first;
+            status = first.status;
+            left = stop - first.start;
+            return left > 0 ? prefix_run<kKeys>(args, sh.units, first, stop) : PrefixRun<kKeys>{};
+        } else {
+            __shared__ int64_t buf[34];
+            Place first;
+            find_place<Units>(a, sh.groups, sh.ctas, blockIdx.x, buf, first);
+            const int64_t stop = piece_start(first.total, sh.ctas, blockIdx.x + 1);
+            if (tid == 0) sh.places[blockIdx.x] = first;
+            status = first.status;
+            left = stop - first.start;
+            return CutRun<Units>{left, first.n, first.r, first.len, (int32_t)(first.start - first.unit0),
+                                 Units::tiles(first.len, M)};
+        }
+    };
+    int64_t todo;
+    auto run = first_run(todo);
+    if (todo <= 0) {                                        // the whole block
+        if (PREFIX) tc::wait_prerequisites();               // (the next kernel counts on the ones before this)
+        return;
+    }
+    auto advance = [&]() {
+        if constexpr (PREFIX) run.advance(args, sh.units);
+        else run.advance(a, sh.groups);
+    };
     __shared__ int32_t s_status;
-    if (tid == 0) s_status = first.status;
-    for (; run.left > 0; run.advance(a, sh.groups)) {
-        const int64_t n = run.n;
-        const int h = run.r / sh.groups, row0 = run.r % sh.groups * crows, len = run.len;
-        const int32_t *table = a.page_table + n * a.max_pages;
+    if (tid == 0) s_status = status;
+    for (; run.left > 0; advance()) {
+        // first_node: the unit's rows are those of its nodes there on; groups: units per cache head
+        int64_t first_node;
+        int groups, rows;
+        const int32_t *table;
+        if constexpr (PREFIX) {
+            first_node = (int64_t)run.seq0 * M;
+            groups = run.groups;
+            rows = run.rows;
+            table = args.table + (int64_t)run.p * args.max_pages;
+        } else {
+            first_node = (int64_t)run.n * M;
+            groups = sh.groups;
+            rows = M * G;
+            table = a.page_table + (int64_t)run.n * a.max_pages;
+        }
+        const int h = run.r / groups, row0 = run.r % groups * crows, len = run.len;
         const int cache_tiles = (len + kKeys - 1) / kKeys, t0 = run.t0, t1 = t0 + run.count();
         __syncthreads();                                    // the last unit is done with shared memory
         auto base_of = [&](int t) { return t >= cache_tiles ? (t - cache_tiles) * kKeys : t * kKeys; };
@@ -223,10 +277,10 @@ tree_attention_kernel(const TreeAttention a, const Shape sh) {
             }
         };
         auto fetch = [&](int t) {
-            const bool tree = t >= cache_tiles;
+            const bool tree = !PREFIX && t >= cache_tiles;
             int64_t at = -1;                                // the key's row
             if (tree) {
-                if (base_of(t) + lane < M) at = (n * M + base_of(t) + lane) * a.H_kv + h;
+                if (base_of(t) + lane < M) at = (first_node + base_of(t) + lane) * a.H_kv + h;
             } else if (place >= 0) {
                 if (page >= 0 && page < a.num_pages)
                     at = ((int64_t)page * a.H_kv + h) * a.page_size + place;
@@ -251,11 +305,12 @@ tree_attention_kernel(const TreeAttention a, const Shape sh) {
         if (t0 < t1) fetch(t0);
         ask(t0 + 1);
 
-        for (int m = tid; m < M; m += threads) par[m] = a.parent[n * M + m];
+        if (!PREFIX)
+            for (int m = tid; m < M; m += threads) par[m] = a.parent[first_node + m];
         for (int i = tid; i < crows * (D / 8); i += threads) {
             const int r = row0 + i / (D / 8), c = i % (D / 8) * 8;
             float x[8] = {0.f};
-            if (r < rows) Elem<Tin>::load8(q + ((n * M + r / G) * a.H + h * G + r % G) * D + c, x);
+            if (r < rows) Elem<Tin>::load8(q + ((first_node + r / G) * a.H + h * G + r % G) * D + c, x);
             float x1[8], x2[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -266,8 +321,10 @@ tree_attention_kernel(const TreeAttention a, const Shape sh) {
             if (RESTS) Elem<float>::store8(sq_rest + i / (D / 8) * LK + c, x2);
         }
         __syncthreads();
-        for (int m = tid; m < M; m += threads) line[m] = tree_line(par, m);
-        __syncthreads();
+        if (!PREFIX) {
+            for (int m = tid; m < M; m += threads) line[m] = tree_line(par, m);
+            __syncthreads();
+        }
 
         // A lane's rows of the warp are g, g + 8, its keys of eight 2 t, 2 t + 1.
         const int g = lane >> 2, t4 = lane & 3;
@@ -276,7 +333,7 @@ tree_attention_kernel(const TreeAttention a, const Shape sh) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int row = row0 + wrow + g + 8 * r;
-            node[r] = row < rows && line[row / G] != 0 ? row / G : -1;
+            node[r] = row < rows && (PREFIX || line[row / G] != 0) ? row / G : -1;
         }
 #pragma unroll
         for (int e = 0; e < E; ++e)
@@ -290,7 +347,7 @@ tree_attention_kernel(const TreeAttention a, const Shape sh) {
             __syncthreads();                                    // the tile is there, its predecessor is done with
             if (t + 1 < t1) fetch(t + 1);
             ask(t + 2);
-            const bool tree = t >= cache_tiles;
+            const bool tree = !PREFIX && t >= cache_tiles;
             const int base = base_of(t), count = min(kKeys, (tree ? M : len) - base);
             const Tin *tk = sk + ((t & 1) * kKeys + my_key + g) * LK + 4 * t4;
             const Tin *tv = sv + ((t & 1) * kKeys + my_key) * LV;
@@ -451,6 +508,7 @@ tree_attention_kernel(const TreeAttention a, const Shape sh) {
         const bool whole = t0 == 0 && t1 == run.tiles;
         float *part = sh.part + (size_t)(2 * blockIdx.x + (t0 > 0 ? 0 : 1)) * crows * (D + 2);
         float *so = reinterpret_cast<float *>(smem);
+        if (PREFIX && whole) tc::wait_prerequisites();      // the own keys' sums are there
         __syncthreads();
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -489,9 +547,29 @@ tree_attention_kernel(const TreeAttention a, const Shape sh) {
                 o.z += by * y.z;
                 o.w += by * y.w;
             }
+            if constexpr (PREFIX) {
+                const int64_t o_row = (first_node + row / G) * a.H + h * G + row % G;
+                if (whole) {
+                    const RowJoin<false> join(x, z, a.rows.top[o_row], a.rows.sum[o_row]);
+                    store_out4(static_cast<Tin *>(a.out) + o_row * D + c,
+                               join(o, *reinterpret_cast<const float4 *>(a.rows.o + o_row * D + c)));
+                    if (c == 0 && a.lse != nullptr) a.lse[o_row] = join.lse;
+                } else {
+                    reinterpret_cast<float4 *>(part)[(size_t)(c / 4) * crows + lr] = o;
+                    if (c == 0) {
+                        part[crows * D + lr] = x;
+                        part[crows * D + crows + lr] = z;
+                    }
+                }
+                continue;
+            }
             if (whole) {
-                const int64_t o_row = (n * M + row / G) * a.H + h * G + row % G;
+                const int64_t o_row = (first_node + row / G) * a.H + h * G + row % G;
                 const bool none = line[row / G] == 0;
+                if (a.rows.o != nullptr) {
+                    put_sums(a.rows, o_row, D, c, o, x, none ? -1.f : z);
+                    continue;
+                }
                 store4(static_cast<Tin *>(a.out) + o_row * D + c, none, o, 1.f / z);
                 if (c == 0 && a.lse != nullptr) a.lse[o_row] = none ? -INFINITY : x + logf(z);
             } else {
@@ -506,6 +584,7 @@ tree_attention_kernel(const TreeAttention a, const Shape sh) {
     }
     __syncthreads();
     if (tid == 0) sh.places[blockIdx.x].status = s_status;
+    if (PREFIX) tc::wait_prerequisites();                   // (the next kernel counts on the ones before this)
     tc::launch_dependents();
 }
 
@@ -565,6 +644,10 @@ tree_attention_join_kernel(const TreeAttention a, const Shape sh) {
             }
         }
         const int64_t o_row = ((int64_t)p.n * a.M + row / G) * a.H + h * G + row % G;
+        if (a.rows.o != nullptr) {
+            put_sums(a.rows, o_row, D, c, o, top, none ? -1.f : sum);
+            continue;
+        }
         store4(static_cast<Tin *>(a.out) + o_row * D + c, none, o, 1.f / sum);
         if (c == 0 && a.lse != nullptr) a.lse[o_row] = none ? -INFINITY : top + logf(sum);
     }
@@ -590,10 +673,10 @@ template <typename Tin, int D> int ctas_of(const Warps &w) {
 template <typename Tin, int D, int WK>
 cudaError_t run_main(const TreeAttention &a, const Shape &sh, int row_warps, cudaStream_t stream) {
     static std::atomic<uint64_t> smem_set{0};
-    const cudaError_t e = allow_dynamic_smem(tree_attention_kernel<Tin, D, WK>,
+    const cudaError_t e = allow_dynamic_smem(tree_attention_kernel<Tin, D, WK, TreeAttention>,
                                              smem_bytes<Tin, D, WK>(kMaxWarps / WK), smem_set);
     if (e != cudaSuccess) return e;
-    tree_attention_kernel<Tin, D, WK>
+    tree_attention_kernel<Tin, D, WK, TreeAttention>
         <<<sh.ctas, 32 * row_warps * WK, smem_bytes<Tin, D, WK>(row_warps), stream>>>(a, sh);
     count_launches(1);
     return cudaGetLastError();
@@ -625,6 +708,48 @@ template <typename Tin, int D> cudaError_t run(const TreeAttention &a, void *wor
     }
     count_launches(1);
     return cudaSuccess;
+}
+
+// The rows of a prefix: sixteen to a warp, four warps (fewer where there are fewer rows), by two of keys.
+int prefix_row_warps(int64_t N, int M, int H, int H_kv) {
+    const int64_t all = N * M * (H / H_kv);
+    return (int)std::min<int64_t>(kMaxRowWarps, (all + kRowsPerWarp - 1) / kRowsPerWarp);
+}
+template <typename Tin, int D> int prefix_ctas(int row_warps) { return ctas_of<Tin, D>(Warps{0, row_warps, 2}); }
+
+template <typename Tin, int D> cudaError_t run_prefix(const PrefixAttention &a, void *workspace, cudaStream_t stream) {
+    const int warps = prefix_row_warps(a.t.N, a.t.M, a.t.H, a.t.H_kv);
+    PrefixShape sh;
+    sh.units = {1, warps * kRowsPerWarp, warps * kRowsPerWarp};
+    sh.ctas = prefix_ctas<Tin, D>(warps);
+    sh.places = static_cast<PrefixPlace *>(workspace);
+    sh.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + prefix_place_bytes(sh.ctas));
+    static std::atomic<uint64_t> smem_set{0};
+    cudaError_t e = allow_dynamic_smem(tree_attention_kernel<Tin, D, 2, PrefixAttention>,
+                                       smem_bytes<Tin, D, 2>(kMaxRowWarps), smem_set);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute overlap;
+    overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    overlap.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sh.ctas);
+    cfg.blockDim = dim3(32 * warps * 2);
+    cfg.dynamicSmemBytes = smem_bytes<Tin, D, 2>(warps);
+    cfg.stream = stream;
+    cfg.attrs = &overlap;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, tree_attention_kernel<Tin, D, 2, PrefixAttention>, a, sh);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();                           // reported here
+        return e;
+    }
+    count_launches(1);
+    return launch_prefix_join<Tin, D, kKeys, false>(a, sh, stream);
+}
+
+template <typename Tin, int D> size_t prefix_bytes(int32_t N, int32_t M, int32_t H, int32_t H_kv) {
+    const int warps = prefix_row_warps(N, M, H, H_kv), ctas = prefix_ctas<Tin, D>(warps);
+    return prefix_place_bytes(ctas) + prefix_part_bytes(ctas, warps * kRowsPerWarp, D);
 }
 
 template <typename Tin, int D> size_t partial_bytes(int M, int H, int H_kv) {
@@ -662,6 +787,28 @@ cudaError_t launch_tree_attention(const TreeAttention &a, int32_t D, kda_dtype d
         return launch_tree_attention_tc(a, D, workspace, stream);
     if (dt == KDA_BF16) KDA_DISPATCH_D(D, (run<__nv_bfloat16, DD>(a, workspace, stream)))
     else KDA_DISPATCH_D(D, (run<float, DD>(a, workspace, stream)))
+    return cudaErrorInvalidValue;
+}
+
+size_t prefix_attention_bytes(int32_t N, int32_t M, int32_t P, int32_t H, int32_t H_kv, int32_t D, kda_dtype dt,
+                              int32_t page_size) {
+    const size_t tc = tree_attention_tc_supported(H, H_kv, D, dt, 1, page_size)
+                          ? prefix_attention_tc_bytes(N, M, P, H, H_kv, D) : 0;
+    const size_t other = [&]() -> size_t {
+        if (dt == KDA_BF16) KDA_DISPATCH_D(D, (prefix_bytes<__nv_bfloat16, DD>(N, M, H, H_kv)))
+        else KDA_DISPATCH_D(D, (prefix_bytes<float, DD>(N, M, H, H_kv)))
+        return 0;
+    }();
+    return std::max(tc, other);
+}
+
+cudaError_t launch_prefix_attention(const PrefixAttention &a, int32_t D, kda_dtype dt, void *workspace,
+                                    cudaStream_t stream) {
+    // the form of the own keys' sums, whose units the join shares
+    if (tree_attention_tc_supported(a.t.H, a.t.H_kv, D, dt, a.t.num_pages, a.t.page_size))
+        return launch_prefix_attention_tc(a, D, workspace, stream);
+    if (dt == KDA_BF16) KDA_DISPATCH_D(D, (run_prefix<__nv_bfloat16, DD>(a, workspace, stream)))
+    else KDA_DISPATCH_D(D, (run_prefix<float, DD>(a, workspace, stream)))
     return cudaErrorInvalidValue;
 }
 

@@ -47,21 +47,17 @@
 #include "kda_internal.cuh"
 #include "kda_tc.cuh"
 #include "kda_tree.cuh"
+#include "kda_attention_tc.cuh"
 #include "kda_tree_cut.cuh"
 
-#include <cuda.h>
 #include <math.h>
 
-#include <algorithm>
+#include <type_traits>
 
 namespace kda {
 namespace {
 
 using namespace tc;
-
-constexpr int kTile = 128;                 // rows per row tile, keys per key tile
-constexpr float kGrow = 8.f;               // log2 growth of the maximum that rescales the sums
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int D, int QT> struct Cfg {
     static constexpr int HALVES = D / 64;
@@ -123,29 +119,13 @@ struct Shape {
                             // in the part with the unit's last tile)
 };
 
-// 64 bytes of a row, in whole 32-byte sectors where the address allows it
-__device__ __forceinline__ void store64(void *to, const uint32_t (&u)[16], bool aligned32) {
-    if (aligned32) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                             static_cast<unsigned char *>(to) + 32 * e),
-                         "r"(u[8 * e]), "r"(u[8 * e + 1]), "r"(u[8 * e + 2]), "r"(u[8 * e + 3]), "r"(u[8 * e + 4]),
-                         "r"(u[8 * e + 5]), "r"(u[8 * e + 6]), "r"(u[8 * e + 7])
-                         : "memory");
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            reinterpret_cast<uint4 *>(to)[e] = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
-    }
-}
-
 // keys of the unit's tile t
 __device__ __forceinline__ int valid_keys(const TreeAttention &a, const Run &run, int t) {
     return t == run.tiles - 1 ? last_tile(run.len, a.M).tree + a.M : min(kTile, run.len - t * kTile);
 }
 
-template <int D, int QT>
+// SUMS: the sums go to a.rows as they are, for the kernel that joins them with a prefix's.
+template <int D, int QT, bool SUMS>
 __global__ void __launch_bounds__(Cfg<D, QT>::THREADS, 1)
 tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention a, const Shape sh) {
     using C = Cfg<D, QT>;
@@ -589,7 +569,12 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                     }
                 }
                 if (!real) continue;
-                if (whole) {
+                if (whole && SUMS) {
+                    float4 *dst = reinterpret_cast<float4 *>(a.rows.o + o_row * D + x);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                } else if (whole) {
                     uint32_t u[16];
 #pragma unroll
                     for (int y = 0; y < 16; ++y)
@@ -603,7 +588,10 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                 }
             }
             if (real) {
-                if (whole) {
+                if (whole && SUMS) {
+                    a.rows.top[o_row] = top;
+                    a.rows.sum[o_row] = mine == 0 ? -1.f : sum;
+                } else if (whole) {
                     if (a.lse != nullptr) a.lse[o_row] = mine == 0 ? -INFINITY : (top + log2f(sum)) * kLn2;
                 } else {
                     float *ml = part + (size_t)R * D + t * kTile + wg;
@@ -627,7 +615,7 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
 // b - 1 and b, rows 16 y .. 16 y + 15 of its unit; it works when that is the
 // unit's first cut.  Block (0, 0) gathers the status.  Its launch overlaps the
 // kernel before it, whose results it waits for.
-template <int D, int QT>
+template <int D, int QT, bool SUMS>
 __global__ void __launch_bounds__(256)
 tree_attention_tc_join_kernel(const TreeAttention a, const Shape sh) {
     constexpr int R = QT * kTile, ROWS = 16;
@@ -682,8 +670,16 @@ tree_attention_tc_join_kernel(const TreeAttention a, const Shape sh) {
                 }
             }
         }
-        const float inv = 1.f / sum;
         const int64_t o_row = ((int64_t)p.n * a.M + node) * a.H + h * G + lr % kTile % G;
+        if (SUMS) {
+            *reinterpret_cast<float4 *>(a.rows.o + o_row * D + 4 * c4) = o;
+            if (c4 == 0) {
+                a.rows.top[o_row] = top;
+                a.rows.sum[o_row] = none ? -1.f : sum;
+            }
+            continue;
+        }
+        const float inv = 1.f / sum;
         *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + o_row * D + 4 * c4) =
             none ? make_uint2(0u, 0u)
                  : make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
@@ -691,55 +687,13 @@ tree_attention_tc_join_kernel(const TreeAttention a, const Shape sh) {
     }
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static const EncodeTiledFn fn = [] {
-        cudaDriverEntryPointQueryResult q;
-        void *p = nullptr;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess || q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeTiledFn>(p);
-    }();
-    return fn;
-}
-
-bool make_map(CUtensorMap *map, const void *base, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3],
-              const cuuint32_t (&box)[4]) {
-    const cuuint32_t ones[4] = {1, 1, 1, 1};
-    return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, ones,
-                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// The cache as groups of eight rows: [groups][D/64 halves][8 rows][64], so that
-// a box lands as whole 128-byte-swizzle blocks, the halves of a row next to
-// each other.
-bool cache_map(CUtensorMap *map, const void *base, const TreeAttention &a, int D, int box) {
-    const cuuint64_t groups = (cuuint64_t)a.num_pages * a.H_kv * a.page_size / 8;
-    return make_map(map, base, {64, 8, (cuuint64_t)(D / 64), groups}, {(cuuint64_t)D * 2, 128, (cuuint64_t)D * 16},
-                    {64, 8, (cuuint32_t)(D / 64), (cuuint32_t)(box / 8)});
-}
-// The queries [N * M][H][D]: a row tile's nodes, the query heads of one cache head, half a row.
-bool query_map(CUtensorMap *map, const TreeAttention &a, int D, int nodes) {
-    return make_map(map, a.q, {64, (cuuint64_t)a.H, (cuuint64_t)(D / 64), (cuuint64_t)a.N * a.M},
-                    {(cuuint64_t)D * 2, 128, (cuuint64_t)a.H * D * 2},
-                    {64, (cuuint32_t)(a.H / a.H_kv), 1, (cuuint32_t)nodes});
-}
 // The drafted rows [N * M][H_kv][D], eight rows of one head per box.
 bool new_map(CUtensorMap *map, const void *base, const TreeAttention &a, int D) {
     return make_map(map, base, {64, (cuuint64_t)a.N * a.M, (cuuint64_t)(D / 64), (cuuint64_t)a.H_kv},
                     {(cuuint64_t)a.H_kv * D * 2, 128, (cuuint64_t)D * 2}, {64, 8, (cuuint32_t)(D / 64), 1});
 }
 
-// as many whole nodes as 128 rows hold (their query heads are G rows each)
-int nodes_per_tile(int M, int H, int H_kv) { return std::min(M, kTile / (H / H_kv)); }
-
-template <int D, int QT> cudaError_t run_tc(const TreeAttention &a, void *workspace, cudaStream_t stream) {
+template <int D, int QT, bool SUMS> cudaError_t run_tc(const TreeAttention &a, void *workspace, cudaStream_t stream) {
     using C = Cfg<D, QT>;
     Maps maps;
     Shape sh;
@@ -756,9 +710,9 @@ template <int D, int QT> cudaError_t run_tc(const TreeAttention &a, void *worksp
     sh.places = static_cast<Place *>(workspace);
     sh.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + place_bytes(sh.ctas));
     static std::atomic<uint64_t> smem_set{0};
-    cudaError_t e = allow_dynamic_smem(tree_attention_tc_kernel<D, QT>, C::SMEM, smem_set);
+    cudaError_t e = allow_dynamic_smem(tree_attention_tc_kernel<D, QT, SUMS>, C::SMEM, smem_set);
     if (e != cudaSuccess) return e;
-    tree_attention_tc_kernel<D, QT><<<sh.ctas, C::THREADS, C::SMEM, stream>>>(maps, a, sh);
+    tree_attention_tc_kernel<D, QT, SUMS><<<sh.ctas, C::THREADS, C::SMEM, stream>>>(maps, a, sh);
     count_launches(1);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int blocks = QT == 1 ? (sh.nodes * (a.H / a.H_kv) + 15) / 16 : QT * kTile / 16;
@@ -771,7 +725,7 @@ template <int D, int QT> cudaError_t run_tc(const TreeAttention &a, void *worksp
     cfg.stream = stream;
     cfg.attrs = &overlap;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, tree_attention_tc_join_kernel<D, QT>, a, sh);
+    e = cudaLaunchKernelEx(&cfg, tree_attention_tc_join_kernel<D, QT, SUMS>, a, sh);
     if (e != cudaSuccess) {
         (void)cudaGetLastError();                            // reported here
         return e;
@@ -796,8 +750,12 @@ size_t tree_attention_tc_partial_bytes(int32_t M, int32_t H, int32_t H_kv, int32
 
 cudaError_t launch_tree_attention_tc(const TreeAttention &a, int32_t D, void *workspace, cudaStream_t stream) {
     const bool one = a.M <= nodes_per_tile(a.M, a.H, a.H_kv);
-    if (D == 64) return one ? run_tc<64, 1>(a, workspace, stream) : run_tc<64, 2>(a, workspace, stream);
-    return one ? run_tc<128, 1>(a, workspace, stream) : run_tc<128, 2>(a, workspace, stream);
+    auto pick = [&](auto rows) {
+        constexpr bool R = decltype(rows)::value;
+        if (D == 64) return one ? run_tc<64, 1, R>(a, workspace, stream) : run_tc<64, 2, R>(a, workspace, stream);
+        return one ? run_tc<128, 1, R>(a, workspace, stream) : run_tc<128, 2, R>(a, workspace, stream);
+    };
+    return a.rows.o != nullptr ? pick(std::true_type{}) : pick(std::false_type{});
 }
 
 }  // namespace kda

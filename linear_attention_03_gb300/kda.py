@@ -36,7 +36,8 @@ SYMBOLS = ("kda_prefill_workspace_size", "kda_prefill", "kda_decode_step",
            "kda_prologue_prefill_workspace_size", "kda_prologue_prefill",
            "kda_prefill_snapshots", "kda_decode_tree", "kda_decode_commit",
            "kda_tree_attention_workspace_size", "kda_tree_attention",
-           "kda_verify_drafts", "kda_cache_append", "kda_head_norm_rope")
+           "kda_verify_drafts", "kda_cache_append", "kda_head_norm_rope",
+           "kda_prefix_attention_workspace_size", "kda_prefix_attention")
 
 
 class kda_dims(ctypes.Structure):
@@ -77,6 +78,10 @@ lib.kda_cache_append.argtypes = [_P, _P, _P, _P, _P, _P, _i32, _i32, _i32, _i32,
                                  _P, _P, _P, _P]
 lib.kda_head_norm_rope.argtypes = [_P, _i64, _P, _i64, _P, _P, _i32, _P, _P, _i64, _i32, kda_dims, _i32,
                                    ctypes.c_float, _P, _i64, _P, _i64, _P]
+lib.kda_prefix_attention_workspace_size.argtypes = [kda_dims, _i32, _i32, _i32, _i32, _i32, _i32, _i32]
+lib.kda_prefix_attention_workspace_size.restype = _sz
+lib.kda_prefix_attention.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _i32, _i32,
+                                     _i32, _i32, ctypes.c_float, kda_dims, _P, _P, _P, _sz, _P]
 lib.kda_selftest_wait.argtypes = [_i64, _P, _sz, _P]
 lib.kda_selftest_wait.restype = ctypes.c_int
 lib.kda_last_error.argtypes = []
@@ -89,7 +94,8 @@ for _fn in (lib.kda_prefill, lib.kda_prefill_snapshots, lib.kda_prefill_segmente
             lib.kda_get_device_status,
             lib.kda_decode_step_conv, lib.kda_decode_verify, lib.kda_output_gate,
             lib.kda_decode_tree, lib.kda_decode_commit, lib.kda_tree_attention,
-            lib.kda_verify_drafts, lib.kda_cache_append, lib.kda_head_norm_rope):
+            lib.kda_verify_drafts, lib.kda_cache_append, lib.kda_head_norm_rope,
+            lib.kda_prefix_attention):
     _fn.restype = ctypes.c_int
 
 
@@ -691,6 +697,66 @@ def kda_head_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, 
     if st != KDA_OK:
         raise KDAError(st, "kda_head_norm_rope")
     return q_out, k_out
+
+
+def kda_prefix_attention_workspace_size(H: int, H_kv: int, d: int, dtype: torch.dtype, N: int, M: int, P: int,
+                                        page_size: int, max_prefix_pages: int, max_pages: int) -> int:
+    code = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
+    return int(lib.kda_prefix_attention_workspace_size(kda_dims(H, d, d, code), H_kv, N, M, P, page_size,
+                                                       max_prefix_pages, max_pages))
+
+
+def kda_prefix_attention(q, k_new, v_new, k_cache, v_cache, prefix_table, prefix_lens, prefix_seqs, page_table,
+                         cache_lens, parent, scale=None, out=None, lse=None, want_lse=False, workspace=None):
+    """kda_tree_attention whose sequences also see the prefix that they share, read
+    once for all of them; returns (out, lse), lse None unless given or asked for.
+
+    prefix_seqs [P + 1] int32: prefix p is that of sequences prefix_seqs[p] ..
+    prefix_seqs[p+1]-1; prefix_table [P, max_prefix_pages], prefix_lens [P] int32:
+    its pages and tokens, in the same pools as the sequences' own (page_table,
+    cache_lens), which follow it.  The other arguments as kda_tree_attention; a
+    page, a length or an offset out of range is reported in the workspace's
+    status word alone (kda_prefix_attention_workspace_size, kda_get_device_status)."""
+    rows, H, d = q.shape
+    N, M = _tree(parent, rows)
+    _dev(q, "q")
+    _dev(k_cache, "k_cache", q.dtype)
+    if k_cache.dim() != 4 or k_cache.shape[3] != d:
+        raise ValueError(f"k_cache must be [num_pages, H_kv, page_size, {d}], got {tuple(k_cache.shape)}")
+    num_pages, H_kv, page_size, _ = k_cache.shape
+    _dev(v_cache, "v_cache", q.dtype, k_cache.shape)
+    _dev(k_new, "k_new", q.dtype, (rows, H_kv, d))
+    _dev(v_new, "v_new", q.dtype, (rows, H_kv, d))
+    _dev(prefix_table, "prefix_table", torch.int32)
+    if prefix_table.dim() != 2:
+        raise ValueError(f"prefix_table must be [P, max_prefix_pages], got {tuple(prefix_table.shape)}")
+    P, max_prefix_pages = prefix_table.shape
+    _dev(prefix_lens, "prefix_lens", torch.int32, (P,))
+    _dev(prefix_seqs, "prefix_seqs", torch.int32, (P + 1,))
+    _dev(page_table, "page_table", torch.int32)
+    if page_table.dim() != 2 or page_table.shape[0] != N:
+        raise ValueError(f"page_table must be [{N}, max_pages], got {tuple(page_table.shape)}")
+    _dev(cache_lens, "cache_lens", torch.int32, (N,))
+    if out is None:
+        out = torch.empty_like(q)
+    _dev(out, "out", q.dtype, q.shape)
+    if lse is None and want_lse:
+        lse = torch.empty((rows, H), dtype=torch.float32, device=q.device)
+    _dev(lse, "lse", torch.float32, (rows, H))
+    dims, max_pages = dims_of(q), page_table.shape[1]
+    if workspace is None:
+        ws_bytes = int(lib.kda_prefix_attention_workspace_size(dims, H_kv, N, M, P, page_size, max_prefix_pages,
+                                                               max_pages))
+        workspace = torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device=q.device)
+    _dev(workspace, "workspace", torch.uint8)
+    st = lib.kda_prefix_attention(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
+                                  _ptr(prefix_table), _ptr(prefix_lens), _ptr(prefix_seqs), _ptr(page_table),
+                                  _ptr(cache_lens), _ptr(parent), N, M, P, H_kv, num_pages, page_size,
+                                  max_prefix_pages, max_pages, d ** -0.5 if scale is None else float(scale), dims,
+                                  _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _stream())
+    if st != KDA_OK:
+        raise KDAError(st, "kda_prefix_attention")
+    return out, lse
 
 
 def kda_get_device_status(workspace) -> int:

@@ -27,3 +27,50 @@ def norm_rope(x, positions, inv_freq, weight=None, eps=1e-6, interleaved=False):
 
 # pi to the 64 bits of the extended type (on machines where that is a double, angles are taken there)
 PI = np.longdouble("3.14159265358979323846264338327950288")
+
+
+def prefix_attention(q, k_new, v_new, k_cache, v_cache, ptable, plens, seqs, table, lens, parent, scale):
+    """(out, lse, weight) as tree_ref.attention, over each sequence's prefix, own keys and line."""
+    N, M = parent.shape
+    H, d = q.shape[1:]
+    Hkv, page = k_cache.shape[1:3]
+    G = H // Hkv
+    out, wt = np.zeros((N * M, H, d)), np.zeros((N * M, H, d))
+    lse = np.full((N * M, H), -np.inf)
+
+    def keys(pages, count):
+        pos = np.arange(count)
+        return [c[pages[pos // page], :, pos % page] for c in (k_cache, v_cache)]       # [count, Hkv, d]
+
+    for n in range(N):
+        own = keys(table[n], lens[n])
+        for p in range(len(plens)):
+            if seqs[p] <= n < seqs[p + 1]:
+                own = [np.concatenate([a, b]) for a, b in zip(keys(ptable[p], plens[p]), own)]
+        for m, line in enumerate(tree_ref.lines(parent[n])):
+            if not line:
+                continue
+            rows = [n * M + j for j in line]
+            K, V = np.concatenate([own[0], k_new[rows]]), np.concatenate([own[1], v_new[rows]])
+            for h in range(Hkv):
+                at = slice(h * G, (h + 1) * G)
+                s = scale * (q[n * M + m, at] @ K[:, h].T)
+                top = s.max(-1, keepdims=True)
+                e = np.exp(s - top)
+                z = e.sum(-1, keepdims=True)
+                lse[n * M + m, at] = (top + np.log(z))[:, 0]
+                out[n * M + m, at] = e @ V[:, h] / z
+                wt[n * M + m, at] = e @ np.abs(V[:, h]) / z
+    return out, lse, wt
+
+
+def prefix_inputs(N, M, H, Hkv, d, page, lens, plens, seqs, dtype, rng):
+    """Pages of all sequences and prefixes in one pool in random order; what is past a length holds NaN."""
+    import torch
+    x = tree_ref.cache_inputs(N + len(plens), M, H, Hkv, d, page, list(lens) + list(plens), dtype, rng)
+    for name in ("q", "k_new", "v_new"):
+        x[name] = x[name][:N * M].contiguous()
+    table, all_lens = x.pop("page_table"), x.pop("cache_lens")
+    x.update(page_table=table[:N].contiguous(), prefix_table=table[N:].contiguous(), cache_lens=all_lens[:N].contiguous(),
+             prefix_lens=all_lens[N:].contiguous(), prefix_seqs=torch.from_numpy(np.asarray(seqs, np.int32)))
+    return x

@@ -39,3 +39,25 @@ def test_head_norm_rope_argument_checks(kda, ptrs):
     assert call(qo=p, qs=97 * 128) == kda.KDA_ERR_INVALID and "in place" in kda.kda_last_error()
     assert call(d=dims(kda, d=256)) == kda.KDA_ERR_UNSUPPORTED
     assert call(d=dims(kda, dt=2)) == kda.KDA_ERR_UNSUPPORTED
+
+
+def test_prefix_attention_argument_checks(kda, ptrs):
+    p, mis = ptrs
+    size = lambda **a: kda.lib.kda_prefix_attention_workspace_size(
+        a.get("d", dims(kda)), a.get("Hkv", 8), a.get("N", 2), a.get("M", 8), a.get("P", 1), a.get("page", 16),
+        a.get("mpp", 9), a.get("mp", 10))
+    assert size() >= 256 and size(P=0) >= 256 and size(P=0, mpp=0) >= 256
+    for bad in (dict(Hkv=7), dict(page=0), dict(mp=0), dict(mpp=0), dict(M=65), dict(N=0), dict(P=-1), dict(P=65536)):
+        assert size(**bad) == 0
+    call = lambda **a: kda.lib.kda_prefix_attention(
+        a.get("q", p), p, p, p, p, a.get("pt", p), a.get("pl", p), a.get("ps", p), a.get("table", p), p, p,
+        a.get("N", 2), a.get("M", 8), a.get("P", 1), a.get("Hkv", 8), a.get("np", 20), a.get("page", 16),
+        a.get("mpp", 9), a.get("mp", 10), a.get("scale", 0.1), a.get("d", dims(kda)), p, a.get("lse", None),
+        a.get("ws", p), a.get("wsb", 1 << 40), None)
+    assert call(N=0) == kda.KDA_OK
+    for bad in (dict(Hkv=7), dict(Hkv=0), dict(np=0), dict(page=0), dict(mp=0), dict(mpp=0), dict(P=-1), dict(P=65536),
+                dict(mpp=2 ** 28), dict(q=None), dict(q=mis), dict(pt=None), dict(pl=None), dict(ps=None),
+                dict(table=None), dict(ws=None), dict(ws=mis), dict(lse=ctypes.c_void_p(FAKE + 2)), dict(wsb=size() - 1),
+                dict(N=2 ** 20, M=8), dict(scale=0.0), dict(scale=float("nan"))):
+        assert call(**bad) == kda.KDA_ERR_INVALID, bad
+    assert call(M=65) == kda.KDA_ERR_UNSUPPORTED and call(d=dims(kda, d=96)) == kda.KDA_ERR_UNSUPPORTED
