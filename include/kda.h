@@ -542,8 +542,8 @@ KDA_API size_t kda_prefix_attention_workspace_size(kda_dims dims, int32_t H_kv, 
  *          prefix's; they start a page of their own wherever the prefix ends
  *   the other arguments, the status word, the types, forms and roundings as
  *          kda_tree_attention; offsets out of order set KDA_DEVICE_BAD_OFFSETS
- *   workspace  kda_prefix_attention_workspace_size() bytes; calls that overlap on the GPU
- *          need one each
+ *   workspace  kda_prefix_attention_workspace_size() bytes, 256-byte aligned; calls that
+ *          overlap on the GPU need one each
  * Positions are the caller's: a key's rotation was applied when it was made.  P = 0 is
  * kda_tree_attention.  N * M * H must not exceed 2^29.  The same call gives the same bits.
  */

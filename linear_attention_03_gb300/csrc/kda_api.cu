@@ -686,6 +686,8 @@ kda_status kda_prefix_attention(const void *q, const void *k_new, const void *v_
     KDA_TRY(need(out, "out"));
     if (lse != nullptr) KDA_TRY(need4(lse, "lse"));
     KDA_TRY(need(workspace, "workspace"));
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return fail(KDA_ERR_INVALID, "workspace must be 256-byte aligned%s");
     const PrefixSpace space = prefix_space(dims, H_kv, N, M, P, page_size);
     if (workspace_bytes < space.all())
         return fail(KDA_ERR_INVALID, "workspace too small (see kda_prefix_attention_workspace_size)%s");

@@ -33,6 +33,18 @@ __device__ __forceinline__ void store64(void *to, const uint32_t (&u)[16], bool 
     }
 }
 
+// 32 sums of a row, whole 32-byte sectors (the workspace's rows start at multiples of 32 bytes)
+__device__ __forceinline__ void store_sums32(float *to, const float (&o)[32]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 8 * e),
+                     "r"(__float_as_uint(o[8 * e])), "r"(__float_as_uint(o[8 * e + 1])),
+                     "r"(__float_as_uint(o[8 * e + 2])), "r"(__float_as_uint(o[8 * e + 3])),
+                     "r"(__float_as_uint(o[8 * e + 4])), "r"(__float_as_uint(o[8 * e + 5])),
+                     "r"(__float_as_uint(o[8 * e + 6])), "r"(__float_as_uint(o[8 * e + 7]))
+                     : "memory");
+}
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,

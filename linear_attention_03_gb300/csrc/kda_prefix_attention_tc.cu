@@ -41,7 +41,7 @@ template <int D, int QT> struct Cfg {
     static constexpr int SLOTS = D == 64 ? 8 : (QT == 1 ? 6 : 5);
     static constexpr int O_RING = QT * SLOT;
     static constexpr int O_MISC = O_RING + SLOTS * SLOT;
-    static constexpr int PER_TILE = 4, NBARS = 2 * SLOTS + PER_TILE * QT + 3;
+    static constexpr int PER_TILE = 5, NBARS = 2 * SLOTS + PER_TILE * QT + 3;
     static constexpr int O_WORDS = O_MISC + 8 * NBARS;
     static constexpr int SMEM = O_MISC + 1024;
     static_assert(O_WORDS + 16 <= SMEM, "misc");
@@ -78,6 +78,7 @@ prefix_attention_tc_kernel(const __grid_constant__ Maps maps, const PrefixAttent
     auto s_full = [&](int t) { return tile_bar(t, 0); };
     auto p_full = [&](int t, uint32_t half) { return tile_bar(t, 1 + half); };
     auto o_full = [&](int t) { return tile_bar(t, 3); };
+    auto turn = [&](int t) { return tile_bar(t, 4); };
     const uint32_t q_full = tile_bar(QT, 0), q_free = tile_bar(QT, 1), v_ready = tile_bar(QT, 2);
 
     const PrefixPlace place = find_prefix_place<kTile>(a, sh.units, sh.ctas, blockIdx.x);
@@ -89,7 +90,7 @@ prefix_attention_tc_kernel(const __grid_constant__ Maps maps, const PrefixAttent
         wait_prerequisites();                                // (the next kernel counts on the ones before this)
         return;
     }
-    Run run = prefix_run<kTile>(a, sh.units, place, stop);
+    Run run = prefix_run<kTile>(a, place, stop);
 
     if (warp == 0) tmem_alloc(base + C::O_WORDS + 4 * W_TMEM, 512);
     if (tid == 32) {
@@ -102,6 +103,7 @@ prefix_attention_tc_kernel(const __grid_constant__ Maps maps, const PrefixAttent
             mbar_init(p_full(t, 0), 128);
             mbar_init(p_full(t, 1), 128);
             mbar_init(o_full(t), 1);
+            mbar_init(turn(t), 1);
         }
         mbar_init(q_full, 1);
         mbar_init(q_free, QT);
@@ -191,35 +193,50 @@ prefix_attention_tc_kernel(const __grid_constant__ Maps maps, const PrefixAttent
         }
     } else if (warp <= QT) {
         // ---------------------------------------------------------------- products
-        // One elected thread of the warp issues a tile's products.
+        // One elected thread of the warp issues a tile's products: a step's sums with the next
+        // step's scores, in turns with the other tile's.  Side by side the tiles fell into step, so
+        // that both softmaxes ran while the tensor core stood still (3,380 clocks for 128 keys).
         const int t = warp - 1;
         constexpr uint32_t ID_QK = idesc_bf16(kTile, kTile, 0, 0), ID_PV = idesc_bf16(kTile, D, 0, 1);
         constexpr uint64_t HI_Q = sw128_hi(0, 1024), HI_K = sw128_hi(0, C::HALVES * 1024);
         constexpr uint64_t HI_V = sw128_hi(1024, C::HALVES * 1024);
         const uint32_t s_col = uniform(tmem + t * 128), o_col = uniform(tmem + C::TM_O + t * 128);
         const uint32_t qb = uniform(base + t * C::SLOT);
-        uint32_t use = 0, j = 0, seg = 0, cuts = 0;          // ring uses, tiles, segments, tiles cut short before
+        uint32_t j = 0, seg = 0, cuts = 0, turns = 0;        // tiles, segments, tiles cut short, turns before
+        // the ring's slot of tile i's keys (kv = 0) or values, and the wait for it
+        auto slot_of = [&](uint32_t i, uint32_t kv) { return uniform((2 * i + kv) % C::SLOTS); };
+        auto landed = [&](uint32_t i, uint32_t kv) {
+            return wait(full(slot_of(i, kv)), ((2 * i + kv) / C::SLOTS) & 1);
+        };
+        auto my_turn = [&]() {
+            const uint32_t n = turns++;
+            if (QT == 1 || (t == 0 && n == 0)) return ok;
+            return wait(turn(t), (t == 0 ? n - 1 : n) & 1);
+        };
+        auto your_turn = [&]() {
+            if (QT == 2 && lane == 0) mbar_arrive(turn(1 - t));
+            __syncwarp();
+        };
+        auto scores = [&](uint32_t i, bool last) {
+            const uint32_t s = slot_of(i, 0), at = uniform(base + C::O_RING + s * C::SLOT);
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+                mma_bf16_w(s_col, HI_Q | sw128_lo(qb + (ks >> 2) * 16384 + (ks & 3) * 32),
+                           HI_K | sw128_lo(at + (ks >> 2) * 1024 + (ks & 3) * 32), ID_QK, ks > 0);
+            mma_commit_w(s_full(t));
+            mma_commit_w(empty(s));                          // the keys are read
+            if (last) mma_commit_w(q_free);
+        };
         for (; run.left > 0 && ok; run.advance(a, sh.units), ++seg) {
             const int cnt = (int)uniform((uint32_t)run.count());
-            if (!wait(q_full, seg & 1)) break;
+            if (!wait(q_full, seg & 1) || !landed(j, 0) || !my_turn()) break;
+            scores(j, cnt == 1);
+            your_turn();
             for (int i = 0; i < cnt && ok; ++i, ++j) {
                 const int valid = (int)uniform((uint32_t)valid_keys(run, run.t0 + i));
-                uint32_t s = uniform(use % C::SLOTS);
-                if (!wait(full(s), (use / C::SLOTS) & 1)) break;
-                ++use;
-                tc_fence_after();
-                uint32_t at = uniform(base + C::O_RING + s * C::SLOT);
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                    mma_bf16_w(s_col, HI_Q | sw128_lo(qb + (ks >> 2) * 16384 + (ks & 3) * 32),
-                               HI_K | sw128_lo(at + (ks >> 2) * 1024 + (ks & 3) * 32), ID_QK, ks > 0);
-                mma_commit_w(s_full(t));
-                mma_commit_w(empty(s));                      // the keys are read
-                if (i == cnt - 1) mma_commit_w(q_free);
-                s = uniform(use % C::SLOTS);
-                if (!wait(full(s), (use / C::SLOTS) & 1)) break;
-                ++use;
-                at = uniform(base + C::O_RING + s * C::SLOT);
+                const uint32_t s = slot_of(j, 1), at = uniform(base + C::O_RING + s * C::SLOT);
+                if (!landed(j, 1)) break;
                 if (valid < kTile) {
                     if (t == 0) {
                         unsigned char *vs = smem + C::O_RING + s * C::SLOT;
@@ -238,10 +255,12 @@ prefix_attention_tc_kernel(const __grid_constant__ Maps maps, const PrefixAttent
                     }
                     ++cuts;
                 }
+                const bool next = i + 1 < cnt;
+                if (next && !landed(j + 1, 0)) break;
                 const uint32_t more = i > 0;                 // not the segment's first tile
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    if (!wait(p_full(t, half), j & 1)) break;
+                    if (!wait(p_full(t, half), j & 1) || (half == 0 && !my_turn())) break;
                     tc_fence_after();
 #pragma unroll
                     for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
@@ -251,7 +270,9 @@ prefix_attention_tc_kernel(const __grid_constant__ Maps maps, const PrefixAttent
                 }
                 if (!ok) break;
                 mma_commit_w(empty(s));                      // the values are read
-                if (i == cnt - 1) mma_commit_w(o_full(t));
+                if (next) scores(j + 1, i + 2 == cnt);
+                else mma_commit_w(o_full(t));
+                your_turn();
             }
         }
     } else if (warp >= 4) {
@@ -367,10 +388,7 @@ prefix_attention_tc_kernel(const __grid_constant__ Maps maps, const PrefixAttent
                     }
                     store64(out + o_row * D + x, u, out32);
                 } else {
-                    float4 *dst = reinterpret_cast<float4 *>(part) + (size_t)(x / 4) * R + t * kTile + wg;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        dst[(size_t)e * R] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    store_sums32(part + (size_t)(t * kTile + wg) * D + x, o);
                 }
             }
             if (real) {

@@ -48,8 +48,8 @@ struct RowUnits {
 struct PrefixPlace {
     int64_t total, start, unit0;    // tiles of the line, the piece's first one, where its unit starts
     int32_t p, r;                   // the prefix and the unit within it
+    int32_t tiles, groups, seq0, rows, len;     // of the unit's prefix, as in PrefixRun: the join needs no table
     int32_t status;
-    int32_t pad;
 };
 
 // A CTA's run through its piece.
@@ -86,28 +86,28 @@ template <int KEYS> struct PrefixRun {
 template <int KEYS>
 __device__ __forceinline__ PrefixPlace find_prefix_place(const PrefixAttention &a, const RowUnits &u, int ctas, int b) {
     const int lane = threadIdx.x & 31;
-    PrefixPlace out{0, 0, 0, 0, 0, KDA_DEVICE_OK, 0};
-    auto one = [&](int p, int32_t &tiles, int32_t &status) -> int64_t {
-        PrefixRun<KEYS> run;
-        run.p = p;
-        tiles = 1;
+    PrefixPlace out{0, 0, 0, 0, 0, 1, 1, 0, 0, 0, KDA_DEVICE_OK};
+    int32_t status = KDA_DEVICE_OK;
+    PrefixRun<KEYS> it;
+    auto one = [&](int p) -> int64_t {
+        it.p = p;
         if (p >= a.P) return 0;
-        status = max(status, run.load(a, u));
-        tiles = max(run.tiles, 1);
-        return run.line();
+        status = max(status, it.load(a, u));
+        return it.line();
     };
-    int32_t tiles, status = KDA_DEVICE_OK;
+    int64_t mine = 0;
     for (int p0 = 0; p0 < a.P; p0 += 32) {
-        int64_t mine = one(p0 + lane, tiles, status);
+        mine = one(p0 + lane);
+        int64_t sum = mine;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-        out.total += mine;
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        out.total += sum;
     }
     out.status = (int32_t)__reduce_max_sync(0xffffffffu, (unsigned)status);
     out.start = out.unit0 = piece_start(out.total, ctas, b);
     int64_t base = 0;
     for (int p0 = 0; p0 < a.P; p0 += 32) {
-        const int64_t mine = one(p0 + lane, tiles, status);
+        if (a.P > 32) mine = one(p0 + lane);
         int64_t run = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -118,11 +118,15 @@ __device__ __forceinline__ PrefixPlace find_prefix_place(const PrefixAttention &
         const uint32_t here = __ballot_sync(0xffffffffu, mine > 0 && out.start >= begin && out.start < begin + mine);
         if (here != 0) {
             const int src = __ffs(here) - 1;
-            const int its = __shfl_sync(0xffffffffu, tiles, src);
             const int64_t from = __shfl_sync(0xffffffffu, begin, src);
             out.p = p0 + src;
-            out.r = (int32_t)quotient(out.start - from, its);
-            out.unit0 = from + (int64_t)out.r * its;
+            out.tiles = __shfl_sync(0xffffffffu, it.tiles, src);
+            out.groups = __shfl_sync(0xffffffffu, it.groups, src);
+            out.seq0 = __shfl_sync(0xffffffffu, it.seq0, src);
+            out.rows = __shfl_sync(0xffffffffu, it.rows, src);
+            out.len = __shfl_sync(0xffffffffu, it.len, src);
+            out.r = (int32_t)quotient(out.start - from, out.tiles);
+            out.unit0 = from + (int64_t)out.r * out.tiles;
             break;
         }
         base += __shfl_sync(0xffffffffu, run, 31);
@@ -131,14 +135,18 @@ __device__ __forceinline__ PrefixPlace find_prefix_place(const PrefixAttention &
 }
 
 template <int KEYS>
-__device__ __forceinline__ PrefixRun<KEYS> prefix_run(const PrefixAttention &a, const RowUnits &u, const PrefixPlace &at,
-                                                      int64_t stop) {
+__device__ __forceinline__ PrefixRun<KEYS> prefix_run(const PrefixAttention &a, const PrefixPlace &at, int64_t stop) {
     PrefixRun<KEYS> run;
     run.left = stop - at.start;
     run.p = at.p;
     run.r = at.r;
     run.t0 = (int32_t)(at.start - at.unit0);
-    run.load(a, u);
+    run.tiles = at.tiles;
+    run.groups = at.groups;
+    run.units = at.groups * a.t.H_kv;
+    run.seq0 = at.seq0;
+    run.rows = at.rows;
+    run.len = at.len;
     return run;
 }
 
@@ -147,6 +155,7 @@ __device__ __forceinline__ PrefixRun<KEYS> prefix_run(const PrefixAttention &a, 
 template <bool EXP2> struct RowJoin {
     float prefix, own, lse;
     bool none;
+    RowJoin() = default;
     __device__ __forceinline__ RowJoin(float top, float sum, float own_top, float own_sum) {
         none = own_sum < 0.f;
         const float m = fmaxf(top, own_top), from = m == -INFINITY ? 0.f : m;
@@ -156,6 +165,10 @@ template <bool EXP2> struct RowJoin {
         prefix = none ? 0.f : x / z;
         own = none ? 0.f : y / z;
         lse = none ? -INFINITY : EXP2 ? (m + log2f(z)) * 0.6931471805599453f : m + logf(z);
+    }
+    __device__ __forceinline__ float2 operator()(float2 o, float2 own_o) const {
+        if (none) return make_float2(0.f, 0.f);
+        return make_float2(prefix * o.x + own * own_o.x, prefix * o.y + own * own_o.y);
     }
     __device__ __forceinline__ float4 operator()(float4 o, float4 own_o) const {
         if (none) return make_float4(0.f, 0.f, 0.f, 0.f);
@@ -169,8 +182,8 @@ __device__ __forceinline__ void store_out4(__nv_bfloat16 *p, float4 o) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(tc::pack_bf16x2(o.x, o.y), tc::pack_bf16x2(o.z, o.w));
 }
 
-// The kernels' work space: a place per CTA, then two slots per CTA for pieces of units: D / 4 x
-// slots float4, slots maxima, slots sums.
+// The kernels' work space: a place per CTA, then two slots per CTA for pieces of units: the rows' D
+// sums one row after another, the rows' maxima, their sums of weights.
 struct PrefixShape {
     RowUnits units;
     int32_t ctas;
@@ -180,13 +193,16 @@ struct PrefixShape {
 inline size_t prefix_place_bytes(int ctas) { return ((size_t)ctas * sizeof(PrefixPlace) + 255) / 256 * 256; }
 inline size_t prefix_part_bytes(int ctas, int slots, int D) { return (size_t)ctas * 2 * slots * (D + 2) * 4; }
 
-constexpr int kJoinRows = 16;
+// Small blocks, four sums of two rows to a thread: a unit that is cut into many pieces has to be read
+// by many SMs at once, and a block's time is the latency of its few reads.
+constexpr int kJoinThreads = 128, kJoinAtOnce = 2;
+template <int D> constexpr int kJoinRows = kJoinThreads * 4 / D;        // rows at a time
 
-// Block (b, y), 0 < b < ctas: the cut between CTAs b - 1 and b, sixteen rows of its unit, when
+// Block (b, y), 0 < b < ctas: the cut between CTAs b - 1 and b, 2 kJoinRows rows of its unit, when
 // that is the unit's first cut.  Blocks (0, y): the status.  Block (ctas + n, y): sequence n's rows,
 // when no prefix reaches them: their own sums alone.
 template <typename Tout, int D, int KEYS, bool EXP2>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kJoinThreads)
 prefix_join_kernel(const PrefixAttention a, const PrefixShape sh) {
     const int b = blockIdx.x, G = a.t.H / a.t.H_kv, tid = threadIdx.x;
     Tout *out = static_cast<Tout *>(a.t.out);
@@ -194,7 +210,7 @@ prefix_join_kernel(const PrefixAttention a, const PrefixShape sh) {
     if (b == 0) {
         if (blockIdx.y != 0) return;
         int32_t code = 0;
-        for (int i = tid; i < sh.ctas; i += 256) code = max(code, sh.places[i].status);
+        for (int i = tid; i < sh.ctas; i += kJoinThreads) code = max(code, sh.places[i].status);
         const bool timeout = __syncthreads_or(code == KDA_DEVICE_TIMEOUT) != 0;
         const bool offsets = __syncthreads_or(code == KDA_DEVICE_BAD_OFFSETS) != 0;
         const bool page = __syncthreads_or(code == KDA_DEVICE_BAD_PAGE) != 0;
@@ -205,15 +221,16 @@ prefix_join_kernel(const PrefixAttention a, const PrefixShape sh) {
         return;
     }
     if (b >= sh.ctas) {
+        if (blockIdx.y >= 8) return;
         const int n = b - sh.ctas;
         bool covered = false;
-        for (int p = tid; p < a.P; p += 256) {
+        for (int p = tid; p < a.P; p += kJoinThreads) {
             const Prefix x = prefix_at(a, p);
             covered = covered || (x.len > 0 && n >= x.seq0 && n < x.seq0 + x.seqs);
         }
         if (__syncthreads_or(covered) != 0) return;
         const int64_t rows = (int64_t)a.t.M * a.t.H, items = rows * (D / 4);
-        for (int64_t i = (int64_t)blockIdx.y * 256 + tid; i < items; i += (int64_t)gridDim.y * 256) {
+        for (int64_t i = (int64_t)blockIdx.y * kJoinThreads + tid; i < items; i += (int64_t)min(gridDim.y, 8u) * kJoinThreads) {
             const int64_t row = n * rows + i / (D / 4);
             const int c = (int)(i % (D / 4)) * 4;
             const RowJoin<EXP2> join(-INFINITY, 0.f, a.t.rows.top[row], a.t.rows.sum[row]);
@@ -226,49 +243,67 @@ prefix_join_kernel(const PrefixAttention a, const PrefixShape sh) {
     const PrefixPlace p = sh.places[b];
     const int64_t before = sh.places[b - 1].start;
     if (p.start >= p.total || p.unit0 == p.start || before > p.unit0) return;
-    const PrefixRun<KEYS> run = prefix_run<KEYS>(a, sh.units, p, p.start + 1);
-    const int parts = first_past(p.total, sh.ctas, p.unit0 + run.tiles) - (b - 1), slots = sh.units.slots();
-    const int h = run.r / run.groups, row0 = run.r % run.groups * sh.units.rows();
+    const int parts = first_past(p.total, sh.ctas, p.unit0 + p.tiles) - (b - 1), slots = sh.units.slots();
+    const int h = p.r / p.groups, row0 = p.r % p.groups * sh.units.rows();
     // part i is CTA b - 1 + i's: its last segment for the first, its first one after that
     auto part_of = [&](int i) { return sh.part + (size_t)(2 * (b - 1 + i) + (i == 0 ? 1 : 0)) * slots * (D + 2); };
-    for (int e = tid; e < kJoinRows * (D / 4); e += 256) {
-        const int lr = blockIdx.y * kJoinRows + e % kJoinRows, c4 = e / kJoinRows;
-        const int in_tile = lr % sh.units.tile, row = row0 + lr / sh.units.tile * sh.units.used + in_tile;
-        if (lr >= slots || in_tile >= sh.units.used || row >= run.rows) continue;
-        const int64_t o_row = ((int64_t)run.seq0 * a.t.M + row / G) * a.t.H + h * G + row % G;
-        const float own_top = a.t.rows.top[o_row], own_sum = a.t.rows.sum[o_row];
-        const float4 own = *reinterpret_cast<const float4 *>(a.t.rows.o + o_row * D + 4 * c4);
-        float top = -INFINITY, sum = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i0 = 0; i0 < parts; i0 += 8) {
-            // eight parts at a time, so that their reads are under way together
-            float x[8], z[8];
-            float4 y[8];
+    const int c = tid % (D / 4) * 4;
+    int lr[kJoinAtOnce];
+    int64_t o_row[kJoinAtOnce];             // -1: none
+    float own_top[kJoinAtOnce], own_sum[kJoinAtOnce], top[kJoinAtOnce], sum[kJoinAtOnce];
+    float4 own[kJoinAtOnce], o[kJoinAtOnce];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+    for (int y = 0; y < kJoinAtOnce; ++y) {
+        lr[y] = (blockIdx.y * kJoinAtOnce + y) * kJoinRows<D> + tid / (D / 4);
+        const int in_tile = lr[y] % sh.units.tile, row = row0 + lr[y] / sh.units.tile * sh.units.used + in_tile;
+        const bool real = lr[y] < slots && in_tile < sh.units.used && row < p.rows;
+        o_row[y] = real ? ((int64_t)p.seq0 * a.t.M + row / G) * a.t.H + h * G + row % G : -1;
+        own_top[y] = real ? a.t.rows.top[o_row[y]] : 0.f;
+        own_sum[y] = real ? a.t.rows.sum[o_row[y]] : -1.f;
+        top[y] = -INFINITY;
+        sum[y] = 0.f;
+        own[y] = o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (real) own[y] = *reinterpret_cast<const float4 *>(a.t.rows.o + o_row[y] * D + c);
+        else lr[y] = 0;
+    }
+    for (int i0 = 0; i0 < parts; i0 += 4) {
+        // four parts of two rows at a time, so that their reads are under way together
+        float x[kJoinAtOnce][4], z[kJoinAtOnce][4];
+        float4 v[kJoinAtOnce][4];
+#pragma unroll
+        for (int y = 0; y < kJoinAtOnce; ++y)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
                 const float *q = part_of(min(i0 + i, parts - 1));
-                x[i] = i0 + i < parts ? q[(size_t)slots * D + lr] : -INFINITY;
-                z[i] = q[(size_t)slots * D + slots + lr];
-                y[i] = reinterpret_cast<const float4 *>(q)[(size_t)c4 * slots + lr];
+                x[y][i] = i0 + i < parts ? q[(size_t)slots * D + lr[y]] : -INFINITY;
+                z[y][i] = q[(size_t)slots * D + slots + lr[y]];
+                v[y][i] = *reinterpret_cast<const float4 *>(q + (size_t)lr[y] * D + c);
             }
-            const float was = top;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, x[i]);
-            const float from = top == -INFINITY ? 0.f : top, shrink = EXP2 ? exp2f(was - from) : expf(was - from);
-            sum *= shrink;
-            o.x *= shrink; o.y *= shrink; o.z *= shrink; o.w *= shrink;
+        for (int y = 0; y < kJoinAtOnce; ++y) {
+            const float was = top[y];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4; ++i) top[y] = fmaxf(top[y], x[y][i]);
+            const float from = top[y] == -INFINITY ? 0.f : top[y], shrink = EXP2 ? exp2f(was - from) : expf(was - from);
+            sum[y] *= shrink;
+            o[y].x *= shrink; o[y].y *= shrink; o[y].z *= shrink; o[y].w *= shrink;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
                 if (i0 + i < parts) {
-                    const float w = EXP2 ? exp2f(x[i] - from) : expf(x[i] - from);
-                    sum += w * z[i];
-                    o.x += w * y[i].x; o.y += w * y[i].y; o.z += w * y[i].z; o.w += w * y[i].w;
+                    const float w = EXP2 ? exp2f(x[y][i] - from) : expf(x[y][i] - from);
+                    sum[y] += w * z[y][i];
+                    o[y].x += w * v[y][i].x; o[y].y += w * v[y][i].y;
+                    o[y].z += w * v[y][i].z; o[y].w += w * v[y][i].w;
                 }
             }
         }
-        const RowJoin<EXP2> join(top, sum, own_top, own_sum);
-        store_out4(out + o_row * D + 4 * c4, join(o, own));
-        if (c4 == 0 && a.t.lse != nullptr) a.t.lse[o_row] = join.lse;
+    }
+#pragma unroll
+    for (int y = 0; y < kJoinAtOnce; ++y) {
+        if (o_row[y] < 0) continue;
+        const RowJoin<EXP2> join(top[y], sum[y], own_top[y], own_sum[y]);
+        store_out4(out + o_row[y] * D + c, join(o[y], own[y]));
+        if (c == 0 && a.t.lse != nullptr) a.t.lse[o_row[y]] = join.lse;
     }
 }
 
@@ -279,8 +314,10 @@ cudaError_t launch_prefix_join(const PrefixAttention &a, const PrefixShape &sh, 
     overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     overlap.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)sh.ctas + a.t.N, (unsigned)((sh.units.tiles * sh.units.tile + kJoinRows - 1) / kJoinRows));
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3((unsigned)sh.ctas + a.t.N,
+                       (unsigned)((sh.units.tiles * sh.units.tile + kJoinAtOnce * kJoinRows<D> - 1) /
+                                  (kJoinAtOnce * kJoinRows<D>)));
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cfg.attrs = &overlap;
     cfg.numAttrs = 1;

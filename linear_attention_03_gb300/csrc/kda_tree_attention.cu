@@ -219,7 +219,7 @@ tree_attention_kernel(const Args args, const typename std::conditional<std::is_s
             if (tid == 0) sh.places[blockIdx.x] = first;
             status = first.status;
             left = stop - first.start;
-            return left > 0 ? prefix_run<kKeys>(args, sh.units, first, stop) : PrefixRun<kKeys>{};
+            return left > 0 ? prefix_run<kKeys>(args, first, stop) : PrefixRun<kKeys>{};
         } else {
             __shared__ int64_t buf[34];
             Place first;
@@ -555,7 +555,7 @@ tree_attention_kernel(const Args args, const typename std::conditional<std::is_s
                                join(o, *reinterpret_cast<const float4 *>(a.rows.o + o_row * D + c)));
                     if (c == 0 && a.lse != nullptr) a.lse[o_row] = join.lse;
                 } else {
-                    reinterpret_cast<float4 *>(part)[(size_t)(c / 4) * crows + lr] = o;
+                    *reinterpret_cast<float4 *>(part + lr * D + c) = o;
                     if (c == 0) {
                         part[crows * D + lr] = x;
                         part[crows * D + crows + lr] = z;
@@ -596,6 +596,7 @@ template <typename Tin, int D>
 __global__ void __launch_bounds__(256)
 tree_attention_join_kernel(const TreeAttention a, const Shape sh) {
     const int b = blockIdx.x, G = a.H / a.H_kv, crows = gridDim.y * kRowsPerWarp;
+    if (a.rows.o != nullptr) tc::launch_dependents();       // the prefix's kernel, which waits before it takes the sums
     tc::wait_prerequisites();
     if (b == 0) {
         if (blockIdx.y == 0) gather_status(sh.places, sh.ctas, a.status);

@@ -570,16 +570,15 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                 }
                 if (!real) continue;
                 if (whole && SUMS) {
-                    float4 *dst = reinterpret_cast<float4 *>(a.rows.o + o_row * D + x);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    store_sums32(a.rows.o + o_row * D + x, o);
                 } else if (whole) {
                     uint32_t u[16];
 #pragma unroll
                     for (int y = 0; y < 16; ++y)
                         u[y] = mine == 0 ? 0u : pack_bf16x2(o[2 * y] * inv, o[2 * y + 1] * inv);
                     store64(out + o_row * D + x, u, out32);
+                } else if (SUMS) {                   // (one row after another, as the sums are joined)
+                    store_sums32(part + (size_t)(t * kTile + wg) * D + x, o);
                 } else {
                     float4 *dst = reinterpret_cast<float4 *>(part) + (size_t)(x / 4) * R + t * kTile + wg;
 #pragma unroll
@@ -621,6 +620,7 @@ tree_attention_tc_join_kernel(const TreeAttention a, const Shape sh) {
     constexpr int R = QT * kTile, ROWS = 16;
     const int b = blockIdx.x;
     const int G = a.H / a.H_kv;
+    if (SUMS) launch_dependents();                   // the prefix's kernel, which waits before it takes the sums
     wait_prerequisites();
     if (b == 0) {
         if (blockIdx.y != 0) return;
@@ -636,7 +636,7 @@ tree_attention_tc_join_kernel(const TreeAttention a, const Shape sh) {
     // part i is CTA b - 1 + i's: its last segment for the first, its first one after that
     auto part_of = [&](int i) { return sh.part + (size_t)(2 * (b - 1 + i) + (i == 0 ? 1 : 0)) * R * (D + 2); };
     for (int e = threadIdx.x; e < ROWS * (D / 4); e += 256) {
-        const int lr = blockIdx.y * ROWS + e % ROWS, c4 = e / ROWS;
+        const int lr = blockIdx.y * ROWS + (SUMS ? e / (D / 4) : e % ROWS), c4 = SUMS ? e % (D / 4) : e / ROWS;
         const int node = node0 + lr / kTile * sh.nodes + lr % kTile / G;
         if (lr >= R || lr % kTile >= sh.nodes * G || node >= a.M) continue;
         float top = -INFINITY, sum = 0.f;
@@ -651,7 +651,7 @@ tree_attention_tc_join_kernel(const TreeAttention a, const Shape sh) {
                 const float *q = part_of(min(i0 + i, parts - 1));
                 x[i] = i0 + i < parts ? q[(size_t)R * D + lr] : -INFINITY;
                 z[i] = q[(size_t)R * D + R + lr];
-                y[i] = reinterpret_cast<const float4 *>(q)[(size_t)c4 * R + lr];
+                y[i] = reinterpret_cast<const float4 *>(q)[SUMS ? (size_t)lr * (D / 4) + c4 : (size_t)c4 * R + lr];
             }
             float was = top;
 #pragma unroll

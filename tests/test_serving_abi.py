@@ -57,7 +57,7 @@ def test_prefix_attention_argument_checks(kda, ptrs):
     assert call(N=0) == kda.KDA_OK
     for bad in (dict(Hkv=7), dict(Hkv=0), dict(np=0), dict(page=0), dict(mp=0), dict(mpp=0), dict(P=-1), dict(P=65536),
                 dict(mpp=2 ** 28), dict(q=None), dict(q=mis), dict(pt=None), dict(pl=None), dict(ps=None),
-                dict(table=None), dict(ws=None), dict(ws=mis), dict(lse=ctypes.c_void_p(FAKE + 2)), dict(wsb=size() - 1),
+                dict(table=None), dict(ws=None), dict(ws=mis), dict(ws=ctypes.c_void_p(FAKE + 16)), dict(lse=ctypes.c_void_p(FAKE + 2)), dict(wsb=size() - 1),
                 dict(N=2 ** 20, M=8), dict(scale=0.0), dict(scale=float("nan"))):
         assert call(**bad) == kda.KDA_ERR_INVALID, bad
     assert call(M=65) == kda.KDA_ERR_UNSUPPORTED and call(d=dims(kda, d=96)) == kda.KDA_ERR_UNSUPPORTED
