@@ -12,11 +12,10 @@
 // Roles: warp 0 loads (TMA, one box per page or part of one), warps 1 and 2 issue the
 // products of one row tile each, and a warpgroup per row tile does the softmax with a
 // thread per row.  A tile's weights lie in the columns of its scores; while one
-// tile's softmax runs, the other tile's products do.  The weights of the first
-// 64 keys are handed over before the others are formed, so that their product does
-// not wait for these.  One thread issues all of a tile's products and the tensor core
-// takes them in that order: scores that are there mean sums that are done, and the next
-// scores do not overtake the sums that read the weights in their place.
+// tile's softmax runs, the other tile's products do: the two take turns at the tensor
+// core.  One thread issues all of a tile's products and the tensor core takes them in
+// that order: scores that are there mean sums that are done, and the next scores do not
+// overtake the sums that read the weights in their place.
 //
 // The sums are rescaled only when the maximum grows by more than 2^8; weights are rounded
 // to bf16 for their product (2^-9 of each), maximum, sums and output sums are fp32, as
@@ -41,7 +40,7 @@ template <int D, int QT> struct Cfg {
     static constexpr int SLOTS = D == 64 ? 8 : (QT == 1 ? 6 : 5);
     static constexpr int O_RING = QT * SLOT;
     static constexpr int O_MISC = O_RING + SLOTS * SLOT;
-    static constexpr int PER_TILE = 5, NBARS = 2 * SLOTS + PER_TILE * QT + 3;
+    static constexpr int PER_TILE = 4, NBARS = 2 * SLOTS + PER_TILE * QT + 3;
     static constexpr int O_WORDS = O_MISC + 8 * NBARS;
     static constexpr int SMEM = O_MISC + 1024;
     static_assert(O_WORDS + 16 <= SMEM, "misc");
@@ -76,9 +75,9 @@ prefix_attention_tc_kernel(const __grid_constant__ Maps maps, const PrefixAttent
     auto empty = [&](uint32_t s) { return bars + 8u * (C::SLOTS + s); };
     auto tile_bar = [&](int t, uint32_t i) { return bars + 8u * (2 * C::SLOTS + C::PER_TILE * t + i); };
     auto s_full = [&](int t) { return tile_bar(t, 0); };
-    auto p_full = [&](int t, uint32_t half) { return tile_bar(t, 1 + half); };
-    auto o_full = [&](int t) { return tile_bar(t, 3); };
-    auto turn = [&](int t) { return tile_bar(t, 4); };
+    auto p_full = [&](int t) { return tile_bar(t, 1); };
+    auto o_full = [&](int t) { return tile_bar(t, 2); };
+    auto turn = [&](int t) { return tile_bar(t, 3); };
     const uint32_t q_full = tile_bar(QT, 0), q_free = tile_bar(QT, 1), v_ready = tile_bar(QT, 2);
 
     const PrefixPlace place = find_prefix_place<kTile>(a, sh.units, sh.ctas, blockIdx.x);
@@ -100,8 +99,7 @@ prefix_attention_tc_kernel(const __grid_constant__ Maps maps, const PrefixAttent
         }
         for (int t = 0; t < QT; ++t) {
             mbar_init(s_full(t), 1);
-            mbar_init(p_full(t, 0), 128);
-            mbar_init(p_full(t, 1), 128);
+            mbar_init(p_full(t), 4);
             mbar_init(o_full(t), 1);
             mbar_init(turn(t), 1);
         }
@@ -132,6 +130,12 @@ prefix_attention_tc_kernel(const __grid_constant__ Maps maps, const PrefixAttent
     auto valid_keys = [&](const Run &r, int t) { return min(kTile, r.len - t * kTile); };
     auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
 
+    // of the 384 x 168 registers that the block has, most to the softmax (425 -> 392 us for 1,024 rows
+    // behind 16,384 keys): 128 x 72 + 256 x 208
+    if (QT == 2) {
+        if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    }
     if (warp == 0) {
         // ---------------------------------------------------------------- loads
         const int32_t none = (int32_t)((int64_t)a.t.num_pages * a.t.H_kv * a.t.page_size / 8);   // past the end: zeros
@@ -221,9 +225,11 @@ prefix_attention_tc_kernel(const __grid_constant__ Maps maps, const PrefixAttent
             const uint32_t s = slot_of(i, 0), at = uniform(base + C::O_RING + s * C::SLOT);
             tc_fence_after();
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
+            for (int ks = 0; ks < D / 16; ++ks) {
                 mma_bf16_w(s_col, HI_Q | sw128_lo(qb + (ks >> 2) * 16384 + (ks & 3) * 32),
                            HI_K | sw128_lo(at + (ks >> 2) * 1024 + (ks & 3) * 32), ID_QK, ks > 0);
+                if (ks == D / 16 - 3) your_turn();   // the other warp needs some 150 clocks to take it up
+            }
             mma_commit_w(s_full(t));
             mma_commit_w(empty(s));                          // the keys are read
             if (last) mma_commit_w(q_free);
@@ -232,7 +238,6 @@ prefix_attention_tc_kernel(const __grid_constant__ Maps maps, const PrefixAttent
             const int cnt = (int)uniform((uint32_t)run.count());
             if (!wait(q_full, seg & 1) || !landed(j, 0) || !my_turn()) break;
             scores(j, cnt == 1);
-            your_turn();
             for (int i = 0; i < cnt && ok; ++i, ++j) {
                 const int valid = (int)uniform((uint32_t)valid_keys(run, run.t0 + i));
                 const uint32_t s = slot_of(j, 1), at = uniform(base + C::O_RING + s * C::SLOT);
@@ -257,22 +262,27 @@ prefix_attention_tc_kernel(const __grid_constant__ Maps maps, const PrefixAttent
                 }
                 const bool next = i + 1 < cnt;
                 if (next && !landed(j + 1, 0)) break;
+                if (!my_turn() || !wait(p_full(t), j & 1)) break;
+                tc_fence_after();
                 const uint32_t more = i > 0;                 // not the segment's first tile
+                if (valid == kTile) {
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (!wait(p_full(t, half), j & 1) || (half == 0 && !my_turn())) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
-                        if (16 * ks < valid)
-                            mma_tmem_a_w(o_col, s_col + ks * 8, HI_V | sw128_lo(at + ks * 2 * C::HALVES * 1024), ID_PV,
-                                         ks > 0 ? 1u : more);
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_tmem_a_w(o_col, s_col + ks * 8, HI_V | sw128_lo(at + ks * 2 * C::HALVES * 1024), ID_PV,
+                                     ks > 0 ? 1u : more);
+                } else {
+#pragma unroll 1
+                    for (int ks = 0; 16 * ks < valid; ++ks)
+                        mma_tmem_a_w(o_col, s_col + ks * 8, HI_V | sw128_lo(at + ks * 2 * C::HALVES * 1024), ID_PV,
+                                     ks > 0 ? 1u : more);
                 }
-                if (!ok) break;
                 mma_commit_w(empty(s));                      // the values are read
-                if (next) scores(j + 1, i + 2 == cnt);
-                else mma_commit_w(o_full(t));
-                your_turn();
+                if (next) {
+                    scores(j + 1, i + 2 == cnt);
+                } else {
+                    mma_commit_w(o_full(t));
+                    your_turn();
+                }
             }
         }
     } else if (warp >= 4) {
@@ -335,24 +345,22 @@ prefix_attention_tc_kernel(const __grid_constant__ Maps maps, const PrefixAttent
                 const float2 f2 = make_float2(-from, -from);
                 float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
+                for (int x = 0; x < 4; ++x) {
+                    uint32_t w[16];
 #pragma unroll
-                    for (int x = 2 * half; x < 2 * half + 2; ++x) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float2 y = f2fma(make_float2(score(32 * x + 2 * e), score(32 * x + 2 * e + 1)), c2, f2);
-                            y.x = ex2(y.x);
-                            y.y = ex2(y.y);
-                            add[e & 1] = f2add(add[e & 1], y);
-                            w[e] = pack_bf16x2(y.x, y.y);
-                        }
-                        tmem_st16_nowait(s_col + 16 * x, w);
+                    for (int e = 0; e < 16; ++e) {
+                        float2 y = f2fma(make_float2(score(32 * x + 2 * e), score(32 * x + 2 * e + 1)), c2, f2);
+                        y.x = ex2(y.x);
+                        y.y = ex2(y.y);
+                        add[e & 1] = f2add(add[e & 1], y);
+                        w[e] = pack_bf16x2(y.x, y.y);
                     }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    mbar_arrive(p_full(t, half));
+                    tmem_st16_nowait(s_col + 16 * x, w);
                 }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(t));
                 sum += (add[0].x + add[0].y) + (add[1].x + add[1].y);
             }
             if (!ok || !wait(o_full(t), seg & 1)) break;
