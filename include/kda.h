@@ -86,6 +86,9 @@ typedef enum { KDA_F32 = 0, KDA_BF16 = 1 } kda_dtype;
 /* The most nodes a sequence's tree of drafted tokens may have. */
 #define KDA_MAX_TREE_NODES 64
 
+/* The largest vocabulary of kda_sample. */
+#define KDA_MAX_VOCABULARY 262144
+
 /* Prefix snapshots are taken every multiple of this many tokens into a document. */
 #define KDA_SNAPSHOT_ALIGN 64
 
@@ -556,6 +559,32 @@ KDA_API kda_status kda_prefix_attention(const void *q, const void *k_new, const 
                                         int32_t max_prefix_pages, int32_t max_pages, float scale, kda_dims dims,
                                         void *out, float *lse, void *workspace, size_t workspace_bytes,
                                         void *stream);
+
+/*
+ * From logits to a distribution and a token drawn from it, row by row: with weights
+ * w_i = exp((x_i - max x) / T) and the order by value, equal ones by index,
+ *   top-k  the first k of the order stay;
+ *   top-p  of these the shortest beginning whose weight is at least p times theirs (at
+ *          least one);
+ *   min-p  of these those with w_i >= m (the first always does);
+ *   token  the first index at which the weights that stay, added up in index order, exceed
+ *          u times their sum;   probs  w_i / sum where i stays, else zero.
+ *   logits [N, V] logits_dtype, from a row to the next `stride` elements (>= V); logits and
+ *          probs may start at any element; -infinity
+ *          and NaN are never drawn; beside +infinity all others count as -infinity
+ *   temperature, top_p, min_p, uniforms [N] fp32, top_k [N] int32, device; each may be NULL:
+ *          1, 1 (all), 0 (all), not needed without token, 0 (all).  A temperature that is not
+ *          above zero keeps the first of the order alone; top_k <= 0 or >= V, top_p >= 1 (or
+ *          NaN) and min_p <= 0 (or NaN) leave all.  uniforms in [0, 1), in steps of 2^-24.
+ *   token  [N] int32 or NULL: -1 where a row allows nothing (its probs are zeros)
+ *   probs  [N, V] probs_dtype, dense, or NULL; not both NULL.  kda_verify_drafts takes it.
+ * Weights are summed as whole multiples of 2^-42: results do not depend on the order of any
+ * sum.  A weight below 2^-43 is never drawn.  V <= KDA_MAX_VOCABULARY; N * 8 < 2^31.
+ */
+KDA_API kda_status kda_sample(const void *logits, int64_t stride, const float *temperature,
+                              const int32_t *top_k, const float *top_p, const float *min_p,
+                              const float *uniforms, int32_t N, int32_t V, int32_t logits_dtype,
+                              int32_t probs_dtype, int32_t *token, void *probs, void *stream);
 
 /*
  * Diagnostic of the bounded device-side waits (the method's sources have no

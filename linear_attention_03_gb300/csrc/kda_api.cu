@@ -711,6 +711,42 @@ kda_status kda_prefix_attention(const void *q, const void *k_new, const void *v_
     return KDA_OK;
 }
 
+kda_status kda_sample(const void *logits, int64_t stride, const float *temperature, const int32_t *top_k,
+                      const float *top_p, const float *min_p, const float *uniforms, int32_t N, int32_t V,
+                      int32_t logits_dtype, int32_t probs_dtype, int32_t *token, void *probs, void *stream) {
+    g_last_error[0] = '\0';
+    if (logits_dtype != KDA_F32 && logits_dtype != KDA_BF16)
+        return fail(KDA_ERR_UNSUPPORTED, "logits_dtype must be KDA_F32 or KDA_BF16%s");
+    if (probs != nullptr && probs_dtype != KDA_F32 && probs_dtype != KDA_BF16)
+        return fail(KDA_ERR_UNSUPPORTED, "probs_dtype must be KDA_F32 or KDA_BF16%s");
+    if (N < 0 || N > INT32_MAX / 8) return fail(KDA_ERR_INVALID, "N must be in [0, 2^28)%s");
+    if (V < 1) return fail(KDA_ERR_INVALID, "V must be >= 1%s");
+    if (V > KDA_MAX_VOCABULARY) return fail(KDA_ERR_UNSUPPORTED, "V must be <= 262144%s");
+    if (stride < V && N > 1) return fail(KDA_ERR_INVALID, "stride must be >= V%s");
+    if (N == 0) return KDA_OK;
+    if (token == nullptr && probs == nullptr) return fail(KDA_ERR_INVALID, "token and probs are both NULL%s");
+    auto whole = [](const void *x, int32_t dt) {
+        return (reinterpret_cast<uintptr_t>(x) & (dt == KDA_BF16 ? 1u : 3u)) == 0;
+    };
+    if (logits == nullptr) return fail(KDA_ERR_INVALID, "logits must not be NULL%s");
+    if (!whole(logits, logits_dtype)) return fail(KDA_ERR_INVALID, "logits must be aligned to an element%s");
+    if (probs != nullptr && !whole(probs, probs_dtype))
+        return fail(KDA_ERR_INVALID, "probs must be aligned to an element%s");
+    if (temperature != nullptr) KDA_TRY(need4(temperature, "temperature"));
+    if (top_k != nullptr) KDA_TRY(need4(top_k, "top_k"));
+    if (top_p != nullptr) KDA_TRY(need4(top_p, "top_p"));
+    if (min_p != nullptr) KDA_TRY(need4(min_p, "min_p"));
+    if (token != nullptr) {
+        KDA_TRY(need4(token, "token"));
+        KDA_TRY(need4(uniforms, "uniforms"));
+    }
+    cudaError_t err = kda::launch_sample(logits, stride, N, V, (kda_dtype)logits_dtype, temperature, top_k, top_p,
+                                         min_p, token != nullptr ? uniforms : nullptr, token, probs,
+                                         (kda_dtype)probs_dtype, static_cast<cudaStream_t>(stream));
+    if (err != cudaSuccess) return cuda_fail(err, "sampling launch");
+    return KDA_OK;
+}
+
 kda_status kda_selftest_wait(int64_t limit_ns, void *workspace, size_t workspace_bytes,
                              void *stream) {
     g_last_error[0] = '\0';

@@ -252,6 +252,10 @@ cudaError_t launch_head_norm_rope(const void *q, int64_t q_stride, const void *k
                                   int32_t H_kv, int32_t D, kda_dtype dt, bool interleaved, float eps, void *q_out,
                                   int64_t q_out_stride, void *k_out, int64_t k_out_stride, cudaStream_t stream);
 
+cudaError_t launch_sample(const void *logits, int64_t stride, int32_t N, int32_t V, kda_dtype dt, const float *temperature,
+                          const int32_t *top_k, const float *top_p, const float *min_p, const float *uniforms,
+                          int32_t *token, void *probs, kda_dtype probs_dt, cudaStream_t stream);
+
 cudaError_t launch_selftest_wait(uint64_t limit_ns, int32_t *status, cudaStream_t stream);
 
 // Tensor-core chunked prefill (d = 128, bf16 q/k/v).  With out_f32 set, the

@@ -28,6 +28,7 @@ KDA_DEVICE_OK, KDA_DEVICE_BAD_OFFSETS, KDA_DEVICE_TIMEOUT, KDA_DEVICE_RANGE, \
     KDA_DEVICE_BAD_SNAPSHOT, KDA_DEVICE_BAD_PAGE, KDA_DEVICE_BAD_LENGTH = range(7)
 KDA_MAX_TREE_NODES = 64
 KDA_SNAPSHOT_ALIGN = 64
+KDA_MAX_VOCABULARY = 262144
 SYMBOLS = ("kda_prefill_workspace_size", "kda_prefill", "kda_decode_step",
            "kda_prologue", "kda_get_device_status", "kda_last_error",
            "kda_kernel_launches", "kda_decode_step_conv", "kda_decode_verify",
@@ -37,7 +38,7 @@ SYMBOLS = ("kda_prefill_workspace_size", "kda_prefill", "kda_decode_step",
            "kda_prefill_snapshots", "kda_decode_tree", "kda_decode_commit",
            "kda_tree_attention_workspace_size", "kda_tree_attention",
            "kda_verify_drafts", "kda_cache_append", "kda_head_norm_rope",
-           "kda_prefix_attention_workspace_size", "kda_prefix_attention")
+           "kda_prefix_attention_workspace_size", "kda_prefix_attention", "kda_sample")
 
 
 class kda_dims(ctypes.Structure):
@@ -82,6 +83,7 @@ lib.kda_prefix_attention_workspace_size.argtypes = [kda_dims, _i32, _i32, _i32, 
 lib.kda_prefix_attention_workspace_size.restype = _sz
 lib.kda_prefix_attention.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _i32, _i32,
                                      _i32, _i32, ctypes.c_float, kda_dims, _P, _P, _P, _sz, _P]
+lib.kda_sample.argtypes = [_P, _i64, _P, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _P, _P, _P]
 lib.kda_selftest_wait.argtypes = [_i64, _P, _sz, _P]
 lib.kda_selftest_wait.restype = ctypes.c_int
 lib.kda_last_error.argtypes = []
@@ -95,7 +97,7 @@ for _fn in (lib.kda_prefill, lib.kda_prefill_snapshots, lib.kda_prefill_segmente
             lib.kda_decode_step_conv, lib.kda_decode_verify, lib.kda_output_gate,
             lib.kda_decode_tree, lib.kda_decode_commit, lib.kda_tree_attention,
             lib.kda_verify_drafts, lib.kda_cache_append, lib.kda_head_norm_rope,
-            lib.kda_prefix_attention):
+            lib.kda_prefix_attention, lib.kda_sample):
     _fn.restype = ctypes.c_int
 
 
@@ -757,6 +759,45 @@ def kda_prefix_attention(q, k_new, v_new, k_cache, v_cache, prefix_table, prefix
     if st != KDA_OK:
         raise KDAError(st, "kda_prefix_attention")
     return out, lse
+
+
+def kda_sample(logits, uniforms=None, temperature=None, top_k=None, top_p=None, min_p=None, token=None, probs=None,
+               want_probs=False):
+    """Temperature, top-k, top-p and min-p on logits [N, V] (bf16 or fp32; rows may
+    lie further apart), and a token per row drawn with `uniforms` [N] in [0, 1);
+    returns (token [N] int32, probs [N, V]).
+
+    Without uniforms there is no draw (token None); probs, the filtered
+    distribution as kda_verify_drafts takes it, is None unless given (bf16 or
+    fp32) or asked for (fp32).  temperature, top_p, min_p [N] fp32 and top_k [N]
+    int32, all optional: temperature 0 is the largest logit, top_k 0, top_p 1 and
+    min_p 0 leave all.  Equal logits are taken in the order of their indices."""
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
+        raise TypeError("logits must be a CUDA tensor")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [N, V], got {tuple(logits.shape)}")
+    N, V = logits.shape
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError("a row of logits must be dense")
+    code, dev, f32 = _dtype_code(logits), logits.device, torch.float32
+    _dev(uniforms, "uniforms", f32, (N,))
+    _dev(temperature, "temperature", f32, (N,))
+    _dev(top_k, "top_k", torch.int32, (N,))
+    _dev(top_p, "top_p", f32, (N,))
+    _dev(min_p, "min_p", f32, (N,))
+    if token is None and uniforms is not None:
+        token = torch.empty(N, dtype=torch.int32, device=dev)
+    _dev(token, "token", torch.int32, (N,))
+    if probs is None and want_probs:
+        probs = torch.empty((N, V), dtype=f32, device=dev)
+    if probs is not None:
+        _dev(probs, "probs", None, (N, V))
+    st = lib.kda_sample(_ptr(logits), logits.stride(0) if N > 1 else V, _ptr(temperature), _ptr(top_k), _ptr(top_p),
+                        _ptr(min_p), _ptr(uniforms), N, V, code, KDA_F32 if probs is None else _dtype_code(probs),
+                        _ptr(token), _ptr(probs), _stream())
+    if st != KDA_OK:
+        raise KDAError(st, "kda_sample")
+    return token, probs
 
 
 def kda_get_device_status(workspace) -> int:

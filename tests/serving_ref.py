@@ -74,3 +74,36 @@ def prefix_inputs(N, M, H, Hkv, d, page, lens, plens, seqs, dtype, rng):
     x.update(page_table=table[:N].contiguous(), prefix_table=table[N:].contiguous(), cache_lens=all_lens[:N].contiguous(),
              prefix_lens=all_lens[N:].contiguous(), prefix_seqs=torch.from_numpy(np.asarray(seqs, np.int32)))
     return x
+
+
+def sample_row(x, u=None, T=1.0, k=0, p=1.0, m=0.0, tol=0.0):
+    """One row (float64 values of the logits): (token, probs), from the definition.  `tol` moves the
+    weight that top-p asks for, relative to it."""
+    V = len(x)
+    x = np.where(np.isnan(x), -np.inf, x)
+    if np.isposinf(x).any():
+        x = np.where(np.isposinf(x), 0.0, -np.inf)
+    top = x.max()
+    probs = np.zeros(V)
+    if np.isneginf(top):
+        return -1, probs
+    order = np.lexsort((np.arange(V), -x))
+    if not T > 0:
+        order, T = order[:1], 1.0
+    w = np.exp((x - top) / T)
+    if 0 < k < V:
+        order = order[:k]
+    if p < 1:
+        mass = w[order]
+        before = np.concatenate([[0.0], np.cumsum(mass)[:-1]])
+        on = before < max(p, 0.0) * mass.sum() * (1 + tol)
+        on[0] = True
+        order = order[on]
+    if m > 0:
+        order = order[w[order] >= min(m, 1.0)]
+    probs[order] = w[order]
+    total = probs.sum()
+    token = None
+    if u is not None:
+        token = int(np.searchsorted(np.cumsum(probs), u * total, side="right"))
+    return token, probs / total

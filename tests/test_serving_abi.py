@@ -61,3 +61,17 @@ def test_prefix_attention_argument_checks(kda, ptrs):
                 dict(N=2 ** 20, M=8), dict(scale=0.0), dict(scale=float("nan"))):
         assert call(**bad) == kda.KDA_ERR_INVALID, bad
     assert call(M=65) == kda.KDA_ERR_UNSUPPORTED and call(d=dims(kda, d=96)) == kda.KDA_ERR_UNSUPPORTED
+
+
+def test_sample_argument_checks(kda, ptrs):
+    p, mis = ptrs
+    call = lambda **a: kda.lib.kda_sample(a.get("x", p), a.get("s", 100), a.get("T", None), a.get("k", None), None,
+                                          a.get("m", None), a.get("u", p), a.get("N", 2), a.get("V", 100),
+                                          a.get("dt", 0), a.get("pd", 0), a.get("tok", p), a.get("probs", None), None)
+    assert call(N=0) == kda.KDA_OK
+    for bad in (dict(N=-1), dict(N=2 ** 28), dict(V=0), dict(s=99), dict(tok=None), dict(x=None), dict(x=ctypes.c_void_p(FAKE + 2)),
+                dict(u=None), dict(probs=ctypes.c_void_p(FAKE + 2)), dict(T=ctypes.c_void_p(FAKE + 2)), dict(k=ctypes.c_void_p(FAKE + 1)),
+                dict(m=ctypes.c_void_p(FAKE + 3))):
+        assert call(**bad) == kda.KDA_ERR_INVALID, bad
+    assert call(V=262145, s=262145) == kda.KDA_ERR_UNSUPPORTED and call(dt=2) == kda.KDA_ERR_UNSUPPORTED
+    assert call(probs=p, pd=5) == kda.KDA_ERR_UNSUPPORTED
