@@ -26,12 +26,15 @@ namespace {
 
 typedef unsigned long long u64;
 constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxRanks = 8;
-constexpr int kBins = 512, kList = 2048;
+constexpr int kBins = 512;                      // of a histogram; two of 64-bit sums have a list's place
+constexpr int kList = 2048, kListK = 1024;      // logits that are sorted at most, and the k for which that is tried
 constexpr int kOneBits = 42;                    // w = 1
 constexpr float kCut = -43.f;                   // log2 w below which w counts as zero
 constexpr int32_t kAll = 0x7fffffff;
 // a row of 2^18 logits over eight CTAs, and the histograms
-constexpr int kMaxSmem = KDA_MAX_VOCABULARY / kMaxRanks * 4 + 32 + kBins * 8;
+constexpr int kScratch = kList * 8;
+static_assert(kList * 8 >= 2 * kBins * 8 && kList <= 4 * kThreads, "histograms in the list's place, four elements a thread");
+constexpr int kMaxSmem = KDA_MAX_VOCABULARY / kMaxRanks * 4 + 32 + kScratch;
 
 struct Sampling {
     const void *logits;
@@ -120,17 +123,41 @@ __device__ __forceinline__ u64 weight(const Scale &s, float x) {
     return ((u64)mant << 32) >> (62 - kOneBits - n);
 }
 
+// list[0 .. n) by size, the largest first; the block's threads.  (Bitonic; what lies behind n up to the
+// next power of two is set to zero.)
+__device__ __forceinline__ void sort_down(u64 *list, int n, int tid) {
+    int all = 2;
+    while (all < n) all *= 2;
+    for (int i = n + tid; i < all; i += kThreads) list[i] = 0;
+    __syncthreads();
+    for (int size = 2; size <= all; size *= 2)
+        for (int step = size / 2; step > 0; step /= 2) {
+            for (int i = tid; i < all / 2; i += kThreads) {
+                const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
+                const u64 x = list[lo], y = list[hi];
+                if ((x < y) == ((lo & size) == 0)) {
+                    list[lo] = y;
+                    list[hi] = x;
+                }
+            }
+            __syncthreads();
+        }
+}
+
 template <typename Tin>
 __global__ void __launch_bounds__(kThreads, 2)
 sample_kernel(const Sampling a, const int32_t slice) {
     constexpr int VEC = Vec<Tin>::N;
     extern __shared__ __align__(16) unsigned char smem[];
     uint4 *data = reinterpret_cast<uint4 *>(smem);                  // the CTA's vectors of the row
-    uint32_t *hist = reinterpret_cast<uint32_t *>(smem + (size_t)slice * 16);   // low words, then high words
+    // two histograms: low words, then high words;  in their place: the few that matter, and their sums
+    uint32_t *const hists = reinterpret_cast<uint32_t *>(smem + (size_t)slice * 16), *hist = hists;
+    u64 *const list = reinterpret_cast<u64 *>(hists);
     __shared__ u64 part[kWarps], found[2];                          // found: what lies above the border, the border bin's
     __shared__ u64 totals[2][kMaxRanks];
     __shared__ float tops[kMaxRanks], warp_top[kWarps];
-    __shared__ int32_t found_bin, chosen_index;
+    __shared__ int32_t found_bin, chosen_index, count, chosen_count;
+    __shared__ uint32_t chosen_key;
     __shared__ Scale scale;
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
     cluster.barrier_arrive();
@@ -159,7 +186,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
     }
 
     // ---- the row into shared memory, and its maximum
-    float top = -INFINITY;
+    float top = -INFINITY, my_top;
     for (int v = w0 + lane; v < w1; v += 32) {
         const int e0 = index_of(v);
         uint4 x;
@@ -184,9 +211,11 @@ sample_kernel(const Sampling a, const int32_t slice) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) top = fmaxf(top, f[e]);
     }
+    my_top = top;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) warp_top[warp] = top;
+    if (tid == 0) count = 0;
     cluster.barrier_wait();                     // every CTA has started
     __syncthreads();
     if (warp == 0) {
@@ -248,16 +277,21 @@ sample_kernel(const Sampling a, const int32_t slice) {
         return all;
     };
 
-    // A histogram's bins, added up over the cluster and in order: the first bin at which they reach
-    // `goal(total)` (at least one).  Everyone gets what lies above that bin, and what is in it.
+    // A histogram's bins, added up over the cluster and in order (every CTA for itself): the first bin at
+    // which they reach `goal(total)`, at least one; `above` lies above the first bin.  Two histograms in
+    // turn: when all have come together here, the last one has been read.
+    auto next_histogram = [&]() {
+        hist = hist == hists ? hists + 2 * kBins : hists;
+        for (int i = tid; i < 2 * kBins; i += kThreads) hist[i] = 0;
+        __syncthreads();
+    };
     auto border = [&](u64 above, bool wide, auto goal, u64 &total) {
         cluster.sync();                         // the histograms are complete
-        const int own = kBins / ranks, b = rank * own + tid;
         u64 x = 0;
-        if (tid < own)
+        if (tid < kBins)
             for (int r = 0; r < ranks; ++r) {
                 const uint32_t *h = cluster.map_shared_rank(hist, r);
-                x += wide ? (u64)h[b] + ((u64)h[kBins + b] << 32) : (u64)h[b];
+                x += wide ? (u64)h[tid] + ((u64)h[kBins + tid] << 32) : (u64)h[tid];
             }
         u64 run = x;
 #pragma unroll
@@ -265,40 +299,24 @@ sample_kernel(const Sampling a, const int32_t slice) {
             const u64 z = __shfl_up_sync(0xffffffffu, run, o);
             if (lane >= o) run += z;
         }
-        __syncthreads();
         if (lane == 31) part[warp] = run;
         __syncthreads();
-        u64 all = 0, before = above;
+        total = 0;
         for (int w = 0; w < kWarps; ++w) {
             run += w < warp ? part[w] : 0;
-            all += part[w];
+            total += part[w];
         }
-        if (tid < ranks) *cluster.map_shared_rank(&totals[turn][rank], tid) = all;
-        cluster.sync();
-        total = 0;
-        for (int r = 0; r < ranks; ++r) {
-            before += r < rank ? totals[turn][r] : 0;
-            total += totals[turn][r];
-        }
-        turn ^= 1;
         const u64 want = goal(total);
-        run += before;
-        if (tid < own && run >= want && run - x < want) {
-            for (int r = 0; r < ranks; ++r) {
-                *cluster.map_shared_rank(&found_bin, r) = b;
-                *cluster.map_shared_rank(&found[0], r) = run - x;
-                *cluster.map_shared_rank(&found[1], r) = x;
-            }
+        run += above;
+        if (tid < kBins && run >= want && run - x < want) {
+            found_bin = tid;
+            found[0] = run - x;
+            found[1] = x;
         }
-        cluster.sync();
+        __syncthreads();
         return want;
     };
     static_assert(kBins <= kThreads, "a thread per bin");
-    auto clear = [&]() {
-        __syncthreads();
-        for (int i = tid; i < 2 * kBins; i += kThreads) hist[i] = 0;
-        __syncthreads();
-    };
     auto add_weight = [&](int b, u64 w) {
         const uint32_t lo = (uint32_t)w, old = atomicAdd(&hist[b], lo);
         const uint32_t hi = (uint32_t)(w >> 32) + (old + lo < old ? 1u : 0u);
@@ -317,7 +335,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
     // Narrows the border down to the first elements of the order that reach a count (k) or a weight.
     auto narrow = [&](bool by_weight, auto goal) {
         u64 total, want = 0;
-        clear();
+        next_histogram();
         each([&](int i, float x) {
             x = value(x);
             if (x == -INFINITY || !stays(i, key_of(x))) return;
@@ -343,7 +361,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
         for (;;) {
             int shift = 0;
             while (((most - lowest) >> shift) >= (uint32_t)kBins) ++shift;
-            clear();
+            next_histogram();
             each([&](int i, float x) {
                 x = value(x);
                 if (x == -INFINITY) return;
@@ -358,7 +376,6 @@ sample_kernel(const Sampling a, const int32_t slice) {
                 }
             });
             const u64 above_it = found[0];
-            __syncthreads();
             border(above_it, by_weight, [&](u64) { return want; }, total);
             most = most - ((uint32_t)found_bin << shift);
             if (shift == 0) break;
@@ -421,14 +438,129 @@ sample_kernel(const Sampling a, const int32_t slice) {
     u64 w_least = 0;
     if (least > 0.f) w_least = (u64)(fminf(least, 1.f) * 0x1p42f);
     const bool none = top == -INFINITY;
-    int32_t token = -1;
-    if (!none) {
+    // the weight that top-p asks of a total (rounded up, at least something)
+    auto share = [&](u64 total) {
+        const u64 by64 = p > 0.f ? (u64)(p * 0x1p63f) << 1 : 0, whole = __umul64hi(total, by64);
+        return max(total * by64 != 0 ? whole + 1 : whole, (u64)1);
+    };
+    // the first token whose running sum exceeds floor(u sum / 2^24) (the sum of all does, since u < 2^24)
+    auto drawn = [&]() {
+        const uint32_t tick = __float2uint_rz(fminf(fmaxf(u, 0.f) * 16777216.f, 16777215.f));
+        return __umul64hi((u64)tick << 40, sum);
+    };
+
+    // ---- a small k: the few logits that can be among the first k, sorted in one CTA
+    bool done = false;
+    if (!none && k > 0 && k < V && k <= kListK && k <= ranks * kThreads / 2) {
+        // k of the threads' largest logits are no smaller than this bin's
+        next_histogram();
+        const float mine_top = value(my_top);
+        if (mine_top != -INFINITY) atomicAdd(&hist[bin_of(position(mine_top))], 1u);
+        u64 total;
+        const u64 want = border(0, false, [&](u64) { return (u64)k; }, total);
+        const float until = total < want || found_bin == kBins - 1 ? INFINITY : (float)(found_bin + 1);
+        cluster.sync();                         // the histograms are read: the lists take their place
+        each([&](int i, float x) {
+            x = value(x);
+            if (x == -INFINITY || !(position(x) < until)) return;
+            const int at = atomicAdd(&count, 1);
+            if (at < kList) list[at] = (u64)key_of(x) << 32 | (uint32_t)~i;
+        });
+        cluster.sync();
+        int all = 0, before = 0;
+        for (int r = 0; r < ranks; ++r) {
+            const int c = *cluster.map_shared_rank(&count, r);
+            before += r < rank ? c : 0;
+            all += c;
+        }
+        done = all <= kList;
+        if (done && rank == 0) {
+            for (int r = 1, at = count; r < ranks; ++r) {
+                const int c = *cluster.map_shared_rank(&count, r);
+                const u64 *from = cluster.map_shared_rank(list, r);
+                for (int i = tid; i < c; i += kThreads) list[at + i] = from[i];
+                at += c;
+            }
+            __syncthreads();
+            sort_down(list, all, tid);
+            // cum(n, w): the sums of w(i) up to each of the thread's elements 4 tid .. 4 tid + 3 of n
+            u64 w[4], cum[4];
+            auto scan = [&](int n, auto f) {
+                u64 run = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 4 * tid + e;
+                    w[e] = i < n ? f(list[i]) : 0;
+                    run += w[e];
+                    cum[e] = run;
+                }
+                const u64 own = run;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const u64 z = __shfl_up_sync(0xffffffffu, run, o);
+                    if (lane >= o) run += z;
+                }
+                __syncthreads();
+                if (lane == 31) part[warp] = run;
+                __syncthreads();
+                u64 sum_all = 0, add = run - own;
+                for (int x = 0; x < kWarps; ++x) {
+                    add += x < warp ? part[x] : 0;
+                    sum_all += part[x];
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) cum[e] += add;
+                return sum_all;
+            };
+            const int first_k = min(k, all);
+            const u64 of_k = scan(first_k, [&](u64 c) { return weight(s, value_of((uint32_t)(c >> 32))); });
+            const u64 goal = p < 1.f && !greedy ? share(of_k) : ~(u64)0;
+            int stay = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                stay += 4 * tid + e < first_k && cum[e] - w[e] < goal && (4 * tid + e == 0 || w[e] >= w_least) ? 1 : 0;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) stay += __shfl_xor_sync(0xffffffffu, stay, o);
+            if (tid == 0) chosen_count = 0;
+            __syncthreads();
+            if (lane == 0) atomicAdd(&chosen_count, stay);
+            __syncthreads();
+            stay = chosen_count;                // a beginning of the order
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (4 * tid + e == stay - 1) {
+                    const u64 c = list[stay - 1];
+                    for (int r = 0; r < ranks; ++r) {
+                        *cluster.map_shared_rank(&chosen_key, r) = (uint32_t)(c >> 32);
+                        *cluster.map_shared_rank(&chosen_index, r) = (int32_t)~(uint32_t)c;
+                        *cluster.map_shared_rank(&found[0], r) = cum[e];
+                    }
+                }
+            __syncthreads();
+            sum = found[0];
+            if (a.token != nullptr) {
+                // in index order
+                for (int i = tid; i < stay; i += kThreads) list[i] = list[i] << 32 | list[i] >> 32;
+                __syncthreads();
+                sort_down(list, stay, tid);
+                scan(stay, [&](u64 c) { return weight(s, value_of((uint32_t)c)); });
+                const u64 need = drawn();
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (4 * tid + e < stay && cum[e] > need && cum[e] - w[e] <= need)
+                        a.token[n] = (int32_t)~(uint32_t)(list[4 * tid + e] >> 32);
+            }
+        }
+        cluster.sync();
+        if (done) {
+            border_key = chosen_key;
+            last = chosen_index;
+            sum = found[0];
+        }
+    }
+    if (!none && !done) {
         if (k > 0 && k < V) narrow(false, [&](u64) { return (u64)k; });
-        if (p < 1.f && !greedy)
-            narrow(true, [&](u64 total) {
-                const u64 by64 = p > 0.f ? (u64)(p * 0x1p63f) << 1 : 0, whole = __umul64hi(total, by64);
-                return max(total * by64 != 0 ? whole + 1 : whole, (u64)1);
-            });
+        if (p < 1.f && !greedy) narrow(true, share);
         // ---- the draw, in index order
         u64 before;
         each([&](int i, float x) {
@@ -442,9 +574,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
         if (a.token != nullptr) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) here += __shfl_xor_sync(0xffffffffu, here, o);
-            // the first token whose running sum exceeds floor(u sum / 2^24) (the sum of all does, since u < 2^24)
-            const uint32_t tick = __float2uint_rz(fminf(fmaxf(u, 0.f) * 16777216.f, 16777215.f));
-            const u64 need = __umul64hi((u64)tick << 40, sum);
+            const u64 need = drawn();
             if (before <= need && before + here > need) {
                 for (int v0 = w0; v0 < w1; v0 += 32) {
                     const int v = v0 + lane;
@@ -482,8 +612,8 @@ sample_kernel(const Sampling a, const int32_t slice) {
                 }
             }
         }
-    } else if (a.token != nullptr && rank == 0 && tid == 0) {
-        a.token[n] = token;
+    } else if (none && a.token != nullptr && rank == 0 && tid == 0) {
+        a.token[n] = -1;
     }
     if (a.probs != nullptr) {
         const float inv = none ? 0.f : (float)(0x1p42 / (double)sum);
@@ -550,7 +680,7 @@ template <typename Tin> cudaError_t run(const Sampling &a, int32_t N, cudaStream
            (int64_t)vecs * 16 <= (ranks / 2) * (int64_t)(72 * 1024))
         ranks /= 2;
     const int slice = (vecs + ranks - 1) / ranks;
-    const size_t smem = (size_t)slice * 16 + kBins * 8;
+    const size_t smem = (size_t)slice * 16 + kScratch;
     static std::atomic<uint64_t> smem_set{0};
     cudaError_t e = allow_dynamic_smem(sample_kernel<Tin>, kMaxSmem, smem_set);
     if (e != cudaSuccess) return e;
