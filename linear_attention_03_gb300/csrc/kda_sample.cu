@@ -7,17 +7,19 @@
 //     weights of the ones that stay, added up in index order, exceed u times their sum
 //
 // Weights are whole multiples of 2^-42, held in 64 bits, so sums do not depend on their order.
-// Each is right to some 2^-25 of itself: the draw moves by a token at one in about 10^6 rows.
+// Each is right to some 2^-24 of itself, with errors of either sign: the draw moves by a token at
+// fewer than one in 10^5 rows.
 //
 // A cluster of up to eight CTAs takes a row and keeps it in shared memory, so that the logits
 // are read once.  What stays is a beginning of the order: a border value, and the
-// last index among the logits equal to it.  It is found by histograms that narrow the values
-// down, first by w (bins of equal width in log2 w, which spread the logits well whatever their
-// scale), then by the value's bits, each of counts (top-k) or of weights (top-p).
-// For the usual small k the histogram is of every thread's largest logit alone: k of these
-// bound the k-th largest logit from below, and the few logits above the bound are sorted in
-// one CTA, which makes the whole choice there.
+// last index among the logits equal to it.
+//   A small k: k of the threads' largest logits bound the k-th largest from below; the few logits
+// above the bound go to one CTA, which makes the whole choice there, the draw included.
+//   Otherwise histograms narrow the values down, first by w (bins of equal width in log2 w,
+// which spread the logits well whatever their scale), then by the value's bits: of counts for a
+// large k, of weights for top-p.
 #include "kda_internal.cuh"
+#include "kda_tc.cuh"
 
 #include <cooperative_groups.h>
 
@@ -26,15 +28,16 @@ namespace {
 
 typedef unsigned long long u64;
 constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxRanks = 8;
-constexpr int kBins = 512;                      // of a histogram; two of 64-bit sums have a list's place
+constexpr int kBins = 512;                      // of a histogram
+constexpr float kPerOctave = 12.f;              // bins for a halving of w
 constexpr int kList = 2048, kListK = 1024;      // logits that are sorted at most, and the k for which that is tried
-constexpr int kOneBits = 42;                    // w = 1
-constexpr float kCut = -43.f;                   // log2 w below which w counts as zero
+constexpr int kFew = 128;                       // logits of which every pair is compared instead
 constexpr int32_t kAll = 0x7fffffff;
-// a row of 2^18 logits over eight CTAs, and the histograms
-constexpr int kScratch = kList * 8;
-static_assert(kList * 8 >= 2 * kBins * 8 && kList <= 4 * kThreads, "histograms in the list's place, four elements a thread");
+// two histograms and a list; a row of 2^18 logits over eight CTAs beside them
+constexpr int kScratch = 4 * kBins * 4 + kList * 8;
 constexpr int kMaxSmem = KDA_MAX_VOCABULARY / kMaxRanks * 4 + 32 + kScratch;
+static_assert(kList <= 4 * kThreads && 4 * kFew == kThreads && 2 * kFew <= kList, "threads to the elements of a list");
+static_assert(kBins == kThreads, "a thread per bin");
 
 struct Sampling {
     const void *logits;
@@ -56,71 +59,96 @@ __device__ __forceinline__ float value_of(uint32_t key) {
     return __uint_as_float((key >> 31) != 0 ? key & 0x7fffffffu : ~key);
 }
 
-// 16 bytes of logits; NaN becomes -infinity
+// 16 bytes of logits as pairs.  clean: NaN becomes -infinity.
 template <typename Tin> struct Vec;
 template <> struct Vec<float> {
     static constexpr int N = 4;
-    static __device__ __forceinline__ void unpack(uint4 u, float (&x)[4]) {
-        x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y);
-        x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
+    static __device__ __forceinline__ void unpack(uint4 u, float2 (&x)[2]) {
+        x[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+        x[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
     }
     static __device__ __forceinline__ uint32_t clean(uint32_t w) {
         return __float_as_uint(fmaxf(__uint_as_float(w), -INFINITY));
     }
-    static __device__ __forceinline__ uint32_t word(float lo, float) { return __float_as_uint(lo); }
+    static __device__ __forceinline__ float largest(uint4 u) {
+        return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
+    }
+    static __device__ __forceinline__ float load(const uint4 *p, int e) { return reinterpret_cast<const float *>(p)[e]; }
 };
 template <> struct Vec<__nv_bfloat16> {
     static constexpr int N = 8;
-    static __device__ __forceinline__ void unpack(uint4 u, float (&x)[8]) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+    static __device__ __forceinline__ void unpack(uint4 u, float2 (&x)[4]) {
+        x[0] = tc::unpack_bf16x2(u.x);
+        x[1] = tc::unpack_bf16x2(u.y);
+        x[2] = tc::unpack_bf16x2(u.z);
+        x[3] = tc::unpack_bf16x2(u.w);
     }
-    static __device__ __forceinline__ uint32_t clean(uint32_t w) {
-        const __nv_bfloat162 low = __halves2bfloat162(__ushort_as_bfloat16(0xff80), __ushort_as_bfloat16(0xff80));
-        __nv_bfloat162 x;
-        memcpy(&x, &w, 4);
-        x = __hmax2(x, low);
-        memcpy(&w, &x, 4);
-        return w;
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));       // (a number beside a NaN)
+        return d;
+    }
+    static __device__ __forceinline__ uint32_t clean(uint32_t w) { return max2(w, 0xff80ff80u); }
+    static __device__ __forceinline__ float largest(uint4 u) {
+        const uint32_t m = max2(max2(u.x, u.y), max2(u.z, u.w));
+        return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    }
+    static __device__ __forceinline__ float load(const uint4 *p, int e) {
+        return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[e]);
     }
 };
 
-// log2 w = (x - m)(c + cl)
+// log2 w = (x - m)(c + cl); below x = least w counts as zero
 struct Scale {
-    float m, c, cl;
+    float m, c, cl, least;
 };
 
-// w = 2^n (1 + q), or false where log2 w <= cut.  x - m with its rounding error, the product with c
-// in one rounding behind the point, and 2^f - 1 by its series (to 2^-27 for |f| <= 1/2).
-__device__ __forceinline__ bool weight_parts(const Scale &s, float x, float cut, float &q, int &n) {
-    const float d = x - s.m;
-    if (!(d * s.c > cut)) return false;
-    const float mv = x - d, xv = d + mv, err = (x - xv) + (mv - s.m);
-    const float t = fmaf(d, s.c, 12582912.f), whole = t - 12582912.f;
-    float f = fmaf(d, s.c, -whole);
-    f = fmaf(d, s.cl, f);
-    f = fmaf(err, s.c, f);
-    n = __float_as_int(t) - 0x4b400000;
-    float p = 1.5252733804059841e-5f;           // ln(2)^k / k!, k = 7 .. 1
-    p = fmaf(p, f, 1.5403530393381610e-4f);
-    p = fmaf(p, f, 1.3333558146428443e-3f);
-    p = fmaf(p, f, 9.6181291076284772e-3f);
-    p = fmaf(p, f, 5.5504108664821580e-2f);
-    p = fmaf(p, f, 2.4022650695910071e-1f);
-    p = fmaf(p, f, 6.9314718055994531e-1f);
-    q = p * f;
-    return true;
+// The weights of two logits, to 2^-24: x - m with its rounding error, the product with c in one
+// rounding behind the point, 2^f by its series (to 2^-27 for |f| <= 1/2) and the exponent put on
+// in whole numbers.  Paired arithmetic: some 12 instructions a weight.  (No number of meaning below s.least.)
+__device__ __forceinline__ float2 weights2(const Scale &s, float2 x) {
+    auto both = [](float a) { return make_float2(a, a); };
+    const float2 d = tc::f2sub(x, both(s.m)), mv = tc::f2sub(x, d), xv = tc::f2add(d, mv);
+    const float2 err = tc::f2add(tc::f2sub(x, xv), tc::f2sub(mv, both(s.m)));
+    const float2 t = tc::f2fma(d, both(s.c), both(12582912.f)), whole = tc::f2sub(both(12582912.f), t);
+    float2 f = tc::f2fma(d, both(s.c), whole);
+    f = tc::f2fma(d, both(s.cl), f);
+    f = tc::f2fma(err, both(s.c), f);
+    float2 p = both(1.5252733804059841e-5f);    // ln(2)^k / k!, k = 7 .. 0
+    p = tc::f2fma(p, f, both(1.5403530393381610e-4f));
+    p = tc::f2fma(p, f, both(1.3333558146428443e-3f));
+    p = tc::f2fma(p, f, both(9.6181291076284772e-3f));
+    p = tc::f2fma(p, f, both(5.5504108664821580e-2f));
+    p = tc::f2fma(p, f, both(2.4022650695910071e-1f));
+    p = tc::f2fma(p, f, both(6.9314718055994531e-1f));
+    p = tc::f2fma(p, f, both(1.f));
+    p.x = __int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23));
+    p.y = __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23));
+    return p;
+}
+// A weight as a whole number of 2^-42, cut off, in two digits of 21 bits.  Adding 2^23 with rounding toward
+// zero leaves the whole part in the significand's low bits, and what remains is exact.  The digits
+// carry 2^23's bits with them.
+constexpr uint32_t kBias = 0x4b000000u;
+__device__ __forceinline__ float2 fma_cut2(float2 a, float2 b, float2 c) {
+    unsigned long long d;
+    asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(tc::f2u(a)), "l"(tc::f2u(b)), "l"(tc::f2u(c)));
+    return tc::u2f(d);
+}
+__device__ __forceinline__ void digits42(float2 w, float2 &hi, float2 &lo) {
+    const float2 scale = make_float2(2097152.f, 2097152.f), one = make_float2(8388608.f, 8388608.f);
+    hi = fma_cut2(w, scale, one);
+    lo = fma_cut2(tc::f2fma(w, scale, tc::f2sub(one, hi)), scale, one);
+}
+__device__ __forceinline__ uint32_t digit(float x) { return __float_as_uint(x) - kBias; }
+__device__ __forceinline__ u64 fixed42(float w) {
+    float2 hi, lo;
+    digits42(make_float2(w, w), hi, lo);
+    return ((u64)digit(hi.x) << 21) + digit(lo.x);
 }
 __device__ __forceinline__ u64 weight(const Scale &s, float x) {
-    float q;
-    int n;
-    if (!weight_parts(s, x, kCut, q, n)) return 0;
-    const uint32_t mant = (1u << 30) + __float2int_rn(q * 0x1p30f);
-    return ((u64)mant << 32) >> (62 - kOneBits - n);
+    const float w = weights2(s, make_float2(x, x)).x;
+    return fixed42(x >= s.least ? w : 0.f);
 }
 
 // list[0 .. n) by size, the largest first; the block's threads.  (Bitonic; what lies behind n up to the
@@ -149,16 +177,15 @@ __global__ void __launch_bounds__(kThreads, 2)
 sample_kernel(const Sampling a, const int32_t slice) {
     constexpr int VEC = Vec<Tin>::N;
     extern __shared__ __align__(16) unsigned char smem[];
-    uint4 *data = reinterpret_cast<uint4 *>(smem);                  // the CTA's vectors of the row
-    // two histograms: low words, then high words;  in their place: the few that matter, and their sums
+    uint4 *const data = reinterpret_cast<uint4 *>(smem);            // the CTA's vectors of the row
+    // two histograms (low words, then high words) and a list
     uint32_t *const hists = reinterpret_cast<uint32_t *>(smem + (size_t)slice * 16), *hist = hists;
-    u64 *const list = reinterpret_cast<u64 *>(hists);
-    __shared__ u64 part[kWarps], found[2];                          // found: what lies above the border, the border bin's
+    u64 *const list = reinterpret_cast<u64 *>(hists + 4 * kBins);
+    __shared__ u64 part[kWarps], part_all, found[2];                          // found: what lies above the border's bin, what is in it
     __shared__ u64 totals[2][kMaxRanks];
     __shared__ float tops[kMaxRanks], warp_top[kWarps];
     __shared__ int32_t found_bin, chosen_index, count, chosen_count;
     __shared__ uint32_t chosen_key;
-    __shared__ Scale scale;
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
     cluster.barrier_arrive();
     const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -171,27 +198,29 @@ sample_kernel(const Sampling a, const int32_t slice) {
     const int lead = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(Tin));
     const int vecs = (V + lead + VEC - 1) / VEC, first = min(vecs, rank * slice), mine = min(vecs - first, slice);
     const int per_warp = (slice + kWarps - 1) / kWarps, w0 = min(mine, warp * per_warp), w1 = min(mine, w0 + per_warp);
-    const uint4 *grid = reinterpret_cast<const uint4 *>(row - lead);
+    const uint4 *grid = reinterpret_cast<const uint4 *>(row - lead) + first;
     auto index_of = [&](int v) { return (first + v) * VEC - lead; };    // of a vector's first element
 
     float T = a.temperature != nullptr ? a.temperature[n] : 1.f;
     int32_t k = a.top_k != nullptr ? a.top_k[n] : 0;
-    const float p = a.top_p != nullptr ? a.top_p[n] : 1.f;
+    float p = a.top_p != nullptr ? a.top_p[n] : 1.f;
     const float least = a.min_p != nullptr ? a.min_p[n] : 0.f;
     const float u = a.uniforms != nullptr ? a.uniforms[n] : 0.f;
-    const bool greedy = !(T > 0.f);             // the first of the order
-    if (greedy) {
+    if (!(T > 0.f)) {                           // the first of the order alone
         T = 1.f;
         k = 1;
     }
+    if (k == 1) p = 1.f;
+    if (tid == 0) count = 0;
 
     // ---- the row into shared memory, and its maximum
-    float top = -INFINITY, my_top;
+    float my_top = -INFINITY;
+#pragma unroll 4
     for (int v = w0 + lane; v < w1; v += 32) {
         const int e0 = index_of(v);
         uint4 x;
         if (e0 >= 0 && e0 + VEC <= V) {
-            x = __ldg(grid + first + v);
+            x = __ldg(grid + v);
         } else {                                // the row's ends
             Tin y[VEC];
 #pragma unroll
@@ -206,16 +235,12 @@ sample_kernel(const Sampling a, const int32_t slice) {
         x.z = Vec<Tin>::clean(x.z);
         x.w = Vec<Tin>::clean(x.w);
         data[v] = x;
-        float f[VEC];
-        Vec<Tin>::unpack(x, f);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) top = fmaxf(top, f[e]);
+        my_top = fmaxf(my_top, Vec<Tin>::largest(x));
     }
-    my_top = top;
+    float top = my_top;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) warp_top[warp] = top;
-    if (tid == 0) count = 0;
     cluster.barrier_wait();                     // every CTA has started
     __syncthreads();
     if (warp == 0) {
@@ -223,49 +248,112 @@ sample_kernel(const Sampling a, const int32_t slice) {
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         if (lane < ranks) *cluster.map_shared_rank(&tops[rank], lane) = top;
-        if (lane == 0) {
-            const double c = 1.4426950408889634 / (double)T;
-            scale.c = fminf((float)c, 1e37f);
-            scale.cl = scale.c < 1e37f ? (float)(c - (double)scale.c) : 0.f;
-        }
     }
     cluster.sync();
     top = -INFINITY;
     for (int r = 0; r < ranks; ++r) top = fmaxf(top, tops[r]);
-
-    // Runs f(index, x) over the warp's elements, VEC to a lane; what lies outside the row is -infinity.
-    auto each = [&](auto f) {
-        for (int v = w0 + lane; v < w1; v += 32) {
-            float x[VEC];
-            Vec<Tin>::unpack(data[v], x);
-            const int e0 = index_of(v);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) f(e0 + e, x[e]);
-        }
-    };
-    bool inf_row = false;
+    const bool none = top == -INFINITY;
     if (top == INFINITY) {                      // the infinite ones share everything
-        inf_row = true;
+        for (int v = w0 + lane; v < w1; v += 32) {
+            Tin y[VEC];
+            memcpy(y, &data[v], 16);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) y[e] = static_cast<Tin>(static_cast<float>(y[e]) == INFINITY ? 0.f : -INFINITY);
+            memcpy(&data[v], y, 16);
+        }
+        my_top = my_top == INFINITY ? 0.f : -INFINITY;
         top = 0.f;
     }
-    Scale s = scale;
+    // log2(e) / T as a number and what is left of it, within a range where nothing overflows
+    Scale s;
     s.m = top;
-    auto value = [&](float x) { return !inf_row ? x : x == INFINITY ? 0.f : -INFINITY; };
+    s.c = fminf(fmaxf(1.44269502f / T, 1e-36f), 1e37f);
+    s.cl = s.c < 1e37f && s.c > 1e-36f ? (fmaf(-s.c, T, 1.44269502f) + 1.92596303e-8f) / T : 0.f;
+    if (!(fabsf(s.cl) < 1e30f)) s.cl = 0.f;
+    s.least = fmaxf(s.m - 44.f / s.c, -3.402823466e38f);
+    // bins of equal width in log2 w; the last one takes everything below
+    const float by = s.c * kPerOctave;
+    auto position = [&](float x) { return (s.m - x) * by; };
+    auto bin_of = [&](float pos) { return pos < (float)(kBins - 1) ? (int)pos : kBins - 1; };
 
-    // sums over the warps of all CTAs: every thread gets the total, and what the warps before its own hold
+    // Runs f(i, x) over the elements of the warp that lie in [from, to], few of them (one comparison each lets
+    // all others pass by).
+    auto each_in = [&](float from, float to, auto f) {
+#pragma unroll 1
+        for (int v = w0 + lane; v < w1; v += 32) {
+            const uint4 y = data[v];
+            if (Vec<Tin>::largest(y) < from) continue;
+            float2 x[VEC / 2];
+            Vec<Tin>::unpack(y, x);
+            uint32_t bits = 0;
+#pragma unroll
+            for (int e = 0; e < VEC / 2; ++e) {
+                bits |= x[e].x >= from && x[e].x <= to ? 1u << (2 * e) : 0u;
+                bits |= x[e].y >= from && x[e].y <= to ? 2u << (2 * e) : 0u;
+            }
+            for (; bits != 0; bits &= bits - 1) {
+                const int e = __ffs(bits) - 1;
+                f(index_of(v) + e, Vec<Tin>::load(data + v, e));
+            }
+        }
+    };
+    // The weights of the thread's elements that are at least `from` and of which which(i, x, w) holds, added up;
+    // also(x, hi, lo) sees these with their digits.
+    auto weigh = [&](float from, auto which, auto also) {
+        from = fmaxf(from, s.least);
+        uint32_t hi = 0, lo = 0;                // (digits of 21 bits: no thread has 2,048 elements)
+#pragma unroll 1
+        for (int v = w0 + lane; v < w1; v += 32) {
+            const uint4 y = data[v];
+            if (Vec<Tin>::largest(y) < from) continue;
+            float2 x[VEC / 2];
+            Vec<Tin>::unpack(y, x);
+            const int i = index_of(v);
+#pragma unroll
+            for (int e = 0; e < VEC / 2; ++e) {
+                float2 w = weights2(s, x[e]), h, l;
+                w.x = x[e].x >= from && which(i + 2 * e, x[e].x, w.x) ? w.x : 0.f;
+                w.y = x[e].y >= from && which(i + 2 * e + 1, x[e].y, w.y) ? w.y : 0.f;
+                digits42(w, h, l);
+                const uint32_t h0 = digit(h.x), h1 = digit(h.y), l0 = digit(l.x), l1 = digit(l.y);
+                hi += h0 + h1;
+                lo += l0 + l1;
+                also(x[e].x, h0, l0);
+                also(x[e].y, h1, l1);
+            }
+        }
+        return ((u64)hi << 21) + lo;
+    };
+
+    // Sums over all warps of all CTAs: every thread gets the total, what the warps before its own have,
+    // and its warp's.  With its barrier the histograms are complete, too.
     int turn = 0;
-    auto cluster_sum = [&](u64 x, u64 &before) {
+    // what the warps before have of the parts that the warps left, and the total
+    auto parts_before = [&](u64 &all) {
+        __syncthreads();
+        if (warp == 0) {
+            const u64 x = lane < kWarps ? part[lane] : 0;
+            u64 run = x;
+#pragma unroll
+            for (int o = 1; o < kWarps; o <<= 1) {
+                const u64 z = __shfl_up_sync(0xffffffffu, run, o);
+                if (lane >= o) run += z;
+            }
+            if (lane < kWarps) part[lane] = run - x;
+            if (lane == kWarps - 1) part_all = run;
+        }
+        __syncthreads();
+        all = part_all;
+        return part[warp];
+    };
+    auto cluster_sum = [&](u64 x, u64 &before, u64 &here) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        here = x;
         __syncthreads();
         if (lane == 0) part[warp] = x;
-        __syncthreads();
-        u64 all = 0;
-        before = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            before += w < warp ? part[w] : 0;
-            all += part[w];
-        }
+        u64 all;
+        before = parts_before(all);
         if (tid < ranks) *cluster.map_shared_rank(&totals[turn][rank], tid) = all;
         cluster.sync();
         all = 0;
@@ -276,125 +364,130 @@ sample_kernel(const Sampling a, const int32_t slice) {
         turn ^= 1;
         return all;
     };
-
-    // A histogram's bins, added up over the cluster and in order (every CTA for itself): the first bin at
-    // which they reach `goal(total)`, at least one; `above` lies above the first bin.  Two histograms in
-    // turn: when all have come together here, the last one has been read.
+    // Two histograms in turn: when all have come together over one, the last one has been read.
     auto next_histogram = [&]() {
         hist = hist == hists ? hists + 2 * kBins : hists;
         for (int i = tid; i < 2 * kBins; i += kThreads) hist[i] = 0;
         __syncthreads();
     };
-    auto border = [&](u64 above, bool wide, auto goal, u64 &total) {
-        cluster.sync();                         // the histograms are complete
-        u64 x = 0;
-        if (tid < kBins)
-            for (int r = 0; r < ranks; ++r) {
-                const uint32_t *h = cluster.map_shared_rank(hist, r);
-                x += wide ? (u64)h[tid] + ((u64)h[kBins + tid] << 32) : (u64)h[tid];
-            }
+    // the thread's bin, added up over the cluster
+    auto bin_sum = [&](int word) {
+        uint32_t x[kMaxRanks];
+#pragma unroll
+        for (int r = 0; r < kMaxRanks; ++r)     // (reads of all ranks on their way together)
+            x[r] = cluster.map_shared_rank(hist, r < ranks ? r : 0)[word * kBins + tid];
+        u64 all = 0;
+#pragma unroll
+        for (int r = 0; r < kMaxRanks; ++r) all += r < ranks ? x[r] : 0;
+        return all;
+    };
+    // The first bin at which the bins, added up in order, reach want(total); `above` lies above the first
+    // one.  Every CTA does it for itself.  Returns whether they do.
+    auto border = [&](u64 x, u64 above, auto want) {
         u64 run = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const u64 z = __shfl_up_sync(0xffffffffu, run, o);
             if (lane >= o) run += z;
         }
-        if (lane == 31) part[warp] = run;
         __syncthreads();
-        total = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            run += w < warp ? part[w] : 0;
-            total += part[w];
-        }
-        const u64 want = goal(total);
-        run += above;
-        if (tid < kBins && run >= want && run - x < want) {
+        if (lane == 31) part[warp] = run;
+        u64 total;
+        run += parts_before(total) + above;
+        total += above;
+        const u64 goal = want(total);
+        if (run >= goal && run - x < goal) {
             found_bin = tid;
             found[0] = run - x;
             found[1] = x;
         }
         __syncthreads();
-        return want;
+        return total >= goal;
     };
-    static_assert(kBins <= kThreads, "a thread per bin");
-    auto add_weight = [&](int b, u64 w) {
-        const uint32_t lo = (uint32_t)w, old = atomicAdd(&hist[b], lo);
-        const uint32_t hi = (uint32_t)(w >> 32) + (old + lo < old ? 1u : 0u);
-        if (hi != 0) atomicAdd(&hist[kBins + b], hi);
+    auto add_weight = [&](int b, uint32_t hi, uint32_t lo) {        // (two digits of 21 bits)
+        const uint32_t low = (hi << 21) + lo, old = atomicAdd(&hist[b], low);
+        const uint32_t high = (hi >> 11) + (old + low < old ? 1u : 0u);
+        if (high != 0) atomicAdd(&hist[kBins + b], high);
     };
-    // bins of log2 w; the last one takes everything below
-    const float by = s.c * ((kBins - 1) / -kCut);
-    auto position = [&](float x) { return (s.m - x) * by; };
-    auto bin_of = [&](float pos) { return pos < (float)(kBins - 1) ? (int)pos : kBins - 1; };
 
-    // What stays: values above the border's, and of the equal ones those up to `last`.
-    uint32_t border_key = 0;                    // (key 0 is no value's)
+    // What stays: values above the border, and of the equal ones those up to `last`.
+    float border_at = -INFINITY;
     int32_t last = kAll;
-    auto stays = [&](int i, uint32_t key) { return key > border_key || (key == border_key && i <= last); };
+    auto stays = [&](int i, float x) { return x > border_at || (x == border_at && i <= last); };
+    auto lowest_value = [&]() { return fmaxf(border_at, -3.402823466e38f); };
+    // the weight that top-p asks of a total (rounded up, at least something)
+    auto share = [&](u64 total) {
+        const u64 by64 = p > 0.f ? (u64)(p * 0x1p63f) << 1 : 0, whole = __umul64hi(total, by64);
+        return max(total * by64 != 0 ? whole + 1 : whole, (u64)1);
+    };
+    // a value that is below all of the bins up to b, give or take the roundings; and one above all from b on
+    auto below_bin = [&](int b) {
+        const float d = (float)(b + 1) / by;
+        const float x = s.m - d * (1.f + 1e-6f);
+        return b >= kBins - 1 || !(x > -3e38f) ? -3.402823466e38f : x - 4e-7f * (fabsf(s.m) + fabsf(x)) - 1e-37f;
+    };
+    auto above_bin = [&](int b) {
+        const float x = s.m - (float)b / by * (1.f - 1e-6f);
+        return fminf(s.m, x + 4e-7f * (fabsf(s.m) + fabsf(x)) + 1e-37f);
+    };
 
-    // Narrows the border down to the first elements of the order that reach a count (k) or a weight.
-    auto narrow = [&](bool by_weight, auto goal) {
-        u64 total, want = 0;
+    // Narrows the border down to the first elements of the order that reach a count (k) or a share of
+    // the weight: first by bins of log2 w, then by the values' bits.
+    auto narrow = [&](bool by_weight) {
+        u64 want = (u64)k, above, before, here;
+        auto goal = [&](u64 total) {
+            if (by_weight) want = share(total);
+            return want;
+        };
         next_histogram();
-        each([&](int i, float x) {
-            x = value(x);
-            if (x == -INFINITY || !stays(i, key_of(x))) return;
-            const int b = bin_of(position(x));
-            if (by_weight) {
-                const u64 w = weight(s, x);
-                if (w != 0) add_weight(b, w);
-            } else {
-                atomicAdd(&hist[b], 1u);
-            }
-        });
-        want = border(0, by_weight, goal, total);
-        if (total < want || total == 0) return;  // fewer than that: all stay
+        if (!by_weight) {
+            each_in(lowest_value(), s.m, [&](int, float x) { atomicAdd(&hist[bin_of(position(x))], 1u); });
+        } else if (border_at == -INFINITY) {
+            weigh(lowest_value(), [](int, float, float) { return true; }, [&](float x, uint32_t hi, uint32_t lo) {
+                if ((hi | lo) != 0) add_weight(bin_of(position(x)), hi, lo);
+            });
+        } else {
+            each_in(lowest_value(), s.m, [&](int i, float x) {
+                const u64 w = stays(i, x) ? weight(s, x) : 0;
+                if (w != 0) add_weight(bin_of(position(x)), (uint32_t)(w >> 21), (uint32_t)w & 0x1fffffu);
+            });
+        }
+        cluster.sync();
+        if (!border(by_weight ? bin_sum(0) + (bin_sum(1) << 32) : bin_sum(0), 0, goal)) return;  // fewer: all stay
         const int bin = found_bin;
-        // the values of the bin lie between these, give or take the roundings; then by their bits
-        const float slack = 4e-7f * fabsf(s.m) + 1e-37f;
-        const float width = 1.f / by, below = (float)bin * width, above = (float)(bin + 1) * width;
-        uint32_t most = key_of(fminf(s.m, s.m - below * (1.f - 1e-6f) + slack + fabsf(s.m - below) * 4e-7f));
-        uint32_t lowest = bin == kBins - 1 || !(above < 3e38f)
-                              ? 0x00800000u     // (keys of finite numbers start there)
-                              : key_of(s.m - above * (1.f + 1e-6f) - slack - fabsf(s.m - above) * 4e-7f);
-        if (lowest > most) lowest = 0;
+        above = found[0];
+        uint32_t most = key_of(above_bin(bin)), lowest = key_of(below_bin(bin));
+        const float pos0 = (float)bin, pos1 = bin == kBins - 1 ? INFINITY : (float)(bin + 1);
         for (;;) {
-            int shift = 0;
-            while (((most - lowest) >> shift) >= (uint32_t)kBins) ++shift;
+            const int shift = max(0, 23 - __clz(most - lowest));        // 2^9 bins at most
             next_histogram();
-            each([&](int i, float x) {
-                x = value(x);
-                if (x == -INFINITY) return;
-                const uint32_t key = key_of(x);
-                if (key < lowest || key > most || !stays(i, key) || bin_of(position(x)) != bin) return;
-                const int b = (int)((most - key) >> shift);
+            each_in(value_of(lowest), value_of(most), [&](int i, float x) {
+                const float pos = position(x);
+                if (!stays(i, x) || pos < pos0 || !(pos < pos1 || pos1 == INFINITY)) return;
+                const int b = (int)((most - key_of(x)) >> shift);
                 if (by_weight) {
                     const u64 w = weight(s, x);
-                    if (w != 0) add_weight(b, w);
+                    if (w != 0) add_weight(b, (uint32_t)(w >> 21), (uint32_t)w & 0x1fffffu);
                 } else {
                     atomicAdd(&hist[b], 1u);
                 }
             });
-            const u64 above_it = found[0];
-            border(above_it, by_weight, [&](u64) { return want; }, total);
-            most = most - ((uint32_t)found_bin << shift);
+            cluster.sync();
+            // (the bin's values lie in that range, so they reach it)
+            if (!border(by_weight ? bin_sum(0) + (bin_sum(1) << 32) : bin_sum(0), above, [&](u64) { return want; })) return;
+            above = found[0];
+            most -= (uint32_t)found_bin << shift;
             if (shift == 0) break;
             lowest = max(lowest, most - ((1u << shift) - 1));
         }
         // the values equal to the border's: the first of them by their index
-        const uint32_t key = most;
-        const u64 one = by_weight ? weight(s, value_of(key)) : 1;
-        const u64 rest = want - found[0], keep = (rest + one - 1) / one;
+        const float it = value_of(most);
+        const u64 one = by_weight ? weight(s, it) : 1, keep = (want - above + one - 1) / one;
         int32_t until = kAll;
-        if (found[1] > rest || found[1] > one) {
-            // (where only one is there, it stays)
-            u64 equal = 0, before;
-            each([&](int i, float x) { equal += value(x) != -INFINITY && key_of(value(x)) == key && stays(i, key) ? 1 : 0; });
-            const u64 there = equal;
-            const u64 all = cluster_sum(equal, before);
-            u64 here = there;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) here += __shfl_xor_sync(0xffffffffu, here, o);
+        if (found[1] > one) {                   // (where only one is there, it stays)
+            u64 equal = 0;
+            each_in(it, it, [&](int i, float x) { equal += stays(i, x) ? 1 : 0; });
+            const u64 all = cluster_sum(equal, before, here);
             if (keep < all) {
                 if (keep > before && keep <= before + here) {
                     // this warp has the last one
@@ -402,14 +495,12 @@ sample_kernel(const Sampling a, const int32_t slice) {
                     for (int v0 = w0; v0 < w1; v0 += 32) {
                         const int v = v0 + lane;
                         uint32_t bits = 0;
-                        if (v < w1) {
-                            float x[VEC];
-                            Vec<Tin>::unpack(data[v], x);
+                        if (v < w1)
 #pragma unroll
-                            for (int e = 0; e < VEC; ++e)
-                                if (value(x[e]) != -INFINITY && key_of(value(x[e])) == key && stays(index_of(v) + e, key))
-                                    bits |= 1u << e;
-                        }
+                            for (int e = 0; e < VEC; ++e) {
+                                const float x = Vec<Tin>::load(data + v, e);
+                                if (x == it && stays(index_of(v) + e, x)) bits |= 1u << e;
+                            }
                         int run = __popc(bits);
                         const int cnt = run;
 #pragma unroll
@@ -418,9 +509,8 @@ sample_kernel(const Sampling a, const int32_t slice) {
                             if (lane >= o) run += z;
                         }
                         if (keep > seen + run - cnt && keep <= seen + run) {
-                            uint32_t left = bits;
-                            for (int c = (int)(keep - (seen + run - cnt)); c > 1; --c) left &= left - 1;
-                            const int at = index_of(v) + __ffs(left) - 1;
+                            for (int c = (int)(keep - (seen + run - cnt)); c > 1; --c) bits &= bits - 1;
+                            const int at = index_of(v) + __ffs(bits) - 1;
                             for (int r = 0; r < ranks; ++r) *cluster.map_shared_rank(&chosen_index, r) = at;
                         }
                         seen += __shfl_sync(0xffffffffu, run, 31);
@@ -430,19 +520,12 @@ sample_kernel(const Sampling a, const int32_t slice) {
                 until = chosen_index;
             }
         }
-        last = key == border_key ? min(last, until) : until;
-        border_key = key;
+        last = it == border_at ? min(last, until) : until;
+        border_at = it;
     };
 
     u64 sum = 0;                                // of what stays
-    u64 w_least = 0;
-    if (least > 0.f) w_least = (u64)(fminf(least, 1.f) * 0x1p42f);
-    const bool none = top == -INFINITY;
-    // the weight that top-p asks of a total (rounded up, at least something)
-    auto share = [&](u64 total) {
-        const u64 by64 = p > 0.f ? (u64)(p * 0x1p63f) << 1 : 0, whole = __umul64hi(total, by64);
-        return max(total * by64 != 0 ? whole + 1 : whole, (u64)1);
-    };
+    const u64 w_least = least > 0.f ? (u64)(fminf(least, 1.f) * 0x1p42f) : 0;
     // the first token whose running sum exceeds floor(u sum / 2^24) (the sum of all does, since u < 2^24)
     auto drawn = [&]() {
         const uint32_t tick = __float2uint_rz(fminf(fmaxf(u, 0.f) * 16777216.f, 16777215.f));
@@ -452,164 +535,204 @@ sample_kernel(const Sampling a, const int32_t slice) {
     // ---- a small k: the few logits that can be among the first k, sorted in one CTA
     bool done = false;
     if (!none && k > 0 && k < V && k <= kListK && k <= ranks * kThreads / 2) {
-        // k of the threads' largest logits are no smaller than this bin's
+        // k of the threads' largest logits lie in the bins up to this one
         next_histogram();
-        const float mine_top = value(my_top);
-        if (mine_top != -INFINITY) atomicAdd(&hist[bin_of(position(mine_top))], 1u);
-        u64 total;
-        const u64 want = border(0, false, [&](u64) { return (u64)k; }, total);
-        const float until = total < want || found_bin == kBins - 1 ? INFINITY : (float)(found_bin + 1);
-        cluster.sync();                         // the histograms are read: the lists take their place
-        each([&](int i, float x) {
-            x = value(x);
-            if (x == -INFINITY || !(position(x) < until)) return;
+        if (my_top != -INFINITY) atomicAdd(&hist[bin_of(position(my_top))], 1u);
+        cluster.sync();
+        const float from = border(bin_sum(0), 0, [&](u64) { return (u64)k; }) ? below_bin(found_bin) : -3.402823466e38f;
+        each_in(from, s.m, [&](int i, float x) {
             const int at = atomicAdd(&count, 1);
-            if (at < kList) list[at] = (u64)key_of(x) << 32 | (uint32_t)~i;
+            if (at >= kList) return;
+            list[at] = (u64)key_of(x) << 32 | (uint32_t)~i;
         });
         cluster.sync();
-        int all = 0, before = 0;
-        for (int r = 0; r < ranks; ++r) {
-            const int c = *cluster.map_shared_rank(&count, r);
-            before += r < rank ? c : 0;
-            all += c;
+        // the lists' lengths, a rank to a lane; warp r brings rank r's to the first CTA
+        const int length = lane < ranks ? *cluster.map_shared_rank(&count, lane) : 0;
+        int upto = length;
+#pragma unroll
+        for (int o = 1; o < kMaxRanks; o <<= 1) {
+            const int z = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += z;
         }
+        const int all = __shfl_sync(0xffffffffu, upto, kMaxRanks - 1);
         done = all <= kList;
         if (done && rank == 0) {
-            for (int r = 1, at = count; r < ranks; ++r) {
-                const int c = *cluster.map_shared_rank(&count, r);
-                const u64 *from = cluster.map_shared_rank(list, r);
-                for (int i = tid; i < c; i += kThreads) list[at + i] = from[i];
-                at += c;
+            if (warp > 0 && warp < ranks) {
+                const int c = __shfl_sync(0xffffffffu, length, warp), at = __shfl_sync(0xffffffffu, upto, warp) - c;
+                const u64 *from_it = cluster.map_shared_rank(list, warp);
+                for (int i = lane; i < c; i += 32) list[at + i] = from_it[i];
             }
-            __syncthreads();
-            sort_down(list, all, tid);
-            // cum(n, w): the sums of w(i) up to each of the thread's elements 4 tid .. 4 tid + 3 of n
-            u64 w[4], cum[4];
-            auto scan = [&](int n, auto f) {
-                u64 run = 0;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = 4 * tid + e;
-                    w[e] = i < n ? f(list[i]) : 0;
-                    run += w[e];
-                    cum[e] = run;
-                }
-                const u64 own = run;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const u64 z = __shfl_up_sync(0xffffffffu, run, o);
-                    if (lane >= o) run += z;
-                }
-                __syncthreads();
-                if (lane == 31) part[warp] = run;
-                __syncthreads();
-                u64 sum_all = 0, add = run - own;
-                for (int x = 0; x < kWarps; ++x) {
-                    add += x < warp ? part[x] : 0;
-                    sum_all += part[x];
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) cum[e] += add;
-                return sum_all;
-            };
-            const int first_k = min(k, all);
-            const u64 of_k = scan(first_k, [&](u64 c) { return weight(s, value_of((uint32_t)(c >> 32))); });
-            const u64 goal = p < 1.f && !greedy ? share(of_k) : ~(u64)0;
-            int stay = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                stay += 4 * tid + e < first_k && cum[e] - w[e] < goal && (4 * tid + e == 0 || w[e] >= w_least) ? 1 : 0;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) stay += __shfl_xor_sync(0xffffffffu, stay, o);
             if (tid == 0) chosen_count = 0;
             __syncthreads();
-            if (lane == 0) atomicAdd(&chosen_count, stay);
-            __syncthreads();
-            stay = chosen_count;                // a beginning of the order
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (4 * tid + e == stay - 1) {
-                    const u64 c = list[stay - 1];
-                    for (int r = 0; r < ranks; ++r) {
-                        *cluster.map_shared_rank(&chosen_key, r) = (uint32_t)(c >> 32);
-                        *cluster.map_shared_rank(&chosen_index, r) = (int32_t)~(uint32_t)c;
-                        *cluster.map_shared_rank(&found[0], r) = cum[e];
-                    }
+            auto choose = [&](u64 c, u64 all_of_it) {           // c is the last of the order that stays
+                for (int r = 0; r < ranks; ++r) {
+                    *cluster.map_shared_rank(&chosen_key, r) = (uint32_t)(c >> 32);
+                    *cluster.map_shared_rank(&chosen_index, r) = (int32_t)~(uint32_t)c;
+                    *cluster.map_shared_rank(&found[0], r) = all_of_it;
                 }
-            __syncthreads();
-            sum = found[0];
-            if (a.token != nullptr) {
-                // in index order
-                for (int i = tid; i < stay; i += kThreads) list[i] = list[i] << 32 | list[i] >> 32;
+            };
+            if (all <= kFew) {
+                // Every pair is compared, four threads to an element: which stand before it in the order, and
+                // what they weigh; then what those weigh that stay and have a smaller index.
+                u64 *const weights = list + kFew;
+                for (int i = tid; i < all; i += kThreads) weights[i] = weight(s, value_of((uint32_t)(list[i] >> 32)));
                 __syncthreads();
-                sort_down(list, stay, tid);
-                scan(stay, [&](u64 c) { return weight(s, value_of((uint32_t)c)); });
-                const u64 need = drawn();
+                const int i = tid >> 2, h = tid & 3;
+                const u64 mine_c = i < all ? list[i] : 0, mine_w = i < all ? weights[i] : 0;
+                int place = 0;
+                u64 ahead = 0;
+                for (int j = h; j < all; j += 4) {
+                    const bool it = list[j] > mine_c;
+                    place += it ? 1 : 0;
+                    ahead += it ? weights[j] : 0;
+                }
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (4 * tid + e < stay && cum[e] > need && cum[e] - w[e] <= need)
-                        a.token[n] = (int32_t)~(uint32_t)(list[4 * tid + e] >> 32);
-            }
-        }
-        cluster.sync();
-        if (done) {
-            border_key = chosen_key;
-            last = chosen_index;
-            sum = found[0];
-        }
-    }
-    if (!none && !done) {
-        if (k > 0 && k < V) narrow(false, [&](u64) { return (u64)k; });
-        if (p < 1.f && !greedy) narrow(true, share);
-        // ---- the draw, in index order
-        u64 before;
-        each([&](int i, float x) {
-            x = value(x);
-            if (!stays(i, key_of(x))) return;
-            const u64 w = weight(s, x);
-            sum += w >= w_least ? w : 0;
-        });
-        u64 here = sum;
-        sum = cluster_sum(sum, before);
-        if (a.token != nullptr) {
+                for (int o = 1; o < 4; o <<= 1) {
+                    place += __shfl_xor_sync(0xffffffffu, place, o);
+                    ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
+                }
+                // sums over the block, each element once
+                auto block_sum = [&](u64 x) {
+                    x = h == 0 ? x : 0;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) here += __shfl_xor_sync(0xffffffffu, here, o);
-            const u64 need = drawn();
-            if (before <= need && before + here > need) {
-                for (int v0 = w0; v0 < w1; v0 += 32) {
-                    const int v = v0 + lane;
-                    u64 w[VEC], all = 0;
-                    float x[VEC];
-                    if (v < w1) Vec<Tin>::unpack(data[v], x);
+                    for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+                    __syncthreads();
+                    if (lane == 0) part[warp] = x;
+                    __syncthreads();
+                    x = 0;
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        w[e] = 0;
-                        if (v < w1 && stays(index_of(v) + e, key_of(value(x[e])))) w[e] = weight(s, value(x[e]));
-                        if (w[e] < w_least) w[e] = 0;
-                        all += w[e];
+                    for (int w = 0; w < kWarps; ++w) x += part[w];
+                    return x;
+                };
+                const bool of_k = i < all && place < k;
+                const u64 goal = p < 1.f ? share(block_sum(of_k ? mine_w : 0)) : ~(u64)0;
+                const bool stay = of_k && ahead < goal && (place == 0 || mine_w >= w_least);
+                __syncthreads();
+                if (i < all && h == 0) weights[i] = stay ? mine_w : 0;
+                if (stay && h == 0) atomicAdd(&chosen_count, 1);
+                sum = block_sum(stay ? mine_w : 0);
+                if (stay && h == 0 && place == chosen_count - 1) choose(mine_c, sum);
+                if (a.token != nullptr) {
+                    u64 run = 0;
+                    for (int j = h; j < all; j += 4) run += (uint32_t)list[j] >= (uint32_t)mine_c ? weights[j] : 0;
+#pragma unroll
+                    for (int o = 1; o < 4; o <<= 1) run += __shfl_xor_sync(0xffffffffu, run, o);
+                    const u64 need = drawn();
+                    if (stay && h == 0 && run > need && run - mine_w <= need) a.token[n] = (int32_t)~(uint32_t)mine_c;
+                }
+            } else {
+                sort_down(list, all, tid);
+                // the sums of f(list[i]) up to each of the thread's elements 4 tid .. 4 tid + 3 of n
+                u64 w[4], cum[4];
+                auto scan = [&](int n_of, int shift) {
+                    u64 run = 0;
+#pragma unroll 1
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = 4 * tid + e;
+                        const u64 x = i < n_of ? weight(s, value_of((uint32_t)(list[i] >> shift))) : 0;
+                        run += x;
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            if (y == e) {
+                                w[y] = x;
+                                cum[y] = run;
+                            }
                     }
-                    u64 run = all;
+                    const u64 own = run;
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
                         const u64 z = __shfl_up_sync(0xffffffffu, run, o);
                         if (lane >= o) run += z;
                     }
-                    const unsigned hit = __ballot_sync(0xffffffffu, before + run > need);
-                    if (hit != 0) {
-                        if (lane == __ffs(hit) - 1) {
-                            u64 at = before + run - all;
-                            int e = 0;
+                    __syncthreads();
+                    if (lane == 31) part[warp] = run;
+                    __syncthreads();
+                    u64 all_of_it = 0, add = run - own;
 #pragma unroll
-                            for (int z = 0; z < VEC; ++z) {
-                                at += w[z];
-                                if (at <= need) e = z + 1;
-                            }
-                            a.token[n] = index_of(v) + e;
-                        }
-                        break;
+                    for (int x = 0; x < kWarps; ++x) {
+                        add += x < warp ? part[x] : 0;
+                        all_of_it += part[x];
                     }
-                    before += __shfl_sync(0xffffffffu, run, 31);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) cum[e] += add;
+                    return all_of_it;
+                };
+                const int first_k = min(k, all);
+                const u64 of_k = scan(first_k, 32), goal = p < 1.f ? share(of_k) : ~(u64)0;
+                int stay = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    stay += 4 * tid + e < first_k && cum[e] - w[e] < goal && (4 * tid + e == 0 || w[e] >= w_least) ? 1 : 0;
+                stay = __reduce_add_sync(0xffffffffu, stay);
+                if (lane == 0) atomicAdd(&chosen_count, stay);
+                __syncthreads();
+                stay = chosen_count;            // a beginning of the order
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (4 * tid + e == stay - 1) choose(list[stay - 1], cum[e]);
+                __syncthreads();
+                sum = found[0];
+                if (a.token != nullptr) {
+                    // in index order
+                    for (int i = tid; i < stay; i += kThreads) list[i] = list[i] << 32 | list[i] >> 32;
+                    __syncthreads();
+                    sort_down(list, stay, tid);
+                    scan(stay, 0);
+                    const u64 need = drawn();
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (4 * tid + e < stay && cum[e] > need && cum[e] - w[e] <= need)
+                            a.token[n] = (int32_t)~(uint32_t)(list[4 * tid + e] >> 32);
                 }
+            }
+        }
+        cluster.sync();
+        if (done) {
+            border_at = value_of(chosen_key);
+            last = chosen_index;
+            sum = found[0];
+        }
+    }
+    if (!none && !done) {
+        if (k > 0 && k < V) narrow(false);
+        if (p < 1.f) narrow(true);
+        // ---- the draw, in index order
+        u64 before, here;
+        auto counts = [&](int i, float x, float w) { return stays(i, x) && (w_least == 0 || fixed42(w) >= w_least); };
+        sum = cluster_sum(weigh(lowest_value(), counts, [](float, uint32_t, uint32_t) {}), before, here);
+        const u64 need = drawn();
+        if (a.token != nullptr && before <= need && before + here > need) {
+            for (int v0 = w0; v0 < w1; v0 += 32) {
+                const int v = v0 + lane;
+                u64 all = 0;
+#pragma unroll 1
+                for (int e = 0; e < VEC; ++e) {
+                    const float x = v < w1 ? Vec<Tin>::load(data + v, e) : -INFINITY;
+                    const u64 w = x > -INFINITY && stays(index_of(v) + e, x) ? weight(s, x) : 0;
+                    all += w >= w_least ? w : 0;
+                }
+                u64 run = all;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const u64 z = __shfl_up_sync(0xffffffffu, run, o);
+                    if (lane >= o) run += z;
+                }
+                const unsigned hit = __ballot_sync(0xffffffffu, before + run > need);
+                if (hit != 0) {
+                    if (lane == __ffs(hit) - 1) {
+                        u64 at = before + run - all;
+                        int e = 0;
+                        for (; e < VEC - 1; ++e) {
+                            const float x = Vec<Tin>::load(data + v, e);
+                            const u64 w = x > -INFINITY && stays(index_of(v) + e, x) ? weight(s, x) : 0;
+                            at += w >= w_least ? w : 0;
+                            if (at > need) break;
+                        }
+                        a.token[n] = index_of(v) + e;
+                    }
+                    break;
+                }
+                before += __shfl_sync(0xffffffffu, run, 31);
             }
         }
     } else if (none && a.token != nullptr && rank == 0 && tid == 0) {
@@ -618,32 +741,37 @@ sample_kernel(const Sampling a, const int32_t slice) {
     if (a.probs != nullptr) {
         const float inv = none ? 0.f : (float)(0x1p42 / (double)sum);
         const bool bf16 = a.probs_bf16 != 0;
+        Scale deep = s;                         // down to 2^-125
+        deep.least = fmaxf(s.m - 125.f / s.c, -3.402823466e38f);
+        const float from = none ? INFINITY : fmaxf(lowest_value(), deep.least);
         unsigned char *out = static_cast<unsigned char *>(a.probs) + n * (int64_t)V * (bf16 ? 2 : 4);
         // whole vectors where the output's rows lie as the input's
         const bool whole = ((reinterpret_cast<uintptr_t>(out) - (size_t)lead * (bf16 ? 2 : 4)) & (bf16 ? VEC * 2 - 1 : 15)) == 0;
+#pragma unroll 1
         for (int v = w0 + lane; v < w1; v += 32) {
-            float x[VEC], y[VEC];
-            Vec<Tin>::unpack(data[v], x);
+            const uint4 raw = data[v];
             const int e0 = index_of(v);
+            float y[VEC];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float z = value(x[e]);
-                float q;
-                int ex;
-                y[e] = 0.f;
-                if (!none && z != -INFINITY && stays(e0 + e, key_of(z)) && weight_parts(s, z, -126.f, q, ex) &&
-                    (w_least == 0 || weight(s, z) >= w_least))
-                    y[e] = (1.f + q) * __int_as_float((ex + 127) << 23) * inv;
+            for (int e = 0; e < VEC; ++e) y[e] = 0.f;
+            if (Vec<Tin>::largest(raw) >= from) {
+                float2 x[VEC / 2];
+                Vec<Tin>::unpack(raw, x);
+#pragma unroll
+                for (int e = 0; e < VEC / 2; ++e) {
+                    const float2 w = weights2(deep, x[e]);
+                    if (x[e].x >= from && stays(e0 + 2 * e, x[e].x) && (w_least == 0 || fixed42(w.x) >= w_least))
+                        y[2 * e] = w.x * inv;
+                    if (x[e].y >= from && stays(e0 + 2 * e + 1, x[e].y) && (w_least == 0 || fixed42(w.y) >= w_least))
+                        y[2 * e + 1] = w.y * inv;
+                }
             }
             if (bf16) {
                 __nv_bfloat16 *to = reinterpret_cast<__nv_bfloat16 *>(out) + e0;
                 if (whole && e0 >= 0 && e0 + VEC <= V) {
                     uint32_t z[VEC / 2];
 #pragma unroll
-                    for (int e = 0; e < VEC / 2; ++e) {
-                        const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * e], y[2 * e + 1]);
-                        memcpy(&z[e], &b, 4);
-                    }
+                    for (int e = 0; e < VEC / 2; ++e) z[e] = tc::pack_bf16x2(y[2 * e], y[2 * e + 1]);
                     if (VEC == 8) *reinterpret_cast<uint4 *>(to) = make_uint4(z[0], z[1], z[2], z[VEC / 2 - 1]);
                     else *reinterpret_cast<uint2 *>(to) = make_uint2(z[0], z[1]);
                 } else {
