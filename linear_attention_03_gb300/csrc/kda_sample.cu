@@ -184,7 +184,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
     __shared__ u64 part[kWarps], part_all, found[2];                          // found: what lies above the border's bin, what is in it
     __shared__ u64 totals[2][kMaxRanks];
     __shared__ float tops[kMaxRanks], warp_top[kWarps];
-    __shared__ int32_t found_bin, chosen_index, count, chosen_count;
+    __shared__ int32_t found_bin, chosen_index, count, pool, chosen_count;
     __shared__ uint32_t chosen_key;
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
     cluster.barrier_arrive();
@@ -297,8 +297,9 @@ sample_kernel(const Sampling a, const int32_t slice) {
             }
         }
     };
-    // The weights of the thread's elements that are at least `from` and of which which(i, x, w) holds, added up;
-    // also(x, hi, lo) sees these with their digits.
+    // The weights of the thread's elements that are at least `from` and of which which(i, x, hi, lo) holds (hi, lo:
+    // the weight's digits), added up; also(x, hi, lo) sees vectors with their digits, zeros where it does not
+    // hold.  No branches, so that a vector's weights are formed side by side.
     auto weigh = [&](float from, auto which, auto also) {
         from = fmaxf(from, s.least);
         uint32_t hi = 0, lo = 0;                // (digits of 21 bits: no thread has 2,048 elements)
@@ -309,18 +310,25 @@ sample_kernel(const Sampling a, const int32_t slice) {
             float2 x[VEC / 2];
             Vec<Tin>::unpack(y, x);
             const int i = index_of(v);
+            uint32_t h[VEC], l[VEC];
 #pragma unroll
             for (int e = 0; e < VEC / 2; ++e) {
-                float2 w = weights2(s, x[e]), h, l;
-                w.x = x[e].x >= from && which(i + 2 * e, x[e].x, w.x) ? w.x : 0.f;
-                w.y = x[e].y >= from && which(i + 2 * e + 1, x[e].y, w.y) ? w.y : 0.f;
-                digits42(w, h, l);
-                const uint32_t h0 = digit(h.x), h1 = digit(h.y), l0 = digit(l.x), l1 = digit(l.y);
-                hi += h0 + h1;
-                lo += l0 + l1;
-                also(x[e].x, h0, l0);
-                also(x[e].y, h1, l1);
+                float2 high, low;
+                digits42(weights2(s, x[e]), high, low);
+                const uint32_t h0 = digit(high.x), h1 = digit(high.y), l0 = digit(low.x), l1 = digit(low.y);
+                const bool on0 = (x[e].x >= from) & which(i + 2 * e, x[e].x, h0, l0);
+                const bool on1 = (x[e].y >= from) & which(i + 2 * e + 1, x[e].y, h1, l1);
+                h[2 * e] = on0 ? h0 : 0;
+                h[2 * e + 1] = on1 ? h1 : 0;
+                l[2 * e] = on0 ? l0 : 0;
+                l[2 * e + 1] = on1 ? l1 : 0;
             }
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                hi += h[e];
+                lo += l[e];
+            }
+            also(x, h, l);
         }
         return ((u64)hi << 21) + lo;
     };
@@ -413,7 +421,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
     // What stays: values above the border, and of the equal ones those up to `last`.
     float border_at = -INFINITY;
     int32_t last = kAll;
-    auto stays = [&](int i, float x) { return x > border_at || (x == border_at && i <= last); };
+    auto stays = [&](int i, float x) { return (x > border_at) | ((x == border_at) & (i <= last)); };
     auto lowest_value = [&]() { return fmaxf(border_at, -3.402823466e38f); };
     // the weight that top-p asks of a total (rounded up, at least something)
     auto share = [&](u64 total) {
@@ -443,8 +451,21 @@ sample_kernel(const Sampling a, const int32_t slice) {
         if (!by_weight) {
             each_in(lowest_value(), s.m, [&](int, float x) { atomicAdd(&hist[bin_of(position(x))], 1u); });
         } else if (border_at == -INFINITY) {
-            weigh(lowest_value(), [](int, float, float) { return true; }, [&](float x, uint32_t hi, uint32_t lo) {
-                if ((hi | lo) != 0) add_weight(bin_of(position(x)), hi, lo);
+            weigh(lowest_value(), [](int, float, uint32_t, uint32_t) { return true; },
+                  [&](const float2 (&x)[VEC / 2], const uint32_t (&hi)[VEC], const uint32_t (&lo)[VEC]) {
+                // (all low words on their way before the first one is waited for)
+                uint32_t old[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    old[e] = 0;
+                    const int b = bin_of(position(e & 1 ? x[e / 2].y : x[e / 2].x));
+                    if ((hi[e] | lo[e]) != 0) old[e] = atomicAdd(&hist[b], (hi[e] << 21) + lo[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const uint32_t high = (hi[e] >> 11) + (old[e] + ((hi[e] << 21) + lo[e]) < old[e] ? 1u : 0u);
+                    if (high != 0) atomicAdd(&hist[kBins + bin_of(position(e & 1 ? x[e / 2].y : x[e / 2].x))], high);
+                }
             });
         } else {
             each_in(lowest_value(), s.m, [&](int i, float x) {
@@ -458,20 +479,40 @@ sample_kernel(const Sampling a, const int32_t slice) {
         above = found[0];
         uint32_t most = key_of(above_bin(bin)), lowest = key_of(below_bin(bin));
         const float pos0 = (float)bin, pos1 = bin == kBins - 1 ? INFINITY : (float)(bin + 1);
+        auto in_bin = [&](int i, float x) {
+            const float pos = position(x);
+            return stays(i, x) && pos >= pos0 && (pos < pos1 || pos1 == INFINITY);
+        };
+        // the bin's elements, where the list has room for the CTA's
+        if (tid == 0) pool = 0;
+        __syncthreads();
+        each_in(value_of(lowest), value_of(most), [&](int i, float x) {
+            if (!in_bin(i, x)) return;
+            const int at = atomicAdd(&pool, 1);
+            if (at < kList) list[at] = (u64)key_of(x) << 32 | (uint32_t)i;
+        });
+        __syncthreads();
+        const int pooled = pool;
         for (;;) {
             const int shift = max(0, 23 - __clz(most - lowest));        // 2^9 bins at most
             next_histogram();
-            each_in(value_of(lowest), value_of(most), [&](int i, float x) {
-                const float pos = position(x);
-                if (!stays(i, x) || pos < pos0 || !(pos < pos1 || pos1 == INFINITY)) return;
-                const int b = (int)((most - key_of(x)) >> shift);
+            auto add = [&](uint32_t key) {
+                const int b = (int)((most - key) >> shift);
                 if (by_weight) {
-                    const u64 w = weight(s, x);
+                    const u64 w = weight(s, value_of(key));
                     if (w != 0) add_weight(b, (uint32_t)(w >> 21), (uint32_t)w & 0x1fffffu);
                 } else {
                     atomicAdd(&hist[b], 1u);
                 }
-            });
+            };
+            if (pooled <= kList) {
+                for (int i = tid; i < pooled; i += kThreads) {
+                    const uint32_t key = (uint32_t)(list[i] >> 32);
+                    if (key >= lowest && key <= most) add(key);
+                }
+            } else {
+                each_in(value_of(lowest), value_of(most), [&](int i, float x) { if (in_bin(i, x)) add(key_of(x)); });
+            }
             cluster.sync();
             // (the bin's values lie in that range, so they reach it)
             if (!border(by_weight ? bin_sum(0) + (bin_sum(1) << 32) : bin_sum(0), above, [&](u64) { return want; })) return;
@@ -698,8 +739,11 @@ sample_kernel(const Sampling a, const int32_t slice) {
         if (p < 1.f) narrow(true);
         // ---- the draw, in index order
         u64 before, here;
-        auto counts = [&](int i, float x, float w) { return stays(i, x) && (w_least == 0 || fixed42(w) >= w_least); };
-        sum = cluster_sum(weigh(lowest_value(), counts, [](float, uint32_t, uint32_t) {}), before, here);
+        const uint32_t least_hi = (uint32_t)(w_least >> 21), least_lo = (uint32_t)w_least & 0x1fffffu;
+        auto counts = [&](int i, float x, uint32_t hi, uint32_t lo) {
+            return stays(i, x) & ((hi > least_hi) | ((hi == least_hi) & (lo >= least_lo)));
+        };
+        sum = cluster_sum(weigh(lowest_value(), counts, [](auto &, auto &, auto &) {}), before, here);
         const u64 need = drawn();
         if (a.token != nullptr && before <= need && before + here > need) {
             for (int v0 = w0; v0 < w1; v0 += 32) {
