@@ -30,13 +30,13 @@ typedef unsigned long long u64;
 constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxRanks = 8;
 constexpr int kBins = 512;                      // of a histogram
 constexpr float kPerOctave = 12.f;              // bins for a halving of w
-constexpr int kList = 2048, kListK = 1024;      // logits that are sorted at most, and the k for which that is tried
+constexpr int kList = 2048, kListK = 1024;      // logits that go to one CTA at most, and the k for which that is tried
 constexpr int kFew = 128;                       // logits of which every pair is compared instead
 constexpr int32_t kAll = 0x7fffffff;
 // two histograms and a list; a row of 2^18 logits over eight CTAs beside them
 constexpr int kScratch = 4 * kBins * 4 + kList * 8;
 constexpr int kMaxSmem = KDA_MAX_VOCABULARY / kMaxRanks * 4 + 32 + kScratch;
-static_assert(kList <= 4 * kThreads && 4 * kFew == kThreads && 2 * kFew <= kList, "threads to the elements of a list");
+static_assert(kList == 4 * kThreads && 4 * kFew == kThreads && 2 * kFew <= kList, "threads to the elements of a list");
 static_assert(kBins == kThreads, "a thread per bin");
 
 struct Sampling {
@@ -98,6 +98,17 @@ template <> struct Vec<__nv_bfloat16> {
     }
 };
 
+// The order as a whole number: by value, then by index, the first of all the largest.
+constexpr int kIndexBits = 18;
+static_assert(KDA_MAX_VOCABULARY <= 1 << kIndexBits, "an index's bits");
+__device__ __forceinline__ u64 ordered(uint32_t key, int i) {
+    return (u64)key << kIndexBits | (uint32_t)((1 << kIndexBits) - 1 - i);
+}
+__device__ __forceinline__ uint32_t ordered_key(u64 c) { return (uint32_t)(c >> kIndexBits); }
+__device__ __forceinline__ int ordered_index(u64 c) {
+    return (1 << kIndexBits) - 1 - (int)((uint32_t)c & ((1u << kIndexBits) - 1));
+}
+
 // log2 w = (x - m)(c + cl); below x = least w counts as zero
 struct Scale {
     float m, c, cl, least;
@@ -151,25 +162,59 @@ __device__ __forceinline__ u64 weight(const Scale &s, float x) {
     return fixed42(x >= s.least ? w : 0.f);
 }
 
-// list[0 .. n) by size, the largest first; the block's threads.  (Bitonic; what lies behind n up to the
-// next power of two is set to zero.)
-__device__ __forceinline__ void sort_down(u64 *list, int n, int tid) {
-    int all = 2;
-    while (all < n) all *= 2;
-    for (int i = n + tid; i < all; i += kThreads) list[i] = 0;
-    __syncthreads();
-    for (int size = 2; size <= all; size *= 2)
-        for (int step = size / 2; step > 0; step /= 2) {
-            for (int i = tid; i < all / 2; i += kThreads) {
-                const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
-                const u64 x = list[lo], y = list[hi];
-                if ((x < y) == ((lo & size) == 0)) {
-                    list[lo] = y;
-                    list[hi] = x;
+// The larger one first (or last).
+__device__ __forceinline__ void in_order(u64 &a, u64 &b, bool down) {
+    const bool swap = (a < b) == down;
+    const u64 x = swap ? b : a, y = swap ? a : b;
+    a = x;
+    b = y;
+}
+// The block's elements, thread t's x being 4 t .. 4 t + 3 of `all` (a power of two up to 2,048; the others
+// zeros), by size, the largest first.  Bitonic: steps of one and two within a thread, up to 64 within its
+// warp, the others through shared memory (2,048 elements: 66 steps, ten of them there).
+__device__ __forceinline__ void sort_down(u64 (&x)[4], u64 *room, int all) {
+    const int tid = threadIdx.x;
+    const bool mine = 4 * (tid & ~31) < all;            // (whole warps)
+#pragma unroll 1
+    for (int size = 2; size <= all; size *= 2) {
+#pragma unroll 1
+        for (int step = size / 2; step >= 128; step /= 2) {
+            if (mine)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) room[4 * tid + e] = x[e];
+            __syncthreads();
+            if (mine)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 4 * tid + e;
+                    const u64 y = room[i ^ step];
+                    const bool larger = ((i & step) == 0) == ((i & size) == 0);
+                    x[e] = (x[e] < y) == larger ? y : x[e];
                 }
-            }
             __syncthreads();
         }
+        if (mine) {
+#pragma unroll 1
+            for (int step = min(size / 2, 64); step >= 4; step /= 2)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 4 * tid + e;
+                    const u64 y = __shfl_xor_sync(0xffffffffu, x[e], step / 4);
+                    const bool larger = ((i & step) == 0) == ((i & size) == 0);
+                    x[e] = (x[e] < y) == larger ? y : x[e];
+                }
+            const bool down = (4 * tid & size) == 0;
+            if (size >= 4) {
+                in_order(x[0], x[2], down);
+                in_order(x[1], x[3], down);
+                in_order(x[0], x[1], down);
+                in_order(x[2], x[3], down);
+            } else {
+                in_order(x[0], x[1], true);
+                in_order(x[2], x[3], false);
+            }
+        }
+    }
 }
 
 template <typename Tin>
@@ -181,7 +226,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
     // two histograms (low words, then high words) and a list
     uint32_t *const hists = reinterpret_cast<uint32_t *>(smem + (size_t)slice * 16), *hist = hists;
     u64 *const list = reinterpret_cast<u64 *>(hists + 4 * kBins);
-    __shared__ u64 part[kWarps], part_all, found[2];                          // found: what lies above the border's bin, what is in it
+    __shared__ u64 part[kWarps], part_all, chosen_sum, found[2];                          // found: what lies above the border's bin, what is in it
     __shared__ u64 totals[2][kMaxRanks];
     __shared__ float tops[kMaxRanks], warp_top[kWarps];
     __shared__ int32_t found_bin, chosen_index, count, pool, chosen_count;
@@ -273,8 +318,10 @@ sample_kernel(const Sampling a, const int32_t slice) {
     s.least = fmaxf(s.m - 44.f / s.c, -3.402823466e38f);
     // bins of equal width in log2 w; the last one takes everything below
     const float by = s.c * kPerOctave;
-    auto position = [&](float x) { return (s.m - x) * by; };
-    auto bin_of = [&](float pos) { return pos < (float)(kBins - 1) ? (int)pos : kBins - 1; };
+    // (the whole part of the product is in the significand's low bits, as in digits42)
+    auto bin_of = [&](float x) {
+        return (int)min(__float_as_uint(__fmaf_rz(s.m - x, by, 8388608.f)) - kBias, (uint32_t)(kBins - 1));
+    };
 
     // Runs f(i, x) over the elements of the warp that lie in [from, to], few of them (one comparison each lets
     // all others pass by).
@@ -449,7 +496,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
         };
         next_histogram();
         if (!by_weight) {
-            each_in(lowest_value(), s.m, [&](int, float x) { atomicAdd(&hist[bin_of(position(x))], 1u); });
+            each_in(lowest_value(), s.m, [&](int i, float x) { if (stays(i, x)) atomicAdd(&hist[bin_of(x)], 1u); });
         } else if (border_at == -INFINITY) {
             weigh(lowest_value(), [](int, float, uint32_t, uint32_t) { return true; },
                   [&](const float2 (&x)[VEC / 2], const uint32_t (&hi)[VEC], const uint32_t (&lo)[VEC]) {
@@ -458,19 +505,19 @@ sample_kernel(const Sampling a, const int32_t slice) {
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     old[e] = 0;
-                    const int b = bin_of(position(e & 1 ? x[e / 2].y : x[e / 2].x));
+                    const int b = bin_of(e & 1 ? x[e / 2].y : x[e / 2].x);
                     if ((hi[e] | lo[e]) != 0) old[e] = atomicAdd(&hist[b], (hi[e] << 21) + lo[e]);
                 }
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     const uint32_t high = (hi[e] >> 11) + (old[e] + ((hi[e] << 21) + lo[e]) < old[e] ? 1u : 0u);
-                    if (high != 0) atomicAdd(&hist[kBins + bin_of(position(e & 1 ? x[e / 2].y : x[e / 2].x))], high);
+                    if (high != 0) atomicAdd(&hist[kBins + bin_of(e & 1 ? x[e / 2].y : x[e / 2].x)], high);
                 }
             });
         } else {
             each_in(lowest_value(), s.m, [&](int i, float x) {
                 const u64 w = stays(i, x) ? weight(s, x) : 0;
-                if (w != 0) add_weight(bin_of(position(x)), (uint32_t)(w >> 21), (uint32_t)w & 0x1fffffu);
+                if (w != 0) add_weight(bin_of(x), (uint32_t)(w >> 21), (uint32_t)w & 0x1fffffu);
             });
         }
         cluster.sync();
@@ -478,18 +525,14 @@ sample_kernel(const Sampling a, const int32_t slice) {
         const int bin = found_bin;
         above = found[0];
         uint32_t most = key_of(above_bin(bin)), lowest = key_of(below_bin(bin));
-        const float pos0 = (float)bin, pos1 = bin == kBins - 1 ? INFINITY : (float)(bin + 1);
-        auto in_bin = [&](int i, float x) {
-            const float pos = position(x);
-            return stays(i, x) && pos >= pos0 && (pos < pos1 || pos1 == INFINITY);
-        };
+        auto in_bin = [&](int i, float x) { return stays(i, x) && bin_of(x) == bin; };
         // the bin's elements, where the list has room for the CTA's
         if (tid == 0) pool = 0;
         __syncthreads();
         each_in(value_of(lowest), value_of(most), [&](int i, float x) {
             if (!in_bin(i, x)) return;
             const int at = atomicAdd(&pool, 1);
-            if (at < kList) list[at] = (u64)key_of(x) << 32 | (uint32_t)i;
+            if (at < kList) list[at] = ordered(key_of(x), i);
         });
         __syncthreads();
         const int pooled = pool;
@@ -507,7 +550,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
             };
             if (pooled <= kList) {
                 for (int i = tid; i < pooled; i += kThreads) {
-                    const uint32_t key = (uint32_t)(list[i] >> 32);
+                    const uint32_t key = ordered_key(list[i]);
                     if (key >= lowest && key <= most) add(key);
                 }
             } else {
@@ -527,10 +570,28 @@ sample_kernel(const Sampling a, const int32_t slice) {
         int32_t until = kAll;
         if (found[1] > one) {                   // (where only one is there, it stays)
             u64 equal = 0;
-            each_in(it, it, [&](int i, float x) { equal += stays(i, x) ? 1 : 0; });
+            const bool in_pool = pooled <= kList;
+            if (in_pool) {
+                for (int i = tid; i < pooled; i += kThreads) equal += ordered_key(list[i]) == most ? 1 : 0;
+            } else {
+                each_in(it, it, [&](int i, float x) { equal += stays(i, x) ? 1 : 0; });
+            }
             const u64 all = cluster_sum(equal, before, here);
             if (keep < all) {
-                if (keep > before && keep <= before + here) {
+                auto publish = [&](int at) {
+                    for (int r = 0; r < ranks; ++r) *cluster.map_shared_rank(&chosen_index, r) = at;
+                };
+                if (in_pool) {
+                    // the CTA's equal ones in any order: the one with as many smaller indices as are wanted
+                    const u64 ahead = before - part[warp];      // of the CTAs before
+                    for (int i = tid; i < pooled; i += kThreads) {
+                        const u64 c = list[i];
+                        if (ordered_key(c) != most) continue;
+                        u64 smaller = ahead;            // (equal ones of a smaller index stand higher in the order)
+                        for (int j = 0; j < pooled; ++j) smaller += ordered_key(list[j]) == most && list[j] > c ? 1 : 0;
+                        if (smaller + 1 == keep) publish(ordered_index(c));
+                    }
+                } else if (keep > before && keep <= before + here) {
                     // this warp has the last one
                     u64 seen = before;
                     for (int v0 = w0; v0 < w1; v0 += 32) {
@@ -551,8 +612,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
                         }
                         if (keep > seen + run - cnt && keep <= seen + run) {
                             for (int c = (int)(keep - (seen + run - cnt)); c > 1; --c) bits &= bits - 1;
-                            const int at = index_of(v) + __ffs(bits) - 1;
-                            for (int r = 0; r < ranks; ++r) *cluster.map_shared_rank(&chosen_index, r) = at;
+                            publish(index_of(v) + __ffs(bits) - 1);
                         }
                         seen += __shfl_sync(0xffffffffu, run, 31);
                     }
@@ -578,13 +638,13 @@ sample_kernel(const Sampling a, const int32_t slice) {
     if (!none && k > 0 && k < V && k <= kListK && k <= ranks * kThreads / 2) {
         // k of the threads' largest logits lie in the bins up to this one
         next_histogram();
-        if (my_top != -INFINITY) atomicAdd(&hist[bin_of(position(my_top))], 1u);
+        if (my_top != -INFINITY) atomicAdd(&hist[bin_of(my_top)], 1u);
         cluster.sync();
         const float from = border(bin_sum(0), 0, [&](u64) { return (u64)k; }) ? below_bin(found_bin) : -3.402823466e38f;
         each_in(from, s.m, [&](int i, float x) {
             const int at = atomicAdd(&count, 1);
             if (at >= kList) return;
-            list[at] = (u64)key_of(x) << 32 | (uint32_t)~i;
+            list[at] = ordered(key_of(x), i);
         });
         cluster.sync();
         // the lists' lengths, a rank to a lane; warp r brings rank r's to the first CTA
@@ -607,16 +667,16 @@ sample_kernel(const Sampling a, const int32_t slice) {
             __syncthreads();
             auto choose = [&](u64 c, u64 all_of_it) {           // c is the last of the order that stays
                 for (int r = 0; r < ranks; ++r) {
-                    *cluster.map_shared_rank(&chosen_key, r) = (uint32_t)(c >> 32);
-                    *cluster.map_shared_rank(&chosen_index, r) = (int32_t)~(uint32_t)c;
-                    *cluster.map_shared_rank(&found[0], r) = all_of_it;
+                    *cluster.map_shared_rank(&chosen_key, r) = ordered_key(c);
+                    *cluster.map_shared_rank(&chosen_index, r) = ordered_index(c);
+                    *cluster.map_shared_rank(&chosen_sum, r) = all_of_it;
                 }
             };
             if (all <= kFew) {
                 // Every pair is compared, four threads to an element: which stand before it in the order, and
                 // what they weigh; then what those weigh that stay and have a smaller index.
                 u64 *const weights = list + kFew;
-                for (int i = tid; i < all; i += kThreads) weights[i] = weight(s, value_of((uint32_t)(list[i] >> 32)));
+                for (int i = tid; i < all; i += kThreads) weights[i] = weight(s, value_of(ordered_key(list[i])));
                 __syncthreads();
                 const int i = tid >> 2, h = tid & 3;
                 const u64 mine_c = i < all ? list[i] : 0, mine_w = i < all ? weights[i] : 0;
@@ -655,29 +715,28 @@ sample_kernel(const Sampling a, const int32_t slice) {
                 if (stay && h == 0 && place == chosen_count - 1) choose(mine_c, sum);
                 if (a.token != nullptr) {
                     u64 run = 0;
-                    for (int j = h; j < all; j += 4) run += (uint32_t)list[j] >= (uint32_t)mine_c ? weights[j] : 0;
+                    for (int j = h; j < all; j += 4) run += ordered_index(list[j]) <= ordered_index(mine_c) ? weights[j] : 0;
 #pragma unroll
                     for (int o = 1; o < 4; o <<= 1) run += __shfl_xor_sync(0xffffffffu, run, o);
                     const u64 need = drawn();
-                    if (stay && h == 0 && run > need && run - mine_w <= need) a.token[n] = (int32_t)~(uint32_t)mine_c;
+                    if (stay && h == 0 && run > need && run - mine_w <= need) a.token[n] = ordered_index(mine_c);
                 }
             } else {
-                sort_down(list, all, tid);
-                // the sums of f(list[i]) up to each of the thread's elements 4 tid .. 4 tid + 3 of n
-                u64 w[4], cum[4];
-                auto scan = [&](int n_of, int shift) {
+                // Sorted, four elements to a thread, summed up in the order and once more in index order.
+                u64 c[4], w[4], cum[4];
+                auto sort = [&](int n_of) {
+                    int size = 2;
+                    while (size < n_of) size *= 2;
+                    sort_down(c, list, size);
+                };
+                // sums of f(c) up to each of the thread's elements
+                auto scan = [&](auto f) {
                     u64 run = 0;
-#pragma unroll 1
-                    for (int e = 0; e < 4; ++e) {
-                        const int i = 4 * tid + e;
-                        const u64 x = i < n_of ? weight(s, value_of((uint32_t)(list[i] >> shift))) : 0;
-                        run += x;
 #pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            if (y == e) {
-                                w[y] = x;
-                                cum[y] = run;
-                            }
+                    for (int e = 0; e < 4; ++e) {
+                        w[e] = f(c[e], 4 * tid + e);
+                        run += w[e];
+                        cum[e] = run;
                     }
                     const u64 own = run;
 #pragma unroll
@@ -687,43 +746,45 @@ sample_kernel(const Sampling a, const int32_t slice) {
                     }
                     __syncthreads();
                     if (lane == 31) part[warp] = run;
-                    __syncthreads();
-                    u64 all_of_it = 0, add = run - own;
-#pragma unroll
-                    for (int x = 0; x < kWarps; ++x) {
-                        add += x < warp ? part[x] : 0;
-                        all_of_it += part[x];
-                    }
+                    u64 all_of_it;
+                    const u64 add = parts_before(all_of_it) + run - own;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) cum[e] += add;
                     return all_of_it;
                 };
+                auto weight_of = [&](u64 x) { return weight(s, value_of(ordered_key(x))); };
+#pragma unroll
+                for (int e = 0; e < 4; ++e) c[e] = 4 * tid + e < all ? list[4 * tid + e] : 0;
+                __syncthreads();
+                sort(all);
                 const int first_k = min(k, all);
-                const u64 of_k = scan(first_k, 32), goal = p < 1.f ? share(of_k) : ~(u64)0;
+                const u64 of_k = scan([&](u64 x, int i) { return i < first_k ? weight_of(x) : 0; });
+                const u64 goal = p < 1.f ? share(of_k) : ~(u64)0;
                 int stay = 0;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     stay += 4 * tid + e < first_k && cum[e] - w[e] < goal && (4 * tid + e == 0 || w[e] >= w_least) ? 1 : 0;
                 stay = __reduce_add_sync(0xffffffffu, stay);
-                if (lane == 0) atomicAdd(&chosen_count, stay);
+                if (lane == 0 && stay != 0) atomicAdd(&chosen_count, stay);
                 __syncthreads();
                 stay = chosen_count;            // a beginning of the order
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (4 * tid + e == stay - 1) choose(list[stay - 1], cum[e]);
-                __syncthreads();
-                sum = found[0];
+                    if (4 * tid + e == stay - 1) choose(c[e], cum[e]);
                 if (a.token != nullptr) {
                     // in index order
-                    for (int i = tid; i < stay; i += kThreads) list[i] = list[i] << 32 | list[i] >> 32;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        c[e] = 4 * tid + e < stay ? c[e] << (64 - kIndexBits) | c[e] >> kIndexBits : 0;
                     __syncthreads();
-                    sort_down(list, stay, tid);
-                    scan(stay, 0);
+                    sum = chosen_sum;
+                    sort(stay);
+                    scan([&](u64 x, int i) { return i < stay ? weight(s, value_of((uint32_t)x)) : 0; });
                     const u64 need = drawn();
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (4 * tid + e < stay && cum[e] > need && cum[e] - w[e] <= need)
-                            a.token[n] = (int32_t)~(uint32_t)(list[4 * tid + e] >> 32);
+                            a.token[n] = (1 << kIndexBits) - 1 - (int)(c[e] >> (64 - kIndexBits));
                 }
             }
         }
@@ -731,7 +792,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
         if (done) {
             border_at = value_of(chosen_key);
             last = chosen_index;
-            sum = found[0];
+            sum = chosen_sum;
         }
     }
     if (!none && !done) {
