@@ -155,7 +155,6 @@ __device__ __forceinline__ PrefixRun<KEYS> prefix_run(const PrefixAttention &a, 
 template <bool EXP2> struct RowJoin {
     float prefix, own, lse;
     bool none;
-    RowJoin() = default;
     __device__ __forceinline__ RowJoin(float top, float sum, float own_top, float own_sum) {
         none = own_sum < 0.f;
         const float m = fmaxf(top, own_top), from = m == -INFINITY ? 0.f : m;
@@ -165,10 +164,6 @@ template <bool EXP2> struct RowJoin {
         prefix = none ? 0.f : x / z;
         own = none ? 0.f : y / z;
         lse = none ? -INFINITY : EXP2 ? (m + log2f(z)) * 0.6931471805599453f : m + logf(z);
-    }
-    __device__ __forceinline__ float2 operator()(float2 o, float2 own_o) const {
-        if (none) return make_float2(0.f, 0.f);
-        return make_float2(prefix * o.x + own * own_o.x, prefix * o.y + own * own_o.y);
     }
     __device__ __forceinline__ float4 operator()(float4 o, float4 own_o) const {
         if (none) return make_float4(0.f, 0.f, 0.f, 0.f);
