@@ -62,7 +62,7 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 // 16 bytes of logits as pairs.  clean: NaN becomes -infinity.
 template <typename Tin> struct Vec;
 template <> struct Vec<float> {
-    static constexpr int N = 4;
+    static constexpr int N = 4, GRAIN = 0;      // (low bits in which keys never differ)
     static __device__ __forceinline__ void unpack(uint4 u, float2 (&x)[2]) {
         x[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
         x[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
@@ -76,7 +76,7 @@ template <> struct Vec<float> {
     static __device__ __forceinline__ float load(const uint4 *p, int e) { return reinterpret_cast<const float *>(p)[e]; }
 };
 template <> struct Vec<__nv_bfloat16> {
-    static constexpr int N = 8;
+    static constexpr int N = 8, GRAIN = 16;
     static __device__ __forceinline__ void unpack(uint4 u, float2 (&x)[4]) {
         x[0] = tc::unpack_bf16x2(u.x);
         x[1] = tc::unpack_bf16x2(u.y);
@@ -226,10 +226,10 @@ sample_kernel(const Sampling a, const int32_t slice) {
     // two histograms (low words, then high words) and a list
     uint32_t *const hists = reinterpret_cast<uint32_t *>(smem + (size_t)slice * 16), *hist = hists;
     u64 *const list = reinterpret_cast<u64 *>(hists + 4 * kBins);
-    __shared__ u64 part[kWarps], part_all, chosen_sum, found[2];                          // found: what lies above the border's bin, what is in it
-    __shared__ u64 totals[2][kMaxRanks];
+    __shared__ u64 part[kWarps], part_all, chosen_sum, totals[2][kMaxRanks], more[kWarps], more_totals[kMaxRanks];
+    __shared__ u64 found[2];                    // what lies above the border's bin, what is in it
     __shared__ float tops[kMaxRanks], warp_top[kWarps];
-    __shared__ int32_t found_bin, chosen_index, count, pool, chosen_count;
+    __shared__ int32_t found_bin, chosen_index, count, chosen_count;
     __shared__ uint32_t chosen_key;
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
     cluster.barrier_arrive();
@@ -251,11 +251,6 @@ sample_kernel(const Sampling a, const int32_t slice) {
     float p = a.top_p != nullptr ? a.top_p[n] : 1.f;
     const float least = a.min_p != nullptr ? a.min_p[n] : 0.f;
     const float u = a.uniforms != nullptr ? a.uniforms[n] : 0.f;
-    if (!(T > 0.f)) {                           // the first of the order alone
-        T = 1.f;
-        k = 1;
-    }
-    if (k == 1) p = 1.f;
     if (tid == 0) count = 0;
 
     // ---- the row into shared memory, and its maximum
@@ -282,6 +277,11 @@ sample_kernel(const Sampling a, const int32_t slice) {
         data[v] = x;
         my_top = fmaxf(my_top, Vec<Tin>::largest(x));
     }
+    if (!(T > 0.f)) {                           // the first of the order alone
+        T = 1.f;
+        k = 1;
+    }
+    if (k == 1) p = 1.f;
     float top = my_top;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -344,10 +344,48 @@ sample_kernel(const Sampling a, const int32_t slice) {
             }
         }
     };
+    // The warp's elements of [from, to] that which(i, x) takes go to the list, in any order; `count` counts
+    // them all, the list holds the first kList.  One atomic for a warp's 32 vectors.
+    auto append = [&](uint32_t bits, int v) {
+        if (__any_sync(0xffffffffu, bits != 0) == 0) return;
+        const int n_of = __popc(bits);
+        int at = n_of;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int z = __shfl_up_sync(0xffffffffu, at, o);
+            if (lane >= o) at += z;
+        }
+        int start = 0;
+        if (lane == 31) start = atomicAdd(&count, at);
+        at += __shfl_sync(0xffffffffu, start, 31) - n_of;
+        for (; bits != 0; bits &= bits - 1, ++at) {
+            const int e = __ffs(bits) - 1;
+            if (at < kList) list[at] = ordered(key_of(Vec<Tin>::load(data + v, e)), index_of(v) + e);
+        }
+    };
+    auto collect = [&](float from, float to, auto which) {
+#pragma unroll 1
+        for (int v0 = w0; v0 < w1; v0 += 32) {
+            const int v = v0 + lane;
+            uint32_t bits = 0;
+            if (v < w1) {
+                const uint4 y = data[v];
+                if (Vec<Tin>::largest(y) >= from) {
+                    float2 x[VEC / 2];
+                    Vec<Tin>::unpack(y, x);
+#pragma unroll
+                    for (int e = 0; e < VEC / 2; ++e) {
+                        bits |= x[e].x >= from && x[e].x <= to && which(index_of(v) + 2 * e, x[e].x) ? 1u << (2 * e) : 0u;
+                        bits |= x[e].y >= from && x[e].y <= to && which(index_of(v) + 2 * e + 1, x[e].y) ? 2u << (2 * e) : 0u;
+                    }
+                }
+            }
+            append(bits, v);
+        }
+    };
     // The weights of the thread's elements that are at least `from` and of which which(i, x, hi, lo) holds (hi, lo:
-    // the weight's digits), added up; also(x, hi, lo) sees vectors with their digits, zeros where it does not
-    // hold.  No branches, so that a vector's weights are formed side by side.
-    auto weigh = [&](float from, auto which, auto also) {
+    // the weight's digits), added up.  No branches, so that a vector's weights are formed side by side.
+    auto weigh = [&](float from, auto which) {
         from = fmaxf(from, s.least);
         uint32_t hi = 0, lo = 0;                // (digits of 21 bits: no thread has 2,048 elements)
 #pragma unroll 1
@@ -357,7 +395,6 @@ sample_kernel(const Sampling a, const int32_t slice) {
             float2 x[VEC / 2];
             Vec<Tin>::unpack(y, x);
             const int i = index_of(v);
-            uint32_t h[VEC], l[VEC];
 #pragma unroll
             for (int e = 0; e < VEC / 2; ++e) {
                 float2 high, low;
@@ -365,19 +402,51 @@ sample_kernel(const Sampling a, const int32_t slice) {
                 const uint32_t h0 = digit(high.x), h1 = digit(high.y), l0 = digit(low.x), l1 = digit(low.y);
                 const bool on0 = (x[e].x >= from) & which(i + 2 * e, x[e].x, h0, l0);
                 const bool on1 = (x[e].y >= from) & which(i + 2 * e + 1, x[e].y, h1, l1);
-                h[2 * e] = on0 ? h0 : 0;
-                h[2 * e + 1] = on1 ? h1 : 0;
-                l[2 * e] = on0 ? l0 : 0;
-                l[2 * e + 1] = on1 ? l1 : 0;
+                hi += (on0 ? h0 : 0) + (on1 ? h1 : 0);
+                lo += (on0 ? l0 : 0) + (on1 ? l1 : 0);
             }
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                hi += h[e];
-                lo += l[e];
-            }
-            also(x, h, l);
         }
         return ((u64)hi << 21) + lo;
+    };
+    // All weights added up, those above `to` as well, and the elements of [from, to] to the list.
+    auto weigh_and_collect = [&](float from, float to, u64 &all, u64 &above) {
+        uint32_t hi = 0, lo = 0, hi_above = 0, lo_above = 0;
+#pragma unroll 1
+        for (int v0 = w0; v0 < w1; v0 += 32) {
+            const int v = v0 + lane;
+            uint32_t bits = 0;
+            uint4 y;
+            if (v < w1) y = data[v];
+            if (v < w1 && Vec<Tin>::largest(y) >= fminf(from, s.least)) {
+                float2 x[VEC / 2];
+                Vec<Tin>::unpack(y, x);
+#pragma unroll
+                for (int e = 0; e < VEC / 2; ++e) {
+                    float2 w = weights2(s, x[e]), high, low;
+                    w.x = x[e].x >= s.least ? w.x : 0.f;
+                    w.y = x[e].y >= s.least ? w.y : 0.f;
+                    digits42(w, high, low);
+                    const uint32_t h0 = digit(high.x), h1 = digit(high.y), l0 = digit(low.x), l1 = digit(low.y);
+                    hi += h0 + h1;
+                    lo += l0 + l1;
+                    if (x[e].x > to) {
+                        hi_above += h0;
+                        lo_above += l0;
+                    } else if (x[e].x >= from) {
+                        bits |= 1u << (2 * e);
+                    }
+                    if (x[e].y > to) {
+                        hi_above += h1;
+                        lo_above += l1;
+                    } else if (x[e].y >= from) {
+                        bits |= 2u << (2 * e);
+                    }
+                }
+            }
+            append(bits, v);
+        }
+        all = ((u64)hi << 21) + lo;
+        above = ((u64)hi_above << 21) + lo_above;
     };
 
     // Sums over all warps of all CTAs: every thread gets the total, what the warps before its own have,
@@ -419,6 +488,40 @@ sample_kernel(const Sampling a, const int32_t slice) {
         turn ^= 1;
         return all;
     };
+    // Two totals over the cluster.
+    auto cluster_totals = [&](u64 &x, u64 &y) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            x += __shfl_xor_sync(0xffffffffu, x, o);
+            y += __shfl_xor_sync(0xffffffffu, y, o);
+        }
+        __syncthreads();
+        if (lane == 0) {
+            part[warp] = x;
+            more[warp] = y;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            x = lane < kWarps ? part[lane] : 0;
+            y = lane < kWarps ? more[lane] : 0;
+#pragma unroll
+            for (int o = kWarps / 2; o > 0; o >>= 1) {
+                x += __shfl_xor_sync(0xffffffffu, x, o);
+                y += __shfl_xor_sync(0xffffffffu, y, o);
+            }
+            if (lane < ranks) {                 // (the lower half's sums: ranks <= kWarps)
+                *cluster.map_shared_rank(&totals[turn][rank], lane) = x;
+                *cluster.map_shared_rank(&more_totals[rank], lane) = y;
+            }
+        }
+        cluster.sync();
+        x = y = 0;
+        for (int r = 0; r < ranks; ++r) {
+            x += totals[turn][r];
+            y += more_totals[r];
+        }
+        turn ^= 1;
+    };
     // Two histograms in turn: when all have come together over one, the last one has been read.
     auto next_histogram = [&]() {
         hist = hist == hists ? hists + 2 * kBins : hists;
@@ -438,7 +541,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
     };
     // The first bin at which the bins, added up in order, reach want(total); `above` lies above the first
     // one.  Every CTA does it for itself.  Returns whether they do.
-    auto border = [&](u64 x, u64 above, auto want) {
+    auto border = [&](u64 x, u64 above, auto want, u64 *up_to = nullptr) {
         u64 run = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -451,6 +554,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
         run += parts_before(total) + above;
         total += above;
         const u64 goal = want(total);
+        if (up_to != nullptr) *up_to = run;
         if (run >= goal && run - x < goal) {
             found_bin = tid;
             found[0] = run - x;
@@ -486,58 +590,99 @@ sample_kernel(const Sampling a, const int32_t slice) {
         return fminf(s.m, x + 4e-7f * (fabsf(s.m) + fabsf(x)) + 1e-37f);
     };
 
+    // Where top-p's border is, to a bin or two of log2 w: a value above all candidates and one below.  A bin's
+    // weights lie within 2^(1/12) of each other, so it adds them up relative to its own upper end, to 2^-16
+    // in 32 bits (a CTA has fewer than 2^16 elements).  The estimates are off by less than 2^-14 of the sum and 2^18
+    // units of 2^-42, which `slack` covers on either side.
+    auto candidates = [&](float &from, float &to) {
+        next_histogram();
+#pragma unroll 1
+        for (int v = w0 + lane; v < w1; v += 32) {
+            const uint4 y = data[v];
+            if (Vec<Tin>::largest(y) < s.least) continue;
+            float2 x[VEC / 2];
+            Vec<Tin>::unpack(y, x);
+#pragma unroll
+            for (int e = 0; e < VEC / 2; ++e) {
+                auto both = [](float z) { return make_float2(z, z); };
+                const float2 d = tc::f2sub(both(s.m), x[e]), b = fma_cut2(d, both(by), both(8388608.f));
+                const uint32_t b0 = min(__float_as_uint(b.x), kBias + kBins - 1), b1 = min(__float_as_uint(b.y), kBias + kBins - 1);
+                // (the bins' upper ends, negated)
+                const float2 ends = tc::f2sub(both(8388608.f), make_float2(__uint_as_float(b0), __uint_as_float(b1)));
+                float2 w = tc::f2fma(tc::f2fma(d, both(by), ends), both(-1.f / kPerOctave), both(16.f));
+                w.x = tc::ex2(w.x);
+                w.y = tc::ex2(w.y);
+                w = fma_cut2(w, both(1.f), both(8388608.f));
+                if (digit(w.x) != 0) atomicAdd(&hist[b0 - kBias], digit(w.x));
+                if (digit(w.y) != 0) atomicAdd(&hist[b1 - kBias], digit(w.y));
+            }
+        }
+        cluster.sync();
+        const u64 mine_w = __float2ull_rz((float)bin_sum(0) * exp2f(26.f - (float)tid / kPerOctave));
+        u64 slack = 0, run = 0, goal = 0;
+        border(mine_w, 0, [&](u64 total) {
+            slack = (total >> 12) + (1 << 20);
+            goal = share(total);
+            return goal > slack ? goal - slack : (u64)1;
+        }, &run);
+        const int first_bin = found_bin;
+        __syncthreads();
+        if (tid == 0) found_bin = kBins - 1;
+        __syncthreads();
+        if (run >= goal + slack && run - mine_w < goal + slack) found_bin = tid;
+        __syncthreads();
+        to = above_bin(first_bin);
+        from = below_bin(found_bin);
+    };
+
     // Narrows the border down to the first elements of the order that reach a count (k) or a share of
-    // the weight: first by bins of log2 w, then by the values' bits.
+    // the weight: first by bins of log2 w, then by the values' bits.  ahead_w: of top-p's weights, what the
+    // thread has above the candidates.
+    u64 ahead_w = 0;
+    int pooled = 0;
     auto narrow = [&](bool by_weight) {
-        u64 want = (u64)k, above, before, here;
+        u64 want = (u64)k, above = 0, before, here;
+        int bin = -1;
+        uint32_t most, lowest;
         auto goal = [&](u64 total) {
             if (by_weight) want = share(total);
             return want;
         };
-        next_histogram();
-        if (!by_weight) {
-            each_in(lowest_value(), s.m, [&](int i, float x) { if (stays(i, x)) atomicAdd(&hist[bin_of(x)], 1u); });
-        } else if (border_at == -INFINITY) {
-            weigh(lowest_value(), [](int, float, uint32_t, uint32_t) { return true; },
-                  [&](const float2 (&x)[VEC / 2], const uint32_t (&hi)[VEC], const uint32_t (&lo)[VEC]) {
-                // (all low words on their way before the first one is waited for)
-                uint32_t old[VEC];
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    old[e] = 0;
-                    const int b = bin_of(e & 1 ? x[e / 2].y : x[e / 2].x);
-                    if ((hi[e] | lo[e]) != 0) old[e] = atomicAdd(&hist[b], (hi[e] << 21) + lo[e]);
-                }
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const uint32_t high = (hi[e] >> 11) + (old[e] + ((hi[e] << 21) + lo[e]) < old[e] ? 1u : 0u);
-                    if (high != 0) atomicAdd(&hist[kBins + bin_of(e & 1 ? x[e / 2].y : x[e / 2].x)], high);
-                }
-            });
+        auto in_bin = [&](int i, float x) { return stays(i, x) && (bin < 0 || bin_of(x) == bin); };
+        if (tid == 0) count = 0;
+        if (by_weight && border_at == -INFINITY) {
+            float from, to;
+            candidates(from, to);
+            u64 total;
+            weigh_and_collect(from, to, total, ahead_w);
+            above = ahead_w;
+            cluster_totals(total, above);
+            goal(total);
+            most = key_of(to);
+            lowest = key_of(from);
         } else {
+            next_histogram();
             each_in(lowest_value(), s.m, [&](int i, float x) {
-                const u64 w = stays(i, x) ? weight(s, x) : 0;
-                if (w != 0) add_weight(bin_of(x), (uint32_t)(w >> 21), (uint32_t)w & 0x1fffffu);
+                if (!stays(i, x)) return;
+                if (by_weight) {
+                    const u64 w = weight(s, x);
+                    if (w != 0) add_weight(bin_of(x), (uint32_t)(w >> 21), (uint32_t)w & 0x1fffffu);
+                } else {
+                    atomicAdd(&hist[bin_of(x)], 1u);
+                }
             });
+            cluster.sync();
+            if (!border(by_weight ? bin_sum(0) + (bin_sum(1) << 32) : bin_sum(0), 0, goal)) return;  // fewer: all stay
+            bin = found_bin;
+            above = found[0];
+            most = key_of(above_bin(bin));
+            lowest = key_of(below_bin(bin));
+            collect(value_of(lowest), value_of(most), in_bin);
         }
-        cluster.sync();
-        if (!border(by_weight ? bin_sum(0) + (bin_sum(1) << 32) : bin_sum(0), 0, goal)) return;  // fewer: all stay
-        const int bin = found_bin;
-        above = found[0];
-        uint32_t most = key_of(above_bin(bin)), lowest = key_of(below_bin(bin));
-        auto in_bin = [&](int i, float x) { return stays(i, x) && bin_of(x) == bin; };
-        // the bin's elements, where the list has room for the CTA's
-        if (tid == 0) pool = 0;
         __syncthreads();
-        each_in(value_of(lowest), value_of(most), [&](int i, float x) {
-            if (!in_bin(i, x)) return;
-            const int at = atomicAdd(&pool, 1);
-            if (at < kList) list[at] = ordered(key_of(x), i);
-        });
-        __syncthreads();
-        const int pooled = pool;
+        pooled = count;
         for (;;) {
-            const int shift = max(0, 23 - __clz(most - lowest));        // 2^9 bins at most
+            const int shift = max(Vec<Tin>::GRAIN, 23 - __clz(most - lowest));      // 2^9 bins at most
             next_histogram();
             auto add = [&](uint32_t key) {
                 const int b = (int)((most - key) >> shift);
@@ -557,12 +702,17 @@ sample_kernel(const Sampling a, const int32_t slice) {
                 each_in(value_of(lowest), value_of(most), [&](int i, float x) { if (in_bin(i, x)) add(key_of(x)); });
             }
             cluster.sync();
-            // (the bin's values lie in that range, so they reach it)
+            // (the candidates' values lie in that range, so they reach it)
             if (!border(by_weight ? bin_sum(0) + (bin_sum(1) << 32) : bin_sum(0), above, [&](u64) { return want; })) return;
             above = found[0];
             most -= (uint32_t)found_bin << shift;
-            if (shift == 0) break;
+            if (shift == Vec<Tin>::GRAIN) break;
             lowest = max(lowest, most - ((1u << shift) - 1));
+        }
+        if (Vec<Tin>::GRAIN > 0) {
+            // the one key in (most - 2^GRAIN, most]: negative values' keys end in ones
+            const uint32_t ones = (1u << Vec<Tin>::GRAIN) - 1;
+            most = (most >> 31) != 0 ? most & ~ones : ((most + 1) & ~ones) - 1;
         }
         // the values equal to the border's: the first of them by their index
         const float it = value_of(most);
@@ -576,20 +726,26 @@ sample_kernel(const Sampling a, const int32_t slice) {
             } else {
                 each_in(it, it, [&](int i, float x) { equal += stays(i, x) ? 1 : 0; });
             }
+            if (tid == 0) chosen_count = 0;
             const u64 all = cluster_sum(equal, before, here);
             if (keep < all) {
                 auto publish = [&](int at) {
                     for (int r = 0; r < ranks; ++r) *cluster.map_shared_rank(&chosen_index, r) = at;
                 };
                 if (in_pool) {
-                    // the CTA's equal ones in any order: the one with as many smaller indices as are wanted
+                    // the CTA's equal ones in any order (in the histograms' place, which all have read): the one
+                    // with as many smaller indices as are wanted
+                    int32_t *const equals = reinterpret_cast<int32_t *>(hists);
                     const u64 ahead = before - part[warp];      // of the CTAs before
-                    for (int i = tid; i < pooled; i += kThreads) {
-                        const u64 c = list[i];
-                        if (ordered_key(c) != most) continue;
-                        u64 smaller = ahead;            // (equal ones of a smaller index stand higher in the order)
-                        for (int j = 0; j < pooled; ++j) smaller += ordered_key(list[j]) == most && list[j] > c ? 1 : 0;
-                        if (smaller + 1 == keep) publish(ordered_index(c));
+                    for (int i = tid; i < pooled; i += kThreads)
+                        if (ordered_key(list[i]) == most) equals[atomicAdd(&chosen_count, 1)] = ordered_index(list[i]);
+                    __syncthreads();
+                    const int of_them = chosen_count;
+                    for (int i = tid; i < of_them; i += kThreads) {
+                        const int at = equals[i];
+                        u64 smaller = ahead;
+                        for (int j = 0; j < of_them; ++j) smaller += equals[j] < at ? 1 : 0;
+                        if (smaller + 1 == keep) publish(at);
                     }
                 } else if (keep > before && keep <= before + here) {
                     // this warp has the last one
@@ -641,11 +797,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
         if (my_top != -INFINITY) atomicAdd(&hist[bin_of(my_top)], 1u);
         cluster.sync();
         const float from = border(bin_sum(0), 0, [&](u64) { return (u64)k; }) ? below_bin(found_bin) : -3.402823466e38f;
-        each_in(from, s.m, [&](int i, float x) {
-            const int at = atomicAdd(&count, 1);
-            if (at >= kList) return;
-            list[at] = ordered(key_of(x), i);
-        });
+        collect(from, s.m, [](int, float) { return true; });
         cluster.sync();
         // the lists' lengths, a rank to a lane; warp r brings rank r's to the first CTA
         const int length = lane < ranks ? *cluster.map_shared_rank(&count, lane) : 0;
@@ -722,13 +874,8 @@ sample_kernel(const Sampling a, const int32_t slice) {
                     if (stay && h == 0 && run > need && run - mine_w <= need) a.token[n] = ordered_index(mine_c);
                 }
             } else {
-                // Sorted, four elements to a thread, summed up in the order and once more in index order.
+                // Sorted, four elements to a thread, and summed up in the order.
                 u64 c[4], w[4], cum[4];
-                auto sort = [&](int n_of) {
-                    int size = 2;
-                    while (size < n_of) size *= 2;
-                    sort_down(c, list, size);
-                };
                 // sums of f(c) up to each of the thread's elements
                 auto scan = [&](auto f) {
                     u64 run = 0;
@@ -756,7 +903,9 @@ sample_kernel(const Sampling a, const int32_t slice) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) c[e] = 4 * tid + e < all ? list[4 * tid + e] : 0;
                 __syncthreads();
-                sort(all);
+                int size = 2;
+                while (size < all) size *= 2;
+                sort_down(c, list, size);
                 const int first_k = min(k, all);
                 const u64 of_k = scan([&](u64 x, int i) { return i < first_k ? weight_of(x) : 0; });
                 const u64 goal = p < 1.f ? share(of_k) : ~(u64)0;
@@ -772,19 +921,29 @@ sample_kernel(const Sampling a, const int32_t slice) {
                 for (int e = 0; e < 4; ++e)
                     if (4 * tid + e == stay - 1) choose(c[e], cum[e]);
                 if (a.token != nullptr) {
-                    // in index order
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        c[e] = 4 * tid + e < stay ? c[e] << (64 - kIndexBits) | c[e] >> kIndexBits : 0;
+                    // in index order: by the index's upper half, then by its lower half
                     __syncthreads();
                     sum = chosen_sum;
-                    sort(stay);
-                    scan([&](u64 x, int i) { return i < stay ? weight(s, value_of((uint32_t)x)) : 0; });
                     const u64 need = drawn();
+                    u64 ahead = 0;
+                    int upper = -1;
+                    for (int level = 0; level < 2; ++level) {
+                        next_histogram();
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (4 * tid + e < stay && cum[e] > need && cum[e] - w[e] <= need)
-                            a.token[n] = (1 << kIndexBits) - 1 - (int)(c[e] >> (64 - kIndexBits));
+                        for (int e = 0; e < 4; ++e) {
+                            const int i = ordered_index(c[e]);
+                            if (4 * tid + e < stay && (level == 0 || i / kBins == upper))
+                                add_weight(level == 0 ? i / kBins : i % kBins, (uint32_t)(w[e] >> 21),
+                                           (uint32_t)w[e] & 0x1fffffu);
+                        }
+                        __syncthreads();
+                        border(hist[tid] + ((u64)hist[kBins + tid] << 32), ahead, [&](u64) { return need + 1; });
+                        if (level == 0) {
+                            upper = found_bin;
+                            ahead = found[0];
+                        }
+                    }
+                    if (tid == 0) a.token[n] = upper * kBins + found_bin;
                 }
             }
         }
@@ -804,7 +963,24 @@ sample_kernel(const Sampling a, const int32_t slice) {
         auto counts = [&](int i, float x, uint32_t hi, uint32_t lo) {
             return stays(i, x) & ((hi > least_hi) | ((hi == least_hi) & (lo >= least_lo)));
         };
-        sum = cluster_sum(weigh(lowest_value(), counts, [](auto &, auto &, auto &) {}), before, here);
+        u64 mine_w;
+        if (border_at > -INFINITY && pooled <= kList && w_least == 0 && !(k > 0 && k < V)) {
+            // what lies above the candidates was summed up with them; of these, what stays, to the warps that have it
+            if (tid < kWarps) more[tid] = 0;
+            __syncthreads();
+            for (int i = tid; i < pooled; i += kThreads) {
+                const int at = ordered_index(list[i]);
+                const float x = value_of(ordered_key(list[i]));
+                if (stays(at, x)) atomicAdd(&more[((at + lead) / VEC - first) / per_warp], weight(s, x));
+            }
+            __syncthreads();
+            mine_w = ahead_w + (lane == 0 ? more[warp] : 0);
+        } else {
+            // (with min-p's weight in mind, as a value with room for roundings)
+            const float from = w_least > 0 ? s.m + (log2f(fminf(least, 1.f)) * (1.f + 1e-5f) - 1e-6f) / s.c : -INFINITY;
+            mine_w = weigh(fmaxf(lowest_value(), from - 4e-7f * (fabsf(s.m) + fabsf(from)) - 1e-37f), counts);
+        }
+        sum = cluster_sum(mine_w, before, here);
         const u64 need = drawn();
         if (a.token != nullptr && before <= need && before + here > need) {
             for (int v0 = w0; v0 < w1; v0 += 32) {
