@@ -23,6 +23,8 @@
 
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 namespace kda {
 namespace {
 
@@ -30,13 +32,16 @@ typedef unsigned long long u64;
 constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxRanks = 8;
 constexpr int kBins = 512;                      // of a histogram
 constexpr float kPerOctave = 12.f;              // bins for a halving of w
-constexpr int kList = 2048, kListK = 1024;      // logits that go to one CTA at most, and the k for which that is tried
+constexpr int kGroups = 4;                      // a thread's logits, by which its largest ones are taken
+constexpr int kList = 4096;                     // a CTA's candidates for the border
+constexpr int kSorted = 4 * kThreads, kListK = 1024;    // logits that one CTA sorts, and the k for which that is tried
 constexpr int kFew = 128;                       // logits of which every pair is compared instead
 constexpr int32_t kAll = 0x7fffffff;
-// two histograms and a list; a row of 2^18 logits over eight CTAs beside them
-constexpr int kScratch = 4 * kBins * 4 + kList * 8;
-constexpr int kMaxSmem = KDA_MAX_VOCABULARY / kMaxRanks * 4 + 32 + kScratch;
-static_assert(kList == 4 * kThreads && 4 * kFew == kThreads && 2 * kFew <= kList, "threads to the elements of a list");
+// histograms (two of kBins 64-bit sums in turn, or copies of one of kFine sums) and a list
+constexpr int kFine = 4 * kBins, kCopies = 4;   // of the first histogram of top-p
+constexpr int kSmem = kCopies * kFine * 4 + kList * 8;
+static_assert(4 * kFew == kThreads && 2 * kFew <= kList && kSorted <= kList, "threads to the elements of a list");
+static_assert(kListK <= kGroups * kThreads / 2, "largest ones enough to bound the k-th");
 static_assert(kBins == kThreads, "a thread per bin");
 
 struct Sampling {
@@ -67,13 +72,18 @@ template <> struct Vec<float> {
         x[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
         x[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
     }
+    static __device__ __forceinline__ uint4 nothing() {
+        return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+    }
+    static __device__ __forceinline__ float pick(uint4 u, int e) {
+        return __uint_as_float(e < 2 ? (e == 0 ? u.x : u.y) : e == 2 ? u.z : u.w);
+    }
     static __device__ __forceinline__ uint32_t clean(uint32_t w) {
         return __float_as_uint(fmaxf(__uint_as_float(w), -INFINITY));
     }
     static __device__ __forceinline__ float largest(uint4 u) {
         return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
     }
-    static __device__ __forceinline__ float load(const uint4 *p, int e) { return reinterpret_cast<const float *>(p)[e]; }
 };
 template <> struct Vec<__nv_bfloat16> {
     static constexpr int N = 8, GRAIN = 16;
@@ -88,13 +98,17 @@ template <> struct Vec<__nv_bfloat16> {
         asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));       // (a number beside a NaN)
         return d;
     }
+    static __device__ __forceinline__ uint4 nothing() {
+        return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+    }
+    static __device__ __forceinline__ float pick(uint4 u, int e) {
+        const uint32_t w = e < 4 ? (e < 2 ? u.x : u.y) : e < 6 ? u.z : u.w;
+        return __uint_as_float((e & 1) != 0 ? w & 0xffff0000u : w << 16);
+    }
     static __device__ __forceinline__ uint32_t clean(uint32_t w) { return max2(w, 0xff80ff80u); }
     static __device__ __forceinline__ float largest(uint4 u) {
         const uint32_t m = max2(max2(u.x, u.y), max2(u.z, u.w));
         return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
-    }
-    static __device__ __forceinline__ float load(const uint4 *p, int e) {
-        return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[e]);
     }
 };
 
@@ -222,14 +236,13 @@ __global__ void __launch_bounds__(kThreads, 2)
 sample_kernel(const Sampling a, const int32_t slice) {
     constexpr int VEC = Vec<Tin>::N;
     extern __shared__ __align__(16) unsigned char smem[];
-    uint4 *const data = reinterpret_cast<uint4 *>(smem);            // the CTA's vectors of the row
     // two histograms (low words, then high words) and a list
-    uint32_t *const hists = reinterpret_cast<uint32_t *>(smem + (size_t)slice * 16), *hist = hists;
-    u64 *const list = reinterpret_cast<u64 *>(hists + 4 * kBins);
+    uint32_t *const hists = reinterpret_cast<uint32_t *>(smem), *hist = hists;
+    u64 *const list = reinterpret_cast<u64 *>(hists + kCopies * kFine);
     __shared__ u64 part[kWarps], part_all, chosen_sum, totals[2][kMaxRanks], more[kWarps], more_totals[kMaxRanks];
     __shared__ u64 found[2];                    // what lies above the border's bin, what is in it
     __shared__ float tops[kMaxRanks], warp_top[kWarps];
-    __shared__ int32_t found_bin, chosen_index, count, chosen_count;
+    __shared__ int32_t found_bin, found_last, chosen_index, count, chosen_count;
     __shared__ uint32_t chosen_key;
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
     cluster.barrier_arrive();
@@ -253,15 +266,15 @@ sample_kernel(const Sampling a, const int32_t slice) {
     const float u = a.uniforms != nullptr ? a.uniforms[n] : 0.f;
     if (tid == 0) count = 0;
 
-    // ---- the row into shared memory, and its maximum
-    float my_top = -INFINITY;
-#pragma unroll 4
-    for (int v = w0 + lane; v < w1; v += 32) {
-        const int e0 = index_of(v);
-        uint4 x;
-        if (e0 >= 0 && e0 + VEC <= V) {
-            x = __ldg(grid + v);
-        } else {                                // the row's ends
+    // A vector of the row as it is (all -infinity from `end` on), and what it counts as: the row is read as often
+    // as it is needed, from the L2 or the L1.
+    bool infinite = false;                      // the infinite ones share everything
+    const int whole0 = first == 0 && lead > 0 ? 1 : 0, whole1 = min(mine, (V + lead) / VEC - first);
+    auto raw = [&](int v, int end) {
+        if (v >= whole0 && v < min(end, whole1)) return __ldg(grid + v);
+        uint4 x = Vec<Tin>::nothing();
+        if (v < end) {                          // the row's ends
+            const int e0 = index_of(v);
             Tin y[VEC];
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
@@ -270,19 +283,71 @@ sample_kernel(const Sampling a, const int32_t slice) {
             }
             memcpy(&x, y, 16);
         }
+        return x;
+    };
+    auto clean = [&](uint4 x) {
         x.x = Vec<Tin>::clean(x.x);
         x.y = Vec<Tin>::clean(x.y);
         x.z = Vec<Tin>::clean(x.z);
         x.w = Vec<Tin>::clean(x.w);
-        data[v] = x;
-        my_top = fmaxf(my_top, Vec<Tin>::largest(x));
+        if (infinite) {
+            Tin y[VEC];
+            memcpy(y, &x, 16);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) y[e] = static_cast<Tin>(static_cast<float>(y[e]) == INFINITY ? 0.f : -INFINITY);
+            memcpy(&x, y, 16);
+        }
+        return x;
+    };
+    // f(v, y) for the vectors a .. b - 1, a warp's, 32 at a time in order, all lanes together; the next ones
+    // are on their way meanwhile.
+    auto each_vector = [&](int a_, int b_, auto f) {
+        uint4 next = raw(a_ + lane, b_);
+#pragma unroll 1
+        for (int v0 = a_; v0 < b_; v0 += 32) {
+            const uint4 y = next;
+            next = raw(v0 + 32 + lane, b_);
+            f(v0 + lane, clean(y));
+        }
+    };
+    // The same where few reach `from`: four of a lane's on their way, those that do not are passed by.
+    auto each_above = [&](int a_, int b_, float from, auto f) {
+#pragma unroll 1
+        for (int v0 = a_; v0 < b_; v0 += 128) {
+            uint4 y[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) y[g] = raw(v0 + 32 * g + lane, b_);
+#pragma unroll 1
+            for (int g = 0; g < 4; ++g) {
+                const uint4 z = clean(y[0]);
+                y[0] = y[1];
+                y[1] = y[2];
+                y[2] = y[3];
+                if (Vec<Tin>::largest(z) >= from) f(v0 + 32 * g + lane, z);
+            }
+        }
+    };
+
+    // ---- the maximum, and the largest of each thread's groups
+    float my_top[kGroups];
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) my_top[g] = -INFINITY;
+#pragma unroll 1
+    for (int v = w0 + lane; v < w1; v += 32 * kGroups) {
+        uint4 x[kGroups];
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) x[g] = raw(v + 32 * g, w1);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) my_top[g] = fmaxf(my_top[g], Vec<Tin>::largest(clean(x[g])));
     }
     if (!(T > 0.f)) {                           // the first of the order alone
         T = 1.f;
         k = 1;
     }
     if (k == 1) p = 1.f;
-    float top = my_top;
+    float top = my_top[0];
+#pragma unroll
+    for (int g = 1; g < kGroups; ++g) top = fmaxf(top, my_top[g]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) warp_top[warp] = top;
@@ -298,22 +363,17 @@ sample_kernel(const Sampling a, const int32_t slice) {
     top = -INFINITY;
     for (int r = 0; r < ranks; ++r) top = fmaxf(top, tops[r]);
     const bool none = top == -INFINITY;
-    if (top == INFINITY) {                      // the infinite ones share everything
-        for (int v = w0 + lane; v < w1; v += 32) {
-            Tin y[VEC];
-            memcpy(y, &data[v], 16);
+    if (top == INFINITY) {
+        infinite = true;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) y[e] = static_cast<Tin>(static_cast<float>(y[e]) == INFINITY ? 0.f : -INFINITY);
-            memcpy(&data[v], y, 16);
-        }
-        my_top = my_top == INFINITY ? 0.f : -INFINITY;
+        for (int g = 0; g < kGroups; ++g) my_top[g] = my_top[g] == INFINITY ? 0.f : -INFINITY;
         top = 0.f;
     }
     // log2(e) / T as a number and what is left of it, within a range where nothing overflows
     Scale s;
     s.m = top;
-    s.c = fminf(fmaxf(1.44269502f / T, 1e-36f), 1e37f);
-    s.cl = s.c < 1e37f && s.c > 1e-36f ? (fmaf(-s.c, T, 1.44269502f) + 1.92596303e-8f) / T : 0.f;
+    s.c = fminf(fmaxf(1.44269502f / T, 1e-36f), 5e36f);
+    s.cl = s.c < 5e36f && s.c > 1e-36f ? (fmaf(-s.c, T, 1.44269502f) + 1.92596303e-8f) / T : 0.f;
     if (!(fabsf(s.cl) < 1e30f)) s.cl = 0.f;
     s.least = fmaxf(s.m - 44.f / s.c, -3.402823466e38f);
     // bins of equal width in log2 w; the last one takes everything below
@@ -323,32 +383,31 @@ sample_kernel(const Sampling a, const int32_t slice) {
         return (int)min(__float_as_uint(__fmaf_rz(s.m - x, by, 8388608.f)) - kBias, (uint32_t)(kBins - 1));
     };
 
-    // Runs f(i, x) over the elements of the warp that lie in [from, to], few of them (one comparison each lets
-    // all others pass by).
-    auto each_in = [&](float from, float to, auto f) {
-#pragma unroll 1
-        for (int v = w0 + lane; v < w1; v += 32) {
-            const uint4 y = data[v];
-            if (Vec<Tin>::largest(y) < from) continue;
-            float2 x[VEC / 2];
-            Vec<Tin>::unpack(y, x);
-            uint32_t bits = 0;
+    // which of a vector's elements lie in [from, to], few of them
+    auto in_range = [&](const uint4 &y, float from, float to) {
+        float2 x[VEC / 2];
+        Vec<Tin>::unpack(y, x);
+        uint32_t bits = 0;
 #pragma unroll
-            for (int e = 0; e < VEC / 2; ++e) {
-                bits |= x[e].x >= from && x[e].x <= to ? 1u << (2 * e) : 0u;
-                bits |= x[e].y >= from && x[e].y <= to ? 2u << (2 * e) : 0u;
-            }
-            for (; bits != 0; bits &= bits - 1) {
-                const int e = __ffs(bits) - 1;
-                f(index_of(v) + e, Vec<Tin>::load(data + v, e));
-            }
+        for (int e = 0; e < VEC / 2; ++e) {
+            bits |= x[e].x >= from && x[e].x <= to ? 1u << (2 * e) : 0u;
+            bits |= x[e].y >= from && x[e].y <= to ? 2u << (2 * e) : 0u;
         }
+        return bits;
     };
-    // The warp's elements of [from, to] that which(i, x) takes go to the list, in any order; `count` counts
-    // them all, the list holds the first kList.  One atomic for a warp's 32 vectors.
-    auto append = [&](uint32_t bits, int v) {
-        if (__any_sync(0xffffffffu, bits != 0) == 0) return;
-        const int n_of = __popc(bits);
+    // f(i, x) over the warp's elements in [from, to]
+    auto each_in = [&](float from, float to, auto f) {
+        each_above(w0, w1, from, [&](int v, const uint4 &y) {
+            for (uint32_t bits = in_range(y, from, to); bits != 0; bits &= bits - 1) {
+                const int e = __ffs(bits) - 1;
+                f(index_of(v) + e, Vec<Tin>::pick(y, e));
+            }
+        });
+    };
+    // A place in the list for each lane's n_of elements, in any order; `count` counts them all, the list holds
+    // the first kList.  One atomic for the warp, none where it has no elements.
+    auto places = [&](int n_of) {
+        if (!__any_sync(0xffffffffu, n_of != 0)) return 0;
         int at = n_of;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -357,94 +416,123 @@ sample_kernel(const Sampling a, const int32_t slice) {
         }
         int start = 0;
         if (lane == 31) start = atomicAdd(&count, at);
-        at += __shfl_sync(0xffffffffu, start, 31) - n_of;
-        for (; bits != 0; bits &= bits - 1, ++at) {
-            const int e = __ffs(bits) - 1;
-            if (at < kList) list[at] = ordered(key_of(Vec<Tin>::load(data + v, e)), index_of(v) + e);
-        }
+        return at + __shfl_sync(0xffffffffu, start, 31) - n_of;
     };
+    auto enlist = [&](int at, float x, int i) {
+        if (at < kList) list[at] = ordered(key_of(x), i);
+    };
+    // The warp's elements in [from, to] of which which(i, x) holds, to the list; four vectors of a lane at a time.
     auto collect = [&](float from, float to, auto which) {
 #pragma unroll 1
-        for (int v0 = w0; v0 < w1; v0 += 32) {
-            const int v = v0 + lane;
-            uint32_t bits = 0;
-            if (v < w1) {
-                const uint4 y = data[v];
-                if (Vec<Tin>::largest(y) >= from) {
-                    float2 x[VEC / 2];
-                    Vec<Tin>::unpack(y, x);
+        for (int v0 = w0; v0 < w1; v0 += 128) {
+            uint4 y[4];
+            uint32_t bits = 0;                  // VEC of each
 #pragma unroll
-                    for (int e = 0; e < VEC / 2; ++e) {
-                        bits |= x[e].x >= from && x[e].x <= to && which(index_of(v) + 2 * e, x[e].x) ? 1u << (2 * e) : 0u;
-                        bits |= x[e].y >= from && x[e].y <= to && which(index_of(v) + 2 * e + 1, x[e].y) ? 2u << (2 * e) : 0u;
-                    }
-                }
+            for (int g = 0; g < 4; ++g) y[g] = raw(v0 + 32 * g + lane, w1);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                y[g] = clean(y[g]);
+                if (Vec<Tin>::largest(y[g]) >= from) bits |= in_range(y[g], from, to) << (VEC * g);
             }
-            append(bits, v);
+            auto each = [&](auto f) {
+                for (uint32_t left = bits; left != 0; left &= left - 1) {
+                    const int b = __ffs(left) - 1, g = b / VEC, e = b % VEC;
+                    f(b, index_of(v0 + 32 * g + lane) + e, Vec<Tin>::pick(g < 2 ? (g == 0 ? y[0] : y[1]) : g == 2 ? y[2] : y[3], e));
+                }
+            };
+            each([&](int b, int i, float x) {
+                if (!which(i, x)) bits &= ~(1u << b);
+            });
+            int at = places(__popc(bits));
+            each([&](int, int i, float x) { enlist(at++, x, i); });
         }
     };
-    // The weights of the thread's elements that are at least `from` and of which which(i, x, hi, lo) holds (hi, lo:
-    // the weight's digits), added up.  No branches, so that a vector's weights are formed side by side.
-    auto weigh = [&](float from, auto which) {
-        from = fmaxf(from, s.least);
-        uint32_t hi = 0, lo = 0;                // (digits of 21 bits: no thread has 2,048 elements)
+    // The elements from `from` on of the groups that reach it: a thread's vectors v + 32 g of every 128.
+    auto collect_groups = [&](float from) {
 #pragma unroll 1
-        for (int v = w0 + lane; v < w1; v += 32) {
-            const uint4 y = data[v];
-            if (Vec<Tin>::largest(y) < from) continue;
-            float2 x[VEC / 2];
-            Vec<Tin>::unpack(y, x);
-            const int i = index_of(v);
+        for (int g = 0; g < kGroups; ++g) {
+            const bool on = my_top[0] >= from;
 #pragma unroll
-            for (int e = 0; e < VEC / 2; ++e) {
-                float2 high, low;
-                digits42(weights2(s, x[e]), high, low);
-                const uint32_t h0 = digit(high.x), h1 = digit(high.y), l0 = digit(low.x), l1 = digit(low.y);
-                const bool on0 = (x[e].x >= from) & which(i + 2 * e, x[e].x, h0, l0);
-                const bool on1 = (x[e].y >= from) & which(i + 2 * e + 1, x[e].y, h1, l1);
-                hi += (on0 ? h0 : 0) + (on1 ? h1 : 0);
-                lo += (on0 ? l0 : 0) + (on1 ? l1 : 0);
+            for (int y = 0; y + 1 < kGroups; ++y) my_top[y] = my_top[y + 1];
+            if (!__any_sync(0xffffffffu, on)) continue;
+#pragma unroll 1
+            for (int v0 = w0 + 32 * g + lane; v0 - lane < w1; v0 += 512) {
+                uint4 y[4];
+                uint32_t bits = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = raw(v0 + 128 * e, on ? w1 : 0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    y[e] = clean(y[e]);
+                    if (Vec<Tin>::largest(y[e]) >= from) bits |= in_range(y[e], from, s.m) << (VEC * e);
+                }
+                for (int at = places(__popc(bits)); bits != 0; bits &= bits - 1, ++at) {
+                    const int b = __ffs(bits) - 1, i = b / VEC, e = b % VEC;
+                    enlist(at, Vec<Tin>::pick(i < 2 ? (i == 0 ? y[0] : y[1]) : i == 2 ? y[2] : y[3], e),
+                           index_of(v0 + 128 * i) + e);
+                }
             }
         }
+    };
+    // The weights of a vector's elements that are at least `from` and of which which(i, x, hi, lo) holds (hi, lo:
+    // the weight's digits), added to two digits of 21 bits (no thread has 1,024 elements).  No branches, so that
+    // a vector's weights are formed side by side.
+    auto add_weights = [&](const uint4 &y, int v, float from, auto which, uint32_t &hi, uint32_t &lo) {
+        float2 x[VEC / 2];
+        Vec<Tin>::unpack(y, x);
+        const int i = index_of(v);
+#pragma unroll
+        for (int e = 0; e < VEC / 2; ++e) {
+            float2 high, low;
+            digits42(weights2(s, x[e]), high, low);
+            const uint32_t h0 = digit(high.x), h1 = digit(high.y), l0 = digit(low.x), l1 = digit(low.y);
+            const bool on0 = (x[e].x >= from) & which(i + 2 * e, x[e].x, h0, l0);
+            const bool on1 = (x[e].y >= from) & which(i + 2 * e + 1, x[e].y, h1, l1);
+            hi += (on0 ? h0 : 0) + (on1 ? h1 : 0);
+            lo += (on0 ? l0 : 0) + (on1 ? l1 : 0);
+        }
+    };
+    // The thread's part of those of vectors a .. b - 1, a warp's.
+    auto weigh = [&](int a_, int b_, float from, auto which) {
+        uint32_t hi = 0, lo = 0;
+        each_above(a_, b_, from, [&](int v, const uint4 &y) { add_weights(y, v, from, which, hi, lo); });
         return ((u64)hi << 21) + lo;
     };
-    // All weights added up, those above `to` as well, and the elements of [from, to] to the list.
-    auto weigh_and_collect = [&](float from, float to, u64 &all, u64 &above) {
+    // All weights added up, those above `to` as well, and the elements of [from, to] to the list; or, with
+    // `above_too` not set, all elements from `from` on.
+    auto weigh_and_collect = [&](float from, float to, auto above_too, u64 &all, u64 &above) {
+        constexpr bool ABOVE = decltype(above_too)::value;
         uint32_t hi = 0, lo = 0, hi_above = 0, lo_above = 0;
-#pragma unroll 1
-        for (int v0 = w0; v0 < w1; v0 += 32) {
-            const int v = v0 + lane;
+        each_vector(w0, w1, [&](int v, const uint4 &y) {
             uint32_t bits = 0;
-            uint4 y;
-            if (v < w1) y = data[v];
-            if (v < w1 && Vec<Tin>::largest(y) >= fminf(from, s.least)) {
-                float2 x[VEC / 2];
-                Vec<Tin>::unpack(y, x);
+            float2 x[VEC / 2];
+            Vec<Tin>::unpack(y, x);
 #pragma unroll
-                for (int e = 0; e < VEC / 2; ++e) {
-                    float2 w = weights2(s, x[e]), high, low;
-                    w.x = x[e].x >= s.least ? w.x : 0.f;
-                    w.y = x[e].y >= s.least ? w.y : 0.f;
-                    digits42(w, high, low);
-                    const uint32_t h0 = digit(high.x), h1 = digit(high.y), l0 = digit(low.x), l1 = digit(low.y);
-                    hi += h0 + h1;
-                    lo += l0 + l1;
-                    if (x[e].x > to) {
-                        hi_above += h0;
-                        lo_above += l0;
-                    } else if (x[e].x >= from) {
-                        bits |= 1u << (2 * e);
-                    }
-                    if (x[e].y > to) {
-                        hi_above += h1;
-                        lo_above += l1;
-                    } else if (x[e].y >= from) {
-                        bits |= 2u << (2 * e);
-                    }
+            for (int e = 0; e < VEC / 2; ++e) {
+                float2 w = weights2(s, x[e]), high, low;
+                w.x = x[e].x >= s.least ? w.x : 0.f;
+                w.y = x[e].y >= s.least ? w.y : 0.f;
+                digits42(w, high, low);
+                const uint32_t h0 = __float_as_uint(high.x), h1 = __float_as_uint(high.y);
+                const uint32_t l0 = __float_as_uint(low.x), l1 = __float_as_uint(low.y);
+                hi += h0 + h1;                  // (2^23's bits come off below: of all elements, or of a vector's)
+                lo += l0 + l1;
+                if (ABOVE) {
+                    const bool up0 = x[e].x > to, up1 = x[e].y > to;
+                    hi_above += (up0 ? h0 - kBias : 0u) + (up1 ? h1 - kBias : 0u);
+                    lo_above += (up0 ? l0 - kBias : 0u) + (up1 ? l1 - kBias : 0u);
+                    bits |= (!up0 & (x[e].x >= from) ? 1u << (2 * e) : 0u) | (!up1 & (x[e].y >= from) ? 2u << (2 * e) : 0u);
+                } else {
+                    bits |= (x[e].x >= from ? 1u << (2 * e) : 0u) | (x[e].y >= from ? 2u << (2 * e) : 0u);
                 }
             }
-            append(bits, v);
-        }
+            hi -= VEC * kBias;
+            lo -= VEC * kBias;
+            for (int at = places(__popc(bits)); bits != 0; bits &= bits - 1, ++at) {
+                const int e = __ffs(bits) - 1;
+                enlist(at, Vec<Tin>::pick(y, e), index_of(v) + e);
+            }
+        });
         all = ((u64)hi << 21) + lo;
         above = ((u64)hi_above << 21) + lo_above;
     };
@@ -579,60 +667,115 @@ sample_kernel(const Sampling a, const int32_t slice) {
         const u64 by64 = p > 0.f ? (u64)(p * 0x1p63f) << 1 : 0, whole = __umul64hi(total, by64);
         return max(total * by64 != 0 ? whole + 1 : whole, (u64)1);
     };
-    // a value that is below all of the bins up to b, give or take the roundings; and one above all from b on
-    auto below_bin = [&](int b) {
-        const float d = (float)(b + 1) / by;
-        const float x = s.m - d * (1.f + 1e-6f);
-        return b >= kBins - 1 || !(x > -3e38f) ? -3.402823466e38f : x - 4e-7f * (fabsf(s.m) + fabsf(x)) - 1e-37f;
+    // a value that is below all of the bins before b, give or take the roundings; and one above all from b on
+    // (in bins from the maximum; never -infinity, which is what a vector holds beyond the row)
+    auto below_bin = [&](float b) {
+        const float x = s.m - b / by * (1.f + 1e-6f);
+        return fmaxf(x - 4e-7f * (fabsf(s.m) + fabsf(x)) - 1e-37f, -3.402823466e38f);
     };
-    auto above_bin = [&](int b) {
-        const float x = s.m - (float)b / by * (1.f - 1e-6f);
+    auto above_bin = [&](float b) {
+        const float x = s.m - b / by * (1.f - 1e-6f);
         return fminf(s.m, x + 4e-7f * (fabsf(s.m) + fabsf(x)) + 1e-37f);
     };
 
-    // Where top-p's border is, to a bin or two of log2 w: a value above all candidates and one below.  A bin's
-    // weights lie within 2^(1/12) of each other, so it adds them up relative to its own upper end, to 2^-16
-    // in 32 bits (a CTA has fewer than 2^16 elements).  The estimates are off by less than 2^-14 of the sum and 2^18
-    // units of 2^-42, which `slack` covers on either side.
+    // Where top-p's border is, to a bin or two of log2 w, four times as narrow as the others: a value above all
+    // candidates and one below.  A bin's weights lie within 2^(1/48) of each other, so it adds them up relative to
+    // its own upper end, in whole multiples of 2^-fine, which 32 bits hold for all elements of a copy (a
+    // quarter of the warps).  The estimates are off by less than 2^-fine and 2^-17 of the sum (2^-24 of log w, 30
+    // at most, three times) and 2^18 units of 2^-42; `slack` is more than twice that on either side.  Returns
+    // about how many elements of the row reach `from`.
     auto candidates = [&](float &from, float &to) {
-        next_histogram();
-#pragma unroll 1
-        for (int v = w0 + lane; v < w1; v += 32) {
-            const uint4 y = data[v];
-            if (Vec<Tin>::largest(y) < s.least) continue;
+        const int fine = min(17, __clz(kWarps / kCopies * per_warp * VEC) - 1);
+        const float by4 = 4.f * by, unit = __int_as_float((127 + fine) << 23);
+        const uint32_t bins_at = tc::smem_u32(hists + warp % kCopies * kFine) - 4 * kBias;
+#pragma unroll
+        for (int c = 0; c < kCopies; ++c) reinterpret_cast<uint4 *>(hists + c * kFine)[tid] = make_uint4(0u, 0u, 0u, 0u);
+        if (tid == 0) chosen_count = 0;
+        __syncthreads();
+        each_vector(w0, w1, [&](int, const uint4 &y) {
             float2 x[VEC / 2];
             Vec<Tin>::unpack(y, x);
+            // (nothing for a weight of zero: masked logits would all meet in one bin)
+            auto add = [&](uint32_t b, float weight) {
+                asm volatile("{\n.reg .pred some;\nsetp.ne.u32 some, %1, 0;\n@some red.shared.add.u32 [%0], %1;\n}\n"
+                             ::"r"(bins_at + 4 * b), "r"(digit(weight)) : "memory");
+            };
 #pragma unroll
             for (int e = 0; e < VEC / 2; ++e) {
                 auto both = [](float z) { return make_float2(z, z); };
-                const float2 d = tc::f2sub(both(s.m), x[e]), b = fma_cut2(d, both(by), both(8388608.f));
-                const uint32_t b0 = min(__float_as_uint(b.x), kBias + kBins - 1), b1 = min(__float_as_uint(b.y), kBias + kBins - 1);
+                const float2 d = tc::f2sub(both(s.m), x[e]), b = fma_cut2(d, both(by4), both(8388608.f));
+                const uint32_t b0 = min(__float_as_uint(b.x), kBias + kFine - 1), b1 = min(__float_as_uint(b.y), kBias + kFine - 1);
                 // (the bins' upper ends, negated)
                 const float2 ends = tc::f2sub(both(8388608.f), make_float2(__uint_as_float(b0), __uint_as_float(b1)));
-                float2 w = tc::f2fma(tc::f2fma(d, both(by), ends), both(-1.f / kPerOctave), both(16.f));
-                w.x = tc::ex2(w.x);
-                w.y = tc::ex2(w.y);
-                w = fma_cut2(w, both(1.f), both(8388608.f));
-                if (digit(w.x) != 0) atomicAdd(&hist[b0 - kBias], digit(w.x));
-                if (digit(w.y) != 0) atomicAdd(&hist[b1 - kBias], digit(w.y));
+                const float2 into = tc::f2fma(d, both(by4), ends);
+                float2 w = make_float2(tc::ex2(into.x * (-0.25f / kPerOctave)), tc::ex2(into.y * (-0.25f / kPerOctave)));
+                w = fma_cut2(w, both(unit), both(8388608.f));
+                add(b0, w.x);
+                add(b1, w.y);
             }
+        });
+        __syncthreads();
+        // four bins to a thread
+        float of_4[4];
+        {
+            u64 z[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int c = 0; c < kCopies; ++c) {
+                const uint4 y = reinterpret_cast<const uint4 *>(hists + c * kFine)[tid];
+                z[0] += y.x;
+                z[1] += y.y;
+                z[2] += y.z;
+                z[3] += y.w;
+            }
+            reinterpret_cast<float4 *>(hists)[tid] = make_float4((float)z[0], (float)z[1], (float)z[2], (float)z[3]);
         }
         cluster.sync();
-        const u64 mine_w = __float2ull_rz((float)bin_sum(0) * exp2f(26.f - (float)tid / kPerOctave));
+        of_4[0] = of_4[1] = of_4[2] = of_4[3] = 0.f;
+#pragma unroll
+        for (int r = 0; r < kMaxRanks; ++r) {   // (reads of all ranks on their way together)
+            const float4 y = reinterpret_cast<const float4 *>(cluster.map_shared_rank(hists, r < ranks ? r : 0))[tid];
+            of_4[0] += r < ranks ? y.x : 0.f;
+            of_4[1] += r < ranks ? y.y : 0.f;
+            of_4[2] += r < ranks ? y.z : 0.f;
+            of_4[3] += r < ranks ? y.w : 0.f;
+        }
+        u64 bins[4], mine_w = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            bins[e] = __float2ull_rz(of_4[e] * exp2f((float)(42 - fine) - (float)(4 * tid + e) * (0.25f / kPerOctave)));
+            mine_w += bins[e];
+        }
         u64 slack = 0, run = 0, goal = 0;
         border(mine_w, 0, [&](u64 total) {
-            slack = (total >> 12) + (1 << 20);
+            slack = (total >> (fine - 3)) + (1 << 20);
             goal = share(total);
-            return goal > slack ? goal - slack : (u64)1;
+            return goal;
         }, &run);
-        const int first_bin = found_bin;
+        // the first bin with which the sum may reach the goal, and the first with which it must
+        if (tid == 0) {
+            found_bin = 0;
+            found_last = kFine - 1;
+        }
         __syncthreads();
-        if (tid == 0) found_bin = kBins - 1;
+        run -= mine_w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const u64 next = run + bins[e];
+            if (next + slack >= goal && run + slack < goal) found_bin = 4 * tid + e;
+            if (next >= goal + slack && run < goal + slack) found_last = 4 * tid + e;
+            run = next;
+        }
         __syncthreads();
-        if (run >= goal + slack && run - mine_w < goal + slack) found_bin = tid;
+        const int last_bin = found_last;
+        to = above_bin(0.25f * (float)found_bin);
+        from = last_bin == kFine - 1 ? -3.402823466e38f : below_bin(0.25f * (float)(last_bin + 1));
+        float about = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) about += 4 * tid + e <= last_bin + 1 ? of_4[e] : 0.f;
+        const int of_warp = __reduce_add_sync(0xffffffffu, (int)(about * 1.03f / unit) + 1);
+        if (lane == 0) atomicAdd(&chosen_count, of_warp);
         __syncthreads();
-        to = above_bin(first_bin);
-        from = below_bin(found_bin);
+        return chosen_count - kThreads;
     };
 
     // Narrows the border down to the first elements of the order that reach a count (k) or a share of
@@ -640,6 +783,11 @@ sample_kernel(const Sampling a, const int32_t slice) {
     // thread has above the candidates.
     u64 ahead_w = 0;
     int pooled = 0;
+    bool listed = false;                        // the list holds all that stays
+    const u64 w_least = least > 0.f ? (u64)(fminf(least, 1.f) * 0x1p42f) : 0;
+    // a value below all whose weight reaches min-p's, with room for roundings
+    float least_at = w_least > 0 ? s.m + (log2f(fminf(least, 1.f)) * (1.f + 1e-5f) - 1e-6f) / s.c : -INFINITY;
+    least_at = fmaxf(least_at - 4e-7f * (fabsf(s.m) + fabsf(least_at)) - 1e-37f, -3.402823466e38f);
     auto narrow = [&](bool by_weight) {
         u64 want = (u64)k, above = 0, before, here;
         int bin = -1;
@@ -652,11 +800,41 @@ sample_kernel(const Sampling a, const int32_t slice) {
         if (tid == 0) count = 0;
         if (by_weight && border_at == -INFINITY) {
             float from, to;
-            candidates(from, to);
-            u64 total;
-            weigh_and_collect(from, to, total, ahead_w);
-            above = ahead_w;
-            cluster_totals(total, above);
+            const int about = candidates(from, to);
+            if (least_at > to) {
+                // min-p lets by less than top-p does
+                collect(least_at, s.m, [](int, float) { return true; });
+                __syncthreads();
+                pooled = count;
+                listed = pooled <= kList;
+                return;
+            }
+            u64 total = 0;
+            bool again = about > kList - kThreads;
+            if (!again) {
+                // few enough to be in the list, all that stay (a list's weights are below 2^54, eight marks below 2^64)
+                constexpr u64 kTooMany = 1ull << 60;
+                weigh_and_collect(from, to, std::false_type{}, total, above);
+                __syncthreads();
+                const int have = min(count, kList);
+                above = count > kList ? kTooMany : 0;
+                for (int i = tid; i < have; i += kThreads) {
+                    const float x = value_of(ordered_key(list[i]));
+                    above += x > to ? weight(s, x) : 0;
+                }
+                cluster_totals(total, above);
+                again = above >= kTooMany;
+                listed = !again;
+                if (again) {
+                    if (tid == 0) count = 0;
+                    __syncthreads();
+                }
+            }
+            if (again) {
+                weigh_and_collect(from, to, std::true_type{}, total, ahead_w);
+                above = ahead_w;
+                cluster_totals(total, above);
+            }
             goal(total);
             most = key_of(to);
             lowest = key_of(from);
@@ -675,12 +853,13 @@ sample_kernel(const Sampling a, const int32_t slice) {
             if (!border(by_weight ? bin_sum(0) + (bin_sum(1) << 32) : bin_sum(0), 0, goal)) return;  // fewer: all stay
             bin = found_bin;
             above = found[0];
-            most = key_of(above_bin(bin));
-            lowest = key_of(below_bin(bin));
+            most = key_of(above_bin((float)bin));
+            lowest = key_of(bin == kBins - 1 ? -3.402823466e38f : below_bin((float)(bin + 1)));
             collect(value_of(lowest), value_of(most), in_bin);
         }
         __syncthreads();
         pooled = count;
+        listed = listed && pooled <= kList;
         for (;;) {
             const int shift = max(Vec<Tin>::GRAIN, 23 - __clz(most - lowest));      // 2^9 bins at most
             next_histogram();
@@ -726,39 +905,42 @@ sample_kernel(const Sampling a, const int32_t slice) {
             } else {
                 each_in(it, it, [&](int i, float x) { equal += stays(i, x) ? 1 : 0; });
             }
-            if (tid == 0) chosen_count = 0;
             const u64 all = cluster_sum(equal, before, here);
             if (keep < all) {
                 auto publish = [&](int at) {
                     for (int r = 0; r < ranks; ++r) *cluster.map_shared_rank(&chosen_index, r) = at;
                 };
+                const u64 ahead = before - part[warp];          // of the CTAs before
                 if (in_pool) {
-                    // the CTA's equal ones in any order (in the histograms' place, which all have read): the one
-                    // with as many smaller indices as are wanted
-                    int32_t *const equals = reinterpret_cast<int32_t *>(hists);
-                    const u64 ahead = before - part[warp];      // of the CTAs before
-                    for (int i = tid; i < pooled; i += kThreads)
-                        if (ordered_key(list[i]) == most) equals[atomicAdd(&chosen_count, 1)] = ordered_index(list[i]);
-                    __syncthreads();
-                    const int of_them = chosen_count;
-                    for (int i = tid; i < of_them; i += kThreads) {
-                        const int at = equals[i];
-                        u64 smaller = ahead;
-                        for (int j = 0; j < of_them; ++j) smaller += equals[j] < at ? 1 : 0;
-                        if (smaller + 1 == keep) publish(at);
+                    // the one by its index in the CTA, the index's upper half first
+                    if (keep > ahead && keep <= ahead + part_all) {
+                        u64 passed = ahead;
+                        int upper = -1;
+                        for (int level = 0; level < 2; ++level) {
+                            next_histogram();
+                            for (int i = tid; i < pooled; i += kThreads) {
+                                const int at = ordered_index(list[i]);
+                                if (ordered_key(list[i]) == most && (level == 0 || at / kBins == upper))
+                                    atomicAdd(&hist[level == 0 ? at / kBins : at % kBins], 1u);
+                            }
+                            __syncthreads();
+                            border(hist[tid], passed, [&](u64) { return keep; });
+                            if (level == 0) {
+                                upper = found_bin;
+                                passed = found[0];
+                            }
+                        }
+                        if (tid == 0) publish(upper * kBins + found_bin);
                     }
                 } else if (keep > before && keep <= before + here) {
                     // this warp has the last one
                     u64 seen = before;
                     for (int v0 = w0; v0 < w1; v0 += 32) {
                         const int v = v0 + lane;
-                        uint32_t bits = 0;
-                        if (v < w1)
-#pragma unroll
-                            for (int e = 0; e < VEC; ++e) {
-                                const float x = Vec<Tin>::load(data + v, e);
-                                if (x == it && stays(index_of(v) + e, x)) bits |= 1u << e;
-                            }
+                        const uint4 y = clean(raw(v, w1));
+                        uint32_t bits = in_range(y, it, it);
+                        for (int e = 0; e < VEC; ++e)
+                            if (!stays(index_of(v) + e, it)) bits &= ~(1u << e);
                         int run = __popc(bits);
                         const int cnt = run;
 #pragma unroll
@@ -782,7 +964,6 @@ sample_kernel(const Sampling a, const int32_t slice) {
     };
 
     u64 sum = 0;                                // of what stays
-    const u64 w_least = least > 0.f ? (u64)(fminf(least, 1.f) * 0x1p42f) : 0;
     // the first token whose running sum exceeds floor(u sum / 2^24) (the sum of all does, since u < 2^24)
     auto drawn = [&]() {
         const uint32_t tick = __float2uint_rz(fminf(fmaxf(u, 0.f) * 16777216.f, 16777215.f));
@@ -791,13 +972,16 @@ sample_kernel(const Sampling a, const int32_t slice) {
 
     // ---- a small k: the few logits that can be among the first k, sorted in one CTA
     bool done = false;
-    if (!none && k > 0 && k < V && k <= kListK && k <= ranks * kThreads / 2) {
-        // k of the threads' largest logits lie in the bins up to this one
+    if (!none && k > 0 && k < V && k <= kListK) {
+        // k of the groups' largest logits lie in the bins up to this one
         next_histogram();
-        if (my_top != -INFINITY) atomicAdd(&hist[bin_of(my_top)], 1u);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+            if (my_top[g] != -INFINITY) atomicAdd(&hist[bin_of(my_top[g])], 1u);
         cluster.sync();
-        const float from = border(bin_sum(0), 0, [&](u64) { return (u64)k; }) ? below_bin(found_bin) : -3.402823466e38f;
-        collect(from, s.m, [](int, float) { return true; });
+        const float from = border(bin_sum(0), 0, [&](u64) { return (u64)k; }) && found_bin < kBins - 1
+                               ? below_bin((float)(found_bin + 1)) : -3.402823466e38f;
+        collect_groups(from);
         cluster.sync();
         // the lists' lengths, a rank to a lane; warp r brings rank r's to the first CTA
         const int length = lane < ranks ? *cluster.map_shared_rank(&count, lane) : 0;
@@ -808,7 +992,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
             if (lane >= o) upto += z;
         }
         const int all = __shfl_sync(0xffffffffu, upto, kMaxRanks - 1);
-        done = all <= kList;
+        done = all <= kSorted;
         if (done && rank == 0) {
             if (warp > 0 && warp < ranks) {
                 const int c = __shfl_sync(0xffffffffu, length, warp), at = __shfl_sync(0xffffffffu, upto, warp) - c;
@@ -963,57 +1147,98 @@ sample_kernel(const Sampling a, const int32_t slice) {
         auto counts = [&](int i, float x, uint32_t hi, uint32_t lo) {
             return stays(i, x) & ((hi > least_hi) | ((hi == least_hi) & (lo >= least_lo)));
         };
-        u64 mine_w;
-        if (border_at > -INFINITY && pooled <= kList && w_least == 0 && !(k > 0 && k < V)) {
-            // what lies above the candidates was summed up with them; of these, what stays, to the warps that have it
+        u64 mine_w = 0;
+        const float from = fmaxf(fmaxf(lowest_value(), s.least), least_at);
+        auto in_list = [&](u64 c, u64 &w) {     // does it stay, and its weight
+            const float x = value_of(ordered_key(c));
+            w = weight(s, x);
+            return stays(ordered_index(c), x) && w >= w_least;
+        };
+        if (listed || (border_at > -INFINITY && pooled <= kList && w_least == 0 && !(k > 0 && k < V))) {
+            // what lies above the candidates was summed up with them, unless they are in the list, too; of those, what
+            // stays, to the warps that have it
             if (tid < kWarps) more[tid] = 0;
             __syncthreads();
             for (int i = tid; i < pooled; i += kThreads) {
-                const int at = ordered_index(list[i]);
-                const float x = value_of(ordered_key(list[i]));
-                if (stays(at, x)) atomicAdd(&more[((at + lead) / VEC - first) / per_warp], weight(s, x));
+                u64 w;
+                if (in_list(list[i], w)) atomicAdd(&more[((ordered_index(list[i]) + lead) / VEC - first) / per_warp], w);
             }
             __syncthreads();
             mine_w = ahead_w + (lane == 0 ? more[warp] : 0);
+        } else if (border_at == -INFINITY && w_least == 0) {
+            mine_w = weigh(w0, w1, from, [](int, float, uint32_t, uint32_t) { return true; });
         } else {
-            // (with min-p's weight in mind, as a value with room for roundings)
-            const float from = w_least > 0 ? s.m + (log2f(fminf(least, 1.f)) * (1.f + 1e-5f) - 1e-6f) / s.c : -INFINITY;
-            mine_w = weigh(fmaxf(lowest_value(), from - 4e-7f * (fabsf(s.m) + fabsf(from)) - 1e-37f), counts);
+            mine_w = weigh(w0, w1, from, counts);
         }
         sum = cluster_sum(mine_w, before, here);
         const u64 need = drawn();
-        if (a.token != nullptr && before <= need && before + here > need) {
-            for (int v0 = w0; v0 < w1; v0 += 32) {
-                const int v = v0 + lane;
-                u64 all = 0;
-#pragma unroll 1
-                for (int e = 0; e < VEC; ++e) {
-                    const float x = v < w1 ? Vec<Tin>::load(data + v, e) : -INFINITY;
-                    const u64 w = x > -INFINITY && stays(index_of(v) + e, x) ? weight(s, x) : 0;
-                    all += w >= w_least ? w : 0;
+        const bool hit = a.token != nullptr && before <= need && before + here > need;
+        const u64 of_before = before - part[warp];      // (of the CTAs before)
+        if (__syncthreads_or(hit ? 1 : 0) == 0) {
+            // another CTA has it
+        } else if (listed) {
+            u64 passed = of_before;
+            int upper = -1;
+            for (int level = 0; level < 2; ++level) {
+                next_histogram();
+                for (int i = tid; i < pooled; i += kThreads) {
+                    const int at = ordered_index(list[i]);
+                    u64 w;
+                    if (in_list(list[i], w) && (level == 0 || at / kBins == upper))
+                        add_weight(level == 0 ? at / kBins : at % kBins, (uint32_t)(w >> 21), (uint32_t)w & 0x1fffffu);
                 }
-                u64 run = all;
+                __syncthreads();
+                border(hist[tid] + ((u64)hist[kBins + tid] << 32), passed, [&](u64) { return need + 1; });
+                if (level == 0) {
+                    upper = found_bin;
+                    passed = found[0];
+                }
+            }
+            if (tid == 0) a.token[n] = upper * kBins + found_bin;
+        } else {
+            // the warp's vectors that hold the token, shared out over the CTA's warps
+            if (hit && lane == 0) {
+                found_bin = warp;
+                found[0] = before;
+            }
+            __syncthreads();
+            const int v0 = min(mine, found_bin * per_warp), v1 = min(mine, v0 + per_warp);
+            const int each = (v1 - v0 + kWarps - 1) / kWarps, a0 = min(v1, v0 + warp * each), a1 = min(v1, a0 + each);
+            u64 x = weigh(a0, a1, from, counts), run_all;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const u64 z = __shfl_up_sync(0xffffffffu, run, o);
-                    if (lane >= o) run += z;
-                }
-                const unsigned hit = __ballot_sync(0xffffffffu, before + run > need);
-                if (hit != 0) {
-                    if (lane == __ffs(hit) - 1) {
-                        u64 at = before + run - all;
-                        int e = 0;
-                        for (; e < VEC - 1; ++e) {
-                            const float x = Vec<Tin>::load(data + v, e);
-                            const u64 w = x > -INFINITY && stays(index_of(v) + e, x) ? weight(s, x) : 0;
-                            at += w >= w_least ? w : 0;
-                            if (at > need) break;
-                        }
-                        a.token[n] = index_of(v) + e;
+            for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            if (lane == 0) part[warp] = x;
+            u64 at = parts_before(run_all) + found[0];
+            if (at <= need && at + x > need) {
+                for (int b0 = a0; b0 < a1; b0 += 32) {
+                    const int v = b0 + lane;
+                    uint32_t hi = 0, lo = 0;
+                    const uint4 y = clean(raw(v, a1));
+                    add_weights(y, v, from, counts, hi, lo);
+                    const u64 own = ((u64)hi << 21) + lo;
+                    u64 run = own;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const u64 z = __shfl_up_sync(0xffffffffu, run, o);
+                        if (lane >= o) run += z;
                     }
-                    break;
+                    const unsigned hits = __ballot_sync(0xffffffffu, at + run > need);
+                    if (hits != 0) {
+                        if (lane == __ffs(hits) - 1) {
+                            at += run - own;
+                            int i = index_of(v);
+                            for (int e = 0; e < VEC - 1; ++e, ++i) {
+                                const float z = Vec<Tin>::pick(y, e);
+                                const u64 w = z >= from && stays(i, z) ? weight(s, z) : 0;
+                                at += w >= w_least ? w : 0;
+                                if (at > need) break;
+                            }
+                            a.token[n] = i;
+                        }
+                        break;
+                    }
+                    at += __shfl_sync(0xffffffffu, run, 31);
                 }
-                before += __shfl_sync(0xffffffffu, run, 31);
             }
         }
     } else if (none && a.token != nullptr && rank == 0 && tid == 0) {
@@ -1024,13 +1249,12 @@ sample_kernel(const Sampling a, const int32_t slice) {
         const bool bf16 = a.probs_bf16 != 0;
         Scale deep = s;                         // down to 2^-125
         deep.least = fmaxf(s.m - 125.f / s.c, -3.402823466e38f);
-        const float from = none ? INFINITY : fmaxf(lowest_value(), deep.least);
+        const float from = none ? INFINITY : fmaxf(fmaxf(lowest_value(), deep.least), least_at);
         unsigned char *out = static_cast<unsigned char *>(a.probs) + n * (int64_t)V * (bf16 ? 2 : 4);
         // whole vectors where the output's rows lie as the input's
         const bool whole = ((reinterpret_cast<uintptr_t>(out) - (size_t)lead * (bf16 ? 2 : 4)) & (bf16 ? VEC * 2 - 1 : 15)) == 0;
-#pragma unroll 1
-        for (int v = w0 + lane; v < w1; v += 32) {
-            const uint4 raw = data[v];
+        each_vector(w0, w1, [&](int v, const uint4 &raw) {
+            if (v >= w1) return;
             const int e0 = index_of(v);
             float y[VEC];
 #pragma unroll
@@ -1072,39 +1296,50 @@ sample_kernel(const Sampling a, const int32_t slice) {
                         if (e0 + e >= 0 && e0 + e < V) to[e] = y[e];
                 }
             }
-        }
+        });
     }
     cluster.sync();                             // no CTA leaves while its shared memory is read
 }
 
+// How many clusters of so many CTAs the device holds at once; asked once per device.
+template <typename Tin> int clusters_at_once(int ranks, cudaLaunchConfig_t &cfg, cudaLaunchAttribute &cluster) {
+    static std::atomic<int> known[64][kMaxRanks + 1];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    const bool keep = dev >= 0 && dev < 64;
+    if (keep && (n = known[dev][ranks].load(std::memory_order_relaxed)) != 0) return n;
+    cfg.gridDim = dim3((unsigned)ranks);
+    cluster.val.clusterDim.x = ranks;
+    if (cudaOccupancyMaxActiveClusters(&n, sample_kernel<Tin>, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        n = 0;
+    }
+    if (keep && n > 0) known[dev][ranks].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 template <typename Tin> cudaError_t run(const Sampling &a, int32_t N, cudaStream_t stream) {
-    int dev = 0, sms = 152;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        sms = 152;
     constexpr int VEC = Vec<Tin>::N;
     const int vecs = (a.V + VEC - 1) / VEC + 1;
-    int ranks = kMaxRanks;
-    while (ranks > 1 && ((int64_t)ranks * N > 2 * (int64_t)sms || vecs < ranks * 256) &&
-           (int64_t)vecs * 16 <= (ranks / 2) * (int64_t)(72 * 1024))
-        ranks /= 2;
-    const int slice = (vecs + ranks - 1) / ranks;
-    const size_t smem = (size_t)slice * 16 + kScratch;
     static std::atomic<uint64_t> smem_set{0};
-    cudaError_t e = allow_dynamic_smem(sample_kernel<Tin>, kMaxSmem, smem_set);
+    cudaError_t e = allow_dynamic_smem(sample_kernel<Tin>, kSmem, smem_set);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute cluster;
     cluster.id = cudaLaunchAttributeClusterDimension;
-    cluster.val.clusterDim.x = ranks;
     cluster.val.clusterDim.y = 1;
     cluster.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)N * ranks);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
+    cfg.dynamicSmemBytes = kSmem;
     cfg.attrs = &cluster;
     cfg.numAttrs = 1;
+    // the largest clusters with which all rows run at once, of CTAs that have something to do
+    int ranks = kMaxRanks;
+    while (ranks > 1 && (vecs < ranks * 256 || N > clusters_at_once<Tin>(ranks, cfg, cluster))) --ranks;
+    const int slice = (vecs + ranks - 1) / ranks;
+    cfg.gridDim = dim3((unsigned)N * ranks);
+    cluster.val.clusterDim.x = ranks;
+    cfg.stream = stream;
     e = cudaLaunchKernelEx(&cfg, sample_kernel<Tin>, a, (int32_t)slice);
     if (e == cudaSuccess) count_launches(1);
     else (void)cudaGetLastError();                     // reported here
