@@ -447,20 +447,21 @@ sample_kernel(const Sampling a, const int32_t slice) {
             each([&](int, int i, float x) { enlist(at++, x, i); });
         }
     };
-    // The elements from `from` on of the groups that reach it: a thread's vectors v + 32 g of every 128.
+    // The elements from `from` on of the groups that reach it (a thread's vectors v + 32 g of every 128): each lane
+    // takes its own groups one after another.
     auto collect_groups = [&](float from) {
-#pragma unroll 1
-        for (int g = 0; g < kGroups; ++g) {
-            const bool on = my_top[0] >= from;
+        uint32_t groups = 0;
 #pragma unroll
-            for (int y = 0; y + 1 < kGroups; ++y) my_top[y] = my_top[y + 1];
-            if (!__any_sync(0xffffffffu, on)) continue;
+        for (int g = 0; g < kGroups; ++g) groups |= my_top[g] >= from ? 1u << g : 0u;
+        while (__any_sync(0xffffffffu, groups != 0)) {
+            const int until = groups != 0 ? w1 : 0, g = groups != 0 ? __ffs(groups) - 1 : 0;
+            groups &= groups - 1;
 #pragma unroll 1
-            for (int v0 = w0 + 32 * g + lane; v0 - lane < w1; v0 += 512) {
+            for (int v0 = w0; v0 < w1; v0 += 512) {
                 uint4 y[4];
                 uint32_t bits = 0;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = raw(v0 + 128 * e, on ? w1 : 0);
+                for (int e = 0; e < 4; ++e) y[e] = raw(v0 + 32 * g + lane + 128 * e, until);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     y[e] = clean(y[e]);
@@ -469,7 +470,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
                 for (int at = places(__popc(bits)); bits != 0; bits &= bits - 1, ++at) {
                     const int b = __ffs(bits) - 1, i = b / VEC, e = b % VEC;
                     enlist(at, Vec<Tin>::pick(i < 2 ? (i == 0 ? y[0] : y[1]) : i == 2 ? y[2] : y[3], e),
-                           index_of(v0 + 128 * i) + e);
+                           index_of(v0 + 32 * g + lane + 128 * i) + e);
                 }
             }
         }
@@ -503,7 +504,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
     auto weigh_and_collect = [&](float from, float to, auto above_too, u64 &all, u64 &above) {
         constexpr bool ABOVE = decltype(above_too)::value;
         uint32_t hi = 0, lo = 0, hi_above = 0, lo_above = 0;
-        each_vector(w0, w1, [&](int v, const uint4 &y) {
+        auto one = [&](const uint4 &y) {        // returns which are for the list
             uint32_t bits = 0;
             float2 x[VEC / 2];
             Vec<Tin>::unpack(y, x);
@@ -528,11 +529,27 @@ sample_kernel(const Sampling a, const int32_t slice) {
             }
             hi -= VEC * kBias;
             lo -= VEC * kBias;
-            for (int at = places(__popc(bits)); bits != 0; bits &= bits - 1, ++at) {
-                const int e = __ffs(bits) - 1;
-                enlist(at, Vec<Tin>::pick(y, e), index_of(v) + e);
+            return bits;
+        };
+        // (four vectors of a lane on their way, and to the list, at a time; those for it are read once more)
+#pragma unroll 1
+        for (int v0 = w0; v0 < w1; v0 += 128) {
+            uint4 y[4];
+            uint32_t bits = 0;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) y[g] = raw(v0 + 32 * g + lane, w1);
+#pragma unroll 1
+            for (int g = 0; g < 4; ++g) {
+                bits |= one(clean(y[0])) << (VEC * g);
+                y[0] = y[1];
+                y[1] = y[2];
+                y[2] = y[3];
             }
-        });
+            for (int at = places(__popc(bits)); bits != 0; bits &= bits - 1, ++at) {
+                const int b = __ffs(bits) - 1, i = index_of(v0 + b / VEC * 32 + lane) + b % VEC;
+                enlist(at, infinite ? 0.f : static_cast<float>(row[i]), i);
+            }
+        }
         all = ((u64)hi << 21) + lo;
         above = ((u64)hi_above << 21) + lo_above;
     };
@@ -620,11 +637,13 @@ sample_kernel(const Sampling a, const int32_t slice) {
     auto bin_sum = [&](int word) {
         uint32_t x[kMaxRanks];
 #pragma unroll
-        for (int r = 0; r < kMaxRanks; ++r)     // (reads of all ranks on their way together)
-            x[r] = cluster.map_shared_rank(hist, r < ranks ? r : 0)[word * kBins + tid];
+        for (int r = 0; r < kMaxRanks; ++r) {   // (reads of all ranks on their way together)
+            x[r] = 0;
+            if (r < ranks) x[r] = cluster.map_shared_rank(hist, r)[word * kBins + tid];
+        }
         u64 all = 0;
 #pragma unroll
-        for (int r = 0; r < kMaxRanks; ++r) all += r < ranks ? x[r] : 0;
+        for (int r = 0; r < kMaxRanks; ++r) all += x[r];
         return all;
     };
     // The first bin at which the bins, added up in order, reach want(total); `above` lies above the first
