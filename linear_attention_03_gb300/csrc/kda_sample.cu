@@ -128,17 +128,20 @@ struct Scale {
     float m, c, cl, least;
 };
 
-// The weights of two logits, to 2^-24: x - m with its rounding error, the product with c in one
-// rounding behind the point, 2^f by its series (to 2^-27 for |f| <= 1/2) and the exponent put on
-// in whole numbers.  Paired arithmetic: some 12 instructions a weight.  (No number of meaning below s.least.)
-__device__ __forceinline__ float2 weights2(const Scale &s, float2 x) {
+// The weights of two logits: the product of x - m with c in one rounding behind the point, 2^f by its series (to
+// 2^-27 for |f| <= 1/2) and the exponent put on in whole numbers, in paired arithmetic.  WHOLE: x - m with
+// its rounding error, so to 2^-24; otherwise to that and 2^-25 of log w, with errors of either sign (none for bf16
+// logits of like size).  (No number of meaning below s.least.)
+template <bool WHOLE = false> __device__ __forceinline__ float2 weights2(const Scale &s, float2 x) {
     auto both = [](float a) { return make_float2(a, a); };
-    const float2 d = tc::f2sub(x, both(s.m)), mv = tc::f2sub(x, d), xv = tc::f2add(d, mv);
-    const float2 err = tc::f2add(tc::f2sub(x, xv), tc::f2sub(mv, both(s.m)));
+    const float2 d = tc::f2sub(x, both(s.m));
     const float2 t = tc::f2fma(d, both(s.c), both(12582912.f)), whole = tc::f2sub(both(12582912.f), t);
     float2 f = tc::f2fma(d, both(s.c), whole);
     f = tc::f2fma(d, both(s.cl), f);
-    f = tc::f2fma(err, both(s.c), f);
+    if (WHOLE) {
+        const float2 mv = tc::f2sub(x, d), xv = tc::f2add(d, mv);
+        f = tc::f2fma(tc::f2add(tc::f2sub(x, xv), tc::f2sub(mv, both(s.m))), both(s.c), f);
+    }
     float2 p = both(1.5252733804059841e-5f);    // ln(2)^k / k!, k = 7 .. 0
     p = tc::f2fma(p, f, both(1.5403530393381610e-4f));
     p = tc::f2fma(p, f, both(1.3333558146428443e-3f));
@@ -1185,7 +1188,23 @@ sample_kernel(const Sampling a, const int32_t slice) {
             __syncthreads();
             mine_w = ahead_w + (lane == 0 ? more[warp] : 0);
         } else if (border_at == -INFINITY && w_least == 0) {
-            mine_w = weigh(w0, w1, from, [](int, float, uint32_t, uint32_t) { return true; });
+            uint32_t hi = 0, lo = 0;
+            each_above(w0, w1, from, [&](int, const uint4 &y) {
+                float2 x[VEC / 2];
+                Vec<Tin>::unpack(y, x);
+#pragma unroll
+                for (int e = 0; e < VEC / 2; ++e) {
+                    float2 w = weights2(s, x[e]), high, low;
+                    w.x = x[e].x >= from ? w.x : 0.f;
+                    w.y = x[e].y >= from ? w.y : 0.f;
+                    digits42(w, high, low);
+                    hi += __float_as_uint(high.x) + __float_as_uint(high.y);
+                    lo += __float_as_uint(low.x) + __float_as_uint(low.y);
+                }
+                hi -= VEC * kBias;
+                lo -= VEC * kBias;
+            });
+            mine_w = ((u64)hi << 21) + lo;
         } else {
             mine_w = weigh(w0, w1, from, counts);
         }
@@ -1283,10 +1302,10 @@ sample_kernel(const Sampling a, const int32_t slice) {
                 Vec<Tin>::unpack(raw, x);
 #pragma unroll
                 for (int e = 0; e < VEC / 2; ++e) {
-                    const float2 w = weights2(deep, x[e]);
-                    if (x[e].x >= from && stays(e0 + 2 * e, x[e].x) && (w_least == 0 || fixed42(w.x) >= w_least))
+                    const float2 w = weights2<true>(deep, x[e]);
+                    if (x[e].x >= from && stays(e0 + 2 * e, x[e].x) && (w_least == 0 || weight(s, x[e].x) >= w_least))
                         y[2 * e] = w.x * inv;
-                    if (x[e].y >= from && stays(e0 + 2 * e + 1, x[e].y) && (w_least == 0 || fixed42(w.y) >= w_least))
+                    if (x[e].y >= from && stays(e0 + 2 * e + 1, x[e].y) && (w_least == 0 || weight(s, x[e].y) >= w_least))
                         y[2 * e + 1] = w.y * inv;
                 }
             }
