@@ -35,6 +35,7 @@ constexpr float kPerOctave = 12.f;              // bins for a halving of w
 constexpr int kGroups = 4;                      // a thread's logits, by which its largest ones are taken
 constexpr int kList = 4096;                     // a CTA's candidates for the border
 constexpr int kSorted = 4 * kThreads, kListK = 1024;    // logits that one CTA sorts, and the k for which that is tried
+constexpr int kListAll = 1024;                  // logits that top-p takes from a list altogether
 constexpr int kFew = 128;                       // logits of which every pair is compared instead
 constexpr int32_t kAll = 0x7fffffff;
 // histograms (two of kBins 64-bit sums in turn, or copies of one of kFine sums) and a list
@@ -828,13 +829,13 @@ sample_kernel(const Sampling a, const int32_t slice) {
                 collect(least_at, s.m, [](int, float) { return true; });
                 __syncthreads();
                 pooled = count;
-                listed = pooled <= kList;
+                listed = pooled <= kListAll;
                 return;
             }
             u64 total = 0;
-            bool again = about > kList - kThreads;
+            bool again = about > kListAll;
             if (!again) {
-                // few enough to be in the list, all that stay (a list's weights are below 2^54, eight marks below 2^64)
+                // few enough to be taken from the list, all that stay (a list's weights are below 2^54, eight marks below 2^64)
                 constexpr u64 kTooMany = 1ull << 60;
                 weigh_and_collect(from, to, std::false_type{}, total, above);
                 __syncthreads();
@@ -1176,7 +1177,9 @@ sample_kernel(const Sampling a, const int32_t slice) {
             w = weight(s, x);
             return stays(ordered_index(c), x) && w >= w_least;
         };
-        if (listed || (border_at > -INFINITY && pooled <= kList && w_least == 0 && !(k > 0 && k < V))) {
+        // (min-p lets all by that top-p does, the roundings of the weights included)
+        const bool all_pass = border_at > -INFINITY && weight(s, border_at) >= w_least + (w_least >> 18);
+        if (listed || (all_pass && pooled <= kList && !(k > 0 && k < V))) {
             // what lies above the candidates was summed up with them, unless they are in the list, too; of those, what
             // stays, to the warps that have it
             if (tid < kWarps) more[tid] = 0;
