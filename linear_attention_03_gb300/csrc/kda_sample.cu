@@ -1306,10 +1306,13 @@ sample_kernel(const Sampling a, const int32_t slice) {
 #pragma unroll
                 for (int e = 0; e < VEC / 2; ++e) {
                     const float2 w = weights2<true>(deep, x[e]);
-                    if (x[e].x >= from && stays(e0 + 2 * e, x[e].x) && (w_least == 0 || weight(s, x[e].x) >= w_least))
-                        y[2 * e] = w.x * inv;
-                    if (x[e].y >= from && stays(e0 + 2 * e + 1, x[e].y) && (w_least == 0 || weight(s, x[e].y) >= w_least))
-                        y[2 * e + 1] = w.y * inv;
+                    y[2 * e] = (x[e].x >= from) & stays(e0 + 2 * e, x[e].x) ? w.x * inv : 0.f;
+                    y[2 * e + 1] = (x[e].y >= from) & stays(e0 + 2 * e + 1, x[e].y) ? w.y * inv : 0.f;
+                }
+                if (w_least != 0) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e)
+                        if (weight(s, e & 1 ? x[e / 2].y : x[e / 2].x) < w_least) y[e] = 0.f;
                 }
             }
             if (bf16) {
