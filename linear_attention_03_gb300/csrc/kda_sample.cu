@@ -704,9 +704,10 @@ sample_kernel(const Sampling a, const int32_t slice) {
     // Where top-p's border is, to a bin or two of log2 w, four times as narrow as the others: a value above all
     // candidates and one below.  A bin's weights lie within 2^(1/48) of each other, so it adds them up relative to
     // its own upper end, in whole multiples of 2^-fine, which 32 bits hold for all elements of a copy (a
-    // quarter of the warps).  The estimates are off by less than 2^-fine and 2^-17 of the sum (2^-24 of log w, 30
-    // at most, three times) and 2^18 units of 2^-42; `slack` is more than twice that on either side.  Returns
-    // about how many elements of the row reach `from`.
+    // quarter of the warps).  A sum of bins is off by less than 2^-fine and 2^-17 of it (2^-24 of log w, 30 at
+    // most, three times) and 2^18 units of 2^-42, the sum of those above the border as well as of those below: the
+    // lesser error counts, and `slack` is more than twice that.  Returns about how many elements of the row reach
+    // `from`.
     auto candidates = [&](float &from, float &to) {
         const int fine = min(17, __clz(kWarps / kCopies * per_warp * VEC) - 1);
         const float by4 = 4.f * by, unit = __int_as_float((127 + fine) << 23);
@@ -768,12 +769,13 @@ sample_kernel(const Sampling a, const int32_t slice) {
             bins[e] = __float2ull_rz(of_4[e] * exp2f((float)(42 - fine) - (float)(4 * tid + e) * (0.25f / kPerOctave)));
             mine_w += bins[e];
         }
-        u64 slack = 0, run = 0, goal = 0;
+        u64 run = 0, goal = 0, twice = 0;
         border(mine_w, 0, [&](u64 total) {
-            slack = (total >> (fine - 3)) + (1 << 20);
             goal = share(total);
+            twice = 2 * total;
             return goal;
         }, &run);
+        auto slack = [&](u64 up_to) { return (min(up_to + goal, twice - up_to - goal) >> (fine - 2)) + (1 << 20); };
         // the first bin with which the sum may reach the goal, and the first with which it must
         if (tid == 0) {
             found_bin = 0;
@@ -784,8 +786,8 @@ sample_kernel(const Sampling a, const int32_t slice) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const u64 next = run + bins[e];
-            if (next + slack >= goal && run + slack < goal) found_bin = 4 * tid + e;
-            if (next >= goal + slack && run < goal + slack) found_last = 4 * tid + e;
+            if (next + slack(next) >= goal && run + slack(run) < goal) found_bin = 4 * tid + e;
+            if (next >= goal + slack(next) && run < goal + slack(run)) found_last = 4 * tid + e;
             run = next;
         }
         __syncthreads();
@@ -807,6 +809,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
     u64 ahead_w = 0;
     int pooled = 0;
     bool listed = false;                        // the list holds all that stays
+    bool summed = true;                         // ahead_w holds what is above the list's
     const u64 w_least = least > 0.f ? (u64)(fminf(least, 1.f) * 0x1p42f) : 0;
     // a value below all whose weight reaches min-p's, with room for roundings
     float least_at = w_least > 0 ? s.m + (log2f(fminf(least, 1.f)) * (1.f + 1e-5f) - 1e-6f) / s.c : -INFINITY;
@@ -910,6 +913,16 @@ sample_kernel(const Sampling a, const int32_t slice) {
             most -= (uint32_t)found_bin << shift;
             if (shift == Vec<Tin>::GRAIN) break;
             lowest = max(lowest, most - ((1u << shift) - 1));
+            if (pooled > kList) {
+                // what is left may fit
+                __syncthreads();
+                if (tid == 0) count = 0;
+                __syncthreads();
+                collect(value_of(lowest), value_of(most), in_bin);
+                __syncthreads();
+                pooled = count;
+                summed = false;
+            }
         }
         if (Vec<Tin>::GRAIN > 0) {
             // the one key in (most - 2^GRAIN, most]: negative values' keys end in ones
@@ -1179,7 +1192,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
         };
         // (min-p lets all by that top-p does, the roundings of the weights included)
         const bool all_pass = border_at > -INFINITY && weight(s, border_at) >= w_least + (w_least >> 18);
-        if (listed || (all_pass && pooled <= kList && !(k > 0 && k < V))) {
+        if (listed || (all_pass && summed && pooled <= kList && !(k > 0 && k < V))) {
             // what lies above the candidates was summed up with them, unless they are in the list, too; of those, what
             // stays, to the warps that have it
             if (tid < kWarps) more[tid] = 0;
@@ -1330,7 +1343,10 @@ sample_kernel(const Sampling a, const int32_t slice) {
                 }
             } else {
                 float *to = reinterpret_cast<float *>(out) + e0;
-                if (whole && e0 >= 0 && e0 + VEC <= V) {
+                if (VEC == 8 && (reinterpret_cast<uintptr_t>(to) & 31) == 0 && e0 >= 0 && e0 + VEC <= V) {
+                    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "f"(y[0]), "f"(y[1]),
+                                 "f"(y[2]), "f"(y[3]), "f"(y[4 % VEC]), "f"(y[5 % VEC]), "f"(y[6 % VEC]), "f"(y[7 % VEC]) : "memory");
+                } else if (whole && e0 >= 0 && e0 + VEC <= V) {
 #pragma unroll
                     for (int e = 0; e < VEC; e += 4)
                         *reinterpret_cast<float4 *>(to + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
