@@ -130,10 +130,10 @@ struct Scale {
 };
 
 // The weights of two logits: the product of x - m with c in one rounding behind the point, 2^f by its series (to
-// 2^-27 for |f| <= 1/2) and the exponent put on in whole numbers, in paired arithmetic.  WHOLE: x - m with
-// its rounding error, so to 2^-24; otherwise to that and 2^-25 of log w, with errors of either sign (none for bf16
-// logits of like size).  (No number of meaning below s.least.)
-template <bool WHOLE = false> __device__ __forceinline__ float2 weights2(const Scale &s, float2 x) {
+// 2^-27 for |f| <= 1/2) and the exponent put on in whole numbers, in paired arithmetic.  WHOLE: with the rounding
+// error of x - m, which bf16 logits have only where one is 2^16 times the other (then 2^-24 of log w).  (No number
+// of meaning below s.least.)
+template <bool WHOLE> __device__ __forceinline__ float2 weights2(const Scale &s, float2 x) {
     auto both = [](float a) { return make_float2(a, a); };
     const float2 d = tc::f2sub(x, both(s.m));
     const float2 t = tc::f2fma(d, both(s.c), both(12582912.f)), whole = tc::f2sub(both(12582912.f), t);
@@ -175,8 +175,8 @@ __device__ __forceinline__ u64 fixed42(float w) {
     digits42(make_float2(w, w), hi, lo);
     return ((u64)digit(hi.x) << 21) + digit(lo.x);
 }
-__device__ __forceinline__ u64 weight(const Scale &s, float x) {
-    const float w = weights2(s, make_float2(x, x)).x;
+template <bool WHOLE> __device__ __forceinline__ u64 weight_of(const Scale &s, float x) {
+    const float w = weights2<WHOLE>(s, make_float2(x, x)).x;
     return fixed42(x >= s.least ? w : 0.f);
 }
 
@@ -239,6 +239,7 @@ template <typename Tin>
 __global__ void __launch_bounds__(kThreads, 2)
 sample_kernel(const Sampling a, const int32_t slice) {
     constexpr int VEC = Vec<Tin>::N;
+    constexpr bool WHOLE = sizeof(Tin) == 4;
     extern __shared__ __align__(16) unsigned char smem[];
     // two histograms (low words, then high words) and a list
     uint32_t *const hists = reinterpret_cast<uint32_t *>(smem), *hist = hists;
@@ -380,6 +381,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
     s.cl = s.c < 5e36f && s.c > 1e-36f ? (fmaf(-s.c, T, 1.44269502f) + 1.92596303e-8f) / T : 0.f;
     if (!(fabsf(s.cl) < 1e30f)) s.cl = 0.f;
     s.least = fmaxf(s.m - 44.f / s.c, -3.402823466e38f);
+    auto weight = [&](float x) { return weight_of<WHOLE>(s, x); };
     // bins of equal width in log2 w; the last one takes everything below
     const float by = s.c * kPerOctave;
     // (the whole part of the product is in the significand's low bits, as in digits42)
@@ -489,7 +491,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
 #pragma unroll
         for (int e = 0; e < VEC / 2; ++e) {
             float2 high, low;
-            digits42(weights2(s, x[e]), high, low);
+            digits42(weights2<WHOLE>(s, x[e]), high, low);
             const uint32_t h0 = digit(high.x), h1 = digit(high.y), l0 = digit(low.x), l1 = digit(low.y);
             const bool on0 = (x[e].x >= from) & which(i + 2 * e, x[e].x, h0, l0);
             const bool on1 = (x[e].y >= from) & which(i + 2 * e + 1, x[e].y, h1, l1);
@@ -514,7 +516,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
             Vec<Tin>::unpack(y, x);
 #pragma unroll
             for (int e = 0; e < VEC / 2; ++e) {
-                float2 w = weights2(s, x[e]), high, low;
+                float2 w = weights2<WHOLE>(s, x[e]), high, low;
                 w.x = x[e].x >= s.least ? w.x : 0.f;
                 w.y = x[e].y >= s.least ? w.y : 0.f;
                 digits42(w, high, low);
@@ -846,7 +848,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
                 above = count > kList ? kTooMany : 0;
                 for (int i = tid; i < have; i += kThreads) {
                     const float x = value_of(ordered_key(list[i]));
-                    above += x > to ? weight(s, x) : 0;
+                    above += x > to ? weight(x) : 0;
                 }
                 cluster_totals(total, above);
                 again = above >= kTooMany;
@@ -869,7 +871,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
             each_in(lowest_value(), s.m, [&](int i, float x) {
                 if (!stays(i, x)) return;
                 if (by_weight) {
-                    const u64 w = weight(s, x);
+                    const u64 w = weight(x);
                     if (w != 0) add_weight(bin_of(x), (uint32_t)(w >> 21), (uint32_t)w & 0x1fffffu);
                 } else {
                     atomicAdd(&hist[bin_of(x)], 1u);
@@ -892,7 +894,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
             auto add = [&](uint32_t key) {
                 const int b = (int)((most - key) >> shift);
                 if (by_weight) {
-                    const u64 w = weight(s, value_of(key));
+                    const u64 w = weight(value_of(key));
                     if (w != 0) add_weight(b, (uint32_t)(w >> 21), (uint32_t)w & 0x1fffffu);
                 } else {
                     atomicAdd(&hist[b], 1u);
@@ -931,7 +933,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
         }
         // the values equal to the border's: the first of them by their index
         const float it = value_of(most);
-        const u64 one = by_weight ? weight(s, it) : 1, keep = (want - above + one - 1) / one;
+        const u64 one = by_weight ? weight(it) : 1, keep = (want - above + one - 1) / one;
         int32_t until = kAll;
         if (found[1] > one) {                   // (where only one is there, it stays)
             u64 equal = 0;
@@ -1048,7 +1050,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
                 // Every pair is compared, four threads to an element: which stand before it in the order, and
                 // what they weigh; then what those weigh that stay and have a smaller index.
                 u64 *const weights = list + kFew;
-                for (int i = tid; i < all; i += kThreads) weights[i] = weight(s, value_of(ordered_key(list[i])));
+                for (int i = tid; i < all; i += kThreads) weights[i] = weight(value_of(ordered_key(list[i])));
                 __syncthreads();
                 const int i = tid >> 2, h = tid & 3;
                 const u64 mine_c = i < all ? list[i] : 0, mine_w = i < all ? weights[i] : 0;
@@ -1119,7 +1121,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
                     for (int e = 0; e < 4; ++e) cum[e] += add;
                     return all_of_it;
                 };
-                auto weight_of = [&](u64 x) { return weight(s, value_of(ordered_key(x))); };
+                auto weight_at = [&](u64 x) { return weight(value_of(ordered_key(x))); };
 #pragma unroll
                 for (int e = 0; e < 4; ++e) c[e] = 4 * tid + e < all ? list[4 * tid + e] : 0;
                 __syncthreads();
@@ -1127,7 +1129,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
                 while (size < all) size *= 2;
                 sort_down(c, list, size);
                 const int first_k = min(k, all);
-                const u64 of_k = scan([&](u64 x, int i) { return i < first_k ? weight_of(x) : 0; });
+                const u64 of_k = scan([&](u64 x, int i) { return i < first_k ? weight_at(x) : 0; });
                 const u64 goal = p < 1.f ? share(of_k) : ~(u64)0;
                 int stay = 0;
 #pragma unroll
@@ -1187,11 +1189,11 @@ sample_kernel(const Sampling a, const int32_t slice) {
         const float from = fmaxf(fmaxf(lowest_value(), s.least), least_at);
         auto in_list = [&](u64 c, u64 &w) {     // does it stay, and its weight
             const float x = value_of(ordered_key(c));
-            w = weight(s, x);
+            w = weight(x);
             return stays(ordered_index(c), x) && w >= w_least;
         };
         // (min-p lets all by that top-p does, the roundings of the weights included)
-        const bool all_pass = border_at > -INFINITY && weight(s, border_at) >= w_least + (w_least >> 18);
+        const bool all_pass = border_at > -INFINITY && weight(border_at) >= w_least + (w_least >> 18);
         if (listed || (all_pass && summed && pooled <= kList && !(k > 0 && k < V))) {
             // what lies above the candidates was summed up with them, unless they are in the list, too; of those, what
             // stays, to the warps that have it
@@ -1210,7 +1212,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
                 Vec<Tin>::unpack(y, x);
 #pragma unroll
                 for (int e = 0; e < VEC / 2; ++e) {
-                    float2 w = weights2(s, x[e]), high, low;
+                    float2 w = weights2<WHOLE>(s, x[e]), high, low;
                     w.x = x[e].x >= from ? w.x : 0.f;
                     w.y = x[e].y >= from ? w.y : 0.f;
                     digits42(w, high, low);
@@ -1283,7 +1285,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
                             int i = index_of(v);
                             for (int e = 0; e < VEC - 1; ++e, ++i) {
                                 const float z = Vec<Tin>::pick(y, e);
-                                const u64 w = z >= from && stays(i, z) ? weight(s, z) : 0;
+                                const u64 w = z >= from && stays(i, z) ? weight(z) : 0;
                                 at += w >= w_least ? w : 0;
                                 if (at > need) break;
                             }
@@ -1325,7 +1327,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
                 if (w_least != 0) {
 #pragma unroll
                     for (int e = 0; e < VEC; ++e)
-                        if (weight(s, e & 1 ? x[e / 2].y : x[e / 2].x) < w_least) y[e] = 0.f;
+                        if (weight(e & 1 ? x[e / 2].y : x[e / 2].x) < w_least) y[e] = 0.f;
                 }
             }
             if (bf16) {

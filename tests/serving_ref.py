@@ -76,9 +76,9 @@ def prefix_inputs(N, M, H, Hkv, d, page, lens, plens, seqs, dtype, rng):
     return x
 
 
-def sample_row(x, u=None, T=1.0, k=0, p=1.0, m=0.0, tol=0.0):
+def sample_row(x, u=None, T=1.0, k=0, p=1.0, m=0.0, tol=0.0, first=None):
     """One row (float64 values of the logits): (token, probs), from the definition.  `tol` moves the
-    weight that top-p asks for, relative to it."""
+    weight that top-p asks for, relative to it; `first` is how many it leaves."""
     V = len(x)
     x = np.where(np.isnan(x), -np.inf, x)
     if np.isposinf(x).any():
@@ -98,7 +98,7 @@ def sample_row(x, u=None, T=1.0, k=0, p=1.0, m=0.0, tol=0.0):
         before = np.concatenate([[0.0], np.cumsum(mass)[:-1]])
         on = before < max(p, 0.0) * mass.sum() * (1 + tol)
         on[0] = True
-        order = order[on]
+        order = order[on] if first is None else order[:first]
     if m > 0:
         order = order[w[order] >= min(m, 1.0)]
     probs[order] = w[order]

@@ -38,6 +38,14 @@ def check(kda, logits, u, T=None, k=None, p=None, m=None, probs_dtype=F32, what=
             t, want = ref.sample_row(x[n], **kw, tol=tol)
             if np.array_equal(want > 1e-37, got[n] > 1e-37):
                 break
+        else:
+            # The sums' errors put the border anywhere within 2^-22 of p times the weight, not at the ends of that
+            # range alone (with p = 1 - 2^-24 it holds the last thousand of a row's tokens).
+            if kw["p"] < 1 and kw["m"] <= 0:
+                kept = int((got[n] > 1e-37).sum())
+                few, many = (int((ref.sample_row(x[n], **kw, tol=z)[1] > 1e-37).sum()) for z in (-TOL, TOL))
+                assert few <= kept <= many, (what, n, kw, few, kept, many)
+                t, want = ref.sample_row(x[n], **kw, first=kept)
         bound = TOL * want + (half_ulp_bf16(want) * 1.01 if probs_dtype == BF else 0.0) + 1e-37
         diff = np.abs(got[n] - want)
         assert (diff <= bound).all(), (what, n, kw, int((want > 0).sum()), int((got[n] > 0).sum()), float((diff - bound).max()))
@@ -152,6 +160,33 @@ def test_many_rows_and_large_vocabularies(kda, N, V, dtype):
     kw = dict(T=np.where(rng.random(N) < 0.1, 0.0, rng.uniform(0.5, 1.5, N)), k=rng.choice([0, 1, 40, 200, 1000, 5000], N),
               p=rng.uniform(0.5, 1.0, N), m=rng.uniform(0, 0.05, N))
     check(kda, x, uniform(N, 1), **kw)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("copies,V", [(1, 70001), (14, 40000)])
+def test_rows_that_fill_lists(kda, dtype, copies, V):
+    """Flat rows, few values, shares close to one: more candidates than the kernel lists, in few and in many CTAs."""
+    gen = torch.Generator(device="cuda").manual_seed(V)
+    scales = torch.tensor([1e-3, 0.05, 0.3, 1.0, 1.0, 1.0, 2.0, 3.0, 1.0, 1.0, 1.0, 1.0], device="cuda")
+    x = torch.randn(12, V, generator=gen, device="cuda") * scales[:, None]
+    x[8] = torch.randint(0, 3, (V,), generator=gen, device="cuda") * 0.5      # three values
+    x[9] = 0.25                                                               # one
+    x[10] = torch.where(torch.rand(V, generator=gen, device="cuda") < 0.5, x[10], -float("inf"))
+    x[11, V // 3] = 12.0                                                      # one far above the others
+    x = x.to(dtype).repeat(copies, 1)
+    N = len(x)
+    for i, kw in enumerate((dict(p=0.5), dict(p=0.9), dict(p=0.999), dict(p=0.99999), dict(p=1 - 2.0 ** -24), dict(p=1e-5),
+                            dict(p=0.7, m=0.05), dict(p=0.95, m=0.3), dict(p=0.6, m=1e-4), dict(m=0.2), dict(p=0.8, T=0.2),
+                            dict(p=0.8, T=5.0), dict(p=0.9, k=V - 9), dict(p=0.5, k=1025), dict(p=0.99, k=1024), dict(k=20000))):
+        check(kda, x[:12] if copies == 1 else x, uniform(N, i), **{a: np.full(N, b) for a, b in kw.items()}, what=str(kw))
+        if i == 0 and copies > 1:
+            # as many rows as fill the GPU, or one at a time: the same bits
+            u = torch.rand(N, generator=gen, device="cuda")
+            p = torch.full((N,), 0.9, device="cuda")
+            tok, probs = kda.kda_sample(x, u, top_p=p, want_probs=True)
+            for n in range(12):
+                t, q = kda.kda_sample(x[n:n + 1], u[n:n + 1], top_p=p[:1], want_probs=True)
+                assert int(t) == int(tok[n]) and torch.equal(q[0], probs[n]), n
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
