@@ -570,8 +570,9 @@ KDA_API kda_status kda_prefix_attention(const void *q, const void *k_new, const 
  *   token  the first index at which the weights that stay, added up in index order, exceed
  *          u times their sum;   probs  w_i / sum where i stays, else zero.
  *   logits [N, V] logits_dtype, from a row to the next `stride` elements (>= V); logits and
- *          probs may start at any element; -infinity
- *          and NaN are never drawn; beside +infinity all others count as -infinity
+ *          probs may start at any element and must not overlap (the logits are read more than
+ *          once); -infinity and NaN are never drawn; beside +infinity all others count as
+ *          -infinity
  *   temperature, top_p, min_p, uniforms [N] fp32, top_k [N] int32, device; each may be NULL:
  *          1, 1 (all), 0 (all), not needed without token, 0 (all).  A temperature that is not
  *          above zero keeps the first of the order alone; top_k <= 0 or >= V, top_p >= 1 (or

@@ -21,6 +21,13 @@
 // to bf16 for their product (2^-9 of each), maximum, sums and output sums are fp32, as
 // in the tree kernels.  Keys past the end are masked; the values' rows there are made
 // zeros before their product, since a weight of zero would not cancel a NaN.
+//
+// Measured (d = 128): 1,024 rows behind 16,384 keys, 8 cache heads of 8 query heads each, 340 us, 1,617 TFLOP/s
+// in the products (85% of a library product's rate); 256 rows of a cache head behind 65,001 keys, 54 us, 4.9 TB/s
+// of keys and values, where reading them takes 39.  128 keys of both row tiles take some 3,020 clocks, the
+// products alone 2,048: a tile's softmax (load, maximum, exponentials, store) is a chain that the other tile's
+// products do not fill.  Two warps to 16 rows in place of one thread to a row took 432 us against 420, the
+// maximum formed beside the exponentials 429 against 417, the first half of P V outside the turn 459 against 425.
 #include "kda_attention_tc.cuh"
 #include "kda_prefix_cut.cuh"
 
@@ -48,6 +55,7 @@ template <int D, int QT> struct Cfg {
 };
 static_assert(Cfg<128, 1>::SMEM <= 232448 && Cfg<128, 2>::SMEM <= 232448, "227 KB of shared memory");
 
+constexpr int kLoadRegs = 72, kSoftmaxRegs = 208;                 // of a thread, with two row tiles
 enum { W_TMEM = 0, W_ABORT, W_STATUS };
 
 struct Maps {
@@ -130,11 +138,11 @@ prefix_attention_tc_kernel(const __grid_constant__ Maps maps, const PrefixAttent
     auto valid_keys = [&](const Run &r, int t) { return min(kTile, r.len - t * kTile); };
     auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
 
-    // of the 384 x 168 registers that the block has, most to the softmax (425 -> 392 us for 1,024 rows
-    // behind 16,384 keys): 128 x 72 + 256 x 208
+    // of the 384 x 168 registers that the block has, most to the softmax (409 -> 392 us for 1,024 rows
+    // behind 16,384 keys)
     if (QT == 2) {
-        if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     }
     if (warp == 0) {
         // ---------------------------------------------------------------- loads
@@ -422,7 +430,8 @@ prefix_attention_tc_kernel(const __grid_constant__ Maps maps, const PrefixAttent
     wait_prerequisites();                                    // (the next kernel counts on the ones before this)
 }
 
-// One row tile where a prefix has no more rows on average: two make no better use of the keys then.
+// One row tile where a prefix has no more rows on average: the second would hold none, and cost its share of
+// the softmax, the ring's slots and the pieces' space.
 bool one_tile(int32_t N, int32_t M, int32_t P, int32_t H, int32_t H_kv) {
     return ((int64_t)N * M + P - 1) / P <= kTile / (H / H_kv);
 }
@@ -445,6 +454,18 @@ template <int D, int QT> cudaError_t run_tc(const PrefixAttention &a, void *work
     static std::atomic<uint64_t> smem_set{0};
     cudaError_t e = allow_dynamic_smem(prefix_attention_tc_kernel<D, QT>, C::SMEM, smem_set);
     if (e != cudaSuccess) return e;
+    if (QT == 2) {
+        // the split of the registers draws on what the block was launched with: never on less
+        static std::atomic<int> registers{0};
+        if (registers.load(std::memory_order_relaxed) == 0) {
+            cudaFuncAttributes at;
+            e = cudaFuncGetAttributes(&at, prefix_attention_tc_kernel<D, QT>);
+            if (e != cudaSuccess) return e;
+            registers.store(at.numRegs, std::memory_order_relaxed);
+        }
+        if (registers.load(std::memory_order_relaxed) * C::THREADS < 128 * kLoadRegs + 256 * kSoftmaxRegs)
+            return cudaErrorInvalidConfiguration;
+    }
     cudaLaunchAttribute overlap;
     overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     overlap.val.programmaticStreamSerializationAllowed = 1;

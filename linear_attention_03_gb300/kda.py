@@ -146,6 +146,14 @@ def _stream():
     return torch.cuda.current_stream().cuda_stream
 
 
+def _here(*tensors):
+    """The current device is the one that a call runs on: refuses tensors of another."""
+    at = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != at:
+            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is cuda:{at}")
+
+
 def _offsets(cu_seqlens, T, device):
     if cu_seqlens is None:
         return None, 1
@@ -692,6 +700,7 @@ def kda_head_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, 
             k_out_stride = _heads(k_out, "k_out", q.dtype, k.shape)
     elif k_out is not None:
         raise ValueError("k_out is given without k")
+    _here(q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
     st = lib.kda_head_norm_rope(_ptr(q), q_stride, _ptr(k), k_stride, _ptr(positions), _ptr(inv_freq),
                                 inv_freq.numel(), _ptr(q_weight), _ptr(k_weight), T, H_kv, dims_of(q),
                                 1 if interleaved else 0, float(eps), _ptr(q_out), q_out_stride, _ptr(k_out),
@@ -751,6 +760,8 @@ def kda_prefix_attention(q, k_new, v_new, k_cache, v_cache, prefix_table, prefix
                                                                max_pages))
         workspace = torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device=q.device)
     _dev(workspace, "workspace", torch.uint8)
+    _here(q, k_new, v_new, k_cache, v_cache, prefix_table, prefix_lens, prefix_seqs, page_table, cache_lens, parent,
+          out, lse, workspace)
     st = lib.kda_prefix_attention(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
                                   _ptr(prefix_table), _ptr(prefix_lens), _ptr(prefix_seqs), _ptr(page_table),
                                   _ptr(cache_lens), _ptr(parent), N, M, P, H_kv, num_pages, page_size,
@@ -792,6 +803,7 @@ def kda_sample(logits, uniforms=None, temperature=None, top_k=None, top_p=None, 
         probs = torch.empty((N, V), dtype=f32, device=dev)
     if probs is not None:
         _dev(probs, "probs", None, (N, V))
+    _here(logits, uniforms, temperature, top_k, top_p, min_p, token, probs)
     st = lib.kda_sample(_ptr(logits), logits.stride(0) if N > 1 else V, _ptr(temperature), _ptr(top_k), _ptr(top_p),
                         _ptr(min_p), _ptr(uniforms), N, V, code, KDA_F32 if probs is None else _dtype_code(probs),
                         _ptr(token), _ptr(probs), _stream())

@@ -3,6 +3,7 @@ reaches the GPU (no GPU)."""
 import ctypes
 
 import pytest
+import torch
 
 FAKE = 0x10000     # 16-byte aligned, never dereferenced: the checks fail first
 
@@ -75,3 +76,17 @@ def test_sample_argument_checks(kda, ptrs):
         assert call(**bad) == kda.KDA_ERR_INVALID, bad
     assert call(V=262145, s=262145) == kda.KDA_ERR_UNSUPPORTED and call(dt=2) == kda.KDA_ERR_UNSUPPORTED
     assert call(probs=p, pd=5) == kda.KDA_ERR_UNSUPPORTED
+
+
+def test_tensors_of_another_device_are_refused(kda, monkeypatch):
+    class On:
+        def __init__(self, device):
+            self.device = device
+
+        def get_device(self):
+            return self.device
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    kda._here(On(1), None, On(1))
+    with pytest.raises(ValueError, match="cuda:0"):
+        kda._here(On(1), None, On(0))
