@@ -254,7 +254,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
     // two histograms (low words, then high words) and a list
     uint32_t *const hists = reinterpret_cast<uint32_t *>(smem), *hist = hists;
     u64 *const list = reinterpret_cast<u64 *>(hists + kCopies * kFine);
-    __shared__ u64 part[kWarps], part_all, chosen_sum, totals[2][kMaxRanks], more[kWarps], more_totals[kMaxRanks];
+    __shared__ u64 part[kWarps], part_all, chosen_sum, totals[2][kMaxRanks], more[kWarps], more_totals[2][kMaxRanks];
     __shared__ u64 found[2];                    // what lies above the border's bin, what is in it
     __shared__ float tops[kMaxRanks], warp_top[kWarps];
     __shared__ int32_t found_bin, found_last, chosen_index, count, chosen_count;
@@ -632,14 +632,14 @@ sample_kernel(const Sampling a, const int32_t slice) {
             }
             if (lane < ranks) {                 // (the lower half's sums: ranks <= kWarps)
                 *cluster.map_shared_rank(&totals[turn][rank], lane) = x;
-                *cluster.map_shared_rank(&more_totals[rank], lane) = y;
+                *cluster.map_shared_rank(&more_totals[turn][rank], lane) = y;
             }
         }
         cluster.sync();
         x = y = 0;
         for (int r = 0; r < ranks; ++r) {
             x += totals[turn][r];
-            y += more_totals[r];
+            y += more_totals[turn][r];
         }
         turn ^= 1;
     };
@@ -850,12 +850,13 @@ sample_kernel(const Sampling a, const int32_t slice) {
             u64 total = 0;
             bool again = about > kListAll;
             if (!again) {
-                // few enough to be taken from the list, all that stay (a list's weights are below 2^54, eight marks below 2^64)
+                // few enough to be taken from the list, all that stay; one thread adds a mark where there are more (a
+                // list's weights are below 2^54, eight marks below 2^64)
                 constexpr u64 kTooMany = 1ull << 60;
                 weigh_and_collect(from, to, std::false_type{}, total, above);
                 __syncthreads();
                 const int have = min(count, kList);
-                above = count > kList ? kTooMany : 0;
+                above = tid == 0 && count > kList ? kTooMany : 0;
                 for (int i = tid; i < have; i += kThreads) {
                     const float x = value_of(ordered_key(list[i]));
                     above += x > to ? weight(x) : 0;

@@ -189,6 +189,15 @@ def test_rows_that_fill_lists(kda, dtype, copies, V):
                 assert int(t) == int(tok[n]) and torch.equal(q[0], probs[n]), n
 
 
+@pytest.mark.parametrize("V", [30000, 200000])
+def test_far_from_zero(kda, V):
+    """Logits whose distances are near their rounding: the bounds of a bin take in many more than the bin has."""
+    x = rows(6, V, F32, V, 0.3) + torch.tensor([1e4, 1e5, 1e6, -1e5, -1e6, 3e6], device="cuda")[:, None]
+    for i, kw in enumerate((dict(p=1e-6), dict(p=1e-3), dict(p=0.5), dict(p=1e-5, m=1e-3), dict(p=0.9, m=0.5), dict(k=30), dict(k=900),
+                            dict(k=9000, p=0.3), dict(m=0.9), dict(p=1e-6, T=0.1))):
+        check(kda, x, uniform(6, i), **{a: np.full(6, b) for a, b in kw.items()}, what=str(kw))
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_strided_rows_and_alignment(kda, dtype):
     """Rows of a wider tensor, at every alignment, whose other columns are never looked at."""
