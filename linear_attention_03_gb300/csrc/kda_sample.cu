@@ -51,6 +51,7 @@ constexpr int32_t kAll = 0x7fffffff;
 // histograms (two of kBins 64-bit sums in turn, or copies of one of kFine sums) and a list
 constexpr int kFine = 4 * kBins, kCopies = 4;   // of the first histogram of top-p
 constexpr int kSmem = kCopies * kFine * 4 + kList * 8;
+static_assert(2 * kThreads * 8 <= kCopies * kFine * 4, "a list and room to sort it");
 static_assert(4 * kFew == kThreads && 2 * kFew <= kList && kSorted <= kList, "threads to the elements of a list");
 static_assert(kListK <= kGroups * kThreads / 2, "largest ones enough to bound the k-th");
 static_assert(kBins == kThreads, "a thread per bin");
@@ -815,6 +816,50 @@ sample_kernel(const Sampling a, const int32_t slice) {
         return chosen_count - kThreads;
     };
 
+    // The block's sums up to each of a thread's four elements; returns all.
+    auto scan4 = [&](const u64 (&w)[4], u64 (&cum)[4]) {
+        u64 run = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            run += w[e];
+            cum[e] = run;
+        }
+        const u64 own = run;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const u64 z = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += z;
+        }
+        __syncthreads();
+        if (lane == 31) part[warp] = run;
+        u64 all;
+        const u64 add = parts_before(all) + run - own;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) cum[e] += add;
+        return all;
+    };
+    // The lengths of all CTAs' lists, one to a lane: `upto` is what the lists up to the lane's have, all is returned.
+    auto lengths = [&](int &length, int &upto) {
+        length = lane < ranks ? *cluster.map_shared_rank(&count, lane) : 0;
+        upto = length;
+#pragma unroll
+        for (int o = 1; o < kMaxRanks; o <<= 1) {
+            const int z = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += z;
+        }
+        return __shfl_sync(0xffffffffu, upto, kMaxRanks - 1);
+    };
+    // The lists one after another, warp r bringing rank r's.
+    auto bring = [&](u64 *to, int length, int upto) {
+        if (warp < ranks) {
+            const int c = __shfl_sync(0xffffffffu, length, warp), at = __shfl_sync(0xffffffffu, upto, warp) - c;
+            const u64 *from = cluster.map_shared_rank(list, warp);
+            if (to + at != from)
+                for (int i = lane; i < c; i += 32) to[at + i] = from[i];
+        }
+        __syncthreads();
+    };
+
     // Narrows the border down to the first elements of the order that reach a count (k) or a share of
     // the weight: first by bins of log2 w, then by the values' bits.  ahead_w: of top-p's weights, what the
     // thread has above the candidates.
@@ -877,6 +922,40 @@ sample_kernel(const Sampling a, const int32_t slice) {
             goal(total);
             most = key_of(to);
             lowest = key_of(from);
+            int length, upto;
+            const int all = lengths(length, upto);
+            if (all <= kThreads) {
+                // few candidates in all: sorted in one CTA (in the histograms' place; one row of 131,072 by top-p 52 -> 40
+                // us; for up to 2,048 of them the sort takes as long as the histograms, with the other CTAs waiting)
+                if (rank == 0) {
+                    u64 *const room = reinterpret_cast<u64 *>(hists), *const together = room + kThreads;
+                    bring(together, length, upto);
+                    u64 c[4], w[4], cum[4];
+                    int size = 2;
+                    while (size < all) size *= 2;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) c[e] = 4 * tid + e < all ? together[4 * tid + e] : 0;
+                    sort_down(c, room, size);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t key = ordered_key(c[e]);
+                        w[e] = 4 * tid + e < all && key <= most ? weight(value_of(key)) : 0;    // (others are above)
+                    }
+                    scan4(w, cum);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (above + cum[e] >= want && above + cum[e] - w[e] < want)
+                            for (int r = 0; r < ranks; ++r) {
+                                *cluster.map_shared_rank(&chosen_key, r) = ordered_key(c[e]);
+                                *cluster.map_shared_rank(&chosen_index, r) = ordered_index(c[e]);
+                            }
+                }
+                cluster.sync();
+                pooled = count;
+                border_at = value_of(chosen_key);
+                last = chosen_index;
+                return;
+            }
         } else {
             next_histogram();
             each_in(lowest_value(), s.m, [&](int i, float x) {
@@ -1033,23 +1112,12 @@ sample_kernel(const Sampling a, const int32_t slice) {
         collect_groups(from);
         cluster.sync();
         // the lists' lengths, a rank to a lane; warp r brings rank r's to the first CTA
-        const int length = lane < ranks ? *cluster.map_shared_rank(&count, lane) : 0;
-        int upto = length;
-#pragma unroll
-        for (int o = 1; o < kMaxRanks; o <<= 1) {
-            const int z = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += z;
-        }
-        const int all = __shfl_sync(0xffffffffu, upto, kMaxRanks - 1);
+        int length, upto;
+        const int all = lengths(length, upto);
         done = all <= kSorted;
         if (done && rank == 0) {
-            if (warp > 0 && warp < ranks) {
-                const int c = __shfl_sync(0xffffffffu, length, warp), at = __shfl_sync(0xffffffffu, upto, warp) - c;
-                const u64 *from_it = cluster.map_shared_rank(list, warp);
-                for (int i = lane; i < c; i += 32) list[at + i] = from_it[i];
-            }
             if (tid == 0) chosen_count = 0;
-            __syncthreads();
+            bring(list, length, upto);
             auto choose = [&](u64 c, u64 all_of_it) {           // c is the last of the order that stays
                 for (int r = 0; r < ranks; ++r) {
                     *cluster.map_shared_rank(&chosen_key, r) = ordered_key(c);
@@ -1109,30 +1177,6 @@ sample_kernel(const Sampling a, const int32_t slice) {
             } else {
                 // Sorted, four elements to a thread, and summed up in the order.
                 u64 c[4], w[4], cum[4];
-                // sums of f(c) up to each of the thread's elements
-                auto scan = [&](auto f) {
-                    u64 run = 0;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        w[e] = f(c[e], 4 * tid + e);
-                        run += w[e];
-                        cum[e] = run;
-                    }
-                    const u64 own = run;
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const u64 z = __shfl_up_sync(0xffffffffu, run, o);
-                        if (lane >= o) run += z;
-                    }
-                    __syncthreads();
-                    if (lane == 31) part[warp] = run;
-                    u64 all_of_it;
-                    const u64 add = parts_before(all_of_it) + run - own;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) cum[e] += add;
-                    return all_of_it;
-                };
-                auto weight_at = [&](u64 x) { return weight(value_of(ordered_key(x))); };
 #pragma unroll
                 for (int e = 0; e < 4; ++e) c[e] = 4 * tid + e < all ? list[4 * tid + e] : 0;
                 __syncthreads();
@@ -1140,7 +1184,9 @@ sample_kernel(const Sampling a, const int32_t slice) {
                 while (size < all) size *= 2;
                 sort_down(c, list, size);
                 const int first_k = min(k, all);
-                const u64 of_k = scan([&](u64 x, int i) { return i < first_k ? weight_at(x) : 0; });
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = 4 * tid + e < first_k ? weight(value_of(ordered_key(c[e]))) : 0;
+                const u64 of_k = scan4(w, cum);
                 const u64 goal = p < 1.f ? share(of_k) : ~(u64)0;
                 int stay = 0;
 #pragma unroll
