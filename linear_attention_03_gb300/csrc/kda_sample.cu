@@ -246,6 +246,19 @@ __device__ __forceinline__ void sort_down(u64 (&x)[4], u64 *room, int all) {
     }
 }
 
+// A vector at a row's end, from element e0 on; a call, since a dozen places have one.
+template <typename Tin> __device__ __noinline__ uint4 row_end(const Tin *row, int e0, int V) {
+    uint4 x;
+    Tin y[Vec<Tin>::N];
+#pragma unroll
+    for (int e = 0; e < Vec<Tin>::N; ++e) {
+        y[e] = static_cast<Tin>(-INFINITY);
+        if (e0 + e >= 0 && e0 + e < V) y[e] = row[e0 + e];
+    }
+    memcpy(&x, y, 16);
+    return x;
+}
+
 template <typename Tin>
 __global__ void __launch_bounds__(kThreads, 2)
 sample_kernel(const Sampling a, const int32_t slice) {
@@ -258,7 +271,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
     __shared__ u64 part[kWarps], part_all, chosen_sum, totals[2][kMaxRanks], more[kWarps], more_totals[2][kMaxRanks];
     __shared__ u64 found[2];                    // what lies above the border's bin, what is in it
     __shared__ float tops[kMaxRanks], warp_top[kWarps];
-    __shared__ int32_t found_bin, found_last, chosen_index, count, chosen_count;
+    __shared__ int32_t found_bin, found_last, reach_least, chosen_index, count, chosen_count;
     __shared__ uint32_t chosen_key;
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
     cluster.barrier_arrive();
@@ -288,18 +301,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
     const int whole0 = first == 0 && lead > 0 ? 1 : 0, whole1 = min(mine, (V + lead) / VEC - first);
     auto raw = [&](int v, int end) {
         if (v >= whole0 && v < min(end, whole1)) return __ldg(grid + v);
-        uint4 x = Vec<Tin>::nothing();
-        if (v < end) {                          // the row's ends
-            const int e0 = index_of(v);
-            Tin y[VEC];
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                y[e] = static_cast<Tin>(-INFINITY);
-                if (e0 + e >= 0 && e0 + e < V) y[e] = row[e0 + e];
-            }
-            memcpy(&x, y, 16);
-        }
-        return x;
+        return v < end ? row_end(row, index_of(v), V) : Vec<Tin>::nothing();
     };
     auto clean = [&](uint4 x) {
         x.x = Vec<Tin>::clean(x.x);
@@ -714,6 +716,10 @@ sample_kernel(const Sampling a, const int32_t slice) {
         return fminf(s.m, x + 4e-7f * (fabsf(s.m) + fabsf(x)) + 1e-37f);
     };
 
+    const u64 w_least = least > 0.f ? (u64)(fminf(least, 1.f) * 0x1p42f) : 0;
+    // a value below all whose weight reaches min-p's, with room for roundings
+    float least_at = w_least > 0 ? s.m + (log2f(fminf(least, 1.f)) * (1.f + 1e-5f) - 1e-6f) / s.c : -INFINITY;
+    least_at = fmaxf(least_at - 4e-7f * (fabsf(s.m) + fabsf(least_at)) - 1e-37f, -3.402823466e38f);
     // Where top-p's border is, to a bin or two of log2 w, four times as narrow as the others: a value above all
     // candidates and one below.  A bin's weights lie within 2^(1/48) of each other, so it adds them up relative to
     // its own upper end, in whole multiples of 2^-fine, which 32 bits hold for all elements of a copy (a
@@ -727,7 +733,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
         const uint32_t bins_at = tc::smem_u32(hists + warp % kCopies * kFine) - 4 * kBias;
 #pragma unroll
         for (int c = 0; c < kCopies; ++c) reinterpret_cast<uint4 *>(hists + c * kFine)[tid] = make_uint4(0u, 0u, 0u, 0u);
-        if (tid == 0) chosen_count = 0;
+        if (tid == 0) chosen_count = reach_least = 0;
         __syncthreads();
         each_vector(w0, w1, [&](int, const uint4 &y) {
             float2 x[VEC / 2];
@@ -807,11 +813,20 @@ sample_kernel(const Sampling a, const int32_t slice) {
         const int last_bin = found_last;
         to = above_bin(0.25f * (float)found_bin);
         from = last_bin == kFine - 1 ? -3.402823466e38f : below_bin(0.25f * (float)(last_bin + 1));
-        float about = 0.f;
+        // about how many reach `from`, and how many reach min-p's weight
+        const float least_bin = fminf((s.m - least_at) * by4, (float)kFine);
+        float about = 0.f, about_least = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) about += 4 * tid + e <= last_bin + 1 ? of_4[e] : 0.f;
+        for (int e = 0; e < 4; ++e) {
+            about += 4 * tid + e <= last_bin + 1 ? of_4[e] : 0.f;
+            about_least += (float)(4 * tid + e) <= least_bin ? of_4[e] : 0.f;
+        }
         const int of_warp = __reduce_add_sync(0xffffffffu, (int)(about * 1.03f / unit) + 1);
-        if (lane == 0) atomicAdd(&chosen_count, of_warp);
+        const int least_of_warp = __reduce_add_sync(0xffffffffu, (int)(about_least / unit));
+        if (lane == 0) {
+            atomicAdd(&chosen_count, of_warp);
+            atomicAdd(&reach_least, least_of_warp);
+        }
         __syncthreads();
         return chosen_count - kThreads;
     };
@@ -867,10 +882,6 @@ sample_kernel(const Sampling a, const int32_t slice) {
     int pooled = 0;
     bool listed = false;                        // the list holds all that stays
     bool summed = true;                         // ahead_w holds what is above the list's
-    const u64 w_least = least > 0.f ? (u64)(fminf(least, 1.f) * 0x1p42f) : 0;
-    // a value below all whose weight reaches min-p's, with room for roundings
-    float least_at = w_least > 0 ? s.m + (log2f(fminf(least, 1.f)) * (1.f + 1e-5f) - 1e-6f) / s.c : -INFINITY;
-    least_at = fmaxf(least_at - 4e-7f * (fabsf(s.m) + fabsf(least_at)) - 1e-37f, -3.402823466e38f);
     auto narrow = [&](bool by_weight) {
         u64 want = (u64)k, above = 0, before, here;
         int bin = -1;
@@ -886,10 +897,12 @@ sample_kernel(const Sampling a, const int32_t slice) {
             const int about = candidates(from, to);
             if (least_at > to) {
                 // min-p lets by less than top-p does
-                collect(least_at, s.m, [](int, float) { return true; });
-                __syncthreads();
-                pooled = count;
-                listed = pooled <= kListAll;
+                if (reach_least <= kListAll) {
+                    collect(least_at, s.m, [](int, float) { return true; });
+                    __syncthreads();
+                    pooled = count;
+                    listed = pooled <= kListAll;
+                }
                 return;
             }
             u64 total = 0;
