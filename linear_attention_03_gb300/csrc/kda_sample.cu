@@ -12,19 +12,19 @@
 //
 // A cluster of up to eight CTAs takes a row, as many as let all rows run at once: more would leave CTAs
 // waiting for the next wave (256 rows of 131,072 over clusters of two, 512 CTAs for 304 places, take 39 us in
-// place of 31 for the largest logit alone, 96 fp32 rows 88 in place of 59 by top-p).  The row is read from the
+// place of 31 for the largest logit alone, 96 fp32 rows 88 in place of 61 by top-p; one CTA to an SM takes 43).  The row is read from the
 // L2 or the L1 as often as it is needed; held in shared memory, its size left two CTAs to an SM and three
-// waves (121 us in place of 88 for 256 rows with settings of their own).  What stays is a
+// waves (121 us in place of 80 for 256 rows with settings of their own).  What stays is a
 // beginning of the order: a border value, and the last index among the logits equal to it.
 //   A small k: k of the largest logits of 2,048 groups bound the k-th largest from below; the few logits above the
 // bound, in groups that have one, go to one CTA, which makes the whole choice there, the draw included.
 //   top-p alone: a histogram of weights relative to their bin says to within a few bins where the border can
 // lie; one exact pass sums up all weights and those above the candidates, and lists the candidates.  Where
-// min-p keeps less than that, its few logits are listed instead, and no exact sum of the row is needed.
+// min-p keeps less than that no exact sum of the row is needed, and its logits are listed where they are few.
 //   A large k: histograms narrow the values down, first by w (bins of equal width in log2 w, which spread
 // the logits well whatever their scale), then by the value's bits.
 // Measured: 256 bf16 rows of 131,072 31 us (the largest logit) to 41 (k = 100), 74 (k = 1,000), 121 (top-p alone)
-// and 64 (no filter), where reading them once takes 10; 96 fp32 rows of 131,072 by top-p 59 us; one row of 50,257
+// and 64 (no filter), where reading them once takes 10; 96 fp32 rows of 131,072 by top-p 61 us; one row of 50,257
 // 14-26 us.  For a small k the chain of steps is the bound (20,000 clocks, four meetings of the cluster), for a
 // larger one the sort of up to 2,048 in one CTA; for top-p the instructions: some 30 an element in the
 // histogram's pass, 40 in the exact one.
