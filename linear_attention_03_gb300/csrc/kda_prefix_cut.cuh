@@ -188,13 +188,14 @@ struct PrefixShape {
 inline size_t prefix_place_bytes(int ctas) { return ((size_t)ctas * sizeof(PrefixPlace) + 255) / 256 * 256; }
 inline size_t prefix_part_bytes(int ctas, int slots, int D) { return (size_t)ctas * 2 * slots * (D + 2) * 4; }
 
-// Small blocks, four sums of two rows to a thread: a unit that is cut into many pieces has to be read
+// Small blocks, four sums of a row to a thread: a unit that is cut into many pieces has to be read
 // by many SMs at once, and a block's time is the latency of its few reads (17 us for 64 sequences behind
-// 65,001 tokens, whose 152 pieces are 20 MB; 24 us where three prefixes' pieces are).
-constexpr int kJoinThreads = 128, kJoinAtOnce = 2;
+// 65,001 tokens, whose 152 pieces are 20 MB; 24 us where three prefixes' pieces are).  Two rows to a thread, or more
+// rows to a block one after another, take the same to 2% longer for many units and longer for few.
+constexpr int kJoinThreads = 128;
 template <int D> constexpr int kJoinRows = kJoinThreads * 4 / D;        // rows at a time
 
-// Block (b, y), 0 < b < ctas: the cut between CTAs b - 1 and b, 2 kJoinRows rows of its unit, when
+// Block (b, y), 0 < b < ctas: the cut between CTAs b - 1 and b, kJoinRows rows of its unit, when
 // that is the unit's first cut.  Blocks (0, y): the status.  Block (ctas + n, y): sequence n's rows,
 // when no prefix reaches them: their own sums alone.
 template <typename Tout, int D, int KEYS, bool EXP2>
@@ -244,63 +245,44 @@ prefix_join_kernel(const PrefixAttention a, const PrefixShape sh) {
     // part i is CTA b - 1 + i's: its last segment for the first, its first one after that
     auto part_of = [&](int i) { return sh.part + (size_t)(2 * (b - 1 + i) + (i == 0 ? 1 : 0)) * slots * (D + 2); };
     const int c = tid % (D / 4) * 4;
-    int lr[kJoinAtOnce];
-    int64_t o_row[kJoinAtOnce];             // -1: none
-    float own_top[kJoinAtOnce], own_sum[kJoinAtOnce], top[kJoinAtOnce], sum[kJoinAtOnce];
-    float4 own[kJoinAtOnce], o[kJoinAtOnce];
-#pragma unroll
-    for (int y = 0; y < kJoinAtOnce; ++y) {
-        lr[y] = (blockIdx.y * kJoinAtOnce + y) * kJoinRows<D> + tid / (D / 4);
-        const int in_tile = lr[y] % sh.units.tile, row = row0 + lr[y] / sh.units.tile * sh.units.used + in_tile;
-        const bool real = lr[y] < slots && in_tile < sh.units.used && row < p.rows;
-        o_row[y] = real ? ((int64_t)p.seq0 * a.t.M + row / G) * a.t.H + h * G + row % G : -1;
-        own_top[y] = real ? a.t.rows.top[o_row[y]] : 0.f;
-        own_sum[y] = real ? a.t.rows.sum[o_row[y]] : -1.f;
-        top[y] = -INFINITY;
-        sum[y] = 0.f;
-        own[y] = o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (real) own[y] = *reinterpret_cast<const float4 *>(a.t.rows.o + o_row[y] * D + c);
-        else lr[y] = 0;
-    }
+    const int lr = blockIdx.y * kJoinRows<D> + tid / (D / 4);
+    const int in_tile = lr % sh.units.tile, row = row0 + lr / sh.units.tile * sh.units.used + in_tile;
+    if (lr >= slots || in_tile >= sh.units.used || row >= p.rows) return;
+    const int64_t o_row = ((int64_t)p.seq0 * a.t.M + row / G) * a.t.H + h * G + row % G;
+    const float own_top = a.t.rows.top[o_row], own_sum = a.t.rows.sum[o_row];
+    const float4 own = *reinterpret_cast<const float4 *>(a.t.rows.o + o_row * D + c);
+    float top = -INFINITY, sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i0 = 0; i0 < parts; i0 += 4) {
-        // four parts of two rows at a time, so that their reads are under way together
-        float x[kJoinAtOnce][4], z[kJoinAtOnce][4];
-        float4 v[kJoinAtOnce][4];
+        // four parts at a time, so that their reads are under way together
+        float x[4], z[4];
+        float4 v[4];
 #pragma unroll
-        for (int y = 0; y < kJoinAtOnce; ++y)
+        for (int i = 0; i < 4; ++i) {
+            const float *q = part_of(min(i0 + i, parts - 1));
+            x[i] = i0 + i < parts ? q[(size_t)slots * D + lr] : -INFINITY;
+            z[i] = q[(size_t)slots * D + slots + lr];
+            v[i] = *reinterpret_cast<const float4 *>(q + (size_t)lr * D + c);
+        }
+        const float was = top;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float *q = part_of(min(i0 + i, parts - 1));
-                x[y][i] = i0 + i < parts ? q[(size_t)slots * D + lr[y]] : -INFINITY;
-                z[y][i] = q[(size_t)slots * D + slots + lr[y]];
-                v[y][i] = *reinterpret_cast<const float4 *>(q + (size_t)lr[y] * D + c);
-            }
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, x[i]);
+        const float from = top == -INFINITY ? 0.f : top, shrink = EXP2 ? exp2f(was - from) : expf(was - from);
+        sum *= shrink;
+        o.x *= shrink; o.y *= shrink; o.z *= shrink; o.w *= shrink;
 #pragma unroll
-        for (int y = 0; y < kJoinAtOnce; ++y) {
-            const float was = top[y];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top[y] = fmaxf(top[y], x[y][i]);
-            const float from = top[y] == -INFINITY ? 0.f : top[y], shrink = EXP2 ? exp2f(was - from) : expf(was - from);
-            sum[y] *= shrink;
-            o[y].x *= shrink; o[y].y *= shrink; o[y].z *= shrink; o[y].w *= shrink;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (i0 + i < parts) {
-                    const float w = EXP2 ? exp2f(x[y][i] - from) : expf(x[y][i] - from);
-                    sum[y] += w * z[y][i];
-                    o[y].x += w * v[y][i].x; o[y].y += w * v[y][i].y;
-                    o[y].z += w * v[y][i].z; o[y].w += w * v[y][i].w;
-                }
+        for (int i = 0; i < 4; ++i) {
+            if (i0 + i < parts) {
+                const float w = EXP2 ? exp2f(x[i] - from) : expf(x[i] - from);
+                sum += w * z[i];
+                o.x += w * v[i].x; o.y += w * v[i].y;
+                o.z += w * v[i].z; o.w += w * v[i].w;
             }
         }
     }
-#pragma unroll
-    for (int y = 0; y < kJoinAtOnce; ++y) {
-        if (o_row[y] < 0) continue;
-        const RowJoin<EXP2> join(top[y], sum[y], own_top[y], own_sum[y]);
-        store_out4(out + o_row[y] * D + c, join(o[y], own[y]));
-        if (c == 0 && a.t.lse != nullptr) a.t.lse[o_row[y]] = join.lse;
-    }
+    const RowJoin<EXP2> join(top, sum, own_top, own_sum);
+    store_out4(out + o_row * D + c, join(o, own));
+    if (c == 0 && a.t.lse != nullptr) a.t.lse[o_row] = join.lse;
 }
 
 // Launched to overlap the kernel before it, whose results it waits for.
@@ -311,8 +293,7 @@ cudaError_t launch_prefix_join(const PrefixAttention &a, const PrefixShape &sh, 
     overlap.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)sh.ctas + a.t.N,
-                       (unsigned)((sh.units.tiles * sh.units.tile + kJoinAtOnce * kJoinRows<D> - 1) /
-                                  (kJoinAtOnce * kJoinRows<D>)));
+                       (unsigned)((sh.units.tiles * sh.units.tile + kJoinRows<D> - 1) / kJoinRows<D>));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cfg.attrs = &overlap;
