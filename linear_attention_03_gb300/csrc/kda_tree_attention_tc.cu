@@ -617,7 +617,9 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
 template <int D, int QT, bool SUMS>
 __global__ void __launch_bounds__(256)
 tree_attention_tc_join_kernel(const TreeAttention a, const Shape sh) {
-    constexpr int R = QT * kTile, ROWS = 16;
+    // parts at a time, so that their reads are under way together (SUMS: own keys behind a prefix, units of few
+    // tiles and so of few parts: three prefixes 267 us with eight, 264 with four)
+    constexpr int R = QT * kTile, ROWS = 16, AT = SUMS ? 4 : 8;
     const int b = blockIdx.x;
     const int G = a.H / a.H_kv;
     if (SUMS) launch_dependents();                   // the prefix's kernel, which waits before it takes the sums
@@ -642,12 +644,11 @@ tree_attention_tc_join_kernel(const TreeAttention a, const Shape sh) {
         float top = -INFINITY, sum = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         const bool none = part_of(parts - 1)[(size_t)R * D + R + lr] < 0.f;
-        for (int i0 = 0; i0 < parts; i0 += 8) {
-            // eight parts at a time, so that their reads are under way together
-            float x[8], z[8];
-            float4 y[8];
+        for (int i0 = 0; i0 < parts; i0 += AT) {
+            float x[AT], z[AT];
+            float4 y[AT];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < AT; ++i) {
                 const float *q = part_of(min(i0 + i, parts - 1));
                 x[i] = i0 + i < parts ? q[(size_t)R * D + lr] : -INFINITY;
                 z[i] = q[(size_t)R * D + R + lr];
@@ -655,12 +656,12 @@ tree_attention_tc_join_kernel(const TreeAttention a, const Shape sh) {
             }
             float was = top;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, x[i]);
+            for (int i = 0; i < AT; ++i) top = fmaxf(top, x[i]);
             const float from = top == -INFINITY ? 0.f : top, shrink = ex2(was - from);
             sum *= shrink;
             o.x *= shrink; o.y *= shrink; o.z *= shrink; o.w *= shrink;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < AT; ++i) {
                 // (a part with nothing seen adds zeros; one whose scores are no numbers has a maximum of
                 // -infinity too and makes the row one: a weight of zero skips nothing)
                 if (i0 + i < parts) {
