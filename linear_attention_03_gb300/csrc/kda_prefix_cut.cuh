@@ -189,8 +189,8 @@ inline size_t prefix_place_bytes(int ctas) { return ((size_t)ctas * sizeof(Prefi
 inline size_t prefix_part_bytes(int ctas, int slots, int D) { return (size_t)ctas * 2 * slots * (D + 2) * 4; }
 
 // Small blocks, four sums of a row to a thread: a unit that is cut into many pieces has to be read
-// by many SMs at once, and a block's time is the latency of its few reads (17 us for 64 sequences behind
-// 65,001 tokens, whose 152 pieces are 20 MB; 24 us where three prefixes' pieces are).  Two rows to a thread, or more
+// by many SMs at once, and a block's time is the latency of its few reads (15 us for 64 sequences behind
+// 65,001 tokens, whose 152 pieces are 20 MB; 23 us where three prefixes' pieces are).  Two rows to a thread, or more
 // rows to a block one after another, take the same to 2% longer for many units and longer for few.
 constexpr int kJoinThreads = 128;
 template <int D> constexpr int kJoinRows = kJoinThreads * 4 / D;        // rows at a time
