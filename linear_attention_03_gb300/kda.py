@@ -727,7 +727,8 @@ def kda_prefix_attention(q, k_new, v_new, k_cache, v_cache, prefix_table, prefix
     its pages and tokens, in the same pools as the sequences' own (page_table,
     cache_lens), which follow it.  The other arguments as kda_tree_attention; a
     page, a length or an offset out of range is reported in the workspace's
-    status word alone (kda_prefix_attention_workspace_size, kda_get_device_status)."""
+    status word alone (kda_prefix_attention_workspace_size, kda_get_device_status).
+    For few rows a third of the call is the making of out, lse and workspace."""
     rows, H, d = q.shape
     N, M = _tree(parent, rows)
     _dev(q, "q")
