@@ -726,7 +726,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
     // quarter of the warps).  A sum of bins is off by less than 2^-fine and 2^-17 of it (2^-24 of log w, 30 at
     // most, three times) and 2^18 units of 2^-42, the sum of those above the border as well as of those below: the
     // lesser error counts, and `slack` is more than twice that.  Returns about how many elements of the row reach
-    // `from`.
+    // `from`.  (Its copies lie where the two histograms in turn do: the cluster has come together since either was read.)
     auto candidates = [&](float &from, float &to) {
         const int fine = min(17, __clz(kWarps / kCopies * per_warp * VEC) - 1);
         const float by4 = 4.f * by, unit = __int_as_float((127 + fine) << 23);
@@ -981,7 +981,12 @@ sample_kernel(const Sampling a, const int32_t slice) {
                 }
             });
             cluster.sync();
-            if (!border(by_weight ? bin_sum(0) + (bin_sum(1) << 32) : bin_sum(0), 0, goal)) return;  // fewer: all stay
+            if (!border(by_weight ? bin_sum(0) + (bin_sum(1) << 32) : bin_sum(0), 0, goal)) {
+                // fewer: all stay.  No CTA leaves while another reads its bins: top-p's first histogram takes the place
+                // of both in turn
+                cluster.sync();
+                return;
+            }
             bin = found_bin;
             above = found[0];
             most = key_of(above_bin((float)bin));
@@ -1013,7 +1018,10 @@ sample_kernel(const Sampling a, const int32_t slice) {
             }
             cluster.sync();
             // (the candidates' values lie in that range, so they reach it)
-            if (!border(by_weight ? bin_sum(0) + (bin_sum(1) << 32) : bin_sum(0), above, [&](u64) { return want; })) return;
+            if (!border(by_weight ? bin_sum(0) + (bin_sum(1) << 32) : bin_sum(0), above, [&](u64) { return want; })) {
+                cluster.sync();
+                return;
+            }
             above = found[0];
             most -= (uint32_t)found_bin << shift;
             if (shift == Vec<Tin>::GRAIN) break;
