@@ -566,7 +566,7 @@ KDA_API kda_status kda_prefix_attention(const void *q, const void *k_new, const 
  *   top-k  the first k of the order stay;
  *   top-p  of these the shortest beginning whose weight is at least p times theirs (at
  *          least one);
- *   min-p  of these those with w_i >= m (the first always does);
+ *   min-p  of these those with w_i >= m, however small m is; above 1 it counts as 1 (the first always stays);
  *   token  the first index at which the weights that stay, added up in index order, exceed
  *          u times their sum;   probs  w_i / sum where i stays, else zero.
  *   logits [N, V] logits_dtype, from a row to the next `stride` elements (>= V); logits and

@@ -273,6 +273,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
     __shared__ float tops[kMaxRanks], warp_top[kWarps];
     __shared__ int32_t found_bin, found_last, reach_least, chosen_index, count, chosen_count;
     __shared__ uint32_t chosen_key;
+    __shared__ float2 least_log;                // T ln m, a number and what is left of it
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
     cluster.barrier_arrive();
     const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -294,6 +295,13 @@ sample_kernel(const Sampling a, const int32_t slice) {
     const float least = a.min_p != nullptr ? a.min_p[n] : 0.f;
     const float u = a.uniforms != nullptr ? a.uniforms[n] : 0.f;
     if (tid == 0) count = 0;
+    // min-p's border as a value, max x + T ln m: weights that are compared come in the wrong order where logits are a
+    // rounding apart, and their whole multiples know none below 2^-42.  In 64 bits by one thread of the block.
+    if (tid == kThreads - 1) {
+        const double x = isinf(T) ? -INFINITY : log((double)fminf(least, 1.f)) * (double)(T > 0.f ? T : 1.f);
+        least_log.x = least > 0.f && x > -3.402823466e38 ? (float)x : -INFINITY;
+        least_log.y = (float)(x - (double)least_log.x);
+    }
 
     // A vector of the row as it is (all -infinity from `end` on), and what it counts as: the row is read as often
     // as it is needed, from the L2 or the L1.
@@ -494,9 +502,8 @@ sample_kernel(const Sampling a, const int32_t slice) {
             }
         }
     };
-    // The weights of a vector's elements that are at least `from` and of which which(i, x, hi, lo) holds (hi, lo:
-    // the weight's digits), added to two digits of 21 bits (no thread has 1,024 elements).  No branches, so that
-    // a vector's weights are formed side by side.
+    // The weights of a vector's elements that are at least `from` and of which which(i, x) holds, added to two digits
+    // of 21 bits (no thread has 1,024 elements).  No branches, so that a vector's weights are formed side by side.
     auto add_weights = [&](const uint4 &y, int v, float from, auto which, uint32_t &hi, uint32_t &lo) {
         float2 x[VEC / 2];
         Vec<Tin>::unpack(y, x);
@@ -506,8 +513,8 @@ sample_kernel(const Sampling a, const int32_t slice) {
             float2 high, low;
             digits42(weights2<WHOLE>(s, x[e]), high, low);
             const uint32_t h0 = digit(high.x), h1 = digit(high.y), l0 = digit(low.x), l1 = digit(low.y);
-            const bool on0 = (x[e].x >= from) & which(i + 2 * e, x[e].x, h0, l0);
-            const bool on1 = (x[e].y >= from) & which(i + 2 * e + 1, x[e].y, h1, l1);
+            const bool on0 = (x[e].x >= from) & which(i + 2 * e, x[e].x);
+            const bool on1 = (x[e].y >= from) & which(i + 2 * e + 1, x[e].y);
             hi += (on0 ? h0 : 0) + (on1 ? h1 : 0);
             lo += (on0 ? l0 : 0) + (on1 ? l1 : 0);
         }
@@ -716,10 +723,12 @@ sample_kernel(const Sampling a, const int32_t slice) {
         return fminf(s.m, x + 4e-7f * (fabsf(s.m) + fabsf(x)) + 1e-37f);
     };
 
-    const u64 w_least = least > 0.f ? (u64)(fminf(least, 1.f) * 0x1p42f) : 0;
-    // a value below all whose weight reaches min-p's, with room for roundings
-    float least_at = w_least > 0 ? s.m + (log2f(fminf(least, 1.f)) * (1.f + 1e-5f) - 1e-6f) / s.c : -INFINITY;
-    least_at = fmaxf(least_at - 4e-7f * (fabsf(s.m) + fabsf(least_at)) - 1e-37f, -3.402823466e38f);
+    // min-p lets by the values from least_at on: the least number that is not below the sum (NaN where there is none)
+    float least_at;
+    {
+        const float b = least_log.x, sum = s.m + b, back = sum - s.m;
+        least_at = fmaxf(__fadd_ru(sum, (s.m - (sum - back)) + (b - back) + least_log.y), -3.402823466e38f);
+    }
     // Where top-p's border is, to a bin or two of log2 w, four times as narrow as the others: a value above all
     // candidates and one below.  A bin's weights lie within 2^(1/48) of each other, so it adds them up relative to
     // its own upper end, in whole multiples of 2^-fine, which 32 bits hold for all elements of a copy (a
@@ -1181,7 +1190,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
                 };
                 const bool of_k = i < all && place < k;
                 const u64 goal = p < 1.f ? share(block_sum(of_k ? mine_w : 0)) : ~(u64)0;
-                const bool stay = of_k && ahead < goal && (place == 0 || mine_w >= w_least);
+                const bool stay = of_k && ahead < goal && value_of(ordered_key(mine_c)) >= least_at;
                 __syncthreads();
                 if (i < all && h == 0) weights[i] = stay ? mine_w : 0;
                 if (stay && h == 0) atomicAdd(&chosen_count, 1);
@@ -1212,7 +1221,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
                 int stay = 0;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    stay += 4 * tid + e < first_k && cum[e] - w[e] < goal && (4 * tid + e == 0 || w[e] >= w_least) ? 1 : 0;
+                    stay += 4 * tid + e < first_k && cum[e] - w[e] < goal && value_of(ordered_key(c[e])) >= least_at ? 1 : 0;
                 stay = __reduce_add_sync(0xffffffffu, stay);
                 if (lane == 0 && stay != 0) atomicAdd(&chosen_count, stay);
                 __syncthreads();
@@ -1259,19 +1268,15 @@ sample_kernel(const Sampling a, const int32_t slice) {
         if (p < 1.f) narrow(true);
         // ---- the draw, in index order
         u64 before, here;
-        const uint32_t least_hi = (uint32_t)(w_least >> 21), least_lo = (uint32_t)w_least & 0x1fffffu;
-        auto counts = [&](int i, float x, uint32_t hi, uint32_t lo) {
-            return stays(i, x) & ((hi > least_hi) | ((hi == least_hi) & (lo >= least_lo)));
-        };
         u64 mine_w = 0;
         const float from = fmaxf(fmaxf(lowest_value(), s.least), least_at);
         auto in_list = [&](u64 c, u64 &w) {     // does it stay, and its weight
             const float x = value_of(ordered_key(c));
             w = weight(x);
-            return stays(ordered_index(c), x) && w >= w_least;
+            return stays(ordered_index(c), x) && x >= least_at;
         };
-        // (min-p lets all by that top-p does, the roundings of the weights included)
-        const bool all_pass = border_at > -INFINITY && weight(border_at) >= w_least + (w_least >> 18);
+        // (min-p lets all by that top-p does)
+        const bool all_pass = border_at > -INFINITY && border_at >= least_at;
         if (listed || (all_pass && summed && pooled <= kList && !(k > 0 && k < V))) {
             // what lies above the candidates was summed up with them, unless they are in the list, too; of those, what
             // stays, to the warps that have it
@@ -1283,7 +1288,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
             }
             __syncthreads();
             mine_w = ahead_w + (lane == 0 ? more[warp] : 0);
-        } else if (border_at == -INFINITY && w_least == 0) {
+        } else if (border_at == -INFINITY) {
             uint32_t hi = 0, lo = 0;
             each_above(w0, w1, from, [&](int, const uint4 &y) {
                 float2 x[VEC / 2];
@@ -1302,7 +1307,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
             });
             mine_w = ((u64)hi << 21) + lo;
         } else {
-            mine_w = weigh(w0, w1, from, counts);
+            mine_w = weigh(w0, w1, from, stays);
         }
         sum = cluster_sum(mine_w, before, here);
         const u64 need = drawn();
@@ -1338,7 +1343,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
             __syncthreads();
             const int v0 = min(mine, found_bin * per_warp), v1 = min(mine, v0 + per_warp);
             const int each = (v1 - v0 + kWarps - 1) / kWarps, a0 = min(v1, v0 + warp * each), a1 = min(v1, a0 + each);
-            u64 x = weigh(a0, a1, from, counts), run_all;
+            u64 x = weigh(a0, a1, from, stays), run_all;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
             if (lane == 0) part[warp] = x;
@@ -1348,7 +1353,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
                     const int v = b0 + lane;
                     uint32_t hi = 0, lo = 0;
                     const uint4 y = clean(raw(v, a1));
-                    add_weights(y, v, from, counts, hi, lo);
+                    add_weights(y, v, from, stays, hi, lo);
                     const u64 own = ((u64)hi << 21) + lo;
                     u64 run = own;
 #pragma unroll
@@ -1363,8 +1368,7 @@ sample_kernel(const Sampling a, const int32_t slice) {
                             int i = index_of(v);
                             for (int e = 0; e < VEC - 1; ++e, ++i) {
                                 const float z = Vec<Tin>::pick(y, e);
-                                const u64 w = z >= from && stays(i, z) ? weight(z) : 0;
-                                at += w >= w_least ? w : 0;
+                                at += z >= from && stays(i, z) ? weight(z) : 0;
                                 if (at > need) break;
                             }
                             a.token[n] = i;
@@ -1401,11 +1405,6 @@ sample_kernel(const Sampling a, const int32_t slice) {
                     const float2 w = weights2<true>(deep, x[e]);
                     y[2 * e] = (x[e].x >= from) & stays(e0 + 2 * e, x[e].x) ? w.x * inv : 0.f;
                     y[2 * e + 1] = (x[e].y >= from) & stays(e0 + 2 * e + 1, x[e].y) ? w.y * inv : 0.f;
-                }
-                if (w_least != 0) {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e)
-                        if (weight(e & 1 ? x[e / 2].y : x[e / 2].x) < w_least) y[e] = 0.f;
                 }
             }
             if (bf16) {
