@@ -516,7 +516,8 @@ KDA_API kda_status kda_cache_append(const void *k_new, const void *v_new, const 
  *       (then with the same stride)
  * k and k_out are NULL when H_kv = 0.  0 <= n_freq <= d / 2.  T = 0 launches nothing.
  * Angles are formed modulo one turn in integers: they are as good at position 2^31
- * as at 1.  The squares' sum is fp32: rows whose squares overflow it become zeros.
+ * as at 1.  The squares' sum is fp32: rows whose squares overflow it become zeros, but for NaN in
+ * an infinity's place and, turned, its partner's.
  */
 KDA_API kda_status kda_head_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                                       const int32_t *positions, const float *inv_freq, int32_t n_freq,
