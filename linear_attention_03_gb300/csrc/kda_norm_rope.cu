@@ -137,14 +137,15 @@ norm_rope_kernel(const NormRope a) {
                        : static_cast<const Tin *>(a.k) + token * a.k_stride + (int64_t)(r - a.H) * D;
     };
     uint4 raw[AT_ONCE][2 * WORDS];                              // as they lie: half the registers in bf16
+    // (by plain loads: in place the rows are written here, too, which the read-only path does not allow)
     auto load = [&](int first) {
 #pragma unroll
         for (int y = 0; y < AT_ONCE; ++y) {
             const uint4 *p = reinterpret_cast<const uint4 *>(source(min(first + y * ROWS + lane / LANES, end - 1)));
 #pragma unroll
             for (int i = 0; i < WORDS; ++i) {
-                raw[y][i] = __ldg(p + WORDS * g0 + i);
-                raw[y][WORDS + i] = __ldg(p + WORDS * g1 + i);
+                raw[y][i] = p[WORDS * g0 + i];
+                raw[y][WORDS + i] = p[WORDS * g1 + i];
             }
         }
     };
