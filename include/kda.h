@@ -414,7 +414,8 @@ KDA_API size_t kda_tree_attention_workspace_size(kda_dims dims, int32_t H_kv, in
  *          device status word, set by this call: KDA_DEVICE_BAD_PAGE,
  *          KDA_DEVICE_BAD_LENGTH and KDA_DEVICE_TIMEOUT (a bounded wait) are
  *          reported there (out and lse are then unspecified; no access leaves
- *          the buffers)
+ *          the buffers); of several findings the first of a wait that ran out,
+ *          offsets (kda_prefix_attention), a page, a length
  * Any page_size serves; bf16 with d = 64 or 128, pages of whole groups of eight
  * tokens and up to 128 query heads to a cache head takes the tcgen05 path.  It
  * rounds the weights to bf16 for their product with the values (2^-9 of each, the

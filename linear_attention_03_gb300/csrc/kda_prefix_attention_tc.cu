@@ -56,7 +56,7 @@ template <int D, int QT> struct Cfg {
 static_assert(Cfg<128, 1>::SMEM <= 232448 && Cfg<128, 2>::SMEM <= 232448, "227 KB of shared memory");
 
 constexpr int kLoadRegs = 72, kSoftmaxRegs = 208;                 // of a thread, with two row tiles
-enum { W_TMEM = 0, W_ABORT, W_STATUS };
+enum { W_TMEM = 0, W_ABORT, W_STATUS, W_PAGE };
 
 struct Maps {
     CUtensorMap q, k, v;
@@ -115,7 +115,7 @@ prefix_attention_tc_kernel(const __grid_constant__ Maps maps, const PrefixAttent
         mbar_init(q_free, QT);
         mbar_init(v_ready, 1);
         fence_mbar_init();
-        words[W_ABORT] = 0;
+        words[W_ABORT] = words[W_PAGE] = 0;
         words[W_STATUS] = place.status;
     }
     tc_fence_before();
@@ -123,15 +123,11 @@ prefix_attention_tc_kernel(const __grid_constant__ Maps maps, const PrefixAttent
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, words[W_TMEM], 0);
     bool ok = true;
-    auto flag = [&](uint32_t code) { atomicCAS(const_cast<uint32_t *>(&words[W_STATUS]), 0u, code); };
     // a bounded wait of a whole warp; once one gives up, the warp stops
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (ok && !__all_sync(0xffffffffu, mbar_try(bar, parity))) {
             ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
-            if (!ok) {
-                words[W_ABORT] = 1;
-                flag(KDA_DEVICE_TIMEOUT);
-            }
+            if (!ok) words[W_ABORT] = 1;
         }
         return ok;
     };
@@ -177,7 +173,7 @@ prefix_attention_tc_kernel(const __grid_constant__ Maps maps, const PrefixAttent
                     const int pos = t * kTile + lane * box;
                     const int page = table[pos / a.t.page_size];
                     if (page < 0 || page >= a.t.num_pages) {
-                        flag(KDA_DEVICE_BAD_PAGE);
+                        words[W_PAGE] = 1;
                         group = none;
                     } else {
                         group = (int32_t)((((int64_t)page * a.t.H_kv + h) * a.t.page_size + pos % a.t.page_size) / 8);
@@ -426,7 +422,9 @@ prefix_attention_tc_kernel(const __grid_constant__ Maps maps, const PrefixAttent
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-    if (tid == 0) left->status = (int32_t)words[W_STATUS];
+    if (tid == 0)
+        left->status = (int32_t)words[W_STATUS] | finding(words[W_ABORT] != 0 ? KDA_DEVICE_TIMEOUT : KDA_DEVICE_OK) |
+                       finding(words[W_PAGE] != 0 ? KDA_DEVICE_BAD_PAGE : KDA_DEVICE_OK);
     wait_prerequisites();                                    // (the next kernel counts on the ones before this)
 }
 

@@ -19,21 +19,21 @@ namespace kda {
 // Prefix p: sequences seq0 .. seq0 + seqs - 1, keys 0 .. len - 1; what is out of range counts as empty.
 struct Prefix {
     int32_t seq0, seqs, len;
-    int32_t status;
+    int32_t status;                 // findings
 };
 __device__ __forceinline__ Prefix prefix_at(const PrefixAttention &a, int p) {
     const int s0 = a.seqs[p], s1 = a.seqs[p + 1], len = a.lens[p];
     const int64_t room = (int64_t)a.max_pages * a.t.page_size;
-    Prefix x{0, 0, len, KDA_DEVICE_OK};
+    Prefix x{0, 0, len, 0};
     if (len < 0 || len > room) {
         x.len = len < 0 ? 0 : (int)room;
-        x.status = KDA_DEVICE_BAD_LENGTH;
+        x.status = finding(KDA_DEVICE_BAD_LENGTH);
     }
     if (s0 >= 0 && s1 >= s0 && s1 <= a.t.N) {
         x.seq0 = s0;
         x.seqs = s1 - s0;
     } else {
-        x.status = KDA_DEVICE_BAD_OFFSETS;
+        x.status |= finding(KDA_DEVICE_BAD_OFFSETS);
     }
     return x;
 }
@@ -49,7 +49,7 @@ struct PrefixPlace {
     int64_t total, start, unit0;    // tiles of the line, the piece's first one, where its unit starts
     int32_t p, r;                   // the prefix and the unit within it
     int32_t tiles, groups, seq0, rows, len;     // of the unit's prefix, as in PrefixRun: the join needs no table
-    int32_t status;
+    int32_t status;                 // findings
 };
 
 // A CTA's run through its piece.
@@ -86,13 +86,13 @@ template <int KEYS> struct PrefixRun {
 template <int KEYS>
 __device__ __forceinline__ PrefixPlace find_prefix_place(const PrefixAttention &a, const RowUnits &u, int ctas, int b) {
     const int lane = threadIdx.x & 31;
-    PrefixPlace out{0, 0, 0, 0, 0, 1, 1, 0, 0, 0, KDA_DEVICE_OK};
-    int32_t status = KDA_DEVICE_OK;
+    PrefixPlace out{0, 0, 0, 0, 0, 1, 1, 0, 0, 0, 0};
+    int32_t status = 0;
     PrefixRun<KEYS> it;
     auto one = [&](int p) -> int64_t {
         it.p = p;
         if (p >= a.P) return 0;
-        status = max(status, it.load(a, u));
+        status |= it.load(a, u);
         return it.line();
     };
     int64_t mine = 0;
@@ -103,7 +103,7 @@ __device__ __forceinline__ PrefixPlace find_prefix_place(const PrefixAttention &
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         out.total += sum;
     }
-    out.status = (int32_t)__reduce_max_sync(0xffffffffu, (unsigned)status);
+    out.status = (int32_t)__reduce_or_sync(0xffffffffu, (unsigned)status);
     out.start = out.unit0 = piece_start(out.total, ctas, b);
     int64_t base = 0;
     for (int p0 = 0; p0 < a.P; p0 += 32) {
@@ -206,15 +206,11 @@ prefix_join_kernel(const PrefixAttention a, const PrefixShape sh) {
     tc::wait_prerequisites();
     if (b == 0) {
         if (blockIdx.y != 0) return;
-        int32_t code = 0;
-        for (int i = tid; i < sh.ctas; i += kJoinThreads) code = max(code, sh.places[i].status);
-        const bool timeout = __syncthreads_or(code == KDA_DEVICE_TIMEOUT) != 0;
-        const bool offsets = __syncthreads_or(code == KDA_DEVICE_BAD_OFFSETS) != 0;
-        const bool page = __syncthreads_or(code == KDA_DEVICE_BAD_PAGE) != 0;
-        const bool length = __syncthreads_or(code == KDA_DEVICE_BAD_LENGTH) != 0;
-        if (tid == 0 && *a.t.status == KDA_DEVICE_OK)
-            *a.t.status = timeout ? KDA_DEVICE_TIMEOUT : offsets ? KDA_DEVICE_BAD_OFFSETS
-                          : page ? KDA_DEVICE_BAD_PAGE : length ? KDA_DEVICE_BAD_LENGTH : KDA_DEVICE_OK;
+        int32_t mine = 0;
+        for (int i = tid; i < sh.ctas; i += kJoinThreads) mine |= sh.places[i].status;
+        const int32_t all = all_findings(mine);
+        // (the word holds what was found with the sequences' own keys)
+        if (tid == 0 && all != 0) *a.t.status = reported(all | finding(*a.t.status));
         return;
     }
     if (b >= sh.ctas) {

@@ -285,7 +285,7 @@ tree_attention_kernel(const Args args, const typename std::conditional<std::is_s
                 if (page >= 0 && page < a.num_pages)
                     at = ((int64_t)page * a.H_kv + h) * a.page_size + place;
                 else
-                    s_status = KDA_DEVICE_BAD_PAGE;             // the key then counts as zeros
+                    atomicOr(&s_status, finding(KDA_DEVICE_BAD_PAGE));      // the key then counts as zeros
             }
             const Tin *pk = tree ? k_new : k_cache, *pv = tree ? v_new : v_cache;
             constexpr int RUN = 16 / (int)sizeof(Tin), CH = D / RUN;

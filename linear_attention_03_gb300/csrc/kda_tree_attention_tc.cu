@@ -80,13 +80,13 @@ template <int D, int QT> struct Cfg {
     static constexpr int NBARS = FULLS + SLOTS + (2 * BUFS + 6) * QT + 2 + 2 * RING;
     static constexpr int O_LINES = O_MISC + 8 * NBARS, O_WORDS = O_LINES + RING * 8 * kMaxTreeNodes;
     static constexpr int SMEM = O_MISC + (D == 64 ? 8192 : 3072);
-    static_assert(O_WORDS + 16 + 8 * RING <= SMEM, "misc");
+    static_assert(O_WORDS + 20 + 8 * RING <= SMEM, "misc");
     static constexpr int TM_O = 256;
 };
 static_assert(Cfg<128, 1>::SMEM <= 232448 && Cfg<128, 2>::SMEM <= 232448, "227 KB of shared memory");
 
 // misc: the mbarriers, the trees' lines, then these 32-bit words (two of W_BAD per segment of the ring)
-enum { W_TMEM = 0, W_ABORT, W_STATUS, W_BAD };
+enum { W_TMEM = 0, W_ABORT, W_STATUS, W_PAGE, W_BAD };
 
 struct Maps {
     CUtensorMap q, k, v, k8, v8, kn, vn;   // k8, v8: the cache in boxes of eight rows
@@ -190,7 +190,7 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
             mbar_init(l_ready(i), 1);
         }
         fence_mbar_init();
-        words[W_ABORT] = 0;
+        words[W_ABORT] = words[W_PAGE] = 0;
         words[W_STATUS] = place.status;
     }
     tc_fence_before();
@@ -198,15 +198,11 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, words[W_TMEM], 0);
     bool ok = true;
-    auto flag = [&](uint32_t code) { atomicCAS(const_cast<uint32_t *>(&words[W_STATUS]), 0u, code); };
     // a bounded wait of a whole warp; once one gives up, the warp stops
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (ok && !__all_sync(0xffffffffu, mbar_try(bar, parity))) {
             ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
-            if (!ok) {
-                words[W_ABORT] = 1;
-                flag(KDA_DEVICE_TIMEOUT);
-            }
+            if (!ok) words[W_ABORT] = 1;
         }
         return ok;
     };
@@ -230,7 +226,7 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
                     const int pos = t * kTile + lane * box;
                     const int page = table[pos / a.page_size];
                     if (page < 0 || page >= a.num_pages) {
-                        flag(KDA_DEVICE_BAD_PAGE);
+                        words[W_PAGE] = 1;
                         group = none;
                     } else {
                         group = (int32_t)((((int64_t)page * a.H_kv + h) * a.page_size + pos % a.page_size) / 8);
@@ -607,7 +603,9 @@ tree_attention_tc_kernel(const __grid_constant__ Maps maps, const TreeAttention 
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-    if (tid == 0) left->status = (int32_t)words[W_STATUS];
+    if (tid == 0)
+        left->status = (int32_t)words[W_STATUS] | finding(words[W_ABORT] != 0 ? KDA_DEVICE_TIMEOUT : KDA_DEVICE_OK) |
+                       finding(words[W_PAGE] != 0 ? KDA_DEVICE_BAD_PAGE : KDA_DEVICE_OK);
 }
 
 // Joins the units that were cut.  Block (b, y), b > 0: the cut between CTAs

@@ -13,6 +13,28 @@
 
 namespace kda {
 
+// What a CTA found, a bit for each code, so that none takes the place of another; and the code that the status
+// word reports of them: results that were not written, then what was not read, then what was cut.
+__host__ __device__ constexpr int32_t finding(int32_t code) { return code == KDA_DEVICE_OK ? 0 : 1 << code; }
+__host__ __device__ constexpr int32_t reported(int32_t findings) {
+    return (findings & finding(KDA_DEVICE_TIMEOUT)) != 0       ? KDA_DEVICE_TIMEOUT
+           : (findings & finding(KDA_DEVICE_BAD_OFFSETS)) != 0 ? KDA_DEVICE_BAD_OFFSETS
+           : (findings & finding(KDA_DEVICE_BAD_PAGE)) != 0    ? KDA_DEVICE_BAD_PAGE
+           : (findings & finding(KDA_DEVICE_BAD_LENGTH)) != 0  ? KDA_DEVICE_BAD_LENGTH
+                                                               : KDA_DEVICE_OK;
+}
+constexpr bool first_of(int32_t code, int32_t later) { return reported(finding(code) | finding(later)) == code; }
+static_assert(first_of(KDA_DEVICE_TIMEOUT, KDA_DEVICE_BAD_OFFSETS) && first_of(KDA_DEVICE_TIMEOUT, KDA_DEVICE_BAD_PAGE) &&
+              first_of(KDA_DEVICE_TIMEOUT, KDA_DEVICE_BAD_LENGTH) && reported(0) == KDA_DEVICE_OK,
+              "no finding hides a wait that ran out");
+// The findings of all of the block's threads.
+__device__ __forceinline__ int32_t all_findings(int32_t mine) {
+    int32_t all = 0;
+    for (const int32_t code : {KDA_DEVICE_TIMEOUT, KDA_DEVICE_BAD_OFFSETS, KDA_DEVICE_BAD_PAGE, KDA_DEVICE_BAD_LENGTH})
+        all |= __syncthreads_or(mine & finding(code)) != 0 ? finding(code) : 0;
+    return all;
+}
+
 __device__ __forceinline__ int clamped_len(const TreeAttention &a, int64_t n) {
     const int len = a.cache_lens[n];
     const int64_t room = (int64_t)a.max_pages * a.page_size;
@@ -42,7 +64,7 @@ __device__ __forceinline__ int first_past(int64_t total, int ctas, int64_t end) 
 struct Place {
     int64_t total, start, unit0;    // unit0: where the unit starts on the line
     int32_t n, r, len;              // sequence, unit within it, its clamped length
-    int32_t status;
+    int32_t status;                 // findings
 };
 
 // The whole block calls it; `buf` holds 34 int64 of shared memory.
@@ -64,7 +86,7 @@ __device__ void find_place(const TreeAttention &a, int groups, int ctas, int b, 
         const int raw = real ? a.cache_lens[lane] : 0, len = real ? clamped_len(a, lane) : 0;
         const int tiles = Units::tiles(len, a.M);
         const int64_t mine = real ? (int64_t)tiles * per_seq : 0, run = scan(mine), begin = run - mine;
-        out.status = __any_sync(0xffffffffu, raw != len) ? KDA_DEVICE_BAD_LENGTH : KDA_DEVICE_OK;
+        out.status = finding(__any_sync(0xffffffffu, raw != len) ? KDA_DEVICE_BAD_LENGTH : KDA_DEVICE_OK);
         out.total = __shfl_sync(0xffffffffu, run, 31);
         out.start = piece_start(out.total, ctas, b);
         const uint32_t here = __ballot_sync(0xffffffffu, mine > 0 && out.start >= begin && out.start < run);
@@ -87,7 +109,7 @@ __device__ void find_place(const TreeAttention &a, int groups, int ctas, int b, 
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) buf[warp] = sum;
-    out.status = __syncthreads_or(bad) != 0 ? KDA_DEVICE_BAD_LENGTH : KDA_DEVICE_OK;
+    out.status = finding(__syncthreads_or(bad) != 0 ? KDA_DEVICE_BAD_LENGTH : KDA_DEVICE_OK);
     int64_t total = 0;
     for (int w = 0; w < warps; ++w) total += buf[w];
     __syncthreads();
@@ -142,14 +164,10 @@ template <class Units> struct CutRun {
 
 // The block's threads: the status that the CTAs left.
 __device__ __forceinline__ void gather_status(const Place *places, int ctas, int32_t *status) {
-    int32_t code = 0;
-    for (int i = threadIdx.x; i < ctas; i += blockDim.x) code = max(code, places[i].status);
-    const bool timeout = __syncthreads_or(code == KDA_DEVICE_TIMEOUT) != 0;
-    const bool page = __syncthreads_or(code == KDA_DEVICE_BAD_PAGE) != 0;
-    const bool length = __syncthreads_or(code == KDA_DEVICE_BAD_LENGTH) != 0;
-    if (threadIdx.x == 0)
-        *status = timeout ? KDA_DEVICE_TIMEOUT : page ? KDA_DEVICE_BAD_PAGE
-                  : length ? KDA_DEVICE_BAD_LENGTH : KDA_DEVICE_OK;
+    int32_t mine = 0;
+    for (int i = threadIdx.x; i < ctas; i += blockDim.x) mine |= places[i].status;
+    const int32_t all = all_findings(mine);
+    if (threadIdx.x == 0) *status = reported(all);
 }
 
 inline int sm_count() {
