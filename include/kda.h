@@ -568,7 +568,8 @@ KDA_API kda_status kda_prefix_attention(const void *q, const void *k_new, const 
  *   top-k  the first k of the order stay;
  *   top-p  of these the shortest beginning whose weight is at least p times theirs (at
  *          least one);
- *   min-p  of these those with w_i >= m, however small m is; above 1 it counts as 1 (the first always stays);
+ *   min-p  of these those with w_i >= m, compared as x_i >= max x + T ln m, however small m is; above
+ *          1 it counts as 1 (the first always stays);
  *   token  the first index at which the weights that stay, added up in index order, exceed
  *          u times their sum;   probs  w_i / sum where i stays, else zero.
  *   logits [N, V] logits_dtype, from a row to the next `stride` elements (>= V); logits and
@@ -581,8 +582,9 @@ KDA_API kda_status kda_prefix_attention(const void *q, const void *k_new, const 
  *          NaN) and min_p <= 0 (or NaN) leave all.  uniforms in [0, 1), in steps of 2^-24.
  *   token  [N] int32 or NULL: -1 where a row allows nothing (its probs are zeros)
  *   probs  [N, V] probs_dtype, dense, or NULL; not both NULL.  kda_verify_drafts takes it.
- * Weights are summed as whole multiples of 2^-42: results do not depend on the order of any
- * sum.  A weight below 2^-43 is never drawn.  V <= KDA_MAX_VOCABULARY; N * 8 < 2^31.
+ * Weights are summed as whole multiples of 2^-42, cut toward zero: results do not depend on the
+ * order of any sum, and a weight below 2^-42 is never drawn (probs, where it stays, holds it
+ * down to 2^-125).  V <= KDA_MAX_VOCABULARY; N * 8 < 2^31.
  */
 KDA_API kda_status kda_sample(const void *logits, int64_t stride, const float *temperature,
                               const int32_t *top_k, const float *top_p, const float *min_p,

@@ -20,8 +20,10 @@
 // 2^31 for inv_freq <= 1, where an angle in fp32 is off by 0.016 rad at position 262,144.
 //
 // Measured (graphs of the call on two inputs): 32,388 tokens of 96 + 8 heads of 128
-// out of a projection, bf16, 1.72 GB: 276 us, 6.25 TB/s, 92% of a copy's rate (271 us
-// interleaved); 16,000 tokens in fp32 262 us, 6.5 TB/s; one token 4.2 us.  On the way
+// out of a projection, bf16, 1.72 GB: 274 us, 6.3 TB/s, 92% of a copy's rate (269 us
+// interleaved); 16,000 tokens in fp32 261 us, 6.5 TB/s; one token 4.2 us.  Half of the pairs
+// turned: 300 us in halves, 274 interleaved; 17 halves, whose partners go through shared
+// memory with bank conflicts (16 channels from lane to lane): 818 us, fp32 553.  On the way
 // (bf16): elements unpacked at their load 333 us, loaded as they lie 288, paired fp32
 // arithmetic 276.  Two rows per lane at three CTAs an SM: four CTAs (64 registers,
 // spills) take 337, three rows 317, four rows at two CTAs 280, one row at five 374; in

@@ -22,12 +22,13 @@
 // in the tree kernels.  Keys past the end are masked; the values' rows there are made
 // zeros before their product, since a weight of zero would not cancel a NaN.
 //
-// Measured (d = 128): 1,024 rows behind 16,384 keys, 8 cache heads of 8 query heads each, 340 us, 1,617 TFLOP/s
-// in the products (85% of a library product's rate); 256 rows of a cache head behind 65,001 keys, 54 us, 4.9 TB/s
-// of keys and values, where reading them takes 39.  128 keys of both row tiles take some 3,020 clocks, the
-// products alone 2,048: a tile's softmax (load, maximum, exponentials, store) is a chain that the other tile's
-// products do not fill.  Two warps to 16 rows in place of one thread to a row took 432 us against 420, the
-// maximum formed beside the exponentials 429 against 417, the first half of P V outside the turn 459 against 425.
+// Measured (d = 128, this kernel alone): 1,024 nodes behind 16,384 keys, 8 cache heads of 8 query heads, so 8,192 rows
+// to a cache head, 340 us, 1,617 TFLOP/s in the products (85% of a library product's rate; the whole call 395 us);
+// 256 rows to a cache head behind 65,001 keys, 54 us, 4.9 TB/s of keys and values, where reading them takes 39.
+// 128 keys of both row tiles take some 3,020 clocks, the products alone 2,048: a tile's softmax (load, maximum,
+// exponentials, store) is a chain that the other tile's products do not fill.  By the call of 1,024 nodes: two warps
+// to 16 rows in place of one thread to a row took 432 us against 420, the maximum formed beside the exponentials 429
+// against 417, the first half of P V outside the turn 459 against 425.
 #include "kda_attention_tc.cuh"
 #include "kda_prefix_cut.cuh"
 
@@ -134,7 +135,7 @@ prefix_attention_tc_kernel(const __grid_constant__ Maps maps, const PrefixAttent
     auto valid_keys = [&](const Run &r, int t) { return min(kTile, r.len - t * kTile); };
     auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
 
-    // of the 384 x 168 registers that the block has, most to the softmax (409 -> 392 us for 1,024 rows
+    // of the 384 x 168 registers that the block has, most to the softmax (409 -> 392 us for 1,024 nodes
     // behind 16,384 keys)
     if (QT == 2) {
         if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));

@@ -7,8 +7,9 @@
 //     weights of the ones that stay, added up in index order, exceed u times their sum
 //
 // Weights are whole multiples of 2^-42, held in 64 bits, so sums do not depend on their order, nor on how many
-// CTAs a row has.  Each is right to some 2^-24 of itself, with errors of either sign: the draw moves by a token
-// at fewer than one in 10^5 rows.
+// CTAs a row has.  Before it is cut to them a weight is right to some 2^-24 of itself; the cut takes up to 2^-42 off,
+// always downward: less than 2^-24 of a weight above 2^-18, all of one below 2^-42, and up to V 2^-42 of a sum.
+// Min-p needs no weights: its border is a value, max x + T ln m.
 //
 // A cluster of up to eight CTAs takes a row, as many as let all rows run at once: more would leave CTAs
 // waiting for the next wave (256 rows of 131,072 over clusters of two, 512 CTAs for 304 places, take 39 us in
@@ -23,11 +24,11 @@
 // min-p keeps less than that no exact sum of the row is needed, and its logits are listed where they are few.
 //   A large k: histograms narrow the values down, first by w (bins of equal width in log2 w, which spread
 // the logits well whatever their scale), then by the value's bits.
-// Measured: 256 bf16 rows of 131,072 31 us (the largest logit) to 41 (k = 100), 74 (k = 1,000), 121 (top-p alone)
-// and 64 (no filter), where reading them once takes 10; 96 fp32 rows of 131,072 by top-p 61 us; one row of 50,257
-// 14-26 us.  For a small k the chain of steps is the bound (20,000 clocks, four meetings of the cluster), for a
-// larger one the sort of up to 2,048 in one CTA; for top-p the instructions: some 30 an element in the
-// histogram's pass, 40 in the exact one.
+// Measured: 256 bf16 rows of 131,072 31 us (the largest logit) to 41 (k = 100), 72 (k = 1,000), 117 (top-p alone),
+// 250 (k = 5,000 and top-p) and 64 (no filter), where reading them once takes 10; 96 fp32 rows of 131,072 by top-p
+// 61 us; one row of 50,257 13-26 us.  For a small k the chain of steps is the bound (20,000 clocks, four meetings of
+// the cluster), for a larger one the sort of up to 2,048 in one CTA; for top-p the waits for the L2 and at barriers
+// beside the instructions: some 30 an element in the histogram's pass, 40 in the exact one, half of the issue slots.
 #include "kda_internal.cuh"
 #include "kda_tc.cuh"
 
