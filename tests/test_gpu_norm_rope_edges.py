@@ -31,3 +31,18 @@ def test_an_infinity_stays_in_its_pair(kda, n, pairs, dtype):
         for got in (f64(qo)[t, 1], f64(ko)[t, 0]):
             assert set(np.flatnonzero(np.isnan(got))) == bad, (t, n)
             assert (got[[c for c in range(d) if c not in bad]] == 0).all()
+
+
+@pytest.mark.parametrize("n", [0, 3, 16, 32])
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_in_place_gives_the_same(kda, n, pairs, dtype):
+    """Bit for bit, rows with infinities among them, for one token and for many out of a projection."""
+    for T in (1, 700):
+        q, k, w = inputs(T, 7, 2, 64, dtype, True, seed=n)
+        q[T // 2, 3, 40], k[T // 2, 1, 5], q[0, 6, 63] = float("inf"), float("-inf"), float("inf")
+        pos, f = torch.arange(T, dtype=torch.int32, device="cuda") * 371, freqs(n)
+        want = kda.kda_head_norm_rope(q, k, pos, f, w[0], w[1], interleaved=pairs)
+        got = kda.kda_head_norm_rope(q, k, pos, f, w[0], w[1], interleaved=pairs, q_out=q, k_out=k)
+        for a, b in zip(got, want):
+            assert torch.equal(torch.isnan(a), torch.isnan(b)) and torch.equal(a.nan_to_num(), b.nan_to_num())
